@@ -77,7 +77,8 @@ typedef enum {
   QL_ERR_UNSUPPORTED = 4, /* unknown format */
   QL_ERR_WORKSPACE = 5,   /* workspace missing or smaller than qlinear_workspace_bytes() */
   QL_ERR_CUDA = 6,        /* a CUDA runtime call or kernel launch failed */
-  QL_ERR_LIBRARY = 7      /* reserved (no library is opened at run time) */
+  QL_ERR_LIBRARY = 7,     /* reserved (no library is opened at run time) */
+  QL_ERR_ALIAS = 8        /* an output overlaps an input or another output (fused layers) */
 } ql_status;
 
 typedef enum {
@@ -433,6 +434,88 @@ ql_status qlinear_policy_lookup(int fmt, int M, int N, int K, ql_policy_entry* o
 ql_status qlinear_matmul(int fmt, const uint16_t* x, const void* packed, const void* p0,
                          const void* p1, uint16_t* y, int M, int N, int K, void* workspace,
                          size_t workspace_bytes, uint16_t* w_fp16, ql_stream_t stream);
+
+/* ---------------------------------------------------------------------------
+ * Fused linear layers: bias, activation and residual in the product's epilogue, the gated
+ * feed-forward projection, and the backward passes of both through the frozen quantized
+ * weights.  Formats W2 / W4 / W8 (group 128) and LUT4 (block 64), any M >= 1.  No page
+ * describes these entries; they are what surrounds the quantized product in a decoder layer.
+ *
+ *   linear          z = x . W + bias;  y = act(z) + residual
+ *   linear_backward dz = dy * act'(z);  dx = dz . W^T;  dbias[n] = sum_m dz[m][n]
+ *   gated           g = x . Wg + bias[0], u = x . Wu + bias[1];  h = act(g) * u
+ *   gated_backward  dg = dh * u * act'(g), du = dh * act(g);  dx = dg . Wg^T + du . Wu^T;
+ *                   dbias = sum_m (dg, du)
+ *
+ * Numbers: sums over K (N in the backward products), the epilogue and the column sums are
+ * fp32; every fp16 output is rounded once, to nearest even.  At M > 16, and in the backward
+ * products, the tensor cores multiply fp16 weights (those of qlinear_dequant_fp16) and the
+ * gradients dz rounded to fp16, as the fp16 GEMM of qlinear_prefill does; at M <= 16 the
+ * forward products use the GEMV's exact codes.  Results are reproducible bit for bit.
+ *
+ * Arguments common to the four entries (device pointers, rows contiguous):
+ *   packed, p0, p1 : as for qlinear_prefill_fused, packed 32-byte aligned; the gated entries
+ *                    take the arrays of qlinear_pack_gated / qlinear_pack_params_gated
+ *   act            : a ql_act
+ *   workspace      : qlinear_fused_workspace_bytes(), 256-byte aligned, zero-filled once
+ *                    before its first use; calls that share it must not overlap in time, but
+ *                    may be of different entries, formats and shapes (up to N = 524288
+ *                    columns; gated: N = 2 F).  qlinear_read_error reads its error word.
+ *   fp16 tensors   : 16-byte aligned; fp32 dbias 16-byte aligned
+ * Asynchronous on `stream`; nothing is allocated.  An output may not overlap an input or
+ * another output (QL_ERR_ALIAS), except that y may be exactly the residual.
+ * Shapes: M >= 1, N (F) % 16 == 0, K % 128 == 0 (QL_ERR_SHAPE); format or act outside the
+ * lists: QL_ERR_UNSUPPORTED.
+ * ------------------------------------------------------------------------- */
+typedef enum {
+  QL_ACT_NONE = 0,
+  QL_ACT_RELU = 1,
+  QL_ACT_GELU = 2,      /* z Phi(z), with the error function */
+  QL_ACT_GELU_TANH = 3, /* its tanh form */
+  QL_ACT_SILU = 4
+} ql_act;
+
+/* Bytes of the workspace for the forward entry (backward = 0) or both directions (1) with at
+ * most M rows, on the current device; N = 2 F for the gated entries.  0 for invalid arguments
+ * or without a device.  Query again after qlinear_policy_set. */
+size_t qlinear_fused_workspace_bytes(int fmt, int M, int N, int K, int backward);
+
+/* y[M][N] = act(x[M][K] . W + bias[N]) + residual[M][N].  bias and residual may be NULL; z
+ * [M][N], when given, receives the pre-activation x . W + bias (fp16) for the backward pass. */
+ql_status qlinear_linear(int fmt, const uint16_t* x, const void* packed, const void* p0,
+                         const void* p1, const uint16_t* bias, const uint16_t* residual, int act,
+                         uint16_t* y, uint16_t* z, int M, int N, int K, void* workspace,
+                         size_t workspace_bytes, ql_stream_t stream);
+
+/* dx[M][K] from dy[M][N] and the kept pre-activation z[M][N] (NULL only with QL_ACT_NONE);
+ * dbias (fp32 [N], overwritten) may be NULL.  The residual's gradient is dy itself. */
+ql_status qlinear_linear_backward(int fmt, const uint16_t* dy, const uint16_t* z,
+                                  const void* packed, const void* p0, const void* p1, int act,
+                                  uint16_t* dx, float* dbias, int M, int N, int K,
+                                  void* workspace, size_t workspace_bytes, ql_stream_t stream);
+
+/* h[M][F] = act(g) * u.  bias fp16 [2][F] (gate, up) or NULL; gu [M][2][F], when given,
+ * receives g and u (fp16) for the backward pass. */
+ql_status qlinear_gated(int fmt, const uint16_t* x, const void* packed, const void* p0,
+                        const void* p1, const uint16_t* bias, int act, uint16_t* h, uint16_t* gu,
+                        int M, int F, int K, void* workspace, size_t workspace_bytes,
+                        ql_stream_t stream);
+
+/* dx[M][K] from dh[M][F] and the kept gu[M][2][F]; dbias (fp32 [2][F]) may be NULL. */
+ql_status qlinear_gated_backward(int fmt, const uint16_t* dh, const uint16_t* gu,
+                                 const void* packed, const void* p0, const void* p1, int act,
+                                 uint16_t* dx, float* dbias, int M, int F, int K,
+                                 void* workspace, size_t workspace_bytes, ql_stream_t stream);
+
+/* Host packers of the gate and up projections (two [K, F] matrices in the canonical layouts)
+ * into one packed matrix of 2 F columns whose 16-column tiles alternate gate, up, gate, ...:
+ * a column of the gate and its partner of the up projection are then in one warp's registers
+ * in every kernel.  Packed sizes: qlinear_packed_bytes / qlinear_params_bytes of N = 2 F.
+ * LUT4: one table serves both projections.  F % 16 == 0, K % 128 == 0; host buffers. */
+ql_status qlinear_pack_gated(int fmt, const void* gate, const void* up, void* packed, int F,
+                             int K);
+ql_status qlinear_pack_params_gated(int fmt, const void* gate, const void* up, void* packed,
+                                    int F, int K);
 
 /* ---------------------------------------------------------------------------
  * Debug entries (device pointers, asynchronous).  They decode the packed layout

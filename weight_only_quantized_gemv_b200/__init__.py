@@ -32,7 +32,8 @@ FORMATS = {"w2": QL_FMT_W2, "w3": QL_FMT_W3, "w4": QL_FMT_W4, "w8": QL_FMT_W8,
            "lut4": QL_FMT_LUT4}
 STATUS = {0: "QL_OK", 1: "QL_ERR_NULL", 2: "QL_ERR_SHAPE", 3: "QL_ERR_ALIGN",
           4: "QL_ERR_UNSUPPORTED", 5: "QL_ERR_WORKSPACE", 6: "QL_ERR_CUDA",
-          7: "QL_ERR_LIBRARY"}
+          7: "QL_ERR_LIBRARY", 8: "QL_ERR_ALIAS"}
+ACTS = {"none": 0, "relu": 1, "gelu": 2, "gelu_tanh": 3, "silu": 4}  # ql_act
 
 _P = ctypes.c_void_p
 _I = ctypes.c_int
@@ -93,6 +94,15 @@ _SIGS = {
     "qlinear_codebook": (_I, [_P, _P, _P, _P, _P, _I, _I, _I, _P, _SZ, _P]),
     "qlinear_pack_codebook_tc": (_I, [_P, _P, _I, _I]),
     "qlinear_codebook_tc": (_I, [_P, _P, _P, _P, _P, _I, _I, _I, _P, _SZ, _P]),
+    "qlinear_fused_workspace_bytes": (_SZ, [_I, _I, _I, _I, _I]),
+    "qlinear_linear": (_I, [_I, _P, _P, _P, _P, _P, _P, _I, _P, _P, _I, _I, _I, _P, _SZ, _P]),
+    "qlinear_linear_backward": (_I, [_I, _P, _P, _P, _P, _P, _I, _P, _P, _I, _I, _I, _P, _SZ,
+                                     _P]),
+    "qlinear_gated": (_I, [_I, _P, _P, _P, _P, _P, _I, _P, _P, _I, _I, _I, _P, _SZ, _P]),
+    "qlinear_gated_backward": (_I, [_I, _P, _P, _P, _P, _P, _I, _P, _P, _I, _I, _I, _P, _SZ,
+                                    _P]),
+    "qlinear_pack_gated": (_I, [_I, _P, _P, _P, _I, _I]),
+    "qlinear_pack_params_gated": (_I, [_I, _P, _P, _P, _I, _I]),
 }
 for _name, (_res, _args) in _SIGS.items():
     _f = getattr(_lib, _name)
@@ -444,3 +454,90 @@ def qlinear_codebook_tc(x, codes, scales, codebook, y, M, N, K, workspace, strea
                                   if workspace is not None else 0, _stream(stream))
     _check(st, "qlinear_codebook_tc")
     return y
+
+
+# ---------------------------------------------------------------------------
+# fused linear layers: bias, activation and residual in the epilogue, the gated projection,
+# and their backward passes.  act: a key of ACTS, or a ql_act value.
+
+
+def _act(act) -> int:
+    if isinstance(act, str):
+        if act not in ACTS:
+            raise QLinearError(4, f"activation {act!r}")
+        return ACTS[act]
+    return int(act)
+
+
+def _ws(workspace):
+    return _ptr(workspace), (workspace.numel() * workspace.element_size()
+                             if workspace is not None else 0)
+
+
+def qlinear_fused_workspace_bytes(fmt: int, M: int, N: int, K: int, backward: bool = True) -> int:
+    return int(_lib.qlinear_fused_workspace_bytes(fmt, M, N, K, int(backward)))
+
+
+def qlinear_linear(fmt, x, packed, p0, p1, y, M, N, K, workspace, bias=None, residual=None,
+                   act="none", z=None, stream=None):
+    """``y[M, N] = act(x . W + bias) + residual``; z, when given, receives x . W + bias."""
+    _check(_lib.qlinear_linear(fmt, _ptr(x), _ptr(packed), _ptr(p0), _ptr(p1), _ptr(bias),
+                               _ptr(residual), _act(act), _ptr(y), _ptr(z), M, N, K,
+                               *_ws(workspace), _stream(stream)), "qlinear_linear")
+    return y
+
+
+def qlinear_linear_backward(fmt, dy, z, packed, p0, p1, dx, M, N, K, workspace, act="none",
+                            dbias=None, stream=None):
+    """``dx[M, K] = (dy * act'(z)) . W^T``; dbias (fp32 [N]), when given, the column sums."""
+    _check(_lib.qlinear_linear_backward(fmt, _ptr(dy), _ptr(z), _ptr(packed), _ptr(p0), _ptr(p1),
+                                        _act(act), _ptr(dx), _ptr(dbias), M, N, K,
+                                        *_ws(workspace), _stream(stream)),
+           "qlinear_linear_backward")
+    return dx
+
+
+def qlinear_gated(fmt, x, packed, p0, p1, h, M, F, K, workspace, bias=None, act="silu", gu=None,
+                  stream=None):
+    """``h[M, F] = act(x . Wg + bias[0]) * (x . Wu + bias[1])``; gu [M, 2, F], when given,
+    receives the two factors before the activation."""
+    _check(_lib.qlinear_gated(fmt, _ptr(x), _ptr(packed), _ptr(p0), _ptr(p1), _ptr(bias),
+                              _act(act), _ptr(h), _ptr(gu), M, F, K, *_ws(workspace),
+                              _stream(stream)), "qlinear_gated")
+    return h
+
+
+def qlinear_gated_backward(fmt, dh, gu, packed, p0, p1, dx, M, F, K, workspace, act="silu",
+                           dbias=None, stream=None):
+    """``dx[M, K]`` of qlinear_gated from dh and the kept gu; dbias fp32 [2, F]."""
+    _check(_lib.qlinear_gated_backward(fmt, _ptr(dh), _ptr(gu), _ptr(packed), _ptr(p0), _ptr(p1),
+                                       _act(act), _ptr(dx), _ptr(dbias), M, F, K,
+                                       *_ws(workspace), _stream(stream)),
+           "qlinear_gated_backward")
+    return dx
+
+
+def qlinear_pack_gated(fmt: int, gate: np.ndarray, up: np.ndarray, F: int, K: int) -> np.ndarray:
+    """Canonical codes of the gate and up projections -> one packed matrix of 2 F columns."""
+    gate, up = np.ascontiguousarray(gate), np.ascontiguousarray(up)
+    out = np.empty(qlinear_packed_bytes(fmt, 2 * F, K), dtype=np.uint8)
+    if out.size == 0 or 2 * gate.nbytes != out.size or 2 * up.nbytes != out.size:
+        raise QLinearError(2, "qlinear_pack_gated")
+    _check(_lib.qlinear_pack_gated(fmt, _np_ptr(gate), _np_ptr(up), _np_ptr(out), F, K),
+           "qlinear_pack_gated")
+    return out
+
+
+def qlinear_pack_params_gated(fmt: int, gate: np.ndarray, up: np.ndarray, F: int,
+                              K: int) -> np.ndarray:
+    """One parameter array of each projection (fp16 [K / 128, F], or LUT4's fp32 absmax
+    [K / 64, F]) -> the kernel layout of the 2 F columns."""
+    dtype = np.float32 if fmt == QL_FMT_LUT4 else np.float16
+    gate, up = np.ascontiguousarray(gate, dtype=dtype), np.ascontiguousarray(up, dtype=dtype)
+    nbytes = qlinear_params_bytes(fmt, 2 * F, K)
+    if nbytes == 0 or 2 * gate.nbytes != nbytes or 2 * up.nbytes != nbytes:
+        raise QLinearError(2, "qlinear_pack_params_gated")
+    out = np.empty(nbytes // dtype().itemsize, dtype=dtype)
+    _check(_lib.qlinear_pack_params_gated(fmt, _np_ptr(gate), _np_ptr(up), _np_ptr(out), F, K),
+           "qlinear_pack_params_gated")
+    return out

@@ -16,8 +16,9 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libqlinear.so")
 
-SOURCES = ["qlinear.cu", "dequant.cu", "prefill_tc.cu", "codebook.cu", "policy.cpp", "pack.cpp"]
-HEADERS = ["kernels.cuh", "layout.h", "policy.h", "dequant_frag.cuh"]
+SOURCES = ["qlinear.cu", "dequant.cu", "prefill_tc.cu", "codebook.cu", "fused.cu", "fused_tc.cu",
+           "policy.cpp", "pack.cpp"]
+HEADERS = ["kernels.cuh", "layout.h", "policy.h", "dequant_frag.cuh", "act.cuh", "fused.h"]
 
 
 def nvcc_path() -> str:
@@ -29,7 +30,7 @@ def nvcc_path() -> str:
 
 def command(out: str = LIB, ptxas_verbose: bool = False) -> list:
     cmd = [nvcc_path(), "-gencode", "arch=compute_100a,code=sm_100a", "-O3", "-lineinfo",
-           "-std=c++17", "-shared", "-cudart", "static", "-Xcompiler", "-fPIC,-fopenmp",
+           "-std=c++17", "--threads", "0", "-shared", "-cudart", "static", "-Xcompiler", "-fPIC,-fopenmp",
            "-I", INCLUDE, "-I", CSRC]
     if ptxas_verbose:
         cmd += ["-Xptxas", "-v"]

@@ -38,23 +38,26 @@ inline uint32_t canonical_code(int fmt, const void* canon, int N, int k, int n) 
   return (uint32_t)(v >> sh) & ((1u << bits) - 1);
 }
 
-}  // namespace
+constexpr int kMaxGatedWidth = 0x3FFFFFF0;  // 2 F fits an int
 
-extern "C" size_t qlinear_packed_bytes(int fmt, int N, int K) {
-  if (!fmt_ok(fmt) || !shape_ok(N, K)) return 0;
-  return (size_t)N * K * code_bits(fmt) / 8;
-}
+// The matrix a packed column comes from: one canonical array of `width` columns, or (gated) two
+// whose 16-column tiles alternate, the gate's first.
+struct Columns {
+  const void* a;
+  const void* b;  // null: a alone
+  int width;
+  const void* source(int n, int* col) const {
+    if (!b) {
+      *col = n;
+      return a;
+    }
+    const int tile = n / kTileN;
+    *col = (tile >> 1) * kTileN + n % kTileN;
+    return (tile & 1) ? b : a;
+  }
+};
 
-extern "C" size_t qlinear_params_bytes(int fmt, int N, int K) {
-  if (!fmt_ok(fmt) || !shape_ok(N, K)) return 0;
-  if (fmt == kLUT4) return (size_t)(K / kLutBlock) * N * sizeof(float);
-  return (size_t)(K / kGroup) * N * sizeof(uint16_t);
-}
-
-extern "C" ql_status qlinear_pack(int fmt, const void* canonical, void* packed, int N, int K) {
-  if (!fmt_ok(fmt)) return QL_ERR_UNSUPPORTED;
-  if (!canonical || !packed) return QL_ERR_NULL;
-  if (!shape_ok(N, K)) return QL_ERR_SHAPE;
+void pack_codes(int fmt, const Columns& c, void* packed, int N, int K) {
   const int G = K / kGroup;
   const int ntiles = N / kTileN;
   const int nblocks = (ntiles + kBlockTiles - 1) / kBlockTiles;
@@ -76,7 +79,9 @@ extern "C" ql_status qlinear_pack(int fmt, const void* canonical, void* packed, 
                 const int k = g * kGroup + k_in_group(s, t, dk);
                 const int n = n_base + gi + r8;
                 int wi, bit;
-                const uint32_t q = canonical_code(fmt, canonical, N, k, n);
+                int col;
+                const void* src = c.source(n, &col);
+                const uint32_t q = canonical_code(fmt, src, c.width, k, col);
                 if (fmt == kW3) {  // low two bits as a W2 code, high bit in its own plane
                   code_position(kW2, s, dk, r8, &wi, &bit);
                   words[wi] |= (q & 3u) << bit;
@@ -92,13 +97,9 @@ extern "C" ql_status qlinear_pack(int fmt, const void* canonical, void* packed, 
       }
     }
   }
-  return QL_OK;
 }
 
-extern "C" ql_status qlinear_pack_params(int fmt, const void* canonical, void* packed, int N, int K) {
-  if (!fmt_ok(fmt)) return QL_ERR_UNSUPPORTED;
-  if (!canonical || !packed) return QL_ERR_NULL;
-  if (!shape_ok(N, K)) return QL_ERR_SHAPE;
+void pack_param_array(int fmt, const Columns& c, void* packed, int N, int K) {
   const int G = K / kGroup;
   const int ntiles = N / kTileN;
   const int nblocks = (ntiles + kBlockTiles - 1) / kBlockTiles;
@@ -106,24 +107,72 @@ extern "C" ql_status qlinear_pack_params(int fmt, const void* canonical, void* p
     const int tb = tiles_in_block(b, ntiles);
     for (int g = 0; g < G; ++g)
       for (int jj = 0; jj < tb; ++jj) {
-        const long long c = chunk_index(b, g, jj, G, ntiles);
+        const long long ch = chunk_index(b, g, jj, G, ntiles);
         const int n_base = (b * kBlockTiles + jj) * kTileN;
         for (int gi = 0; gi < 8; ++gi)
           for (int h = 0; h < 2; ++h) {
-            const int n = n_base + gi + 8 * h;
+            int n;
+            const void* canonical = c.source(n_base + gi + 8 * h, &n);
             if (fmt == kLUT4) {
               const float* a = static_cast<const float*>(canonical);
               float* o = static_cast<float*>(packed);
               for (int blk = 0; blk < 2; ++blk)
-                o[c * 32 + gi * 4 + blk * 2 + h] = a[(size_t)(2 * g + blk) * N + n];
+                o[ch * 32 + gi * 4 + blk * 2 + h] = a[(size_t)(2 * g + blk) * c.width + n];
             } else {
               const uint16_t* a = static_cast<const uint16_t*>(canonical);
               uint16_t* o = static_cast<uint16_t*>(packed);
-              o[c * 16 + gi * 2 + h] = a[(size_t)g * N + n];
+              o[ch * 16 + gi * 2 + h] = a[(size_t)g * c.width + n];
             }
           }
       }
   }
+}
+
+}  // namespace
+
+extern "C" size_t qlinear_packed_bytes(int fmt, int N, int K) {
+  if (!fmt_ok(fmt) || !shape_ok(N, K)) return 0;
+  return (size_t)N * K * code_bits(fmt) / 8;
+}
+
+extern "C" size_t qlinear_params_bytes(int fmt, int N, int K) {
+  if (!fmt_ok(fmt) || !shape_ok(N, K)) return 0;
+  if (fmt == kLUT4) return (size_t)(K / kLutBlock) * N * sizeof(float);
+  return (size_t)(K / kGroup) * N * sizeof(uint16_t);
+}
+
+extern "C" ql_status qlinear_pack(int fmt, const void* canonical, void* packed, int N, int K) {
+  if (!fmt_ok(fmt)) return QL_ERR_UNSUPPORTED;
+  if (!canonical || !packed) return QL_ERR_NULL;
+  if (!shape_ok(N, K)) return QL_ERR_SHAPE;
+  pack_codes(fmt, Columns{canonical, nullptr, N}, packed, N, K);
+  return QL_OK;
+}
+
+extern "C" ql_status qlinear_pack_params(int fmt, const void* canonical, void* packed, int N, int K) {
+  if (!fmt_ok(fmt)) return QL_ERR_UNSUPPORTED;
+  if (!canonical || !packed) return QL_ERR_NULL;
+  if (!shape_ok(N, K)) return QL_ERR_SHAPE;
+  pack_param_array(fmt, Columns{canonical, nullptr, N}, packed, N, K);
+  return QL_OK;
+}
+
+// The gate and up projections as one matrix of 2 F columns, tiles alternating.
+extern "C" ql_status qlinear_pack_gated(int fmt, const void* gate, const void* up, void* packed,
+                                        int F, int K) {
+  if (!fmt_ok(fmt) || fmt == kW3) return QL_ERR_UNSUPPORTED;
+  if (!gate || !up || !packed) return QL_ERR_NULL;
+  if (F > kMaxGatedWidth || !shape_ok(F, K)) return QL_ERR_SHAPE;
+  pack_codes(fmt, Columns{gate, up, F}, packed, 2 * F, K);
+  return QL_OK;
+}
+
+extern "C" ql_status qlinear_pack_params_gated(int fmt, const void* gate, const void* up,
+                                               void* packed, int F, int K) {
+  if (!fmt_ok(fmt) || fmt == kW3) return QL_ERR_UNSUPPORTED;
+  if (!gate || !up || !packed) return QL_ERR_NULL;
+  if (F > kMaxGatedWidth || !shape_ok(F, K)) return QL_ERR_SHAPE;
+  pack_param_array(fmt, Columns{gate, up, F}, packed, 2 * F, K);
   return QL_OK;
 }
 

@@ -532,6 +532,7 @@ extern "C" const char* ql_status_str(int status) {
     case QL_ERR_WORKSPACE: return "workspace missing or too small";
     case QL_ERR_CUDA: return "CUDA error";
     case QL_ERR_LIBRARY: return "reserved (no library is opened at run time)";
+    case QL_ERR_ALIAS: return "an output overlaps an input or another output";
     default: return "unknown status";
   }
 }

@@ -19,6 +19,9 @@ from . import (QL_FMT_CB, QL_FMT_LUT4, QL_FMT_W2, QL_FMT_W3, QL_FMT_W4, QL_FMT_W
                qlinear_debug_unpack, qlinear_dequant_fp16, qlinear_lut4, qlinear_pack,
                qlinear_matmul, qlinear_pack_params, qlinear_pack_params_grouped,
                qlinear_prefill, qlinear_prefill_fused, qlinear_prefill_workspace_bytes,
+               qlinear_fused_workspace_bytes, qlinear_gated, qlinear_gated_backward,
+               qlinear_linear, qlinear_linear_backward, qlinear_pack_gated,
+               qlinear_pack_params_gated,
                qlinear_read_error,
                qlinear_pack_tilecoo, qlinear_w2a16, qlinear_w3a16, qlinear_w4a16,
                qlinear_w4a16_outlier,
@@ -32,7 +35,108 @@ def _dev(a: np.ndarray, device) -> torch.Tensor:
     return torch.from_numpy(np.ascontiguousarray(a)).to(device)
 
 
-class QuantLinear:
+def _as_stream(stream, device) -> torch.cuda.Stream:
+    """A torch stream, a raw cudaStream_t or None (the current one) as a torch stream."""
+    if stream is None:
+        return torch.cuda.current_stream(device)
+    if isinstance(stream, torch.cuda.Stream):
+        return stream
+    return (torch.cuda.ExternalStream(stream, device=device) if stream
+            else torch.cuda.default_stream(device))
+
+
+_FUSED_FORMATS = (QL_FMT_W2, QL_FMT_W4, QL_FMT_W8, QL_FMT_LUT4)
+
+
+class _FusedWorkspace:
+    """What the fused entries (bias / activation / residual, gated, backward) of a layer share:
+    argument checks and the workspace.
+
+    The workspace is one zero-filled buffer, grown by ``reserve`` as more rows are asked for;
+    buffers that were outgrown stay alive with the layer, since a captured graph may still use
+    them.  Calls of one layer run one after the other: an eager call on another stream than
+    the last waits for that stream's work.  Work that overlaps in time - graphs captured from
+    one layer and replayed at the same time - needs a workspace of its own:
+    ``workspace=layer.new_workspace(rows)``.  Tensors a call makes are made on its stream.
+    """
+
+    _fused_shape: tuple  # (fmt, N, K) of the packed matrix
+
+    def _fused_bytes(self, rows: int, backward: bool) -> int:
+        fmt, N, K = self._fused_shape
+        if fmt not in _FUSED_FORMATS:
+            raise ValueError("the fused layers cover W2, W4, W8 (group 128) and LUT4")
+        need = qlinear_fused_workspace_bytes(fmt, rows, N, K, backward)
+        if need == 0:
+            raise ValueError(f"no fused product for {rows} rows, N={N}, K={K}")
+        return need
+
+    def new_workspace(self, rows: int, backward: bool = True) -> torch.Tensor:
+        """A zero-filled workspace for calls of up to `rows` rows."""
+        device = self.qweight.device
+        with torch.cuda.device(device):
+            if torch.cuda.is_current_stream_capturing():
+                raise RuntimeError("reserve(rows) the workspace before capturing a graph")
+            ws = torch.zeros(self._fused_bytes(rows, backward), dtype=torch.uint8, device=device)
+            torch.cuda.synchronize()  # the zero fill has landed, whichever stream uses it
+        return ws
+
+    def reserve(self, rows: int, backward: bool = True) -> None:
+        """Make the layer's own workspace large enough for calls of up to `rows` rows (a call
+        that needs more does this itself, except while a graph is being captured)."""
+        held = self.__dict__.setdefault("_fused_ws", [])
+        with torch.cuda.device(self.qweight.device):
+            need = self._fused_bytes(rows, backward)
+        if not held or held[-1].numel() < need:
+            held.append(self.new_workspace(rows, backward))
+
+    def _fused_call(self, fn, rows: int, backward: bool, workspace, stream):
+        """fn(workspace, stream) with the layer's device current."""
+        device = self.qweight.device
+        with torch.cuda.device(device):
+            stream = _as_stream(stream, device)
+            if workspace is None:
+                self.reserve(rows, backward)
+                workspace = self._fused_ws[-1]
+                with torch.cuda.stream(stream):
+                    capturing = torch.cuda.is_current_stream_capturing()
+                if not capturing:
+                    last = self.__dict__.get("_fused_stream")
+                    if last is not None and last.cuda_stream != stream.cuda_stream:
+                        stream.wait_stream(last)
+                    self._fused_stream = stream
+            elif workspace.device != device or not workspace.is_contiguous():
+                raise ValueError(f"the workspace must be a contiguous tensor on {device}")
+            fn(workspace, stream)
+
+    def _fused_tensor(self, t, shape, name, dtype=torch.float16, make=False, stream=None):
+        """`t` checked (or, with make, a new tensor when None)."""
+        device = self.qweight.device
+        if t is None:
+            if not make:
+                return None
+            with torch.cuda.device(device), torch.cuda.stream(_as_stream(stream, device)):
+                return torch.empty(shape, dtype=dtype, device=device)
+        if t.device != device:
+            raise ValueError(f"{name} is on {t.device}, the layer on {device}")
+        if t.dtype != dtype or tuple(t.shape) != tuple(shape) or not t.is_contiguous():
+            raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape "
+                             f"{tuple(shape)}, not {t.dtype} {tuple(t.shape)} with strides "
+                             f"{t.stride()}")
+        return t
+
+    def fused_read_error(self, workspace=None, stream=None) -> int:
+        """Sticky error flags of the calls that used the workspace (then cleared); 0 = every
+        device wait completed."""
+        if workspace is None:
+            if not self.__dict__.get("_fused_ws"):
+                return 0
+            workspace = self._fused_ws[-1]
+        with torch.cuda.device(self.qweight.device):
+            return qlinear_read_error(workspace, stream)
+
+
+class QuantLinear(_FusedWorkspace):
     """One quantized weight matrix [K, N] resident on a CUDA device."""
 
     def __init__(self, fmt: int, K: int, N: int, canonical_codes: np.ndarray,
@@ -168,6 +272,55 @@ class QuantLinear:
                        y.view(torch.int16), M, self.N, self.K, self.workspace, None, stream)
         return y
 
+    @property
+    def _fused_shape(self) -> tuple:
+        if self.tile is not None:
+            raise ValueError("the fused layers cover the dense formats")
+        self._group128("the fused layer")
+        return self.fmt, self.N, self.K
+
+    def linear(self, x: torch.Tensor, bias: Optional[torch.Tensor] = None,
+               residual: Optional[torch.Tensor] = None, act: str = "none",
+               y: Optional[torch.Tensor] = None, z: Optional[torch.Tensor] = None,
+               workspace: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+        """y[M, N] = act(x[M, K] . W + bias[N]) + residual[M, N] in one kernel, for any M.  act:
+        "none", "relu", "gelu", "gelu_tanh" or "silu".  z ([M, N] fp16), when given, receives
+        x . W + bias for ``linear_backward``.  y may be the residual itself."""
+        fmt, N, K = self._fused_shape
+        M = x.shape[0]
+        self._fused_tensor(x, (M, K), "x")
+        self._fused_tensor(bias, (N,), "bias")
+        self._fused_tensor(residual, (M, N), "residual")
+        self._fused_tensor(z, (M, N), "z")
+        y = self._fused_tensor(y, (M, N), "y", make=True, stream=stream)
+        if M:
+            self._fused_call(lambda ws, st: qlinear_linear(
+                fmt, x, self.qweight, self.p0, self.p1, y, M, N, K, ws, bias, residual, act, z,
+                st), M, False, workspace, stream)
+        return y
+
+    def linear_backward(self, dy: torch.Tensor, z: Optional[torch.Tensor] = None,
+                        act: str = "none", dx: Optional[torch.Tensor] = None,
+                        dbias: Optional[torch.Tensor] = None,
+                        workspace: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+        """The gradient of ``linear`` through the frozen weights: dx[M, K] = dz . W^T with
+        dz = dy * act'(z), z as kept by ``linear`` (None with act "none").  dbias (fp32 [N]),
+        when given, receives the column sums of dz.  The residual's gradient is dy."""
+        fmt, N, K = self._fused_shape
+        M = dy.shape[0]
+        self._fused_tensor(dy, (M, N), "dy")
+        self._fused_tensor(z, (M, N), "z")
+        self._fused_tensor(dbias, (N,), "dbias", torch.float32)
+        dx = self._fused_tensor(dx, (M, K), "dx", make=True, stream=stream)
+        if M:
+            self._fused_call(lambda ws, st: qlinear_linear_backward(
+                fmt, dy, z, self.qweight, self.p0, self.p1, dx, M, N, K, ws, act, dbias, st),
+                M, True, workspace, stream)
+        elif dbias is not None:
+            with torch.cuda.stream(_as_stream(stream, dbias.device)):
+                dbias.zero_()
+        return dx
+
     def debug_unpack(self, stream=None) -> torch.Tensor:
         codes = torch.empty((self.K, self.N), dtype=torch.uint8, device=self.device)
         qlinear_debug_unpack(self.fmt, self.qweight, codes, self.N, self.K, stream)
@@ -178,6 +331,90 @@ class QuantLinear:
         w = torch.empty((self.K, self.N), dtype=torch.float32, device=self.device)
         qlinear_debug_dequant(self.fmt, self.qweight, self.p0, self.p1, w, self.N, self.K, stream)
         return w
+
+
+class GatedLinear(_FusedWorkspace):
+    """The gate and up projections of a gated feed-forward block as one packed matrix
+    [K, 2 F] on the device: gate and up are (codes, p0, p1) of two [K, F] matrices in the
+    canonical layouts (p0, p1: scales and zeros of group 128, or for LUT4 the table, which
+    must be the same for both, and the absmax)."""
+
+    def __init__(self, fmt: int, K: int, F: int, gate: tuple, up: tuple, device="cuda"):
+        if fmt not in _FUSED_FORMATS:
+            raise ValueError("the gated layer covers W2, W4, W8 (group 128) and LUT4")
+        self.fmt, self.K, self.F, self.device = fmt, K, F, torch.device(device)
+        self.qweight = _dev(qlinear_pack_gated(fmt, gate[0], up[0], F, K), self.device)
+        if fmt == QL_FMT_LUT4:
+            tables = [np.asarray(m[1], dtype=np.float16) for m in (gate, up)]
+            if not np.array_equal(*tables):
+                raise ValueError("gate and up share one LUT4 table")
+            self.p0 = _dev(tables[0].view(np.uint16), self.device)
+        else:
+            self.p0 = _dev(qlinear_pack_params_gated(fmt, gate[1], up[1], F, K)
+                           .view(np.uint16), self.device)
+        p1 = qlinear_pack_params_gated(fmt, gate[2], up[2], F, K)
+        self.p1 = _dev(p1 if fmt == QL_FMT_LUT4 else p1.view(np.uint16), self.device)
+        self._fused_shape = (fmt, 2 * F, K)
+
+    def forward(self, x: torch.Tensor, bias: Optional[torch.Tensor] = None, act: str = "silu",
+                h: Optional[torch.Tensor] = None, gu: Optional[torch.Tensor] = None,
+                workspace: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+        """h[M, F] = act(g) * u, g = x . Wg + bias[0], u = x . Wu + bias[1], in one kernel, for
+        any M.  bias: [2, F] or None.  gu ([M, 2, F] fp16), when given, receives g and u for
+        ``backward``."""
+        M = x.shape[0]
+        self._fused_tensor(x, (M, self.K), "x")
+        self._fused_tensor(bias, (2, self.F), "bias")
+        self._fused_tensor(gu, (M, 2, self.F), "gu")
+        h = self._fused_tensor(h, (M, self.F), "h", make=True, stream=stream)
+        if M:
+            self._fused_call(lambda ws, st: qlinear_gated(
+                self.fmt, x, self.qweight, self.p0, self.p1, h, M, self.F, self.K, ws, bias,
+                act, gu, st), M, False, workspace, stream)
+        return h
+
+    def backward(self, dh: torch.Tensor, gu: torch.Tensor, act: str = "silu",
+                 dx: Optional[torch.Tensor] = None, dbias: Optional[torch.Tensor] = None,
+                 workspace: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+        """dx[M, K] of ``forward`` through the frozen weights, from dh and the kept gu; dbias
+        (fp32 [2, F]), when given, receives the column sums of the gradients of g and u."""
+        M = dh.shape[0]
+        self._fused_tensor(dh, (M, self.F), "dh")
+        self._fused_tensor(gu, (M, 2, self.F), "gu")
+        self._fused_tensor(dbias, (2, self.F), "dbias", torch.float32)
+        dx = self._fused_tensor(dx, (M, self.K), "dx", make=True, stream=stream)
+        if M:
+            self._fused_call(lambda ws, st: qlinear_gated_backward(
+                self.fmt, dh, gu, self.qweight, self.p0, self.p1, dx, M, self.F, self.K, ws,
+                act, dbias, st), M, True, workspace, stream)
+        elif dbias is not None:
+            with torch.cuda.stream(_as_stream(stream, dbias.device)):
+                dbias.zero_()
+        return dx
+
+
+class GatedMLP:
+    """A gated feed-forward block: y = (act(x Wg) * (x Wu)) Wd + residual, two kernels forward;
+    backward through the frozen weights from the kept gate and up values."""
+
+    def __init__(self, gate_up: GatedLinear, down: QuantLinear, act: str = "silu"):
+        if gate_up.F != down.K or gate_up.K != down.N:
+            raise ValueError("the down projection is [F, K] for a gate and up of [K, F]")
+        self.gate_up, self.down, self.act = gate_up, down, act
+
+    def reserve(self, rows: int, backward: bool = True) -> None:
+        self.gate_up.reserve(rows, backward)
+        self.down.reserve(rows, backward)
+
+    def forward(self, x: torch.Tensor, residual: Optional[torch.Tensor] = None,
+                gu: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+        h = self.gate_up.forward(x, act=self.act, gu=gu, stream=stream)
+        return self.down.linear(h, residual=residual, stream=stream)
+
+    def backward(self, dy: torch.Tensor, gu: torch.Tensor, stream=None) -> torch.Tensor:
+        """dx from dy and the gu that ``forward`` kept (the residual's gradient is dy)."""
+        dh = self.down.linear_backward(dy, stream=stream)
+        return self.gate_up.backward(dh, gu, act=self.act, stream=stream)
 
 
 def from_uniform(layer, device="cuda", max_m: int = 16) -> QuantLinear:
