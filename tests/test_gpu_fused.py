@@ -436,7 +436,7 @@ def test_layer_refusals():
         lay.linear(x.float())
     with pytest.raises(ValueError, match="x must be"):
         lay.linear(_t(1, 384, 4).t())
-    with pytest.raises(ValueError, match="x is on"):
+    with pytest.raises(ValueError, match="on cpu"):
         lay.linear(x.cpu())
     with pytest.raises(ValueError, match="bias"):
         lay.linear(x, bias=res)

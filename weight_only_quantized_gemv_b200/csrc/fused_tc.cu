@@ -161,7 +161,4 @@ ql_status launch_tc(const Product& p) {
   return cudaGetLastError() == cudaSuccess ? QL_OK : QL_ERR_CUDA;
 }
 
-ql_status launch_gemv(const Product& p) { return launch_tc(p); }
-size_t gemv_partial_bytes(int, int, int, int, bool) { return 256; }
-
 }  // namespace qfused

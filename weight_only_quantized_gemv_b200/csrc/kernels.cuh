@@ -46,6 +46,8 @@
 #include <cuda_fp16.h>
 #include <stdint.h>
 
+#include "act.cuh"
+#include "fused.h"
 #include "layout.h"
 
 namespace qlk {
@@ -78,6 +80,14 @@ struct GemvParams {
   // stage, in microseconds
   uint32_t test_us;
 };
+
+// Instances with an epilogue (EPI): 1 = y = act(z + bias) + residual, 2 = the gated product
+// of the columns' alternating 16-column gate and up tiles (fused.h).
+struct GemvEpiParams : GemvParams {
+  qfused::Epilogue epi;
+};
+template <int EPI> struct GemvParamsOf { using type = GemvEpiParams; };
+template <> struct GemvParamsOf<0> { using type = GemvParams; };
 
 template <int FMT> struct Fmt;
 template <> struct Fmt<kW4> {
@@ -429,7 +439,7 @@ __host__ __device__ __forceinline__ int cta_of_unit(int u, int U, int C) {
 // ---------------------------------------------------------------------------
 
 template <int FMT, int MT, bool OUTL, int WPU_, bool M1_ = false, int OCC_ = 0, int NS_ = 1,
-          bool TH = false>
+          bool TH = false, int EPI = 0>
 struct Gemv {
   using C_ = Cfg<FMT, MT, OUTL, WPU_, M1_, OCC_, NS_>;
   static constexpr int NS = C_::NS;
@@ -676,6 +686,49 @@ struct Gemv {
   __device__ static void store_y(const GemvParams& P, int b, int warp, int lane, int tb,
                                  const float (&v)[T][NACC]) {
     const int gi = lane >> 2, t4 = lane & 3;
+    if constexpr (EPI == 1) {
+      const qfused::Epilogue& E = static_cast<const GemvEpiParams&>(P).epi;
+#pragma unroll
+      for (int i = 0; i < T; ++i) {
+        const int jj = warp * T + i;
+        if (jj >= tb) continue;
+        const int nb = (b * kBlockTiles + jj) * kTileN + gi;
+#pragma unroll
+        for (int e = 0; e < NACC; ++e) {
+          const int m = 2 * t4 + (e & 1) + 8 * (e >> 2);
+          const int n = nb + ((e & 2) ? 8 : 0);
+          if (m >= P.M) continue;
+          const size_t o = (size_t)m * P.N + n;
+          const float z = v[i][e] + (E.bias ? __half2float(E.bias[n]) : 0.f);
+          if (E.zsave) E.zsave[o] = __float2half_rn(z);
+          const float a = qact::act_forward(E.act, z);
+          P.y[o] = __float2half_rn(E.residual ? a + __half2float(E.residual[o]) : a);
+        }
+      }
+      return;
+    }
+    if constexpr (EPI == 2) {
+      // tiles 2 w (gate) and 2 w + 1 (up) of the block are the warp's own: 2 F columns are a
+      // multiple of 32, so both are there or neither
+      static_assert(T == 2, "a gate tile and its up tile per warp");
+      const qfused::Epilogue& E = static_cast<const GemvEpiParams&>(P).epi;
+      const int F = P.N >> 1;
+      const int fb = (b * (kBlockTiles / 2) + warp) * kTileN + gi;
+#pragma unroll
+      for (int e = 0; e < NACC; ++e) {
+        const int m = 2 * t4 + (e & 1) + 8 * (e >> 2);
+        const int f = fb + ((e & 2) ? 8 : 0);
+        if (m >= P.M) continue;
+        const float g = v[0][e] + (E.bias ? __half2float(E.bias[f]) : 0.f);
+        const float u = v[1][e] + (E.bias ? __half2float(E.bias[F + f]) : 0.f);
+        if (E.zsave) {
+          E.zsave[((size_t)m * 2) * F + f] = __float2half_rn(g);
+          E.zsave[((size_t)m * 2 + 1) * F + f] = __float2half_rn(u);
+        }
+        P.y[(size_t)m * F + f] = __float2half_rn(qact::act_forward(E.act, g) * u);
+      }
+      return;
+    }
 #pragma unroll
     for (int i = 0; i < T; ++i) {
       const int jj = warp * T + i;
@@ -1206,13 +1259,14 @@ struct NoXMap {
 template <bool XT> struct XMapParam { using type = NoXMap; };
 template <> struct XMapParam<true> { using type = CUtensorMap; };
 
-template <int FMT, int MT, bool OUTL, int WPU, bool M1, int OCC, int NS = 1, bool TH = false>
+template <int FMT, int MT, bool OUTL, int WPU, bool M1, int OCC, int NS = 1, bool TH = false,
+          int EPI = 0>
 __global__ void __launch_bounds__(Cfg<FMT, MT, OUTL, WPU, M1, OCC, NS>::kThreads,
                                   Cfg<FMT, MT, OUTL, WPU, M1, OCC, NS>::kMinCtas)
-    qgemv_kernel(const GemvParams P, const __grid_constant__ typename XMapParam<!M1>::type xm) {
+    qgemv_kernel(const typename GemvParamsOf<EPI>::type P, const __grid_constant__ typename XMapParam<!M1>::type xm) {
   const CUtensorMap* xmap = nullptr;
   if constexpr (!M1) xmap = &xm;
-  using G_ = Gemv<FMT, MT, OUTL, WPU, M1, OCC, NS, TH>;
+  using G_ = Gemv<FMT, MT, OUTL, WPU, M1, OCC, NS, TH, EPI>;
   using C_ = Cfg<FMT, MT, OUTL, WPU, M1, OCC, NS>;
   extern __shared__ __align__(128) uint8_t smem[];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;

@@ -50,11 +50,11 @@ struct KernelInfo {
 };
 
 template <int FMT, int MT, bool OUTL, int WPU = qlk::default_wpu(FMT, MT), bool M1 = false,
-          int OCC = 0, int NS = 1, bool TH = false>
+          int OCC = 0, int NS = 1, bool TH = false, int EPI = 0>
 KernelInfo kernel_info() {
   using C = qlk::Cfg<FMT, MT, OUTL, WPU, M1, OCC, NS>;
   return KernelInfo{
-      reinterpret_cast<const void*>(qlk::qgemv_kernel<FMT, MT, OUTL, WPU, M1, OCC, NS, TH>),
+      reinterpret_cast<const void*>(qlk::qgemv_kernel<FMT, MT, OUTL, WPU, M1, OCC, NS, TH, EPI>),
       C::kThreads, C::kSmemBytes, C::NC, C::T, !M1};
 }
 
@@ -130,6 +130,39 @@ KernelInfo select_kernel(int fmt, int MT, bool outl, int wpu, bool m1, bool occ2
   }
 }
 
+// The instances with an epilogue (fused.h): the same variants of the four formats it covers.
+template <int FMT, int EPI, int WPU = qlk::default_wpu(FMT, 1)>
+KernelInfo epi_m8_kernel(bool m1) {
+  return m1 ? kernel_info<FMT, 1, false, WPU, true, 0, 1, false, EPI>()
+            : kernel_info<FMT, 1, false, WPU, false, 0, 1, false, EPI>();
+}
+template <int FMT, int EPI>
+KernelInfo epi_kernel_fmt(int MT, bool m1) {
+  return MT == 1 ? epi_m8_kernel<FMT, EPI>(m1)
+                 : kernel_info<FMT, 2, false, qlk::default_wpu(FMT, 2), false, 0, 1, false, EPI>();
+}
+template <int EPI>
+KernelInfo epi_kernel(int fmt, int MT, int wpu, bool m1, bool occ2) {
+  switch (fmt) {
+    case kW2: return epi_kernel_fmt<kW2, EPI>(MT, m1);
+    case kW8: return epi_kernel_fmt<kW8, EPI>(MT, m1);
+    case kLUT4: return epi_kernel_fmt<kLUT4, EPI>(MT, m1);
+    default:
+      if (MT == 1 && m1 && wpu == 1 && occ2)
+        return kernel_info<kW4, 1, false, 1, true, 2, 1, false, EPI>();
+      if (MT == 1 && wpu == 4) return epi_m8_kernel<kW4, EPI, 4>(m1);
+      if (MT == 1 && wpu == 2) return epi_m8_kernel<kW4, EPI, 2>(m1);
+      return epi_kernel_fmt<kW4, EPI>(MT, m1);
+  }
+}
+
+// epi: 0 none, 1 linear, 2 gated
+KernelInfo pick_kernel(int fmt, int MT, bool outl, int wpu, bool m1, bool occ2, int ns, int epi) {
+  if (epi == 1) return epi_kernel<1>(fmt, MT, wpu, m1, occ2);
+  if (epi == 2) return epi_kernel<2>(fmt, MT, wpu, m1, occ2);
+  return select_kernel(fmt, MT, outl, wpu, m1, occ2, ns);
+}
+
 // Opt a kernel into its dynamic shared memory and query its resident CTAs per SM
 // (once per kernel and device, then cached).
 cudaError_t prepare_kernel(const KernelInfo& k, int dev, int* ctas) {
@@ -154,7 +187,7 @@ cudaError_t prepare_kernel(const KernelInfo& k, int dev, int* ctas) {
   return cudaSuccess;
 }
 
-cudaError_t make_plan(int fmt, int M, int N, int K, bool outl, Plan* p, int ns = 1) {
+cudaError_t make_plan(int fmt, int M, int N, int K, bool outl, Plan* p, int ns = 1, int epi = 0) {
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
@@ -166,7 +199,7 @@ cudaError_t make_plan(int fmt, int M, int N, int K, bool outl, Plan* p, int ns =
   p->M1 = M == 1;
   p->OCC2 = false;
   p->NS = ns;
-  const KernelInfo k = select_kernel(fmt, p->MT, outl, p->WPU, p->M1, false, ns);
+  const KernelInfo k = pick_kernel(fmt, p->MT, outl, p->WPU, p->M1, false, ns, epi);
   int occ = 1;
   e = prepare_kernel(k, dev, &occ);
   if (e != cudaSuccess) return e;
@@ -238,7 +271,7 @@ cudaError_t make_plan(int fmt, int M, int N, int K, bool outl, Plan* p, int ns =
       if (v == 1 || v == 2 || v == 4) wpu = v;
     }
     if (wpu != p->WPU) {
-      const KernelInfo k2 = select_kernel(fmt, p->MT, outl, wpu, p->M1);
+      const KernelInfo k2 = pick_kernel(fmt, p->MT, outl, wpu, p->M1, false, 1, epi);
       int occ2 = 1;
       e = prepare_kernel(k2, dev, &occ2);
       if (e != cudaSuccess) return e;
@@ -251,7 +284,7 @@ cudaError_t make_plan(int fmt, int M, int N, int K, bool outl, Plan* p, int ns =
     // A grid of at most two CTAs per SM leaves the third slot empty: then the M = 1 kernel
     // with more registers per thread (fewer spills) is faster.
     if (p->M1 && p->WPU == 1 && (small_m1 || C <= 2LL * sms)) {
-      const KernelInfo k3 = select_kernel(fmt, p->MT, outl, 1, true, true);
+      const KernelInfo k3 = pick_kernel(fmt, p->MT, outl, 1, true, true, 1, epi);
       int occ3 = 1;
       e = prepare_kernel(k3, dev, &occ3);
       if (e != cudaSuccess) return e;
@@ -352,14 +385,10 @@ ql_status check_call(const Call& c) {
   return QL_OK;
 }
 
-ql_status run(const Call& c) {
-  const ql_status chk = check_call(c);
-  if (chk != QL_OK) return chk;
-  Plan p;
-  if (make_plan(c.fmt, c.M, c.N, c.K, c.outl, &p, c.ns) != cudaSuccess) return QL_ERR_CUDA;
-  if (!c.ws || c.ws_bytes < p.ws_bytes) return QL_ERR_WORKSPACE;
-  if (!aligned(c.ws, 16)) return QL_ERR_ALIGN;
-  qlk::GemvParams P;
+// Launch a planned call: its error word, counters and partial sums at the given addresses.
+ql_status enqueue(const Call& c, const Plan& p, uint32_t* err, uint32_t* counters, float* partials,
+                  const qfused::Epilogue* epi) {
+  qlk::GemvEpiParams P;
   P.x = static_cast<const __half*>(c.x);
   P.qw = static_cast<const uint8_t*>(c.qw);
   P.sc = static_cast<const __half*>(c.p0);
@@ -368,9 +397,9 @@ ql_status run(const Call& c) {
   P.tile_rc = reinterpret_cast<const uint16_t*>(c.trc);
   P.tile_val = c.tval;
   P.y = static_cast<__half*>(c.y);
-  P.err = static_cast<uint32_t*>(c.ws);
-  P.counters = reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(c.ws) + p.counter_offset);
-  P.partials = reinterpret_cast<float*>(static_cast<uint8_t*>(c.ws) + p.partial_offset);
+  P.err = err;
+  P.counters = counters;
+  P.partials = partials;
   P.M = c.M;
   P.N = c.N;
   P.K = c.K;
@@ -381,8 +410,10 @@ ql_status run(const Call& c) {
   P.C = p.C;
   P.wait_limit = g_wait_limit.load(std::memory_order_relaxed);
   P.test_us = g_test_us.load(std::memory_order_relaxed);
-  KernelInfo k = select_kernel(c.fmt, p.MT, c.outl, p.WPU, p.M1, p.OCC2, p.NS);
-  if (P.wait_limit != qlk::kSpinLimit || P.test_us != 0) {  // qlinear_debug_wait_test is active
+  if (epi) P.epi = *epi;
+  KernelInfo k = pick_kernel(c.fmt, p.MT, c.outl, p.WPU, p.M1, p.OCC2, p.NS,
+                             !epi ? 0 : epi->gated ? 2 : 1);
+  if (!epi && (P.wait_limit != qlk::kSpinLimit || P.test_us != 0)) {  // qlinear_debug_wait_test is active
     KernelInfo kt;
     if (test_kernel(c.fmt, p.MT, c.outl, p.WPU, p.M1, p.OCC2, p.NS, &kt)) {
       int dev = 0, occ = 0;
@@ -403,17 +434,31 @@ ql_status run(const Call& c) {
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
+  void* arg0 = epi ? static_cast<void*>(&P) : static_cast<void*>(static_cast<qlk::GemvParams*>(&P));
   if (k.xt) {
     CUtensorMap xmap;
     if (!encode_x_map(&xmap, c.x, c.M, c.K)) return QL_ERR_CUDA;
-    void* args[2] = {&P, &xmap};
+    void* args[2] = {arg0, &xmap};
     if (cudaLaunchKernelExC(&cfg, k.fn, args) != cudaSuccess) return QL_ERR_CUDA;
   } else {
     qlk::NoXMap none{0};
-    void* args[2] = {&P, &none};
+    void* args[2] = {arg0, &none};
     if (cudaLaunchKernelExC(&cfg, k.fn, args) != cudaSuccess) return QL_ERR_CUDA;
   }
   return cudaGetLastError() == cudaSuccess ? QL_OK : QL_ERR_CUDA;
+}
+
+ql_status run(const Call& c) {
+  const ql_status chk = check_call(c);
+  if (chk != QL_OK) return chk;
+  Plan p;
+  if (make_plan(c.fmt, c.M, c.N, c.K, c.outl, &p, c.ns) != cudaSuccess) return QL_ERR_CUDA;
+  if (!c.ws || c.ws_bytes < p.ws_bytes) return QL_ERR_WORKSPACE;
+  if (!aligned(c.ws, 16)) return QL_ERR_ALIGN;
+  uint8_t* ws = static_cast<uint8_t*>(c.ws);
+  return enqueue(c, p, static_cast<uint32_t*>(c.ws),
+                 reinterpret_cast<uint32_t*>(ws + p.counter_offset),
+                 reinterpret_cast<float*>(ws + p.partial_offset), nullptr);
 }
 
 // ---------------------------------------------------------------------------
@@ -518,6 +563,24 @@ ql_status launch_debug(int fmt, const void* packed, const void* p0, const void* 
 }
 
 }  // namespace
+
+// ---------------------------------------------------------------------------
+// the GEMV with an epilogue (entries in fused.cu, which checks the arguments)
+
+size_t qfused::gemv_partial_bytes(int fmt, int M, int N, int K, bool gated) {
+  Plan p;
+  if (make_plan(fmt, M, N, K, false, &p, 1, gated ? 2 : 1) != cudaSuccess) return 0;
+  return p.ws_bytes - p.partial_offset;
+}
+
+ql_status qfused::launch_gemv(const Product& q) {
+  Plan p;
+  if (make_plan(q.fmt, q.M, q.N, q.K, false, &p, 1, q.epi.gated ? 2 : 1) != cudaSuccess)
+    return QL_ERR_CUDA;
+  Call c{q.fmt, false, q.x, q.packed, q.p0, q.p1, nullptr, nullptr, nullptr, q.epi.y,
+         q.M, q.N, q.K, nullptr, 0, q.stream};
+  return enqueue(c, p, q.err, q.counters, q.partials, &q.epi);
+}
 
 // ---------------------------------------------------------------------------
 // exported entry points

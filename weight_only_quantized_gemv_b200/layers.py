@@ -12,20 +12,18 @@ from typing import Optional
 import numpy as np
 import torch
 
-from . import (QL_FMT_CB, QL_FMT_LUT4, QL_FMT_W2, QL_FMT_W3, QL_FMT_W4, QL_FMT_W8,
+from . import (QL_ERR_WORKSPACE, QL_FMT_CB, QL_FMT_LUT4, QL_FMT_W2, QL_FMT_W3, QL_FMT_W4, QL_FMT_W8,
                qlinear_codebook, qlinear_codebook_tc, qlinear_codebook_workspace_bytes,
                qlinear_debug_dequant, qlinear_pack_codebook, qlinear_pack_codebook_scales,
                qlinear_pack_codebook_tc,
                qlinear_debug_unpack, qlinear_dequant_fp16, qlinear_lut4, qlinear_pack,
                qlinear_matmul, qlinear_pack_params, qlinear_pack_params_grouped,
                qlinear_prefill, qlinear_prefill_fused, qlinear_prefill_workspace_bytes,
-               qlinear_fused_workspace_bytes, qlinear_gated, qlinear_gated_backward,
-               qlinear_linear, qlinear_linear_backward, qlinear_pack_gated,
-               qlinear_pack_params_gated,
+               qlinear_fused_workspace_bytes, qlinear_pack_gated, qlinear_pack_params_gated,
                qlinear_read_error,
                qlinear_pack_tilecoo, qlinear_w2a16, qlinear_w3a16, qlinear_w4a16,
                qlinear_w4a16_outlier,
-               qlinear_w8a16, qlinear_workspace_bytes)
+               qlinear_w8a16, qlinear_workspace_bytes, _act, _check, _lib)
 
 _ENTRY = {QL_FMT_W2: qlinear_w2a16, QL_FMT_W3: qlinear_w3a16, QL_FMT_W4: qlinear_w4a16,
           QL_FMT_W8: qlinear_w8a16}
@@ -35,17 +33,35 @@ def _dev(a: np.ndarray, device) -> torch.Tensor:
     return torch.from_numpy(np.ascontiguousarray(a)).to(device)
 
 
-def _as_stream(stream, device) -> torch.cuda.Stream:
+_FUSED_FORMATS = (QL_FMT_W2, QL_FMT_W4, QL_FMT_W8, QL_FMT_LUT4)
+_F16, _F32 = torch.float16, torch.float32
+# (the handle alone, without a Stream object around it, where torch offers that)
+_current_stream = getattr(torch._C, "_cuda_getCurrentRawStream",
+                          lambda index: torch.cuda.current_stream(index).cuda_stream)
+
+
+def _as_stream(stream, index: int) -> torch.cuda.Stream:
     """A torch stream, a raw cudaStream_t or None (the current one) as a torch stream."""
     if stream is None:
-        return torch.cuda.current_stream(device)
+        return torch.cuda.current_stream(index)
     if isinstance(stream, torch.cuda.Stream):
         return stream
+    device = torch.device("cuda", index)
     return (torch.cuda.ExternalStream(stream, device=device) if stream
             else torch.cuda.default_stream(device))
 
 
-_FUSED_FORMATS = (QL_FMT_W2, QL_FMT_W4, QL_FMT_W8, QL_FMT_LUT4)
+def _fused_ptr(t, shape: tuple, index: int, name: str, dtype=_F16) -> Optional[int]:
+    """The data pointer of `t` once checked (None for None): `shape`, `dtype`, contiguous, on
+    CUDA device `index`."""
+    if t is None:
+        return None
+    if (t.dtype is not dtype or t.shape != shape or not t.is_contiguous()
+            or t.get_device() != index):
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {shape} on "
+                         f"cuda:{index}, not {t.dtype} {tuple(t.shape)} with strides "
+                         f"{t.stride()} on {t.device}")
+    return t.data_ptr()
 
 
 class _FusedWorkspace:
@@ -60,79 +76,103 @@ class _FusedWorkspace:
     ``workspace=layer.new_workspace(rows)``.  Tensors a call makes are made on its stream.
     """
 
-    _fused_shape: tuple  # (fmt, N, K) of the packed matrix
+    _fused_ws: tuple = ()    # buffers, the one in use last
+    _fused_last = None       # stream of the last eager call: (raw handle, torch stream)
 
-    def _fused_bytes(self, rows: int, backward: bool) -> int:
-        fmt, N, K = self._fused_shape
+    def _fused_setup(self):
+        """(fmt, N, K, device index) of the packed matrix, checked at the first call."""
+        fmt, N, K = self._fused_matrix()
         if fmt not in _FUSED_FORMATS:
             raise ValueError("the fused layers cover W2, W4, W8 (group 128) and LUT4")
-        need = qlinear_fused_workspace_bytes(fmt, rows, N, K, backward)
+        self._fused = (fmt, N, K, self.qweight.get_device())
+        return self._fused
+
+    def _fused_weights(self) -> tuple:
+        return self.qweight.data_ptr(), self.p0.data_ptr(), self.p1.data_ptr()
+
+    _fused = None
+
+    def _fused_bytes(self, rows: int, backward: bool) -> int:
+        fmt, N, K, index = self._fused or self._fused_setup()
+        with torch.cuda.device(index):
+            need = qlinear_fused_workspace_bytes(fmt, rows, N, K, backward)
         if need == 0:
             raise ValueError(f"no fused product for {rows} rows, N={N}, K={K}")
         return need
 
     def new_workspace(self, rows: int, backward: bool = True) -> torch.Tensor:
         """A zero-filled workspace for calls of up to `rows` rows."""
-        device = self.qweight.device
-        with torch.cuda.device(device):
+        need = self._fused_bytes(rows, backward)
+        with torch.cuda.device(self._fused[3]):
             if torch.cuda.is_current_stream_capturing():
                 raise RuntimeError("reserve(rows) the workspace before capturing a graph")
-            ws = torch.zeros(self._fused_bytes(rows, backward), dtype=torch.uint8, device=device)
+            ws = torch.zeros(need, dtype=torch.uint8, device="cuda")
             torch.cuda.synchronize()  # the zero fill has landed, whichever stream uses it
         return ws
 
     def reserve(self, rows: int, backward: bool = True) -> None:
         """Make the layer's own workspace large enough for calls of up to `rows` rows (a call
         that needs more does this itself, except while a graph is being captured)."""
-        held = self.__dict__.setdefault("_fused_ws", [])
-        with torch.cuda.device(self.qweight.device):
-            need = self._fused_bytes(rows, backward)
-        if not held or held[-1].numel() < need:
-            held.append(self.new_workspace(rows, backward))
+        if not self._fused_ws or self._fused_ws[-1].numel() < self._fused_bytes(rows, backward):
+            self._fused_ws = self._fused_ws + (self.new_workspace(rows, backward),)
 
-    def _fused_call(self, fn, rows: int, backward: bool, workspace, stream):
-        """fn(workspace, stream) with the layer's device current."""
-        device = self.qweight.device
-        with torch.cuda.device(device):
-            stream = _as_stream(stream, device)
-            if workspace is None:
-                self.reserve(rows, backward)
-                workspace = self._fused_ws[-1]
-                with torch.cuda.stream(stream):
-                    capturing = torch.cuda.is_current_stream_capturing()
-                if not capturing:
-                    last = self.__dict__.get("_fused_stream")
-                    if last is not None and last.cuda_stream != stream.cuda_stream:
-                        stream.wait_stream(last)
-                    self._fused_stream = stream
-            elif workspace.device != device or not workspace.is_contiguous():
-                raise ValueError(f"the workspace must be a contiguous tensor on {device}")
-            fn(workspace, stream)
+    def _fused_call(self, entry, name: str, head: tuple, rows: int, backward: bool, workspace,
+                    stream):
+        """entry(*head, workspace, bytes, stream), the layer's device being current.  The
+        layer's own workspace is grown when the entry finds it too small."""
+        index = self._fused[3]
+        if stream is None:
+            raw = _current_stream(index)
+        else:
+            raw = getattr(stream, "cuda_stream", stream)
+        if workspace is not None:
+            if workspace.get_device() != index or not workspace.is_contiguous():
+                raise ValueError(f"the workspace must be a contiguous tensor on cuda:{index}")
+            _check(entry(*head, workspace.data_ptr(),
+                         workspace.numel() * workspace.element_size(), raw), name)
+            return
+        if self._fused_last is None or self._fused_last[0] != raw:
+            self._fused_switch(raw, stream)
+        if self._fused_ws:
+            ws = self._fused_ws[-1]
+            status = entry(*head, ws.data_ptr(), ws.numel(), raw)
+            if status != QL_ERR_WORKSPACE:
+                _check(status, name)
+                return
+        self.reserve(rows, backward)
+        ws = self._fused_ws[-1]
+        _check(entry(*head, ws.data_ptr(), ws.numel(), raw), name)
 
-    def _fused_tensor(self, t, shape, name, dtype=torch.float16, make=False, stream=None):
-        """`t` checked (or, with make, a new tensor when None)."""
-        device = self.qweight.device
-        if t is None:
-            if not make:
-                return None
-            with torch.cuda.device(device), torch.cuda.stream(_as_stream(stream, device)):
-                return torch.empty(shape, dtype=dtype, device=device)
-        if t.device != device:
-            raise ValueError(f"{name} is on {t.device}, the layer on {device}")
-        if t.dtype != dtype or tuple(t.shape) != tuple(shape) or not t.is_contiguous():
-            raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape "
-                             f"{tuple(shape)}, not {t.dtype} {tuple(t.shape)} with strides "
-                             f"{t.stride()}")
-        return t
+    def _fused_switch(self, raw: int, stream) -> None:
+        """The layer's workspace moves to another stream: that one waits for the last."""
+        stream = _as_stream(stream, self._fused[3])
+        with torch.cuda.stream(stream):
+            if torch.cuda.is_current_stream_capturing():
+                return
+        if self._fused_last is not None:
+            stream.wait_stream(self._fused_last[1])
+        self._fused_last = (raw, stream)
+
+    def _fused_new(self, shape: tuple, index: int, stream) -> torch.Tensor:
+        """A new fp16 tensor, made on the call's stream."""
+        if stream is None:
+            return torch.empty(shape, dtype=_F16, device=self.qweight.device)
+        with torch.cuda.stream(_as_stream(stream, index)):
+            return torch.empty(shape, dtype=_F16, device=self.qweight.device)
+
+    def _fused_elsewhere(self, method, *args, **kw):
+        """method(*args, **kw) with the layer's device current, if another one is now."""
+        with torch.cuda.device(self._fused[3]):
+            return method(*args, **kw)
 
     def fused_read_error(self, workspace=None, stream=None) -> int:
         """Sticky error flags of the calls that used the workspace (then cleared); 0 = every
         device wait completed."""
         if workspace is None:
-            if not self.__dict__.get("_fused_ws"):
+            if not self._fused_ws:
                 return 0
             workspace = self._fused_ws[-1]
-        with torch.cuda.device(self.qweight.device):
+        with torch.cuda.device(workspace.device):
             return qlinear_read_error(workspace, stream)
 
 
@@ -272,8 +312,7 @@ class QuantLinear(_FusedWorkspace):
                        y.view(torch.int16), M, self.N, self.K, self.workspace, None, stream)
         return y
 
-    @property
-    def _fused_shape(self) -> tuple:
+    def _fused_matrix(self) -> tuple:
         if self.tile is not None:
             raise ValueError("the fused layers cover the dense formats")
         self._group128("the fused layer")
@@ -286,17 +325,20 @@ class QuantLinear(_FusedWorkspace):
         """y[M, N] = act(x[M, K] . W + bias[N]) + residual[M, N] in one kernel, for any M.  act:
         "none", "relu", "gelu", "gelu_tanh" or "silu".  z ([M, N] fp16), when given, receives
         x . W + bias for ``linear_backward``.  y may be the residual itself."""
-        fmt, N, K = self._fused_shape
+        fmt, N, K, index = self._fused or self._fused_setup()
+        if torch.cuda.current_device() != index:
+            return self._fused_elsewhere(self.linear, x, bias, residual, act, y, z, workspace,
+                                         stream)
         M = x.shape[0]
-        self._fused_tensor(x, (M, K), "x")
-        self._fused_tensor(bias, (N,), "bias")
-        self._fused_tensor(residual, (M, N), "residual")
-        self._fused_tensor(z, (M, N), "z")
-        y = self._fused_tensor(y, (M, N), "y", make=True, stream=stream)
+        px = _fused_ptr(x, (M, K), index, "x")
+        if y is None:
+            y = self._fused_new((M, N), index, stream)
+        head = (fmt, px, *self._fused_weights(), _fused_ptr(bias, (N,), index, "bias"),
+                _fused_ptr(residual, (M, N), index, "residual"), _act(act),
+                _fused_ptr(y, (M, N), index, "y"), _fused_ptr(z, (M, N), index, "z"), M, N, K)
         if M:
-            self._fused_call(lambda ws, st: qlinear_linear(
-                fmt, x, self.qweight, self.p0, self.p1, y, M, N, K, ws, bias, residual, act, z,
-                st), M, False, workspace, stream)
+            self._fused_call(_lib.qlinear_linear, "qlinear_linear", head, M, False, workspace,
+                             stream)
         return y
 
     def linear_backward(self, dy: torch.Tensor, z: Optional[torch.Tensor] = None,
@@ -306,18 +348,22 @@ class QuantLinear(_FusedWorkspace):
         """The gradient of ``linear`` through the frozen weights: dx[M, K] = dz . W^T with
         dz = dy * act'(z), z as kept by ``linear`` (None with act "none").  dbias (fp32 [N]),
         when given, receives the column sums of dz.  The residual's gradient is dy."""
-        fmt, N, K = self._fused_shape
+        fmt, N, K, index = self._fused or self._fused_setup()
+        if torch.cuda.current_device() != index:
+            return self._fused_elsewhere(self.linear_backward, dy, z, act, dx, dbias, workspace,
+                                         stream)
         M = dy.shape[0]
-        self._fused_tensor(dy, (M, N), "dy")
-        self._fused_tensor(z, (M, N), "z")
-        self._fused_tensor(dbias, (N,), "dbias", torch.float32)
-        dx = self._fused_tensor(dx, (M, K), "dx", make=True, stream=stream)
+        pdy = _fused_ptr(dy, (M, N), index, "dy")
+        if dx is None:
+            dx = self._fused_new((M, K), index, stream)
+        head = (fmt, pdy, _fused_ptr(z, (M, N), index, "z"), *self._fused_weights(), _act(act),
+                _fused_ptr(dx, (M, K), index, "dx"),
+                _fused_ptr(dbias, (N,), index, "dbias", _F32), M, N, K)
         if M:
-            self._fused_call(lambda ws, st: qlinear_linear_backward(
-                fmt, dy, z, self.qweight, self.p0, self.p1, dx, M, N, K, ws, act, dbias, st),
-                M, True, workspace, stream)
+            self._fused_call(_lib.qlinear_linear_backward, "qlinear_linear_backward", head, M,
+                             True, workspace, stream)
         elif dbias is not None:
-            with torch.cuda.stream(_as_stream(stream, dbias.device)):
+            with torch.cuda.stream(_as_stream(stream, index)):
                 dbias.zero_()
         return dx
 
@@ -354,7 +400,9 @@ class GatedLinear(_FusedWorkspace):
                            .view(np.uint16), self.device)
         p1 = qlinear_pack_params_gated(fmt, gate[2], up[2], F, K)
         self.p1 = _dev(p1 if fmt == QL_FMT_LUT4 else p1.view(np.uint16), self.device)
-        self._fused_shape = (fmt, 2 * F, K)
+
+    def _fused_matrix(self) -> tuple:
+        return self.fmt, 2 * self.F, self.K
 
     def forward(self, x: torch.Tensor, bias: Optional[torch.Tensor] = None, act: str = "silu",
                 h: Optional[torch.Tensor] = None, gu: Optional[torch.Tensor] = None,
@@ -362,15 +410,19 @@ class GatedLinear(_FusedWorkspace):
         """h[M, F] = act(g) * u, g = x . Wg + bias[0], u = x . Wu + bias[1], in one kernel, for
         any M.  bias: [2, F] or None.  gu ([M, 2, F] fp16), when given, receives g and u for
         ``backward``."""
-        M = x.shape[0]
-        self._fused_tensor(x, (M, self.K), "x")
-        self._fused_tensor(bias, (2, self.F), "bias")
-        self._fused_tensor(gu, (M, 2, self.F), "gu")
-        h = self._fused_tensor(h, (M, self.F), "h", make=True, stream=stream)
+        fmt, _, K, index = self._fused or self._fused_setup()
+        if torch.cuda.current_device() != index:
+            return self._fused_elsewhere(self.forward, x, bias, act, h, gu, workspace, stream)
+        M, F = x.shape[0], self.F
+        px = _fused_ptr(x, (M, K), index, "x")
+        if h is None:
+            h = self._fused_new((M, F), index, stream)
+        head = (fmt, px, *self._fused_weights(), _fused_ptr(bias, (2, F), index, "bias"), _act(act),
+                _fused_ptr(h, (M, F), index, "h"), _fused_ptr(gu, (M, 2, F), index, "gu"), M, F,
+                K)
         if M:
-            self._fused_call(lambda ws, st: qlinear_gated(
-                self.fmt, x, self.qweight, self.p0, self.p1, h, M, self.F, self.K, ws, bias,
-                act, gu, st), M, False, workspace, stream)
+            self._fused_call(_lib.qlinear_gated, "qlinear_gated", head, M, False, workspace,
+                             stream)
         return h
 
     def backward(self, dh: torch.Tensor, gu: torch.Tensor, act: str = "silu",
@@ -378,17 +430,22 @@ class GatedLinear(_FusedWorkspace):
                  workspace: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
         """dx[M, K] of ``forward`` through the frozen weights, from dh and the kept gu; dbias
         (fp32 [2, F]), when given, receives the column sums of the gradients of g and u."""
-        M = dh.shape[0]
-        self._fused_tensor(dh, (M, self.F), "dh")
-        self._fused_tensor(gu, (M, 2, self.F), "gu")
-        self._fused_tensor(dbias, (2, self.F), "dbias", torch.float32)
-        dx = self._fused_tensor(dx, (M, self.K), "dx", make=True, stream=stream)
+        fmt, _, K, index = self._fused or self._fused_setup()
+        if torch.cuda.current_device() != index:
+            return self._fused_elsewhere(self.backward, dh, gu, act, dx, dbias, workspace,
+                                         stream)
+        M, F = dh.shape[0], self.F
+        pdh = _fused_ptr(dh, (M, F), index, "dh")
+        if dx is None:
+            dx = self._fused_new((M, K), index, stream)
+        head = (fmt, pdh, _fused_ptr(gu, (M, 2, F), index, "gu"), *self._fused_weights(), _act(act),
+                _fused_ptr(dx, (M, K), index, "dx"),
+                _fused_ptr(dbias, (2, F), index, "dbias", _F32), M, F, K)
         if M:
-            self._fused_call(lambda ws, st: qlinear_gated_backward(
-                self.fmt, dh, gu, self.qweight, self.p0, self.p1, dx, M, self.F, self.K, ws,
-                act, dbias, st), M, True, workspace, stream)
+            self._fused_call(_lib.qlinear_gated_backward, "qlinear_gated_backward", head, M,
+                             True, workspace, stream)
         elif dbias is not None:
-            with torch.cuda.stream(_as_stream(stream, dbias.device)):
+            with torch.cuda.stream(_as_stream(stream, index)):
                 dbias.zero_()
         return dx
 
