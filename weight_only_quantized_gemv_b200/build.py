@@ -18,7 +18,8 @@ LIB = os.path.join(PKG, "libqlinear.so")
 
 SOURCES = ["qlinear.cu", "dequant.cu", "prefill_tc.cu", "codebook.cu", "fused.cu", "fused_tc.cu",
            "policy.cpp", "pack.cpp"]
-HEADERS = ["kernels.cuh", "layout.h", "policy.h", "dequant_frag.cuh", "act.cuh", "fused.h"]
+HEADERS = ["kernels.cuh", "layout.h", "policy.h", "dequant_frag.cuh", "act.cuh", "fused.h",
+           "tc.cuh"]
 
 
 def nvcc_path() -> str:

@@ -82,6 +82,7 @@ __global__ void __launch_bounds__(32 * kGradWarps) grad_kernel(const GradParams 
   for (int b = 0; b < NB; ++b)
 #pragma unroll
     for (int e = 0; e < 8; ++e) sum[b][e] = 0.f;
+  qlk::grid_dependents_launch();
   qlk::grid_dependency_wait();
   if (in) {
     for (int m = m0 + warp; m < m1; m += kGradWarps) {
