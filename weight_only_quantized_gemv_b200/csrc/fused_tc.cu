@@ -78,9 +78,12 @@ struct TcCfg {
   static_assert(SC >= 2, "code ring");
   static constexpr int kRingC = S * kStageBytes;
   static constexpr int kBarOff = kRingC + SC * kSlot;
-  // full[S] empty[S] accf[2] acce[2] fin cfull[SC] cempty[SC], tensor memory base, abort, lut
-  static constexpr int kMiscOff = kBarOff + 8 * (2 * S + 5 + 2 * SC);
-  static constexpr int kLutOff = kMiscOff + 16;
+  // full[S] empty[S] accf[2] acce[2] fin cfull[SC] cempty[SC] tail[4][2] last; then the tensor
+  // memory's base, the abort flag, arrivals before the last segment's per quadrant; the table
+  static constexpr int kTailBar = 2 * S + 5 + 2 * SC;
+  static constexpr int kLastBar = kTailBar + 8;
+  static constexpr int kMiscOff = kBarOff + 8 * (kLastBar + 1);
+  static constexpr int kLutOff = kMiscOff + 24;
   static constexpr int kSmem = kLutOff + 64 + 1024;
   static_assert(kSmem <= 232448, "shared memory");
   static constexpr int kEpiWarp0 = 4, kDqWarp0 = 8;
@@ -110,21 +113,21 @@ struct TcParams {
 // The work of a worker (CTA or pair): whole tiles w, w + W, ..., then its run of the stages of
 // tiles [whole, tiles), cut at tile boundaries.
 struct Segments {
-  long long u, u1;
-  int t, w, W;
-  bool first;  // no stage of the run has been handed out yet
-  __device__ __forceinline__ void init(const TcParams& P, int w_, int W_) {
-    w = w_;
+  int t, W;         // next whole tile of this worker, workers
+  int rt, rk, left; // the run: next tile and stage, stages left
+  bool first;       // no stage of the run has been handed out yet
+  __device__ __forceinline__ void init(const TcParams& P, int w, int W_) {
     W = W_;
-    t = w_;
+    t = w;
     const long long U = (long long)(P.tiles - P.whole) * P.steps;
-    u = w * U / W;
-    u1 = (w + 1) * U / W;
+    const long long u = w * U / W_;
+    left = (int)((w + 1) * U / W_ - u);
+    rt = P.whole + (int)(u / P.steps);
+    rk = (int)(u % P.steps);
     first = true;
   }
   // tile, stages [k0, k1); slot: workspace slot of a partial sum (0: the run's first segment)
   __device__ __forceinline__ bool next(const TcParams& P, int& tile, int& k0, int& k1, int& slot) {
-    slot = 0;
     if (t < P.whole) {
       tile = t;
       t += W;
@@ -132,15 +135,18 @@ struct Segments {
       k1 = P.steps;
       return true;
     }
-    if (u >= u1) return false;
-    const int tt = (int)(u / P.steps);
-    tile = P.whole + tt;
-    k0 = (int)(u - (long long)tt * P.steps);
-    k1 = (u1 - u < (long long)(P.steps - k0)) ? k0 + (int)(u1 - u) : P.steps;
-    u += k1 - k0;
+    if (left <= 0) return false;
+    tile = rt++;
+    k0 = rk;
+    k1 = left < P.steps - rk ? rk + left : P.steps;
+    left -= k1 - k0;
+    rk = 0;
     slot = first ? 0 : 1;
     first = false;
     return true;
+  }
+  __device__ __forceinline__ bool done(const TcParams& P) const {  // no segment is left
+    return t >= P.whole && left <= 0;
   }
 };
 
@@ -153,30 +159,23 @@ __device__ __forceinline__ int worker_of(long long u, long long U, int W) {
 // bounded waits
 
 struct WaitCtx {
-  volatile uint32_t* abort;  // shared memory
-  uint32_t* err;             // global memory
+  uint32_t abort;  // shared-memory address of the CTA's abort flag
+  uint32_t* err;   // global memory
 };
 constexpr uint64_t kWaitNs = 100ull * 1000 * 1000;
 
-__device__ __noinline__ bool wait_slow(uint32_t bar, uint32_t parity, WaitCtx w, uint32_t bit,
-                                       bool cluster, bool patient, bool honor_abort) {
+__device__ __noinline__ bool wait_slow(uint32_t bar, uint32_t parity, uint32_t abort, uint32_t* err,
+                                       uint32_t bit, bool cluster, bool honor_abort) {
   uint64_t t0 = 0;
   for (uint32_t it = 0;; ++it) {
-    if (patient && it >= 64) {  // long waits: suspend up to 500 ns at a time
-      uint32_t done;
-      asm volatile(
-          "{\n\t.reg .pred p;\n\t"
-          "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
-          "selp.u32 %0, 1, 0, p;\n\t}"
-          : "=r"(done)
-          : "r"(bar), "r"(parity), "r"(500u)
-          : "memory");
-      if (done) return true;
-    }
     if (mbar_ready(bar, parity, cluster)) return true;
-    if (it >= 256) __nanosleep(32);
+    if (it >= 256) __nanosleep(32);  // leave the issue slots to the working warps
     if ((it & 63u) == 63u) {
-      if (honor_abort && *w.abort) break;
+      if (honor_abort) {
+        uint32_t a;
+        asm volatile("ld.volatile.shared.u32 %0, [%1];" : "=r"(a) : "r"(abort) : "memory");
+        if (a) break;
+      }
       const uint64_t now = globaltimer_ns();
       if (t0 == 0)
         t0 = now;
@@ -184,24 +183,23 @@ __device__ __noinline__ bool wait_slow(uint32_t bar, uint32_t parity, WaitCtx w,
         break;
     }
   }
-  atomicOr(w.err, bit);
-  *w.abort = 1u;
+  atomicOr(err, bit);
+  asm volatile("st.volatile.shared.u32 [%0], %1;" ::"r"(abort), "r"(1u) : "memory");
   return false;
 }
 
 __device__ __forceinline__ bool wait(uint32_t bar, uint32_t parity, const WaitCtx& w, uint32_t bit,
-                                     bool cluster = false, bool patient = false,
-                                     bool honor_abort = true) {
+                                     bool cluster = false, bool honor_abort = true) {
   if (mbar_ready(bar, parity, cluster)) return true;
-  return wait_slow(bar, parity, w, bit, cluster, patient, honor_abort);
+  return wait_slow(bar, parity, w.abort, w.err, bit, cluster, honor_abort);
 }
 
 // A whole warp: every lane sees the phase complete (the usual case), or one lane waits.
 __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, const WaitCtx& w,
-                                          uint32_t bit, int lane, bool patient = false) {
+                                          uint32_t bit, int lane, bool honor_abort = true) {
   if (__all_sync(0xffffffffu, mbar_ready(bar, parity, false))) return true;
   bool ok = true;
-  if (lane == 0) ok = wait_slow(bar, parity, w, bit, false, patient, true);
+  if (lane == 0) ok = wait_slow(bar, parity, w.abort, w.err, bit, false, honor_abort);
   return __shfl_sync(0xffffffffu, ok, 0);
 }
 
@@ -212,21 +210,20 @@ __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, const W
 // pairs in the order 1, 0, 3, 2: the eight lanes of a store phase (two rows, four t) then
 // write eight distinct granules, without bank conflicts.
 
-template <int FMT>
-__device__ __forceinline__ uint32_t a_address(uint32_t a, int row, int i, int t) {
-  return a + (i >> 1) * (128 * 128) + row * 128 + (((4 * (i & 1) + t) ^ (row & 7)) << 4);
-}
+struct Decoded {
+  uint4 v[4][2];  // [pair of steps, in the lane's order][row gi, gi + 8]
+};
 
 template <class C>
-__device__ __forceinline__ void decode_tile(uint32_t slot, uint32_t a, int tile, int lane,
-                                            const float* lut) {
+__device__ __forceinline__ void decode_tile(uint32_t slot, int tile, int lane, const float* lut,
+                                            Decoded& d) {
   constexpr int FMT = C::FMT;
   constexpr int KW = qlk::Fmt<FMT>::kWords, KP = KW / 4;  // words per lane, per step pair
-  const int gi = lane >> 2, t = lane & 3;
+  const int gi = lane >> 2;
   const int swap = gi & 1;
   uint32_t w[KW];
   const uint32_t cs = slot + tile * C::kChunk + lane * 16;
-  if constexpr (FMT == kW8) {  // a quad is a pair: the swap is in the address
+  if constexpr (FMT == kW8) {  // a quad is a pair: the order is in the address
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const uint4 v = qlk::lds128(cs + (i ^ swap) * 512);
@@ -256,11 +253,10 @@ __device__ __forceinline__ void decode_tile(uint32_t slot, uint32_t a, int tile,
 #pragma unroll
     for (int i = 0; i < 4; ++i)
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const float m = __uint_as_float(i >= 2 ? (h ? am.w : am.z) : (h ? am.y : am.x));
-        const uint4 v = qdq::lut_pair8(w + KP * i, 0, h, lut, m);
-        sts128(a_address<FMT>(a, 16 * tile + gi + 8 * h, i ^ swap, t), v);
-      }
+      for (int h = 0; h < 2; ++h)
+        d.v[i][h] = qdq::lut_pair8(
+            w + KP * i, 0, h, lut,
+            __uint_as_float(i >= 2 ? (h ? am.w : am.z) : (h ? am.y : am.x)));
   } else {
     const __half2 s2 = qdq::u32_as_h2(qlk::lds32(pa + gi * 4));
     const __half2 z2 = qdq::u32_as_h2(qlk::lds32(pa + kBlockTiles * C::kParChunk + gi * 4));
@@ -270,75 +266,143 @@ __device__ __forceinline__ void decode_tile(uint32_t slot, uint32_t a, int tile,
 #pragma unroll
     for (int i = 0; i < 4; ++i)
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const uint4 v = qdq::uniform_pair8<FMT>(w + KP * i, 0, h, zb, h ? sh : sl);
-        sts128(a_address<FMT>(a, 16 * tile + gi + 8 * h, i ^ swap, t), v);
-      }
+      for (int h = 0; h < 2; ++h)
+        d.v[i][h] = qdq::uniform_pair8<FMT>(w + KP * i, 0, h, zb, h ? sh : sl);
   }
 }
 
-// Rows of a tile past the last column, contracted in the backward product: zeros.
-template <int FMT>
-__device__ __forceinline__ void zero_tile(uint32_t a, int tile, int lane) {
+__device__ __forceinline__ void store_tile(uint32_t a, int tile, int lane, const Decoded& d) {
   const int gi = lane >> 2, t = lane & 3;
+  const uint32_t row = a + (16 * tile + gi) * 128;
+  // granule 4 (pair mod 2) + t of a row, at granule ^ (row mod 8) = ^ gi
+  const uint32_t g0 = ((uint32_t)((4 * (gi & 1) + t) ^ gi)) << 4, g1 = g0 ^ 64u;
 #pragma unroll
   for (int i = 0; i < 4; ++i)
 #pragma unroll
     for (int h = 0; h < 2; ++h)
-      sts128(a_address<FMT>(a, 16 * tile + gi + 8 * h, i ^ (gi & 1), t), make_uint4(0, 0, 0, 0));
+      sts128(row + (i >> 1) * (128 * 128) + h * 8 * 128 + ((i & 1) ? g1 : g0), d.v[i][h]);
 }
 
 // ---------------------------------------------------------------------------
-// epilogue: 16 tokens (m0 .. m0 + count - 1 of them real) of one row per lane
+// epilogue: kTok tokens m0 .. (the first `count` of them real) of one row per lane
 
-__device__ __forceinline__ void finish16(const TcParams& P, const float (&v)[16], int m0, int count,
-                                         int row) {
+constexpr int kTok = 8;
+
+// One row's values to tokens `stride` elements apart.
+__device__ __forceinline__ void store_tokens(__half* o, size_t stride, const float (&v)[kTok],
+                                             int count) {
+  if (count >= kTok) {
+#pragma unroll
+    for (int e = 0; e < kTok; ++e, o += stride) *o = __float2half_rn(v[e]);
+  } else {
+#pragma unroll
+    for (int e = 0; e < kTok - 1; ++e, o += stride)
+      if (e < count) *o = __float2half_rn(v[e]);
+  }
+}
+
+template <int ACT, int N>
+__device__ __forceinline__ void act_each(float (&v)[N]) {
+#pragma unroll
+  for (int e = 0; e < N; ++e) v[e] = qact::act_forward(ACT, v[e]);
+}
+template <int N>
+__device__ __forceinline__ void act_all(int act, float (&v)[N]) {  // one branch for all values
+  switch (act) {
+    case QL_ACT_RELU: return act_each<QL_ACT_RELU>(v);
+    case QL_ACT_GELU: return act_each<QL_ACT_GELU>(v);
+    case QL_ACT_GELU_TANH: return act_each<QL_ACT_GELU_TANH>(v);
+    case QL_ACT_SILU: return act_each<QL_ACT_SILU>(v);
+    default: return;
+  }
+}
+
+// rows alternate 16 gate / 16 up: the lanes exchange, per pair of tokens, so that the gate
+// lanes finish the even token and the up lanes the odd one
+__device__ __forceinline__ void finish_gated(const TcParams& P, float (&v)[kTok], int m0, int count,
+                                             int row, float bias) {
   const qfused::Epilogue& E = P.epi;
   const bool in = row < P.rows;
-  if (E.gated) {
-    // rows alternate 16 gate / 16 up; the lanes exchange, per pair of tokens, so that the gate
-    // lanes finish the even token and the up lanes the odd one
-    const int F = P.ld, f = (row >> 5) * 16 + (row & 15), up = (row >> 4) & 1;
-    const float bias = in && E.bias ? __half2float(E.bias[(size_t)up * F + f]) : 0.f;
+  const int F = P.ld, f = (row >> 5) * 16 + (row & 15), up = (row >> 4) & 1;
 #pragma unroll
-    for (int e = 0; e < 16; e += 2) {
-      const float z0 = v[e] + bias, z1 = v[e + 1] + bias;
-      if (E.zsave && in) {
-        __half* o = E.zsave + ((size_t)(m0 + e) * 2 + up) * F + f;
-        if (e < count) o[0] = __float2half_rn(z0);
-        if (e + 1 < count) o[(size_t)2 * F] = __float2half_rn(z1);
-      }
-      const float other = __shfl_xor_sync(0xffffffffu, up ? z0 : z1, 16);
-      const float g = up ? other : z0, u = up ? z1 : other;
-      if (in && e + up < count)
-        E.y[(size_t)(m0 + e + up) * F + f] = __float2half_rn(qact::act_forward(E.act, g) * u);
-    }
-    return;
+  for (int e = 0; e < kTok; ++e) v[e] += bias;
+  if (E.zsave && in)
+    store_tokens(E.zsave + ((size_t)m0 * 2 + up) * F + f, (size_t)2 * F, v, count);
+  float g[kTok / 2], u[kTok / 2];
+#pragma unroll
+  for (int e = 0; e < kTok / 2; ++e) {
+    const float other = __shfl_xor_sync(0xffffffffu, up ? v[2 * e] : v[2 * e + 1], 16);
+    g[e] = up ? other : v[2 * e];
+    u[e] = up ? v[2 * e + 1] : other;
   }
+  act_all(E.act, g);
   if (!in) return;
-  const float bias = E.bias ? __half2float(E.bias[row]) : 0.f;
-  const size_t o = (size_t)m0 * P.ld + row;
-  float r[16];
+  __half* o = E.y + (size_t)(m0 + up) * F + f;
 #pragma unroll
-  for (int e = 0; e < 16; ++e)
-    r[e] = E.residual && e < count ? __half2float(E.residual[o + (size_t)e * P.ld]) : 0.f;
-#pragma unroll
-  for (int e = 0; e < 16; ++e) {
-    if (e >= count) break;
-    const float z = v[e] + bias;
-    if (E.zsave) E.zsave[o + (size_t)e * P.ld] = __float2half_rn(z);
-    E.y[o + (size_t)e * P.ld] = __float2half_rn(qact::act_forward(E.act, z) + r[e]);
-  }
+  for (int e = 0; e < kTok / 2; ++e, o += 2 * (size_t)F)
+    if (2 * e + up < count) *o = __float2half_rn(g[e] * u[e]);
 }
 
-// A-operand descriptor of the backward product: MN-major, 128-byte swizzle, 64-wide MN panels
-// 16384 bytes apart (leading offset), 8-row groups of the contraction 1024 bytes apart
-// (stride).  Forward: K-major (desc_sw128).
-__device__ __forceinline__ uint64_t desc_mn(uint32_t addr) {
-  return (uint64_t)((addr >> 4) & 0x3FFFu) | ((uint64_t)(128 * 128 / 16) << 16) | (64ull << 32) |
-         (1ull << 46) | (2ull << 61);
+__device__ __forceinline__ void load_residual(const TcParams& P, __half (&r)[kTok], int m0,
+                                              int count, int row) {
+  if (!P.epi.residual || row >= P.rows) return;
+  const __half* o = P.epi.residual + (size_t)m0 * P.ld + row;
+#pragma unroll
+  for (int e = 0; e < kTok; ++e, o += P.ld)
+    if (e < count) r[e] = *o;
 }
+
+// residual: the row's values, loaded ahead
+__device__ __forceinline__ void finish(const TcParams& P, float (&v)[kTok], int m0, int count,
+                                       int row, float bias, const __half (&residual)[kTok]) {
+  const qfused::Epilogue& E = P.epi;
+  if (row >= P.rows) return;
+  const size_t o = (size_t)m0 * P.ld + row;
+#pragma unroll
+  for (int e = 0; e < kTok; ++e) v[e] += bias;
+  if (E.zsave) store_tokens(E.zsave + o, P.ld, v, count);
+  act_all(E.act, v);
+  if (E.residual) {
+#pragma unroll
+    for (int e = 0; e < kTok; ++e) v[e] += __half2float(residual[e]);
+  }
+  store_tokens(E.y + o, P.ld, v, count);
+}
+
+__device__ __forceinline__ void tmem_ld8(uint32_t taddr, uint32_t (&r)[8]) {
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]),
+                 "=r"(r[6]), "=r"(r[7])
+               : "r"(taddr)
+               : "memory");
+}
+
+// Operand descriptors, in two words: the low one holds the address (16-byte units) and the
+// leading offset, the high one is the same for all (stride 1024 bytes between 8-row groups,
+// 128-byte swizzle).  K-major rows of 128 bytes; the backward product reads A MN-major: its
+// 64-wide MN panels are 16384 bytes apart (leading offset).
+constexpr uint32_t kDescHi = 64u | (1u << 14) | (2u << 29);
+constexpr uint32_t kDescLoK = 1u << 16, kDescLoMn = (128u * 128u / 16u) << 16;
 constexpr uint32_t kTransposeA = 1u << 15;  // instruction descriptor: A is MN-major
+
+template <bool PAIR>
+__device__ __forceinline__ void mma(uint32_t d, uint32_t alo, uint32_t blo, uint32_t idesc,
+                                    uint32_t accumulate) {
+  if constexpr (PAIR)
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t.reg .b64 a, b;\n\t"
+        "setp.ne.b32 p, %5, 0;\n\tmov.b64 a, {%1, %4};\n\tmov.b64 b, {%2, %4};\n\t"
+        "tcgen05.mma.cta_group::2.kind::f16 [%0], a, b, %3, p;\n\t}" ::"r"(d),
+        "r"(alo), "r"(blo), "r"(idesc), "r"(kDescHi), "r"(accumulate)
+        : "memory");
+  else
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t.reg .b64 a, b;\n\t"
+        "setp.ne.b32 p, %5, 0;\n\tmov.b64 a, {%1, %4};\n\tmov.b64 b, {%2, %4};\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, p;\n\t}" ::"r"(d),
+        "r"(alo), "r"(blo), "r"(idesc), "r"(kDescHi), "r"(accumulate)
+        : "memory");
+}
 
 template <int BNX, int FMT, bool PAIR, bool BWD>
 __global__ void __launch_bounds__(TcCfg<BNX, FMT, PAIR>::kThreads, 1)
@@ -356,9 +420,10 @@ __global__ void __launch_bounds__(TcCfg<BNX, FMT, PAIR>::kThreads, 1)
   const uint32_t fin = bars + 8 * (2 * C::S + 4);
   auto cfull = [&](int c) { return bars + 8 * (2 * C::S + 5 + c); };
   auto cempty = [&](int c) { return bars + 8 * (2 * C::S + 5 + C::SC + c); };
+  const uint32_t lastf = bars + 8 * C::kLastBar;  // the worker's last accumulator is complete
   volatile uint32_t* misc = reinterpret_cast<volatile uint32_t*>(smem + C::kMiscOff);
   float* lut = reinterpret_cast<float*>(smem + C::kLutOff);
-  const WaitCtx W{misc + 1, P.err};
+  const WaitCtx W{ring + C::kMiscOff + 4, P.err};
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = PAIR ? cluster_rank() : 0u;
   const bool leader = rank == 0;
@@ -392,6 +457,11 @@ __global__ void __launch_bounds__(TcCfg<BNX, FMT, PAIR>::kThreads, 1)
       qlk::mbar_init(acce(a), C::kAccEmptyCount);
     }
     qlk::mbar_init(fin, 1);
+    qlk::mbar_init(lastf, 1);
+    for (int i = 0; i < 4; ++i) {
+      qlk::mbar_init(bars + 8 * C::kTailBar + 16 * i, 5);
+      qlk::mbar_init(bars + 8 * C::kTailBar + 16 * i + 8, 1);
+    }
     misc[1] = 0u;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
@@ -439,7 +509,7 @@ __global__ void __launch_bounds__(TcCfg<BNX, FMT, PAIR>::kThreads, 1)
       // no copy is in flight when the CTA exits (the leader's barriers count both CTAs')
       if (leader)
         for (int i = n > C::S ? n - C::S : 0; i < n; ++i)
-          wait(full(i % C::S), (i / C::S) & 1, W, kErrStage, PAIR, false, false);
+          wait(full(i % C::S), (i / C::S) & 1, W, kErrStage, PAIR, false);
     }
   } else if (warp == 2) {
     // ---- copies of the units' codes and parameters
@@ -484,7 +554,7 @@ __global__ void __launch_bounds__(TcCfg<BNX, FMT, PAIR>::kThreads, 1)
         }
       }
       for (int i = n > C::SC ? n - C::SC : 0; i < n; ++i)
-        wait(cfull(i % C::SC), (i / C::SC) & 1, W, kErrStage, false, false, false);
+        wait(cfull(i % C::SC), (i / C::SC) & 1, W, kErrStage, false, false);
     }
   } else if (warp == 1) {
     // ---- MMA issue (the leader of a pair)
@@ -492,136 +562,206 @@ __global__ void __launch_bounds__(TcCfg<BNX, FMT, PAIR>::kThreads, 1)
       qlk::grid_dependency_wait();
       const uint32_t idesc = idesc_f16(128 * C::kCtas, P.bn) | (BWD ? kTransposeA : 0u);
       int s = 0, ph = 0, j = 0;
-      bool ok = true;
+      bool ok = true, ready = false;
       for (; ok && sg.next(P, tile, k0, k1, slot); ++j) {
         const int a = j & 1;
         if (j >= 2 && !(ok = wait(acce(a), ((j >> 1) - 1) & 1, W, kErrAcc, PAIR))) break;
         tc_fence_after();
         const uint32_t d = tmem + (uint32_t)(a * BNX);
         for (int k = k0; k < k1; ++k) {
-          if (!(ok = wait(full(s), ph, W, kErrStage, PAIR))) break;
+          if (!ready && !(ok = wait(full(s), ph, W, kErrStage, PAIR))) break;
           tc_fence_after();
-          const uint32_t pa = ring + s * C::kStageBytes, pb = pa + C::kABytes;
+          const uint32_t st = (ring + s * C::kStageBytes) >> 4;
+          const uint32_t pa = st | (BWD ? kDescLoMn : kDescLoK);
+          const uint32_t pb = (st + (C::kABytes >> 4)) | kDescLoK;
+          const int s1 = s + 1 == C::S ? 0 : s + 1, ph1 = s + 1 == C::S ? ph ^ 1 : ph;
+          // the next stage's barrier is looked at while this stage's MMAs are issued
+          ready = mbar_ready(full(s1), ph1, PAIR);
 #pragma unroll
-          for (int kk = 0; kk < 8; ++kk) {
-            const uint64_t ad = BWD ? desc_mn(pa + 2048 * kk)
-                                    : desc_sw128(pa + (kk >> 2) * C::kHalfA + 32 * (kk & 3));
-            const uint64_t bd = desc_sw128(pb + (kk >> 2) * C::kHalfB + 32 * (kk & 3));
-            tc_mma<PAIR>(d, ad, bd, idesc, (k != k0) || (kk != 0));
-          }
+          for (int kk = 0; kk < 8; ++kk)
+            mma<PAIR>(d, pa + (BWD ? 128 * kk : (kk >> 2) * (C::kHalfA >> 4) + 2 * (kk & 3)),
+                      pb + (kk >> 2) * (C::kHalfB >> 4) + 2 * (kk & 3), idesc,
+                      kk == 0 ? (uint32_t)(k != k0) : 1u);
           commit_both(empty(s));
-          if (++s == C::S) {
-            s = 0;
-            ph ^= 1;
-          }
+          s = s1;
+          ph = ph1;
         }
-        if (ok) commit_both(accf(a));
+        if (ok) commit_both(sg.done(P) ? lastf : accf(a));
       }
       tc_commit<PAIR>(fin);
-      wait(fin, 0, W, kErrAcc, false, false, false);
-    }
-  } else if (warp >= C::kDqWarp0) {
-    // ---- decoding teams
-    const int team = (warp - C::kDqWarp0) / kTeamWarps, dt = (warp - C::kDqWarp0) % kTeamWarps;
-    int n = 0, s = 0, sph = 1, c = 0, cph = 0;
-    bool ok = true;
-    while (ok && sg.next(P, tile, k0, k1, slot)) {
-      const int rb = (tile / P.mtiles) * C::kCtas + (int)rank;
-      for (int k = k0; k < k1; ++k, ++n) {
-        if ((n & 1) == team) {
-          const int tb = rb < P.rblocks ? tiles_in_block(BWD ? k : rb, P.ntiles) : 0;
-          if (n >= C::S) {
-            if (n <= C::S + 1) qlk::grid_dependency_wait();
-            if (!(ok = warp_wait(empty(s), sph, W, kErrStage, lane))) break;
-          }
-          if (!(ok = warp_wait(cfull(c), cph, W, kErrStage, lane))) break;
-          const uint32_t a = ring + s * C::kStageBytes;
-          if (dt < tb)
-            decode_tile<C>(ring + C::kRingC + c * C::kSlot, a, dt, lane, lut);
-          else if (BWD)
-            zero_tile<FMT>(a, dt, lane);
-          asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // visible to the MMAs
-          __syncwarp();
-          if (lane == 0) {
-            qlk::mbar_arrive(cempty(c));
-            arrive_lead(full(s));
-          }
-        }
-        if (++s == C::S) {
-          s = 0;
-          sph ^= 1;
-        }
-        if (++c == C::SC) {
-          c = 0;
-          cph ^= 1;
-        }
-      }
+      wait(fin, 0, W, kErrAcc, false, false);
     }
   } else if (warp >= C::kEpiWarp0) {
-    // ---- epilogue: accumulator lanes 32 q .. 32 q + 31
+    const bool decoder = warp >= C::kDqWarp0;
+    int j = 0;  // segment
+    bool ok = true;
+    if (decoder) {
+      // ---- decoding teams
+      const int team = (warp - C::kDqWarp0) / kTeamWarps;
+      const int dt = (warp - C::kDqWarp0) % kTeamWarps;
+      int n = 0, s = 0, sph = 1, c = 0, cph = 0;
+      for (; ok && sg.next(P, tile, k0, k1, slot); ++j) {
+        const int rb = (tile / P.mtiles) * C::kCtas + (int)rank;
+        for (int k = k0; k < k1; ++k, ++n) {
+          if ((n & 1) == team) {
+            const int tb = rb < P.rblocks ? tiles_in_block(BWD ? k : rb, P.ntiles) : 0;
+            // decode into registers while the MMAs may still read the stage
+            if (!(ok = warp_wait(cfull(c), cph, W, kErrStage, lane))) break;
+            Decoded d;
+            if (dt < tb) {
+              decode_tile<C>(ring + C::kRingC + c * C::kSlot, dt, lane, lut, d);
+            } else if (BWD) {  // rows past the last column are contracted: zeros
+#pragma unroll
+              for (int i = 0; i < 8; ++i) d.v[i >> 1][i & 1] = make_uint4(0, 0, 0, 0);
+            }
+            if (n >= C::S) {
+              if (n <= C::S + 1) qlk::grid_dependency_wait();
+              if (!(ok = warp_wait(empty(s), sph, W, kErrStage, lane))) break;
+            }
+            if (BWD || dt < tb) store_tile(ring + s * C::kStageBytes, dt, lane, d);
+            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // visible to the MMAs
+            __syncwarp();
+            if (lane == 0) {
+              qlk::mbar_arrive(cempty(c));
+              arrive_lead(full(s));
+            }
+          }
+          if (++s == C::S) {
+            s = 0;
+            sph ^= 1;
+          }
+          if (++c == C::SC) {
+            c = 0;
+            cph ^= 1;
+          }
+        }
+      }
+      --j;
+    }
+    // ---- epilogue: accumulator lanes 32 q .. 32 q + 31, the tokens in chunks of kTok.  The
+    // four epilogue warps take every segment but the worker's last, while the next one is
+    // multiplied; nothing follows the last, so the decoding warps share its chunks.
     qlk::grid_dependency_wait();
     const int q = warp & 3;
+    const int member = decoder ? 1 + (warp - C::kDqWarp0) / 4 : 0;  // of the quadrant's five
+    const uint32_t tail = bars + 8 * C::kTailBar + 16 * q;          // two barriers
     const long long U = (long long)(P.tiles - P.whole) * P.steps;
-    for (int j = 0; sg.next(P, tile, k0, k1, slot); ++j) {
+    const qfused::Epilogue& E = P.epi;
+    for (; ok; ++j) {
+      if (!decoder && !sg.next(P, tile, k0, k1, slot)) break;
+      const bool last = decoder || sg.done(P);
       const int a = j & 1;
-      if (!warp_wait(accf(a), (j >> 1) & 1, W, kErrAcc, lane, true)) break;
+      // the last accumulator has a barrier of its own, which completes once: the decoding warps
+      // have not followed the phases of the others (the five see it complete, or all time out)
+      if (!(last ? warp_wait(lastf, 0, W, kErrAcc, lane, false)
+                 : warp_wait(accf(a), (j >> 1) & 1, W, kErrAcc, lane)))
+        break;
       tc_fence_after();
       const int lrow = 32 * q + lane;
       const int row = ((tile / P.mtiles) * C::kCtas + (int)rank) * 128 + lrow;
       const int m0 = (tile % P.mtiles) * P.bn;
       const int cols = P.M - m0 < P.bn ? P.M - m0 : P.bn;
       const uint32_t tb = tmem + ((uint32_t)(32 * q) << 16) + (uint32_t)(a * BNX);
-      if (k0 == 0 && k1 == P.steps) {
-        for (int c0 = 0; c0 < cols; c0 += 16) {
-          uint32_t r[16];
-          tmem_ld16(tb + (uint32_t)c0, r);
+      const int step = last ? 5 * kTok : kTok, c_first = last ? member * kTok : 0;
+      float bias = 0.f;
+      if (E.bias && row < P.rows)
+        bias = __half2float(E.bias[E.gated ? (size_t)((row >> 4) & 1) * P.ld + (row >> 5) * 16 +
+                                                 (row & 15)
+                                           : (size_t)row]);
+      const bool whole = k0 == 0 && k1 == P.steps;
+      int wf = 0, wl = 0;
+      long long ub = 0;
+      uint32_t* counter = nullptr;
+      if (!whole) {
+        // part of a tile: partial sums [token / 4][row][token mod 4]; the last contributor of
+        // the tile goes on, with the sums in place of the accumulator
+        float* mine = P.partials + (size_t)(2 * blockIdx.x + slot) * 128 * P.bn + 4 * lrow;
+        for (int c0 = c_first; c0 < cols; c0 += step) {
+          uint32_t r[8];
+          tmem_ld8(tb + (uint32_t)c0, r);
           tc_wait_ld();
-          float v[16];
 #pragma unroll
-          for (int e = 0; e < 16; ++e) v[e] = __uint_as_float(r[e]);
-          finish16(P, v, m0 + c0, cols - c0, row);
+          for (int e = 0; e < kTok; e += 4)
+            __stcg(reinterpret_cast<uint4*>(mine + (size_t)(c0 + e) * 128),
+                   make_uint4(r[e], r[e + 1], r[e + 2], r[e + 3]));
         }
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) arrive_lead(acce(a));
-        continue;
-      }
-      // part of a tile: [token][row] partial sums, one row of 128 per token
-      float* mine = P.partials + (size_t)(2 * blockIdx.x + slot) * 128 * P.bn + lrow;
-      for (int c0 = 0; c0 < cols; c0 += 16) {
-        uint32_t r[16];
-        tmem_ld16(tb + (uint32_t)c0, r);
-        tc_wait_ld();
-#pragma unroll
-        for (int e = 0; e < 16; ++e)
-          if (c0 + e < cols) __stcg(mine + (size_t)(c0 + e) * 128, __uint_as_float(r[e]));
-      }
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) arrive_lead(acce(a));
-      const long long ub = (long long)(tile - P.whole) * P.steps;
-      const int wf = worker_of(ub, U, nwk), wl = worker_of(ub + P.steps - 1, U, nwk);
-      uint32_t* counter = P.counters + ((size_t)(tile - P.whole) * C::kCtas + rank) * 4 + q;
-      uint32_t prev = 0;
-      if (lane == 0) prev = qlk::arrive_acq_rel(counter);
-      prev = __shfl_sync(0xffffffffu, prev, 0);
-      if (prev + 1 != (uint32_t)(wl - wf + 1)) continue;
-      __syncwarp();
-      for (int c0 = 0; c0 < cols; c0 += 16) {
-        float v[16];
-#pragma unroll
-        for (int e = 0; e < 16; ++e) v[e] = 0.f;
-        for (int w = wf; w <= wl; ++w) {
-          const int cta = w * C::kCtas + (int)rank;
-          const int sl = run_begin(w, U, nwk) >= ub ? 0 : 1;
-          const float* src = P.partials + (size_t)(2 * cta + sl) * 128 * P.bn + lrow;
-#pragma unroll
-          for (int e = 0; e < 16; ++e)
-            if (c0 + e < cols) v[e] += __ldcg(src + (size_t)(c0 + e) * 128);
+        ub = (long long)(tile - P.whole) * P.steps;
+        wf = worker_of(ub, U, nwk);
+        wl = worker_of(ub + P.steps - 1, U, nwk);
+        counter = P.counters + ((size_t)(tile - P.whole) * C::kCtas + rank) * 4 + q;
+        uint32_t prev = 0;
+        if (!last) {
+          if (lane == 0) {
+            arrive_lead(acce(a));
+            prev = qlk::arrive_acq_rel(counter);
+          }
+          prev = __shfl_sync(0xffffffffu, prev, 0);
+        } else {
+          // the five warps' sums are written, then one arrival for all of them
+          if (lane == 0) qlk::mbar_arrive(tail);
+          if (member == 0) {
+            if (!warp_wait(tail, 0, W, kErrAcc, lane, false)) break;
+            if (lane == 0) {
+              misc[2 + q] = qlk::arrive_acq_rel(counter);
+              qlk::mbar_arrive(tail + 8);
+            }
+          }
+          if (!warp_wait(tail + 8, 0, W, kErrAcc, lane, false)) break;
+          prev = misc[2 + q];
         }
-        finish16(P, v, m0 + c0, cols - c0, row);
+        if (prev + 1 != (uint32_t)(wl - wf + 1)) {
+          if (last) break;
+          continue;
+        }
+        __syncwarp();
       }
-      if (lane == 0) *counter = 0u;  // ready for the next call
+      __half res[kTok];
+      load_residual(P, res, m0 + c_first, cols - c_first, row);
+      for (int c0 = c_first; c0 < cols; c0 += step) {
+        __half res_next[kTok];
+        if (c0 + step < cols) load_residual(P, res_next, m0 + c0 + step, cols - c0 - step, row);
+        float v[kTok];
+        if (whole) {
+          uint32_t r[8];
+          tmem_ld8(tb + (uint32_t)c0, r);
+          tc_wait_ld();
+#pragma unroll
+          for (int e = 0; e < kTok; ++e) v[e] = __uint_as_float(r[e]);
+        } else {
+#pragma unroll
+          for (int e = 0; e < kTok; ++e) v[e] = 0.f;
+#pragma unroll 4
+          for (int w = wf; w <= wl; ++w) {
+            const int cta = w * C::kCtas + (int)rank;
+            const int sl = run_begin(w, U, nwk) >= ub ? 0 : 1;
+            const float* src =
+                P.partials + (size_t)(2 * cta + sl) * 128 * P.bn + (size_t)c0 * 128 + 4 * lrow;
+#pragma unroll
+            for (int e = 0; e < kTok; e += 4) {
+              const float4 f = __ldcg(reinterpret_cast<const float4*>(src + (size_t)e * 128));
+              v[e] += f.x;
+              v[e + 1] += f.y;
+              v[e + 2] += f.z;
+              v[e + 3] += f.w;
+            }
+          }
+        }
+        if (E.gated)
+          finish_gated(P, v, m0 + c0, cols - c0, row, bias);
+        else
+          finish(P, v, m0 + c0, cols - c0, row, bias, res);
+#pragma unroll
+        for (int e = 0; e < kTok; ++e) res[e] = res_next[e];
+      }
+      if (!whole && lane == 0 && member == 0) *counter = 0u;  // ready for the next call
+      if (last) break;
+      if (whole) {
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) arrive_lead(acce(a));
+      }
     }
   }
 
