@@ -55,6 +55,7 @@ namespace {
 
 constexpr uint32_t kErrStage = 1u, kErrAcc = 2u;
 constexpr int kTeams = 2, kTeamWarps = 8;
+constexpr int kAhead = 8;  // units between the L2 prefetch of the codes and their copy
 
 template <int BNX_, int FMT_, bool PAIR_>
 struct TcCfg {
@@ -84,7 +85,8 @@ struct TcCfg {
   static constexpr int kLastBar = kTailBar + 8;
   static constexpr int kMiscOff = kBarOff + 8 * (kLastBar + 1);
   static constexpr int kLutOff = kMiscOff + 24;
-  static constexpr int kSmem = kLutOff + 64 + 1024;
+  static constexpr int kSpareOff = kLutOff + 64;  // a word per decoding warp
+  static constexpr int kSmem = kSpareOff + 4 * kTeams * kTeamWarps + 1024;
   static_assert(kSmem <= 232448, "shared memory");
   static constexpr int kEpiWarp0 = 4, kDqWarp0 = 8;
   static constexpr int kWarps = kDqWarp0 + kTeams * kTeamWarps;
@@ -196,10 +198,11 @@ __device__ __forceinline__ bool wait(uint32_t bar, uint32_t parity, const WaitCt
 
 // A whole warp: every lane sees the phase complete (the usual case), or one lane waits.
 __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, const WaitCtx& w,
-                                          uint32_t bit, int lane, bool honor_abort = true) {
-  if (__all_sync(0xffffffffu, mbar_ready(bar, parity, false))) return true;
+                                          uint32_t bit, int lane, bool honor_abort = true,
+                                          bool cluster = false) {
+  if (__all_sync(0xffffffffu, mbar_ready(bar, parity, cluster))) return true;
   bool ok = true;
-  if (lane == 0) ok = wait_slow(bar, parity, w.abort, w.err, bit, false, honor_abort);
+  if (lane == 0) ok = wait_slow(bar, parity, w.abort, w.err, bit, cluster, honor_abort);
   return __shfl_sync(0xffffffffu, ok, 0);
 }
 
@@ -214,9 +217,12 @@ struct Decoded {
   uint4 v[4][2];  // [pair of steps, in the lane's order][row gi, gi + 8]
 };
 
+// The code slot is handed back (`release`, `spare`: a shared word of the warp) as soon as every
+// lane holds its words.  The barrier arrival does not wait for shared loads in flight; the
+// store of a value made from all of them does, and the arrival comes after it.
 template <class C>
 __device__ __forceinline__ void decode_tile(uint32_t slot, int tile, int lane, const float* lut,
-                                            Decoded& d) {
+                                            uint32_t release, uint32_t spare, Decoded& d) {
   constexpr int FMT = C::FMT;
   constexpr int KW = qlk::Fmt<FMT>::kWords, KP = KW / 4;  // words per lane, per step pair
   const int gi = lane >> 2;
@@ -248,8 +254,20 @@ __device__ __forceinline__ void decode_tile(uint32_t slot, int tile, int lane, c
       for (int k = 0; k < KP; ++k) w[KP * i + k] = swap ? r[KP * (i ^ 1) + k] : r[KP * i + k];
   }
   const uint32_t pa = slot + C::kCodeBytes + tile * C::kParChunk;
+  uint4 am = make_uint4(0, 0, 0, 0);  // LUT4 [64-block][row half]; else scales, zeros
   if constexpr (FMT == kLUT4) {
-    const uint4 am = qlk::lds128(pa + gi * 16);  // [64-block][row half]
+    am = qlk::lds128(pa + gi * 16);
+  } else {
+    am.x = qlk::lds32(pa + gi * 4);
+    am.y = qlk::lds32(pa + kBlockTiles * C::kParChunk + gi * 4);
+  }
+  uint32_t all = am.x ^ am.y ^ am.z ^ am.w;
+#pragma unroll
+  for (int k = 0; k < KW; ++k) all ^= w[k];
+  asm volatile("st.shared.u32 [%0], %1;" ::"r"(spare), "r"(all) : "memory");
+  __syncwarp();
+  if (lane == 0) qlk::mbar_arrive(release);
+  if constexpr (FMT == kLUT4) {
 #pragma unroll
     for (int i = 0; i < 4; ++i)
 #pragma unroll
@@ -258,8 +276,7 @@ __device__ __forceinline__ void decode_tile(uint32_t slot, int tile, int lane, c
             w + KP * i, 0, h, lut,
             __uint_as_float(i >= 2 ? (h ? am.w : am.z) : (h ? am.y : am.x)));
   } else {
-    const __half2 s2 = qdq::u32_as_h2(qlk::lds32(pa + gi * 4));
-    const __half2 z2 = qdq::u32_as_h2(qlk::lds32(pa + kBlockTiles * C::kParChunk + gi * 4));
+    const __half2 s2 = qdq::u32_as_h2(am.x), z2 = qdq::u32_as_h2(am.y);
     __half2 zb[2][2];
     qdq::zero_bias<FMT>(__low2float(z2), __high2float(z2), zb);
     const __half2 sl = __low2half2(s2), sh = __high2half2(s2);
@@ -377,6 +394,11 @@ __device__ __forceinline__ void tmem_ld8(uint32_t taddr, uint32_t (&r)[8]) {
                : "memory");
 }
 
+// Bring a run of bytes (16-byte aligned, a multiple of 16) into L2.
+__device__ __forceinline__ void prefetch_l2(const void* p, uint32_t bytes) {
+  asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(p), "r"(bytes) : "memory");
+}
+
 // Operand descriptors, in two words: the low one holds the address (16-byte units) and the
 // leading offset, the high one is the same for all (stride 1024 bytes between 8-row groups,
 // 128-byte swizzle).  K-major rows of 128 bytes; the backward product reads A MN-major: its
@@ -384,6 +406,15 @@ __device__ __forceinline__ void tmem_ld8(uint32_t taddr, uint32_t (&r)[8]) {
 constexpr uint32_t kDescHi = 64u | (1u << 14) | (2u << 29);
 constexpr uint32_t kDescLoK = 1u << 16, kDescLoMn = (128u * 128u / 16u) << 16;
 constexpr uint32_t kTransposeA = 1u << 15;  // instruction descriptor: A is MN-major
+
+// One lane of the warp, the same every time.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(p));
+  return p != 0;
+}
 
 template <bool PAIR>
 __device__ __forceinline__ void mma(uint32_t d, uint32_t alo, uint32_t blo, uint32_t idesc,
@@ -424,8 +455,9 @@ __global__ void __launch_bounds__(TcCfg<BNX, FMT, PAIR>::kThreads, 1)
   volatile uint32_t* misc = reinterpret_cast<volatile uint32_t*>(smem + C::kMiscOff);
   float* lut = reinterpret_cast<float*>(smem + C::kLutOff);
   const WaitCtx W{ring + C::kMiscOff + 4, P.err};
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const uint32_t rank = PAIR ? cluster_rank() : 0u;
+  const int warp = __shfl_sync(0xffffffffu, (int)(threadIdx.x >> 5), 0);  // uniform
+  const int lane = threadIdx.x & 31;
+  const uint32_t rank = PAIR ? blockIdx.x & 1u : 0u;  // of the cluster (2, 1, 1)
   const bool leader = rank == 0;
   const int wk = PAIR ? (int)(blockIdx.x >> 1) : (int)blockIdx.x;
   const int nwk = PAIR ? (int)(gridDim.x >> 1) : (int)gridDim.x;
@@ -526,6 +558,11 @@ __global__ void __launch_bounds__(TcCfg<BNX, FMT, PAIR>::kThreads, 1)
           }
           const int b = BWD ? k : rb, g = BWD ? rb : k;
           const uint32_t dst = ring + C::kRingC + c * C::kSlot;
+          if (rb < P.rblocks && k + kAhead < k1) {
+            const int b2 = BWD ? k + kAhead : rb, g2 = BWD ? rb : k + kAhead;
+            const long long ch = chunk_index(b2, g2, 0, P.G, P.ntiles);
+            prefetch_l2(P.qw + ch * C::kChunk, tiles_in_block(b2, P.ntiles) * C::kChunk);
+          }
           if (rb < P.rblocks) {
             const int tb = tiles_in_block(b, P.ntiles);
             const long long ch = chunk_index(b, g, 0, P.G, P.ntiles);
@@ -557,39 +594,46 @@ __global__ void __launch_bounds__(TcCfg<BNX, FMT, PAIR>::kThreads, 1)
         wait(cfull(i % C::SC), (i / C::SC) & 1, W, kErrStage, false, false);
     }
   } else if (warp == 1) {
-    // ---- MMA issue (the leader of a pair)
-    if (lane == 0 && leader) {
+    // ---- MMA issue (the leader of a pair).  The whole warp runs the loop, so that the
+    // descriptors stay in uniform registers; one elected lane issues.
+    if (leader) {
       qlk::grid_dependency_wait();
       const uint32_t idesc = idesc_f16(128 * C::kCtas, P.bn) | (BWD ? kTransposeA : 0u);
       int s = 0, ph = 0, j = 0;
       bool ok = true, ready = false;
       for (; ok && sg.next(P, tile, k0, k1, slot); ++j) {
         const int a = j & 1;
-        if (j >= 2 && !(ok = wait(acce(a), ((j >> 1) - 1) & 1, W, kErrAcc, PAIR))) break;
+        if (j >= 2 && !(ok = warp_wait(acce(a), ((j >> 1) - 1) & 1, W, kErrAcc, lane, true, PAIR)))
+          break;
         tc_fence_after();
         const uint32_t d = tmem + (uint32_t)(a * BNX);
         for (int k = k0; k < k1; ++k) {
-          if (!ready && !(ok = wait(full(s), ph, W, kErrStage, PAIR))) break;
+          if (!ready && !(ok = warp_wait(full(s), ph, W, kErrStage, lane, true, PAIR))) break;
           tc_fence_after();
           const uint32_t st = (ring + s * C::kStageBytes) >> 4;
           const uint32_t pa = st | (BWD ? kDescLoMn : kDescLoK);
           const uint32_t pb = (st + (C::kABytes >> 4)) | kDescLoK;
           const int s1 = s + 1 == C::S ? 0 : s + 1, ph1 = s + 1 == C::S ? ph ^ 1 : ph;
-          // the next stage's barrier is looked at while this stage's MMAs are issued
-          ready = mbar_ready(full(s1), ph1, PAIR);
+          if (elect_one()) {
 #pragma unroll
-          for (int kk = 0; kk < 8; ++kk)
-            mma<PAIR>(d, pa + (BWD ? 128 * kk : (kk >> 2) * (C::kHalfA >> 4) + 2 * (kk & 3)),
-                      pb + (kk >> 2) * (C::kHalfB >> 4) + 2 * (kk & 3), idesc,
-                      kk == 0 ? (uint32_t)(k != k0) : 1u);
-          commit_both(empty(s));
+            for (int kk = 0; kk < 8; ++kk)
+              mma<PAIR>(d, pa + (BWD ? 128 * kk : (kk >> 2) * (C::kHalfA >> 4) + 2 * (kk & 3)),
+                        pb + (kk >> 2) * (C::kHalfB >> 4) + 2 * (kk & 3), idesc,
+                        kk == 0 ? (uint32_t)(k != k0) : 1u);
+            commit_both(empty(s));
+          }
+          __syncwarp();
+          // (all lanes look at the next stage's barrier before they wait for it)
+          ready = __all_sync(0xffffffffu, mbar_ready(full(s1), ph1, PAIR));
           s = s1;
           ph = ph1;
         }
-        if (ok) commit_both(sg.done(P) ? lastf : accf(a));
+        if (ok && elect_one()) commit_both(sg.done(P) ? lastf : accf(a));
+        __syncwarp();
       }
-      tc_commit<PAIR>(fin);
-      wait(fin, 0, W, kErrAcc, false, false);
+      if (elect_one()) tc_commit<PAIR>(fin);
+      __syncwarp();
+      warp_wait(fin, 0, W, kErrAcc, lane, false);
     }
   } else if (warp >= C::kEpiWarp0) {
     const bool decoder = warp >= C::kDqWarp0;
@@ -609,10 +653,14 @@ __global__ void __launch_bounds__(TcCfg<BNX, FMT, PAIR>::kThreads, 1)
             if (!(ok = warp_wait(cfull(c), cph, W, kErrStage, lane))) break;
             Decoded d;
             if (dt < tb) {
-              decode_tile<C>(ring + C::kRingC + c * C::kSlot, dt, lane, lut, d);
-            } else if (BWD) {  // rows past the last column are contracted: zeros
+              decode_tile<C>(ring + C::kRingC + c * C::kSlot, dt, lane, lut, cempty(c),
+                             ring + C::kSpareOff + 4 * (warp - C::kDqWarp0), d);
+            } else {
+              if (lane == 0) qlk::mbar_arrive(cempty(c));
+              if (BWD) {  // rows past the last column are contracted: zeros
 #pragma unroll
-              for (int i = 0; i < 8; ++i) d.v[i >> 1][i & 1] = make_uint4(0, 0, 0, 0);
+                for (int i = 0; i < 8; ++i) d.v[i >> 1][i & 1] = make_uint4(0, 0, 0, 0);
+              }
             }
             if (n >= C::S) {
               if (n <= C::S + 1) qlk::grid_dependency_wait();
@@ -621,10 +669,7 @@ __global__ void __launch_bounds__(TcCfg<BNX, FMT, PAIR>::kThreads, 1)
             if (BWD || dt < tb) store_tile(ring + s * C::kStageBytes, dt, lane, d);
             asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // visible to the MMAs
             __syncwarp();
-            if (lane == 0) {
-              qlk::mbar_arrive(cempty(c));
-              arrive_lead(full(s));
-            }
+            if (lane == 0) arrive_lead(full(s));
           }
           if (++s == C::S) {
             s = 0;
