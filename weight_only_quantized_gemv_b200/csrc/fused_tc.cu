@@ -55,7 +55,6 @@ namespace {
 
 constexpr uint32_t kErrStage = 1u, kErrAcc = 2u;
 constexpr int kTeams = 2, kTeamWarps = 8;
-constexpr int kAhead = 8;  // units between the L2 prefetch of the codes and their copy
 
 template <int BNX_, int FMT_, bool PAIR_>
 struct TcCfg {
@@ -110,7 +109,13 @@ struct TcParams {
   int rblocks;   // 128-row blocks
   int steps;     // units per tile: groups (forward) or blocks (backward)
   int bn, mtiles, tiles, whole;  // tokens per tile; tiles [0, whole) are not split
+  int runners;                   // workers that share the stages of tiles [whole, tiles)
 };
+
+__device__ __forceinline__ long long run_begin(int w, long long U, int W) { return w * U / W; }
+__device__ __forceinline__ int worker_of(long long u, long long U, int W) {
+  return (int)(((u + 1) * W - 1) / U);
+}
 
 // The work of a worker (CTA or pair): whole tiles w, w + W, ..., then its run of the stages of
 // tiles [whole, tiles), cut at tile boundaries.
@@ -122,8 +127,8 @@ struct Segments {
     W = W_;
     t = w;
     const long long U = (long long)(P.tiles - P.whole) * P.steps;
-    const long long u = w * U / W_;
-    left = (int)((w + 1) * U / W_ - u);
+    const long long u = run_begin(w, U, P.runners);
+    left = w < P.runners ? (int)(run_begin(w + 1, U, P.runners) - u) : 0;
     rt = P.whole + (int)(u / P.steps);
     rk = (int)(u % P.steps);
     first = true;
@@ -152,11 +157,6 @@ struct Segments {
   }
 };
 
-__device__ __forceinline__ long long run_begin(int w, long long U, int W) { return w * U / W; }
-__device__ __forceinline__ int worker_of(long long u, long long U, int W) {
-  return (int)(((u + 1) * W - 1) / U);
-}
-
 // ---------------------------------------------------------------------------
 // bounded waits
 
@@ -166,13 +166,22 @@ struct WaitCtx {
 };
 constexpr uint64_t kWaitNs = 100ull * 1000 * 1000;
 
+// try_wait may suspend the thread until the phase completes (or a time limit of the hardware
+// passes), which leaves the issue slots to the working warps; the clock is read rarely.
 __device__ __noinline__ bool wait_slow(uint32_t bar, uint32_t parity, uint32_t abort, uint32_t* err,
-                                       uint32_t bit, bool cluster, bool honor_abort) {
+                                       uint32_t bit, bool honor_abort) {
   uint64_t t0 = 0;
-  for (uint32_t it = 0;; ++it) {
-    if (mbar_ready(bar, parity, cluster)) return true;
-    if (it >= 256) __nanosleep(32);  // leave the issue slots to the working warps
-    if ((it & 63u) == 63u) {
+  for (uint32_t it = 1;; ++it) {
+    uint32_t done;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(done)
+        : "r"(bar), "r"(parity)
+        : "memory");
+    if (done) return true;
+    if ((it & 31u) == 0) {
       if (honor_abort) {
         uint32_t a;
         asm volatile("ld.volatile.shared.u32 %0, [%1];" : "=r"(a) : "r"(abort) : "memory");
@@ -191,18 +200,17 @@ __device__ __noinline__ bool wait_slow(uint32_t bar, uint32_t parity, uint32_t a
 }
 
 __device__ __forceinline__ bool wait(uint32_t bar, uint32_t parity, const WaitCtx& w, uint32_t bit,
-                                     bool cluster = false, bool honor_abort = true) {
-  if (mbar_ready(bar, parity, cluster)) return true;
-  return wait_slow(bar, parity, w.abort, w.err, bit, cluster, honor_abort);
+                                     bool honor_abort = true) {
+  if (mbar_ready(bar, parity, false)) return true;
+  return wait_slow(bar, parity, w.abort, w.err, bit, honor_abort);
 }
 
 // A whole warp: every lane sees the phase complete (the usual case), or one lane waits.
 __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, const WaitCtx& w,
-                                          uint32_t bit, int lane, bool honor_abort = true,
-                                          bool cluster = false) {
-  if (__all_sync(0xffffffffu, mbar_ready(bar, parity, cluster))) return true;
+                                          uint32_t bit, int lane, bool honor_abort = true) {
+  if (__all_sync(0xffffffffu, mbar_ready(bar, parity, false))) return true;
   bool ok = true;
-  if (lane == 0) ok = wait_slow(bar, parity, w.abort, w.err, bit, cluster, honor_abort);
+  if (lane == 0) ok = wait_slow(bar, parity, w.abort, w.err, bit, honor_abort);
   return __shfl_sync(0xffffffffu, ok, 0);
 }
 
@@ -277,8 +285,14 @@ __device__ __forceinline__ void decode_tile(uint32_t slot, int tile, int lane, c
             __uint_as_float(i >= 2 ? (h ? am.w : am.z) : (h ? am.y : am.x)));
   } else {
     const __half2 s2 = qdq::u32_as_h2(am.x), z2 = qdq::u32_as_h2(am.y);
+    // z + 2^(10 - shift): exact in fp16 for integer zeros up to 1024
     __half2 zb[2][2];
-    qdq::zero_bias<FMT>(__low2float(z2), __high2float(z2), zb);
+#pragma unroll
+    for (int p = 0; p < 2; ++p)
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+        zb[p][h] = __hadd2(h ? __high2half2(z2) : __low2half2(z2),
+                           qdq::u32_as_h2(qdq::magic_half(qdq::field_shift<FMT>(p, h)) * 0x10001u));
     const __half2 sl = __low2half2(s2), sh = __high2half2(s2);
 #pragma unroll
     for (int i = 0; i < 4; ++i)
@@ -394,11 +408,6 @@ __device__ __forceinline__ void tmem_ld8(uint32_t taddr, uint32_t (&r)[8]) {
                : "memory");
 }
 
-// Bring a run of bytes (16-byte aligned, a multiple of 16) into L2.
-__device__ __forceinline__ void prefetch_l2(const void* p, uint32_t bytes) {
-  asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(p), "r"(bytes) : "memory");
-}
-
 // Operand descriptors, in two words: the low one holds the address (16-byte units) and the
 // leading offset, the high one is the same for all (stride 1024 bytes between 8-row groups,
 // 128-byte swizzle).  K-major rows of 128 bytes; the backward product reads A MN-major: its
@@ -406,6 +415,14 @@ __device__ __forceinline__ void prefetch_l2(const void* p, uint32_t bytes) {
 constexpr uint32_t kDescHi = 64u | (1u << 14) | (2u << 29);
 constexpr uint32_t kDescLoK = 1u << 16, kDescLoMn = (128u * 128u / 16u) << 16;
 constexpr uint32_t kTransposeA = 1u << 15;  // instruction descriptor: A is MN-major
+
+// Arrive on a barrier of the pair's other CTA.  What the arrival stands for is already done:
+// the decoding warps' stores by their proxy fence, the epilogue's tensor memory loads by their
+// wait; so the default release at CTA scope does, where one at cluster scope takes about a
+// thousand cycles more.
+__device__ __forceinline__ void arrive_remote(uint32_t bar) {
+  asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
 
 // One lane of the warp, the same every time.
 __device__ __forceinline__ bool elect_one() {
@@ -464,7 +481,7 @@ __global__ void __launch_bounds__(TcCfg<BNX, FMT, PAIR>::kThreads, 1)
   auto lead = [&](uint32_t b) { return (PAIR && !leader) ? cluster_addr(b, 0) : b; };
   auto arrive_lead = [&](uint32_t b) {
     if (PAIR && !leader)
-      mbar_arrive_remote(cluster_addr(b, 0));
+      arrive_remote(cluster_addr(b, 0));
     else
       qlk::mbar_arrive(b);
   };
@@ -541,46 +558,40 @@ __global__ void __launch_bounds__(TcCfg<BNX, FMT, PAIR>::kThreads, 1)
       // no copy is in flight when the CTA exits (the leader's barriers count both CTAs')
       if (leader)
         for (int i = n > C::S ? n - C::S : 0; i < n; ++i)
-          wait(full(i % C::S), (i / C::S) & 1, W, kErrStage, PAIR, false);
+          wait(full(i % C::S), (i / C::S) & 1, W, kErrStage, false);
     }
   } else if (warp == 2) {
-    // ---- copies of the units' codes and parameters
-    if (lane == 0) {
+    // ---- copies of the units' codes and parameters: lanes 0, 1, 2 each issue one of a unit's
+    // copies (LUT4: two) with one instruction
+    {
       int c = 0, ph = 1, n = 0;
       bool ok = true;
-      const uint64_t pol = qlk::evict_first_policy();
+      const uint8_t* base = P.qw;      // this lane's array, bytes per chunk of it
+      uint32_t per = C::kChunk, off = 0;
+      if (lane >= 1) {
+        base = static_cast<const uint8_t*>(FMT == kLUT4 || lane >= 2 ? P.p1 : P.p0);
+        per = C::kParChunk;
+        off = C::kCodeBytes + (lane >= 2 ? kBlockTiles * C::kParChunk : 0);
+      }
+      constexpr int kCopies = FMT == kLUT4 ? 2 : 3;
       while (ok && sg.next(P, tile, k0, k1, slot)) {
         const int rb = (tile / P.mtiles) * C::kCtas + (int)rank;
         for (int k = k0; k < k1; ++k) {
           if (n >= C::SC) {
             if (n == C::SC) qlk::grid_dependency_wait();
-            if (!(ok = wait(cempty(c), ph, W, kErrStage))) break;
+            if (!(ok = warp_wait(cempty(c), ph, W, kErrStage, lane))) break;
           }
           const int b = BWD ? k : rb, g = BWD ? rb : k;
-          const uint32_t dst = ring + C::kRingC + c * C::kSlot;
-          if (rb < P.rblocks && k + kAhead < k1) {
-            const int b2 = BWD ? k + kAhead : rb, g2 = BWD ? rb : k + kAhead;
-            const long long ch = chunk_index(b2, g2, 0, P.G, P.ntiles);
-            prefetch_l2(P.qw + ch * C::kChunk, tiles_in_block(b2, P.ntiles) * C::kChunk);
-          }
           if (rb < P.rblocks) {
             const int tb = tiles_in_block(b, P.ntiles);
             const long long ch = chunk_index(b, g, 0, P.G, P.ntiles);
-            const uint32_t cb = tb * C::kChunk, pb = tb * C::kParChunk;
-            qlk::mbar_arrive_expect_tx(cfull(c), cb + (FMT == kLUT4 ? 1 : 2) * pb);
-            if (P.mtiles == 1)  // read once
-              qlk::bulk_g2s(dst, P.qw + ch * C::kChunk, cb, cfull(c), pol);
-            else
-              qlk::bulk_g2s(dst, P.qw + ch * C::kChunk, cb, cfull(c));
-            const uint32_t pd = dst + C::kCodeBytes;
-            if constexpr (FMT == kLUT4) {
-              qlk::bulk_g2s(pd, static_cast<const float*>(P.p1) + ch * 32, pb, cfull(c));
-            } else {
-              qlk::bulk_g2s(pd, static_cast<const __half*>(P.p0) + ch * 16, pb, cfull(c));
-              qlk::bulk_g2s(pd + kBlockTiles * C::kParChunk,
-                            static_cast<const __half*>(P.p1) + ch * 16, pb, cfull(c));
-            }
-          } else {  // no rows for this CTA of the pair
+            if (lane == 0)
+              qlk::mbar_arrive_expect_tx(cfull(c), tb * (C::kChunk + (kCopies - 1) * C::kParChunk));
+            __syncwarp();
+            if (lane < kCopies)
+              qlk::bulk_g2s(ring + C::kRingC + c * C::kSlot + off, base + ch * per, tb * per,
+                            cfull(c));
+          } else if (lane == 0) {  // no rows for this CTA of the pair
             qlk::mbar_arrive(cfull(c));
           }
           ++n;
@@ -591,7 +602,7 @@ __global__ void __launch_bounds__(TcCfg<BNX, FMT, PAIR>::kThreads, 1)
         }
       }
       for (int i = n > C::SC ? n - C::SC : 0; i < n; ++i)
-        wait(cfull(i % C::SC), (i / C::SC) & 1, W, kErrStage, false, false);
+        warp_wait(cfull(i % C::SC), (i / C::SC) & 1, W, kErrStage, lane, false);
     }
   } else if (warp == 1) {
     // ---- MMA issue (the leader of a pair).  The whole warp runs the loop, so that the
@@ -603,12 +614,12 @@ __global__ void __launch_bounds__(TcCfg<BNX, FMT, PAIR>::kThreads, 1)
       bool ok = true, ready = false;
       for (; ok && sg.next(P, tile, k0, k1, slot); ++j) {
         const int a = j & 1;
-        if (j >= 2 && !(ok = warp_wait(acce(a), ((j >> 1) - 1) & 1, W, kErrAcc, lane, true, PAIR)))
+        if (j >= 2 && !(ok = warp_wait(acce(a), ((j >> 1) - 1) & 1, W, kErrAcc, lane)))
           break;
         tc_fence_after();
         const uint32_t d = tmem + (uint32_t)(a * BNX);
         for (int k = k0; k < k1; ++k) {
-          if (!ready && !(ok = warp_wait(full(s), ph, W, kErrStage, lane, true, PAIR))) break;
+          if (!ready && !(ok = warp_wait(full(s), ph, W, kErrStage, lane))) break;
           tc_fence_after();
           const uint32_t st = (ring + s * C::kStageBytes) >> 4;
           const uint32_t pa = st | (BWD ? kDescLoMn : kDescLoK);
@@ -624,7 +635,7 @@ __global__ void __launch_bounds__(TcCfg<BNX, FMT, PAIR>::kThreads, 1)
           }
           __syncwarp();
           // (all lanes look at the next stage's barrier before they wait for it)
-          ready = __all_sync(0xffffffffu, mbar_ready(full(s1), ph1, PAIR));
+          ready = __all_sync(0xffffffffu, mbar_ready(full(s1), ph1, false));
           s = s1;
           ph = ph1;
         }
@@ -733,8 +744,8 @@ __global__ void __launch_bounds__(TcCfg<BNX, FMT, PAIR>::kThreads, 1)
         tc_fence_before();
         __syncwarp();
         ub = (long long)(tile - P.whole) * P.steps;
-        wf = worker_of(ub, U, nwk);
-        wl = worker_of(ub + P.steps - 1, U, nwk);
+        wf = worker_of(ub, U, P.runners);
+        wl = worker_of(ub + P.steps - 1, U, P.runners);
         counter = P.counters + ((size_t)(tile - P.whole) * C::kCtas + rank) * 4 + q;
         uint32_t prev = 0;
         if (!last) {
@@ -780,7 +791,7 @@ __global__ void __launch_bounds__(TcCfg<BNX, FMT, PAIR>::kThreads, 1)
 #pragma unroll 4
           for (int w = wf; w <= wl; ++w) {
             const int cta = w * C::kCtas + (int)rank;
-            const int sl = run_begin(w, U, nwk) >= ub ? 0 : 1;
+            const int sl = run_begin(w, U, P.runners) >= ub ? 0 : 1;
             const float* src =
                 P.partials + (size_t)(2 * cta + sl) * 128 * P.bn + (size_t)c0 * 128 + 4 * lrow;
 #pragma unroll
@@ -918,6 +929,49 @@ Tokens token_tiles(int M) {
   return Tokens{true, bn, (M + bn - 1) / bn};
 }
 
+// Whole waves of tiles, then the remaining R tiles over `runners` workers by stage, in one of
+// two ways:
+//  * parts: each of the R tiles in f equal parts, f <= W / R.  The workers stay in step and
+//    read the same tokens at the same time; the parts of a tile are joined by twenty warps.
+//  * runs (stream-K): R tiles and one whole wave in W equal runs.  No worker idles, but each is
+//    at a depth of its own, and most sums are joined by four warps beside the next tile.
+// In us: a stage takes about max(0.3, bn / 465), joining one more part bn / 160 + 0.3, and runs
+// cost bn / 7 more than their stages (measured: 300 x 4096 x 4096 27 in parts, 59 in runs;
+// 512 x 28672 x 8192 with R = 2, f = 37 parts 375, runs 235; 96 x 28672 x 8192 equal).
+struct Schedule {
+  int whole, runners;
+};
+Schedule schedule(int tiles, int steps, int W, int bn) {
+  const int R = tiles % W;
+  if (R == 0) return Schedule{tiles, 0};
+  const float stage = bn > 140 ? bn / 465.f : 0.3f, join = bn / 160.f + 0.3f;
+  int f = 1;
+  float parts = steps * stage;
+  for (int g = 2; g <= W / R && g <= steps; ++g) {
+    const float t = (steps + g - 1) / g * stage + g * join;
+    if (t < parts) {
+      parts = t;
+      f = g;
+    }
+  }
+  const float runs = steps * stage * R / W + bn / 7.f;
+#ifdef SCHEDENV
+  if (const char* e = getenv("SCHED")) {if (e[0]=='0') goto R_; else goto P_;}
+#endif
+  if (runs < parts) {
+#ifdef SCHEDENV
+R_:
+#endif
+    const int t = tiles < W ? tiles : R + W;  // shared out
+    const long long units = (long long)t * steps;
+    return Schedule{tiles - t, units < W ? (int)units : W};
+  }
+#ifdef SCHEDENV
+P_:
+#endif
+  return Schedule{tiles - R, R * f};
+}
+
 template <int BNX, int FMT, bool PAIR, bool BWD>
 ql_status launch_as(const qfused::Product& p, const Tokens& tk) {
   int dev = 0, sms = 0;
@@ -950,12 +1004,10 @@ ql_status launch_as(const qfused::Product& p, const Tokens& tk) {
   const long long tiles = (long long)((P.rblocks + ctas - 1) / ctas) * tk.mtiles;
   if (tiles >= (1LL << 31)) return QL_ERR_SHAPE;
   P.tiles = (int)tiles;
-  // whole waves of tiles, then the rest shared out by stage: the remainder together with one
-  // whole wave, so that a tile is cut in a few long runs
-  const int rem = P.tiles % maxw;
-  P.whole = rem == 0 ? P.tiles : P.tiles < maxw ? 0 : P.tiles - rem - maxw;
-  const long long units = (long long)(P.tiles - P.whole) * P.steps;
-  const int workers = P.whole > 0 || units >= maxw ? maxw : (int)units;
+  const Schedule sc = schedule(P.tiles, P.steps, maxw, tk.bn);
+  P.whole = sc.whole;
+  P.runners = sc.runners;
+  const int workers = P.whole > 0 ? maxw : P.runners;
   CUtensorMap xmap;
   if (!encode_rows(&xmap, p.x, p.M, BWD ? p.N : p.K, tk.bn / ctas)) return QL_ERR_CUDA;
   cudaLaunchConfig_t cfg;
@@ -969,7 +1021,9 @@ ql_status launch_as(const qfused::Product& p, const Tokens& tk) {
 template <int FMT, bool BWD>
 ql_status launch_fmt(const qfused::Product& p) {
   const Tokens tk = token_tiles(p.M);
-  if (!tk.pair) return launch_as<64, FMT, false, BWD>(p, tk);
+  if (!tk.pair)
+    return tk.bn <= 32 ? launch_as<32, FMT, false, BWD>(p, tk)
+                       : launch_as<64, FMT, false, BWD>(p, tk);
   return tk.bn <= 128 ? launch_as<128, FMT, true, BWD>(p, tk)
                       : launch_as<256, FMT, true, BWD>(p, tk);
 }
