@@ -166,49 +166,50 @@ struct WaitCtx {
 };
 constexpr uint64_t kWaitNs = 100ull * 1000 * 1000;
 
-// try_wait may suspend the thread until the phase completes (or a time limit of the hardware
-// passes), which leaves the issue slots to the working warps; the clock is read rarely.
+// Suspends the thread until the phase completes, or for up to kSuspendNs; whether it completed.
+// (Polling instead took as many issue slots as the decoding.)
+constexpr uint32_t kSuspendNs = 20000;
+__device__ __forceinline__ bool try_wait(uint32_t bar, uint32_t parity) {
+  uint32_t done;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(done)
+      : "r"(bar), "r"(parity), "r"(kSuspendNs)
+      : "memory");
+  return done != 0;
+}
+
+// The phase has not completed within one suspension: keep waiting up to kWaitNs, or until
+// another role has given up; then set the flag.
 __device__ __noinline__ bool wait_slow(uint32_t bar, uint32_t parity, uint32_t abort, uint32_t* err,
                                        uint32_t bit, bool honor_abort) {
-  uint64_t t0 = 0;
-  for (uint32_t it = 1;; ++it) {
-    uint32_t done;
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
-        "selp.u32 %0, 1, 0, p;\n\t}"
-        : "=r"(done)
-        : "r"(bar), "r"(parity)
-        : "memory");
-    if (done) return true;
-    if ((it & 31u) == 0) {
-      if (honor_abort) {
-        uint32_t a;
-        asm volatile("ld.volatile.shared.u32 %0, [%1];" : "=r"(a) : "r"(abort) : "memory");
-        if (a) break;
-      }
-      const uint64_t now = globaltimer_ns();
-      if (t0 == 0)
-        t0 = now;
-      else if (now - t0 > kWaitNs)
-        break;
+  const uint64_t t0 = globaltimer_ns();
+  for (;;) {
+    if (try_wait(bar, parity)) return true;
+    if (honor_abort) {
+      uint32_t a;
+      asm volatile("ld.volatile.shared.u32 %0, [%1];" : "=r"(a) : "r"(abort) : "memory");
+      if (a) break;
     }
+    if (globaltimer_ns() - t0 > kWaitNs) break;
   }
   atomicOr(err, bit);
   asm volatile("st.volatile.shared.u32 [%0], %1;" ::"r"(abort), "r"(1u) : "memory");
   return false;
 }
 
+// One thread.
 __device__ __forceinline__ bool wait(uint32_t bar, uint32_t parity, const WaitCtx& w, uint32_t bit,
                                      bool honor_abort = true) {
-  if (mbar_ready(bar, parity, false)) return true;
-  return wait_slow(bar, parity, w.abort, w.err, bit, honor_abort);
+  return try_wait(bar, parity) || wait_slow(bar, parity, w.abort, w.err, bit, honor_abort);
 }
 
-// A whole warp: every lane sees the phase complete (the usual case), or one lane waits.
+// A whole warp: every lane sees the phase complete (the usual case), or one lane waits on.
 __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, const WaitCtx& w,
                                           uint32_t bit, int lane, bool honor_abort = true) {
-  if (__all_sync(0xffffffffu, mbar_ready(bar, parity, false))) return true;
+  if (__all_sync(0xffffffffu, try_wait(bar, parity))) return true;
   bool ok = true;
   if (lane == 0) ok = wait_slow(bar, parity, w.abort, w.err, bit, honor_abort);
   return __shfl_sync(0xffffffffu, ok, 0);
@@ -424,6 +425,18 @@ __device__ __forceinline__ void arrive_remote(uint32_t bar) {
   asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
 
+// Every thread of the CTA (PAIR: of both CTAs).  The roles leave their warps divergent, so the
+// lanes meet first, and the cluster barrier is the form that does not ask for it.
+template <bool PAIR>
+__device__ __forceinline__ void sync_all() {
+  __syncwarp();
+  if constexpr (PAIR)
+    asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
+  else
+    __syncthreads();
+  __syncwarp();
+}
+
 // One lane of the warp, the same every time.
 __device__ __forceinline__ bool elect_one() {
   uint32_t p;
@@ -516,10 +529,7 @@ __global__ void __launch_bounds__(TcCfg<BNX, FMT, PAIR>::kThreads, 1)
   }
   if (warp == 1) tmem_alloc<PAIR>(ring + C::kMiscOff, C::kTmemCols);
   tc_fence_before();
-  if constexpr (PAIR)
-    cluster_sync();
-  else
-    __syncthreads();
+  sync_all<PAIR>();
   tc_fence_after();
   const uint32_t tmem = misc[0];
   qlk::grid_dependents_launch();
@@ -625,6 +635,8 @@ __global__ void __launch_bounds__(TcCfg<BNX, FMT, PAIR>::kThreads, 1)
           const uint32_t pa = st | (BWD ? kDescLoMn : kDescLoK);
           const uint32_t pb = (st + (C::kABytes >> 4)) | kDescLoK;
           const int s1 = s + 1 == C::S ? 0 : s + 1, ph1 = s + 1 == C::S ? ph ^ 1 : ph;
+          // the next stage's barrier is looked at while this stage's MMAs are issued
+          const bool next_ready = mbar_ready(full(s1), ph1, false);
           if (elect_one()) {
 #pragma unroll
             for (int kk = 0; kk < 8; ++kk)
@@ -633,9 +645,7 @@ __global__ void __launch_bounds__(TcCfg<BNX, FMT, PAIR>::kThreads, 1)
                         kk == 0 ? (uint32_t)(k != k0) : 1u);
             commit_both(empty(s));
           }
-          __syncwarp();
-          // (all lanes look at the next stage's barrier before they wait for it)
-          ready = __all_sync(0xffffffffu, mbar_ready(full(s1), ph1, false));
+          ready = __all_sync(0xffffffffu, next_ready);
           s = s1;
           ph = ph1;
         }
@@ -734,6 +744,7 @@ __global__ void __launch_bounds__(TcCfg<BNX, FMT, PAIR>::kThreads, 1)
         float* mine = P.partials + (size_t)(2 * blockIdx.x + slot) * 128 * P.bn + 4 * lrow;
         for (int c0 = c_first; c0 < cols; c0 += step) {
           uint32_t r[8];
+          __syncwarp();
           tmem_ld8(tb + (uint32_t)c0, r);
           tc_wait_ld();
 #pragma unroll
@@ -781,6 +792,7 @@ __global__ void __launch_bounds__(TcCfg<BNX, FMT, PAIR>::kThreads, 1)
         float v[kTok];
         if (whole) {
           uint32_t r[8];
+          __syncwarp();
           tmem_ld8(tb + (uint32_t)c0, r);
           tc_wait_ld();
 #pragma unroll
@@ -822,10 +834,7 @@ __global__ void __launch_bounds__(TcCfg<BNX, FMT, PAIR>::kThreads, 1)
   }
 
   tc_fence_before();
-  if constexpr (PAIR)
-    cluster_sync();
-  else
-    __syncthreads();
+  sync_all<PAIR>();
   if (warp == 1) {
     tc_fence_after();
     tmem_dealloc<PAIR>(tmem, C::kTmemCols);

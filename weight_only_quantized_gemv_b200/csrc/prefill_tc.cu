@@ -666,6 +666,7 @@ __global__ void __launch_bounds__(TcCfg<BN, FUSED, FMT, PAIR>::kThreads, 1)
   tc_fence_before();
   // PAIR: neither CTA exits (or releases its tensor memory) while the other may still
   // arrive on its barriers or the leader's MMAs may still use its memory
+  __syncwarp();  // the roles left their warps divergent; the cluster barrier is the aligned form
   if constexpr (PAIR)
     cluster_sync();
   else
