@@ -67,6 +67,52 @@ __device__ __forceinline__ uint4 pack8(const float (&f)[8]) {
   return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
+__device__ __forceinline__ uint4 load8(const __half* p) {
+  return __ldg(reinterpret_cast<const uint4*>(p));
+}
+
+// d *= act'(z); the activation's branch outside the loop
+template <int ACT>
+__device__ __forceinline__ void times_gradient_of(float (&d)[8], const float (&z)[8]) {
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    float f, df;
+    qact::act_both(ACT, z[e], f, df);
+    d[e] *= df;
+  }
+}
+__device__ __forceinline__ void times_gradient(int act, float (&d)[8], const float (&z)[8]) {
+  switch (act) {
+    case QL_ACT_RELU: return times_gradient_of<QL_ACT_RELU>(d, z);
+    case QL_ACT_GELU: return times_gradient_of<QL_ACT_GELU>(d, z);
+    case QL_ACT_GELU_TANH: return times_gradient_of<QL_ACT_GELU_TANH>(d, z);
+    case QL_ACT_SILU: return times_gradient_of<QL_ACT_SILU>(d, z);
+    default: return;
+  }
+}
+// dg = dh u act'(g), dh becomes du = dh act(g)
+template <int ACT>
+__device__ __forceinline__ void gated_gradients_of(float (&dh)[8], const float (&g)[8],
+                                                   const float (&u)[8], float (&dg)[8]) {
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    float f, df;
+    qact::act_both(ACT, g[e], f, df);
+    dg[e] = dh[e] * u[e] * df;
+    dh[e] *= f;
+  }
+}
+__device__ __forceinline__ void gated_gradients(int act, float (&dh)[8], const float (&g)[8],
+                                                const float (&u)[8], float (&dg)[8]) {
+  switch (act) {
+    case QL_ACT_RELU: return gated_gradients_of<QL_ACT_RELU>(dh, g, u, dg);
+    case QL_ACT_GELU: return gated_gradients_of<QL_ACT_GELU>(dh, g, u, dg);
+    case QL_ACT_GELU_TANH: return gated_gradients_of<QL_ACT_GELU_TANH>(dh, g, u, dg);
+    case QL_ACT_SILU: return gated_gradients_of<QL_ACT_SILU>(dh, g, u, dg);
+    default: return gated_gradients_of<QL_ACT_NONE>(dh, g, u, dg);
+  }
+}
+
 template <bool GATED>
 __global__ void __launch_bounds__(32 * kGradWarps) grad_kernel(const GradParams P) {
   constexpr int NB = GATED ? 2 : 1;
@@ -85,41 +131,53 @@ __global__ void __launch_bounds__(32 * kGradWarps) grad_kernel(const GradParams 
   qlk::grid_dependents_launch();
   qlk::grid_dependency_wait();
   if (in) {
-    for (int m = m0 + warp; m < m1; m += kGradWarps) {
-      const size_t row = (size_t)m * P.W;
-      float d[8];
-      unpack8(*reinterpret_cast<const uint4*>(P.dy + row + c), d);
-      if constexpr (GATED) {
-        float g[8], u[8], dg[8], du[8];
-        unpack8(*reinterpret_cast<const uint4*>(P.z + 2 * row + c), g);
-        unpack8(*reinterpret_cast<const uint4*>(P.z + 2 * row + P.W + c), u);
+    // kRows rows at a time: their loads are in flight together
+    constexpr int kRows = GATED ? 2 : 4;
+    for (int mm = m0 + warp; mm < m1; mm += kRows * kGradWarps) {
+      uint4 vd[kRows], va[kRows], vb[kRows];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          float f, df;
-          qact::act_both(P.act, g[e], f, df);
-          dg[e] = d[e] * u[e] * df;
-          du[e] = d[e] * f;
-          sum[0][e] += dg[e];
-          sum[1][e] += du[e];
+      for (int i = 0; i < kRows; ++i) {
+        const int m = mm + i * kGradWarps;
+        if (m >= m1) continue;
+        const size_t row = (size_t)m * P.W;
+        vd[i] = load8(P.dy + row + c);
+        if constexpr (GATED) {
+          va[i] = load8(P.z + 2 * row + c);
+          vb[i] = load8(P.z + 2 * row + P.W + c);
+        } else if (P.z) {
+          va[i] = load8(P.z + row + c);
         }
-        // packed order: gate column f at 32 (f / 16) + f % 16, its up column 16 further
-        __half* o = P.dz + 2 * row + 32 * (c >> 4) + (c & 15);
-        *reinterpret_cast<uint4*>(o) = pack8(dg);
-        *reinterpret_cast<uint4*>(o + 16) = pack8(du);
-      } else {
-        if (P.z) {
-          float z[8];
-          unpack8(*reinterpret_cast<const uint4*>(P.z + row + c), z);
+      }
+#pragma unroll
+      for (int i = 0; i < kRows; ++i) {
+        const int m = mm + i * kGradWarps;
+        if (m >= m1) continue;
+        const size_t row = (size_t)m * P.W;
+        float d[8], a[8];
+        unpack8(vd[i], d);
+        if constexpr (GATED) {
+          float u[8], dg[8];
+          unpack8(va[i], a);
+          unpack8(vb[i], u);
+          gated_gradients(P.act, d, a, u, dg);  // d becomes du
 #pragma unroll
           for (int e = 0; e < 8; ++e) {
-            float f, df;
-            qact::act_both(P.act, z[e], f, df);
-            d[e] *= df;
+            sum[0][e] += dg[e];
+            sum[1][e] += d[e];
           }
-        }
+          // packed order: gate column f at 32 (f / 16) + f % 16, its up column 16 further
+          __half* o = P.dz + 2 * row + 32 * (c >> 4) + (c & 15);
+          *reinterpret_cast<uint4*>(o) = pack8(dg);
+          *reinterpret_cast<uint4*>(o + 16) = pack8(d);
+        } else {
+          if (P.z) {
+            unpack8(va[i], a);
+            times_gradient(P.act, d, a);
+          }
 #pragma unroll
-        for (int e = 0; e < 8; ++e) sum[0][e] += d[e];
-        if (P.dz) *reinterpret_cast<uint4*>(P.dz + row + c) = pack8(d);
+          for (int e = 0; e < 8; ++e) sum[0][e] += d[e];
+          if (P.dz) *reinterpret_cast<uint4*>(P.dz + row + c) = pack8(d);
+        }
       }
     }
   }

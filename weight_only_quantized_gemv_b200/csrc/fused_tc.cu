@@ -320,16 +320,28 @@ __device__ __forceinline__ void store_tile(uint32_t a, int tile, int lane, const
 
 constexpr int kTok = 8;
 
-// One row's values to tokens `stride` elements apart.
-__device__ __forceinline__ void store_tokens(__half* o, size_t stride, const float (&v)[kTok],
-                                             int count) {
-  if (count >= kTok) {
+// Between "one row, two tokens" and "two rows, one token" (packed fp16): lanes l and l ^ 1 hold
+// neighbouring rows; the even one ends up with the first token of both, the odd one with the
+// second.  The same exchange goes back.
+__device__ __forceinline__ uint32_t exchange_rows(uint32_t v, int lane) {
+  const uint32_t o = __shfl_xor_sync(0xffffffffu, v, 1);
+  uint32_t r;
+  asm("prmt.b32 %0, %1, %2, %3;" : "=r"(r) : "r"(v), "r"(o), "r"((lane & 1) ? 0x3276u : 0x5410u));
+  return r;
+}
+
+// The warp's values of N tokens, the first `count` of them real, `stride` elements apart; `o`
+// points at token 0 of the lane's row, `in`: the row exists.  Two rows in one 4-byte store.
+template <int N>
+__device__ __forceinline__ void store_tokens(__half* o, size_t stride, const float (&v)[N],
+                                             int count, int lane, bool in) {
+  const int odd = lane & 1;
+  __half* p = o + odd * stride - odd;
 #pragma unroll
-    for (int e = 0; e < kTok; ++e, o += stride) *o = __float2half_rn(v[e]);
-  } else {
-#pragma unroll
-    for (int e = 0; e < kTok - 1; ++e, o += stride)
-      if (e < count) *o = __float2half_rn(v[e]);
+  for (int e = 0; e < N; e += 2, p += 2 * stride) {
+    const __half2 h = __floats2half2_rn(v[e], v[e + 1]);
+    const uint32_t w = exchange_rows(qdq::h2_as_u32(h), lane);
+    if (in && e + odd < count) *reinterpret_cast<uint32_t*>(p) = w;
   }
 }
 
@@ -352,14 +364,14 @@ __device__ __forceinline__ void act_all(int act, float (&v)[N]) {  // one branch
 // rows alternate 16 gate / 16 up: the lanes exchange, per pair of tokens, so that the gate
 // lanes finish the even token and the up lanes the odd one
 __device__ __forceinline__ void finish_gated(const TcParams& P, float (&v)[kTok], int m0, int count,
-                                             int row, float bias) {
+                                             int row, float bias, int lane) {
   const qfused::Epilogue& E = P.epi;
   const bool in = row < P.rows;
   const int F = P.ld, f = (row >> 5) * 16 + (row & 15), up = (row >> 4) & 1;
 #pragma unroll
   for (int e = 0; e < kTok; ++e) v[e] += bias;
-  if (E.zsave && in)
-    store_tokens(E.zsave + ((size_t)m0 * 2 + up) * F + f, (size_t)2 * F, v, count);
+  if (E.zsave)
+    store_tokens(E.zsave + ((size_t)m0 * 2 + up) * F + f, (size_t)2 * F, v, count, lane, in);
   float g[kTok / 2], u[kTok / 2];
 #pragma unroll
   for (int e = 0; e < kTok / 2; ++e) {
@@ -368,37 +380,42 @@ __device__ __forceinline__ void finish_gated(const TcParams& P, float (&v)[kTok]
     u[e] = up ? v[2 * e + 1] : other;
   }
   act_all(E.act, g);
-  if (!in) return;
-  __half* o = E.y + (size_t)(m0 + up) * F + f;
 #pragma unroll
-  for (int e = 0; e < kTok / 2; ++e, o += 2 * (size_t)F)
-    if (2 * e + up < count) *o = __float2half_rn(g[e] * u[e]);
+  for (int e = 0; e < kTok / 2; ++e) g[e] *= u[e];
+  // this lane's tokens: up, up + 2, ..
+  store_tokens(E.y + (size_t)(m0 + up) * F + f, (size_t)2 * F, g, (count - up + 1) / 2, lane, in);
 }
 
-__device__ __forceinline__ void load_residual(const TcParams& P, __half (&r)[kTok], int m0,
-                                              int count, int row) {
-  if (!P.epi.residual || row >= P.rows) return;
-  const __half* o = P.epi.residual + (size_t)m0 * P.ld + row;
+// The warp's residual of kTok tokens, two rows in one 4-byte load each (exchanged when used).
+__device__ __forceinline__ void load_residual(const TcParams& P, uint32_t (&r)[kTok / 2], int m0,
+                                              int count, int row, int lane) {
+  if (!P.epi.residual) return;
+  const int odd = lane & 1;
+  const __half* p = P.epi.residual + (size_t)(m0 + odd) * P.ld + row - odd;
 #pragma unroll
-  for (int e = 0; e < kTok; ++e, o += P.ld)
-    if (e < count) r[e] = *o;
+  for (int e = 0; e < kTok; e += 2, p += 2 * (size_t)P.ld)
+    if (row < P.rows && e + odd < count) r[e / 2] = *reinterpret_cast<const uint32_t*>(p);
 }
 
-// residual: the row's values, loaded ahead
 __device__ __forceinline__ void finish(const TcParams& P, float (&v)[kTok], int m0, int count,
-                                       int row, float bias, const __half (&residual)[kTok]) {
+                                       int row, float bias, const uint32_t (&residual)[kTok / 2],
+                                       int lane) {
   const qfused::Epilogue& E = P.epi;
-  if (row >= P.rows) return;
+  const bool in = row < P.rows;
   const size_t o = (size_t)m0 * P.ld + row;
 #pragma unroll
   for (int e = 0; e < kTok; ++e) v[e] += bias;
-  if (E.zsave) store_tokens(E.zsave + o, P.ld, v, count);
+  if (E.zsave) store_tokens(E.zsave + o, P.ld, v, count, lane, in);
   act_all(E.act, v);
   if (E.residual) {
 #pragma unroll
-    for (int e = 0; e < kTok; ++e) v[e] += __half2float(residual[e]);
+    for (int e = 0; e < kTok; e += 2) {
+      const float2 r = __half22float2(qdq::u32_as_h2(exchange_rows(residual[e / 2], lane)));
+      v[e] += r.x;
+      v[e + 1] += r.y;
+    }
   }
-  store_tokens(E.y + o, P.ld, v, count);
+  store_tokens(E.y + o, P.ld, v, count, lane, in);
 }
 
 __device__ __forceinline__ void tmem_ld8(uint32_t taddr, uint32_t (&r)[8]) {
@@ -784,11 +801,12 @@ __global__ void __launch_bounds__(TcCfg<BNX, FMT, PAIR>::kThreads, 1)
         }
         __syncwarp();
       }
-      __half res[kTok];
-      load_residual(P, res, m0 + c_first, cols - c_first, row);
+      uint32_t res[kTok / 2] = {};
+      load_residual(P, res, m0 + c_first, cols - c_first, row, lane);
       for (int c0 = c_first; c0 < cols; c0 += step) {
-        __half res_next[kTok];
-        if (c0 + step < cols) load_residual(P, res_next, m0 + c0 + step, cols - c0 - step, row);
+        uint32_t res_next[kTok / 2] = {};
+        if (c0 + step < cols)
+          load_residual(P, res_next, m0 + c0 + step, cols - c0 - step, row, lane);
         float v[kTok];
         if (whole) {
           uint32_t r[8];
@@ -817,11 +835,11 @@ __global__ void __launch_bounds__(TcCfg<BNX, FMT, PAIR>::kThreads, 1)
           }
         }
         if (E.gated)
-          finish_gated(P, v, m0 + c0, cols - c0, row, bias);
+          finish_gated(P, v, m0 + c0, cols - c0, row, bias, lane);
         else
-          finish(P, v, m0 + c0, cols - c0, row, bias, res);
+          finish(P, v, m0 + c0, cols - c0, row, bias, res, lane);
 #pragma unroll
-        for (int e = 0; e < kTok; ++e) res[e] = res_next[e];
+        for (int e = 0; e < kTok / 2; ++e) res[e] = res_next[e];
       }
       if (!whole && lane == 0 && member == 0) *counter = 0u;  // ready for the next call
       if (last) break;
