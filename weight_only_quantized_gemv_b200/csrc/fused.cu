@@ -214,6 +214,7 @@ __global__ void __launch_bounds__(32 * kGradWarps) grad_kernel(const GradParams 
 #pragma unroll
     for (int b = 0; b < NB; ++b) {
       float t = 0.f;
+#pragma unroll 8
       for (unsigned y = 0; y < gridDim.y; ++y)
         t += __ldcg(P.partials + ((size_t)y * NB + b) * P.W + cc);
       P.dbias[(size_t)b * P.W + cc] = t;
@@ -221,13 +222,19 @@ __global__ void __launch_bounds__(32 * kGradWarps) grad_kernel(const GradParams 
   if (threadIdx.x == 0) P.counters[blockIdx.x] = 0u;  // ready for the next call
 }
 
-// Strips of rows: enough blocks for a few per SM, at least 32 rows (four per warp) each.
+// Rows per strip: 64 (eight a warp), or fewer, down to one a warp, while the blocks do not fill
+// the SMs twice; at most kMaxStrips strips are joined.
+constexpr int kMaxStrips = 64;
+int grad_rows(int M, int W, int sms) {
+  const long long cols = (W + kGradCols - 1) / kGradCols;
+  const int least = ((M + kMaxStrips - 1) / kMaxStrips + kGradWarps - 1) / kGradWarps * kGradWarps;
+  int rows = 64;
+  while (rows > kGradWarps && cols * ((M + rows - 1) / rows) < 2LL * sms) rows /= 2;
+  return rows > least ? rows : least;
+}
 int grad_strips(int M, int W, int sms) {
-  const int cols = (W + kGradCols - 1) / kGradCols;
-  int strips = (4 * sms + cols - 1) / cols;
-  const int most = (M + 31) / 32;
-  if (strips > most) strips = most;
-  return strips < 1 ? 1 : strips;
+  const int rows = grad_rows(M, W, sms);
+  return (M + rows - 1) / rows;
 }
 
 // ---------------------------------------------------------------------------
@@ -271,25 +278,21 @@ int sm_count() {
 }
 
 // dz follows the partial sums
-size_t grad_partial_bytes(int M, int N, int sms) {
-  // (strips of the linear kernel, W = N, or of the gated one, W = N / 2; the larger)
-  const size_t a = (size_t)grad_strips(M, N, sms), b = (size_t)grad_strips(M, N / 2, sms);
-  return (a > b ? a : b) * N * sizeof(float);
+size_t grad_partial_bytes(int M, int N) {  // bound over every M up to this one
+  return (size_t)(M < 64 * kGradWarps ? (M + kGradWarps - 1) / kGradWarps : kMaxStrips) * N *
+         sizeof(float);
 }
-size_t backward_partial_bytes(int M, int N, int sms) {
-  const size_t a = qfused::tc_partial_bytes(M), b = grad_partial_bytes(M, N, sms);
+size_t backward_partial_bytes(int M, int N) {
+  const size_t a = qfused::tc_partial_bytes(M), b = grad_partial_bytes(M, N);
   return qfused::align_up(a > b ? a : b, 256);
 }
 
 // Runs a forward product: the GEMV up to 16 rows, the tensor-core product above.
 ql_status forward(qfused::Product& p, void* workspace, size_t workspace_bytes) {
   const size_t off = qfused::partial_offset(p.N);
-  const size_t part = p.M <= kGemvRows
-                          ? qfused::gemv_partial_bytes(p.fmt, p.M, p.N, p.K, p.epi.gated)
-                          : qfused::tc_partial_bytes(p.M);
-  if (!part) return QL_ERR_CUDA;
-  if (!workspace || workspace_bytes < off + part) return QL_ERR_WORKSPACE;
+  if (!workspace || workspace_bytes < off) return QL_ERR_WORKSPACE;
   if (!aligned(workspace, 256)) return QL_ERR_ALIGN;
+  p.partial_bytes = workspace_bytes - off;
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   p.err = static_cast<uint32_t*>(workspace);
   p.counters = reinterpret_cast<uint32_t*>(
@@ -320,7 +323,7 @@ ql_status backward(qfused::Product& p, const __half* dy, const __half* z, int W,
   const int sms = sm_count();
   if (sms <= 0) return QL_ERR_CUDA;
   const size_t off = qfused::partial_offset(p.N);
-  const size_t part = backward_partial_bytes(p.M, p.N, sms);
+  const size_t part = backward_partial_bytes(p.M, p.N);
   const size_t dz_bytes = dz_is_dy ? 0 : (size_t)p.M * p.N * sizeof(__half);
   if (!workspace || workspace_bytes < off + part + dz_bytes) return QL_ERR_WORKSPACE;
   if (!aligned(workspace, 256)) return QL_ERR_ALIGN;
@@ -329,6 +332,7 @@ ql_status backward(qfused::Product& p, const __half* dy, const __half* z, int W,
   p.err = static_cast<uint32_t*>(workspace);
   p.counters = reinterpret_cast<uint32_t*>(ws + qfused::kErrBytes);
   p.partials = reinterpret_cast<float*>(ws + off);
+  p.partial_bytes = part;
   p.x = dz_is_dy ? dy : dz;
   if (!dz_is_dy || dbias) {
     GradParams g;
@@ -341,9 +345,8 @@ ql_status backward(qfused::Product& p, const __half* dy, const __half* z, int W,
     g.M = p.M;
     g.W = W;
     g.act = p.epi.act;
-    int strips = grad_strips(p.M, W, sms);
-    g.rows = (p.M + strips - 1) / strips;
-    strips = (p.M + g.rows - 1) / g.rows;  // no empty strip
+    g.rows = grad_rows(p.M, W, sms);
+    const int strips = grad_strips(p.M, W, sms);
     const ql_status s = gated ? launch_grad<true>(g, strips, p.stream)
                               : launch_grad<false>(g, strips, p.stream);
     if (s != QL_OK) return s;
@@ -360,8 +363,6 @@ ql_status backward(qfused::Product& p, const __half* dy, const __half* z, int W,
 
 extern "C" size_t qlinear_fused_workspace_bytes(int fmt, int M, int N, int K, int backward) {
   if (!fmt_ok(fmt) || !shape_ok(M, N, K)) return 0;
-  const int sms = sm_count();
-  if (sms <= 0) return 0;
   size_t part = 0;
   for (int m = 1; m <= M && m <= kGemvRows; ++m)
     for (int gated = 0; gated < (N % (2 * kTileN) ? 1 : 2); ++gated) {
@@ -371,7 +372,7 @@ extern "C" size_t qlinear_fused_workspace_bytes(int fmt, int M, int N, int K, in
     }
   if (qfused::tc_partial_bytes(M) > part) part = qfused::tc_partial_bytes(M);
   if (backward) {
-    const size_t b = backward_partial_bytes(M, N, sms) + (size_t)M * N * sizeof(__half);
+    const size_t b = backward_partial_bytes(M, N) + (size_t)M * N * sizeof(__half);
     if (b > part) part = b;
   }
   return qfused::partial_offset(N) + qfused::align_up(part, 256);

@@ -36,6 +36,7 @@ struct Product {
   uint32_t* err;        // sticky wait flags
   uint32_t* counters;   // arrivals, zero between calls
   float* partials;
+  size_t partial_bytes;  // room at partials (QL_ERR_WORKSPACE if it is too little)
   cudaStream_t stream;
 };
 

@@ -54,7 +54,11 @@ using namespace qtc;
 namespace {
 
 constexpr uint32_t kErrStage = 1u, kErrAcc = 2u;
-constexpr int kTeams = 2, kTeamWarps = 8;
+#ifndef TEAMS
+#define TEAMS 2
+#endif
+constexpr int kTeams = TEAMS, kTeamWarps = 8;
+constexpr int kMembers = 1 + kTeams * kTeamWarps / 4;  // warps per quadrant in the last epilogue
 
 template <int BNX_, int FMT_, bool PAIR_>
 struct TcCfg {
@@ -538,12 +542,16 @@ __global__ void __launch_bounds__(TcCfg<BNX, FMT, PAIR>::kThreads, 1)
     qlk::mbar_init(fin, 1);
     qlk::mbar_init(lastf, 1);
     for (int i = 0; i < 4; ++i) {
-      qlk::mbar_init(bars + 8 * C::kTailBar + 16 * i, 5);
+      qlk::mbar_init(bars + 8 * C::kTailBar + 16 * i, kMembers);
       qlk::mbar_init(bars + 8 * C::kTailBar + 16 * i + 8, 1);
     }
     misc[1] = 0u;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
+  // The pair's allocation needs both CTAs to be running: one that started ahead of its peer
+  // waits here (without this, launches beside other kernels now and then ended with a launch
+  // failure).  Likewise at the end: neither leaves before both have freed.
+  if constexpr (PAIR) sync_all<PAIR>();
   if (warp == 1) tmem_alloc<PAIR>(ring + C::kMiscOff, C::kTmemCols);
   tc_fence_before();
   sync_all<PAIR>();
@@ -685,7 +693,7 @@ __global__ void __launch_bounds__(TcCfg<BNX, FMT, PAIR>::kThreads, 1)
       for (; ok && sg.next(P, tile, k0, k1, slot); ++j) {
         const int rb = (tile / P.mtiles) * C::kCtas + (int)rank;
         for (int k = k0; k < k1; ++k, ++n) {
-          if ((n & 1) == team) {
+          if (n % kTeams == team) {
             const int tb = rb < P.rblocks ? tiles_in_block(BWD ? k : rb, P.ntiles) : 0;
             // decode into registers while the MMAs may still read the stage
             if (!(ok = warp_wait(cfull(c), cph, W, kErrStage, lane))) break;
@@ -701,7 +709,7 @@ __global__ void __launch_bounds__(TcCfg<BNX, FMT, PAIR>::kThreads, 1)
               }
             }
             if (n >= C::S) {
-              if (n <= C::S + 1) qlk::grid_dependency_wait();
+              if (n < C::S + kTeams) qlk::grid_dependency_wait();
               if (!(ok = warp_wait(empty(s), sph, W, kErrStage, lane))) break;
             }
             if (BWD || dt < tb) store_tile(ring + s * C::kStageBytes, dt, lane, d);
@@ -726,7 +734,7 @@ __global__ void __launch_bounds__(TcCfg<BNX, FMT, PAIR>::kThreads, 1)
     // multiplied; nothing follows the last, so the decoding warps share its chunks.
     qlk::grid_dependency_wait();
     const int q = warp & 3;
-    const int member = decoder ? 1 + (warp - C::kDqWarp0) / 4 : 0;  // of the quadrant's five
+    const int member = decoder ? 1 + (warp - C::kDqWarp0) / 4 : 0;  // of the quadrant's
     const uint32_t tail = bars + 8 * C::kTailBar + 16 * q;          // two barriers
     const long long U = (long long)(P.tiles - P.whole) * P.steps;
     const qfused::Epilogue& E = P.epi;
@@ -735,7 +743,7 @@ __global__ void __launch_bounds__(TcCfg<BNX, FMT, PAIR>::kThreads, 1)
       const bool last = decoder || sg.done(P);
       const int a = j & 1;
       // the last accumulator has a barrier of its own, which completes once: the decoding warps
-      // have not followed the phases of the others (the five see it complete, or all time out)
+      // have not followed the phases of the others (all see it complete, or all time out)
       if (!(last ? warp_wait(lastf, 0, W, kErrAcc, lane, false)
                  : warp_wait(accf(a), (j >> 1) & 1, W, kErrAcc, lane)))
         break;
@@ -745,7 +753,7 @@ __global__ void __launch_bounds__(TcCfg<BNX, FMT, PAIR>::kThreads, 1)
       const int m0 = (tile % P.mtiles) * P.bn;
       const int cols = P.M - m0 < P.bn ? P.M - m0 : P.bn;
       const uint32_t tb = tmem + ((uint32_t)(32 * q) << 16) + (uint32_t)(a * BNX);
-      const int step = last ? 5 * kTok : kTok, c_first = last ? member * kTok : 0;
+      const int step = last ? kMembers * kTok : kTok, c_first = last ? member * kTok : 0;
       float bias = 0.f;
       if (E.bias && row < P.rows)
         bias = __half2float(E.bias[E.gated ? (size_t)((row >> 4) & 1) * P.ld + (row >> 5) * 16 +
@@ -783,7 +791,7 @@ __global__ void __launch_bounds__(TcCfg<BNX, FMT, PAIR>::kThreads, 1)
           }
           prev = __shfl_sync(0xffffffffu, prev, 0);
         } else {
-          // the five warps' sums are written, then one arrival for all of them
+          // the members' sums are written, then one arrival for all of them
           if (lane == 0) qlk::mbar_arrive(tail);
           if (member == 0) {
             if (!warp_wait(tail, 0, W, kErrAcc, lane, false)) break;
@@ -857,6 +865,7 @@ __global__ void __launch_bounds__(TcCfg<BNX, FMT, PAIR>::kThreads, 1)
     tc_fence_after();
     tmem_dealloc<PAIR>(tmem, C::kTmemCols);
   }
+  if constexpr (PAIR) sync_all<PAIR>();
 }
 
 // ---------------------------------------------------------------------------
@@ -1007,6 +1016,7 @@ ql_status launch_as(const qfused::Product& p, const Tokens& tk) {
     return QL_ERR_CUDA;
   const int maxw = resident_workers<BNX, FMT, PAIR, BWD>(dev, sms);
   if (maxw <= 0) return QL_ERR_CUDA;
+  if (p.partial_bytes < (size_t)2 * sms * 128 * tk.bn * sizeof(float)) return QL_ERR_WORKSPACE;
   constexpr int ctas = PAIR ? 2 : 1;
   TcParams P;
   P.qw = static_cast<const uint8_t*>(p.packed);

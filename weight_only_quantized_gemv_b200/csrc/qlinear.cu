@@ -577,6 +577,7 @@ ql_status qfused::launch_gemv(const Product& q) {
   Plan p;
   if (make_plan(q.fmt, q.M, q.N, q.K, false, &p, 1, q.epi.gated ? 2 : 1) != cudaSuccess)
     return QL_ERR_CUDA;
+  if (q.partial_bytes < p.ws_bytes - p.partial_offset) return QL_ERR_WORKSPACE;
   Call c{q.fmt, false, q.x, q.packed, q.p0, q.p1, nullptr, nullptr, nullptr, q.epi.y,
          q.M, q.N, q.K, nullptr, 0, q.stream};
   return enqueue(c, p, q.err, q.counters, q.partials, &q.epi);

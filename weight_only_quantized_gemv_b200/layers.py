@@ -153,12 +153,14 @@ class _FusedWorkspace:
             stream.wait_stream(self._fused_last[1])
         self._fused_last = (raw, stream)
 
-    def _fused_new(self, shape: tuple, index: int, stream) -> torch.Tensor:
-        """A new fp16 tensor, made on the call's stream."""
+    @staticmethod
+    def _fused_new(like: torch.Tensor, shape: tuple, index: int, stream) -> torch.Tensor:
+        """A new tensor of an (already checked) input's type and device, made on the call's
+        stream."""
         if stream is None:
-            return torch.empty(shape, dtype=_F16, device=self.qweight.device)
+            return like.new_empty(shape)
         with torch.cuda.stream(_as_stream(stream, index)):
-            return torch.empty(shape, dtype=_F16, device=self.qweight.device)
+            return like.new_empty(shape)
 
     def _fused_elsewhere(self, method, *args, **kw):
         """method(*args, **kw) with the layer's device current, if another one is now."""
@@ -332,7 +334,7 @@ class QuantLinear(_FusedWorkspace):
         M = x.shape[0]
         px = _fused_ptr(x, (M, K), index, "x")
         if y is None:
-            y = self._fused_new((M, N), index, stream)
+            y = self._fused_new(x, (M, N), index, stream)
         head = (fmt, px, *self._fused_weights(), _fused_ptr(bias, (N,), index, "bias"),
                 _fused_ptr(residual, (M, N), index, "residual"), _act(act),
                 _fused_ptr(y, (M, N), index, "y"), _fused_ptr(z, (M, N), index, "z"), M, N, K)
@@ -355,7 +357,7 @@ class QuantLinear(_FusedWorkspace):
         M = dy.shape[0]
         pdy = _fused_ptr(dy, (M, N), index, "dy")
         if dx is None:
-            dx = self._fused_new((M, K), index, stream)
+            dx = self._fused_new(dy, (M, K), index, stream)
         head = (fmt, pdy, _fused_ptr(z, (M, N), index, "z"), *self._fused_weights(), _act(act),
                 _fused_ptr(dx, (M, K), index, "dx"),
                 _fused_ptr(dbias, (N,), index, "dbias", _F32), M, N, K)
@@ -416,7 +418,7 @@ class GatedLinear(_FusedWorkspace):
         M, F = x.shape[0], self.F
         px = _fused_ptr(x, (M, K), index, "x")
         if h is None:
-            h = self._fused_new((M, F), index, stream)
+            h = self._fused_new(x, (M, F), index, stream)
         head = (fmt, px, *self._fused_weights(), _fused_ptr(bias, (2, F), index, "bias"), _act(act),
                 _fused_ptr(h, (M, F), index, "h"), _fused_ptr(gu, (M, 2, F), index, "gu"), M, F,
                 K)
@@ -437,7 +439,7 @@ class GatedLinear(_FusedWorkspace):
         M, F = dh.shape[0], self.F
         pdh = _fused_ptr(dh, (M, F), index, "dh")
         if dx is None:
-            dx = self._fused_new((M, K), index, stream)
+            dx = self._fused_new(dh, (M, K), index, stream)
         head = (fmt, pdh, _fused_ptr(gu, (M, 2, F), index, "gu"), *self._fused_weights(), _act(act),
                 _fused_ptr(dx, (M, K), index, "dx"),
                 _fused_ptr(dbias, (2, F), index, "dbias", _F32), M, F, K)
