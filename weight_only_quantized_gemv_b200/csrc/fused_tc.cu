@@ -76,20 +76,26 @@ struct TcCfg {
   static constexpr int kParChunk = FMT == kLUT4 ? 128 : 32;  // per tile and array
   static constexpr int kSlot = kCodeBytes + (FMT == kLUT4 ? 1 : 2) * kBlockTiles * kParChunk;
   static constexpr int S = 3;
-  static constexpr int kBudget = 232448 - 1024 - 512;        // alignment, barriers
+  // A team of decoding warps must follow every phase of a barrier that it waits for (a parity
+  // says "this phase or the one before the last"), and the teams take the stages in turn.  So
+  // the barriers that tell them of codes in the SC slots and of the S stages handed back are
+  // kTeams times as many, each of which then belongs to one team.
+  static constexpr int SE = kTeams * S;
+  static constexpr int kBudget = 232448 - 768;               // barriers
   static constexpr int SC0 = (kBudget - S * kStageBytes) / kSlot;
   static constexpr int SC = SC0 < 12 ? SC0 : 12;
+  static constexpr int SF = kTeams * SC;
   static_assert(SC >= 2, "code ring");
   static constexpr int kRingC = S * kStageBytes;
   static constexpr int kBarOff = kRingC + SC * kSlot;
-  // full[S] empty[S] accf[2] acce[2] fin cfull[SC] cempty[SC] tail[4][2] last; then the tensor
+  // full[S] empty[SE] accf[2] acce[2] fin cfull[SF] cempty[SC] tail[4][2] last; then the tensor
   // memory's base, the abort flag, arrivals before the last segment's per quadrant; the table
-  static constexpr int kTailBar = 2 * S + 5 + 2 * SC;
+  static constexpr int kTailBar = S + SE + 5 + SF + SC;
   static constexpr int kLastBar = kTailBar + 8;
   static constexpr int kMiscOff = kBarOff + 8 * (kLastBar + 1);
   static constexpr int kLutOff = kMiscOff + 24;
   static constexpr int kSpareOff = kLutOff + 64;  // a word per decoding warp
-  static constexpr int kSmem = kSpareOff + 4 * kTeams * kTeamWarps + 1024;
+  static constexpr int kSmem = kSpareOff + 4 * kTeams * kTeamWarps;
   static_assert(kSmem <= 232448, "shared memory");
   static constexpr int kEpiWarp0 = 4, kDqWarp0 = 8;
   static constexpr int kWarps = kDqWarp0 + kTeams * kTeamWarps;
@@ -491,17 +497,16 @@ __global__ void __launch_bounds__(TcCfg<BNX, FMT, PAIR>::kThreads, 1)
     fused_tc_kernel(const TcParams P, const __grid_constant__ CUtensorMap xmap) {
   using C = TcCfg<BNX, FMT, PAIR>;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
-  const uint32_t raw = qlk::smem_addr(smem_raw);
-  const uint32_t ring = (raw + 1023u) & ~1023u;
-  uint8_t* smem = smem_raw + (ring - raw);
+  const uint32_t ring = qlk::smem_addr(smem_raw);  // 1024-byte aligned, as the swizzle wants
+  uint8_t* smem = smem_raw;
   const uint32_t bars = ring + C::kBarOff;
   auto full = [&](int s) { return bars + 8 * s; };
-  auto empty = [&](int s) { return bars + 8 * (C::S + s); };
-  auto accf = [&](int a) { return bars + 8 * (2 * C::S + a); };
-  auto acce = [&](int a) { return bars + 8 * (2 * C::S + 2 + a); };
-  const uint32_t fin = bars + 8 * (2 * C::S + 4);
-  auto cfull = [&](int c) { return bars + 8 * (2 * C::S + 5 + c); };
-  auto cempty = [&](int c) { return bars + 8 * (2 * C::S + 5 + C::SC + c); };
+  auto empty = [&](int e) { return bars + 8 * (C::S + e); };
+  auto accf = [&](int a) { return bars + 8 * (C::S + C::SE + a); };
+  auto acce = [&](int a) { return bars + 8 * (C::S + C::SE + 2 + a); };
+  const uint32_t fin = bars + 8 * (C::S + C::SE + 4);
+  auto cfull = [&](int f) { return bars + 8 * (C::S + C::SE + 5 + f); };
+  auto cempty = [&](int c) { return bars + 8 * (C::S + C::SE + 5 + C::SF + c); };
   const uint32_t lastf = bars + 8 * C::kLastBar;  // the worker's last accumulator is complete
   volatile uint32_t* misc = reinterpret_cast<volatile uint32_t*>(smem + C::kMiscOff);
   float* lut = reinterpret_cast<float*>(smem + C::kLutOff);
@@ -527,14 +532,10 @@ __global__ void __launch_bounds__(TcCfg<BNX, FMT, PAIR>::kThreads, 1)
   if (FMT == kLUT4 && threadIdx.x < 16)
     lut[threadIdx.x] = __half2float(static_cast<const __half*>(P.p0)[threadIdx.x]);
   if (threadIdx.x == 0) {
-    for (int s = 0; s < C::S; ++s) {
-      qlk::mbar_init(full(s), C::kFullCount);
-      qlk::mbar_init(empty(s), 1);
-    }
-    for (int c = 0; c < C::SC; ++c) {
-      qlk::mbar_init(cfull(c), 1);
-      qlk::mbar_init(cempty(c), kTeamWarps);
-    }
+    for (int s = 0; s < C::S; ++s) qlk::mbar_init(full(s), C::kFullCount);
+    for (int e = 0; e < C::SE; ++e) qlk::mbar_init(empty(e), 1);
+    for (int f = 0; f < C::SF; ++f) qlk::mbar_init(cfull(f), 1);
+    for (int c = 0; c < C::SC; ++c) qlk::mbar_init(cempty(c), kTeamWarps);
     for (int a = 0; a < 2; ++a) {
       qlk::mbar_init(accf(a), 1);
       qlk::mbar_init(acce(a), C::kAccEmptyCount);
@@ -548,13 +549,10 @@ __global__ void __launch_bounds__(TcCfg<BNX, FMT, PAIR>::kThreads, 1)
     misc[1] = 0u;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
-  // The pair's allocation needs both CTAs to be running: one that started ahead of its peer
-  // waits here (without this, launches beside other kernels now and then ended with a launch
-  // failure).  Likewise at the end: neither leaves before both have freed.
-  if constexpr (PAIR) sync_all<PAIR>();
+  sync_all<PAIR>();  // barriers are set up (a pair's allocation also wants both CTAs running)
   if (warp == 1) tmem_alloc<PAIR>(ring + C::kMiscOff, C::kTmemCols);
   tc_fence_before();
-  sync_all<PAIR>();
+  __syncthreads();
   tc_fence_after();
   const uint32_t tmem = misc[0];
   qlk::grid_dependents_launch();
@@ -567,13 +565,19 @@ __global__ void __launch_bounds__(TcCfg<BNX, FMT, PAIR>::kThreads, 1)
     // ---- copies of x (dz)
     if (lane == 0) {
       qlk::grid_dependency_wait();
-      int s = 0, ph = 1, n = 0;
+      int s = 0, n = 0, e = 0, eph = 0;  // e: the barrier of stage n - S
       bool ok = true;
       const uint32_t bytes = (uint32_t)P.bn * 256u;  // both CTAs, both boxes
       while (ok && sg.next(P, tile, k0, k1, slot)) {
         const int m = (tile % P.mtiles) * P.bn + (int)rank * (P.bn / C::kCtas);
         for (int k = k0; k < k1; ++k) {
-          if (n >= C::S && !(ok = wait(empty(s), ph, W, kErrStage))) break;
+          if (n >= C::S) {
+            if (!(ok = wait(empty(e), eph, W, kErrStage))) break;
+            if (++e == C::SE) {
+              e = 0;
+              eph ^= 1;
+            }
+          }
           const uint32_t b = ring + s * C::kStageBytes + C::kABytes;
           if (leader) qlk::mbar_arrive_expect_tx(full(s), bytes);
 #pragma unroll
@@ -584,10 +588,7 @@ __global__ void __launch_bounds__(TcCfg<BNX, FMT, PAIR>::kThreads, 1)
               tma_2d(b + h * C::kHalfB, &xmap, k * 128 + h * 64, m, full(s));
           }
           ++n;
-          if (++s == C::S) {
-            s = 0;
-            ph ^= 1;
-          }
+          if (++s == C::S) s = 0;
         }
       }
       // no copy is in flight when the CTA exits (the leader's barriers count both CTAs')
@@ -599,7 +600,7 @@ __global__ void __launch_bounds__(TcCfg<BNX, FMT, PAIR>::kThreads, 1)
     // ---- copies of the units' codes and parameters: lanes 0, 1, 2 each issue one of a unit's
     // copies (LUT4: two) with one instruction
     {
-      int c = 0, ph = 1, n = 0;
+      int c = 0, ph = 1, n = 0, f = 0;
       bool ok = true;
       const uint8_t* base = P.qw;      // this lane's array, bytes per chunk of it
       uint32_t per = C::kChunk, off = 0;
@@ -621,23 +622,24 @@ __global__ void __launch_bounds__(TcCfg<BNX, FMT, PAIR>::kThreads, 1)
             const int tb = tiles_in_block(b, P.ntiles);
             const long long ch = chunk_index(b, g, 0, P.G, P.ntiles);
             if (lane == 0)
-              qlk::mbar_arrive_expect_tx(cfull(c), tb * (C::kChunk + (kCopies - 1) * C::kParChunk));
+              qlk::mbar_arrive_expect_tx(cfull(f), tb * (C::kChunk + (kCopies - 1) * C::kParChunk));
             __syncwarp();
             if (lane < kCopies)
               qlk::bulk_g2s(ring + C::kRingC + c * C::kSlot + off, base + ch * per, tb * per,
-                            cfull(c));
+                            cfull(f));
           } else if (lane == 0) {  // no rows for this CTA of the pair
-            qlk::mbar_arrive(cfull(c));
+            qlk::mbar_arrive(cfull(f));
           }
           ++n;
+          f = f + 1 == C::SF ? 0 : f + 1;
           if (++c == C::SC) {
             c = 0;
             ph ^= 1;
           }
         }
       }
-      for (int i = n > C::SC ? n - C::SC : 0; i < n; ++i)
-        warp_wait(cfull(i % C::SC), (i / C::SC) & 1, W, kErrStage, lane, false);
+      for (int i = n > C::SC ? n - C::SC : 0; i < n; ++i)  // none in flight at the end
+        warp_wait(cfull(i % C::SF), (i / C::SF) & 1, W, kErrStage, lane, false);
     }
   } else if (warp == 1) {
     // ---- MMA issue (the leader of a pair).  The whole warp runs the loop, so that the
@@ -645,7 +647,7 @@ __global__ void __launch_bounds__(TcCfg<BNX, FMT, PAIR>::kThreads, 1)
     if (leader) {
       qlk::grid_dependency_wait();
       const uint32_t idesc = idesc_f16(128 * C::kCtas, P.bn) | (BWD ? kTransposeA : 0u);
-      int s = 0, ph = 0, j = 0;
+      int s = 0, ph = 0, e = 0, j = 0;
       bool ok = true, ready = false;
       for (; ok && sg.next(P, tile, k0, k1, slot); ++j) {
         const int a = j & 1;
@@ -668,8 +670,9 @@ __global__ void __launch_bounds__(TcCfg<BNX, FMT, PAIR>::kThreads, 1)
               mma<PAIR>(d, pa + (BWD ? 128 * kk : (kk >> 2) * (C::kHalfA >> 4) + 2 * (kk & 3)),
                         pb + (kk >> 2) * (C::kHalfB >> 4) + 2 * (kk & 3), idesc,
                         kk == 0 ? (uint32_t)(k != k0) : 1u);
-            commit_both(empty(s));
+            commit_both(empty(e));
           }
+          e = e + 1 == C::SE ? 0 : e + 1;
           ready = __all_sync(0xffffffffu, next_ready);
           s = s1;
           ph = ph1;
@@ -689,14 +692,14 @@ __global__ void __launch_bounds__(TcCfg<BNX, FMT, PAIR>::kThreads, 1)
       // ---- decoding teams
       const int team = (warp - C::kDqWarp0) / kTeamWarps;
       const int dt = (warp - C::kDqWarp0) % kTeamWarps;
-      int n = 0, s = 0, sph = 1, c = 0, cph = 0;
+      int n = 0, s = 0, e = 0, eph = 0, c = 0, f = 0, fph = 0;  // e: the barrier of stage n - S
       for (; ok && sg.next(P, tile, k0, k1, slot); ++j) {
         const int rb = (tile / P.mtiles) * C::kCtas + (int)rank;
         for (int k = k0; k < k1; ++k, ++n) {
           if (n % kTeams == team) {
             const int tb = rb < P.rblocks ? tiles_in_block(BWD ? k : rb, P.ntiles) : 0;
             // decode into registers while the MMAs may still read the stage
-            if (!(ok = warp_wait(cfull(c), cph, W, kErrStage, lane))) break;
+            if (!(ok = warp_wait(cfull(f), fph, W, kErrStage, lane))) break;
             Decoded d;
             if (dt < tb) {
               decode_tile<C>(ring + C::kRingC + c * C::kSlot, dt, lane, lut, cempty(c),
@@ -710,20 +713,22 @@ __global__ void __launch_bounds__(TcCfg<BNX, FMT, PAIR>::kThreads, 1)
             }
             if (n >= C::S) {
               if (n < C::S + kTeams) qlk::grid_dependency_wait();
-              if (!(ok = warp_wait(empty(s), sph, W, kErrStage, lane))) break;
+              if (!(ok = warp_wait(empty(e), eph, W, kErrStage, lane))) break;
             }
             if (BWD || dt < tb) store_tile(ring + s * C::kStageBytes, dt, lane, d);
             asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // visible to the MMAs
             __syncwarp();
             if (lane == 0) arrive_lead(full(s));
           }
-          if (++s == C::S) {
-            s = 0;
-            sph ^= 1;
+          if (++s == C::S) s = 0;
+          if (n >= C::S && ++e == C::SE) {
+            e = 0;
+            eph ^= 1;
           }
-          if (++c == C::SC) {
-            c = 0;
-            cph ^= 1;
+          if (++c == C::SC) c = 0;
+          if (++f == C::SF) {
+            f = 0;
+            fph ^= 1;
           }
         }
       }
@@ -865,7 +870,6 @@ __global__ void __launch_bounds__(TcCfg<BNX, FMT, PAIR>::kThreads, 1)
     tc_fence_after();
     tmem_dealloc<PAIR>(tmem, C::kTmemCols);
   }
-  if constexpr (PAIR) sync_all<PAIR>();
 }
 
 // ---------------------------------------------------------------------------

@@ -426,11 +426,6 @@ __global__ void __launch_bounds__(TcCfg<BN, FUSED, FMT, PAIR>::kThreads, 1)
     *abort = 0u;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
-  // the pair's allocation needs both CTAs to be running
-  if constexpr (PAIR) {
-    __syncwarp();
-    cluster_sync();
-  }
   if (warp == 1) tmem_alloc<PAIR>(slot, C::kTmemCols);
   tc_fence_before();
   // the peer's copies and arrivals reach the leader's barriers only once they are set up
@@ -679,10 +674,6 @@ __global__ void __launch_bounds__(TcCfg<BN, FUSED, FMT, PAIR>::kThreads, 1)
   if (warp == 1) {
     tc_fence_after();
     tmem_dealloc<PAIR>(tmem, C::kTmemCols);
-  }
-  if constexpr (PAIR) {  // neither leaves before both have freed
-    __syncwarp();
-    cluster_sync();
   }
 }
 
