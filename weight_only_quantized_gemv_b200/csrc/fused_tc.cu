@@ -54,10 +54,7 @@ using namespace qtc;
 namespace {
 
 constexpr uint32_t kErrStage = 1u, kErrAcc = 2u;
-#ifndef TEAMS
-#define TEAMS 2
-#endif
-constexpr int kTeams = TEAMS, kTeamWarps = 8;
+constexpr int kTeams = 2, kTeamWarps = 8;
 constexpr int kMembers = 1 + kTeams * kTeamWarps / 4;  // warps per quadrant in the last epilogue
 
 template <int BNX_, int FMT_, bool PAIR_>
@@ -97,6 +94,7 @@ struct TcCfg {
   static constexpr int kSpareOff = kLutOff + 64;  // a word per decoding warp
   static constexpr int kSmem = kSpareOff + 4 * kTeams * kTeamWarps;
   static_assert(kSmem <= 232448, "shared memory");
+  static constexpr int kSpin = BNX == 256 ? 64 : 0;          // polls before a suspended wait
   static constexpr int kEpiWarp0 = 4, kDqWarp0 = 8;
   static constexpr int kWarps = kDqWarp0 + kTeams * kTeamWarps;
   static constexpr int kThreads = 32 * kWarps;
@@ -210,15 +208,28 @@ __device__ __noinline__ bool wait_slow(uint32_t bar, uint32_t parity, uint32_t a
   return false;
 }
 
+// Waking up from a suspended wait takes hundreds of cycles; polling takes issue slots.  So the
+// waits between the pipeline's roles (SPIN > 0) poll SPIN times first where the MMAs set the pace
+// (256-token tiles: 190 against 290 us on 1024 x 4096 x 28672 backward) and suspend at once where
+// the decoding does (32 rows, 8192 x 18944: 35.1 against 37.6 us).
+
 // One thread.
+template <int SPIN>
 __device__ __forceinline__ bool wait(uint32_t bar, uint32_t parity, const WaitCtx& w, uint32_t bit,
                                      bool honor_abort = true) {
+#pragma unroll 1
+  for (int i = 0; i < SPIN; ++i)
+    if (mbar_ready(bar, parity, false)) return true;
   return try_wait(bar, parity) || wait_slow(bar, parity, w.abort, w.err, bit, honor_abort);
 }
 
 // A whole warp: every lane sees the phase complete (the usual case), or one lane waits on.
+template <int SPIN>
 __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, const WaitCtx& w,
                                           uint32_t bit, int lane, bool honor_abort = true) {
+#pragma unroll 1
+  for (int i = 0; i < SPIN; ++i)
+    if (__all_sync(0xffffffffu, mbar_ready(bar, parity, false))) return true;
   if (__all_sync(0xffffffffu, try_wait(bar, parity))) return true;
   bool ok = true;
   if (lane == 0) ok = wait_slow(bar, parity, w.abort, w.err, bit, honor_abort);
@@ -235,6 +246,29 @@ __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, const W
 struct Decoded {
   uint4 v[4][2];  // [pair of steps, in the lane's order][row gi, gi + 8]
 };
+
+// Eight weights fp16(s (q - z)) of a pair of steps for row half h (see uniform_pair8), with the
+// field and the exponent of 2^(10 - shift) put together by one logic operation.
+template <int FMT>
+__device__ __forceinline__ uint4 uniform8(const uint32_t* w, int h, const __half2 (&zb)[2][2],
+                                          __half2 scale) {
+  uint32_t o[4];
+#pragma unroll
+  for (int ss = 0; ss < 2; ++ss)
+#pragma unroll
+    for (int dkp = 0; dkp < 2; ++dkp) {
+      const uint32_t word = FMT == kW8 ? w[2 * ss + h] : FMT == kW2 ? w[0] : w[ss];
+      const uint32_t v = dkp ? word >> 8 : word;
+      const uint32_t mask = FMT == kW8   ? 0x00FF00FFu
+                            : FMT == kW4 ? (h ? 0x00F000F0u : 0x000F000Fu)
+                                         : 0x00030003u << (4 * ss + 2 * h);
+      const uint32_t magic = qdq::magic_half(qdq::field_shift<FMT>(ss, h)) * 0x10001u;
+      uint32_t f;
+      asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(f) : "r"(v), "r"(mask), "r"(magic));
+      o[2 * ss + dkp] = qdq::h2_as_u32(__hmul2(__hsub2(qdq::u32_as_h2(f), zb[ss][h]), scale));
+    }
+  return make_uint4(o[0], o[1], o[2], o[3]);
+}
 
 // The code slot is handed back (`release`, `spare`: a shared word of the warp) as soon as every
 // lane holds its words.  The barrier arrival does not wait for shared loads in flight; the
@@ -309,7 +343,7 @@ __device__ __forceinline__ void decode_tile(uint32_t slot, int tile, int lane, c
     for (int i = 0; i < 4; ++i)
 #pragma unroll
       for (int h = 0; h < 2; ++h)
-        d.v[i][h] = qdq::uniform_pair8<FMT>(w + KP * i, 0, h, zb, h ? sh : sl);
+        d.v[i][h] = uniform8<FMT>(w + KP * i, h, zb, h ? sh : sl);
   }
 }
 
@@ -570,9 +604,10 @@ __global__ void __launch_bounds__(TcCfg<BNX, FMT, PAIR>::kThreads, 1)
       const uint32_t bytes = (uint32_t)P.bn * 256u;  // both CTAs, both boxes
       while (ok && sg.next(P, tile, k0, k1, slot)) {
         const int m = (tile % P.mtiles) * P.bn + (int)rank * (P.bn / C::kCtas);
+#pragma unroll 1
         for (int k = k0; k < k1; ++k) {
           if (n >= C::S) {
-            if (!(ok = wait(empty(e), eph, W, kErrStage))) break;
+            if (!(ok = wait<C::kSpin>(empty(e), eph, W, kErrStage))) break;
             if (++e == C::SE) {
               e = 0;
               eph ^= 1;
@@ -594,7 +629,7 @@ __global__ void __launch_bounds__(TcCfg<BNX, FMT, PAIR>::kThreads, 1)
       // no copy is in flight when the CTA exits (the leader's barriers count both CTAs')
       if (leader)
         for (int i = n > C::S ? n - C::S : 0; i < n; ++i)
-          wait(full(i % C::S), (i / C::S) & 1, W, kErrStage, false);
+          wait<0>(full(i % C::S), (i / C::S) & 1, W, kErrStage, false);
     }
   } else if (warp == 2) {
     // ---- copies of the units' codes and parameters: lanes 0, 1, 2 each issue one of a unit's
@@ -612,10 +647,11 @@ __global__ void __launch_bounds__(TcCfg<BNX, FMT, PAIR>::kThreads, 1)
       constexpr int kCopies = FMT == kLUT4 ? 2 : 3;
       while (ok && sg.next(P, tile, k0, k1, slot)) {
         const int rb = (tile / P.mtiles) * C::kCtas + (int)rank;
+#pragma unroll 1
         for (int k = k0; k < k1; ++k) {
           if (n >= C::SC) {
             if (n == C::SC) qlk::grid_dependency_wait();
-            if (!(ok = warp_wait(cempty(c), ph, W, kErrStage, lane))) break;
+            if (!(ok = warp_wait<C::kSpin>(cempty(c), ph, W, kErrStage, lane))) break;
           }
           const int b = BWD ? k : rb, g = BWD ? rb : k;
           if (rb < P.rblocks) {
@@ -639,7 +675,7 @@ __global__ void __launch_bounds__(TcCfg<BNX, FMT, PAIR>::kThreads, 1)
         }
       }
       for (int i = n > C::SC ? n - C::SC : 0; i < n; ++i)  // none in flight at the end
-        warp_wait(cfull(i % C::SF), (i / C::SF) & 1, W, kErrStage, lane, false);
+        warp_wait<0>(cfull(i % C::SF), (i / C::SF) & 1, W, kErrStage, lane, false);
     }
   } else if (warp == 1) {
     // ---- MMA issue (the leader of a pair).  The whole warp runs the loop, so that the
@@ -651,12 +687,13 @@ __global__ void __launch_bounds__(TcCfg<BNX, FMT, PAIR>::kThreads, 1)
       bool ok = true, ready = false;
       for (; ok && sg.next(P, tile, k0, k1, slot); ++j) {
         const int a = j & 1;
-        if (j >= 2 && !(ok = warp_wait(acce(a), ((j >> 1) - 1) & 1, W, kErrAcc, lane)))
+        if (j >= 2 && !(ok = warp_wait<0>(acce(a), ((j >> 1) - 1) & 1, W, kErrAcc, lane)))
           break;
         tc_fence_after();
         const uint32_t d = tmem + (uint32_t)(a * BNX);
+#pragma unroll 1
         for (int k = k0; k < k1; ++k) {
-          if (!ready && !(ok = warp_wait(full(s), ph, W, kErrStage, lane))) break;
+          if (!ready && !(ok = warp_wait<C::kSpin>(full(s), ph, W, kErrStage, lane))) break;
           tc_fence_after();
           const uint32_t st = (ring + s * C::kStageBytes) >> 4;
           const uint32_t pa = st | (BWD ? kDescLoMn : kDescLoK);
@@ -682,7 +719,7 @@ __global__ void __launch_bounds__(TcCfg<BNX, FMT, PAIR>::kThreads, 1)
       }
       if (elect_one()) tc_commit<PAIR>(fin);
       __syncwarp();
-      warp_wait(fin, 0, W, kErrAcc, lane, false);
+      warp_wait<0>(fin, 0, W, kErrAcc, lane, false);
     }
   } else if (warp >= C::kEpiWarp0) {
     const bool decoder = warp >= C::kDqWarp0;
@@ -692,45 +729,50 @@ __global__ void __launch_bounds__(TcCfg<BNX, FMT, PAIR>::kThreads, 1)
       // ---- decoding teams
       const int team = (warp - C::kDqWarp0) / kTeamWarps;
       const int dt = (warp - C::kDqWarp0) % kTeamWarps;
-      int n = 0, s = 0, e = 0, eph = 0, c = 0, f = 0, fph = 0;  // e: the barrier of stage n - S
+      // the team's stages n = team, team + 2, ...: slots n mod S and n mod SC, the barriers of
+      // codes n mod SF and of stage n - S
+      int s = team, c = team, f = team, fph = 0, e = (C::S ^ team) & 1, eph = 0;
+      int n0 = 0;  // stages before the segment
       for (; ok && sg.next(P, tile, k0, k1, slot); ++j) {
         const int rb = (tile / P.mtiles) * C::kCtas + (int)rank;
-        for (int k = k0; k < k1; ++k, ++n) {
-          if (n % kTeams == team) {
-            const int tb = rb < P.rblocks ? tiles_in_block(BWD ? k : rb, P.ntiles) : 0;
-            // decode into registers while the MMAs may still read the stage
-            if (!(ok = warp_wait(cfull(f), fph, W, kErrStage, lane))) break;
-            Decoded d;
-            if (dt < tb) {
-              decode_tile<C>(ring + C::kRingC + c * C::kSlot, dt, lane, lut, cempty(c),
-                             ring + C::kSpareOff + 4 * (warp - C::kDqWarp0), d);
-            } else {
-              if (lane == 0) qlk::mbar_arrive(cempty(c));
-              if (BWD) {  // rows past the last column are contracted: zeros
+        const int ftb = rb < P.rblocks ? (BWD ? kBlockTiles : tiles_in_block(rb, P.ntiles)) : 0;
+#pragma unroll 1
+        for (int k = k0 + ((n0 ^ team) & 1); k < k1; k += kTeams) {
+          // decode into registers while the MMAs may still read the stage
+          if (!(ok = warp_wait<C::kSpin>(cfull(f), fph, W, kErrStage, lane))) break;
+          const bool have = dt < (BWD && k == P.steps - 1 ? min(ftb, tiles_in_block(k, P.ntiles)) : ftb);
+          Decoded d;
+          if (have) {
+            decode_tile<C>(ring + C::kRingC + c * C::kSlot, dt, lane, lut, cempty(c),
+                           ring + C::kSpareOff + 4 * (warp - C::kDqWarp0), d);
+          } else {
+            if (lane == 0) qlk::mbar_arrive(cempty(c));
+            if (BWD) {  // rows past the last column are contracted: zeros
 #pragma unroll
-                for (int i = 0; i < 8; ++i) d.v[i >> 1][i & 1] = make_uint4(0, 0, 0, 0);
-              }
+              for (int i = 0; i < 8; ++i) d.v[i >> 1][i & 1] = make_uint4(0, 0, 0, 0);
             }
-            if (n >= C::S) {
-              if (n < C::S + kTeams) qlk::grid_dependency_wait();
-              if (!(ok = warp_wait(empty(e), eph, W, kErrStage, lane))) break;
+          }
+          const int n = n0 + k - k0;
+          if (n >= C::S) {
+            if (n < C::S + kTeams) qlk::grid_dependency_wait();
+            if (!(ok = warp_wait<C::kSpin>(empty(e), eph, W, kErrStage, lane))) break;
+            if ((e += kTeams) >= C::SE) {
+              e -= C::SE;
+              eph ^= 1;
             }
-            if (BWD || dt < tb) store_tile(ring + s * C::kStageBytes, dt, lane, d);
-            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // visible to the MMAs
-            __syncwarp();
-            if (lane == 0) arrive_lead(full(s));
           }
-          if (++s == C::S) s = 0;
-          if (n >= C::S && ++e == C::SE) {
-            e = 0;
-            eph ^= 1;
-          }
-          if (++c == C::SC) c = 0;
-          if (++f == C::SF) {
-            f = 0;
+          if (BWD || have) store_tile(ring + s * C::kStageBytes, dt, lane, d);
+          asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // visible to the MMAs
+          __syncwarp();
+          if (lane == 0) arrive_lead(full(s));
+          if ((s += kTeams) >= C::S) s -= C::S;
+          if ((c += kTeams) >= C::SC) c -= C::SC;
+          if ((f += kTeams) >= C::SF) {
+            f -= C::SF;
             fph ^= 1;
           }
         }
+        n0 += k1 - k0;
       }
       --j;
     }
@@ -749,8 +791,8 @@ __global__ void __launch_bounds__(TcCfg<BNX, FMT, PAIR>::kThreads, 1)
       const int a = j & 1;
       // the last accumulator has a barrier of its own, which completes once: the decoding warps
       // have not followed the phases of the others (all see it complete, or all time out)
-      if (!(last ? warp_wait(lastf, 0, W, kErrAcc, lane, false)
-                 : warp_wait(accf(a), (j >> 1) & 1, W, kErrAcc, lane)))
+      if (!(last ? warp_wait<0>(lastf, 0, W, kErrAcc, lane, false)
+                 : warp_wait<0>(accf(a), (j >> 1) & 1, W, kErrAcc, lane)))
         break;
       tc_fence_after();
       const int lrow = 32 * q + lane;
@@ -772,6 +814,7 @@ __global__ void __launch_bounds__(TcCfg<BNX, FMT, PAIR>::kThreads, 1)
         // part of a tile: partial sums [token / 4][row][token mod 4]; the last contributor of
         // the tile goes on, with the sums in place of the accumulator
         float* mine = P.partials + (size_t)(2 * blockIdx.x + slot) * 128 * P.bn + 4 * lrow;
+#pragma unroll 1
         for (int c0 = c_first; c0 < cols; c0 += step) {
           uint32_t r[8];
           __syncwarp();
@@ -799,13 +842,13 @@ __global__ void __launch_bounds__(TcCfg<BNX, FMT, PAIR>::kThreads, 1)
           // the members' sums are written, then one arrival for all of them
           if (lane == 0) qlk::mbar_arrive(tail);
           if (member == 0) {
-            if (!warp_wait(tail, 0, W, kErrAcc, lane, false)) break;
+            if (!warp_wait<0>(tail, 0, W, kErrAcc, lane, false)) break;
             if (lane == 0) {
               misc[2 + q] = qlk::arrive_acq_rel(counter);
               qlk::mbar_arrive(tail + 8);
             }
           }
-          if (!warp_wait(tail + 8, 0, W, kErrAcc, lane, false)) break;
+          if (!warp_wait<0>(tail + 8, 0, W, kErrAcc, lane, false)) break;
           prev = misc[2 + q];
         }
         if (prev + 1 != (uint32_t)(wl - wf + 1)) {
@@ -816,6 +859,7 @@ __global__ void __launch_bounds__(TcCfg<BNX, FMT, PAIR>::kThreads, 1)
       }
       uint32_t res[kTok / 2] = {};
       load_residual(P, res, m0 + c_first, cols - c_first, row, lane);
+#pragma unroll 1
       for (int c0 = c_first; c0 < cols; c0 += step) {
         uint32_t res_next[kTok / 2] = {};
         if (c0 + step < cols)
