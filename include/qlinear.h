@@ -464,8 +464,9 @@ ql_status qlinear_matmul(int fmt, const uint16_t* x, const void* packed, const v
  *   fp16 tensors   : 16-byte aligned; fp32 dbias 16-byte aligned
  * Asynchronous on `stream`; nothing is allocated.  An output may not overlap an input or
  * another output (QL_ERR_ALIAS), except that y may be exactly the residual.
- * Shapes: M >= 1, N (F) % 16 == 0, K % 128 == 0 (QL_ERR_SHAPE); format or act outside the
- * lists: QL_ERR_UNSUPPORTED.
+ * Shapes: 1 <= M <= 2^24, N (F) % 16 == 0, K % 128 == 0, K and N (2 F) up to 2^30
+ * (QL_ERR_SHAPE); format or act outside the lists: QL_ERR_UNSUPPORTED.  The weights must not
+ * be written by work still running on the stream (they are read before earlier kernels end).
  * ------------------------------------------------------------------------- */
 typedef enum {
   QL_ACT_NONE = 0,

@@ -40,7 +40,7 @@ def test_gated_packing_refusals():
         ql.qlinear_pack_gated(3, a, a, 32, 128)
     assert ql._lib.qlinear_pack_gated(4, None, P, P, 32, 128) == 1
     assert ql._lib.qlinear_pack_params_gated(4, P, None, P, 32, 128) == 1
-    assert ql._lib.qlinear_pack_gated(4, P, P, P, 0x40000000, 128) == 2
+    assert ql._lib.qlinear_pack_gated(4, P, P, P, (1 << 29) + 16, 128) == 2
 
 
 def _linear(fmt=4, x=P, w=P * 1000, p0=P * 2000, p1=P * 3000, bias=None, res=None, act=0,
@@ -81,8 +81,9 @@ def test_common_refusals(call):
     for K in (0, 64, 130, -128):
         assert call(K=K) == SHAPE
     width = "N" if call in (_linear, _linear_bwd) else "F"
-    for n in (0, 8, 24, -16):
+    for n in (0, 8, 24, -16, (1 << 30) + 16, 2 ** 31 - 16):
         assert call(**{width: n}) == SHAPE
+    assert call(K=(1 << 30) + 128) == SHAPE
     assert call(w=P * 1000 + 16) == ALIGN
     assert call(p0=P * 2000 + 2) == ALIGN and call(p1=P * 3000 + 8) == ALIGN
     assert call(fmt=16, p0=P * 2000 + 1) == ALIGN

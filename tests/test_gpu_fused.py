@@ -223,7 +223,7 @@ def test_feed_forward_block(M):
     y = mlp.forward(x, residual=x, gu=gu)
     xd = x.double().requires_grad_(True)
     want = (ref.act("silu", xd @ wg) * (xd @ wu)) @ wd + xd.detach()
-    assert float((y.double() - want).norm()) <= 3 * ref.REL * float(want.norm())
+    assert float((y.double() - want.detach()).norm()) <= 3 * ref.REL * float(want.detach().norm())
     grad = torch.autograd.grad(want, xd, dy.double())[0]
     dx = mlp.backward(dy, gu)
     assert float((dx.double() - grad).norm()) <= 3 * ref.REL * float(grad.norm())
@@ -462,3 +462,61 @@ def test_layer_refusals():
             l3 = layers.from_uniform(gen.uniform_layer(1, 384, 208, 4, group=64), DEV)
         with pytest.raises(ValueError):
             l3.linear(x)
+
+
+@pytest.mark.parametrize("M", [24, 64, 100, 200, 256, 520])
+@pytest.mark.parametrize("fmt", FMTS)
+def test_many_calls(fmt, M):
+    """Thirty calls, each with dozens of units per pipeline (every code ring goes round many
+    times, the decoding teams run apart), all bit-identical, in both directions, and right."""
+    K, N = 4096, 2320
+    lay, w = _linear(fmt, K, N, seed=50)
+    x, dy = _t(M, M, K), _t(M + 1, M, N, std=0.25)
+    y, dx = lay.linear(x), lay.linear_backward(dy)
+    ref.check(y, ref.linear(x.double(), w)[0], "y")
+    ref.check(dx, ref.linear_backward(dy.double(), None, w, "none")[0], "dx")
+    for _ in range(30):
+        assert torch.equal(lay.linear(x), y)
+        assert torch.equal(lay.linear_backward(dy), dx)
+    _clean(lay)
+
+
+@pytest.mark.parametrize("M", [1, 16, 64, 300])
+def test_two_calls_at_once(M):
+    """Two layers' calls on two streams, overlapping as the device sees fit."""
+    a, _, _ = _gated("w4", 2048, 592)
+    b, _ = _linear("w8", 1024, 512)
+    xa, xb = _t(1, M, 2048), _t(2, M, 1024)
+    dh, gu, dy, z = _t(3, M, 592), _t(4, M, 2, 592), _t(5, M, 512), _t(6, M, 512)
+
+    def call_a(**kw):
+        return a.forward(xa, **kw), a.backward(dh, gu, **kw)
+
+    def call_b(**kw):
+        return b.linear(xb, act="gelu", **kw), b.linear_backward(dy, z=z, act="gelu", **kw)
+
+    want = call_a() + call_b()
+    torch.cuda.synchronize()
+    s, t = torch.cuda.Stream(), torch.cuda.Stream()
+    got = [call_a(stream=s) + call_b(stream=t) for _ in range(20)]
+    torch.cuda.synchronize()
+    for g in got:
+        assert all(torch.equal(u, v) for u, v in zip(g, want))
+    _clean(a, b)
+
+
+def test_more_rows_than_reserved():
+    """Rows rise and fall; a policy table that changes the grid asks for a larger workspace."""
+    lay, w = _linear("w4", 1024, 512, seed=60)
+    for M in (1, 300, 8, 16, 700, 2):
+        x = _t(M, M, 1024)
+        ref.check(lay.linear(x), ref.linear(x.double(), w)[0], str(M))
+    fresh, _ = _linear("w4", 1024, 512, seed=61)
+    x = _t(1, 9, 1024)
+    want = fresh.linear(x)
+    ql.qlinear_policy_set([dict(fmt=4, N=512, K=1024, m_lo=1, m_hi=16, ctas=32)])
+    try:
+        assert torch.allclose(fresh.linear(x).float(), want.float(), rtol=2 ** -9, atol=2 ** -9)
+    finally:
+        ql.qlinear_policy_set([])
+    _clean(lay, fresh)

@@ -17,14 +17,15 @@ using namespace qlayout;
 
 namespace {
 
-constexpr int kMaxRows = 1 << 24;
+constexpr int kMaxRows = 1 << 24, kMaxColumns = 1 << 30;
 constexpr int kGemvRows = 16;  // the GEMV up to here, the tensor-core product above
 
 bool fmt_ok(int fmt) { return fmt == kW2 || fmt == kW4 || fmt == kW8 || fmt == kLUT4; }
 bool aligned(const void* p, size_t a) { return ((uintptr_t)p & (a - 1)) == 0; }
 bool shape_ok(int M, int N, int K) {
-  return M >= 1 && M <= kMaxRows && N >= kTileN && N <= 0x7FFFFFE0 && N % kTileN == 0 &&
-         K >= kGroup && K <= 0x7FFFFF80 && K % kGroup == 0 &&
+  // (the kernels count rows, columns and units in 32 bits)
+  return M >= 1 && M <= kMaxRows && N >= kTileN && N <= kMaxColumns && N % kTileN == 0 &&
+         K >= kGroup && K <= kMaxColumns && K % kGroup == 0 &&
          (long long)((N + 127) / 128) * (K / kGroup) < (1LL << 31);
 }
 
@@ -419,7 +420,7 @@ extern "C" ql_status qlinear_gated(int fmt, const uint16_t* x, const void* packe
                                    size_t workspace_bytes, ql_stream_t stream) {
   if (!fmt_ok(fmt) || !qact::act_ok(act)) return QL_ERR_UNSUPPORTED;
   if (!x || !h) return QL_ERR_NULL;
-  if (F < kTileN || F % kTileN || F > 0x3FFFFFF0 || !shape_ok(M, 2 * F, K)) return QL_ERR_SHAPE;
+  if (F < kTileN || F % kTileN || F > kMaxColumns / 2 || !shape_ok(M, 2 * F, K)) return QL_ERR_SHAPE;
   if (const ql_status s = check_weights(fmt, packed, p0, p1)) return s;
   if (!aligned(x, 16) || !aligned(h, 16) || !aligned(gu, 16) || !aligned(bias, 16))
     return QL_ERR_ALIGN;
@@ -484,7 +485,7 @@ extern "C" ql_status qlinear_gated_backward(int fmt, const uint16_t* dh, const u
                                             ql_stream_t stream) {
   if (!fmt_ok(fmt) || !qact::act_ok(act)) return QL_ERR_UNSUPPORTED;
   if (!dh || !gu || !dx) return QL_ERR_NULL;
-  if (F < kTileN || F % kTileN || F > 0x3FFFFFF0 || !shape_ok(M, 2 * F, K)) return QL_ERR_SHAPE;
+  if (F < kTileN || F % kTileN || F > kMaxColumns / 2 || !shape_ok(M, 2 * F, K)) return QL_ERR_SHAPE;
   if (const ql_status s = check_weights(fmt, packed, p0, p1)) return s;
   if (!aligned(dh, 16) || !aligned(gu, 16) || !aligned(dx, 16) || !aligned(dbias, 16))
     return QL_ERR_ALIGN;

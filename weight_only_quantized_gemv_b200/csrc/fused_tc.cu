@@ -1039,20 +1039,11 @@ Schedule schedule(int tiles, int steps, int W, int bn) {
     }
   }
   const float runs = steps * stage * R / W + bn / 7.f;
-#ifdef SCHEDENV
-  if (const char* e = getenv("SCHED")) {if (e[0]=='0') goto R_; else goto P_;}
-#endif
   if (runs < parts) {
-#ifdef SCHEDENV
-R_:
-#endif
     const int t = tiles < W ? tiles : R + W;  // shared out
     const long long units = (long long)t * steps;
     return Schedule{tiles - t, units < W ? (int)units : W};
   }
-#ifdef SCHEDENV
-P_:
-#endif
   return Schedule{tiles - R, R * f};
 }
 
@@ -1092,6 +1083,8 @@ ql_status launch_as(const qfused::Product& p, const Tokens& tk) {
   const Schedule sc = schedule(P.tiles, P.steps, maxw, tk.bn);
   P.whole = sc.whole;
   P.runners = sc.runners;
+  if ((size_t)(P.tiles - P.whole) * ctas * 4 * sizeof(uint32_t) > qfused::kTcCounterBytes)
+    return QL_ERR_UNSUPPORTED;  // more than five hundred SMs
   const int workers = P.whole > 0 ? maxw : P.runners;
   CUtensorMap xmap;
   if (!encode_rows(&xmap, p.x, p.M, BWD ? p.N : p.K, tk.bn / ctas)) return QL_ERR_CUDA;

@@ -38,7 +38,7 @@ inline uint32_t canonical_code(int fmt, const void* canon, int N, int k, int n) 
   return (uint32_t)(v >> sh) & ((1u << bits) - 1);
 }
 
-constexpr int kMaxGatedWidth = 0x3FFFFFF0;  // 2 F fits an int
+constexpr int kMaxGatedWidth = 1 << 29;  // 2 F at most 2^30, as in the fused layers
 
 // The matrix a packed column comes from: one canonical array of `width` columns, or (gated) two
 // whose 16-column tiles alternate, the gate's first.
