@@ -807,8 +807,7 @@ __global__ void __launch_bounds__(TcCfg<BNX, FMT, PAIR>::kThreads, 1)
                                                  (row & 15)
                                            : (size_t)row]);
       const bool whole = k0 == 0 && k1 == P.steps;
-      int wf = 0, wl = 0;
-      long long ub = 0;
+      int wf = 0, wl = 0, first_slot = 0;
       uint32_t* counter = nullptr;
       if (!whole) {
         // part of a tile: partial sums [token / 4][row][token mod 4]; the last contributor of
@@ -827,8 +826,9 @@ __global__ void __launch_bounds__(TcCfg<BNX, FMT, PAIR>::kThreads, 1)
         }
         tc_fence_before();
         __syncwarp();
-        ub = (long long)(tile - P.whole) * P.steps;
+        const long long ub = (long long)(tile - P.whole) * P.steps;
         wf = worker_of(ub, U, P.runners);
+        first_slot = run_begin(wf, U, P.runners) >= ub ? 0 : 1;
         wl = worker_of(ub + P.steps - 1, U, P.runners);
         counter = P.counters + ((size_t)(tile - P.whole) * C::kCtas + rank) * 4 + q;
         uint32_t prev = 0;
@@ -875,12 +875,13 @@ __global__ void __launch_bounds__(TcCfg<BNX, FMT, PAIR>::kThreads, 1)
         } else {
 #pragma unroll
           for (int e = 0; e < kTok; ++e) v[e] = 0.f;
+          // slot 0 of every contributor (their runs start in this tile), but slot 1 of one
+          // whose run started in an earlier tile
+          const float* src = P.partials + (size_t)(2 * (wf * C::kCtas + (int)rank) + first_slot) *
+                                              128 * P.bn + (size_t)c0 * 128 + 4 * lrow;
+          size_t hop = (size_t)(2 * C::kCtas - first_slot) * 128 * P.bn;
 #pragma unroll 4
           for (int w = wf; w <= wl; ++w) {
-            const int cta = w * C::kCtas + (int)rank;
-            const int sl = run_begin(w, U, P.runners) >= ub ? 0 : 1;
-            const float* src =
-                P.partials + (size_t)(2 * cta + sl) * 128 * P.bn + (size_t)c0 * 128 + 4 * lrow;
 #pragma unroll
             for (int e = 0; e < kTok; e += 4) {
               const float4 f = __ldcg(reinterpret_cast<const float4*>(src + (size_t)e * 128));
@@ -889,6 +890,8 @@ __global__ void __launch_bounds__(TcCfg<BNX, FMT, PAIR>::kThreads, 1)
               v[e + 2] += f.z;
               v[e + 3] += f.w;
             }
+            src += hop;
+            hop = (size_t)(2 * C::kCtas) * 128 * P.bn;
           }
         }
         if (E.gated)
@@ -1019,16 +1022,18 @@ Tokens token_tiles(int M) {
 //    read the same tokens at the same time; the parts of a tile are joined by twenty warps.
 //  * runs (stream-K): R tiles and one whole wave in W equal runs.  No worker idles, but each is
 //    at a depth of its own, and most sums are joined by four warps beside the next tile.
-// In us: a stage takes about max(0.3, bn / 465), joining one more part bn / 160 + 0.3, and runs
-// cost bn / 7 more than their stages (measured: 300 x 4096 x 4096 27 in parts, 59 in runs;
-// 512 x 28672 x 8192 with R = 2, f = 37 parts 375, runs 235; 96 x 28672 x 8192 equal).
+// In us: a stage takes about max(0.45, bn / 465), joining one more part bn / 160 + 0.3, and runs
+// cost more than their stages: bn / 14 + 1, and bn / 6.5 + 2 where there is no whole wave, since
+// the joins then all fall at the end.  Measured, tokens x columns x k, runs against parts:
+// 64 x 28672 x 8192 56 / 66, 96 x 28672 x 8192 62 / 71, 256 x 28672 x 8192 103 / 102,
+// 513 x 28672 x 4096 127 / 118, 64 x 12288 x 4096 27 / 20, 200 x 12288 x 4096 53 / 28.
 struct Schedule {
   int whole, runners;
 };
 Schedule schedule(int tiles, int steps, int W, int bn) {
   const int R = tiles % W;
   if (R == 0) return Schedule{tiles, 0};
-  const float stage = bn > 140 ? bn / 465.f : 0.3f, join = bn / 160.f + 0.3f;
+  const float stage = bn > 209 ? bn / 465.f : 0.45f, join = bn / 160.f + 0.3f;
   int f = 1;
   float parts = steps * stage;
   for (int g = 2; g <= W / R && g <= steps; ++g) {
@@ -1038,7 +1043,8 @@ Schedule schedule(int tiles, int steps, int W, int bn) {
       f = g;
     }
   }
-  const float runs = steps * stage * R / W + bn / 7.f;
+  const float runs =
+      steps * stage * R / W + (tiles < W ? bn / 6.5f + 2.f : bn / 14.f + 1.f);
   if (runs < parts) {
     const int t = tiles < W ? tiles : R + W;  // shared out
     const long long units = (long long)t * steps;
