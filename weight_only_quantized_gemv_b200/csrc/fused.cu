@@ -115,7 +115,7 @@ __device__ __forceinline__ void gated_gradients(int act, float (&dh)[8], const f
 }
 
 template <bool GATED>
-__global__ void __launch_bounds__(32 * kGradWarps) grad_kernel(const GradParams P) {
+__global__ void __launch_bounds__(32 * kGradWarps, GATED ? 3 : 4) grad_kernel(const GradParams P) {
   constexpr int NB = GATED ? 2 : 1;
   __shared__ float red[NB][kGradWarps][kGradCols];
   __shared__ uint32_t last;
