@@ -84,14 +84,15 @@ struct TcCfg {
   static constexpr int SF = kTeams * SC;
   static_assert(SC >= 2, "code ring");
   static constexpr int kRingC = S * kStageBytes;
-  static constexpr int kBarOff = kRingC + SC * kSlot;
+  static constexpr int kLutOff = kRingC + SC * kSlot;        // LUT4: the table, 64 bytes
+  static_assert(FMT != kLUT4 || kLutOff % 256 == 0, "table address");
+  static constexpr int kBarOff = kLutOff + (FMT == kLUT4 ? 64 : 0);
   // full[S] empty[SE] accf[2] acce[2] fin cfull[SF] cempty[SC] tail[4][2] last; then the tensor
-  // memory's base, the abort flag, arrivals before the last segment's per quadrant; the table
+  // memory's base, the abort flag, arrivals before the last segment's per quadrant
   static constexpr int kTailBar = S + SE + 5 + SF + SC;
   static constexpr int kLastBar = kTailBar + 8;
   static constexpr int kMiscOff = kBarOff + 8 * (kLastBar + 1);
-  static constexpr int kLutOff = kMiscOff + 24;
-  static constexpr int kSpareOff = kLutOff + 64;  // a word per decoding warp
+  static constexpr int kSpareOff = kMiscOff + 24;  // a word per decoding warp
   static constexpr int kSmem = kSpareOff + 4 * kTeams * kTeamWarps;
   static_assert(kSmem <= 232448, "shared memory");
   static constexpr int kSpin = BNX == 256 ? 64 : 0;          // polls before a suspended wait
@@ -270,11 +271,32 @@ __device__ __forceinline__ uint4 uniform8(const uint32_t* w, int h, const __half
   return make_uint4(o[0], o[1], o[2], o[3]);
 }
 
+// LUT4: eight weights fp16(fp32(lut[q]) * absmax) of a pair of steps for row half h (see
+// lut_pair8).  `table`: shared-memory address of the 16 entries in fp32, a multiple of 256, so
+// that a byte permute of the codes (times 4, by two shifts a word) makes the address of an entry.
+// Entries lie in different banks.  (Looked up by byte permutes in registers instead, with no
+// shared loads, it took 107 against 88 us: 64 x 28672 x 8192.)
+__device__ __forceinline__ uint4 lut8(uint32_t table, const uint32_t* w, int h, float a) {
+  uint32_t o[4];
+#pragma unroll
+  for (int ss = 0; ss < 2; ++ss) {
+    const uint32_t even = (w[ss] << 2) & 0x3C3C3C3Cu, odd = (w[ss] >> 2) & 0x3C3C3C3Cu;
+#pragma unroll
+    for (int dkp = 0; dkp < 2; ++dkp) {
+      const uint32_t byte = 0x7650u + h + 2 * dkp;
+      const float lo = __uint_as_float(qlk::lds32(__byte_perm(even, table, byte)));
+      const float hi = __uint_as_float(qlk::lds32(__byte_perm(odd, table, byte)));
+      o[2 * ss + dkp] = qdq::h2_as_u32(__floats2half2_rn(__fmul_rn(lo, a), __fmul_rn(hi, a)));
+    }
+  }
+  return make_uint4(o[0], o[1], o[2], o[3]);
+}
+
 // The code slot is handed back (`release`, `spare`: a shared word of the warp) as soon as every
 // lane holds its words.  The barrier arrival does not wait for shared loads in flight; the
 // store of a value made from all of them does, and the arrival comes after it.
 template <class C>
-__device__ __forceinline__ void decode_tile(uint32_t slot, int tile, int lane, const float* lut,
+__device__ __forceinline__ void decode_tile(uint32_t slot, int tile, int lane, uint32_t table,
                                             uint32_t release, uint32_t spare, Decoded& d) {
   constexpr int FMT = C::FMT;
   constexpr int KW = qlk::Fmt<FMT>::kWords, KP = KW / 4;  // words per lane, per step pair
@@ -325,9 +347,8 @@ __device__ __forceinline__ void decode_tile(uint32_t slot, int tile, int lane, c
     for (int i = 0; i < 4; ++i)
 #pragma unroll
       for (int h = 0; h < 2; ++h)
-        d.v[i][h] = qdq::lut_pair8(
-            w + KP * i, 0, h, lut,
-            __uint_as_float(i >= 2 ? (h ? am.w : am.z) : (h ? am.y : am.x)));
+        d.v[i][h] = lut8(table, w + KP * i, h,
+                         __uint_as_float(i >= 2 ? (h ? am.w : am.z) : (h ? am.y : am.x)));
   } else {
     const __half2 s2 = qdq::u32_as_h2(am.x), z2 = qdq::u32_as_h2(am.y);
     // z + 2^(10 - shift): exact in fp16 for integer zeros up to 1024
@@ -543,7 +564,6 @@ __global__ void __launch_bounds__(TcCfg<BNX, FMT, PAIR>::kThreads, 1)
   auto cempty = [&](int c) { return bars + 8 * (C::S + C::SE + 5 + C::SF + c); };
   const uint32_t lastf = bars + 8 * C::kLastBar;  // the worker's last accumulator is complete
   volatile uint32_t* misc = reinterpret_cast<volatile uint32_t*>(smem + C::kMiscOff);
-  float* lut = reinterpret_cast<float*>(smem + C::kLutOff);
   const WaitCtx W{ring + C::kMiscOff + 4, P.err};
   const int warp = __shfl_sync(0xffffffffu, (int)(threadIdx.x >> 5), 0);  // uniform
   const int lane = threadIdx.x & 31;
@@ -564,7 +584,8 @@ __global__ void __launch_bounds__(TcCfg<BNX, FMT, PAIR>::kThreads, 1)
   };
 
   if (FMT == kLUT4 && threadIdx.x < 16)
-    lut[threadIdx.x] = __half2float(static_cast<const __half*>(P.p0)[threadIdx.x]);
+    reinterpret_cast<float*>(smem + C::kLutOff)[threadIdx.x] =
+        __half2float(static_cast<const __half*>(P.p0)[threadIdx.x]);
   if (threadIdx.x == 0) {
     for (int s = 0; s < C::S; ++s) qlk::mbar_init(full(s), C::kFullCount);
     for (int e = 0; e < C::SE; ++e) qlk::mbar_init(empty(e), 1);
@@ -743,7 +764,7 @@ __global__ void __launch_bounds__(TcCfg<BNX, FMT, PAIR>::kThreads, 1)
           const bool have = dt < (BWD && k == P.steps - 1 ? min(ftb, tiles_in_block(k, P.ntiles)) : ftb);
           Decoded d;
           if (have) {
-            decode_tile<C>(ring + C::kRingC + c * C::kSlot, dt, lane, lut, cempty(c),
+            decode_tile<C>(ring + C::kRingC + c * C::kSlot, dt, lane, ring + C::kLutOff, cempty(c),
                            ring + C::kSpareOff + 4 * (warp - C::kDqWarp0), d);
           } else {
             if (lane == 0) qlk::mbar_arrive(cempty(c));
