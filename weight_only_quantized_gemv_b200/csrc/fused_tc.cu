@@ -16,10 +16,10 @@
 //    copies into a ring of their own, filled ahead by a producer warp.
 //  * x (dz) arrives by tensor copies, two 64-column boxes per stage.
 //
-// Roles of the 24 warps: 0 copies of x, 1 MMA issue and tensor memory, 2 copies of codes,
-// 4..7 epilogue, 8..23 two teams of eight decoding warps that take the stages in turn, so that
-// the latency of one unit's decoding (wait, shared loads, stores, proxy fence, arrival) is
-// hidden behind the other's.
+// Roles of the 24 or 28 warps: 0 copies of x, 1 MMA issue and tensor memory, 2 copies of codes,
+// then four or eight epilogue warps, and two teams of eight decoding warps that take the stages
+// in turn, so that the latency of one unit's decoding (wait, shared loads, stores, proxy fence,
+// arrival) is hidden behind the other's.
 //
 // PAIR: a cluster of two CTAs on two SMs computes 256 rows with tcgen05 cta_group::2; each CTA
 // decodes its own 128 rows and copies half of the tokens, which halves what the tokens cost
@@ -55,10 +55,14 @@ namespace {
 
 constexpr uint32_t kErrStage = 1u, kErrAcc = 2u;
 constexpr int kTeams = 2, kTeamWarps = 8;
-constexpr int kMembers = 1 + kTeams * kTeamWarps / 4;  // warps per quadrant in the last epilogue
 
-template <int BNX_, int FMT_, bool PAIR_>
+// EP: epilogue warps per quadrant of the accumulators.  Two where one would finish a tile later
+// than the MMAs the next (launch_fmt), one elsewhere, which leaves the decoding more registers
+// (32 x 18944 x 8192: 35.5 against 38.0 us).
+template <int BNX_, int FMT_, bool PAIR_, int EP>
 struct TcCfg {
+  static constexpr int kEpiPer = EP;
+  static constexpr int kMembers = kEpiPer + kTeams * kTeamWarps / 4;  // ... with the decoding warps
   static constexpr int BNX = BNX_, FMT = FMT_;     // most tokens per tile, format
   static constexpr bool PAIR = PAIR_;
   static constexpr int kCtas = PAIR ? 2 : 1;
@@ -96,12 +100,12 @@ struct TcCfg {
   static constexpr int kSmem = kSpareOff + 4 * kTeams * kTeamWarps;
   static_assert(kSmem <= 232448, "shared memory");
   static constexpr int kSpin = BNX == 256 ? 64 : 0;          // polls before a suspended wait
-  static constexpr int kEpiWarp0 = 4, kDqWarp0 = 8;
+  static constexpr int kEpiWarp0 = 4, kDqWarp0 = kEpiWarp0 + 4 * kEpiPer;
   static constexpr int kWarps = kDqWarp0 + kTeams * kTeamWarps;
   static constexpr int kThreads = 32 * kWarps;
   static constexpr uint32_t kTmemCols = 2 * BNX;
   static constexpr uint32_t kFullCount = 1 + kCtas * kTeamWarps;
-  static constexpr uint32_t kAccEmptyCount = kCtas * 4;
+  static constexpr uint32_t kAccEmptyCount = kCtas * 4 * kEpiPer;
 };
 
 struct TcParams {
@@ -499,6 +503,16 @@ constexpr uint32_t kDescHi = 64u | (1u << 14) | (2u << 29);
 constexpr uint32_t kDescLoK = 1u << 16, kDescLoMn = (128u * 128u / 16u) << 16;
 constexpr uint32_t kTransposeA = 1u << 15;  // instruction descriptor: A is MN-major
 
+// Split-sum arrival with a weight; the count before it.
+__device__ __forceinline__ uint32_t arrive_weight(uint32_t* counter, uint32_t weight) {
+  uint32_t old;
+  asm volatile("atom.add.acq_rel.gpu.global.u32 %0, [%1], %2;"
+               : "=r"(old)
+               : "l"(counter), "r"(weight)
+               : "memory");
+  return old;
+}
+
 // Arrive on a barrier of the pair's other CTA.  What the arrival stands for is already done:
 // the decoding warps' stores by their proxy fence, the epilogue's tensor memory loads by their
 // wait; so the default release at CTA scope does, where one at cluster scope takes about a
@@ -547,10 +561,10 @@ __device__ __forceinline__ void mma(uint32_t d, uint32_t alo, uint32_t blo, uint
         : "memory");
 }
 
-template <int BNX, int FMT, bool PAIR, bool BWD>
-__global__ void __launch_bounds__(TcCfg<BNX, FMT, PAIR>::kThreads, 1)
+template <int BNX, int FMT, bool PAIR, bool BWD, int EP>
+__global__ void __launch_bounds__(TcCfg<BNX, FMT, PAIR, EP>::kThreads, 1)
     fused_tc_kernel(const TcParams P, const __grid_constant__ CUtensorMap xmap) {
-  using C = TcCfg<BNX, FMT, PAIR>;
+  using C = TcCfg<BNX, FMT, PAIR, EP>;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   const uint32_t ring = qlk::smem_addr(smem_raw);  // 1024-byte aligned, as the swizzle wants
   uint8_t* smem = smem_raw;
@@ -598,7 +612,7 @@ __global__ void __launch_bounds__(TcCfg<BNX, FMT, PAIR>::kThreads, 1)
     qlk::mbar_init(fin, 1);
     qlk::mbar_init(lastf, 1);
     for (int i = 0; i < 4; ++i) {
-      qlk::mbar_init(bars + 8 * C::kTailBar + 16 * i, kMembers);
+      qlk::mbar_init(bars + 8 * C::kTailBar + 16 * i, C::kMembers);
       qlk::mbar_init(bars + 8 * C::kTailBar + 16 * i + 8, 1);
     }
     misc[1] = 0u;
@@ -798,11 +812,12 @@ __global__ void __launch_bounds__(TcCfg<BNX, FMT, PAIR>::kThreads, 1)
       --j;
     }
     // ---- epilogue: accumulator lanes 32 q .. 32 q + 31, the tokens in chunks of kTok.  The
-    // four epilogue warps take every segment but the worker's last, while the next one is
+    // epilogue warps take every segment but the worker's last, while the next one is
     // multiplied; nothing follows the last, so the decoding warps share its chunks.
     qlk::grid_dependency_wait();
     const int q = warp & 3;
-    const int member = decoder ? 1 + (warp - C::kDqWarp0) / 4 : 0;  // of the quadrant's
+    const int member =  // of the quadrant's
+        decoder ? C::kEpiPer + (warp - C::kDqWarp0) / 4 : (warp - C::kEpiWarp0) / 4;
     const uint32_t tail = bars + 8 * C::kTailBar + 16 * q;          // two barriers
     const long long U = (long long)(P.tiles - P.whole) * P.steps;
     const qfused::Epilogue& E = P.epi;
@@ -821,7 +836,7 @@ __global__ void __launch_bounds__(TcCfg<BNX, FMT, PAIR>::kThreads, 1)
       const int m0 = (tile % P.mtiles) * P.bn;
       const int cols = P.M - m0 < P.bn ? P.M - m0 : P.bn;
       const uint32_t tb = tmem + ((uint32_t)(32 * q) << 16) + (uint32_t)(a * BNX);
-      const int step = last ? kMembers * kTok : kTok, c_first = last ? member * kTok : 0;
+      int step = (last ? C::kMembers : C::kEpiPer) * kTok, c_first = member * kTok;
       float bias = 0.f;
       if (E.bias && row < P.rows)
         bias = __half2float(E.bias[E.gated ? (size_t)((row >> 4) & 1) * P.ld + (row >> 5) * 16 +
@@ -856,23 +871,26 @@ __global__ void __launch_bounds__(TcCfg<BNX, FMT, PAIR>::kThreads, 1)
         if (!last) {
           if (lane == 0) {
             arrive_lead(acce(a));
-            prev = qlk::arrive_acq_rel(counter);
+            prev = arrive_weight(counter, 1u);
           }
-          prev = __shfl_sync(0xffffffffu, prev, 0);
+          prev = __shfl_sync(0xffffffffu, prev, 0) + 1u;
+          c_first = 0;  // the last of a tile's warps joins all of its tokens
+          step = kTok;
         } else {
           // the members' sums are written, then one arrival for all of them
           if (lane == 0) qlk::mbar_arrive(tail);
           if (member == 0) {
             if (!warp_wait<0>(tail, 0, W, kErrAcc, lane, false)) break;
             if (lane == 0) {
-              misc[2 + q] = qlk::arrive_acq_rel(counter);
+              misc[2 + q] = arrive_weight(counter, C::kEpiPer);
               qlk::mbar_arrive(tail + 8);
             }
           }
           if (!warp_wait<0>(tail + 8, 0, W, kErrAcc, lane, false)) break;
-          prev = misc[2 + q];
+          prev = misc[2 + q] + C::kEpiPer;
         }
-        if (prev + 1 != (uint32_t)(wl - wf + 1)) {
+        // (every contributor counts kEpiPer: its warps one each, or all in one arrival)
+        if (prev != (uint32_t)(C::kEpiPer * (wl - wf + 1))) {
           if (last) break;
           continue;
         }
@@ -922,7 +940,7 @@ __global__ void __launch_bounds__(TcCfg<BNX, FMT, PAIR>::kThreads, 1)
 #pragma unroll
         for (int e = 0; e < kTok / 2; ++e) res[e] = res_next[e];
       }
-      if (!whole && lane == 0 && member == 0) *counter = 0u;  // ready for the next call
+      if (!whole && lane == 0 && (!last || member == 0)) *counter = 0u;  // ready for the next call
       if (last) break;
       if (whole) {
         tc_fence_before();
@@ -973,10 +991,10 @@ bool encode_rows(CUtensorMap* map, const void* base, int rows, int cols, int box
 constexpr int kMaxDevices = 64;
 
 // attr: two entries, the cluster first (the occupancy query takes that one alone)
-template <int BNX, int FMT, bool PAIR>
+template <int BNX, int FMT, bool PAIR, int EP>
 void launch_config(cudaLaunchConfig_t* cfg, cudaLaunchAttribute* attr, unsigned ctas,
                    cudaStream_t st) {
-  using C = TcCfg<BNX, FMT, PAIR>;
+  using C = TcCfg<BNX, FMT, PAIR, EP>;
   *cfg = cudaLaunchConfig_t{};
   cfg->gridDim = dim3(ctas);
   cfg->blockDim = dim3(C::kThreads);
@@ -997,20 +1015,20 @@ void launch_config(cudaLaunchConfig_t* cfg, cudaLaunchAttribute* attr, unsigned 
 }
 
 // Workers resident at once, once per instance and device.
-template <int BNX, int FMT, bool PAIR, bool BWD>
+template <int BNX, int FMT, bool PAIR, bool BWD, int EP>
 int resident_workers(int dev, int sms) {
-  using C = TcCfg<BNX, FMT, PAIR>;
+  using C = TcCfg<BNX, FMT, PAIR, EP>;
   static std::atomic<int> known[kMaxDevices];
   if (dev < 0 || dev >= kMaxDevices) return 0;
   int n = known[dev].load(std::memory_order_acquire);
   if (n > 0) return n;
-  auto fn = fused_tc_kernel<BNX, FMT, PAIR, BWD>;
+  auto fn = fused_tc_kernel<BNX, FMT, PAIR, BWD, EP>;
   if (cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem) != cudaSuccess)
     return 0;
   if constexpr (PAIR) {
     cudaLaunchConfig_t cfg;
     cudaLaunchAttribute attr[2];
-    launch_config<BNX, FMT, PAIR>(&cfg, attr, 2 * (sms / 2), nullptr);
+    launch_config<BNX, FMT, PAIR, EP>(&cfg, attr, 2 * (sms / 2), nullptr);
     cfg.numAttrs = 1;
     if (cudaOccupancyMaxActiveClusters(&n, fn, &cfg) != cudaSuccess) n = 0;
   } else {
@@ -1074,13 +1092,13 @@ Schedule schedule(int tiles, int steps, int W, int bn) {
   return Schedule{tiles - R, R * f};
 }
 
-template <int BNX, int FMT, bool PAIR, bool BWD>
+template <int BNX, int FMT, bool PAIR, bool BWD, int EP = 1>
 ql_status launch_as(const qfused::Product& p, const Tokens& tk) {
   int dev = 0, sms = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return QL_ERR_CUDA;
   if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
     return QL_ERR_CUDA;
-  const int maxw = resident_workers<BNX, FMT, PAIR, BWD>(dev, sms);
+  const int maxw = resident_workers<BNX, FMT, PAIR, BWD, EP>(dev, sms);
   if (maxw <= 0) return QL_ERR_CUDA;
   if (p.partial_bytes < (size_t)2 * sms * 128 * tk.bn * sizeof(float)) return QL_ERR_WORKSPACE;
   constexpr int ctas = PAIR ? 2 : 1;
@@ -1117,8 +1135,8 @@ ql_status launch_as(const qfused::Product& p, const Tokens& tk) {
   if (!encode_rows(&xmap, p.x, p.M, BWD ? p.N : p.K, tk.bn / ctas)) return QL_ERR_CUDA;
   cudaLaunchConfig_t cfg;
   cudaLaunchAttribute attr[2];
-  launch_config<BNX, FMT, PAIR>(&cfg, attr, (unsigned)(workers * ctas), p.stream);
-  if (cudaLaunchKernelEx(&cfg, fused_tc_kernel<BNX, FMT, PAIR, BWD>, P, xmap) != cudaSuccess)
+  launch_config<BNX, FMT, PAIR, EP>(&cfg, attr, (unsigned)(workers * ctas), p.stream);
+  if (cudaLaunchKernelEx(&cfg, fused_tc_kernel<BNX, FMT, PAIR, BWD, EP>, P, xmap) != cudaSuccess)
     return QL_ERR_CUDA;
   return QL_OK;
 }
@@ -1129,8 +1147,15 @@ ql_status launch_fmt(const qfused::Product& p) {
   if (!tk.pair)
     return tk.bn <= 32 ? launch_as<32, FMT, false, BWD>(p, tk)
                        : launch_as<64, FMT, false, BWD>(p, tk);
-  return tk.bn <= 128 ? launch_as<128, FMT, true, BWD>(p, tk)
-                      : launch_as<256, FMT, true, BWD>(p, tk);
+  if (tk.bn <= 128) return launch_as<128, FMT, true, BWD>(p, tk);
+  if constexpr (!BWD) {
+    // Per 256 tokens a stage takes about 1100 cycles, the epilogue of one warp per quadrant
+    // 48000, and 32000 more for each array beside the output: with two warps 2048 x 28672 x 8192
+    // with the pre-activation kept takes 785 against 1007 us, without it 800 against 763.
+    const int arrays = (p.epi.zsave != nullptr) + (p.epi.residual != nullptr);
+    if (p.K / kGroup < 44 + 30 * arrays) return launch_as<256, FMT, true, BWD, 2>(p, tk);
+  }
+  return launch_as<256, FMT, true, BWD>(p, tk);
 }
 
 }  // namespace
