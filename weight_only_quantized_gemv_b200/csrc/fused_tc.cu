@@ -1058,7 +1058,7 @@ Tokens token_tiles(int M) {
 // Whole waves of tiles, then the remaining R tiles over `runners` workers by stage, in one of
 // two ways:
 //  * parts: each of the R tiles in f equal parts, f <= W / R.  The workers stay in step and
-//    read the same tokens at the same time; the parts of a tile are joined by twenty warps.
+//    read the same tokens at the same time; the parts of a tile are joined by 20 or 24 warps.
 //  * runs (stream-K): R tiles and one whole wave in W equal runs.  No worker idles, but each is
 //    at a depth of its own, and most sums are joined by four warps beside the next tile.
 // In us: a stage takes about max(0.45, bn / 465), joining one more part bn / 160 + 0.3, and runs
