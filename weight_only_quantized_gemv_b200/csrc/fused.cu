@@ -68,8 +68,10 @@ __device__ __forceinline__ uint4 pack8(const float (&f)[8]) {
   return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
+// From L2: this grid may start before the one that writes the data has ended, and the
+// read-only path asks for data that nobody writes during the grid's whole life.
 __device__ __forceinline__ uint4 load8(const __half* p) {
-  return __ldg(reinterpret_cast<const uint4*>(p));
+  return __ldcg(reinterpret_cast<const uint4*>(p));
 }
 
 // d *= act'(z); the activation's branch outside the loop
