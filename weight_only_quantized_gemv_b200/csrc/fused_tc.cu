@@ -26,9 +26,18 @@
 // in shared memory and L2.
 //
 // Work: tiles of 128 (PAIR 256) rows x bn tokens.  Whole waves of tiles go round the
-// workers; the remaining tiles, at least one wave where there is one, are cut into equal
-// runs of stages (stream-K), whose partial sums meet in the workspace: the last contributor
+// workers; the remaining tiles are cut into equal parts, or with one whole wave into equal
+// runs of stages (schedule), whose partial sums meet in the workspace: the last contributor
 // to arrive adds them in worker order, nobody waits.
+//
+// Measured, W4: 8192 x 8192 with 512 tokens 54 us (1.27 PFLOP/s; the tensor pipe is busy for 76 %
+// of the cycles in which an SM has work), 8192 x 18944 with 32 tokens 37 us against 13 us for its
+// bytes (decoding: 56 % of the issue slots, the tensor pipe 35 %), 8192 x 28672 with 2048 tokens,
+// GELU, bias, residual and the pre-activation kept 843 us (1.14 PFLOP/s, at the power limit).
+//
+// The weights and, backward, dz are rounded to fp16 once: the operand type of kind::f16.  That adds
+// about one rounding each to the output's own (2.1e-4 in the relative L2 norm becomes 2.8e-4, with
+// two of them 3.3e-4 to 3.7e-4); keeping dz in two halves would double the MMAs.
 //
 // Every barrier wait is bounded in time (100 ms against microseconds); one that runs out sets
 // a flag in the workspace's error word, all roles leave their loops, and the CTA waits for its
@@ -515,8 +524,8 @@ __device__ __forceinline__ uint32_t arrive_weight(uint32_t* counter, uint32_t we
 
 // Arrive on a barrier of the pair's other CTA.  What the arrival stands for is already done:
 // the decoding warps' stores by their proxy fence, the epilogue's tensor memory loads by their
-// wait; so the default release at CTA scope does, where one at cluster scope takes about a
-// thousand cycles more.
+// wait; so the default scope does, where a release at cluster scope held the warp for about
+// 1200 cycles in a trace of the stages.
 __device__ __forceinline__ void arrive_remote(uint32_t bar) {
   asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
@@ -661,7 +670,16 @@ __global__ void __launch_bounds__(TcCfg<BNX, FMT, PAIR, EP>::kThreads, 1)
           if (++s == C::S) s = 0;
         }
       }
-      // no copy is in flight when the CTA exits (the leader's barriers count both CTAs')
+      // all stages are handed back (a pair's other CTA gets these arrivals from the leader: none
+      // may be on its way when it exits), and no copy is in flight (the leader's barriers count
+      // both CTAs')
+      for (int i = n > C::S ? n - C::S : 0; ok && i < n; ++i) {
+        ok = wait<0>(empty(e), eph, W, kErrStage);
+        if (++e == C::SE) {
+          e = 0;
+          eph ^= 1;
+        }
+      }
       if (leader)
         for (int i = n > C::S ? n - C::S : 0; i < n; ++i)
           wait<0>(full(i % C::S), (i / C::S) & 1, W, kErrStage, false);
