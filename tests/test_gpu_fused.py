@@ -520,3 +520,51 @@ def test_more_rows_than_reserved():
     finally:
         ql.qlinear_policy_set([])
     _clean(lay, fresh)
+
+
+def test_offsets_beyond_32_bits():
+    """Outputs, kept values and gradients of more than 2^31 elements, checked at both ends."""
+    K, N, M = 128, 65536, 33000
+    assert M * N > 2 ** 31
+    ends = [slice(0, 40), slice(M - 40, M)]
+    x = _t(1, M, K)
+    lay, w = _linear("w4", K, N)
+    z = torch.empty((M, N), dtype=torch.float16, device=DEV)
+    y = lay.linear(x, act="relu", z=z)
+    for r in ends:
+        wy, wz = ref.linear(x[r].double(), w, name="relu")
+        ref.check(y[r], wy, "y")
+        ref.check(z[r], wz, "z")
+    dx = lay.linear_backward(y, z=z, act="silu")
+    for r in ends:
+        ref.check(dx[r], ref.linear_backward(y[r].double(), z[r].double(), w, "silu")[0], "dx")
+    _clean(lay)
+    del y, z, dx
+    gat, wg, wu = _gated("w4", K, N // 2)
+    gu = torch.empty((M, 2, N // 2), dtype=torch.float16, device=DEV)
+    h = gat.forward(x, gu=gu)
+    for r in ends:
+        wh, wgu = ref.gated(x[r].double(), wg, wu)
+        ref.check(h[r], wh, "h")
+        ref.check(gu[r], wgu, "gu")
+    h.clamp_(-1, 1)  # as a gradient: its product with the gate and up values stays in fp16
+    dx = gat.backward(h, gu)
+    for r in ends:
+        want = ref.gated_backward(h[r].double(), gu[r].double(), wg, wu, "silu")[0]
+        ref.check(dx[r], want, "dx")
+    _clean(gat)
+    lay._fused_ws = gat._fused_ws = ()  # gigabytes
+
+
+def test_workspace_after_an_error_flag():
+    """A flag in the workspace is reported once, and arrivals that a call left are cleared."""
+    lay, _ = _linear("w4", 2048, 1168)
+    x = _t(1, 40, 2048)
+    want = lay.linear(x)
+    ws = lay.new_workspace(40)
+    words = ws.view(torch.int32)
+    words[0] = 1
+    words[64:96] = 1
+    assert lay.fused_read_error(ws) == 1
+    assert not ws.any() and lay.fused_read_error(ws) == 0
+    assert torch.equal(lay.linear(x, workspace=ws), want)

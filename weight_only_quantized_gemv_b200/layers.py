@@ -73,7 +73,9 @@ class _FusedWorkspace:
     them.  Calls of one layer run one after the other: an eager call on another stream than
     the last waits for that stream's work.  Work that overlaps in time - graphs captured from
     one layer and replayed at the same time - needs a workspace of its own:
-    ``workspace=layer.new_workspace(rows)``.  Tensors a call makes are made on its stream.
+    ``workspace=layer.new_workspace(rows)``.  Tensors a call makes are made on its stream.  A
+    stream given as a raw handle must live until the layer's next call on another stream, which
+    waits for it.
     """
 
     _fused_ws: tuple = ()    # buffers, the one in use last
@@ -169,13 +171,18 @@ class _FusedWorkspace:
 
     def fused_read_error(self, workspace=None, stream=None) -> int:
         """Sticky error flags of the calls that used the workspace (then cleared); 0 = every
-        device wait completed."""
+        device wait completed.  After a flag the workspace is zero-filled again: a call that
+        gave up leaves arrivals in its counters."""
         if workspace is None:
             if not self._fused_ws:
                 return 0
             workspace = self._fused_ws[-1]
         with torch.cuda.device(workspace.device):
-            return qlinear_read_error(workspace, stream)
+            flags = qlinear_read_error(workspace, stream)
+            if flags:
+                workspace.zero_()
+                torch.cuda.synchronize()
+            return flags
 
 
 class QuantLinear(_FusedWorkspace):
