@@ -37,7 +37,7 @@
 //
 // The weights and, backward, dz are rounded to fp16 once: the operand type of kind::f16.  That adds
 // about one rounding each to the output's own (2.1e-4 in the relative L2 norm becomes 2.8e-4, with
-// two of them 3.3e-4 to 3.7e-4); keeping dz in two halves would double the MMAs.
+// two of them 3.3e-4 to 4.2e-4); keeping dz in two halves would double the MMAs.
 //
 // Every barrier wait is bounded in time (100 ms against microseconds); one that runs out sets
 // a flag in the workspace's error word, all roles leave their loops, and the CTA waits for its
