@@ -199,3 +199,30 @@ def test_prefill_fused_full_size_sampled(tile_form):
     ref16 = oracle.dequant_uniform_fp16_nk(u.qweight[:, cols], u.scales[:, cols],
                                            u.zeros[:, cols], 4, 128)
     assert_parity(y[:, cols], oracle.prefill_matmul(x, ref16), what=f"fused {K}x{N} M={M}")
+
+
+@pytest.mark.parametrize("K", [128, 256, 640])
+def test_short_calls_back_to_back(K, tile_form):
+    """Calls whose pipelines hardly fill (fewer stages than the ring holds, a last pair without
+    rows for its second CTA), two hundred in a row without a wait in between: the CTAs of one
+    start on SMs that those of the last have just left."""
+    N, M = 1168, 130
+    lay, w16 = _layer("w4", K, N, 900)
+    x = torch.from_numpy(gen.activations(901, M, K)).to(DEV)
+    w = torch.empty((N, K), dtype=torch.float16, device=DEV)
+    lay.dequant_fp16(w)
+    want = lay.prefill(x, w_fp16=w).clone()
+    fused = lay.prefill_fused(x).clone()
+    torch.cuda.synchronize()
+    outs = [torch.empty_like(want) for _ in range(8)]
+    for i in range(200):
+        if i % 2:
+            lay.prefill_fused(x, outs[i % 8])
+        else:
+            lay.prefill(x, outs[i % 8], w_fp16=w)
+    torch.cuda.synchronize()
+    for i, o in enumerate(outs):
+        assert torch.equal(o, fused if i % 2 else want)
+    ref = x.double().cpu().numpy() @ w16.astype(np.float64).T
+    assert_parity(want.float().cpu().numpy(), ref, what=f"K={K}")
+    assert_parity(fused.float().cpu().numpy(), ref, what=f"fused K={K}")

@@ -426,13 +426,13 @@ __global__ void __launch_bounds__(TcCfg<BN, FUSED, FMT, PAIR>::kThreads, 1)
     *abort = 0u;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
+  // the peer's copies and arrivals reach the leader's barriers only once they are set up, and a
+  // pair's allocation takes columns of both SMs: both CTAs are running from here on
+  __syncwarp();
+  if constexpr (PAIR) cluster_sync();
   if (warp == 1) tmem_alloc<PAIR>(slot, C::kTmemCols);
   tc_fence_before();
-  // the peer's copies and arrivals reach the leader's barriers only once they are set up
-  if constexpr (PAIR)
-    cluster_sync();
-  else
-    __syncthreads();
+  __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(smem + C::kSlotOff);
 
@@ -464,6 +464,10 @@ __global__ void __launch_bounds__(TcCfg<BN, FUSED, FMT, PAIR>::kThreads, 1)
           }
         }
       }
+      // every stage is handed back: the leader's commits also arrive on the other CTA's
+      // barriers, and none of those arrivals may still be on its way when that CTA exits
+      for (int i = (it > C::S ? it - C::S : 0); i < it; ++i)
+        tc_wait(empty(i % C::S), (i / C::S) & 1, abort, kErrStage, kWaitNs / 10, false);
       // no copy of this CTA is still in flight when it exits: wait for the last stages filled
       // (the leader's full barriers count the bytes of both CTAs of a pair; the pair meets
       // at a cluster barrier before either exits)
