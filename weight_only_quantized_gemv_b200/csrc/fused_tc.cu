@@ -191,25 +191,34 @@ constexpr uint64_t kWaitNs = 100ull * 1000 * 1000;
 // Suspends the thread until the phase completes, or for up to kSuspendNs; whether it completed.
 // (Polling instead took as many issue slots as the decoding.)
 constexpr uint32_t kSuspendNs = 20000;
-__device__ __forceinline__ bool try_wait(uint32_t bar, uint32_t parity) {
+__device__ __forceinline__ bool try_wait(uint32_t bar, uint32_t parity, bool cluster) {
   uint32_t done;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
-      "selp.u32 %0, 1, 0, p;\n\t}"
-      : "=r"(done)
-      : "r"(bar), "r"(parity), "r"(kSuspendNs)
-      : "memory");
+  if (cluster)
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2, %3;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(done)
+        : "r"(bar), "r"(parity), "r"(kSuspendNs)
+        : "memory");
+  else
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(done)
+        : "r"(bar), "r"(parity), "r"(kSuspendNs)
+        : "memory");
   return done != 0;
 }
 
 // The phase has not completed within one suspension: keep waiting up to kWaitNs, or until
 // another role has given up; then set the flag.
 __device__ __noinline__ bool wait_slow(uint32_t bar, uint32_t parity, uint32_t abort, uint32_t* err,
-                                       uint32_t bit, bool honor_abort) {
+                                       uint32_t bit, bool honor_abort, bool cluster) {
   const uint64_t t0 = globaltimer_ns();
   for (;;) {
-    if (try_wait(bar, parity)) return true;
+    if (try_wait(bar, parity, cluster)) return true;
     if (honor_abort) {
       uint32_t a;
       asm volatile("ld.volatile.shared.u32 %0, [%1];" : "=r"(a) : "r"(abort) : "memory");
@@ -226,6 +235,7 @@ __device__ __noinline__ bool wait_slow(uint32_t bar, uint32_t parity, uint32_t a
 // waits between the pipeline's roles (SPIN > 0) poll SPIN times first where the MMAs set the pace
 // (256-token tiles: 190 against 290 us on 1024 x 4096 x 28672 backward) and suspend at once where
 // the decoding does (32 rows, 8192 x 18944: 35.1 against 37.6 us).
+// CLUSTER: some of the arrivals come from the pair's other CTA (acquire at cluster scope).
 
 // One thread.
 template <int SPIN>
@@ -234,19 +244,20 @@ __device__ __forceinline__ bool wait(uint32_t bar, uint32_t parity, const WaitCt
 #pragma unroll 1
   for (int i = 0; i < SPIN; ++i)
     if (mbar_ready(bar, parity, false)) return true;
-  return try_wait(bar, parity) || wait_slow(bar, parity, w.abort, w.err, bit, honor_abort);
+  return try_wait(bar, parity, false) ||
+         wait_slow(bar, parity, w.abort, w.err, bit, honor_abort, false);
 }
 
 // A whole warp: every lane sees the phase complete (the usual case), or one lane waits on.
-template <int SPIN>
+template <int SPIN, bool CLUSTER = false>
 __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, const WaitCtx& w,
                                           uint32_t bit, int lane, bool honor_abort = true) {
 #pragma unroll 1
   for (int i = 0; i < SPIN; ++i)
-    if (__all_sync(0xffffffffu, mbar_ready(bar, parity, false))) return true;
-  if (__all_sync(0xffffffffu, try_wait(bar, parity))) return true;
+    if (__all_sync(0xffffffffu, mbar_ready(bar, parity, CLUSTER))) return true;
+  if (__all_sync(0xffffffffu, try_wait(bar, parity, CLUSTER))) return true;
   bool ok = true;
-  if (lane == 0) ok = wait_slow(bar, parity, w.abort, w.err, bit, honor_abort);
+  if (lane == 0) ok = wait_slow(bar, parity, w.abort, w.err, bit, honor_abort, CLUSTER);
   return __shfl_sync(0xffffffffu, ok, 0);
 }
 
@@ -522,11 +533,15 @@ __device__ __forceinline__ uint32_t arrive_weight(uint32_t* counter, uint32_t we
   return old;
 }
 
-// Arrive on a barrier of the pair's other CTA.  What the arrival stands for is already done:
-// the decoding warps' stores by their proxy fence, the epilogue's tensor memory loads by their
-// wait; so the default scope does, where a release at cluster scope held the warp for about
-// 1200 cycles in a trace of the stages.
-__device__ __forceinline__ void arrive_remote(uint32_t bar) {
+// A stage of the pair's other CTA is complete: arrive on the leader's barrier.  The default scope
+// (the CTA) orders nothing between the two CTAs in the memory model, so this is what it rests on:
+// no thread of the leader reads what the arrival stands for.  A pair's MMA takes each half of
+// its operands from the shared memory of the SM that holds it, where the decoding warps' proxy
+// fence, complete before the arrival is issued, has made their stores visible to that SM's tensor
+// core; the arrival only says when.  (Copied tokens complete on the leader's barrier themselves.)
+// A release at cluster scope instead takes about 1900 cycles, longer than the ring of three stages
+// hides: 512 x 8192 x 8192 87 against 54 us, even when one warp passes a stage on for all.
+__device__ __forceinline__ void arrive_stage(uint32_t bar) {
   asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
 
@@ -597,7 +612,7 @@ __global__ void __launch_bounds__(TcCfg<BNX, FMT, PAIR, EP>::kThreads, 1)
   auto lead = [&](uint32_t b) { return (PAIR && !leader) ? cluster_addr(b, 0) : b; };
   auto arrive_lead = [&](uint32_t b) {
     if (PAIR && !leader)
-      arrive_remote(cluster_addr(b, 0));
+      mbar_arrive_remote(cluster_addr(b, 0));
     else
       qlk::mbar_arrive(b);
   };
@@ -740,20 +755,20 @@ __global__ void __launch_bounds__(TcCfg<BNX, FMT, PAIR, EP>::kThreads, 1)
       bool ok = true, ready = false;
       for (; ok && sg.next(P, tile, k0, k1, slot); ++j) {
         const int a = j & 1;
-        if (j >= 2 && !(ok = warp_wait<0>(acce(a), ((j >> 1) - 1) & 1, W, kErrAcc, lane)))
+        if (j >= 2 && !(ok = warp_wait<0, PAIR>(acce(a), ((j >> 1) - 1) & 1, W, kErrAcc, lane)))
           break;
         tc_fence_after();
         const uint32_t d = tmem + (uint32_t)(a * BNX);
 #pragma unroll 1
         for (int k = k0; k < k1; ++k) {
-          if (!ready && !(ok = warp_wait<C::kSpin>(full(s), ph, W, kErrStage, lane))) break;
+          if (!ready && !(ok = warp_wait<C::kSpin, PAIR>(full(s), ph, W, kErrStage, lane))) break;
           tc_fence_after();
           const uint32_t st = (ring + s * C::kStageBytes) >> 4;
           const uint32_t pa = st | (BWD ? kDescLoMn : kDescLoK);
           const uint32_t pb = (st + (C::kABytes >> 4)) | kDescLoK;
           const int s1 = s + 1 == C::S ? 0 : s + 1, ph1 = s + 1 == C::S ? ph ^ 1 : ph;
           // the next stage's barrier is looked at while this stage's MMAs are issued
-          const bool next_ready = mbar_ready(full(s1), ph1, false);
+          const bool next_ready = mbar_ready(full(s1), ph1, PAIR);
           if (elect_one()) {
 #pragma unroll
             for (int kk = 0; kk < 8; ++kk)
@@ -817,7 +832,12 @@ __global__ void __launch_bounds__(TcCfg<BNX, FMT, PAIR, EP>::kThreads, 1)
           if (BWD || have) store_tile(ring + s * C::kStageBytes, dt, lane, d);
           asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // visible to the MMAs
           __syncwarp();
-          if (lane == 0) arrive_lead(full(s));
+          if (lane == 0) {
+            if (PAIR && !leader)
+              arrive_stage(lead(full(s)));
+            else
+              qlk::mbar_arrive(full(s));
+          }
           if ((s += kTeams) >= C::S) s -= C::S;
           if ((c += kTeams) >= C::SC) c -= C::SC;
           if ((f += kTeams) >= C::SF) {
