@@ -58,6 +58,13 @@ inline size_t partial_offset(int N) { return kVecCounterOffset + vec_counter_byt
 ql_status launch_tc(const Product& p);
 size_t tc_partial_bytes(int M);  // bound over every call with at most M rows
 
+// Limit of a barrier wait of the tensor-core products and the delays of qlinear_debug_wait_test:
+// worker 0's copies of the activations (low half) and its first MMA (high half).
+struct WaitTest {
+  uint32_t limit_us, delays;
+};
+WaitTest wait_test();
+
 // GEMV with an epilogue (qlinear.cu), M <= 16
 ql_status launch_gemv(const Product& p);
 size_t gemv_partial_bytes(int fmt, int M, int N, int K, bool gated);  // 0: no plan

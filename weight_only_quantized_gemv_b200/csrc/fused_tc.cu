@@ -39,9 +39,10 @@
 // about one rounding each to the output's own (2.1e-4 in the relative L2 norm becomes 2.8e-4, with
 // two of them 3.3e-4 to 4.2e-4); keeping dz in two halves would double the MMAs.
 //
-// Every barrier wait is bounded in time (100 ms against microseconds); one that runs out sets
-// a flag in the workspace's error word, all roles leave their loops, and the CTA waits for its
-// own copies and MMAs, frees its tensor memory and exits.
+// Every barrier wait is bounded in time (100 ms against microseconds; qlinear_debug_wait_test
+// sets another limit); one that runs out sets a flag in the workspace's error word, all roles
+// leave their loops, and the CTA waits for its own copies and MMAs, frees its tensor memory and
+// exits.
 #include <cuda.h>
 #include <cudaTypedefs.h>
 #include <cuda_fp16.h>
@@ -132,6 +133,8 @@ struct TcParams {
   int steps;     // units per tile: groups (forward) or blocks (backward)
   int bn, mtiles, tiles, whole;  // tokens per tile; tiles [0, whole) are not split
   int runners;                   // workers that share the stages of tiles [whole, tiles)
+  uint32_t wait_us;              // limit of a wait
+  uint32_t test_us;              // tests of the waits: delays (qfused::WaitTest)
 };
 
 __device__ __forceinline__ long long run_begin(int w, long long U, int W) { return w * U / W; }
@@ -185,8 +188,8 @@ struct Segments {
 struct WaitCtx {
   uint32_t abort;  // shared-memory address of the CTA's abort flag
   uint32_t* err;   // global memory
+  uint32_t limit_us;
 };
-constexpr uint64_t kWaitNs = 100ull * 1000 * 1000;
 
 // Suspends the thread until the phase completes, or for up to kSuspendNs; whether it completed.
 // (Polling instead took as many issue slots as the decoding.)
@@ -212,10 +215,11 @@ __device__ __forceinline__ bool try_wait(uint32_t bar, uint32_t parity, bool clu
   return done != 0;
 }
 
-// The phase has not completed within one suspension: keep waiting up to kWaitNs, or until
+// The phase has not completed within one suspension: keep waiting up to the limit, or until
 // another role has given up; then set the flag.
 __device__ __noinline__ bool wait_slow(uint32_t bar, uint32_t parity, uint32_t abort, uint32_t* err,
-                                       uint32_t bit, bool honor_abort, bool cluster) {
+                                       uint32_t limit_us, uint32_t bit, bool honor_abort,
+                                       bool cluster) {
   const uint64_t t0 = globaltimer_ns();
   for (;;) {
     if (try_wait(bar, parity, cluster)) return true;
@@ -224,7 +228,7 @@ __device__ __noinline__ bool wait_slow(uint32_t bar, uint32_t parity, uint32_t a
       asm volatile("ld.volatile.shared.u32 %0, [%1];" : "=r"(a) : "r"(abort) : "memory");
       if (a) break;
     }
-    if (globaltimer_ns() - t0 > kWaitNs) break;
+    if (globaltimer_ns() - t0 > 1000ull * limit_us) break;
   }
   atomicOr(err, bit);
   asm volatile("st.volatile.shared.u32 [%0], %1;" ::"r"(abort), "r"(1u) : "memory");
@@ -245,7 +249,7 @@ __device__ __forceinline__ bool wait(uint32_t bar, uint32_t parity, const WaitCt
   for (int i = 0; i < SPIN; ++i)
     if (mbar_ready(bar, parity, false)) return true;
   return try_wait(bar, parity, false) ||
-         wait_slow(bar, parity, w.abort, w.err, bit, honor_abort, false);
+         wait_slow(bar, parity, w.abort, w.err, w.limit_us, bit, honor_abort, false);
 }
 
 // A whole warp: every lane sees the phase complete (the usual case), or one lane waits on.
@@ -257,9 +261,14 @@ __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, const W
     if (__all_sync(0xffffffffu, mbar_ready(bar, parity, CLUSTER))) return true;
   if (__all_sync(0xffffffffu, try_wait(bar, parity, CLUSTER))) return true;
   bool ok = true;
-  if (lane == 0) ok = wait_slow(bar, parity, w.abort, w.err, bit, honor_abort, CLUSTER);
+  if (lane == 0)
+    ok = wait_slow(bar, parity, w.abort, w.err, w.limit_us, bit, honor_abort, CLUSTER);
   return __shfl_sync(0xffffffffu, ok, 0);
 }
+
+// A role that gave up: what it has sent to the pair's other CTA, or has that CTA's barriers count,
+// arrives long before this ends (nothing is left to wait on).
+constexpr uint32_t kSettleUs = 20000;
 
 // ---------------------------------------------------------------------------
 // decoding: one warp, one 16-column tile of a unit, into rows 16 tile .. 16 tile + 15 of the
@@ -602,7 +611,7 @@ __global__ void __launch_bounds__(TcCfg<BNX, FMT, PAIR, EP>::kThreads, 1)
   auto cempty = [&](int c) { return bars + 8 * (C::S + C::SE + 5 + C::SF + c); };
   const uint32_t lastf = bars + 8 * C::kLastBar;  // the worker's last accumulator is complete
   volatile uint32_t* misc = reinterpret_cast<volatile uint32_t*>(smem + C::kMiscOff);
-  const WaitCtx W{ring + C::kMiscOff + 4, P.err};
+  const WaitCtx W{ring + C::kMiscOff + 4, P.err, P.wait_us};
   const int warp = __shfl_sync(0xffffffffu, (int)(threadIdx.x >> 5), 0);  // uniform
   const int lane = threadIdx.x & 31;
   const uint32_t rank = PAIR ? blockIdx.x & 1u : 0u;  // of the cluster (2, 1, 1)
@@ -661,6 +670,7 @@ __global__ void __launch_bounds__(TcCfg<BNX, FMT, PAIR, EP>::kThreads, 1)
       int s = 0, n = 0, e = 0, eph = 0;  // e: the barrier of stage n - S
       bool ok = true;
       const uint32_t bytes = (uint32_t)P.bn * 256u;  // both CTAs, both boxes
+      if ((P.test_us & 0xFFFFu) && wk == 0) qlk::test_delay(P.test_us & 0xFFFFu);
       while (ok && sg.next(P, tile, k0, k1, slot)) {
         const int m = (tile % P.mtiles) * P.bn + (int)rank * (P.bn / C::kCtas);
 #pragma unroll 1
@@ -698,6 +708,7 @@ __global__ void __launch_bounds__(TcCfg<BNX, FMT, PAIR, EP>::kThreads, 1)
       if (leader)
         for (int i = n > C::S ? n - C::S : 0; i < n; ++i)
           wait<0>(full(i % C::S), (i / C::S) & 1, W, kErrStage, false);
+      if (PAIR && !ok) qlk::test_delay(kSettleUs);
     }
   } else if (warp == 2) {
     // ---- copies of the units' codes and parameters: lanes 0, 1, 2 each issue one of a unit's
@@ -751,6 +762,7 @@ __global__ void __launch_bounds__(TcCfg<BNX, FMT, PAIR, EP>::kThreads, 1)
     if (leader) {
       qlk::grid_dependency_wait();
       const uint32_t idesc = idesc_f16(128 * C::kCtas, P.bn) | (BWD ? kTransposeA : 0u);
+      if ((P.test_us >> 16) && wk == 0) qlk::test_delay(P.test_us >> 16);
       int s = 0, ph = 0, e = 0, j = 0;
       bool ok = true, ready = false;
       for (; ok && sg.next(P, tile, k0, k1, slot); ++j) {
@@ -788,6 +800,7 @@ __global__ void __launch_bounds__(TcCfg<BNX, FMT, PAIR, EP>::kThreads, 1)
       if (elect_one()) tc_commit<PAIR>(fin);
       __syncwarp();
       warp_wait<0>(fin, 0, W, kErrAcc, lane, false);
+      if (PAIR && (!ok || misc[1])) qlk::test_delay(kSettleUs);
     }
   } else if (warp >= C::kEpiWarp0) {
     const bool decoder = warp >= C::kDqWarp0;
@@ -1166,6 +1179,9 @@ ql_status launch_as(const qfused::Product& p, const Tokens& tk) {
   const Schedule sc = schedule(P.tiles, P.steps, maxw, tk.bn);
   P.whole = sc.whole;
   P.runners = sc.runners;
+  const qfused::WaitTest wt = qfused::wait_test();
+  P.wait_us = wt.limit_us;
+  P.test_us = wt.delays;
   if ((size_t)(P.tiles - P.whole) * ctas * 4 * sizeof(uint32_t) > qfused::kTcCounterBytes)
     return QL_ERR_UNSUPPORTED;  // more than five hundred SMs
   const int workers = P.whole > 0 ? maxw : P.runners;

@@ -60,19 +60,24 @@ KernelInfo kernel_info() {
 
 // Instances with the test hooks of the bounded waits (same shared memory and threads as the
 // instance they stand in for): W4 with one row of x (three and two CTAs per SM) and W4 at
-// M = 9..16.  Other kernels run without the hooks.
-bool test_kernel(int fmt, int MT, bool outl, int wpu, bool m1, bool occ2, int ns, KernelInfo* k) {
-  if (fmt != kW4 || outl || ns != 1) return false;
+// M = 9..16, without an epilogue and with the linear one.  Other kernels run without the hooks.
+template <int EPI>
+bool test_kernel_epi(int MT, int wpu, bool m1, bool occ2, KernelInfo* k) {
   if (MT == 2) {
-    *k = kernel_info<kW4, 2, false, 2, false, 0, 1, true>();
+    *k = kernel_info<kW4, 2, false, 2, false, 0, 1, true, EPI>();
     return true;
   }
   if (m1 && wpu == 1) {
-    *k = occ2 ? kernel_info<kW4, 1, false, 1, true, 2, 1, true>()
-              : kernel_info<kW4, 1, false, 1, true, 0, 1, true>();
+    *k = occ2 ? kernel_info<kW4, 1, false, 1, true, 2, 1, true, EPI>()
+              : kernel_info<kW4, 1, false, 1, true, 0, 1, true, EPI>();
     return true;
   }
   return false;
+}
+bool test_kernel(int fmt, int MT, bool outl, int wpu, bool m1, bool occ2, int ns, int epi,
+                 KernelInfo* k) {
+  if (fmt != kW4 || outl || ns != 1 || epi == 2) return false;
+  return epi ? test_kernel_epi<1>(MT, wpu, m1, occ2, k) : test_kernel_epi<0>(MT, wpu, m1, occ2, k);
 }
 
 // Finer quantization groups (NS sub-groups per 128-k unit): two warps per unit for every
@@ -411,11 +416,11 @@ ql_status enqueue(const Call& c, const Plan& p, uint32_t* err, uint32_t* counter
   P.wait_limit = g_wait_limit.load(std::memory_order_relaxed);
   P.test_us = g_test_us.load(std::memory_order_relaxed);
   if (epi) P.epi = *epi;
-  KernelInfo k = pick_kernel(c.fmt, p.MT, c.outl, p.WPU, p.M1, p.OCC2, p.NS,
-                             !epi ? 0 : epi->gated ? 2 : 1);
-  if (!epi && (P.wait_limit != qlk::kSpinLimit || P.test_us != 0)) {  // qlinear_debug_wait_test is active
+  const int form = !epi ? 0 : epi->gated ? 2 : 1;
+  KernelInfo k = pick_kernel(c.fmt, p.MT, c.outl, p.WPU, p.M1, p.OCC2, p.NS, form);
+  if (P.wait_limit != qlk::kSpinLimit || P.test_us != 0) {  // qlinear_debug_wait_test is active
     KernelInfo kt;
-    if (test_kernel(c.fmt, p.MT, c.outl, p.WPU, p.M1, p.OCC2, p.NS, &kt)) {
+    if (test_kernel(c.fmt, p.MT, c.outl, p.WPU, p.M1, p.OCC2, p.NS, form, &kt)) {
       int dev = 0, occ = 0;
       if (cudaGetDevice(&dev) != cudaSuccess || prepare_kernel(kt, dev, &occ) != cudaSuccess)
         return QL_ERR_CUDA;
@@ -566,6 +571,12 @@ ql_status launch_debug(int fmt, const void* packed, const void* p0, const void* 
 
 // ---------------------------------------------------------------------------
 // the GEMV with an epilogue (entries in fused.cu, which checks the arguments)
+
+qfused::WaitTest qfused::wait_test() {
+  const uint32_t limit = g_wait_limit.load(std::memory_order_relaxed);
+  return WaitTest{limit == qlk::kSpinLimit ? 100000u : limit,
+                  g_test_us.load(std::memory_order_relaxed)};
+}
 
 size_t qfused::gemv_partial_bytes(int fmt, int M, int N, int K, bool gated) {
   Plan p;
