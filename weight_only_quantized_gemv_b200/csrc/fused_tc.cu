@@ -548,8 +548,9 @@ __device__ __forceinline__ uint32_t arrive_weight(uint32_t* counter, uint32_t we
 // its operands from the shared memory of the SM that holds it, where the decoding warps' proxy
 // fence, complete before the arrival is issued, has made their stores visible to that SM's tensor
 // core; the arrival only says when.  (Copied tokens complete on the leader's barrier themselves.)
-// A release at cluster scope instead takes about 1900 cycles, longer than the ring of three stages
-// hides: 512 x 8192 x 8192 87 against 54 us, even when one warp passes a stage on for all.
+// A release at cluster scope takes longer than the ring of three stages hides, even when a warp of
+// its own passes a stage on for all eight: 512 x 8192 x 8192 78 against 60 us (at the default scope
+// that way 61), 2048 x 28672 x 8192 1010 against 750, timed in turn.
 __device__ __forceinline__ void arrive_stage(uint32_t bar) {
   asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
