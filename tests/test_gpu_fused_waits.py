@@ -75,3 +75,31 @@ def test_gemv_with_epilogue_reports_a_late_copy(M):
     ql.qlinear_debug_wait_test()
     assert torch.equal(lay.linear(x, residual=res, act="silu"), want)
     assert lay.fused_read_error() == 0
+
+
+@pytest.mark.parametrize("fmt,M", [("w4", 200), ("w8", 200), ("w8", 60), ("w8", 100), ("lut4", 300)])
+@pytest.mark.parametrize("backward", [False, True])
+def test_no_flag_behind_a_long_kernel(fmt, M, backward):
+    """A call that starts early, on SMs that the kernel before it leaves idle, waits for that
+    kernel as long as it takes: the limit of its own waits begins after it."""
+    import weight_only_quantized_gemv_b200 as ql
+    from weight_only_quantized_gemv_b200 import layers
+    K, N = 2048, 2320
+    if fmt == "lut4":
+        lay = layers.from_lut4(gen.lut4_layer(72, K, N), DEV)
+    else:
+        lay = layers.from_uniform(gen.uniform_layer(72, K, N, int(fmt[1:])), DEV)
+    small = _layer(73, 128, 16)
+    x, xs = _t(4, M, N if backward else K), _t(5, 20, 128)
+    call = lay.linear_backward if backward else lay.linear
+    want, first = call(x), small.linear(xs)
+    for one in (lay, small):
+        assert one.fused_read_error() == 0
+    ql.qlinear_debug_wait_test(1000000, 60000, 0)  # one CTA, for 60 ms
+    out = small.linear(xs)
+    ql.qlinear_debug_wait_test(5000, 0, 0)
+    got = call(x)
+    torch.cuda.synchronize()
+    assert torch.equal(out, first) and torch.equal(got, want)
+    for one in (lay, small):
+        assert one.fused_read_error() == 0

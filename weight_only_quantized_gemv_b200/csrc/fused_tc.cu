@@ -820,6 +820,11 @@ __global__ void __launch_bounds__(TcCfg<BNX, FMT, PAIR, EP>::kThreads, 1)
         const int ftb = rb < P.rblocks ? (BWD ? kBlockTiles : tiles_in_block(rb, P.ntiles)) : 0;
 #pragma unroll 1
         for (int k = k0 + ((n0 ^ team) & 1); k < k1; k += kTeams) {
+          const int n = n0 + k - k0;
+          // Codes beyond the first SC units, and stages handed back, come once the kernels before
+          // this one have ended: no limited wait for them may start earlier.
+          constexpr int kFree = C::SC < C::S ? C::SC : C::S;
+          if (n >= kFree && n < kFree + kTeams) qlk::grid_dependency_wait();
           // decode into registers while the MMAs may still read the stage
           if (!(ok = warp_wait<C::kSpin>(cfull(f), fph, W, kErrStage, lane))) break;
           const bool have = dt < (BWD && k == P.steps - 1 ? min(ftb, tiles_in_block(k, P.ntiles)) : ftb);
@@ -834,9 +839,7 @@ __global__ void __launch_bounds__(TcCfg<BNX, FMT, PAIR, EP>::kThreads, 1)
               for (int i = 0; i < 8; ++i) d.v[i >> 1][i & 1] = make_uint4(0, 0, 0, 0);
             }
           }
-          const int n = n0 + k - k0;
           if (n >= C::S) {
-            if (n < C::S + kTeams) qlk::grid_dependency_wait();
             if (!(ok = warp_wait<C::kSpin>(empty(e), eph, W, kErrStage, lane))) break;
             if ((e += kTeams) >= C::SE) {
               e -= C::SE;
