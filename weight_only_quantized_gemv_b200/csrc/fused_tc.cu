@@ -152,7 +152,7 @@ struct Segments {
     W = W_;
     t = w;
     const long long U = (long long)(P.tiles - P.whole) * P.steps;
-    const long long u = run_begin(w, U, P.runners);
+    const long long u = w < P.runners ? run_begin(w, U, P.runners) : 0;  // (no runners: 0 tiles)
     left = w < P.runners ? (int)(run_begin(w + 1, U, P.runners) - u) : 0;
     rt = P.whole + (int)(u / P.steps);
     rk = (int)(u % P.steps);
