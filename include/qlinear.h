@@ -174,8 +174,8 @@ ql_status qlinear_read_error(void* workspace, uint32_t* flags, ql_stream_t strea
  * results.  While a setting is active, the W4 kernels for M = 1 and M = 9..16 (without an
  * epilogue, or with qlinear_linear's) run as instances compiled with these hooks (the other
  * GEMV kernels keep their fixed 2^22-round limit and no hooks).  The tensor-core products of
- * the fused layers read wait_limit as microseconds (0: 100000), after which a call sets the
- * same flags (2 also for an accumulator), gives up and leaves its outputs undefined; their
+ * the fused layers read wait_limit as microseconds (0: 100000; each of a tile's 128-wide
+ * stages adds 4), after which a call sets the same flags (2 also for an accumulator), gives up and leaves its outputs undefined; their
  * first worker's copies of the activations come late by producer_delay_us, its first MMA by
  * consumer_hold_us.  Not thread-safe with respect to concurrent calls' settings. */
 ql_status qlinear_debug_wait_test(uint32_t wait_limit, uint32_t producer_delay_us,

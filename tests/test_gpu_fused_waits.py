@@ -103,3 +103,24 @@ def test_no_flag_behind_a_long_kernel(fmt, M, backward):
     assert torch.equal(out, first) and torch.equal(got, want)
     for one in (lay, small):
         assert one.fused_read_error() == 0
+
+
+def test_limit_grows_with_the_tile():
+    """The epilogue waits for a whole tile: 1024 units of about 0.45 us against a limit of 1 us
+    and 4 us a unit.  (148 tiles of 128 columns: every worker has one, and none is shared.)"""
+    import weight_only_quantized_gemv_b200 as ql
+    from weight_only_quantized_gemv_b200 import layers
+    K, N, M = 131072, 18944, 20
+    q = torch.randint(0, 256, (K * N // 4,), dtype=torch.uint8, device=DEV)
+    p0 = torch.full((K // 128 * N,), 2.0 ** -10, dtype=torch.float16, device=DEV)
+    p1 = torch.ones(K // 128 * N, dtype=torch.float16, device=DEV)
+    x, y = _t(6, M, K), torch.empty((M, N), dtype=torch.float16, device=DEV)
+    ws = torch.zeros(ql.qlinear_fused_workspace_bytes(2, M, N, K, False), dtype=torch.uint8,
+                     device=DEV)
+    ql.qlinear_linear(2, x, q, p0, p1, y, M, N, K, ws)
+    want = y.clone()
+    ql.qlinear_debug_wait_test(1, 0, 0)
+    ql.qlinear_linear(2, x, q, p0, p1, y, M, N, K, ws)
+    torch.cuda.synchronize()
+    assert ql.qlinear_read_error(ws) == 0
+    assert torch.equal(y, want) and bool(torch.isfinite(y).all())

@@ -39,8 +39,9 @@
 // about one rounding each to the output's own (2.1e-4 in the relative L2 norm becomes 2.8e-4, with
 // two of them 3.3e-4 to 4.2e-4); keeping dz in two halves would double the MMAs.
 //
-// Every barrier wait is bounded in time (100 ms against microseconds; qlinear_debug_wait_test
-// sets another limit); one that runs out sets a flag in the workspace's error word, all roles
+// Every barrier wait is bounded in time (100 ms against microseconds, and 4 us more for each stage
+// of a tile, several times what one takes, since the epilogue waits for a whole tile;
+// qlinear_debug_wait_test sets another limit); one that runs out sets a flag in the workspace's error word, all roles
 // leave their loops, and the CTA waits for its own copies and MMAs, frees its tensor memory and
 // exits.
 #include <cuda.h>
@@ -133,7 +134,7 @@ struct TcParams {
   int steps;     // units per tile: groups (forward) or blocks (backward)
   int bn, mtiles, tiles, whole;  // tokens per tile; tiles [0, whole) are not split
   int runners;                   // workers that share the stages of tiles [whole, tiles)
-  uint32_t wait_us;              // limit of a wait
+  uint32_t wait_us;              // limit of a wait (the longest, for a tile, included)
   uint32_t test_us;              // tests of the waits: delays (qfused::WaitTest)
 };
 
@@ -1184,7 +1185,7 @@ ql_status launch_as(const qfused::Product& p, const Tokens& tk) {
   P.whole = sc.whole;
   P.runners = sc.runners;
   const qfused::WaitTest wt = qfused::wait_test();
-  P.wait_us = wt.limit_us;
+  P.wait_us = wt.limit_us + 4u * (uint32_t)P.steps;
   P.test_us = wt.delays;
   if ((size_t)(P.tiles - P.whole) * ctas * 4 * sizeof(uint32_t) > qfused::kTcCounterBytes)
     return QL_ERR_UNSUPPORTED;  // more than five hundred SMs
