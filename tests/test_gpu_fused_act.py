@@ -102,3 +102,46 @@ def test_gated_values_in_the_tails(act, M, factor):
     want = _value(act, z.double()) * factor
     keep = want.abs() < 65504
     _check(h[:, keep], want[keep], f"{act} times {factor}")
+
+
+def _derivative(name, z):
+    """fp64: (act', the sum of the sizes of its terms, the sigmoid's argument or 0)."""
+    zero = torch.zeros_like(z)
+    if name == "relu":
+        return (z > 0).double(), zero, zero
+    if name == "gelu":
+        phi = torch.exp(-z * z / 2) / math.sqrt(2 * math.pi)
+        cdf = 0.5 * torch.erfc(-z * math.sqrt(0.5))
+        return cdf + z * phi, cdf + (z * phi).abs(), zero
+    a, slope = z, torch.ones_like(z)
+    if name == "gelu_tanh":
+        k = 2 * math.sqrt(2 / math.pi)
+        a, slope = k * (z + 0.044715 * z ** 3), k * (1 + 3 * 0.044715 * z * z)
+    s = torch.sigmoid(a)
+    t = z * s * torch.sigmoid(-a) * slope
+    return s + t, s + t.abs(), a.abs() if name == "gelu_tanh" else zero
+
+
+@pytest.mark.parametrize("act", ACTS)
+def test_gradients_in_the_tails(act):
+    """The fp32 column sums of one row of ones are the derivatives themselves.  Relative to their
+    terms: a sigmoid and its complement are each within 2 ulp of the exponential and three half
+    steps more, 4.2e-7, a product of both and z within 2^-20; the tanh form's argument adds its
+    own five half steps (2^-21.6 |a|); the normal CDF's polynomial is within 1.5e-6 (2^-19), the
+    density's argument exact."""
+    z = _arguments()
+    lay, gat = _layer()
+    N = z.numel()
+    one = torch.ones((1, N), dtype=torch.float16, device=DEV)
+    db = torch.empty(N, dtype=torch.float32, device=DEV)
+    lay.linear_backward(one, z=z.view(1, N), act=act, dbias=db)
+    want, terms, a = _derivative(act, z.double())
+    rel = 2.0 ** -19 if act == "gelu" else 2.0 ** -20 * (1 + a)
+    worst = ((db.double() - want).abs() / (rel * terms + 2.0 ** -126)).max()
+    assert worst <= 1, f"{float(worst):.3f} of the bound"
+    both = torch.empty((2, N), dtype=torch.float32, device=DEV)
+    gat.backward(one, torch.stack([z, torch.ones_like(z)]).view(1, 2, N), act=act, dbias=both)
+    assert torch.equal(both[0], db)
+    value = _value(act, z.double())
+    worst = ((both[1].double() - value).abs() / (rel * value.abs() + 2.0 ** -126)).max()
+    assert worst <= 1, f"value: {float(worst):.3f} of the bound"

@@ -10,6 +10,7 @@
 // Relative to the value that is at most 2^-15 wherever an fp16 output is not zero (the exponent's
 // own rounding at x = 30 included, which a gated product with a large factor still shows), a
 // sixteenth of half an fp16 step, at every z: no value is formed by a difference.
+// Gradients: expf and a true division, since their column sums are fp32.
 #pragma once
 #include "qlinear.h"
 
@@ -25,16 +26,24 @@ constexpr float kGeluCubic = 0.044715f;
 // 1 / (1 + e^-x): 0 and 1 at the far ends.
 __device__ __forceinline__ float sigmoid(float x) { return __fdividef(1.f, 1.f + __expf(-x)); }
 
+// sigma(x) and 1 - sigma(x), each to a few ulp.
+__device__ __forceinline__ void sigmoid_both(float x, float& s, float& c) {
+  const float e = expf(-fabsf(x)), r = 1.f / (1.f + e), er = e * r;
+  s = x < 0.f ? er : r;
+  c = x < 0.f ? r : er;
+}
+
 // Phi(z) and e^(-z^2 / 2), without branches.  Phi(-|z|) = erfcx(x) e^(-x^2) / 2, x = |z| / sqrt 2,
 // where erfcx(x) = e^(x^2) erfc(x) falls smoothly like 1 / x: t q(t), t = 1 / (1 + 0.6 x), q the
 // polynomial of degree 7 with the least relative error over 0 <= x <= 12 (fitted by reweighted
 // least squares on 4000 Chebyshev points; coefficients halved here).  Relative error 3.1e-7, in
 // fp32 with an exact exponential 6e-7 for |z| <= 2 and 1.5e-6 for |z| <= 8: a tail keeps its
 // digits.
+template <bool FAST>
 __device__ __forceinline__ float normal_cdf(float z, float& e) {
   const float d = fmaf(0.6f * kSqrtHalf, fabsf(z), 1.f), x2 = (-0.5f * z) * z;
-  const float t = __fdividef(1.f, d);
-  e = __expf(x2);
+  const float t = FAST ? __fdividef(1.f, d) : 1.f / d;
+  e = FAST ? __expf(x2) : expf(x2);
   float q = fmaf(-0.0460444614f, t, 0.205987081f);
   q = fmaf(q, t, -0.322253346f);
   q = fmaf(q, t, 0.141909704f);
@@ -51,7 +60,7 @@ __device__ __forceinline__ float act_forward(int act, float z) {
     case QL_ACT_RELU: return z < 0.f ? 0.f : z;  // NaN stays NaN
     case QL_ACT_GELU: {
       float e;
-      return z * normal_cdf(z, e);
+      return z * normal_cdf<true>(z, e);
     }
     case QL_ACT_GELU_TANH:
       return z * sigmoid(2.f * kSqrt2OverPi * (z + kGeluCubic * z * z * z));
@@ -62,6 +71,7 @@ __device__ __forceinline__ float act_forward(int act, float z) {
 
 // Value and derivative.
 __device__ __forceinline__ void act_both(int act, float z, float& f, float& df) {
+  float s, c;
   switch (act) {
     case QL_ACT_RELU:
       f = z < 0.f ? 0.f : z;
@@ -69,23 +79,21 @@ __device__ __forceinline__ void act_both(int act, float z, float& f, float& df) 
       return;
     case QL_ACT_GELU: {
       float e;
-      const float cdf = normal_cdf(z, e);
+      const float cdf = normal_cdf<false>(z, e);
       f = z * cdf;
       df = fmaf(z * kInvSqrt2Pi, e, cdf);
       return;
     }
-    case QL_ACT_GELU_TANH: {
-      const float s = sigmoid(2.f * kSqrt2OverPi * (z + kGeluCubic * z * z * z));
+    case QL_ACT_GELU_TANH:
+      sigmoid_both(2.f * kSqrt2OverPi * (z + kGeluCubic * z * z * z), s, c);
       f = z * s;
-      df = fmaf(z * s * (1.f - s), 2.f * kSqrt2OverPi * (1.f + 3.f * kGeluCubic * z * z), s);
+      df = fmaf(f * c, 2.f * kSqrt2OverPi * (1.f + 3.f * kGeluCubic * z * z), s);
       return;
-    }
-    case QL_ACT_SILU: {
-      const float s = sigmoid(z);
+    case QL_ACT_SILU:
+      sigmoid_both(z, s, c);
       f = z * s;
-      df = s * fmaf(z, 1.f - s, 1.f);
+      df = fmaf(f, c, s);
       return;
-    }
     default:
       f = z;
       df = 1.f;
