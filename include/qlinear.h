@@ -454,8 +454,9 @@ ql_status qlinear_matmul(int fmt, const uint16_t* x, const void* packed, const v
  * Numbers: sums over K (N in the backward products), the epilogue and the column sums are
  * fp32; every fp16 output is rounded once, to nearest even.  At M > 16, and in the backward
  * products, the tensor cores multiply fp16 weights (those of qlinear_dequant_fp16) and the
- * gradients dz rounded to fp16, as the fp16 GEMM of qlinear_prefill does; at M <= 16 the
- * forward products use the GEMV's exact codes.  Results are reproducible bit for bit.
+ * gradients dz rounded to fp16 after each row was scaled by a power of two that is taken back
+ * in fp32 (so dz keeps 11 bits whatever its size, down to 2^-28 of its row's largest |dy|, or
+ * |dh u| and |dh g|); at M <= 16 the forward products use the GEMV's exact codes.  Results are reproducible bit for bit.
  *
  * Arguments common to the four entries (device pointers, rows contiguous):
  *   packed, p0, p1 : as for qlinear_prefill_fused, packed 32-byte aligned; the gated entries

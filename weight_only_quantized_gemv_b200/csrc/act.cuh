@@ -10,7 +10,8 @@
 // Relative to the value that is at most 2^-15 wherever an fp16 output is not zero (the exponent's
 // own rounding at x = 30 included, which a gated product with a large factor still shows), a
 // sixteenth of half an fp16 step, at every z: no value is formed by a difference.
-// Gradients: expf and a true division, since their column sums are fp32.
+// Gradients: the same where they are rounded to fp16 (FAST), expf and true divisions where they are
+// summed in fp32.
 #pragma once
 #include "qlinear.h"
 
@@ -26,9 +27,11 @@ constexpr float kGeluCubic = 0.044715f;
 // 1 / (1 + e^-x): 0 and 1 at the far ends.
 __device__ __forceinline__ float sigmoid(float x) { return __fdividef(1.f, 1.f + __expf(-x)); }
 
-// sigma(x) and 1 - sigma(x), each to a few ulp.
+// sigma(x) and 1 - sigma(x), neither by a difference.
+template <bool FAST>
 __device__ __forceinline__ void sigmoid_both(float x, float& s, float& c) {
-  const float e = expf(-fabsf(x)), r = 1.f / (1.f + e), er = e * r;
+  const float e = FAST ? __expf(-fabsf(x)) : expf(-fabsf(x));
+  const float r = FAST ? __fdividef(1.f, 1.f + e) : 1.f / (1.f + e), er = e * r;
   s = x < 0.f ? er : r;
   c = x < 0.f ? r : er;
 }
@@ -70,6 +73,7 @@ __device__ __forceinline__ float act_forward(int act, float z) {
 }
 
 // Value and derivative.
+template <bool FAST>
 __device__ __forceinline__ void act_both(int act, float z, float& f, float& df) {
   float s, c;
   switch (act) {
@@ -79,18 +83,18 @@ __device__ __forceinline__ void act_both(int act, float z, float& f, float& df) 
       return;
     case QL_ACT_GELU: {
       float e;
-      const float cdf = normal_cdf<false>(z, e);
+      const float cdf = normal_cdf<FAST>(z, e);
       f = z * cdf;
       df = fmaf(z * kInvSqrt2Pi, e, cdf);
       return;
     }
     case QL_ACT_GELU_TANH:
-      sigmoid_both(2.f * kSqrt2OverPi * (z + kGeluCubic * z * z * z), s, c);
+      sigmoid_both<FAST>(2.f * kSqrt2OverPi * (z + kGeluCubic * z * z * z), s, c);
       f = z * s;
       df = fmaf(f * c, 2.f * kSqrt2OverPi * (1.f + 3.f * kGeluCubic * z * z), s);
       return;
     case QL_ACT_SILU:
-      sigmoid_both(z, s, c);
+      sigmoid_both<FAST>(z, s, c);
       f = z * s;
       df = fmaf(f, c, s);
       return;

@@ -1,9 +1,9 @@
-// Entries of the fused linear layers (include/qlinear.h) and the gradient kernel of their
+// Entries of the fused linear layers (include/qlinear.h) and the gradient kernels of their
 // backward passes.
 //
 // Forward: one launch, the GEMV kernel with an epilogue or the tensor-core product with one.
-// Backward: dz = dy act'(z) (or the gated pair) and the column sums in one pass over the
-// activations, then dx = dz W^T on the tensor cores.
+// Backward: dz = dy act'(z) (or the gated pair), with its column sums where they are asked for, then
+// dx = dz W^T on the tensor cores.
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
@@ -30,23 +30,41 @@ bool shape_ok(int M, int N, int K) {
 }
 
 // ---------------------------------------------------------------------------
-// dz and its column sums.
+// dz for the product, and its column sums.
 //
-// One pass over dy and z (dh, g, u): bound by memory (6 bytes an element, gated 10, read and
-// written once).  A thread takes eight consecutive columns as 16-byte vectors, a warp 256
-// columns, the eight warps of a block every eighth row of the block's strip; the fp32 sums of
-// a column over the strip meet in shared memory, and with more than one strip in the
-// workspace, where the last block of a column range to arrive adds the strips in their order.
+// The tensor cores take fp16, whose range gradients leave: dh u act'(g) passes 65504 for ordinary
+// values, and unscaled gradients fall below 6e-8.  So a row of dz is multiplied by a power of two,
+// and the product's epilogue divides its fp32 sums by it, both without rounding.  It is the one that
+// brings the row's largest |dy| (gated: |dh u|, |dh g|) into [2^14, 2^15): |act'| <= 1.13 and
+// |act(g)| <= |g|, so nothing overflows, and every element down to 2^-28 of that keeps 11 bits.
+// (Rows, because a row of dx contracts one row of dz: nothing of one row shows in another.)
+//
+// Without column sums one kernel does both, a block to a row.  With them the same kernel only finds
+// the factors (kFactor), and a second one with blocks of its own shape, whose columns' sums it
+// keeps, writes dz.  All are bound by memory, or GELU's arithmetic.
+constexpr int kDzThreads = 512;
+enum { kFactor, kStore };
+
+struct DzParams {
+  const __half* dy;  // [M][W]
+  const __half* z;   // [M][W]; gated [M][2][W]
+  __half* dz;        // [M][W]; gated [M][2W] in packed column order
+  uint8_t* unscale;  // [M]: the fp32 exponent field of the factor that undoes a row's scaling
+  int W, act;
+};
+
+// A thread takes eight consecutive columns as 16-byte vectors, a warp 256 columns, the eight warps
+// of a block every eighth row of the block's strip; the fp32 sums of a column over the strip meet
+// in shared memory, and with more than one strip in the workspace, where the last block of a
+// column range to arrive adds the strips in their order.
 constexpr int kGradCols = 256, kGradWarps = 8;
 
 struct GradParams {
-  const __half* dy;   // [M][W]
-  const __half* z;    // linear [M][W] or null (act none); gated [M][2][W]
-  __half* dz;         // [M][W]; gated [M][2W] in packed column order; null: not written
-  float* dbias;       // [W]; gated [2][W]; or null
+  DzParams d;         // z: null without an activation, dz: then null (dy serves as it is)
+  float* dbias;       // [W]; gated [2][W]
   float* partials;    // [strips][W] ([strips][2][W])
   uint32_t* counters; // one per column range
-  int M, W, act, rows;  // rows per strip
+  int M, rows;        // rows per strip
 };
 
 __device__ __forceinline__ void unpack8(uint4 v, float (&f)[8]) {
@@ -75,44 +93,168 @@ __device__ __forceinline__ uint4 load8(const __half* p) {
 }
 
 // d *= act'(z); the activation's branch outside the loop
-template <int ACT>
+template <int ACT, bool FAST>
 __device__ __forceinline__ void times_gradient_of(float (&d)[8], const float (&z)[8]) {
 #pragma unroll
   for (int e = 0; e < 8; ++e) {
     float f, df;
-    qact::act_both(ACT, z[e], f, df);
+    qact::act_both<FAST>(ACT, z[e], f, df);
     d[e] *= df;
   }
 }
+template <bool FAST>
 __device__ __forceinline__ void times_gradient(int act, float (&d)[8], const float (&z)[8]) {
   switch (act) {
-    case QL_ACT_RELU: return times_gradient_of<QL_ACT_RELU>(d, z);
-    case QL_ACT_GELU: return times_gradient_of<QL_ACT_GELU>(d, z);
-    case QL_ACT_GELU_TANH: return times_gradient_of<QL_ACT_GELU_TANH>(d, z);
-    case QL_ACT_SILU: return times_gradient_of<QL_ACT_SILU>(d, z);
+    case QL_ACT_RELU: return times_gradient_of<QL_ACT_RELU, FAST>(d, z);
+    case QL_ACT_GELU: return times_gradient_of<QL_ACT_GELU, FAST>(d, z);
+    case QL_ACT_GELU_TANH: return times_gradient_of<QL_ACT_GELU_TANH, FAST>(d, z);
+    case QL_ACT_SILU: return times_gradient_of<QL_ACT_SILU, FAST>(d, z);
     default: return;
   }
 }
 // dg = dh u act'(g), dh becomes du = dh act(g)
-template <int ACT>
+template <int ACT, bool FAST>
 __device__ __forceinline__ void gated_gradients_of(float (&dh)[8], const float (&g)[8],
                                                    const float (&u)[8], float (&dg)[8]) {
 #pragma unroll
   for (int e = 0; e < 8; ++e) {
     float f, df;
-    qact::act_both(ACT, g[e], f, df);
+    qact::act_both<FAST>(ACT, g[e], f, df);
     dg[e] = dh[e] * u[e] * df;
     dh[e] *= f;
   }
 }
+template <bool FAST>
 __device__ __forceinline__ void gated_gradients(int act, float (&dh)[8], const float (&g)[8],
                                                 const float (&u)[8], float (&dg)[8]) {
   switch (act) {
-    case QL_ACT_RELU: return gated_gradients_of<QL_ACT_RELU>(dh, g, u, dg);
-    case QL_ACT_GELU: return gated_gradients_of<QL_ACT_GELU>(dh, g, u, dg);
-    case QL_ACT_GELU_TANH: return gated_gradients_of<QL_ACT_GELU_TANH>(dh, g, u, dg);
-    case QL_ACT_SILU: return gated_gradients_of<QL_ACT_SILU>(dh, g, u, dg);
-    default: return gated_gradients_of<QL_ACT_NONE>(dh, g, u, dg);
+    case QL_ACT_RELU: return gated_gradients_of<QL_ACT_RELU, FAST>(dh, g, u, dg);
+    case QL_ACT_GELU: return gated_gradients_of<QL_ACT_GELU, FAST>(dh, g, u, dg);
+    case QL_ACT_GELU_TANH: return gated_gradients_of<QL_ACT_GELU_TANH, FAST>(dh, g, u, dg);
+    case QL_ACT_SILU: return gated_gradients_of<QL_ACT_SILU, FAST>(dh, g, u, dg);
+    default: return gated_gradients_of<QL_ACT_NONE, FAST>(dh, g, u, dg);
+  }
+}
+
+// Eight columns of a row: dz, or (gated) dg in d[0] and du in d[1].
+template <bool GATED>
+struct Inputs8 {
+  uint4 dy, a, b;  // z; or g, u
+};
+template <bool GATED>
+__device__ __forceinline__ void load_inputs(const __half* dy, const __half* z, size_t row, int W,
+                                            int c, Inputs8<GATED>& in) {
+  in.dy = load8(dy + row + c);
+  if constexpr (GATED) {
+    in.a = load8(z + 2 * row + c);
+    in.b = load8(z + 2 * row + W + c);
+  } else if (z) {
+    in.a = load8(z + row + c);
+  }
+}
+template <bool GATED, bool FAST>
+__device__ __forceinline__ void gradients8(int act, bool has_z, const Inputs8<GATED>& in,
+                                           float (&d)[GATED ? 2 : 1][8]) {
+  float a[8];
+  if constexpr (GATED) {
+    float u[8];
+    unpack8(in.dy, d[1]);
+    unpack8(in.a, a);
+    unpack8(in.b, u);
+    gated_gradients<FAST>(act, d[1], a, u, d[0]);  // d[1] becomes du
+  } else {
+    unpack8(in.dy, d[0]);
+    if (has_z) {
+      unpack8(in.a, a);
+      times_gradient<FAST>(act, d[0], a);
+    }
+  }
+}
+
+// The size that a row's factor goes by, over eight columns: |dy|, or (gated) |dh| max(|g|, |u|).
+// (fmaxf drops NaN.)
+template <bool GATED>
+__device__ __forceinline__ float size8(const Inputs8<GATED>& in) {
+  float d[8], top = 0.f;
+  unpack8(in.dy, d);
+  if constexpr (GATED) {
+    float g[8], u[8];
+    unpack8(in.a, g);
+    unpack8(in.b, u);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) d[e] *= fmaxf(fabsf(g[e]), fabsf(u[e]));
+  }
+#pragma unroll
+  for (int e = 0; e < 8; ++e) top = fmaxf(top, fabsf(d[e]));
+  return top;
+}
+
+// dz of eight columns, each element times `scale`.
+template <bool GATED>
+__device__ __forceinline__ void store_dz(__half* dz, size_t row, int c, float scale,
+                                         const float (&d)[GATED ? 2 : 1][8]) {
+  float v[8];
+#pragma unroll
+  for (int b = 0; b < (GATED ? 2 : 1); ++b) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[e] = d[b][e] * scale;
+    // packed order: gate column f at 32 (f / 16) + f % 16, its up column 16 further
+    __half* o = GATED ? dz + 2 * row + 32 * (size_t)(c >> 4) + (c & 15) + 16 * b : dz + row + c;
+    *reinterpret_cast<uint4*>(o) = pack8(v);
+  }
+}
+
+// A block takes a row.  A thread's first V vectors stay in its registers between the search for
+// the row's factor and the stores; what a wide row has beyond them is read again (from L2).
+template <bool GATED, int WHAT>
+__global__ void __launch_bounds__(kDzThreads, 2) dz_kernel(const DzParams P) {
+  constexpr int NB = GATED ? 2 : 1, V = GATED ? 2 : 3;
+  __shared__ float red[kDzThreads / 32];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const size_t row = (size_t)blockIdx.x * P.W;
+  const int step = 8 * (int)blockDim.x, c0 = 8 * (int)threadIdx.x;  // W is a multiple of 8
+  const __half* z = GATED || WHAT == kStore ? P.z : nullptr;  // (a linear factor needs dy alone)
+  qlk::grid_dependents_launch();
+  qlk::grid_dependency_wait();
+  Inputs8<GATED> in[V];
+  float top = 0.f;
+#pragma unroll
+  for (int i = 0; i < V; ++i)
+    if (c0 + i * step < P.W) load_inputs<GATED>(P.dy, z, row, P.W, c0 + i * step, in[i]);
+#pragma unroll
+  for (int i = 0; i < V; ++i)
+    if (c0 + i * step < P.W) top = fmaxf(top, size8<GATED>(in[i]));
+#pragma unroll 4
+  for (int c = c0 + V * step; c < P.W; c += step) {
+    Inputs8<GATED> more;
+    load_inputs<GATED>(P.dy, GATED ? z : nullptr, row, P.W, c, more);
+    top = fmaxf(top, size8<GATED>(more));
+  }
+#pragma unroll
+  for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+  if (lane == 0) red[warp] = top;
+  __syncthreads();
+  for (int w = 0; w < (int)(blockDim.x >> 5); ++w) top = fmaxf(top, red[w]);
+  // 2^k; a row of zeros, or with an infinity (its dx is not finite either way), stays as it is
+  int k = 0;
+  if (top > 0.f && top <= 3.402823466e38f) k = 14 - ((int)(__float_as_uint(top) >> 23) - 127);
+  if (threadIdx.x == 0) P.unscale[blockIdx.x] = (uint8_t)(127 - k);
+  if constexpr (WHAT == kStore) {
+    const float scale = __uint_as_float((uint32_t)(127 + k) << 23);
+    float d[NB][8];
+#pragma unroll
+    for (int i = 0; i < V; ++i)
+      if (c0 + i * step < P.W) {
+        gradients8<GATED, true>(P.act, true, in[i], d);
+        store_dz<GATED>(P.dz, row, c0 + i * step, scale, d);
+      }
+#pragma unroll 2
+    for (int c = c0 + V * step; c < P.W; c += step) {
+      Inputs8<GATED> more;
+      load_inputs<GATED>(P.dy, z, row, P.W, c, more);
+      gradients8<GATED, true>(P.act, true, more, d);
+      store_dz<GATED>(P.dz, row, c, scale, d);
+    }
   }
 }
 
@@ -121,11 +263,12 @@ __global__ void __launch_bounds__(32 * kGradWarps, GATED ? 3 : 4) grad_kernel(co
   constexpr int NB = GATED ? 2 : 1;
   __shared__ float red[NB][kGradWarps][kGradCols];
   __shared__ uint32_t last;
+  const DzParams& D = P.d;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int c0 = blockIdx.x * kGradCols, c = c0 + 8 * lane;
   const int m0 = blockIdx.y * P.rows;
   const int m1 = m0 + P.rows < P.M ? m0 + P.rows : P.M;
-  const bool in = c < P.W;  // W is a multiple of 8: a thread's columns are all in or all out
+  const bool in = c < D.W;  // W is a multiple of 8: a thread's columns are all in or all out
   float sum[NB][8];
 #pragma unroll
   for (int b = 0; b < NB; ++b)
@@ -135,56 +278,32 @@ __global__ void __launch_bounds__(32 * kGradWarps, GATED ? 3 : 4) grad_kernel(co
   qlk::grid_dependency_wait();
   if (in) {
     // kRows rows at a time: their loads are in flight together
-    constexpr int kRows = GATED ? 2 : 4;
+    constexpr int kRows = 2;
     for (int mm = m0 + warp; mm < m1; mm += kRows * kGradWarps) {
-      uint4 vd[kRows], va[kRows], vb[kRows];
+      Inputs8<GATED> in8[kRows];
+      uint32_t unscale[kRows];
 #pragma unroll
       for (int i = 0; i < kRows; ++i) {
         const int m = mm + i * kGradWarps;
         if (m >= m1) continue;
-        const size_t row = (size_t)m * P.W;
-        vd[i] = load8(P.dy + row + c);
-        if constexpr (GATED) {
-          va[i] = load8(P.z + 2 * row + c);
-          vb[i] = load8(P.z + 2 * row + P.W + c);
-        } else if (P.z) {
-          va[i] = load8(P.z + row + c);
-        }
+        load_inputs<GATED>(D.dy, D.z, (size_t)m * D.W, D.W, c, in8[i]);
+        if (D.dz) unscale[i] = __ldcg(D.unscale + m);
       }
 #pragma unroll
       for (int i = 0; i < kRows; ++i) {
         const int m = mm + i * kGradWarps;
         if (m >= m1) continue;
-        const size_t row = (size_t)m * P.W;
-        float d[8], a[8];
-        unpack8(vd[i], d);
-        if constexpr (GATED) {
-          float u[8], dg[8];
-          unpack8(va[i], a);
-          unpack8(vb[i], u);
-          gated_gradients(P.act, d, a, u, dg);  // d becomes du
+        float d[NB][8];
+        gradients8<GATED, false>(D.act, D.z != nullptr, in8[i], d);
 #pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            sum[0][e] += dg[e];
-            sum[1][e] += d[e];
-          }
-          // packed order: gate column f at 32 (f / 16) + f % 16, its up column 16 further
-          __half* o = P.dz + 2 * row + 32 * (c >> 4) + (c & 15);
-          *reinterpret_cast<uint4*>(o) = pack8(dg);
-          *reinterpret_cast<uint4*>(o + 16) = pack8(d);
-        } else {
-          if (P.z) {
-            unpack8(va[i], a);
-            times_gradient(P.act, d, a);
-          }
+        for (int b = 0; b < NB; ++b)
 #pragma unroll
-          for (int e = 0; e < 8; ++e) sum[0][e] += d[e];
-          if (P.dz) *reinterpret_cast<uint4*>(P.dz + row + c) = pack8(d);
-        }
+          for (int e = 0; e < 8; ++e) sum[b][e] += d[b][e];
+        if (D.dz)
+          store_dz<GATED>(D.dz, (size_t)m * D.W, c, __uint_as_float((254u - unscale[i]) << 23), d);
       }
     }
   }
-  if (!P.dbias) return;
 #pragma unroll
   for (int b = 0; b < NB; ++b)
 #pragma unroll
@@ -199,28 +318,28 @@ __global__ void __launch_bounds__(32 * kGradWarps, GATED ? 3 : 4) grad_kernel(co
     for (int w = 0; w < kGradWarps; ++w) s[b] += red[b][w][threadIdx.x];
   }
   if (gridDim.y == 1) {
-    if (cc < P.W)
+    if (cc < D.W)
 #pragma unroll
-      for (int b = 0; b < NB; ++b) P.dbias[(size_t)b * P.W + cc] = s[b];
+      for (int b = 0; b < NB; ++b) P.dbias[(size_t)b * D.W + cc] = s[b];
     return;
   }
-  if (cc < P.W)
+  if (cc < D.W)
 #pragma unroll
-    for (int b = 0; b < NB; ++b) P.partials[((size_t)blockIdx.y * NB + b) * P.W + cc] = s[b];
+    for (int b = 0; b < NB; ++b) P.partials[((size_t)blockIdx.y * NB + b) * D.W + cc] = s[b];
   __threadfence();
   __syncthreads();
   if (threadIdx.x == 0) last = qlk::arrive_acq_rel(P.counters + blockIdx.x) + 1 == gridDim.y;
   __syncthreads();
   if (!last) return;
   __threadfence();
-  if (cc < P.W)
+  if (cc < D.W)
 #pragma unroll
     for (int b = 0; b < NB; ++b) {
       float t = 0.f;
 #pragma unroll 8
       for (unsigned y = 0; y < gridDim.y; ++y)
-        t += __ldcg(P.partials + ((size_t)y * NB + b) * P.W + cc);
-      P.dbias[(size_t)b * P.W + cc] = t;
+        t += __ldcg(P.partials + ((size_t)y * NB + b) * D.W + cc);
+      P.dbias[(size_t)b * D.W + cc] = t;
     }
   if (threadIdx.x == 0) P.counters[blockIdx.x] = 0u;  // ready for the next call
 }
@@ -280,7 +399,16 @@ int sm_count() {
   return sms;
 }
 
-// dz follows the partial sums
+// A dz block's threads: a vector of eight columns each, up to kDzThreads.
+int dz_threads(int W) {
+  const int t = (W / 8 + 31) / 32 * 32;
+  return t < kDzThreads ? t : kDzThreads;
+}
+
+// the rows' exponents and dz follow the partial sums
+size_t dz_bytes(int M, int N) {
+  return qfused::align_up(M, 256) + (size_t)M * N * sizeof(__half);
+}
 size_t grad_partial_bytes(int M, int N) {  // bound over every M up to this one
   return (size_t)(M < 64 * kGradWarps ? (M + kGradWarps - 1) / kGradWarps : kMaxStrips) * N *
          sizeof(float);
@@ -304,22 +432,37 @@ ql_status forward(qfused::Product& p, void* workspace, size_t workspace_bytes) {
   return p.M <= kGemvRows ? qfused::launch_gemv(p) : qfused::launch_tc(p);
 }
 
-template <bool GATED>
-ql_status launch_grad(const GradParams& g, int strips, cudaStream_t st) {
+template <class Params>
+ql_status launch_early(void (*kernel)(Params), dim3 grid, int threads, const Params& p,
+                       cudaStream_t st) {
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)((g.W + kGradCols - 1) / kGradCols), (unsigned)strips);
-  cfg.blockDim = dim3(32 * kGradWarps);
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3((unsigned)threads);
   cfg.stream = st;
   cudaLaunchAttribute attr;
   attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr.val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
-  if (cudaLaunchKernelEx(&cfg, grad_kernel<GATED>, g) != cudaSuccess) return QL_ERR_CUDA;
-  return QL_OK;
+  return cudaLaunchKernelEx(&cfg, kernel, p) == cudaSuccess ? QL_OK : QL_ERR_CUDA;
 }
 
-// dz (unless dy serves as it is) and dbias, then dx = dz W^T.  W: columns of dy.
+// dz (unless dy serves as it is) and its column sums (if asked for), then dx = dz W^T.  W: columns
+// of dy.
+template <bool GATED>
+ql_status gradients(const GradParams& g, int sms, cudaStream_t st) {
+  const DzParams& d = g.d;
+  const int threads = dz_threads(d.W);
+  if (!g.dbias) return launch_early(dz_kernel<GATED, kStore>, dim3(g.M), threads, d, st);
+  if (d.dz)
+    if (const ql_status s =
+            launch_early(dz_kernel<GATED, kFactor>, dim3(g.M), threads, d, st))
+      return s;
+  const dim3 grid((unsigned)((d.W + kGradCols - 1) / kGradCols),
+                  (unsigned)grad_strips(g.M, d.W, sms));
+  return launch_early(grad_kernel<GATED>, grid, 32 * kGradWarps, g, st);
+}
+
 ql_status backward(qfused::Product& p, const __half* dy, const __half* z, int W, float* dbias,
                    void* workspace, size_t workspace_bytes) {
   const bool gated = p.epi.gated, dz_is_dy = !gated && p.epi.act == QL_ACT_NONE;
@@ -327,31 +470,28 @@ ql_status backward(qfused::Product& p, const __half* dy, const __half* z, int W,
   if (sms <= 0) return QL_ERR_CUDA;
   const size_t off = qfused::partial_offset(p.N);
   const size_t part = backward_partial_bytes(p.M, p.N);
-  const size_t dz_bytes = dz_is_dy ? 0 : (size_t)p.M * p.N * sizeof(__half);
-  if (!workspace || workspace_bytes < off + part + dz_bytes) return QL_ERR_WORKSPACE;
+  if (!workspace || workspace_bytes < off + part + (dz_is_dy ? 0 : dz_bytes(p.M, p.N)))
+    return QL_ERR_WORKSPACE;
   if (!aligned(workspace, 256)) return QL_ERR_ALIGN;
   uint8_t* ws = static_cast<uint8_t*>(workspace);
-  __half* dz = reinterpret_cast<__half*>(ws + off + part);
+  uint8_t* unscale = ws + off + part;
+  __half* dz = reinterpret_cast<__half*>(unscale + qfused::align_up(p.M, 256));
   p.err = static_cast<uint32_t*>(workspace);
   p.counters = reinterpret_cast<uint32_t*>(ws + qfused::kErrBytes);
   p.partials = reinterpret_cast<float*>(ws + off);
   p.partial_bytes = part;
   p.x = dz_is_dy ? dy : dz;
+  p.epi.unscale = dz_is_dy ? nullptr : unscale;
   if (!dz_is_dy || dbias) {
     GradParams g;
-    g.dy = dy;
-    g.z = dz_is_dy ? nullptr : z;
-    g.dz = dz_is_dy ? nullptr : dz;
+    g.d = DzParams{dy, dz_is_dy ? nullptr : z, dz_is_dy ? nullptr : dz, unscale, W, p.epi.act};
     g.dbias = dbias;
     g.partials = p.partials;
     g.counters = reinterpret_cast<uint32_t*>(ws + qfused::kVecCounterOffset);
     g.M = p.M;
-    g.W = W;
-    g.act = p.epi.act;
     g.rows = grad_rows(p.M, W, sms);
-    const int strips = grad_strips(p.M, W, sms);
-    const ql_status s = gated ? launch_grad<true>(g, strips, p.stream)
-                              : launch_grad<false>(g, strips, p.stream);
+    const ql_status s = gated ? gradients<true>(g, sms, p.stream)
+                              : gradients<false>(g, sms, p.stream);
     if (s != QL_OK) return s;
   }
   p.epi.act = QL_ACT_NONE;
@@ -375,7 +515,7 @@ extern "C" size_t qlinear_fused_workspace_bytes(int fmt, int M, int N, int K, in
     }
   if (qfused::tc_partial_bytes(M) > part) part = qfused::tc_partial_bytes(M);
   if (backward) {
-    const size_t b = backward_partial_bytes(M, N) + (size_t)M * N * sizeof(__half);
+    const size_t b = backward_partial_bytes(M, N) + dz_bytes(M, N);
     if (b > part) part = b;
   }
   return qfused::partial_offset(N) + qfused::align_up(part, 256);
@@ -408,7 +548,8 @@ extern "C" ql_status qlinear_linear(int fmt, const uint16_t* x, const void* pack
   p.p1 = p1;
   p.epi = qfused::Epilogue{reinterpret_cast<const __half*>(bias),
                            reinterpret_cast<const __half*>(residual),
-                           reinterpret_cast<__half*>(y), reinterpret_cast<__half*>(z), act, 0};
+                           reinterpret_cast<__half*>(y), reinterpret_cast<__half*>(z),
+                           nullptr, act, 0};
   p.M = M;
   p.N = N;
   p.K = K;
@@ -440,7 +581,8 @@ extern "C" ql_status qlinear_gated(int fmt, const uint16_t* x, const void* packe
   p.p0 = p0;
   p.p1 = p1;
   p.epi = qfused::Epilogue{reinterpret_cast<const __half*>(bias), nullptr,
-                           reinterpret_cast<__half*>(h), reinterpret_cast<__half*>(gu), act, 1};
+                           reinterpret_cast<__half*>(h), reinterpret_cast<__half*>(gu),
+                           nullptr, act, 1};
   p.M = M;
   p.N = N;
   p.K = K;
@@ -471,7 +613,7 @@ extern "C" ql_status qlinear_linear_backward(int fmt, const uint16_t* dy, const 
   p.packed = packed;
   p.p0 = p0;
   p.p1 = p1;
-  p.epi = qfused::Epilogue{nullptr, nullptr, reinterpret_cast<__half*>(dx), nullptr, act, 0};
+  p.epi = qfused::Epilogue{nullptr, nullptr, reinterpret_cast<__half*>(dx), nullptr, nullptr, act, 0};
   p.M = M;
   p.N = N;
   p.K = K;
@@ -504,7 +646,7 @@ extern "C" ql_status qlinear_gated_backward(int fmt, const uint16_t* dh, const u
   p.packed = packed;
   p.p0 = p0;
   p.p1 = p1;
-  p.epi = qfused::Epilogue{nullptr, nullptr, reinterpret_cast<__half*>(dx), nullptr, act, 1};
+  p.epi = qfused::Epilogue{nullptr, nullptr, reinterpret_cast<__half*>(dx), nullptr, nullptr, act, 1};
   p.M = M;
   p.N = N;
   p.K = K;

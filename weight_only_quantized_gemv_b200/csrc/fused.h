@@ -12,12 +12,14 @@ namespace qfused {
 // What happens to an output element z (fp32) of the forward products, bias added first:
 //   linear: y = act(z) + residual, z kept if zsave
 //   gated : the packed columns alternate 16 gate / 16 up; h = act(g) u, (g, u) kept if zsave
-// The backward products store dx = the sum itself (act none, nothing else).
+// The backward products store dx = the sum, times the row's power of two if dz was scaled
+// (unscale[m]: the exponent field of that fp32 power; readable up to a multiple of 8 rows).
 struct Epilogue {
   const __half* bias;      // linear [N]; gated [2][F]; or null
   const __half* residual;  // [M][N] or null (linear)
   __half* y;               // [M][N], gated [M][F], backward [M][K]
   __half* zsave;           // [M][N], gated [M][2][F], or null
+  const uint8_t* unscale;  // backward: [M], or null
   int act;
   int gated;
 };

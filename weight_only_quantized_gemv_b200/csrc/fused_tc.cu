@@ -35,9 +35,10 @@
 // bytes (decoding: 56 % of the issue slots, the tensor pipe 35 %), 8192 x 28672 with 2048 tokens,
 // GELU, bias, residual and the pre-activation kept 843 us (1.14 PFLOP/s, at the power limit).
 //
-// The weights and, backward, dz are rounded to fp16 once: the operand type of kind::f16.  That adds
-// about one rounding each to the output's own (2.1e-4 in the relative L2 norm becomes 2.8e-4, with
-// two of them 3.3e-4 to 4.2e-4); keeping dz in two halves would double the MMAs.
+// The weights and, backward, dz (its rows scaled, fused.cu) are rounded to fp16 once: the operand
+// type of kind::f16.  That adds about one rounding each to the output's own (2.1e-4 in the relative
+// L2 norm becomes 2.8e-4, with two of them 3.3e-4 to 4.2e-4); keeping dz in two halves would double
+// the MMAs.
 //
 // Every barrier wait is bounded in time (100 ms against microseconds, and 4 us more for each stage
 // of a tile, several times what one takes, since the epilogue waits for a whole tile;
@@ -483,6 +484,19 @@ __device__ __forceinline__ void finish_gated(const TcParams& P, float (&v)[kTok]
   for (int e = 0; e < kTok / 2; ++e) g[e] *= u[e];
   // this lane's tokens: up, up + 2, ..
   store_tokens(E.y + (size_t)(m0 + up) * F + f, (size_t)2 * F, g, (count - up + 1) / 2, lane, in);
+}
+
+// Backward: the sums of kTok tokens back from their rows' scaling (fused.cu), exactly.
+__device__ __forceinline__ uint2 load_unscale(const TcParams& P, int m) {
+  return __ldcg(reinterpret_cast<const uint2*>(P.epi.unscale + m));
+}
+__device__ __forceinline__ void unscale_tokens(float (&v)[kTok], uint2 x) {
+#pragma unroll
+  for (int e = 0; e < kTok; ++e) {
+    const uint32_t w = e < 4 ? x.x : x.y;
+    const int up = 23 - 8 * (e & 3);  // the byte's way to the exponent field
+    v[e] *= __uint_as_float((up >= 0 ? w << up : w >> -up) & 0x7F800000u);
+  }
 }
 
 // The warp's residual of kTok tokens, two rows in one 4-byte load each (exchanged when used).
@@ -954,11 +968,15 @@ __global__ void __launch_bounds__(TcCfg<BNX, FMT, PAIR, EP>::kThreads, 1)
       }
       uint32_t res[kTok / 2] = {};
       load_residual(P, res, m0 + c_first, cols - c_first, row, lane);
+      uint2 back = {};
+      if (BWD && E.unscale && c_first < cols) back = load_unscale(P, m0 + c_first);
 #pragma unroll 1
       for (int c0 = c_first; c0 < cols; c0 += step) {
         uint32_t res_next[kTok / 2] = {};
         if (c0 + step < cols)
           load_residual(P, res_next, m0 + c0 + step, cols - c0 - step, row, lane);
+        uint2 back_next = {};
+        if (BWD && E.unscale && c0 + step < cols) back_next = load_unscale(P, m0 + c0 + step);
         float v[kTok];
         if (whole) {
           uint32_t r[8];
@@ -989,6 +1007,8 @@ __global__ void __launch_bounds__(TcCfg<BNX, FMT, PAIR, EP>::kThreads, 1)
             hop = (size_t)(2 * C::kCtas) * 128 * P.bn;
           }
         }
+        if (BWD && E.unscale) unscale_tokens(v, back);
+        back = back_next;
         if (E.gated)
           finish_gated(P, v, m0 + c0, cols - c0, row, bias, lane);
         else
