@@ -7,6 +7,7 @@ class only moves and marshals data; every operation runs in ``libqlinear.so``.
 """
 from __future__ import annotations
 
+import threading
 from typing import Optional
 
 import numpy as np
@@ -70,13 +71,22 @@ class _FusedWorkspace:
 
     The workspace is one zero-filled buffer, grown by ``reserve`` as more rows are asked for;
     buffers that were outgrown stay alive with the layer, since a captured graph may still use
-    them.  Calls of one layer run one after the other: an eager call on another stream than
+    them.  Calls of one layer run one after the other, whichever host threads they come from: a
+    call's launches are enqueued under the layer's lock, and an eager call on another stream than
     the last waits for that stream's work.  Work that overlaps in time - graphs captured from
     one layer and replayed at the same time - needs a workspace of its own:
     ``workspace=layer.new_workspace(rows)``.  Tensors a call makes are made on its stream.  A
     stream given as a raw handle must live until the layer's next call on another stream, which
     waits for it.
     """
+
+    def __getstate__(self):  # a copied or unpickled layer has a lock and workspaces of its own
+        own = ("_fused_lock", "_fused_ws", "_fused_last")
+        return {k: v for k, v in self.__dict__.items() if k not in own}
+
+    def __setstate__(self, state):
+        self.__dict__.update(state)
+        self._fused_lock = threading.RLock()
 
     _fused_ws: tuple = ()    # buffers, the one in use last
     _fused_last = None       # stream of the last eager call: (raw handle, torch stream)
@@ -115,8 +125,10 @@ class _FusedWorkspace:
     def reserve(self, rows: int, backward: bool = True) -> None:
         """Make the layer's own workspace large enough for calls of up to `rows` rows (a call
         that needs more does this itself, except while a graph is being captured)."""
-        if not self._fused_ws or self._fused_ws[-1].numel() < self._fused_bytes(rows, backward):
-            self._fused_ws = self._fused_ws + (self.new_workspace(rows, backward),)
+        with self._fused_lock:
+            if (not self._fused_ws
+                    or self._fused_ws[-1].numel() < self._fused_bytes(rows, backward)):
+                self._fused_ws = self._fused_ws + (self.new_workspace(rows, backward),)
 
     def _fused_call(self, entry, name: str, head: tuple, rows: int, backward: bool, workspace,
                     stream):
@@ -133,17 +145,23 @@ class _FusedWorkspace:
             _check(entry(*head, workspace.data_ptr(),
                          workspace.numel() * workspace.element_size(), raw), name)
             return
-        if self._fused_last is None or self._fused_last[0] != raw:
-            self._fused_switch(raw, stream)
-        if self._fused_ws:
+        # the whole of a call's enqueueing: a second thread's stream must wait for all of it, and
+        # on the same stream its launches must not come between these
+        self._fused_lock.acquire()
+        try:
+            if self._fused_last is None or self._fused_last[0] != raw:
+                self._fused_switch(raw, stream)
+            if self._fused_ws:
+                ws = self._fused_ws[-1]
+                status = entry(*head, ws.data_ptr(), ws.numel(), raw)
+                if status != QL_ERR_WORKSPACE:
+                    _check(status, name)
+                    return
+            self.reserve(rows, backward)
             ws = self._fused_ws[-1]
-            status = entry(*head, ws.data_ptr(), ws.numel(), raw)
-            if status != QL_ERR_WORKSPACE:
-                _check(status, name)
-                return
-        self.reserve(rows, backward)
-        ws = self._fused_ws[-1]
-        _check(entry(*head, ws.data_ptr(), ws.numel(), raw), name)
+            _check(entry(*head, ws.data_ptr(), ws.numel(), raw), name)
+        finally:
+            self._fused_lock.release()
 
     def _fused_switch(self, raw: int, stream) -> None:
         """The layer's workspace moves to another stream: that one waits for the last."""
@@ -194,6 +212,7 @@ class QuantLinear(_FusedWorkspace):
                  group: int = 128):
         self.fmt, self.K, self.N, self.group = fmt, K, N, group
         self.device = torch.device(device)
+        self._fused_lock = threading.RLock()
         packed = qlinear_pack(fmt, canonical_codes, N, K)
         self.qweight = _dev(packed, self.device)
         if fmt == QL_FMT_LUT4:
@@ -398,6 +417,7 @@ class GatedLinear(_FusedWorkspace):
         if fmt not in _FUSED_FORMATS:
             raise ValueError("the gated layer covers W2, W4, W8 (group 128) and LUT4")
         self.fmt, self.K, self.F, self.device = fmt, K, F, torch.device(device)
+        self._fused_lock = threading.RLock()
         self.qweight = _dev(qlinear_pack_gated(fmt, gate[0], up[0], F, K), self.device)
         if fmt == QL_FMT_LUT4:
             tables = [np.asarray(m[1], dtype=np.float16) for m in (gate, up)]
