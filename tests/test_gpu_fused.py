@@ -568,3 +568,54 @@ def test_workspace_after_an_error_flag():
     assert lay.fused_read_error(ws) == 1
     assert not ws.any() and lay.fused_read_error(ws) == 0
     assert torch.equal(lay.linear(x, workspace=ws), want)
+
+
+def test_rising_lengths_keep_few_workspaces():
+    """One buffer per doubling of the rows, not one per length; reserve() takes exactly the rows
+    that it is given."""
+    lay, _ = _linear("w4", 384, 208, seed=62)
+    for M in range(1, 1025, 31):
+        lay.linear_backward(_t(M, M, 208), z=_t(M, M, 208), act="silu")
+    sizes = [w.numel() for w in lay._fused_ws]
+    assert len(sizes) <= 11 and sizes == sorted(sizes)
+    assert sizes[-1] == lay.new_workspace(1024).numel()
+    assert sum(sizes[:-1]) <= 10 * sizes[-1]
+    other, _ = _linear("w4", 384, 208, seed=63)
+    other.reserve(1000)
+    assert other._fused_ws[-1].numel() == other.new_workspace(1000).numel()
+
+
+def test_one_workspace_for_a_model():
+    """The largest layer's workspace serves every layer's calls, forward and backward."""
+    lays = [_linear("w4", 2048, 1168)[0], _linear("w8", 384, 208)[0], _gated("w4", 384, 208)[0]]
+    M = 300
+    ws = max((lay.new_workspace(M) for lay in lays), key=lambda t: t.numel())
+    x, x2 = _t(1, M, 2048), _t(2, M, 384)
+    z, dy, z2, dy2, gu = (_t(3, M, 1168), _t(4, M, 1168), _t(5, M, 208), _t(6, M, 208),
+                          _t(7, M, 2, 208))
+
+    def step(w):
+        return [lays[0].linear(x, workspace=w), lays[1].linear(x2, act="gelu", workspace=w),
+                lays[2].forward(x2, workspace=w),
+                lays[2].backward(dy2, gu, workspace=w),
+                lays[1].linear_backward(dy2, z=z2, act="gelu", workspace=w),
+                lays[0].linear_backward(dy, z=z, act="silu", workspace=w)]
+
+    assert all(torch.equal(a, b) for a, b in zip(step(None), step(ws)))
+    assert ql.qlinear_read_error(ws) == 0
+
+
+def test_growth_falls_back_to_the_rows_asked_for(monkeypatch):
+    """Where the next power of two of rows does not fit into memory."""
+    lay, w = _linear("w4", 384, 208, seed=66)
+    new = lay.new_workspace
+
+    def small(rows, backward=True):
+        if rows > 300:
+            raise torch.OutOfMemoryError("no room")
+        return new(rows, backward)
+
+    monkeypatch.setattr(lay, "new_workspace", small)
+    x = _t(1, 300, 384)
+    ref.check(lay.linear(x), ref.linear(x.double(), w)[0], "y")
+    assert len(lay._fused_ws) == 1

@@ -36,6 +36,7 @@ def _dev(a: np.ndarray, device) -> torch.Tensor:
 
 _FUSED_FORMATS = (QL_FMT_W2, QL_FMT_W4, QL_FMT_W8, QL_FMT_LUT4)
 _F16, _F32 = torch.float16, torch.float32
+_MAX_ROWS = 1 << 24  # of a fused call
 # (the handle alone, without a Stream object around it, where torch offers that)
 _current_stream = getattr(torch._C, "_cuda_getCurrentRawStream",
                           lambda index: torch.cuda.current_stream(index).cuda_stream)
@@ -69,9 +70,12 @@ class _FusedWorkspace:
     """What the fused entries (bias / activation / residual, gated, backward) of a layer share:
     argument checks and the workspace.
 
-    The workspace is one zero-filled buffer, grown by ``reserve`` as more rows are asked for;
-    buffers that were outgrown stay alive with the layer, since a captured graph may still use
-    them.  Calls of one layer run one after the other, whichever host threads they come from: a
+    The workspace is one zero-filled buffer, made by ``reserve`` for the rows asked for, or by the
+    first call that needs it, then for the next power of two of rows: buffers that were outgrown
+    stay alive with the layer, since a captured graph may still use them, and lengths that rise
+    step by step must not leave one each.  All layers lay a workspace out alike, so one that is
+    large enough for the largest of a model's layers can be passed to the calls of all of them
+    that follow one another (``workspace=``), instead of one in each.  Calls of one layer run one after the other, whichever host threads they come from: a
     call's launches are enqueued under the layer's lock, and an eager call on another stream than
     the last waits for that stream's work.  Work that overlaps in time - graphs captured from
     one layer and replayed at the same time - needs a workspace of its own:
@@ -157,7 +161,10 @@ class _FusedWorkspace:
                 if status != QL_ERR_WORKSPACE:
                     _check(status, name)
                     return
-            self.reserve(rows, backward)
+            try:
+                self.reserve(max(rows, min(1 << (rows - 1).bit_length(), _MAX_ROWS)), backward)
+            except torch.OutOfMemoryError:
+                self.reserve(rows, backward)
             ws = self._fused_ws[-1]
             _check(entry(*head, ws.data_ptr(), ws.numel(), raw), name)
         finally:
