@@ -619,3 +619,45 @@ def test_growth_falls_back_to_the_rows_asked_for(monkeypatch):
     x = _t(1, 300, 384)
     ref.check(lay.linear(x), ref.linear(x.double(), w)[0], "y")
     assert len(lay._fused_ws) == 1
+
+
+def test_error_flags_of_outgrown_workspaces():
+    """A flag in a buffer that the layer has outgrown (a captured graph may use it) is reported,
+    and the arrivals beside it are cleared."""
+    lay, _ = _linear("w4", 2048, 1168, seed=64)
+    x = _t(1, 40, 2048)
+    lay.reserve(40)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        y = lay.linear(x)
+    old = lay._fused_ws[-1]
+    lay.reserve(300)
+    assert lay._fused_ws[-1] is not old
+    g.replay()
+    torch.cuda.synchronize()
+    want = y.clone()
+    words = old.view(torch.int32)
+    words[0] = 2
+    words[64:96] = 1
+    assert lay.fused_read_error() == 2
+    assert not old[256:16384].any() and lay.fused_read_error() == 0
+    g.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(y, want)
+
+
+def test_error_flags_wait_for_other_streams():
+    """The flags are those of every call that was made, also of one that still runs on a stream
+    that nobody waited for."""
+    lay, _ = _linear("w4", 1024, 1168, seed=65)
+    x = _t(1, 20, 1024)
+    lay.linear(x)
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    ql.qlinear_debug_wait_test(2000, 20000, 0)
+    try:
+        lay.linear(x, stream=s)  # gives up after 2 ms, done after 20
+    finally:
+        ql.qlinear_debug_wait_test()
+    assert lay.fused_read_error() != 0
+    assert lay.fused_read_error() == 0

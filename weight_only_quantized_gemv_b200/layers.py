@@ -195,18 +195,22 @@ class _FusedWorkspace:
             return method(*args, **kw)
 
     def fused_read_error(self, workspace=None, stream=None) -> int:
-        """Sticky error flags of the calls that used the workspace (then cleared); 0 = every
-        device wait completed.  After a flag the workspace is zero-filled again: a call that
-        gave up leaves arrivals in its counters."""
-        if workspace is None:
-            if not self._fused_ws:
-                return 0
-            workspace = self._fused_ws[-1]
-        with torch.cuda.device(workspace.device):
-            flags = qlinear_read_error(workspace, stream)
-            if flags:
-                workspace.zero_()
-                torch.cuda.synchronize()
+        """Sticky error flags of the calls that used the workspace (then cleared), or without
+        one any of the layer's own, outgrown buffers included; 0 = every device wait completed.
+        The device is synchronized first, whichever streams the calls ran on; `stream` carries
+        the reading.  After a flag the workspace is zero-filled again: a call that gave up
+        leaves arrivals in its counters."""
+        with self._fused_lock:
+            buffers = self._fused_ws if workspace is None else (workspace,)
+            flags = 0
+            for ws in buffers:
+                with torch.cuda.device(ws.device):
+                    torch.cuda.synchronize()
+                    found = qlinear_read_error(ws, stream)
+                    if found:
+                        ws.zero_()
+                        torch.cuda.synchronize()
+                    flags |= found
             return flags
 
 
