@@ -661,3 +661,37 @@ def test_error_flags_wait_for_other_streams():
         ql.qlinear_debug_wait_test()
     assert lay.fused_read_error() != 0
     assert lay.fused_read_error() == 0
+
+
+def test_tensors_that_require_a_gradient_are_refused():
+    """Autograd would drop the gradient silently; inside an autograd.Function, or under no_grad,
+    the calls run."""
+    lay, w = _linear("w4", 384, 208)
+    gat, _, _ = _gated("w4", 384, 208)
+    x, dy = _t(1, 4, 384), _t(2, 4, 208)
+    gu = _t(3, 4, 2, 208)
+    want = lay.linear(x)
+    for bad in (x, dy, gu):
+        bad.requires_grad_(True)
+    for call in (lambda: lay.linear(x), lambda: lay.linear(x.detach(), residual=dy),
+                 lambda: lay.linear(x * 1), lambda: gat.forward(x),
+                 lambda: lay.linear_backward(dy), lambda: gat.backward(dy.detach(), gu)):
+        with pytest.raises(ValueError, match="requires a gradient"):
+            call()
+    with torch.no_grad():
+        assert torch.equal(lay.linear(x), want)
+        assert torch.equal(gat.backward(dy, gu), gat.backward(dy.detach(), gu.detach()))
+
+    class Linear(torch.autograd.Function):
+        @staticmethod
+        def forward(ctx, x):
+            return lay.linear(x)
+
+        @staticmethod
+        def backward(ctx, dy):
+            return lay.linear_backward(dy.contiguous())
+
+    y = Linear.apply(x)
+    assert torch.equal(y, want)
+    y.backward(dy.detach())
+    ref.check(x.grad, ref.linear_backward(dy.detach().double(), None, w, "none")[0], "dx")

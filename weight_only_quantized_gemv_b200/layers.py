@@ -55,9 +55,13 @@ def _as_stream(stream, index: int) -> torch.cuda.Stream:
 
 def _fused_ptr(t, shape: tuple, index: int, name: str, dtype=_F16) -> Optional[int]:
     """The data pointer of `t` once checked (None for None): `shape`, `dtype`, contiguous, on
-    CUDA device `index`."""
+    CUDA device `index`, and nothing that autograd would have to follow."""
     if t is None:
         return None
+    if t.requires_grad and torch.is_grad_enabled():
+        raise ValueError(f"{name} requires a gradient, which autograd does not carry through the "
+                         "fused layers: call them under torch.no_grad() (as inside an "
+                         "autograd.Function) and their backward methods for the gradient")
     if (t.dtype is not dtype or t.shape != shape or not t.is_contiguous()
             or t.get_device() != index):
         raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {shape} on "
@@ -363,7 +367,8 @@ class QuantLinear(_FusedWorkspace):
                workspace: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
         """y[M, N] = act(x[M, K] . W + bias[N]) + residual[M, N] in one kernel, for any M.  act:
         "none", "relu", "gelu", "gelu_tanh" or "silu".  z ([M, N] fp16), when given, receives
-        x . W + bias for ``linear_backward``.  y may be the residual itself."""
+        x . W + bias for ``linear_backward``.  y may be the residual itself.  Autograd does not
+        see the call: tensors that require a gradient are refused where it records."""
         fmt, N, K, index = self._fused or self._fused_setup()
         if torch.cuda.current_device() != index:
             return self._fused_elsewhere(self.linear, x, bias, residual, act, y, z, workspace,
