@@ -695,3 +695,56 @@ def test_tensors_that_require_a_gradient_are_refused():
     assert torch.equal(y, want)
     y.backward(dy.detach())
     ref.check(x.grad, ref.linear_backward(dy.detach().double(), None, w, "none")[0], "dx")
+
+
+@pytest.mark.parametrize("M", [1, 33, 260])
+def test_feed_forward_block_with_biases(M):
+    """Biases, their gradients, outputs of the caller's and one workspace for the whole block."""
+    K, F = 512, 1152
+    gate_up, wg, wu = _gated("w4", K, F)
+    down, wd = _linear("w8", F, K, seed=9)
+    mlp = layers.GatedMLP(gate_up, down)
+    ws = mlp.new_workspace(M)
+    x, dy = _t(1, M, K), _t(2, M, K, std=0.25)
+    bias, down_bias = _t(3, 2, F, std=0.3), _t(4, K, std=0.3)
+    gu = torch.empty((M, 2, F), dtype=torch.float16, device=DEV)
+    y, dx = torch.empty_like(x), torch.empty_like(x)
+    db = torch.empty((2, F), dtype=torch.float32, device=DEV)
+    ddb = torch.empty(K, dtype=torch.float32, device=DEV)
+    assert mlp.forward(x, residual=x, gu=gu, bias=bias, down_bias=down_bias, y=y,
+                       workspace=ws) is y
+    assert mlp.backward(dy, gu, dx=dx, dbias=db, ddown_bias=ddb, workspace=ws) is dx
+    xd, bd, dd = (t.double().requires_grad_(True) for t in (x, bias, down_bias))
+    want = (ref.act("silu", xd @ wg + bd[0]) * (xd @ wu + bd[1])) @ wd + dd + x.double()
+    grads = torch.autograd.grad(want, (xd, bd, dd), dy.double())
+    for got, exp in ((y, want.detach()), (dx, grads[0]), (db, grads[1]), (ddb, grads[2])):
+        assert float((got.double() - exp).norm()) <= 3 * ref.REL * float(exp.norm())
+    assert ql.qlinear_read_error(ws) == 0
+
+
+def test_feed_forward_blocks_replayed_at_once():
+    """Two graphs of one block, each with a workspace of its own, replayed at the same time."""
+    M, K, F = 100, 512, 1152
+    mlp = layers.GatedMLP(_gated("w4", K, F)[0], _linear("w8", F, K, seed=9)[0])
+    x, dy = _t(1, M, K), _t(2, M, K, std=0.25)
+    gu = torch.empty((M, 2, F), dtype=torch.float16, device=DEV)
+    want_y, want_dx = mlp.forward(x, gu=gu), mlp.backward(dy, gu)
+    graphs = []
+    for _ in range(2):
+        ws, g = mlp.new_workspace(M), torch.cuda.CUDAGraph()
+        kept = torch.empty_like(gu)
+        with torch.cuda.graph(g):
+            y = mlp.forward(x, gu=kept, workspace=ws)
+            dx = mlp.backward(dy, kept, workspace=ws)
+        graphs.append((g, y, dx, ws, kept))
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    for _ in range(10):
+        for (g, y, dx, *_), s in zip(graphs, streams):
+            y.zero_(), dx.zero_()
+        torch.cuda.synchronize()
+        for (g, *_), s in zip(graphs, streams):
+            with torch.cuda.stream(s):
+                g.replay()
+        torch.cuda.synchronize()
+        for _, y, dx, *_ in graphs:
+            assert torch.equal(y, want_y) and torch.equal(dx, want_dx)

@@ -496,8 +496,10 @@ class GatedLinear(_FusedWorkspace):
 
 
 class GatedMLP:
-    """A gated feed-forward block: y = (act(x Wg) * (x Wu)) Wd + residual, two kernels forward;
-    backward through the frozen weights from the kept gate and up values."""
+    """A gated feed-forward block: y = (act(x Wg + bias[0]) * (x Wu + bias[1])) Wd + down_bias +
+    residual, two kernels forward; backward through the frozen weights from the kept gate and up
+    values.  Both products of a call may share one workspace (``new_workspace``), which graphs
+    that are replayed at the same time need one each of."""
 
     def __init__(self, gate_up: GatedLinear, down: QuantLinear, act: str = "silu"):
         if gate_up.F != down.K or gate_up.K != down.N:
@@ -508,15 +510,32 @@ class GatedMLP:
         self.gate_up.reserve(rows, backward)
         self.down.reserve(rows, backward)
 
-    def forward(self, x: torch.Tensor, residual: Optional[torch.Tensor] = None,
-                gu: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
-        h = self.gate_up.forward(x, act=self.act, gu=gu, stream=stream)
-        return self.down.linear(h, residual=residual, stream=stream)
+    def new_workspace(self, rows: int, backward: bool = True) -> torch.Tensor:
+        """A zero-filled workspace for calls of up to `rows` rows."""
+        return max((lay.new_workspace(rows, backward) for lay in (self.gate_up, self.down)),
+                   key=lambda ws: ws.numel())
 
-    def backward(self, dy: torch.Tensor, gu: torch.Tensor, stream=None) -> torch.Tensor:
-        """dx from dy and the gu that ``forward`` kept (the residual's gradient is dy)."""
-        dh = self.down.linear_backward(dy, stream=stream)
-        return self.gate_up.backward(dh, gu, act=self.act, stream=stream)
+    def forward(self, x: torch.Tensor, residual: Optional[torch.Tensor] = None,
+                gu: Optional[torch.Tensor] = None, stream=None,
+                bias: Optional[torch.Tensor] = None, down_bias: Optional[torch.Tensor] = None,
+                y: Optional[torch.Tensor] = None,
+                workspace: Optional[torch.Tensor] = None) -> torch.Tensor:
+        """y[M, N] from x[M, K]; bias [2, F] and down_bias [N]; gu ([M, 2, F] fp16), when given,
+        is kept for ``backward``.  y may be the residual itself."""
+        h = self.gate_up.forward(x, bias=bias, act=self.act, gu=gu, workspace=workspace,
+                                 stream=stream)
+        return self.down.linear(h, bias=down_bias, residual=residual, y=y, workspace=workspace,
+                                stream=stream)
+
+    def backward(self, dy: torch.Tensor, gu: torch.Tensor, stream=None,
+                 dx: Optional[torch.Tensor] = None, dbias: Optional[torch.Tensor] = None,
+                 ddown_bias: Optional[torch.Tensor] = None,
+                 workspace: Optional[torch.Tensor] = None) -> torch.Tensor:
+        """dx from dy and the gu that ``forward`` kept (the residual's gradient is dy); dbias
+        (fp32 [2, F]) and ddown_bias (fp32 [N]), when given, receive the biases' gradients."""
+        dh = self.down.linear_backward(dy, dbias=ddown_bias, workspace=workspace, stream=stream)
+        return self.gate_up.backward(dh, gu, act=self.act, dx=dx, dbias=dbias,
+                                     workspace=workspace, stream=stream)
 
 
 def from_uniform(layer, device="cuda", max_m: int = 16) -> QuantLinear:
