@@ -748,3 +748,29 @@ def test_feed_forward_blocks_replayed_at_once():
         torch.cuda.synchronize()
         for _, y, dx, *_ in graphs:
             assert torch.equal(y, want_y) and torch.equal(dx, want_dx)
+
+
+@pytest.mark.parametrize("M", [1, 9, 40])
+def test_shapes_beyond_the_gemv(M, monkeypatch):
+    """More units times CTAs than the GEMV's 32-bit counts hold (a grid capped at its units gets
+    there with a small layer): the tensor-core product takes over, at any M."""
+    K, N = 92800, 8192  # 725 x 64 units
+    monkeypatch.setenv("QLINEAR_MAX_CTAS", "1000000")
+    rows = 64
+    assert (K // 128) * (N // 128) * min(1000000, (K // 128) * (N // 128)) >= 2 ** 31
+    nbytes = ql.qlinear_fused_workspace_bytes(2, rows, N, K, False)
+    assert nbytes > 0
+    ws = torch.zeros(nbytes, dtype=torch.uint8, device=DEV)
+    q = torch.full((K * N // 4,), 0b01010101, dtype=torch.uint8, device=DEV)  # every code 1
+    p0 = torch.full((K // 128 * N,), 0.5, dtype=torch.float16, device=DEV)
+    p1 = torch.zeros(K // 128 * N, dtype=torch.float16, device=DEV)
+    x = torch.zeros((M, K), dtype=torch.float16, device=DEV)
+    x[:, ::29] = torch.arange(1, M + 1, device=DEV).half().unsqueeze(1) / 64
+    y = torch.empty((M, N), dtype=torch.float16, device=DEV)
+    ql.qlinear_linear(2, x, q, p0, p1, y, M, N, K, ws)
+    assert torch.equal(y, (x.double().sum(1) / 2).half().unsqueeze(1).expand(M, N))
+    h = torch.empty((M, N // 2), dtype=torch.float16, device=DEV)
+    ql.qlinear_gated(2, x / 64, q, p0, p1, h, M, N // 2, K, ws, act="relu")
+    want = (x.double().sum(1) / 128) ** 2
+    assert torch.equal(h, want.half().unsqueeze(1).expand(M, N // 2))
+    assert ql.qlinear_read_error(ws) == 0

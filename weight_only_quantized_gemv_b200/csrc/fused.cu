@@ -418,7 +418,7 @@ size_t backward_partial_bytes(int M, int N) {
   return qfused::align_up(a > b ? a : b, 256);
 }
 
-// Runs a forward product: the GEMV up to 16 rows, the tensor-core product above.
+// Runs a forward product: the GEMV up to 16 rows if it has a plan, else the tensor-core product.
 ql_status forward(qfused::Product& p, void* workspace, size_t workspace_bytes) {
   const size_t off = qfused::partial_offset(p.N);
   if (!workspace || workspace_bytes < off) return QL_ERR_WORKSPACE;
@@ -426,10 +426,14 @@ ql_status forward(qfused::Product& p, void* workspace, size_t workspace_bytes) {
   p.partial_bytes = workspace_bytes - off;
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   p.err = static_cast<uint32_t*>(workspace);
-  p.counters = reinterpret_cast<uint32_t*>(
-      ws + (p.M <= kGemvRows ? qfused::kVecCounterOffset : qfused::kErrBytes));
   p.partials = reinterpret_cast<float*>(ws + off);
-  return p.M <= kGemvRows ? qfused::launch_gemv(p) : qfused::launch_tc(p);
+  if (p.M <= kGemvRows) {
+    p.counters = reinterpret_cast<uint32_t*>(ws + qfused::kVecCounterOffset);
+    const ql_status s = qfused::launch_gemv(p);
+    if (s != QL_ERR_SHAPE) return s;
+  }
+  p.counters = reinterpret_cast<uint32_t*>(ws + qfused::kErrBytes);
+  return qfused::launch_tc(p);
 }
 
 template <class Params>
@@ -509,8 +513,8 @@ extern "C" size_t qlinear_fused_workspace_bytes(int fmt, int M, int N, int K, in
   size_t part = 0;
   for (int m = 1; m <= M && m <= kGemvRows; ++m)
     for (int gated = 0; gated < (N % (2 * kTileN) ? 1 : 2); ++gated) {
-      const size_t b = qfused::gemv_partial_bytes(fmt, m, N, K, gated != 0);
-      if (!b) return 0;
+      size_t b;
+      if (qfused::gemv_partial_bytes(fmt, m, N, K, gated != 0, &b) != QL_OK) return 0;
       if (b > part) part = b;
     }
   if (qfused::tc_partial_bytes(M) > part) part = qfused::tc_partial_bytes(M);

@@ -67,8 +67,9 @@ struct WaitTest {
 };
 WaitTest wait_test();
 
-// GEMV with an epilogue (qlinear.cu), M <= 16
+// GEMV with an epilogue (qlinear.cu), M <= 16.  QL_ERR_SHAPE and 0 bytes: it has no plan for the
+// shape (its unit arithmetic is 32-bit), which then is the tensor-core product's.
 ql_status launch_gemv(const Product& p);
-size_t gemv_partial_bytes(int fmt, int M, int N, int K, bool gated);  // 0: no plan
+ql_status gemv_partial_bytes(int fmt, int M, int N, int K, bool gated, size_t* bytes);
 
 }  // namespace qfused

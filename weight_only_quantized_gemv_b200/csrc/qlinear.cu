@@ -192,6 +192,8 @@ cudaError_t prepare_kernel(const KernelInfo& k, int dev, int* ctas) {
   return cudaSuccess;
 }
 
+constexpr cudaError_t kNoPlan = cudaErrorNotSupported;  // more units than the kernel counts
+
 cudaError_t make_plan(int fmt, int M, int N, int K, bool outl, Plan* p, int ns = 1, int epi = 0) {
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
@@ -261,7 +263,7 @@ cudaError_t make_plan(int fmt, int M, int N, int K, bool outl, Plan* p, int ns =
   }
   if (C > p->U) C = p->U;
   // the kernel's stream-K index arithmetic is 32-bit
-  if (p->U * C >= (1LL << 31)) return cudaErrorInvalidValue;
+  if (p->U * C >= (1LL << 31)) return kNoPlan;
   p->C = (int)C;
   // W4 at 2 <= M <= 8: a CTA with few units shares each unit among more warps, which
   // shortens the one unit a warp would otherwise work through alone.  The M = 1 kernel
@@ -578,16 +580,21 @@ qfused::WaitTest qfused::wait_test() {
                   g_test_us.load(std::memory_order_relaxed)};
 }
 
-size_t qfused::gemv_partial_bytes(int fmt, int M, int N, int K, bool gated) {
+ql_status qfused::gemv_partial_bytes(int fmt, int M, int N, int K, bool gated, size_t* bytes) {
   Plan p;
-  if (make_plan(fmt, M, N, K, false, &p, 1, gated ? 2 : 1) != cudaSuccess) return 0;
-  return p.ws_bytes - p.partial_offset;
+  *bytes = 0;
+  const cudaError_t e = make_plan(fmt, M, N, K, false, &p, 1, gated ? 2 : 1);
+  if (e == kNoPlan) return QL_OK;
+  if (e != cudaSuccess) return QL_ERR_CUDA;
+  *bytes = p.ws_bytes - p.partial_offset;
+  return QL_OK;
 }
 
 ql_status qfused::launch_gemv(const Product& q) {
   Plan p;
-  if (make_plan(q.fmt, q.M, q.N, q.K, false, &p, 1, q.epi.gated ? 2 : 1) != cudaSuccess)
-    return QL_ERR_CUDA;
+  const cudaError_t e = make_plan(q.fmt, q.M, q.N, q.K, false, &p, 1, q.epi.gated ? 2 : 1);
+  if (e == kNoPlan) return QL_ERR_SHAPE;
+  if (e != cudaSuccess) return QL_ERR_CUDA;
   if (q.partial_bytes < p.ws_bytes - p.partial_offset) return QL_ERR_WORKSPACE;
   Call c{q.fmt, false, q.x, q.packed, q.p0, q.p1, nullptr, nullptr, nullptr, q.epi.y,
          q.M, q.N, q.K, nullptr, 0, q.stream};
