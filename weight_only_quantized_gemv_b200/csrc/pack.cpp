@@ -46,14 +46,11 @@ struct Columns {
   const void* a;
   const void* b;  // null: a alone
   int width;
-  const void* source(int n, int* col) const {
-    if (!b) {
-      *col = n;
-      return a;
-    }
-    const int tile = n / kTileN;
-    *col = (tile >> 1) * kTileN + n % kTileN;
-    return (tile & 1) ? b : a;
+  // The array a packed tile comes from, and its first column there.  (Asked once a tile; asked for
+  // every weight it made packing 1.4 to 3 times slower.)
+  const void* source(int tile, int* col) const {
+    *col = (b ? tile >> 1 : tile) * kTileN;
+    return (b && (tile & 1)) ? b : a;
   }
 };
 
@@ -69,7 +66,8 @@ void pack_codes(int fmt, const Columns& c, void* packed, int N, int K) {
     for (int g = 0; g < G; ++g) {
       for (int jj = 0; jj < tb; ++jj) {
         uint32_t* chunk = out + chunk_index(b, g, jj, G, ntiles) * 32 * WL;
-        const int n_base = (b * kBlockTiles + jj) * kTileN;
+        int col;
+        const void* src = c.source(b * kBlockTiles + jj, &col);
         for (int lane = 0; lane < 32; ++lane) {
           const int gi = lane >> 2, t = lane & 3;
           uint32_t words[16] = {0};
@@ -77,11 +75,8 @@ void pack_codes(int fmt, const Columns& c, void* packed, int N, int K) {
             for (int dk = 0; dk < 4; ++dk)
               for (int r8 = 0; r8 <= 8; r8 += 8) {
                 const int k = g * kGroup + k_in_group(s, t, dk);
-                const int n = n_base + gi + r8;
                 int wi, bit;
-                int col;
-                const void* src = c.source(n, &col);
-                const uint32_t q = canonical_code(fmt, src, c.width, k, col);
+                const uint32_t q = canonical_code(fmt, src, c.width, k, col + gi + r8);
                 if (fmt == kW3) {  // low two bits as a W2 code, high bit in its own plane
                   code_position(kW2, s, dk, r8, &wi, &bit);
                   words[wi] |= (q & 3u) << bit;
@@ -108,11 +103,11 @@ void pack_param_array(int fmt, const Columns& c, void* packed, int N, int K) {
     for (int g = 0; g < G; ++g)
       for (int jj = 0; jj < tb; ++jj) {
         const long long ch = chunk_index(b, g, jj, G, ntiles);
-        const int n_base = (b * kBlockTiles + jj) * kTileN;
+        int col;
+        const void* canonical = c.source(b * kBlockTiles + jj, &col);
         for (int gi = 0; gi < 8; ++gi)
           for (int h = 0; h < 2; ++h) {
-            int n;
-            const void* canonical = c.source(n_base + gi + 8 * h, &n);
+            const int n = col + gi + 8 * h;
             if (fmt == kLUT4) {
               const float* a = static_cast<const float*>(canonical);
               float* o = static_cast<float*>(packed);
