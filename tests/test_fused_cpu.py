@@ -128,3 +128,18 @@ def test_workspace_query_refuses_bad_arguments():
 def test_unknown_activation_name():
     with pytest.raises(ql.QLinearError):
         ql._act("swish")
+
+
+def test_short_tables_are_refused():
+    """The kernels read 16 entries of a LUT4 table, whatever it holds."""
+    pytest.importorskip("torch")
+    from synth import gen
+    from weight_only_quantized_gemv_b200 import layers
+    lt = gen.lut4_layer(1, 128, 16)
+    good, bad = (lt.qbytes, lt.lut, lt.absmax), (lt.qbytes, lt.lut[:8], lt.absmax)
+    for args in ((bad, bad), (good, bad), (bad, good)):
+        with pytest.raises(ValueError, match="16 entries"):
+            layers.GatedLinear(ql.QL_FMT_LUT4, 128, 16, *args, device="cpu")
+    assert layers.GatedLinear(ql.QL_FMT_LUT4, 128, 16, good, good, device="cpu").p0.numel() == 16
+    with pytest.raises(ValueError, match="16 entries"):
+        layers.QuantLinear(ql.QL_FMT_LUT4, 128, 16, *bad, device="cpu")

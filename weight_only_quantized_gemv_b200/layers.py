@@ -34,6 +34,14 @@ def _dev(a: np.ndarray, device) -> torch.Tensor:
     return torch.from_numpy(np.ascontiguousarray(a)).to(device)
 
 
+def _lut16(table) -> np.ndarray:
+    """A LUT4 table as fp16; the kernels read 16 entries."""
+    table = np.asarray(table, dtype=np.float16)
+    if table.size < 16:
+        raise ValueError(f"a LUT4 table has 16 entries, not {table.size}")
+    return table
+
+
 _FUSED_FORMATS = (QL_FMT_W2, QL_FMT_W4, QL_FMT_W8, QL_FMT_LUT4)
 _F16, _F32 = torch.float16, torch.float32
 _MAX_ROWS = 1 << 24  # of a fused call
@@ -231,7 +239,7 @@ class QuantLinear(_FusedWorkspace):
         packed = qlinear_pack(fmt, canonical_codes, N, K)
         self.qweight = _dev(packed, self.device)
         if fmt == QL_FMT_LUT4:
-            self.p0 = _dev(np.asarray(p0, dtype=np.float16).view(np.uint16), self.device)  # lut16
+            self.p0 = _dev(_lut16(p0).view(np.uint16), self.device)
             self.p1 = _dev(qlinear_pack_params(fmt, np.asarray(p1, dtype=np.float32), N, K),
                            self.device)  # absmax
         elif group != 128:
@@ -436,7 +444,7 @@ class GatedLinear(_FusedWorkspace):
         self._fused_lock = threading.RLock()
         self.qweight = _dev(qlinear_pack_gated(fmt, gate[0], up[0], F, K), self.device)
         if fmt == QL_FMT_LUT4:
-            tables = [np.asarray(m[1], dtype=np.float16) for m in (gate, up)]
+            tables = [_lut16(m[1]) for m in (gate, up)]
             if not np.array_equal(*tables):
                 raise ValueError("gate and up share one LUT4 table")
             self.p0 = _dev(tables[0].view(np.uint16), self.device)
