@@ -158,3 +158,21 @@ def test_not_finite_gradients_stay_in_their_row(bad):
     keep = [m for m in range(M) if m != 9]
     assert torch.equal(dx[keep], clean[keep])
     assert not torch.isfinite(dx[9]).all()
+
+
+@pytest.mark.parametrize("db", [False, True])
+def test_infinities_without_a_gradient(db):
+    """ReLU at g = -infinity (an overflown gate) passes nothing on; the row's other elements, beyond
+    fp16 or far below 1, keep their scaling."""
+    K, F, M = 256, 208, 40
+    for power, std in ((-6, 100.0), (6, 2.0 ** -20)):
+        lay, wg, wu = _gated(K, F, power)
+        dh, gu = _t(13, M, F, std=std), _t(14, M, 2, F)
+        gu[:, 1] *= 700 if std > 1 else 2.0 ** -4
+        clean = gu.clone()
+        clean[:, 0, 5::16] = -1.0
+        gu[:, 0, 5::16] = float("-inf")
+        _gated_case(lay, wg, wu, dh, clean, "relu")
+        sums = torch.empty((2, F), dtype=torch.float32, device=DEV) if db else None
+        got = lay.backward(dh, gu, act="relu", dbias=sums)
+        assert torch.equal(got, lay.backward(dh, clean, act="relu"))

@@ -43,6 +43,7 @@ bool shape_ok(int M, int N, int K) {
 // the factors (kFactor), and a second one with blocks of its own shape, whose columns' sums it
 // keeps, writes dz.  All are bound by memory, or GELU's arithmetic.
 constexpr int kDzThreads = 512;
+constexpr float kLargest = 3.402823466e38f;
 enum { kFactor, kStore };
 
 struct DzParams {
@@ -172,7 +173,8 @@ __device__ __forceinline__ void gradients8(int act, bool has_z, const Inputs8<GA
 }
 
 // The size that a row's factor goes by, over eight columns: |dy|, or (gated) |dh| max(|g|, |u|).
-// (fmaxf drops NaN.)
+// Without NaN (fmaxf drops it) and infinities: most make the row's dx not finite, but ReLU has no
+// gradient at g = -infinity, and the rest of the row keeps its factor.
 template <bool GATED>
 __device__ __forceinline__ float size8(const Inputs8<GATED>& in) {
   float d[8], top = 0.f;
@@ -186,6 +188,11 @@ __device__ __forceinline__ float size8(const Inputs8<GATED>& in) {
   }
 #pragma unroll
   for (int e = 0; e < 8; ++e) top = fmaxf(top, fabsf(d[e]));
+  if (top > kLargest) {
+    top = 0.f;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) top = fabsf(d[e]) <= kLargest ? fmaxf(top, fabsf(d[e])) : top;
+  }
   return top;
 }
 
@@ -235,9 +242,8 @@ __global__ void __launch_bounds__(kDzThreads, 2) dz_kernel(const DzParams P) {
   if (lane == 0) red[warp] = top;
   __syncthreads();
   for (int w = 0; w < (int)(blockDim.x >> 5); ++w) top = fmaxf(top, red[w]);
-  // 2^k; a row of zeros, or with an infinity (its dx is not finite either way), stays as it is
-  int k = 0;
-  if (top > 0.f && top <= 3.402823466e38f) k = 14 - ((int)(__float_as_uint(top) >> 23) - 127);
+  // 2^k (-18 <= k <= 62: sizes are products of at most two fp16); a row of zeros stays as it is
+  const int k = top > 0.f ? 14 - ((int)(__float_as_uint(top) >> 23) - 127) : 0;
   if (threadIdx.x == 0) P.unscale[blockIdx.x] = (uint8_t)(127 - k);
   if constexpr (WHAT == kStore) {
     const float scale = __uint_as_float((uint32_t)(127 + k) << 23);
