@@ -30,10 +30,11 @@
 // runs of stages (schedule), whose partial sums meet in the workspace: the last contributor
 // to arrive adds them in worker order, nobody waits.
 //
-// Measured, W4: 8192 x 8192 with 512 tokens 54 us (1.27 PFLOP/s; the tensor pipe is busy for 76 %
+// Measured, W4: 8192 x 8192 with 512 tokens 55 us (1.25 PFLOP/s; the tensor pipe is busy for 76 %
 // of the cycles in which an SM has work), 8192 x 18944 with 32 tokens 37 us against 13 us for its
-// bytes (decoding: 56 % of the issue slots, the tensor pipe 35 %), 8192 x 28672 with 2048 tokens,
-// GELU, bias, residual and the pre-activation kept 843 us (1.14 PFLOP/s, at the power limit).
+// bytes (decoding: 57 % of the issue slots, the tensor pipe 35 %), 8192 x 28672 with 2048 tokens
+// 662 us (1.45 PFLOP/s) in a run of 20 calls; with GELU, bias, residual and the pre-activation kept
+// 762 us in such a run, 876 us (1.10 PFLOP/s) call after call for seconds, at the power limit.
 //
 // The weights and, backward, dz (its rows scaled, fused.cu) are rounded to fp16 once: the operand
 // type of kind::f16.  That adds about one rounding each to the output's own (2.1e-4 in the relative
@@ -560,9 +561,10 @@ __device__ __forceinline__ uint32_t arrive_weight(uint32_t* counter, uint32_t we
 // A stage of the pair's other CTA is complete: arrive on the leader's barrier.  The default scope
 // (the CTA) orders nothing between the two CTAs in the memory model, so this is what it rests on:
 // no thread of the leader reads what the arrival stands for.  A pair's MMA takes each half of
-// its operands from the shared memory of the SM that holds it, where the decoding warps' proxy
-// fence, complete before the arrival is issued, has made their stores visible to that SM's tensor
-// core; the arrival only says when.  (Copied tokens complete on the leader's barrier themselves.)
+// its operands from the shared memory of the SM that holds it, which has no copy elsewhere: the
+// decoding warps' stores are there, and visible to that SM's tensor core, once their proxy fence
+// has completed, and the arrival, a release for the CTA, is issued after it.  It only says when.
+// (Copied tokens complete on the leader's barrier themselves.)
 // A release at cluster scope takes longer than the ring of three stages hides, even when a warp of
 // its own passes a stage on for all eight: 512 x 8192 x 8192 78 against 60 us (at the default scope
 // that way 61), 2048 x 28672 x 8192 1010 against 750, timed in turn.
@@ -1230,7 +1232,8 @@ ql_status launch_fmt(const qfused::Product& p) {
   if constexpr (!BWD) {
     // Per 256 tokens a stage takes about 1100 cycles, the epilogue of one warp per quadrant
     // 48000, and 32000 more for each array beside the output: with two warps 2048 x 28672 x 8192
-    // with the pre-activation kept takes 785 against 1007 us, without it 800 against 763.
+    // with GELU and the pre-activation kept takes 785 against 952 us, without it 824 against 787
+    // (30 calls each in turn); gated 513 x 28672 x 4096 with both kept 172 against 191.
     const int arrays = (p.epi.zsave != nullptr) + (p.epi.residual != nullptr);
     if (p.K / kGroup < 44 + 30 * arrays) return launch_as<256, FMT, true, BWD, 2>(p, tk);
   }
