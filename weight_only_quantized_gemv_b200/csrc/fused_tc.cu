@@ -1207,7 +1207,7 @@ ql_status launch_as(const qfused::Product& p, const Tokens& tk) {
   P.whole = sc.whole;
   P.runners = sc.runners;
   const qfused::WaitTest wt = qfused::wait_test();
-  P.wait_us = wt.limit_us + 4u * (uint32_t)P.steps;
+  P.wait_us = (wt.limit_us < 1000000000u ? wt.limit_us : 1000000000u) + 4u * (uint32_t)P.steps;
   P.test_us = wt.delays;
   if ((size_t)(P.tiles - P.whole) * ctas * 4 * sizeof(uint32_t) > qfused::kTcCounterBytes)
     return QL_ERR_UNSUPPORTED;  // more than five hundred SMs
