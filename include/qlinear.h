@@ -175,9 +175,10 @@ ql_status qlinear_read_error(void* workspace, uint32_t* flags, ql_stream_t strea
  * epilogue, or with qlinear_linear's) run as instances compiled with these hooks (the other
  * GEMV kernels keep their fixed 2^22-round limit and no hooks).  The tensor-core products of
  * the fused layers read wait_limit as microseconds (0: 100000; each of a tile's 128-wide
- * stages adds 4), after which a call sets the same flags (2 also for an accumulator), gives up and leaves its outputs undefined; their
- * first worker's copies of the activations come late by producer_delay_us, its first MMA by
- * consumer_hold_us.  Not thread-safe with respect to concurrent calls' settings. */
+ * stages adds 4), after which a call sets the same flags (2 also for an accumulator), gives up
+ * and leaves its outputs undefined; their first worker's copies of the activations come late by
+ * producer_delay_us, its first MMA by consumer_hold_us.  Not thread-safe with respect to
+ * concurrent calls' settings. */
 ql_status qlinear_debug_wait_test(uint32_t wait_limit, uint32_t producer_delay_us,
                                   uint32_t consumer_hold_us);
 
@@ -456,7 +457,8 @@ ql_status qlinear_matmul(int fmt, const uint16_t* x, const void* packed, const v
  * products, the tensor cores multiply fp16 weights (those of qlinear_dequant_fp16) and the
  * gradients dz rounded to fp16 after each row was scaled by a power of two that is taken back
  * in fp32 (so dz keeps 11 bits whatever its size, down to 2^-28 of its row's largest |dy|, or
- * |dh u| and |dh g|); at M <= 16 the forward products use the GEMV's exact codes.  Results are reproducible bit for bit.
+ * |dh u| and |dh g|); at M <= 16 the forward products use the GEMV's exact codes.  Results are
+ * reproducible bit for bit.
  *
  * Arguments common to the four entries (device pointers, rows contiguous):
  *   packed, p0, p1 : as for qlinear_prefill_fused, packed 32-byte aligned; the gated entries

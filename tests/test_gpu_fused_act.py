@@ -1,12 +1,13 @@
-"""The activations of the fused layers over every fp16 argument up to 16 in size, on the GPU, against
-fp64: x = 0 and the argument as the bias, so that the pre-activation is exact and only the
+"""The activations of the fused layers over every fp16 argument up to 16 in size, on the GPU,
+against fp64: x = 0 and the argument as the bias, so that the pre-activation is exact and only the
 activation's fp32 evaluation and the output's rounding are seen.
 
 Bound of a value: half an fp16 step, u |y| (u = 2^-11) or 2^-25 below 2^-14, and EVAL |y| for the
 evaluation.  EVAL: each value is a product z s (u) of a sigmoid or normal CDF s, whose relative
 error is
-  * that of its exponential, e^-a for |a| <= 30 (beyond it no output is larger than 2^-25): 2 + 1.173 a ulp
-    of 2^-23 (4.4e-6) and a's own rounding, five of 2^-24 for tanh-GELU's cubic (9e-6);
+  * that of its exponential, e^-a for |a| <= 30 (beyond it no output is larger than 2^-25):
+    2 + 1.173 a ulp of 2^-23 (4.4e-6) and a's own rounding, five of 2^-24 for tanh-GELU's cubic
+    (9e-6);
   * the division's 2 ulp, the polynomial's 1.5e-6 in fp32 and three products: 2e-6.
 Together below 1.6e-5 < 2^-15.
 """

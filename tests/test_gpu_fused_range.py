@@ -2,7 +2,8 @@
 GPU, against fp64.
 
 The kernels round dz to fp16 after scaling its row so that its largest |dy| (gated: |dh u|, |dh g|),
-`top`, lies in [2^14, 2^15).  Bound of an output before its own rounding, S = sum |dz||w| over the N columns:
+`top`, lies in [2^14, 2^15).  Bound of an output before its own rounding, S = sum |dz||w| over the
+N columns:
   * operands: u S for the weights, u S for dz (u = 2^-11; both with their product: 2.01 u);
     2^-25 sum |dz| for subnormal weights; 2^-25 / 2^14 of the row's top for dz elements below
     the scaled row's normal range, times sum |w|;

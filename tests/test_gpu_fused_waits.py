@@ -77,7 +77,8 @@ def test_gemv_with_epilogue_reports_a_late_copy(M):
     assert lay.fused_read_error() == 0
 
 
-@pytest.mark.parametrize("fmt,M", [("w4", 200), ("w8", 200), ("w8", 60), ("w8", 100), ("lut4", 300)])
+@pytest.mark.parametrize("fmt,M", [("w4", 200), ("w8", 200), ("w8", 60), ("w8", 100),
+                                   ("lut4", 300)])
 @pytest.mark.parametrize("backward", [False, True])
 def test_no_flag_behind_a_long_kernel(fmt, M, backward):
     """A call that starts early, on SMs that the kernel before it leaves idle, waits for that

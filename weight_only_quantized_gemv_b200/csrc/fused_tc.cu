@@ -43,9 +43,9 @@
 //
 // Every barrier wait is bounded in time (100 ms against microseconds, and 4 us more for each stage
 // of a tile, several times what one takes, since the epilogue waits for a whole tile;
-// qlinear_debug_wait_test sets another limit); one that runs out sets a flag in the workspace's error word, all roles
-// leave their loops, and the CTA waits for its own copies and MMAs, frees its tensor memory and
-// exits.
+// qlinear_debug_wait_test sets another limit); one that runs out sets a flag in the workspace's
+// error word, all roles leave their loops, and the CTA waits for its own copies and MMAs, frees its
+// tensor memory and exits.
 #include <cuda.h>
 #include <cudaTypedefs.h>
 #include <cuda_fp16.h>

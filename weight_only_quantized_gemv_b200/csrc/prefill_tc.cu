@@ -467,7 +467,8 @@ __global__ void __launch_bounds__(TcCfg<BN, FUSED, FMT, PAIR>::kThreads, 1)
       // every stage is handed back: the leader's commits also arrive on the other CTA's
       // barriers, and none of those arrivals may still be on its way when that CTA exits
       for (int i = (it > C::S ? it - C::S : 0); i < it; ++i)
-        tc_wait(empty(i % C::S), (i / C::S) & 1, abort, kErrStage, ok ? kWaitNs : kWaitNs / 10, false);
+        tc_wait(empty(i % C::S), (i / C::S) & 1, abort, kErrStage, ok ? kWaitNs : kWaitNs / 10,
+                false);
       // no copy of this CTA is still in flight when it exits: wait for the last stages filled
       // (the leader's full barriers count the bytes of both CTAs of a pair; the pair meets
       // at a cluster barrier before either exits)

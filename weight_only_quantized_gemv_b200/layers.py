@@ -87,10 +87,12 @@ class _FusedWorkspace:
     stay alive with the layer, since a captured graph may still use them, and lengths that rise
     step by step must not leave one each.  All layers lay a workspace out alike, so one that is
     large enough for the largest of a model's layers can be passed to the calls of all of them
-    that follow one another (``workspace=``), instead of one in each.  Calls of one layer run one after the other, whichever host threads they come from: a
-    call's launches are enqueued under the layer's lock, and an eager call on another stream than
-    the last waits for that stream's work.  Work that overlaps in time - graphs captured from
-    one layer and replayed at the same time - needs a workspace of its own:
+    that follow one another (``workspace=``), instead of one in each.
+
+    Calls of one layer run one after the other, whichever host threads they come from: a call's
+    launches are enqueued under the layer's lock, and an eager call on another stream than the
+    last waits for that stream's work.  Work that overlaps in time - graphs captured from one
+    layer and replayed at the same time - needs a workspace of its own:
     ``workspace=layer.new_workspace(rows)``.  Tensors a call makes are made on its stream.  A
     stream given as a raw handle must live until the layer's next call on another stream, which
     waits for it.
