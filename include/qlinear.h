@@ -527,6 +527,113 @@ ql_status qlinear_pack_params_gated(int fmt, const void* gate, const void* up, v
                                     int F, int K);
 
 /* ---------------------------------------------------------------------------
+ * 8-bit floating-point layers: both operands of a product are e4m3 codes with an fp32 scale per
+ * 128, and what makes such codes on the way there: RMS norm with the residual's addition, gated
+ * activation, plain quantization.  No page describes these entries; they are the form of the
+ * linear layers above for weights and activations in 8 bits.
+ *
+ *   codes of rows    for every 128 columns (the last block may be shorter): scale = max|v| / 448,
+ *                    q = e4m3(v / scale) to nearest even.  scales fp32 [rows][ceil(columns / 128)]
+ *   codes of weights one scale per 128 x 128 block: fp32 [ceil(N / 128)][ceil(K / 128)]
+ *   linear           y[m][n] = sum_b sx[m][b] sw[n / 128][b] sum_{k in block b} q[m][k] w[n][k]
+ *   linear_backward  dx[m][k] = sum_b sd[m][b] sw[b][k / 128] sum_{n in block b} qd[m][n] w[n][k]
+ *   grouped          the rows offsets[e] .. offsets[e + 1] - 1 by the matrix of expert e
+ *   rmsnorm          t = x + residual, rounded to the tensors' type; rstd = 1 / sqrt(mean(t^2) +
+ *                    eps); y = t rstd weight; codes of y (before y is rounded)
+ *   rmsnorm_backward dx = rstd (weight dy - t rstd^2 mean(weight dy t)) + dt;
+ *                    dweight = sum_m dy t rstd
+ *   gated            h = act(g) u, (g, u) = the halves of a row; codes of h
+ *   gated_backward   dg = dh u act'(g), du = dh act(g); codes of the row (dg, du)
+ *
+ * The quantization has the gradient of the identity, so that a product's dx is the dy of the norm
+ * (dh of the gated activation) before it, and the weights' codes are frozen.
+ *
+ * Numbers: products of codes are summed in fp32 per block of 128, the blocks' sums times their two
+ * scales in fp32; norms, sums of squares, activations and scales are fp32; every 16-bit output is
+ * rounded once, to nearest even.  Results are reproducible bit for bit.  A block of rows' codes
+ * whose largest value is below 2^-100 is coded as if that were 2^-100.  A NaN or an infinity makes
+ * its block's scale NaN or infinite and its code NaN: every output that it goes into is NaN.
+ *
+ * Arguments common to the entries (device pointers, rows contiguous unless a stride is given):
+ *   type           : a ql_type, of every 16-bit tensor of the call
+ *   16-bit tensors, codes : 16-byte aligned; fp32 and int32 arrays 4-byte aligned
+ *   ldx            : elements between the rows of x, >= K and a multiple of 8
+ *   workspace      : qlinear_fp8_workspace_bytes() (the norm's: qlinear_rmsnorm_workspace_bytes),
+ *                    256-byte aligned, zero-filled once before its first use; calls that share it
+ *                    must not overlap in time, but may be of different entries and shapes, those
+ *                    of the fused linear layers included.  qlinear_read_error reads its error word
+ *                    (1, 2: a wait ran out; 4: offsets that fall or leave 0 .. M); after a wait's
+ *                    flag, zero-fill it again.
+ * Asynchronous on `stream`; nothing is allocated.  An output may not overlap an input or another
+ * output (QL_ERR_ALIAS), but for the cases named.  Shapes: 1 <= M <= 2^24; N, K and F multiples of
+ * 16 up to 2^30 (F 2^29, the norm's K 32768); 1 <= E <= 1024 (QL_ERR_SHAPE).  Weights (codes,
+ * scales and the norm's) must not be written by work still running on the stream, unless that is
+ * qlinear_fp8_quantize_weights: they are read before earlier kernels end.
+ * ------------------------------------------------------------------------- */
+typedef enum { QL_TYPE_F16 = 0, QL_TYPE_BF16 = 1 } ql_type;
+
+/* Codes q [M][K] and scales [M][ceil(K / 128)] of x. */
+ql_status qlinear_fp8_quantize(int type, const void* x, long long ldx, uint8_t* q, float* scales,
+                               int M, int K, ql_stream_t stream);
+
+/* Codes q [E][N][K] and scales [E][ceil(N / 128)][ceil(K / 128)] of w [E][N][K]. */
+ql_status qlinear_fp8_quantize_weights(int type, const void* w, uint8_t* q, float* scales, int E,
+                                       int N, int K, ql_stream_t stream);
+
+/* Codes of h [M][F] from gu [M][2 F] (the gate's half first); act: a ql_act. */
+ql_status qlinear_fp8_gated(int type, int act, const void* gu, uint8_t* q, float* scales, int M,
+                            int F, ql_stream_t stream);
+
+/* Codes of (dg, du) [M][2 F] from dh [M][F] and the gu that the forward entry read. */
+ql_status qlinear_fp8_gated_backward(int type, int act, const void* dh, const void* gu, uint8_t* q,
+                                     float* scales, int M, int F, ql_stream_t stream);
+
+/* RMS norm of t = x (+ residual, when given).  Each output may be NULL, but not q and y both, and
+ * q and scales go together: total [M][K] receives t, y [M][K] the norm's values, q and scales their
+ * codes, rstd [M] what the backward entry needs.  total may be exactly x (ldx = K) or residual. */
+ql_status qlinear_rmsnorm(int type, const void* x, long long ldx, const void* residual,
+                          const void* weight, float eps, void* total, void* y, uint8_t* q,
+                          float* scales, float* rstd, int M, int K, ql_stream_t stream);
+
+/* dx [M][K] (the gradient of x and of the residual alike) from dy, the kept total and rstd, and
+ * dtotal, the gradient that comes to total from elsewhere, or NULL; dx may be exactly dtotal.
+ * dweight (fp32 [K], overwritten) may be NULL, the workspace (qlinear_rmsnorm_workspace_bytes)
+ * then too. */
+ql_status qlinear_rmsnorm_backward(int type, const void* dy, const void* total, const float* rstd,
+                                   const void* weight, const void* dtotal, void* dx,
+                                   float* dweight, int M, int K, void* workspace,
+                                   size_t workspace_bytes, ql_stream_t stream);
+/* For calls with these M and K on the current device; 0 for invalid arguments or no device. */
+size_t qlinear_rmsnorm_workspace_bytes(int M, int K);
+
+/* Bytes of a product's workspace for calls with at most M rows and E experts (1 for the linear
+ * entries), in both directions, on the current device; 0 for invalid arguments or no device. */
+size_t qlinear_fp8_workspace_bytes(int M, int E, int N, int K);
+
+/* y [M][N] from the codes q [M][K] and scales of x, and w [N][K]. */
+ql_status qlinear_fp8_linear(int type, const uint8_t* q, const float* scales, const uint8_t* w,
+                             const float* wscales, void* y, int M, int N, int K, void* workspace,
+                             size_t workspace_bytes, ql_stream_t stream);
+
+/* dx [M][K] from the codes q [M][N] and scales of dy. */
+ql_status qlinear_fp8_linear_backward(int type, const uint8_t* q, const float* scales,
+                                      const uint8_t* w, const float* wscales, void* dx, int M,
+                                      int N, int K, void* workspace, size_t workspace_bytes,
+                                      ql_stream_t stream);
+
+/* The same with w [E][N][K], wscales [E][ceil(N / 128)][ceil(K / 128)] and the experts' rows from
+ * offsets int32 [E + 1], in device memory: not falling, within 0 .. M.  Rows before the first and
+ * behind the last offset are neither read nor written.  Offsets that break the rule set a flag in
+ * the workspace's error word and are taken as the largest so far, at most M. */
+ql_status qlinear_fp8_grouped(int type, const uint8_t* q, const float* scales, const int* offsets,
+                              const uint8_t* w, const float* wscales, void* y, int M, int E, int N,
+                              int K, void* workspace, size_t workspace_bytes, ql_stream_t stream);
+ql_status qlinear_fp8_grouped_backward(int type, const uint8_t* q, const float* scales,
+                                       const int* offsets, const uint8_t* w, const float* wscales,
+                                       void* dx, int M, int E, int N, int K, void* workspace,
+                                       size_t workspace_bytes, ql_stream_t stream);
+
+/* ---------------------------------------------------------------------------
  * Debug entries (device pointers, asynchronous).  They decode the packed layout
  * with the same fragment-extraction code the GEMV kernels use.
  *   qlinear_debug_unpack : codes uint8 [K][N] (canonical order, one code per byte)

@@ -34,11 +34,13 @@ STATUS = {0: "QL_OK", 1: "QL_ERR_NULL", 2: "QL_ERR_SHAPE", 3: "QL_ERR_ALIGN",
           4: "QL_ERR_UNSUPPORTED", 5: "QL_ERR_WORKSPACE", 6: "QL_ERR_CUDA",
           7: "QL_ERR_LIBRARY", 8: "QL_ERR_ALIAS"}
 QL_ERR_WORKSPACE = 5
+TYPES = {"float16": 0, "bfloat16": 1}  # ql_type
 ACTS = {"none": 0, "relu": 1, "gelu": 2, "gelu_tanh": 3, "silu": 4}  # ql_act
 
 _P = ctypes.c_void_p
 _I = ctypes.c_int
 _SZ = ctypes.c_size_t
+_LL = ctypes.c_longlong
 
 
 class ql_policy_entry(ctypes.Structure):
@@ -104,6 +106,20 @@ _SIGS = {
                                     _P]),
     "qlinear_pack_gated": (_I, [_I, _P, _P, _P, _I, _I]),
     "qlinear_pack_params_gated": (_I, [_I, _P, _P, _P, _I, _I]),
+    "qlinear_fp8_quantize": (_I, [_I, _P, _LL, _P, _P, _I, _I, _P]),
+    "qlinear_fp8_quantize_weights": (_I, [_I, _P, _P, _P, _I, _I, _I, _P]),
+    "qlinear_fp8_gated": (_I, [_I, _I, _P, _P, _P, _I, _I, _P]),
+    "qlinear_fp8_gated_backward": (_I, [_I, _I, _P, _P, _P, _P, _I, _I, _P]),
+    "qlinear_rmsnorm": (_I, [_I, _P, _LL, _P, _P, ctypes.c_float, _P, _P, _P, _P, _P, _I, _I,
+                             _P]),
+    "qlinear_rmsnorm_backward": (_I, [_I, _P, _P, _P, _P, _P, _P, _P, _I, _I, _P, _SZ, _P]),
+    "qlinear_rmsnorm_workspace_bytes": (_SZ, [_I, _I]),
+    "qlinear_fp8_workspace_bytes": (_SZ, [_I, _I, _I, _I]),
+    "qlinear_fp8_linear": (_I, [_I, _P, _P, _P, _P, _P, _I, _I, _I, _P, _SZ, _P]),
+    "qlinear_fp8_linear_backward": (_I, [_I, _P, _P, _P, _P, _P, _I, _I, _I, _P, _SZ, _P]),
+    "qlinear_fp8_grouped": (_I, [_I, _P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _P, _SZ, _P]),
+    "qlinear_fp8_grouped_backward": (_I, [_I, _P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _P, _SZ,
+                                          _P]),
 }
 for _name, (_res, _args) in _SIGS.items():
     _f = getattr(_lib, _name)
@@ -542,3 +558,108 @@ def qlinear_pack_params_gated(fmt: int, gate: np.ndarray, up: np.ndarray, F: int
     _check(_lib.qlinear_pack_params_gated(fmt, _np_ptr(gate), _np_ptr(up), _np_ptr(out), F, K),
            "qlinear_pack_params_gated")
     return out
+
+
+# ---------------------------------------------------------------------------
+# 8-bit floating-point layers: e4m3 codes with a scale per 128.  type: a key of TYPES (a torch
+# dtype's name), or a ql_type value.
+
+
+def _type(type_) -> int:
+    if isinstance(type_, str):
+        if type_ not in TYPES:
+            raise QLinearError(4, f"type {type_!r}")
+        return TYPES[type_]
+    return int(type_)
+
+
+def qlinear_fp8_quantize(type_, x, q, scales, M, K, ldx=None, stream=None):
+    """Codes ``q[M, K]`` and scales ``[M, ceil(K / 128)]`` of the rows of x, ldx elements apart."""
+    _check(_lib.qlinear_fp8_quantize(_type(type_), _ptr(x), K if ldx is None else ldx, _ptr(q),
+                                     _ptr(scales), M, K, _stream(stream)), "qlinear_fp8_quantize")
+    return q
+
+
+def qlinear_fp8_quantize_weights(type_, w, q, scales, E, N, K, stream=None):
+    """Codes ``q[E, N, K]`` and scales ``[E, ceil(N / 128), ceil(K / 128)]`` of w."""
+    _check(_lib.qlinear_fp8_quantize_weights(_type(type_), _ptr(w), _ptr(q), _ptr(scales), E, N,
+                                             K, _stream(stream)), "qlinear_fp8_quantize_weights")
+    return q
+
+
+def qlinear_fp8_gated(type_, gu, q, scales, M, F, act="silu", stream=None):
+    """Codes ``q[M, F]`` and scales of ``act(g) * u``, gu[M, 2 F] = (g, u)."""
+    _check(_lib.qlinear_fp8_gated(_type(type_), _act(act), _ptr(gu), _ptr(q), _ptr(scales), M, F,
+                                  _stream(stream)), "qlinear_fp8_gated")
+    return q
+
+
+def qlinear_fp8_gated_backward(type_, dh, gu, q, scales, M, F, act="silu", stream=None):
+    """Codes ``q[M, 2 F]`` and scales of the gradients (dg, du)."""
+    _check(_lib.qlinear_fp8_gated_backward(_type(type_), _act(act), _ptr(dh), _ptr(gu), _ptr(q),
+                                           _ptr(scales), M, F, _stream(stream)),
+           "qlinear_fp8_gated_backward")
+    return q
+
+
+def qlinear_rmsnorm(type_, x, weight, eps, M, K, residual=None, total=None, y=None, q=None,
+                    scales=None, rstd=None, ldx=None, stream=None):
+    """RMS norm of x (+ residual) into those of total, y, q with scales, and rstd that are given."""
+    _check(_lib.qlinear_rmsnorm(_type(type_), _ptr(x), K if ldx is None else ldx, _ptr(residual),
+                                _ptr(weight), eps, _ptr(total), _ptr(y), _ptr(q), _ptr(scales),
+                                _ptr(rstd), M, K, _stream(stream)), "qlinear_rmsnorm")
+
+
+def qlinear_rmsnorm_workspace_bytes(M: int, K: int) -> int:
+    return int(_lib.qlinear_rmsnorm_workspace_bytes(M, K))
+
+
+def qlinear_rmsnorm_backward(type_, dy, total, rstd, weight, dx, M, K, dtotal=None, dweight=None,
+                             workspace=None, stream=None):
+    """``dx[M, K]`` of qlinear_rmsnorm; dweight (fp32 [K]), when given, the weight's gradient."""
+    _check(_lib.qlinear_rmsnorm_backward(_type(type_), _ptr(dy), _ptr(total), _ptr(rstd),
+                                         _ptr(weight), _ptr(dtotal), _ptr(dx), _ptr(dweight), M,
+                                         K, *_ws(workspace), _stream(stream)),
+           "qlinear_rmsnorm_backward")
+    return dx
+
+
+def qlinear_fp8_workspace_bytes(M: int, E: int, N: int, K: int) -> int:
+    return int(_lib.qlinear_fp8_workspace_bytes(M, E, N, K))
+
+
+def qlinear_fp8_linear(type_, q, scales, w, wscales, y, M, N, K, workspace, stream=None):
+    """``y[M, N] = x . W^T`` from the codes and scales of x [M, K] and W [N, K]."""
+    _check(_lib.qlinear_fp8_linear(_type(type_), _ptr(q), _ptr(scales), _ptr(w), _ptr(wscales),
+                                   _ptr(y), M, N, K, *_ws(workspace), _stream(stream)),
+           "qlinear_fp8_linear")
+    return y
+
+
+def qlinear_fp8_linear_backward(type_, q, scales, w, wscales, dx, M, N, K, workspace,
+                                stream=None):
+    """``dx[M, K] = dy . W`` from the codes and scales of dy [M, N] and W [N, K]."""
+    _check(_lib.qlinear_fp8_linear_backward(_type(type_), _ptr(q), _ptr(scales), _ptr(w),
+                                            _ptr(wscales), _ptr(dx), M, N, K, *_ws(workspace),
+                                            _stream(stream)), "qlinear_fp8_linear_backward")
+    return dx
+
+
+def qlinear_fp8_grouped(type_, q, scales, offsets, w, wscales, y, M, E, N, K, workspace,
+                        stream=None):
+    """qlinear_fp8_linear with rows offsets[e] .. offsets[e + 1] by W[e]; offsets int32 [E + 1] on
+    the device."""
+    _check(_lib.qlinear_fp8_grouped(_type(type_), _ptr(q), _ptr(scales), _ptr(offsets), _ptr(w),
+                                    _ptr(wscales), _ptr(y), M, E, N, K, *_ws(workspace),
+                                    _stream(stream)), "qlinear_fp8_grouped")
+    return y
+
+
+def qlinear_fp8_grouped_backward(type_, q, scales, offsets, w, wscales, dx, M, E, N, K, workspace,
+                                 stream=None):
+    """qlinear_fp8_linear_backward with rows offsets[e] .. offsets[e + 1] by W[e]."""
+    _check(_lib.qlinear_fp8_grouped_backward(_type(type_), _ptr(q), _ptr(scales), _ptr(offsets),
+                                             _ptr(w), _ptr(wscales), _ptr(dx), M, E, N, K,
+                                             *_ws(workspace), _stream(stream)),
+           "qlinear_fp8_grouped_backward")
+    return dx

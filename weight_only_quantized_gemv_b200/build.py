@@ -17,9 +17,9 @@ INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libqlinear.so")
 
 SOURCES = ["qlinear.cu", "dequant.cu", "prefill_tc.cu", "codebook.cu", "fused.cu", "fused_tc.cu",
-           "policy.cpp", "pack.cpp"]
+           "fp8.cu", "fp8_tc.cu", "policy.cpp", "pack.cpp"]
 HEADERS = ["kernels.cuh", "layout.h", "policy.h", "dequant_frag.cuh", "act.cuh", "fused.h",
-           "tc.cuh"]
+           "tc.cuh", "fp8.cuh", "fp8.h"]
 
 
 def nvcc_path() -> str:

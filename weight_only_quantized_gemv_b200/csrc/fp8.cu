@@ -1,0 +1,705 @@
+// Entries of the 8-bit floating-point path (include/qlinear.h) and its kernels over rows: RMS norm,
+// gated activation and plain quantization with e4m3 output, and their backward passes.  The
+// products are in fp8_tc.cu.
+//
+// All of them are bound by memory: they read and write each element once, as 16-byte vectors of
+// eight columns (8 bytes of codes), and a block's scale is a maximum over sixteen lanes.
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "act.cuh"
+#include "fp8.cuh"
+#include "fp8.h"
+#include "fused.h"
+#include "kernels.cuh"
+
+using namespace qfp8;
+
+namespace {
+
+constexpr int kMaxRows = 1 << 24, kMaxColumns = 1 << 30;
+constexpr int kMaxNorm = 32768;  // columns of a norm: 1024 threads of four vectors
+
+// From L2: a grid may start before the one that writes its input has ended, and the read-only
+// path asks for data that nobody writes during the grid's whole life.
+__device__ __forceinline__ uint4 load16(const void* p) {
+  return __ldcg(reinterpret_cast<const uint4*>(p));
+}
+
+// The block's sum, in every thread; `red` has a word per warp and is used in turn (`half`).
+__device__ __forceinline__ float block_sum(float v, float (&red)[2][32], int half) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
+#pragma unroll
+  for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  if (lane == 0) red[half][warp] = v;
+  __syncthreads();
+  v = lane < warps ? red[half][lane] : 0.f;
+#pragma unroll
+  for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  return v;
+}
+
+// ---------------------------------------------------------------------------
+// RMS norm
+
+struct NormParams {
+  const uint16_t* x;         // rows ldx apart
+  const uint16_t* residual;  // [M][K] or null
+  const uint16_t* weight;    // [K]
+  uint16_t* total;           // [M][K] or null
+  uint16_t* y;               // [M][K] or null
+  uint8_t* q;                // [M][K] or null
+  float* scales;             // [M][blocks]
+  float* rstd;               // [M] or null
+  long long ldx;
+  float eps;
+  int M, K;
+};
+
+// A block takes a row; a thread keeps its V vectors in registers between the sum of squares and the
+// output, so that the row is read once.
+template <bool BF16, int V>
+__global__ void __launch_bounds__(1024) norm_kernel(const NormParams P) {
+  __shared__ float red[2][32];
+  const int row = blockIdx.x, step = 8 * (int)blockDim.x, c0 = 8 * (int)threadIdx.x;
+  const size_t base = (size_t)row * P.K;
+  uint4 w[V];
+#pragma unroll
+  for (int i = 0; i < V; ++i)
+    if (c0 + i * step < P.K) w[i] = *reinterpret_cast<const uint4*>(P.weight + c0 + i * step);
+  qlk::grid_dependents_launch();
+  qlk::grid_dependency_wait();
+  uint4 a[V], r[V];
+#pragma unroll
+  for (int i = 0; i < V; ++i) {
+    const int c = c0 + i * step;
+    if (c >= P.K) continue;
+    a[i] = load16(P.x + (size_t)row * P.ldx + c);
+    if (P.residual) r[i] = load16(P.residual + base + c);
+  }
+  float sum = 0.f;
+#pragma unroll
+  for (int i = 0; i < V; ++i) {
+    const int c = c0 + i * step;
+    if (c >= P.K) continue;
+    float t[8];
+    unpack8<BF16>(a[i], t);
+    if (P.residual) {
+      float u[8];
+      unpack8<BF16>(r[i], u);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) t[e] += u[e];
+      a[i] = pack8<BF16>(t);  // the stream as it is stored: what follows goes by it
+      unpack8<BF16>(a[i], t);
+    }
+    if (P.total) *reinterpret_cast<uint4*>(P.total + base + c) = a[i];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) sum = fmaf(t[e], t[e], sum);
+  }
+  const float rstd = rsqrtf(block_sum(sum, red, 0) / (float)P.K + P.eps);
+  if (P.rstd && threadIdx.x == 0) P.rstd[row] = rstd;
+#pragma unroll
+  for (int i = 0; i < V; ++i) {
+    const int c = c0 + i * step;
+    float t[8] = {};
+    if (c < P.K) {
+      float g[8];
+      unpack8<BF16>(a[i], t);
+      unpack8<BF16>(w[i], g);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) t[e] = t[e] * rstd * g[e];
+      if (P.y) *reinterpret_cast<uint4*>(P.y + base + c) = pack8<BF16>(t);
+    }
+    if (P.q) {
+      const float scale = scale_of(top_of_block(top8(t)));
+      if (c < P.K) {
+        *reinterpret_cast<uint2*>(P.q + base + c) = encode8(t, scale);
+        if ((threadIdx.x & 15) == 0) P.scales[(size_t)row * blocks_of(P.K) + c / kBlock] = scale;
+      }
+    }
+  }
+}
+
+struct NormGradParams {
+  const uint16_t* dy;      // [M][K]
+  const uint16_t* total;   // [M][K]
+  const float* rstd;       // [M]
+  const uint16_t* weight;  // [K]
+  const uint16_t* dtotal;  // [M][K] or null
+  uint16_t* dx;            // [M][K]
+  float* partials;         // [blocks][K] or null: sums of dy t rstd over a block's rows
+  int M, K;
+};
+
+// A block takes every gridDim-th row and keeps the sums of its columns in registers.
+template <bool BF16, int V>
+__global__ void __launch_bounds__(1024) norm_grad_kernel(const NormGradParams P) {
+  __shared__ float red[2][32];
+  const int step = 8 * (int)blockDim.x, c0 = 8 * (int)threadIdx.x;
+  uint4 w[V];
+  float dw[V][8] = {};
+#pragma unroll
+  for (int i = 0; i < V; ++i)
+    if (c0 + i * step < P.K) w[i] = *reinterpret_cast<const uint4*>(P.weight + c0 + i * step);
+  qlk::grid_dependents_launch();
+  qlk::grid_dependency_wait();
+  int half = 0;
+  for (int row = blockIdx.x; row < P.M; row += gridDim.x, half ^= 1) {
+    const size_t base = (size_t)row * P.K;
+    uint4 a[V], d[V], r[V];
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      const int c = c0 + i * step;
+      if (c >= P.K) continue;
+      a[i] = load16(P.total + base + c);
+      d[i] = load16(P.dy + base + c);
+      if (P.dtotal) r[i] = load16(P.dtotal + base + c);
+    }
+    const float rstd = __ldcg(P.rstd + row);
+    float sum = 0.f;
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      if (c0 + i * step >= P.K) continue;
+      float t[8], g[8], v[8];
+      unpack8<BF16>(a[i], t);
+      unpack8<BF16>(d[i], g);
+      unpack8<BF16>(w[i], v);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const float n = t[e] * rstd;
+        sum = fmaf(g[e] * v[e], n, sum);
+        dw[i][e] = fmaf(g[e], n, dw[i][e]);
+      }
+    }
+    const float mean = block_sum(sum, red, half) / (float)P.K;
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      const int c = c0 + i * step;
+      if (c >= P.K) continue;
+      float t[8], g[8], v[8];
+      unpack8<BF16>(a[i], t);
+      unpack8<BF16>(d[i], g);
+      unpack8<BF16>(w[i], v);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) t[e] = rstd * (g[e] * v[e] - t[e] * rstd * mean);
+      if (P.dtotal) {
+        unpack8<BF16>(r[i], g);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) t[e] += g[e];
+      }
+      *reinterpret_cast<uint4*>(P.dx + base + c) = pack8<BF16>(t);
+    }
+  }
+  if (P.partials)
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      const int c = c0 + i * step;
+      if (c >= P.K) continue;
+      float4* o = reinterpret_cast<float4*>(P.partials + (size_t)blockIdx.x * P.K + c);
+      o[0] = make_float4(dw[i][0], dw[i][1], dw[i][2], dw[i][3]);
+      o[1] = make_float4(dw[i][4], dw[i][5], dw[i][6], dw[i][7]);
+    }
+}
+
+// dweight[c] = the blocks' sums, added in a fixed order: warp w of a block takes every eighth, its
+// lanes the columns, and the eight meet in shared memory.
+constexpr int kJoinWarps = 8;
+__global__ void __launch_bounds__(32 * kJoinWarps) norm_join_kernel(const float* partials,
+                                                                    float* dweight, int blocks,
+                                                                    int K) {
+  __shared__ float red[kJoinWarps][33];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, c = 32 * blockIdx.x + lane;
+  qlk::grid_dependents_launch();
+  qlk::grid_dependency_wait();
+  float s = 0.f;
+  if (c < K)
+#pragma unroll 8
+    for (int b = warp; b < blocks; b += kJoinWarps) s += __ldcg(partials + (size_t)b * K + c);
+  red[warp][lane] = s;
+  __syncthreads();
+  if (warp == 0 && c < K) {
+#pragma unroll
+    for (int w = 1; w < kJoinWarps; ++w) s += red[w][lane];
+    dweight[c] = s;
+  }
+}
+
+// ---------------------------------------------------------------------------
+// quantization of rows: of x, of act(g) u, or of the gated pair's gradients
+
+enum { kPlain, kGated, kGatedGrad };
+
+struct CodeParams {
+  const uint16_t* x;   // kPlain: rows ldx apart; else gu [M][2 F]
+  const uint16_t* dh;  // kGatedGrad: [M][F]
+  uint8_t* q;          // [M][C]
+  float* scales;       // [M][blocks of C]
+  long long ldx;
+  int M, C, F, act;    // C columns of output: K, F, 2 F
+  int chunks;          // of kCodeCols columns in a row
+};
+
+constexpr int kCodeThreads = 256, kCodeCols = 8 * kCodeThreads;
+
+template <int WHAT, bool BF16, int ACT>
+__device__ __forceinline__ void code_values(const CodeParams& P, int row, int c, float (&v)[8]) {
+  if constexpr (WHAT == kPlain) {
+    unpack8<BF16>(load16(P.x + (size_t)row * P.ldx + c), v);
+  } else {
+    const int f = c < P.F ? c : c - P.F;  // (kGated: always c)
+    const uint16_t* gu = P.x + (size_t)row * 2 * P.F + f;
+    const uint4 gv = load16(gu), uv = load16(gu + P.F);
+    float g[8], u[8];
+    unpack8<BF16>(gv, g);
+    unpack8<BF16>(uv, u);
+    if constexpr (WHAT == kGated) {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) v[e] = qact::act_forward(ACT, g[e]) * u[e];
+    } else {
+      float d[8];
+      unpack8<BF16>(load16(P.dh + (size_t)row * P.F + f), d);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        float y, dy;
+        qact::act_both<true>(ACT, g[e], y, dy);
+        v[e] = c < P.F ? d[e] * u[e] * dy : d[e] * y;
+      }
+    }
+  }
+}
+
+template <int WHAT, bool BF16, int ACT>
+__global__ void __launch_bounds__(kCodeThreads) code_kernel(const CodeParams P) {
+  qlk::grid_dependents_launch();
+  qlk::grid_dependency_wait();
+  const long long n = (long long)P.M * P.chunks;
+  for (long long i = blockIdx.x; i < n; i += gridDim.x) {
+    const int row = (int)(i / P.chunks);
+    const int c = (int)(i - (long long)row * P.chunks) * kCodeCols + 8 * (int)threadIdx.x;
+    float v[8] = {};
+    if (c < P.C) code_values<WHAT, BF16, ACT>(P, row, c, v);
+    const float scale = scale_of(top_of_block(top8(v)));
+    if (c < P.C) {
+      *reinterpret_cast<uint2*>(P.q + (size_t)row * P.C + c) = encode8(v, scale);
+      if ((threadIdx.x & 15) == 0)
+        P.scales[(size_t)row * blocks_of(P.C) + c / kBlock] = scale;
+    }
+  }
+}
+
+// ---------------------------------------------------------------------------
+// weights: a block of threads to a 128 x 128 block
+
+struct WeightParams {
+  const uint16_t* w;  // [E][N][K]
+  uint8_t* q;
+  float* scales;      // [E][N / 128][K / 128]
+  int N, K;
+};
+
+template <bool BF16>
+__global__ void __launch_bounds__(256) weight_kernel(const WeightParams P) {
+  __shared__ float red[8];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int nb = blocks_of(P.N), kb = blocks_of(P.K);
+  const long long b = blockIdx.x;
+  const int k = (int)(b % kb) * kBlock + 8 * (threadIdx.x & 15);
+  const long long rest = b / kb;
+  const int n0 = (int)(rest % nb) * kBlock + (int)(threadIdx.x >> 4);
+  const size_t base = (size_t)(rest / nb) * P.N * P.K + k;
+  uint4 v[8];
+  float top = 0.f;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    v[i] = make_uint4(0, 0, 0, 0);
+    if (k < P.K && n0 + 16 * i < P.N) v[i] = load16(P.w + base + (size_t)(n0 + 16 * i) * P.K);
+  }
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    float f[8];
+    unpack8<BF16>(v[i], f);
+    top = max_nan(top, top8(f));
+  }
+#pragma unroll
+  for (int o = 16; o; o >>= 1) top = max_nan(top, __shfl_xor_sync(0xffffffffu, top, o));
+  if (lane == 0) red[warp] = top;
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < 8; ++i) top = max_nan(top, red[i]);
+  const float scale = scale_of(top);
+  if (threadIdx.x == 0) P.scales[b] = scale;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    if (k >= P.K || n0 + 16 * i >= P.N) continue;
+    float f[8];
+    unpack8<BF16>(v[i], f);
+    *reinterpret_cast<uint2*>(P.q + base + (size_t)(n0 + 16 * i) * P.K) = encode8(f, scale);
+  }
+}
+
+// ---------------------------------------------------------------------------
+// argument checks and launches
+
+bool type_ok(int type) { return type == QL_TYPE_F16 || type == QL_TYPE_BF16; }
+bool aligned(const void* p, size_t a) { return ((uintptr_t)p & (a - 1)) == 0; }
+bool cols_ok(int c) { return c >= 16 && c <= kMaxColumns && c % 16 == 0; }
+
+struct Span {
+  const void* p;
+  size_t bytes;
+};
+bool overlap(const Span& a, const Span& b) {
+  const uintptr_t x = (uintptr_t)a.p, y = (uintptr_t)b.p;
+  return a.p && b.p && a.bytes && b.bytes && x < y + b.bytes && y < x + a.bytes;
+}
+// no output overlaps an input or another output
+template <int NO, int NI>
+bool disjoint(const Span (&outs)[NO], const Span (&ins)[NI]) {
+  for (int i = 0; i < NO; ++i) {
+    for (int j = i + 1; j < NO; ++j)
+      if (overlap(outs[i], outs[j])) return false;
+    for (int j = 0; j < NI; ++j)
+      if (overlap(outs[i], ins[j])) return false;
+  }
+  return true;
+}
+size_t strided(int M, long long ld, int K) { return ((size_t)(M - 1) * ld + K) * 2; }
+size_t scale_bytes(int M, int C) { return (size_t)M * blocks_of(C) * 4; }
+
+int sm_count() {
+  int dev = 0, sms = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return 0;
+  if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return 0;
+  return sms;
+}
+
+// The kernel may start while the one before it ends (it waits for that one's results itself).
+template <class... Params, class... Args>
+ql_status launch_early(void (*kernel)(Params...), unsigned grid, int threads, ql_stream_t stream,
+                       const Args&... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3((unsigned)threads);
+  cfg.stream = reinterpret_cast<cudaStream_t>(stream);
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, args...) == cudaSuccess ? QL_OK : QL_ERR_CUDA;
+}
+
+// Threads of a norm's block, for V vectors each.
+int norm_threads(int K, int V) { return (K / 8 + 32 * V - 1) / (32 * V) * 32; }
+int norm_vectors(int K) { return K <= 8192 ? 1 : K <= 16384 ? 2 : 4; }
+
+template <bool BF16>
+ql_status launch_norm(const NormParams& P, ql_stream_t st) {
+  const int V = norm_vectors(P.K), t = norm_threads(P.K, V);
+  if (V == 1) return launch_early(norm_kernel<BF16, 1>, P.M, t, st, P);
+  if (V == 2) return launch_early(norm_kernel<BF16, 2>, P.M, t, st, P);
+  return launch_early(norm_kernel<BF16, 4>, P.M, t, st, P);
+}
+
+int norm_grad_blocks(int M, int K, int sms) {
+  const int t = norm_threads(K, norm_vectors(K)), per = t <= 512 ? 2 : 1;
+  return M < sms * per ? M : sms * per;
+}
+template <bool BF16>
+ql_status launch_norm_grad(const NormGradParams& P, int blocks, ql_stream_t st) {
+  const int V = norm_vectors(P.K), t = norm_threads(P.K, V);
+  if (V == 1) return launch_early(norm_grad_kernel<BF16, 1>, blocks, t, st, P);
+  if (V == 2) return launch_early(norm_grad_kernel<BF16, 2>, blocks, t, st, P);
+  return launch_early(norm_grad_kernel<BF16, 4>, blocks, t, st, P);
+}
+
+template <int WHAT, bool BF16, int ACT>
+ql_status launch_codes_as(CodeParams P, ql_stream_t st) {
+  P.chunks = (P.C + kCodeCols - 1) / kCodeCols;
+  const long long n = (long long)P.M * P.chunks, most = 1 << 20;
+  return launch_early(code_kernel<WHAT, BF16, ACT>, (unsigned)(n < most ? n : most), kCodeThreads,
+                      st, P);
+}
+template <int WHAT, bool BF16>
+ql_status launch_codes(const CodeParams& P, ql_stream_t st) {
+  if constexpr (WHAT == kPlain) {
+    return launch_codes_as<WHAT, BF16, QL_ACT_NONE>(P, st);
+  } else {
+    switch (P.act) {
+      case QL_ACT_RELU: return launch_codes_as<WHAT, BF16, QL_ACT_RELU>(P, st);
+      case QL_ACT_GELU: return launch_codes_as<WHAT, BF16, QL_ACT_GELU>(P, st);
+      case QL_ACT_GELU_TANH: return launch_codes_as<WHAT, BF16, QL_ACT_GELU_TANH>(P, st);
+      case QL_ACT_SILU: return launch_codes_as<WHAT, BF16, QL_ACT_SILU>(P, st);
+      default: return launch_codes_as<WHAT, BF16, QL_ACT_NONE>(P, st);
+    }
+  }
+}
+template <int WHAT>
+ql_status codes(int type, const CodeParams& P, ql_stream_t st) {
+  return type == QL_TYPE_BF16 ? launch_codes<WHAT, true>(P, st) : launch_codes<WHAT, false>(P, st);
+}
+
+// Sums of a call's parts lie where those of the other fused layers do, behind their counters, so
+// that one workspace serves all of them (fused.h).
+constexpr size_t kPartials = qfused::kVecCounterOffset + qfused::kVecCounterBytes;
+
+// The checks and the launch of a product; C columns of q, R of the output.
+ql_status product(int type, const uint8_t* q, const float* scales, const int* offsets,
+                  const uint8_t* w, const float* wscales, void* y, int M, int E, int N, int K,
+                  bool backward, bool grouped, void* workspace, size_t workspace_bytes,
+                  ql_stream_t stream) {
+  if (!type_ok(type)) return QL_ERR_UNSUPPORTED;
+  if (!q || !scales || !w || !wscales || !y || (grouped && !offsets)) return QL_ERR_NULL;
+  if (M < 1 || M > kMaxRows || !cols_ok(N) || !cols_ok(K) || E < 1 || E > kMaxExperts)
+    return QL_ERR_SHAPE;
+  const int C = backward ? N : K, R = backward ? K : N;
+  // (a tensor copy's coordinates and the units of work are 32-bit)
+  if ((long long)blocks_of(R) * E * (M < 16 ? 1 : (M + 15) / 16 + 1) * blocks_of(C) >=
+      (1LL << 46))
+    return QL_ERR_SHAPE;
+  if (!aligned(q, 16) || !aligned(scales, 4) || !aligned(w, 16) || !aligned(wscales, 4) ||
+      !aligned(y, 16) || !aligned(offsets, 4))
+    return QL_ERR_ALIGN;
+  if (!workspace || workspace_bytes < kPartials) return QL_ERR_WORKSPACE;
+  if (!aligned(workspace, 256)) return QL_ERR_ALIGN;
+  const Span outs[2] = {{y, (size_t)M * R * 2}, {workspace, workspace_bytes}};
+  const Span ins[5] = {{q, (size_t)M * C}, {scales, scale_bytes(M, C)},
+                       {offsets, (size_t)(E + 1) * 4}, {w, (size_t)E * N * K},
+                       {wscales, (size_t)E * blocks_of(N) * blocks_of(K) * 4}};
+  if (!disjoint(outs, ins)) return QL_ERR_ALIAS;
+  Product p{};
+  p.bf16 = type == QL_TYPE_BF16;
+  p.backward = backward;
+  p.q = q;
+  p.sx = scales;
+  p.offsets = offsets;
+  p.w = w;
+  p.sw = wscales;
+  p.y = y;
+  p.M = M;
+  p.E = E;
+  p.N = N;
+  p.K = K;
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  p.err = reinterpret_cast<uint32_t*>(ws);
+  p.counters = reinterpret_cast<uint32_t*>(ws + qfused::kErrBytes);
+  p.partials = reinterpret_cast<float*>(ws + kPartials);
+  p.partial_bytes = workspace_bytes - kPartials;
+  p.stream = reinterpret_cast<cudaStream_t>(stream);
+  return launch_product(p);
+}
+
+}  // namespace
+
+// ---------------------------------------------------------------------------
+// exported entry points
+
+extern "C" ql_status qlinear_fp8_quantize(int type, const void* x, long long ldx, uint8_t* q,
+                                          float* scales, int M, int K, ql_stream_t stream) {
+  if (!type_ok(type)) return QL_ERR_UNSUPPORTED;
+  if (!x || !q || !scales) return QL_ERR_NULL;
+  if (M < 1 || M > kMaxRows || !cols_ok(K) || ldx < K || ldx > (1LL << 40)) return QL_ERR_SHAPE;
+  if (!aligned(x, 16) || ldx % 8 || !aligned(q, 16) || !aligned(scales, 4)) return QL_ERR_ALIGN;
+  const Span outs[2] = {{q, (size_t)M * K}, {scales, scale_bytes(M, K)}};
+  const Span ins[1] = {{x, strided(M, ldx, K)}};
+  if (!disjoint(outs, ins)) return QL_ERR_ALIAS;
+  CodeParams P{};
+  P.x = static_cast<const uint16_t*>(x);
+  P.q = q;
+  P.scales = scales;
+  P.ldx = ldx;
+  P.M = M;
+  P.C = K;
+  return codes<kPlain>(type, P, stream);
+}
+
+extern "C" ql_status qlinear_fp8_gated(int type, int act, const void* gu, uint8_t* q,
+                                       float* scales, int M, int F, ql_stream_t stream) {
+  if (!type_ok(type) || !qact::act_ok(act)) return QL_ERR_UNSUPPORTED;
+  if (!gu || !q || !scales) return QL_ERR_NULL;
+  if (M < 1 || M > kMaxRows || !cols_ok(F) || F > kMaxColumns / 2) return QL_ERR_SHAPE;
+  if (!aligned(gu, 16) || !aligned(q, 16) || !aligned(scales, 4)) return QL_ERR_ALIGN;
+  const Span outs[2] = {{q, (size_t)M * F}, {scales, scale_bytes(M, F)}};
+  const Span ins[1] = {{gu, (size_t)M * F * 4}};
+  if (!disjoint(outs, ins)) return QL_ERR_ALIAS;
+  CodeParams P{};
+  P.x = static_cast<const uint16_t*>(gu);
+  P.q = q;
+  P.scales = scales;
+  P.M = M;
+  P.C = P.F = F;
+  P.act = act;
+  return codes<kGated>(type, P, stream);
+}
+
+extern "C" ql_status qlinear_fp8_gated_backward(int type, int act, const void* dh, const void* gu,
+                                                uint8_t* q, float* scales, int M, int F,
+                                                ql_stream_t stream) {
+  if (!type_ok(type) || !qact::act_ok(act)) return QL_ERR_UNSUPPORTED;
+  if (!dh || !gu || !q || !scales) return QL_ERR_NULL;
+  if (M < 1 || M > kMaxRows || !cols_ok(F) || F > kMaxColumns / 2) return QL_ERR_SHAPE;
+  if (!aligned(dh, 16) || !aligned(gu, 16) || !aligned(q, 16) || !aligned(scales, 4))
+    return QL_ERR_ALIGN;
+  const Span outs[2] = {{q, (size_t)M * F * 2}, {scales, scale_bytes(M, 2 * F)}};
+  const Span ins[2] = {{dh, (size_t)M * F * 2}, {gu, (size_t)M * F * 4}};
+  if (!disjoint(outs, ins)) return QL_ERR_ALIAS;
+  CodeParams P{};
+  P.x = static_cast<const uint16_t*>(gu);
+  P.dh = static_cast<const uint16_t*>(dh);
+  P.q = q;
+  P.scales = scales;
+  P.M = M;
+  P.C = 2 * F;
+  P.F = F;
+  P.act = act;
+  return codes<kGatedGrad>(type, P, stream);
+}
+
+extern "C" ql_status qlinear_fp8_quantize_weights(int type, const void* w, uint8_t* q,
+                                                  float* scales, int E, int N, int K,
+                                                  ql_stream_t stream) {
+  if (!type_ok(type)) return QL_ERR_UNSUPPORTED;
+  if (!w || !q || !scales) return QL_ERR_NULL;
+  if (E < 1 || E > kMaxExperts || !cols_ok(N) || !cols_ok(K)) return QL_ERR_SHAPE;
+  const long long blocks = (long long)E * blocks_of(N) * blocks_of(K);
+  if (blocks >= (1LL << 31)) return QL_ERR_SHAPE;
+  if (!aligned(w, 16) || !aligned(q, 16) || !aligned(scales, 4)) return QL_ERR_ALIGN;
+  const size_t count = (size_t)E * N * K;
+  const Span outs[2] = {{q, count}, {scales, (size_t)blocks * 4}};
+  const Span ins[1] = {{w, count * 2}};
+  if (!disjoint(outs, ins)) return QL_ERR_ALIAS;
+  const WeightParams P{static_cast<const uint16_t*>(w), q, scales, N, K};
+  // an ordinary launch: what reads the weights may start early and does not wait for them
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  if (type == QL_TYPE_BF16)
+    weight_kernel<true><<<(unsigned)blocks, 256, 0, st>>>(P);
+  else
+    weight_kernel<false><<<(unsigned)blocks, 256, 0, st>>>(P);
+  return cudaGetLastError() == cudaSuccess ? QL_OK : QL_ERR_CUDA;
+}
+
+extern "C" ql_status qlinear_rmsnorm(int type, const void* x, long long ldx, const void* residual,
+                                     const void* weight, float eps, void* total, void* y,
+                                     uint8_t* q, float* scales, float* rstd, int M, int K,
+                                     ql_stream_t stream) {
+  if (!type_ok(type)) return QL_ERR_UNSUPPORTED;
+  if (!x || !weight || (!q && !y) || (!q != !scales)) return QL_ERR_NULL;
+  if (M < 1 || M > kMaxRows || !cols_ok(K) || K > kMaxNorm || ldx < K || ldx > (1LL << 40) ||
+      !(eps >= 0.f))
+    return QL_ERR_SHAPE;
+  if (!aligned(x, 16) || ldx % 8 || !aligned(residual, 16) || !aligned(weight, 16) ||
+      !aligned(total, 16) || !aligned(y, 16) || !aligned(q, 16) || !aligned(scales, 4) ||
+      !aligned(rstd, 4))
+    return QL_ERR_ALIGN;
+  const size_t mk = (size_t)M * K * 2;
+  // the stream may be updated in place: each thread reads an element before it writes it
+  const bool in_x = total == x && ldx == K, in_r = total == residual;
+  const Span outs[5] = {{total, mk}, {y, mk}, {q, mk / 2}, {scales, scale_bytes(M, K)},
+                        {rstd, (size_t)M * 4}};
+  const Span ins[3] = {{in_x ? nullptr : x, strided(M, ldx, K)},
+                       {in_r ? nullptr : residual, mk}, {weight, (size_t)K * 2}};
+  const Span others[4] = {outs[1], outs[2], outs[3], outs[4]};
+  const Span whole[2] = {{x, strided(M, ldx, K)}, {residual, mk}};
+  if (!disjoint(outs, ins) || !disjoint(others, whole)) return QL_ERR_ALIAS;
+  NormParams P{};
+  P.x = static_cast<const uint16_t*>(x);
+  P.residual = static_cast<const uint16_t*>(residual);
+  P.weight = static_cast<const uint16_t*>(weight);
+  P.total = static_cast<uint16_t*>(total);
+  P.y = static_cast<uint16_t*>(y);
+  P.q = q;
+  P.scales = scales;
+  P.rstd = rstd;
+  P.ldx = ldx;
+  P.eps = eps;
+  P.M = M;
+  P.K = K;
+  return type == QL_TYPE_BF16 ? launch_norm<true>(P, stream) : launch_norm<false>(P, stream);
+}
+
+extern "C" size_t qlinear_rmsnorm_workspace_bytes(int M, int K) {
+  if (M < 1 || M > kMaxRows || !cols_ok(K) || K > kMaxNorm) return 0;
+  const int sms = sm_count();
+  return sms > 0 ? kPartials + qfused::align_up((size_t)norm_grad_blocks(M, K, sms) * K * 4, 256)
+                 : 0;
+}
+
+extern "C" ql_status qlinear_rmsnorm_backward(int type, const void* dy, const void* total,
+                                              const float* rstd, const void* weight,
+                                              const void* dtotal, void* dx, float* dweight, int M,
+                                              int K, void* workspace, size_t workspace_bytes,
+                                              ql_stream_t stream) {
+  if (!type_ok(type)) return QL_ERR_UNSUPPORTED;
+  if (!dy || !total || !rstd || !weight || !dx) return QL_ERR_NULL;
+  if (M < 1 || M > kMaxRows || !cols_ok(K) || K > kMaxNorm) return QL_ERR_SHAPE;
+  if (!aligned(dy, 16) || !aligned(total, 16) || !aligned(rstd, 4) || !aligned(weight, 16) ||
+      !aligned(dtotal, 16) || !aligned(dx, 16) || !aligned(dweight, 4))
+    return QL_ERR_ALIGN;
+  const int sms = sm_count();
+  if (sms <= 0) return QL_ERR_CUDA;
+  const int blocks = norm_grad_blocks(M, K, sms);
+  if (dweight) {
+    if (!workspace || workspace_bytes < kPartials + (size_t)blocks * K * 4)
+      return QL_ERR_WORKSPACE;
+    if (!aligned(workspace, 256)) return QL_ERR_ALIGN;
+  }
+  const size_t mk = (size_t)M * K * 2;
+  const Span outs[3] = {{dx, mk}, {dweight, (size_t)K * 4},
+                        {dweight ? workspace : nullptr, workspace_bytes}};
+  const Span ins[5] = {{dy, mk}, {total, mk}, {rstd, (size_t)M * 4}, {weight, (size_t)K * 2},
+                       {dtotal == dx ? nullptr : dtotal, mk}};
+  if (!disjoint(outs, ins)) return QL_ERR_ALIAS;
+  NormGradParams P{};
+  P.dy = static_cast<const uint16_t*>(dy);
+  P.total = static_cast<const uint16_t*>(total);
+  P.rstd = rstd;
+  P.weight = static_cast<const uint16_t*>(weight);
+  P.dtotal = static_cast<const uint16_t*>(dtotal);
+  P.dx = static_cast<uint16_t*>(dx);
+  P.partials = dweight ? reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + kPartials)
+                       : nullptr;
+  P.M = M;
+  P.K = K;
+  const ql_status s = type == QL_TYPE_BF16 ? launch_norm_grad<true>(P, blocks, stream)
+                                           : launch_norm_grad<false>(P, blocks, stream);
+  if (s != QL_OK || !dweight) return s;
+  return launch_early(norm_join_kernel, (unsigned)((K + 31) / 32), 32 * kJoinWarps, stream,
+                      (const float*)P.partials, dweight, blocks, K);
+}
+
+extern "C" size_t qlinear_fp8_workspace_bytes(int M, int E, int N, int K) {
+  if (M < 1 || M > kMaxRows || !cols_ok(N) || !cols_ok(K) || E < 1 || E > kMaxExperts) return 0;
+  const size_t part = product_partial_bytes(M, E);
+  return part ? kPartials + qfused::align_up(part, 256) : 0;
+}
+
+extern "C" ql_status qlinear_fp8_linear(int type, const uint8_t* q, const float* scales,
+                                        const uint8_t* w, const float* wscales, void* y, int M,
+                                        int N, int K, void* workspace, size_t workspace_bytes,
+                                        ql_stream_t stream) {
+  return product(type, q, scales, nullptr, w, wscales, y, M, 1, N, K, false, false, workspace,
+                 workspace_bytes, stream);
+}
+extern "C" ql_status qlinear_fp8_linear_backward(int type, const uint8_t* q, const float* scales,
+                                                 const uint8_t* w, const float* wscales, void* dx,
+                                                 int M, int N, int K, void* workspace,
+                                                 size_t workspace_bytes, ql_stream_t stream) {
+  return product(type, q, scales, nullptr, w, wscales, dx, M, 1, N, K, true, false, workspace,
+                 workspace_bytes, stream);
+}
+extern "C" ql_status qlinear_fp8_grouped(int type, const uint8_t* q, const float* scales,
+                                         const int* offsets, const uint8_t* w,
+                                         const float* wscales, void* y, int M, int E, int N, int K,
+                                         void* workspace, size_t workspace_bytes,
+                                         ql_stream_t stream) {
+  return product(type, q, scales, offsets, w, wscales, y, M, E, N, K, false, true, workspace,
+                 workspace_bytes, stream);
+}
+extern "C" ql_status qlinear_fp8_grouped_backward(int type, const uint8_t* q, const float* scales,
+                                                  const int* offsets, const uint8_t* w,
+                                                  const float* wscales, void* dx, int M, int E,
+                                                  int N, int K, void* workspace,
+                                                  size_t workspace_bytes, ql_stream_t stream) {
+  return product(type, q, scales, offsets, w, wscales, dx, M, E, N, K, true, true, workspace,
+                 workspace_bytes, stream);
+}

@@ -24,6 +24,8 @@ from . import (QL_ERR_WORKSPACE, QL_FMT_CB, QL_FMT_LUT4, QL_FMT_W2, QL_FMT_W3, Q
                qlinear_read_error,
                qlinear_pack_tilecoo, qlinear_w2a16, qlinear_w3a16, qlinear_w4a16,
                qlinear_w4a16_outlier,
+               qlinear_fp8_quantize_weights, qlinear_fp8_workspace_bytes,
+               qlinear_rmsnorm_workspace_bytes,
                qlinear_w8a16, qlinear_workspace_bytes, _act, _check, _lib)
 
 _ENTRY = {QL_FMT_W2: qlinear_w2a16, QL_FMT_W3: qlinear_w3a16, QL_FMT_W4: qlinear_w4a16,
@@ -620,3 +622,406 @@ def from_codebook(layer, device="cuda", max_m: int = 16) -> CodebookLinear:
     """From a ``synth.gen.CodebookLayer``-like object (K, N, codes, scales, codebook)."""
     return CodebookLinear(layer.K, layer.N, layer.codes, layer.scales, layer.codebook,
                           device=device, max_m=max_m)
+
+
+# ---------------------------------------------------------------------------
+# 8-bit floating-point layers: e4m3 codes with an fp32 scale per 128, for both operands
+
+_F8, _I32 = torch.float8_e4m3fn, torch.int32
+_TYPE_OF = {torch.float16: 0, torch.bfloat16: 1}  # ql_type
+
+
+def _blocks(columns: int) -> int:
+    return (columns + 127) // 128
+
+
+def _type_of(t: torch.Tensor, name: str) -> int:
+    kind = _TYPE_OF.get(t.dtype)
+    if kind is None or t.dim() != 2 or not t.is_cuda:
+        raise ValueError(f"{name} must be a float16 or bfloat16 matrix on a CUDA device, not "
+                         f"{t.dtype} {tuple(t.shape)} on {t.device}")
+    return kind
+
+
+def _row_ptr(x: torch.Tensor, index: int, name: str) -> tuple:
+    """(data pointer, elements between rows) of a matrix whose rows are contiguous, once checked
+    like ``_fused_ptr``'s."""
+    if x.is_contiguous():
+        return _fused_ptr(x, x.shape, index, name, x.dtype), x.shape[1]
+    M, K = x.shape
+    if x.requires_grad and torch.is_grad_enabled() or x.stride(1) != 1 and K > 1 or (
+            M > 1 and x.stride(0) < K):
+        _fused_ptr(x, (M, K), index, name, x.dtype)  # says why not
+    return x.data_ptr(), x.stride(0) if M > 1 else K
+
+
+def _raw_stream(stream, index: int):
+    return _current_stream(index) if stream is None else getattr(stream, "cuda_stream", stream)
+
+
+def _new(like: torch.Tensor, shape: tuple, dtype, index: int, stream) -> torch.Tensor:
+    """A new tensor on the call's stream."""
+    if stream is None:
+        return like.new_empty(shape, dtype=dtype)
+    with torch.cuda.stream(_as_stream(stream, index)):
+        return like.new_empty(shape, dtype=dtype)
+
+
+def _codes_out(like, q, scales, M: int, C: int, index: int, stream) -> tuple:
+    """Codes [M, C] and scales, made where they are not given."""
+    if q is None:
+        q = _new(like, (M, C), _F8, index, stream)
+    if scales is None:
+        scales = _new(like, (M, _blocks(C)), _F32, index, stream)
+    return (q, scales, _fused_ptr(q, (M, C), index, "q", _F8),
+            _fused_ptr(scales, (M, _blocks(C)), index, "scales", _F32))
+
+
+def _on_device(index: int, method, *args):
+    """method(*args) with the device current, if another one is now."""
+    with torch.cuda.device(index):
+        return method(*args)
+
+
+def fp8_quantize(x: torch.Tensor, q: Optional[torch.Tensor] = None,
+                 scales: Optional[torch.Tensor] = None, stream=None) -> tuple:
+    """(q, scales): e4m3 codes [M, K] of x[M, K] (fp16 or bf16; its rows may lie apart) and an fp32
+    scale for every 128 columns, [M, ceil(K / 128)]; x is about q * scale."""
+    kind, index, (M, K) = _type_of(x, "x"), x.get_device(), x.shape
+    if torch.cuda.current_device() != index:
+        return _on_device(index, fp8_quantize, x, q, scales, stream)
+    px, ldx = _row_ptr(x, index, "x")
+    q, scales, pq, ps = _codes_out(x, q, scales, M, K, index, stream)
+    if M:
+        _check(_lib.qlinear_fp8_quantize(kind, px, ldx, pq, ps, M, K, _raw_stream(stream, index)),
+               "qlinear_fp8_quantize")
+    return q, scales
+
+
+def fp8_gated(gu: torch.Tensor, act: str = "silu", q: Optional[torch.Tensor] = None,
+              scales: Optional[torch.Tensor] = None, stream=None) -> tuple:
+    """(q, scales): codes [M, F] and scales of act(g) * u, where gu[M, 2 F] = (g, u) (fp16 or
+    bf16) is the output of a product with the gate's and the up projection's rows."""
+    kind, index, (M, C) = _type_of(gu, "gu"), gu.get_device(), gu.shape
+    if torch.cuda.current_device() != index:
+        return _on_device(index, fp8_gated, gu, act, q, scales, stream)
+    if C % 2:
+        raise ValueError("gu holds gate and up values, 2 F columns")
+    pgu = _fused_ptr(gu, (M, C), index, "gu", gu.dtype)
+    q, scales, pq, ps = _codes_out(gu, q, scales, M, C // 2, index, stream)
+    if M:
+        _check(_lib.qlinear_fp8_gated(kind, _act(act), pgu, pq, ps, M, C // 2,
+                                      _raw_stream(stream, index)), "qlinear_fp8_gated")
+    return q, scales
+
+
+def fp8_gated_backward(dh: torch.Tensor, gu: torch.Tensor, act: str = "silu",
+                       q: Optional[torch.Tensor] = None, scales: Optional[torch.Tensor] = None,
+                       stream=None) -> tuple:
+    """(q, scales): codes [M, 2 F] and scales of the gradients of g and u, from dh[M, F] and the gu
+    that ``fp8_gated`` read."""
+    kind, index, (M, C) = _type_of(gu, "gu"), gu.get_device(), gu.shape
+    if torch.cuda.current_device() != index:
+        return _on_device(index, fp8_gated_backward, dh, gu, act, q, scales, stream)
+    if C % 2:
+        raise ValueError("gu holds gate and up values, 2 F columns")
+    pgu = _fused_ptr(gu, (M, C), index, "gu", gu.dtype)
+    pdh = _fused_ptr(dh, (M, C // 2), index, "dh", gu.dtype)
+    q, scales, pq, ps = _codes_out(gu, q, scales, M, C, index, stream)
+    if M:
+        _check(_lib.qlinear_fp8_gated_backward(kind, _act(act), pdh, pgu, pq, ps, M, C // 2,
+                                               _raw_stream(stream, index)),
+               "qlinear_fp8_gated_backward")
+    return q, scales
+
+
+def fp8_quantize_weights(w: torch.Tensor, stream=None) -> tuple:
+    """(codes, scales) of w[N, K] or w[E, N, K] (fp16 or bf16, contiguous): e4m3 codes of the same
+    shape and an fp32 scale per 128 x 128 block, for ``Fp8Linear`` and ``Fp8Experts``."""
+    kind, index = _TYPE_OF.get(w.dtype), w.get_device()
+    if kind is None or w.dim() not in (2, 3) or index < 0:
+        raise ValueError("w must be a float16 or bfloat16 [N, K] or [E, N, K] on a CUDA device")
+    *lead, N, K = w.shape
+    with torch.cuda.device(index):
+        _fused_ptr(w, w.shape, index, "w", w.dtype)
+        codes = _new(w, w.shape, _F8, index, stream)
+        scales = _new(w, (*lead, _blocks(N), _blocks(K)), _F32, index, stream)
+        qlinear_fp8_quantize_weights(kind, w, codes, scales, lead[0] if lead else 1, N, K, stream)
+    return codes, scales
+
+
+class RMSNorm(_FusedWorkspace):
+    """RMS norm with the residual's addition and e4m3 output: weight [K] (fp16 or bf16, the type of
+    the stream) on a CUDA device."""
+
+    def __init__(self, weight: torch.Tensor, eps: float = 1e-6):
+        weight = weight.detach()
+        if weight.dtype not in _TYPE_OF or weight.dim() != 1 or not weight.is_cuda:
+            raise ValueError("the weight is a float16 or bfloat16 vector on a CUDA device")
+        self.weight, self.eps, self.K = weight.contiguous(), eps, weight.shape[0]
+        self._fused_lock = threading.RLock()
+        self._fused = (None, self.K, self.K, weight.get_device())
+
+    def _fused_bytes(self, rows: int, backward: bool) -> int:
+        with torch.cuda.device(self._fused[3]):
+            need = qlinear_rmsnorm_workspace_bytes(rows, self.K)
+        if need == 0:
+            raise ValueError(f"no RMS norm of {rows} rows, K={self.K}")
+        return need
+
+    def forward(self, x: torch.Tensor, residual: Optional[torch.Tensor] = None,
+                total: Optional[torch.Tensor] = None, y: Optional[torch.Tensor] = None,
+                rstd: Optional[torch.Tensor] = None, q: Optional[torch.Tensor] = None,
+                scales: Optional[torch.Tensor] = None, stream=None) -> tuple:
+        """(q, scales): e4m3 codes [M, K] and fp32 scales [M, ceil(K / 128)] of the norm of
+        t = x + residual (t = x without a residual).  total, y ([M, K], the type of x) and rstd
+        (fp32 [M]), when given, receive t, the norm's values in 16 bits and 1 / sqrt(mean(t^2) +
+        eps); ``backward`` needs total (or x) and rstd.  total may be x or the residual itself.
+        The rows of x may lie apart.  Autograd does not see the call: tensors that require a
+        gradient are refused where it records."""
+        weight, (_, _, K, index) = self.weight, self._fused
+        if torch.cuda.current_device() != index:
+            return self._fused_elsewhere(self.forward, x, residual, total, y, rstd, q, scales,
+                                         stream)
+        dtype, M = weight.dtype, x.shape[0]
+        if x.dtype is not dtype or x.dim() != 2 or x.shape[1] != K or x.get_device() != index:
+            _fused_ptr(x, (M, K), index, "x", dtype)
+        px, ldx = _row_ptr(x, index, "x")
+        q, scales, pq, ps = _codes_out(x, q, scales, M, K, index, stream)
+        head = (_TYPE_OF[dtype], px, ldx, _fused_ptr(residual, (M, K), index, "residual", dtype),
+                weight.data_ptr(), self.eps, _fused_ptr(total, (M, K), index, "total", dtype),
+                _fused_ptr(y, (M, K), index, "y", dtype), pq, ps,
+                _fused_ptr(rstd, (M,), index, "rstd", _F32), M, K)
+        if M:
+            _check(_lib.qlinear_rmsnorm(*head, _raw_stream(stream, index)), "qlinear_rmsnorm")
+        return q, scales
+
+    def backward(self, dy: torch.Tensor, total: torch.Tensor, rstd: torch.Tensor,
+                 dtotal: Optional[torch.Tensor] = None, dx: Optional[torch.Tensor] = None,
+                 dweight: Optional[torch.Tensor] = None,
+                 workspace: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+        """dx[M, K], the gradient of x and of the residual, from the gradient dy of the norm's values
+        (the quantization has the identity's), the kept total and rstd, and dtotal, the gradient
+        that comes to total from elsewhere (dx may be dtotal itself).  dweight (fp32 [K]), when
+        given, receives the weight's."""
+        weight, (_, _, K, index) = self.weight, self._fused
+        if torch.cuda.current_device() != index:
+            return self._fused_elsewhere(self.backward, dy, total, rstd, dtotal, dx, dweight,
+                                         workspace, stream)
+        dtype, M = weight.dtype, dy.shape[0]
+        pdy = _fused_ptr(dy, (M, K), index, "dy", dtype)
+        if dx is None:
+            dx = self._fused_new(dy, (M, K), index, stream)
+        pdw = _fused_ptr(dweight, (K,), index, "dweight", _F32)
+        head = (_TYPE_OF[dtype], pdy, _fused_ptr(total, (M, K), index, "total", dtype),
+                _fused_ptr(rstd, (M,), index, "rstd", _F32), weight.data_ptr(),
+                _fused_ptr(dtotal, (M, K), index, "dtotal", dtype),
+                _fused_ptr(dx, (M, K), index, "dx", dtype), pdw, M, K)
+        if M and dweight is None:
+            _check(_lib.qlinear_rmsnorm_backward(*head, None, 0, _raw_stream(stream, index)),
+                   "qlinear_rmsnorm_backward")
+        elif M:
+            self._fused_call(_lib.qlinear_rmsnorm_backward, "qlinear_rmsnorm_backward", head, M,
+                             True, workspace, stream)
+        elif dweight is not None:
+            with torch.cuda.stream(_as_stream(stream, index)):
+                dweight.zero_()
+        return dx
+
+
+class _Fp8Weights(_FusedWorkspace):
+    """e4m3 codes [..., N, K] and scales [..., ceil(N / 128), ceil(K / 128)] on a CUDA device; a
+    workspace as in the fused layers, which any of these layers' calls that follow one another may
+    share."""
+
+    def _fp8_setup(self, codes, scales, dims: int, device) -> None:
+        codes = torch.as_tensor(codes).detach()
+        scales = torch.as_tensor(scales).detach()
+        if codes.dtype is torch.uint8:
+            codes = codes.view(_F8)
+        if device is None:
+            device = codes.device if codes.is_cuda else "cuda"
+        if codes.dtype is not _F8 or codes.dim() != dims or scales.dtype is not _F32:
+            raise ValueError(f"the weights are {dims}-dimensional e4m3 codes (float8_e4m3fn, or "
+                             f"their bytes) and fp32 scales, not {codes.dtype} "
+                             f"{tuple(codes.shape)} and {scales.dtype}")
+        *lead, N, K = codes.shape
+        if tuple(scales.shape) != (*lead, _blocks(N), _blocks(K)):
+            raise ValueError(f"codes {tuple(codes.shape)} have a scale per 128 x 128 block: "
+                             f"{(*lead, _blocks(N), _blocks(K))}, not {tuple(scales.shape)}")
+        self.codes = codes.to(device).contiguous()
+        self.scales = scales.to(device).contiguous()
+        self.device, self.N, self.K = self.codes.device, N, K
+        self.E = lead[0] if lead else 1
+        self._fused_lock = threading.RLock()
+        self._fused = (None, N, K, self.codes.get_device())
+
+    @property
+    def weight_bytes(self) -> int:
+        return self.codes.numel() + 4 * self.scales.numel()
+
+    def _fused_bytes(self, rows: int, backward: bool) -> int:
+        _, N, K, index = self._fused
+        with torch.cuda.device(index):
+            need = qlinear_fp8_workspace_bytes(rows, self.E, N, K)
+        if need == 0:
+            raise ValueError(f"no e4m3 product for {rows} rows, E={self.E}, N={N}, K={K}")
+        return need
+
+    def _product(self, entry, name, what, q, scales, offsets, out, C, R, dtype, backward,
+                 workspace, stream):
+        index = self._fused[3]
+        M = q.shape[0]
+        pq = _fused_ptr(q, (M, C), index, "q", _F8)
+        if out is None:
+            out = _new(q, (M, R), dtype, index, stream)
+        kind = _TYPE_OF.get(out.dtype)
+        if kind is None:
+            raise ValueError(f"{what} is a float16 or bfloat16 tensor, not {out.dtype}")
+        head = (kind, pq, _fused_ptr(scales, (M, (C + 127) // 128), index, "scales", _F32),
+                *offsets, self.codes.data_ptr(), self.scales.data_ptr(),
+                _fused_ptr(out, (M, R), index, what, out.dtype), M,
+                *((self.E,) if offsets else ()), self.N, self.K)
+        if M:
+            self._fused_call(entry, name, head, M, backward, workspace, stream)
+        return out
+
+
+class Fp8Linear(_Fp8Weights):
+    """One weight matrix in e4m3: codes [N, K] (float8_e4m3fn or uint8, a tensor or an array; N and
+    K multiples of 16) and an fp32 scale per 128 x 128 block, [ceil(N / 128), ceil(K / 128)]
+    (``fp8_quantize_weights`` makes both)."""
+
+    def __init__(self, codes, scales, device=None):
+        self._fp8_setup(codes, scales, 2, device)
+
+    def forward(self, q: torch.Tensor, scales: torch.Tensor, y: Optional[torch.Tensor] = None,
+                dtype: torch.dtype = torch.bfloat16, workspace: Optional[torch.Tensor] = None,
+                stream=None) -> torch.Tensor:
+        """y[M, N] (dtype: float16 or bfloat16, or that of y when given) = x . W^T for any M, from
+        the codes q[M, K] and scales of x (``RMSNorm.forward``, ``fp8_gated``,
+        ``fp8_quantize``)."""
+        if torch.cuda.current_device() != self._fused[3]:
+            return self._fused_elsewhere(self.forward, q, scales, y, dtype, workspace, stream)
+        return self._product(_lib.qlinear_fp8_linear, "qlinear_fp8_linear", "y", q, scales, (), y,
+                             self.K, self.N, dtype, False, workspace, stream)
+
+    def backward(self, q: torch.Tensor, scales: torch.Tensor, dx: Optional[torch.Tensor] = None,
+                 dtype: torch.dtype = torch.bfloat16, workspace: Optional[torch.Tensor] = None,
+                 stream=None) -> torch.Tensor:
+        """dx[M, K] = dy . W through the frozen weights, from the codes q[M, N] and scales of dy
+        (``fp8_quantize``, ``fp8_gated_backward``)."""
+        if torch.cuda.current_device() != self._fused[3]:
+            return self._fused_elsewhere(self.backward, q, scales, dx, dtype, workspace, stream)
+        return self._product(_lib.qlinear_fp8_linear_backward, "qlinear_fp8_linear_backward", "dx",
+                             q, scales, (), dx, self.N, self.K, dtype, True, workspace, stream)
+
+
+class Fp8Experts(_Fp8Weights):
+    """One weight matrix per expert in e4m3: codes [E, N, K] and scales [E, ceil(N / 128),
+    ceil(K / 128)] as in ``Fp8Linear``, up to 1024 experts.  The rows of a call are in the order of
+    the experts: rows offsets[e] .. offsets[e + 1] - 1 are expert e's, any number of them, none
+    included.  offsets (int32 [E + 1], on the device) is read by the kernel alone.  Rows before the
+    first and behind the last offset are neither read nor written."""
+
+    def __init__(self, codes, scales, device=None):
+        self._fp8_setup(codes, scales, 3, device)
+
+    def _offsets(self, offsets: torch.Tensor) -> tuple:
+        return (_fused_ptr(offsets, (self.E + 1,), self._fused[3], "offsets", _I32),)
+
+    def forward(self, q: torch.Tensor, scales: torch.Tensor, offsets: torch.Tensor,
+                y: Optional[torch.Tensor] = None, dtype: torch.dtype = torch.bfloat16,
+                workspace: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+        """y[T, N]: each row of x (codes q[T, K], scales) by its expert's W^T."""
+        if torch.cuda.current_device() != self._fused[3]:
+            return self._fused_elsewhere(self.forward, q, scales, offsets, y, dtype, workspace,
+                                         stream)
+        return self._product(_lib.qlinear_fp8_grouped, "qlinear_fp8_grouped", "y", q, scales,
+                             self._offsets(offsets), y, self.K, self.N, dtype, False, workspace,
+                             stream)
+
+    def backward(self, q: torch.Tensor, scales: torch.Tensor, offsets: torch.Tensor,
+                 dx: Optional[torch.Tensor] = None, dtype: torch.dtype = torch.bfloat16,
+                 workspace: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+        """dx[T, K]: each row of dy (codes q[T, N], scales) by its expert's W."""
+        if torch.cuda.current_device() != self._fused[3]:
+            return self._fused_elsewhere(self.backward, q, scales, offsets, dx, dtype, workspace,
+                                         stream)
+        return self._product(_lib.qlinear_fp8_grouped_backward, "qlinear_fp8_grouped_backward",
+                             "dx", q, scales, self._offsets(offsets), dx, self.N, self.K, dtype,
+                             True, workspace, stream)
+
+
+class Fp8GatedMLP:
+    """A gated feed-forward block whose products have both operands in e4m3: y = (act(g) * u) Wd^T,
+    (g, u) = v Wgu^T, where v is the RMS norm of x + residual (with a norm) or x itself.  gate_up
+    holds the gate's rows before the up projection's.  Both may be ``Fp8Linear``, or both
+    ``Fp8Experts``, whose calls take offsets and rows in the order of the experts.  backward goes
+    through the frozen weights from what forward was given to keep."""
+
+    def __init__(self, gate_up, down, norm: Optional[RMSNorm] = None, act: str = "silu"):
+        if type(gate_up) is not type(down) or gate_up.E != down.E:
+            raise ValueError("gate_up and down are both Fp8Linear or both Fp8Experts")
+        if gate_up.N != 2 * down.K or (norm is not None and norm.K != gate_up.K):
+            raise ValueError("gate_up is [2 F, K], down [N, F] and the norm [K]")
+        self.gate_up, self.down, self.norm, self.act = gate_up, down, norm, act
+        self._grouped = isinstance(gate_up, Fp8Experts)
+
+    def reserve(self, rows: int, backward: bool = True) -> None:
+        for layer in (self.gate_up, self.down, self.norm):
+            if layer is not None:
+                layer.reserve(rows, backward)
+
+    def new_workspace(self, rows: int, backward: bool = True) -> torch.Tensor:
+        """A zero-filled workspace for the products of calls of up to `rows` rows."""
+        return max((lay.new_workspace(rows, backward) for lay in (self.gate_up, self.down)),
+                   key=lambda ws: ws.numel())
+
+    def _rows(self, offsets) -> tuple:
+        if (offsets is not None) != self._grouped:
+            raise ValueError("offsets go with Fp8Experts")
+        return (offsets,) if self._grouped else ()
+
+    def forward(self, x: torch.Tensor, residual: Optional[torch.Tensor] = None,
+                offsets: Optional[torch.Tensor] = None, total: Optional[torch.Tensor] = None,
+                rstd: Optional[torch.Tensor] = None, gu: Optional[torch.Tensor] = None,
+                y: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None,
+                stream=None) -> torch.Tensor:
+        """y[M, N] from x[M, K].  total and rstd (see ``RMSNorm.forward``) and gu ([M, 2 F]), when
+        given, are kept for ``backward``; y's residual is total."""
+        rows = self._rows(offsets)
+        if self.norm is not None:
+            q, scales = self.norm.forward(x, residual, total=total, rstd=rstd, stream=stream)
+        elif residual is not None or total is not None or rstd is not None:
+            raise ValueError("residual, total and rstd go with a norm")
+        else:
+            q, scales = fp8_quantize(x, stream=stream)
+        gu = self.gate_up.forward(q, scales, *rows, y=gu, dtype=x.dtype, workspace=workspace,
+                                  stream=stream)
+        q, scales = fp8_gated(gu, self.act, stream=stream)
+        return self.down.forward(q, scales, *rows, y=y, dtype=x.dtype, workspace=workspace,
+                                 stream=stream)
+
+    def backward(self, dy: torch.Tensor, gu: torch.Tensor, total: Optional[torch.Tensor] = None,
+                 rstd: Optional[torch.Tensor] = None, offsets: Optional[torch.Tensor] = None,
+                 dtotal: Optional[torch.Tensor] = None, dx: Optional[torch.Tensor] = None,
+                 dweight: Optional[torch.Tensor] = None,
+                 workspace: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+        """dx from dy and what ``forward`` kept; with a norm, from total (or x) and rstd too, dtotal
+        being the gradient that total gets from elsewhere and dweight (fp32 [K]), when given, the
+        norm weight's."""
+        rows = self._rows(offsets)
+        if self.norm is None and not (total is rstd is dtotal is dweight is None):
+            raise ValueError("total, rstd, dtotal and dweight go with a norm")
+        q, scales = fp8_quantize(dy, stream=stream)
+        dh = self.down.backward(q, scales, *rows, dtype=dy.dtype, workspace=workspace,
+                                stream=stream)
+        q, scales = fp8_gated_backward(dh, gu, self.act, stream=stream)
+        if self.norm is None:
+            return self.gate_up.backward(q, scales, *rows, dx=dx, dtype=dy.dtype,
+                                         workspace=workspace, stream=stream)
+        dv = self.gate_up.backward(q, scales, *rows, dtype=dy.dtype, workspace=workspace,
+                                   stream=stream)
+        return self.norm.backward(dv, total, rstd, dtotal=dtotal, dx=dx, dweight=dweight,
+                                  stream=stream)
