@@ -19,7 +19,7 @@ LIB = os.path.join(PKG, "libqlinear.so")
 SOURCES = ["qlinear.cu", "dequant.cu", "prefill_tc.cu", "codebook.cu", "fused.cu", "fused_tc.cu",
            "fp8.cu", "fp8_tc.cu", "policy.cpp", "pack.cpp"]
 HEADERS = ["kernels.cuh", "layout.h", "policy.h", "dequant_frag.cuh", "act.cuh", "fused.h",
-           "tc.cuh", "fp8.cuh", "fp8.h"]
+           "tc.cuh", "tc_pipe.cuh", "fp8.cuh", "fp8.h"]
 
 
 def nvcc_path() -> str:

@@ -1,96 +1,868 @@
-// Products of e4m3 codes with a scale per 128 (fp8.h): one thread per output, tiles of 32 x 32 in
-// shared memory.
-#include <cuda_fp8.h>
+// Products of e4m3 codes with a scale per 128 on the fifth-generation tensor cores (tcgen05):
+//
+//   forward   D[n][m] = sum_b sx[m][b] sw[n / 128][b] sum_{k in block b} W[n][k] q[m][k]
+//   backward  D[k][m] = sum_b sd[m][b] sw[b][k / 128] sum_{n in block b} W[n][k] q[m][n]
+//
+// for one matrix or for one per expert, whose rows of q follow one another.  The weights are the
+// MMA's A operand (128 rows per CTA), the rows of q its B operand, so that any multiple of 16 rows
+// makes a tile: what an expert's few rows leave empty is small.
+//
+// A pipeline step is one block of the summed index: 128 bytes of every row, the width of the
+// 128-byte swizzle.  Both operands come by tensor copies.  The backward product reads the same
+// 128 x 128 block of the weights MN-major (its rows are then the summed index), so that only the
+// copies' coordinates and the descriptors differ.
+//
+// The scales differ from block to block, so the tensor cores' sum covers one block: a step's four
+// MMAs write a fresh accumulator in tensor memory, and the epilogue warps add it, times sx sw, to
+// fp32 sums in registers.  In their share of the accumulator (tcgen05.ld 16x256b) a thread holds
+// two neighbouring columns of each eight, so a step's scales are one 8-byte shared load per four
+// of its packed multiply-adds.
+//
+// Roles: warp 0 copies, 1 MMA issue and tensor memory, 2 (and 3 for wide tiles) the step's
+// products of scales, then four epilogue warps per column group.
+//
+// PAIR: a cluster of two CTAs on two SMs computes 256 rows with tcgen05 cta_group::2; each CTA
+// copies its own 128 rows of weights and half of the rows of q.
+//
+// Work: tiles of 128 (PAIR 256) rows x up to BNX rows of q.  Whole waves of tiles go round the
+// workers; the rest are cut into runs of steps, whose sums meet in the workspace: the last
+// contributor to arrive adds them in worker order, nobody waits.  For experts all of this is
+// computed on the device, from the offsets.
+//
+// Every barrier wait is bounded in time as in the fused products (fused_tc.cu).
+#include <cuda.h>
+#include <cudaTypedefs.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
+
+#include <atomic>
 
 #include "fp8.cuh"
 #include "fp8.h"
 #include "fused.h"
+#include "kernels.cuh"
+#include "tc.cuh"
+#define QTC_WAIT_SLOW __forceinline__
+#include "tc_pipe.cuh"
 
+using namespace qtc;
 using namespace qfp8;
 
 namespace {
 
-struct Params {
-  const uint8_t *q, *w;
-  const float *sx, *sw;
-  const int* offsets;
-  void* y;
-  uint32_t* err;
-  int M, N, K, bf16, mtiles;
+constexpr uint32_t kErrStage = 1u, kErrAcc = 2u, kErrOffsets = 4u;
+constexpr int kTokStride = 80;  // bytes of a staged row of q's outputs: 32 of them and 16 more
+
+template <int BNX_, bool PAIR_>
+struct Cfg {
+  static constexpr int BNX = BNX_;                 // most rows of q per tile
+  static constexpr bool PAIR = PAIR_;
+  static constexpr int kCtas = PAIR ? 2 : 1;
+  static constexpr int kGran = 16 * kCtas;         // a tile's rows of q: a multiple
+  static constexpr int kBRows = BNX / kCtas;       // most that one CTA copies
+  static constexpr int kABytes = 128 * 128;
+  static constexpr int kBBytes = kBRows * 128;
+  static constexpr int kStageBytes = kABytes + kBBytes;
+  static constexpr int kGroups = BNX > 64 ? 2 : 1; // column groups of the accumulator
+  static constexpr int kCols = BNX / kGroups;      // most columns of a group
+  static constexpr int kEpiWarps = 4 * kGroups;
+  static constexpr int kScaleWarps = BNX > 64 ? 2 : 1;
+  static constexpr int kEpiWarp0 = 4;
+  static constexpr int kWarps = kEpiWarp0 + kEpiWarps;
+  static constexpr int kThreads = 32 * kWarps;
+  static constexpr int kAcc = BNX > 128 ? 2 : 4;   // accumulators
+  static constexpr uint32_t kTmemCols = kAcc * BNX;
+  // Narrow tiles: stages for two CTAs on an SM, so that the next call's weights are on their way
+  // while this one ends.
+  static constexpr int kBudget = PAIR ? 200 * 1024 : 110 * 1024;
+  static constexpr int S = kBudget / kStageBytes < 8 ? kBudget / kStageBytes : 8;
+  static constexpr int kStagingOff = S * kStageBytes;
+  static constexpr int kStaging = 16 * kTokStride;           // per epilogue warp
+  static constexpr int kScaleOff = kStagingOff + kEpiWarps * kStaging;
+  static constexpr int kBarOff = kScaleOff + kAcc * BNX * 4;
+  // full[S] empty[S] accf[kAcc] acce[kAcc] sempty[kAcc] fin
+  static constexpr int kBars = 2 * S + 3 * kAcc + 1;
+  static constexpr int kMiscOff = kBarOff + 8 * kBars;       // tensor memory's base, abort flag
+  static constexpr int kTableOff = kMiscOff + 16;            // start[E + 1], tiles before [E + 1]
+  static constexpr int smem(int E) { return kTableOff + 8 * (E + 1); }
+  static constexpr int kMaxSmem = smem(kMaxExperts);
+  static_assert(kMaxSmem <= 232448, "shared memory");
+  // setmaxnreg: the epilogue warps of wide tiles hold 128 sums a thread
+  static constexpr bool kSplit = kCols == 128;
+  static constexpr int kRegsEpi = 216, kRegsOther = 72;
+  static_assert(!kSplit || (kThreads == 384 && 2 * kRegsEpi + kRegsOther <= 3 * 168), "registers");
 };
 
-__device__ __forceinline__ float decode(uint8_t c) {
-  return __half2float(__half(__nv_cvt_fp8_to_halfraw(c, __NV_E4M3)));
+struct Params {
+  const float* sx;
+  const float* sw;
+  const int* offsets;
+  void* y;
+  float* partials;
+  uint32_t* counters;
+  uint32_t* err;
+  int M, E, R;        // rows of q, experts, rows of D
+  int steps;          // blocks of the summed index
+  int nb, kb;         // blocks of the weights' N and K
+  int rtiles;         // tiles of D's rows
+  int bf16;
+  uint32_t wait_us, test_us;
+};
+
+struct Tile {
+  int e, rt, m0, rows, bn;  // expert, tile of D's rows, first row of q, how many, padded
+};
+
+// The call's tiles: those of expert e are pre[e] .. pre[e + 1] - 1, rows of q varying fastest, so
+// that the workers that are at the same weights read them from L2.
+struct Plan {
+  const int* start;  // shared memory
+  const int* pre;
+  int tiles, whole, runners;
+};
+
+template <class C>
+__device__ __forceinline__ Tile tile_of(const Params& P, const Plan& plan, int t) {
+  int e = 0;
+  if (P.E > 1) {  // the last expert with pre[e] <= t (one with tiles)
+    int hi = P.E;
+    while (hi - e > 1) {
+      const int mid = (e + hi) >> 1;
+      if (plan.pre[mid] <= t)
+        e = mid;
+      else
+        hi = mid;
+    }
+  }
+  Tile r;
+  r.e = e;
+  const int lo = plan.start[e], cnt = plan.start[e + 1] - lo;
+  const int mt = (cnt + C::BNX - 1) / C::BNX, l = t - plan.pre[e];
+  r.rt = l / mt;
+  r.bn = ((cnt + mt - 1) / mt + C::kGran - 1) / C::kGran * C::kGran;
+  const int m = (l - r.rt * mt) * r.bn;
+  r.m0 = lo + m;
+  r.rows = min(r.bn, cnt - m);
+  return r;
 }
 
-constexpr int kTile = 32;
+// The work of a worker (CTA or pair): whole tiles w, w + W, ..., then its run of the steps of
+// tiles [whole, tiles), cut at tile boundaries.
+struct Segments {
+  int t, W, rt, rk, left;
+  bool first;
+  __device__ __forceinline__ void init(const Plan& p, int steps, int w, int W_) {
+    W = W_;
+    t = w;
+    const long long U = (long long)(p.tiles - p.whole) * steps;
+    const long long u = w < p.runners ? run_begin(w, U, p.runners) : 0;
+    left = w < p.runners ? (int)(run_begin(w + 1, U, p.runners) - u) : 0;
+    rt = p.whole + (int)(u / steps);
+    rk = (int)(u % steps);
+    first = true;
+  }
+  __device__ __forceinline__ bool next(const Plan& p, int steps, int& tile, int& k0, int& k1,
+                                       int& slot) {
+    if (t < p.whole) {
+      tile = t;
+      t += W;
+      k0 = 0;
+      k1 = steps;
+      return true;
+    }
+    if (left <= 0) return false;
+    tile = rt++;
+    k0 = rk;
+    k1 = left < steps - rk ? rk + left : steps;
+    left -= k1 - k0;
+    rk = 0;
+    slot = first ? 0 : 1;
+    first = false;
+    return true;
+  }
+};
+
+// The R tiles behind the whole waves, over `runners` workers: each in f equal parts (f workers to a
+// tile), or where that would leave many workers idle in W equal runs.
+constexpr int kMaxParts = 8;
+__device__ __forceinline__ void schedule(Plan& p, int steps, int W) {
+  const int R = p.tiles % W;
+  p.whole = p.tiles - R;
+  p.runners = 0;
+  if (R == 0) return;
+  const int f = min(min(W / R, steps), kMaxParts);
+  if (f < kMaxParts && 100 * R * f < 85 * W && (long long)R * steps >= W)
+    p.runners = W;
+  else
+    p.runners = R * f;
+}
+
+// ---------------------------------------------------------------------------
+// instructions
+
+constexpr uint32_t kDescHi = 64u | (1u << 14) | (2u << 29);  // 8-row groups 1024 bytes apart, 128-byte swizzle
+constexpr uint32_t kDescLo = 1u << 16;
+constexpr uint32_t kTransposeA = 1u << 15;  // instruction descriptor: A is MN-major
+
+// e4m3 operands, fp32 accumulator
+template <bool PAIR>
+__device__ __forceinline__ void mma(uint32_t d, uint32_t alo, uint32_t blo, uint32_t idesc,
+                                    uint32_t accumulate) {
+  if constexpr (PAIR)
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t.reg .b64 a, b;\n\t"
+        "setp.ne.b32 p, %5, 0;\n\tmov.b64 a, {%1, %4};\n\tmov.b64 b, {%2, %4};\n\t"
+        "tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], a, b, %3, p;\n\t}" ::"r"(d),
+        "r"(alo), "r"(blo), "r"(idesc), "r"(kDescHi), "r"(accumulate)
+        : "memory");
+  else
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t.reg .b64 a, b;\n\t"
+        "setp.ne.b32 p, %5, 0;\n\tmov.b64 a, {%1, %4};\n\tmov.b64 b, {%2, %4};\n\t"
+        "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], a, b, %3, p;\n\t}" ::"r"(d),
+        "r"(alo), "r"(blo), "r"(idesc), "r"(kDescHi), "r"(accumulate)
+        : "memory");
+}
+
+template <bool PAIR>
+__device__ __forceinline__ void copy_3d(uint32_t dst, const CUtensorMap* map, int c0, int c1,
+                                        int c2, uint32_t bar) {
+  if constexpr (PAIR)
+    asm volatile(
+        "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2), "r"(bar)
+        : "memory");
+  else
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2), "r"(bar)
+        : "memory");
+}
+
+// 16 lanes of tensor memory x 16 columns: register 4 i + 2 h + c holds row lane / 4 + 8 h of column
+// 8 i + 2 (lane mod 4) + c.
+__device__ __forceinline__ void tmem_ld_16x16(uint32_t taddr, uint32_t (&r)[8]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.16x256b.x2.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+        "=r"(r[7])
+      : "r"(taddr)
+      : "memory");
+}
+
+// The loads above have arrived.  (Their registers go through it, so that no use moves ahead of it.)
+__device__ __forceinline__ void wait_loads(uint32_t (&a)[8], uint32_t (&b)[8]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(a[0]), "+r"(a[1]), "+r"(a[2]), "+r"(a[3]), "+r"(a[4]), "+r"(a[5]),
+                 "+r"(a[6]), "+r"(a[7]), "+r"(b[0]), "+r"(b[1]), "+r"(b[2]), "+r"(b[3]),
+                 "+r"(b[4]), "+r"(b[5]), "+r"(b[6]), "+r"(b[7])
+               :
+               : "memory");
+}
+
+using pair_t = unsigned long long;  // two fp32
+__device__ __forceinline__ pair_t lds_pair(uint32_t a) {
+  pair_t v;
+  asm volatile("ld.shared.b64 %0, [%1];" : "=l"(v) : "r"(a));
+  return v;
+}
+__device__ __forceinline__ void add_scaled(pair_t& acc, uint32_t lo, uint32_t hi, pair_t s) {
+  asm("{\n\t.reg .b64 t;\n\tmov.b64 t, {%1, %2};\n\tfma.rn.f32x2 %0, t, %3, %0;\n\t}"
+      : "+l"(acc)
+      : "r"(lo), "r"(hi), "l"(s));
+}
+__device__ __forceinline__ float2 halves(pair_t v) {
+  float2 f;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(f.x), "=f"(f.y) : "l"(v));
+  return f;
+}
+__device__ __forceinline__ pair_t add_pairs(pair_t a, pair_t b) {
+  pair_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+
+// Four 8 x 8 matrices of 16-bit values, transposed: lane 8 j + i gives the address of row i of
+// matrix j.
+__device__ __forceinline__ void store_transposed(uint32_t a, const uint32_t (&r)[4]) {
+  asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(a),
+               "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3])
+               : "memory");
+}
+
+// ---------------------------------------------------------------------------
+
+// Tensor maps: the weights [E][N][K], boxes of 128 x 128; q, boxes of 128 columns x 128, 64, 32 and
+// 16 rows.
+struct Maps {
+  CUtensorMap w, q[4];
+};
+
+template <int BNX, bool PAIR, bool BWD>
+__global__ void __launch_bounds__(Cfg<BNX, PAIR>::kThreads, PAIR ? 1 : 2)
+    fp8_tc_kernel(const Params P, const __grid_constant__ Maps maps) {
+  using C = Cfg<BNX, PAIR>;
+  extern __shared__ __align__(1024) uint8_t smem[];
+  const uint32_t ring = qlk::smem_addr(smem);  // 1024-byte aligned, as the swizzle wants
+  const uint32_t bars = ring + C::kBarOff;
+  auto full = [&](int s) { return bars + 8 * s; };
+  auto empty = [&](int s) { return bars + 8 * (C::S + s); };
+  auto accf = [&](int a) { return bars + 8 * (2 * C::S + a); };
+  auto acce = [&](int a) { return bars + 8 * (2 * C::S + C::kAcc + a); };
+  auto sempty = [&](int a) { return bars + 8 * (2 * C::S + 2 * C::kAcc + a); };
+  const uint32_t fin = bars + 8 * (2 * C::S + 3 * C::kAcc);
+  volatile uint32_t* misc = reinterpret_cast<volatile uint32_t*>(smem + C::kMiscOff);
+  int* const start = reinterpret_cast<int*>(smem + C::kTableOff);
+  int* const pre = start + P.E + 1;
+  const WaitCtx W{ring + C::kMiscOff + 4, P.err, P.wait_us};
+  const int warp = __shfl_sync(0xffffffffu, (int)(threadIdx.x >> 5), 0);  // uniform
+  const int lane = threadIdx.x & 31;
+  const uint32_t rank = PAIR ? blockIdx.x & 1u : 0u;  // of the cluster (2, 1, 1)
+  const bool leader = rank == 0;
+  const int wk = PAIR ? (int)(blockIdx.x >> 1) : (int)blockIdx.x;
+  const int nwk = PAIR ? (int)(gridDim.x >> 1) : (int)gridDim.x;
+  auto lead = [&](uint32_t b) { return (PAIR && !leader) ? cluster_addr(b, 0) : b; };
+  auto commit_both = [&](uint32_t b) {
+    tc_commit<PAIR>(b);
+    if constexpr (PAIR) tc_commit<PAIR>(cluster_addr(b, 1));
+  };
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < C::S; ++s) {
+      qlk::mbar_init(full(s), 1);
+      qlk::mbar_init(empty(s), 1);
+    }
+    for (int a = 0; a < C::kAcc; ++a) {
+      qlk::mbar_init(accf(a), 1 + C::kScaleWarps);
+      qlk::mbar_init(acce(a), C::kCtas * C::kEpiWarps);
+      qlk::mbar_init(sempty(a), C::kEpiWarps);
+    }
+    qlk::mbar_init(fin, 1);
+    misc[1] = 0u;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  if (warp == 0) {
+    // the experts' rows and tiles
+    if (P.offsets) qlk::grid_dependency_wait();
+    int top = 0, before = 0;
+    bool bad = false;
+    for (int b = 0; b <= P.E; b += 32) {
+      const int j = b + lane;
+      const int raw = j > P.E ? 0 : P.offsets ? __ldcg(P.offsets + j) : j ? P.M : 0;
+      int v = min(max(raw, 0), P.M);
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int u = __shfl_up_sync(0xffffffffu, v, o);
+        if (lane >= o) v = max(v, u);
+      }
+      v = max(v, top);
+      top = __shfl_sync(0xffffffffu, v, 31);
+      if (j <= P.E) {
+        start[j] = v;
+        bad |= v != raw;
+      }
+    }
+    __syncwarp();
+    if (lane == 0) pre[0] = 0;
+    for (int b = 0; b < P.E; b += 32) {
+      const int j = b + lane;
+      int v = j < P.E ? (start[j + 1] - start[j] + BNX - 1) / BNX * P.rtiles : 0;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int u = __shfl_up_sync(0xffffffffu, v, o);
+        if (lane >= o) v += u;
+      }
+      v += before;
+      before = __shfl_sync(0xffffffffu, v, 31);
+      if (j < P.E) pre[j + 1] = v;
+    }
+    if (blockIdx.x == 0 && __any_sync(0xffffffffu, bad) && lane == 0) atomicOr(P.err, kErrOffsets);
+  }
+  sync_all<PAIR>();  // barriers are set up (a pair's allocation also wants both CTAs running)
+  if (warp == 1) tmem_alloc<PAIR>(ring + C::kMiscOff, C::kTmemCols);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = misc[0];
+  qlk::grid_dependents_launch();  // (behind the allocation: the next grid's must not come first)
+
+  Plan plan{start, pre, pre[P.E], 0, 0};
+  schedule(plan, P.steps, nwk);
+  Segments sg;
+  sg.init(plan, P.steps, wk, nwk);
+  int t, k0, k1, slot = 0;
+
+  if (warp < C::kEpiWarp0) {
+    if constexpr (C::kSplit) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::kRegsOther));
+    if (warp == 0) {
+      // ---- copies
+      if (lane == 0) {
+        int s = 0, ph = 1, n = 0;
+        bool ok = true;
+        if (P.offsets == nullptr && (P.test_us & 0xFFFFu) == 0) {
+          // the weights of the first stages, while the kernels before this one end
+          Segments ahead = sg;
+          while (n < C::S && ahead.next(plan, P.steps, t, k0, k1, slot)) {
+            const Tile T = tile_of<C>(P, plan, t);
+            const int row = (T.rt * C::kCtas + (int)rank) * 128;
+            for (int k = k0; k < k1 && n < C::S; ++k, ++n) {
+              if (leader)
+                qlk::mbar_arrive_expect_tx(full(n), C::kCtas * C::kABytes + T.bn * 128);
+              copy_3d<PAIR>(ring + n * C::kStageBytes, &maps.w, BWD ? row : k * 128,
+                            BWD ? k * 128 : row, T.e, lead(full(n)));
+            }
+          }
+        }
+        const int early = n;
+        n = 0;
+        qlk::grid_dependency_wait();
+        if ((P.test_us & 0xFFFFu) && wk == 0) qlk::test_delay(P.test_us & 0xFFFFu);
+        while (ok && sg.next(plan, P.steps, t, k0, k1, slot)) {
+          const Tile T = tile_of<C>(P, plan, t);
+          const int row = (T.rt * C::kCtas + (int)rank) * 128, half = T.bn / C::kCtas;
+          const int m = T.m0 + (int)rank * half;
+#pragma unroll 1
+          for (int k = k0; k < k1; ++k) {
+            if (n >= C::S && !(ok = wait<64>(empty(s), ph, W, kErrStage))) break;
+            const uint32_t a = ring + s * C::kStageBytes, b = a + C::kABytes;
+            if (n >= early) {
+              if (leader)
+                qlk::mbar_arrive_expect_tx(full(s), C::kCtas * C::kABytes + T.bn * 128);
+              copy_3d<PAIR>(a, &maps.w, BWD ? row : k * 128, BWD ? k * 128 : row, T.e,
+                            lead(full(s)));
+            }
+            int at = 0;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const int rows = 128 >> i;
+              if (rows > C::kBRows || !(half & rows)) continue;
+              if constexpr (PAIR)
+                tma_2d_pair(b + at * 128, &maps.q[i], k * 128, m + at, lead(full(s)));
+              else
+                tma_2d(b + at * 128, &maps.q[i], k * 128, m + at, full(s));
+              at += rows;
+            }
+            ++n;
+            if (++s == C::S) {
+              s = 0;
+              ph ^= 1;
+            }
+          }
+        }
+        // all stages are handed back (a pair's other CTA gets these arrivals from the leader: none
+        // may be on its way when it exits), and no copy is in flight (the leader's barriers count
+        // both CTAs')
+        const int last = n > early ? n : early;
+        for (int i = n > C::S ? n - C::S : 0; ok && i < n; ++i)
+          ok = wait<0>(empty(i % C::S), (i / C::S) & 1, W, kErrStage);
+        if (leader)
+          for (int i = last > C::S ? last - C::S : 0; i < last; ++i)
+            wait<0>(full(i % C::S), (i / C::S) & 1, W, kErrStage, false);
+        if (PAIR && !ok) qlk::test_delay(kSettleUs);
+      }
+    } else if (warp == 1) {
+      // ---- MMA issue (the leader of a pair)
+      if (leader) {
+        qlk::grid_dependency_wait();
+        if ((P.test_us >> 16) && wk == 0) qlk::test_delay(P.test_us >> 16);
+        int s = 0, ph = 0, a = 0, aph = 1, n = 0;
+        bool ok = true;
+        while (ok && sg.next(plan, P.steps, t, k0, k1, slot)) {
+          const Tile T = tile_of<C>(P, plan, t);
+          // (the type fields of e4m3 are zeros, as those of fp16 in kind::f16)
+          const uint32_t idesc = idesc_f16(128 * C::kCtas, T.bn) | (BWD ? kTransposeA : 0u);
+#pragma unroll 1
+          for (int k = k0; k < k1; ++k, ++n) {
+            if (n >= C::kAcc && !(ok = warp_wait<64, PAIR>(acce(a), aph, W, kErrAcc, lane))) break;
+            if (!(ok = warp_wait<64, PAIR>(full(s), ph, W, kErrStage, lane))) break;
+            tc_fence_after();
+            const uint32_t pa = ((ring + s * C::kStageBytes) >> 4) | kDescLo;
+            const uint32_t pb = pa + (C::kABytes >> 4);
+            if (elect_one()) {
+#pragma unroll
+              for (int kk = 0; kk < 4; ++kk)
+                mma<PAIR>(tmem + a * BNX, pa + (BWD ? 256 : 2) * kk, pb + 2 * kk, idesc, kk != 0);
+              commit_both(empty(s));
+              commit_both(accf(a));
+            }
+            __syncwarp();
+            if (++s == C::S) {
+              s = 0;
+              ph ^= 1;
+            }
+            if (++a == C::kAcc) {
+              a = 0;
+              aph ^= 1;
+            }
+          }
+        }
+        if (n > 0) {
+          if (elect_one()) tc_commit<PAIR>(fin);
+          __syncwarp();
+          warp_wait<0>(fin, 0, W, kErrAcc, lane, false);
+        }
+        if (PAIR && (!ok || misc[1])) qlk::test_delay(kSettleUs);
+      }
+    } else if (warp < 2 + C::kScaleWarps) {
+      // ---- products of scales: columns lane + 32 (warp - 2 + kScaleWarps i) of the tile, four steps
+      // in registers while the four before them are handed out
+      constexpr int kPer = (BNX + 32 * C::kScaleWarps - 1) / (32 * C::kScaleWarps), kAhead = 4;
+      qlk::grid_dependency_wait();
+      int a = 0, aph = 1, n = 0;
+      bool ok = true;
+      while (ok && sg.next(plan, P.steps, t, k0, k1, slot)) {
+        const Tile T = tile_of<C>(P, plan, t);
+        const int rb = min(T.rt * C::kCtas + (int)rank, (BWD ? P.kb : P.nb) - 1);
+        const float* sw = P.sw + (size_t)T.e * P.nb * P.kb + (BWD ? (size_t)rb : (size_t)rb * P.kb);
+        const int hop = BWD ? P.kb : 1;
+        const int c0 = lane + 32 * (warp - 2);
+        const float* sx = P.sx + (size_t)(T.m0 + c0) * P.steps;
+        const size_t skip = (size_t)32 * C::kScaleWarps * P.steps;
+        float v[kPer][kAhead], w[kAhead];
+        auto load = [&](int k) {
+#pragma unroll
+          for (int j = 0; j < kAhead; ++j) {
+            const bool in = k + j < k1;
+            w[j] = in ? __ldg(sw + (size_t)(k + j) * hop) : 0.f;
+#pragma unroll
+            for (int i = 0; i < kPer; ++i)
+              v[i][j] = in && c0 + 32 * C::kScaleWarps * i < T.rows ? __ldcg(sx + i * skip + k + j)
+                                                                    : 0.f;
+          }
+        };
+        load(k0);
+#pragma unroll 1
+        for (int k = k0; ok && k < k1; k += kAhead) {
+          float s[kPer][kAhead];
+#pragma unroll
+          for (int j = 0; j < kAhead; ++j)
+#pragma unroll
+            for (int i = 0; i < kPer; ++i) s[i][j] = v[i][j] * w[j];
+          load(k + kAhead);
+#pragma unroll
+          for (int j = 0; j < kAhead; ++j) {
+            if (k + j >= k1) break;
+            if (n >= C::kAcc && !(ok = warp_wait<64>(sempty(a), aph, W, kErrAcc, lane))) break;
+            float* o = reinterpret_cast<float*>(smem + C::kScaleOff) + a * BNX + c0;
+#pragma unroll
+            for (int i = 0; i < kPer; ++i)
+              if (c0 + 32 * C::kScaleWarps * i < BNX) o[32 * C::kScaleWarps * i] = s[i][j];
+            __syncwarp();
+            if (lane == 0) qlk::mbar_arrive(accf(a));
+            ++n;
+            if (++a == C::kAcc) {
+              a = 0;
+              aph ^= 1;
+            }
+          }
+        }
+      }
+    }
+  } else {
+    // ---- epilogue: accumulator lanes 32 q .. 32 q + 31, columns of group g
+    if constexpr (C::kSplit) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::kRegsEpi));
+    qlk::grid_dependency_wait();
+    constexpr int kChunks = C::kCols / 16;
+    const int ew = warp - C::kEpiWarp0, q = warp & 3, g = ew >> 2;
+    const long long U = (long long)(plan.tiles - plan.whole) * P.steps;
+    const uint32_t staging = ring + C::kStagingOff + ew * C::kStaging;
+    int a = 0, aph = 0;
+    bool ok = true;
+    while (ok && sg.next(plan, P.steps, t, k0, k1, slot)) {
+      const Tile T = tile_of<C>(P, plan, t);
+      const int cols = T.bn / C::kGroups;           // of this group
+      const int chunks = (cols + 15) / 16, col0 = g * cols;
+      pair_t acc[kChunks][2][2][2];                 // [chunk][16 lanes][8 columns][8 lanes]
+#pragma unroll
+      for (int c = 0; c < kChunks; ++c)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) acc[c][i >> 2][(i >> 1) & 1][i & 1] = 0ull;
+#pragma unroll 1
+      for (int k = k0; k < k1; ++k) {
+        if (!(ok = warp_wait<256>(accf(a), aph, W, kErrAcc, lane))) break;
+        tc_fence_after();
+        const uint32_t ta = tmem + ((uint32_t)(32 * q) << 16) + (uint32_t)(a * BNX + col0);
+        const uint32_t sa = ring + C::kScaleOff + 4 * (a * BNX + col0 + 2 * (lane & 3));
+        uint32_t r[2][2][8];
+        tmem_ld_16x16(ta, r[0][0]);
+        tmem_ld_16x16(ta + (16u << 16), r[0][1]);
+#pragma unroll
+        for (int c = 0; c < kChunks; ++c) {
+          if (c < chunks) {
+            const pair_t s0 = lds_pair(sa + 64 * c), s1 = lds_pair(sa + 64 * c + 32);
+            wait_loads(r[c & 1][0], r[c & 1][1]);
+            if (c + 1 < kChunks && c + 1 < chunks) {
+              tmem_ld_16x16(ta + 16 * (c + 1), r[(c + 1) & 1][0]);
+              tmem_ld_16x16(ta + 16 * (c + 1) + (16u << 16), r[(c + 1) & 1][1]);
+            }
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+#pragma unroll
+              for (int i = 0; i < 2; ++i)
+#pragma unroll
+                for (int e = 0; e < 2; ++e)
+                  add_scaled(acc[c][h][i][e], r[c & 1][h][4 * i + 2 * e],
+                             r[c & 1][h][4 * i + 2 * e + 1], i ? s1 : s0);
+          }
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) {
+          // (for a pair's other CTA the arrival says only when: see arrive_stage in fused_tc.cu)
+          if (PAIR && !leader)
+            asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(lead(acce(a)))
+                         : "memory");
+          else
+            qlk::mbar_arrive(acce(a));
+          qlk::mbar_arrive(sempty(a));
+        }
+        if (++a == C::kAcc) {
+          a = 0;
+          aph ^= 1;
+        }
+      }
+      if (!ok) break;
+      if (k0 != 0 || k1 != P.steps) {
+        // part of a tile: the last contributor goes on, with the sums of all
+        constexpr size_t kWarpBytes = (size_t)32 * C::kCols * 4;
+        uint8_t* base = reinterpret_cast<uint8_t*>(P.partials) + ew * kWarpBytes + 16 * lane;
+        constexpr size_t kSlot = C::kEpiWarps * kWarpBytes;
+        uint8_t* mine = base + (size_t)(2 * blockIdx.x + slot) * kSlot;
+#pragma unroll
+        for (int c = 0; c < kChunks; ++c)
+          if (c < chunks)
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+#pragma unroll
+              for (int i = 0; i < 2; ++i)
+                __stcg(reinterpret_cast<ulonglong2*>(mine + (size_t)(4 * c + 2 * h + i) * 512),
+                       make_ulonglong2(acc[c][h][i][0], acc[c][h][i][1]));
+        __syncwarp();
+        const long long ub = (long long)(t - plan.whole) * P.steps;
+        const int wf = worker_of(ub, U, plan.runners);
+        const int wl = worker_of(ub + P.steps - 1, U, plan.runners);
+        uint32_t* counter =
+            P.counters + ((size_t)(t - plan.whole) * C::kCtas + rank) * C::kEpiWarps + ew;
+        uint32_t prev = 0;
+        if (lane == 0) prev = arrive_weight(counter, 1u);
+        prev = __shfl_sync(0xffffffffu, prev, 0);
+        if (prev != (uint32_t)(wl - wf)) continue;
+        __syncwarp();
+        // slot 0 of every contributor (their runs start in this tile), but slot 1 of one whose run
+        // started in an earlier tile
+        const int first = run_begin(wf, U, plan.runners) >= ub ? 0 : 1;
+#pragma unroll
+        for (int c = 0; c < kChunks; ++c)
+          if (c < chunks)
+#pragma unroll
+            for (int i = 0; i < 8; ++i) acc[c][i >> 2][(i >> 1) & 1][i & 1] = 0ull;
+#pragma unroll 1
+        for (int w = wf; w <= wl; ++w) {
+          const uint8_t* src =
+              base + (size_t)(2 * (w * C::kCtas + (int)rank) + (w == wf ? first : 0)) * kSlot;
+#pragma unroll
+          for (int c = 0; c < kChunks; ++c)
+            if (c < chunks)
+#pragma unroll
+              for (int h = 0; h < 2; ++h)
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                  const ulonglong2 v = __ldcg(
+                      reinterpret_cast<const ulonglong2*>(src + (size_t)(4 * c + 2 * h + i) * 512));
+                  acc[c][h][i][0] = add_pairs(acc[c][h][i][0], v.x);
+                  acc[c][h][i][1] = add_pairs(acc[c][h][i][1], v.y);
+                }
+        }
+        if (lane == 0) *counter = 0u;  // ready for the next call
+      }
+      // 16 rows of q at a time through shared memory: 64 contiguous bytes of a row of y per warp
+      const int n = (T.rt * C::kCtas + (int)rank) * 128 + 32 * q + 8 * (lane & 3);
+#pragma unroll
+      for (int c = 0; c < kChunks; ++c)
+        if (c < chunks) {
+          __syncwarp();
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            uint32_t p[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              const float2 v = halves(acc[c][j >> 1][i][j & 1]);
+              p[j] = P.bf16 ? pack2<true>(v.x, v.y) : pack2<false>(v.x, v.y);
+            }
+            store_transposed(staging + (8 * i + (lane & 7)) * kTokStride + (lane >> 3) * 16, p);
+          }
+          __syncwarp();
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            const int row = 16 * c + 8 * i + (lane >> 2);
+            const uint4 v = qlk::lds128(staging + (8 * i + (lane >> 2)) * kTokStride + (lane & 3) * 16);
+            if (row < cols && col0 + row < T.rows && n < P.R)
+              *reinterpret_cast<uint4*>(static_cast<uint16_t*>(P.y) +
+                                        (size_t)(T.m0 + col0 + row) * P.R + n) = v;
+          }
+        }
+    }
+  }
+
+  tc_fence_before();
+  sync_all<PAIR>();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc<PAIR>(tmem, C::kTmemCols);
+  }
+}
+
+// ---------------------------------------------------------------------------
+// host side
+
+constexpr int kMaxDevices = 64;
+
+bool encode(CUtensorMap* map, const void* base, int rank, const cuuint64_t* dims, int box_rows) {
+  const PFN_cuTensorMapEncodeTiled_v12000 enc = encoder();
+  if (!enc) return false;
+  const cuuint64_t strides[2] = {dims[0], dims[0] * dims[1]};
+  const cuuint32_t box[3] = {128, (cuuint32_t)box_rows, 1};
+  const cuuint32_t estr[3] = {1, 1, 1};
+  return enc(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, rank, const_cast<void*>(base), dims, strides, box,
+             estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int BNX, bool PAIR>
+void launch_config(cudaLaunchConfig_t* cfg, cudaLaunchAttribute* attr, unsigned ctas, int E,
+                   cudaStream_t st) {
+  using C = Cfg<BNX, PAIR>;
+  *cfg = cudaLaunchConfig_t{};
+  cfg->gridDim = dim3(ctas);
+  cfg->blockDim = dim3(C::kThreads);
+  cfg->dynamicSmemBytes = C::smem(E);
+  cfg->stream = st;
+  int n = 0;
+  if constexpr (PAIR) {
+    attr[n].id = cudaLaunchAttributeClusterDimension;
+    attr[n].val.clusterDim.x = 2;
+    attr[n].val.clusterDim.y = 1;
+    attr[n].val.clusterDim.z = 1;
+    ++n;
+  }
+  attr[n].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[n].val.programmaticStreamSerializationAllowed = 1;
+  cfg->attrs = attr;
+  cfg->numAttrs = n + 1;
+}
+
+// Workers resident at once, once per instance and device.
+template <int BNX, bool PAIR, bool BWD>
+int resident_workers(int dev, int sms) {
+  using C = Cfg<BNX, PAIR>;
+  static std::atomic<int> known[kMaxDevices];
+  if (dev < 0 || dev >= kMaxDevices) return 0;
+  int n = known[dev].load(std::memory_order_acquire);
+  if (n > 0) return n;
+  auto fn = fp8_tc_kernel<BNX, PAIR, BWD>;
+  if (cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kMaxSmem) !=
+      cudaSuccess)
+    return 0;
+  if constexpr (PAIR) {
+    cudaLaunchConfig_t cfg;
+    cudaLaunchAttribute attr[2];
+    launch_config<BNX, PAIR>(&cfg, attr, 2 * (sms / 2), kMaxExperts, nullptr);
+    cfg.numAttrs = 1;
+    if (cudaOccupancyMaxActiveClusters(&n, fn, &cfg) != cudaSuccess) n = 0;
+  } else {
+    int occ = 0;
+    n = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&occ, fn, C::kThreads, C::kMaxSmem) ==
+                    cudaSuccess && occ >= 1
+            ? sms
+            : 0;
+  }
+  if (n > 0) known[dev].store(n, std::memory_order_release);
+  return n;
+}
+
+template <int BNX, bool PAIR, bool BWD>
+ql_status launch_as(const Product& p) {
+  using C = Cfg<BNX, PAIR>;
+  int dev = 0, sms = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return QL_ERR_CUDA;
+  if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+    return QL_ERR_CUDA;
+  const int maxw = resident_workers<BNX, PAIR, BWD>(dev, sms);
+  if (maxw <= 0) return QL_ERR_CUDA;
+  Params P;
+  P.sx = p.sx;
+  P.sw = p.sw;
+  P.offsets = p.offsets;
+  P.y = p.y;
+  P.partials = p.partials;
+  P.counters = p.counters;
+  P.err = p.err;
+  P.M = p.M;
+  P.E = p.E;
+  P.R = BWD ? p.K : p.N;
+  P.nb = blocks_of(p.N);
+  P.kb = blocks_of(p.K);
+  P.steps = BWD ? P.nb : P.kb;
+  P.rtiles = (blocks_of(P.R) + C::kCtas - 1) / C::kCtas;
+  P.bf16 = p.bf16;
+  // no more tiles than these, whatever the offsets
+  const long long tiles =
+      (long long)P.rtiles * (p.offsets ? p.M / BNX + (p.E < p.M ? p.E : p.M) : (p.M + BNX - 1) / BNX);
+  if (tiles >= (1LL << 31) || (long long)p.N * p.K >= (1LL << 40)) return QL_ERR_SHAPE;
+  // (a split tile has fewer companions than there are workers)
+  if ((size_t)maxw * C::kCtas * C::kEpiWarps * sizeof(uint32_t) > qfused::kTcCounterBytes)
+    return QL_ERR_UNSUPPORTED;
+  if (p.partial_bytes < (size_t)2 * sms * 128 * BNX * sizeof(float)) return QL_ERR_WORKSPACE;
+  const qfused::WaitTest wt = qfused::wait_test();
+  P.wait_us = (wt.limit_us < 1000000000u ? wt.limit_us : 1000000000u) + 4u * (uint32_t)P.steps;
+  P.test_us = wt.delays;
+  Maps maps;
+  const cuuint64_t wdims[3] = {(cuuint64_t)p.K, (cuuint64_t)p.N, (cuuint64_t)p.E};
+  const cuuint64_t qdims[2] = {(cuuint64_t)(BWD ? p.N : p.K), (cuuint64_t)p.M};
+  if (!encode(&maps.w, p.w, 3, wdims, 128)) return QL_ERR_CUDA;
+  for (int i = 0; i < 4; ++i)
+    if ((128 >> i) <= C::kBRows && !encode(&maps.q[i], p.q, 2, qdims, 128 >> i)) return QL_ERR_CUDA;
+  // every worker that can run: how many have work is known on the device
+  const long long units = tiles * P.steps;
+  const int workers = units < maxw ? (int)units : maxw;
+  cudaLaunchConfig_t cfg;
+  cudaLaunchAttribute attr[2];
+  launch_config<BNX, PAIR>(&cfg, attr, (unsigned)(workers * C::kCtas), p.E, p.stream);
+  return cudaLaunchKernelEx(&cfg, fp8_tc_kernel<BNX, PAIR, BWD>, P, maps) == cudaSuccess
+             ? QL_OK
+             : QL_ERR_CUDA;
+}
 
 template <bool BWD>
-__global__ void __launch_bounds__(kTile* kTile) product_kernel(const Params P) {
-  __shared__ float qs[kTile][kTile + 1], ws[kTile][kTile + 1];
-  const int C = BWD ? P.N : P.K, R = BWD ? P.K : P.N;
-  const int tx = threadIdx.x % kTile, ty = threadIdx.x / kTile;
-  const int e = blockIdx.z, r0 = blockIdx.x * kTile;
-  // the expert's rows: what comes before the largest offset so far belongs to others
-  int lo = 0, hi = P.M;
-  if (P.offsets) {
-    for (int i = 0; i <= e; ++i) lo = max(lo, min(P.offsets[i], P.M));
-    hi = max(lo, min(P.offsets[e + 1], P.M));
-    if (threadIdx.x == 0 && blockIdx.x == 0 && blockIdx.y == 0 &&
-        (lo != P.offsets[e] || hi != P.offsets[e + 1]))
-      atomicOr(P.err, 4u);
-  }
-  const int m0 = lo + blockIdx.y * kTile;
-  if (m0 >= hi) return;
-  const uint8_t* w = P.w + (size_t)e * P.N * P.K;
-  const float* sw = P.sw + (size_t)e * blocks_of(P.N) * blocks_of(P.K);
-  const int m = m0 + ty, r = r0 + tx;
-  float sum = 0.f;
-  for (int b = 0; b < blocks_of(C); ++b) {
-    float part = 0.f;
-    for (int c0 = b * kBlock; c0 < min(C, (b + 1) * kBlock); c0 += kTile) {
-      __syncthreads();
-      qs[ty][tx] = m < hi && c0 + tx < C ? decode(P.q[(size_t)m * C + c0 + tx]) : 0.f;
-      if (BWD)  // ws[c][r]
-        ws[ty][tx] = c0 + ty < C && r < R ? decode(w[(size_t)(c0 + ty) * P.K + r]) : 0.f;
-      else
-        ws[tx][ty] = c0 + tx < C && r0 + ty < R ? decode(w[(size_t)(r0 + ty) * P.K + c0 + tx]) : 0.f;
-      __syncthreads();
-      for (int i = 0; i < kTile; ++i) part = fmaf(qs[ty][i], ws[i][tx], part);
-    }
-    if (m < hi && r < R) {
-      const int nb = BWD ? b : r / kBlock, kb = BWD ? r / kBlock : b;
-      sum = fmaf(part, P.sx[(size_t)m * blocks_of(C) + b] * sw[(size_t)nb * blocks_of(P.K) + kb],
-                 sum);
-    }
-  }
-  if (m < hi && r < R) {
-    const size_t o = (size_t)m * R + r;
-    if (P.bf16)
-      static_cast<__nv_bfloat16*>(P.y)[o] = __float2bfloat16_rn(sum);
-    else
-      static_cast<__half*>(P.y)[o] = __float2half_rn(sum);
-  }
+ql_status launch(const Product& p) {
+  const int rows = (p.M + p.E - 1) / p.E;  // of an average expert
+  if (rows <= 16) return launch_as<16, false, BWD>(p);
+  if (rows <= 32) return launch_as<32, false, BWD>(p);
+  if (rows <= 64) return launch_as<64, false, BWD>(p);
+  if (rows <= 128) return launch_as<128, true, BWD>(p);
+  return launch_as<256, true, BWD>(p);
 }
 
 }  // namespace
 
 namespace qfp8 {
 
-size_t product_partial_bytes(int, int) { return 256; }
+// Two fp32 partial tiles of 128 rows per CTA, of the widest tile that a call with at most M rows
+// has.
+size_t product_partial_bytes(int M, int E) {
+  int dev = 0, sms = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return 0;
+  if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return 0;
+  const int rows = (M + E - 1) / E;
+  int bn = 16;
+  while (bn < 256 && bn < rows) bn *= 2;
+  return (size_t)2 * sms * 128 * bn * sizeof(float);
+}
 
 ql_status launch_product(const Product& p) {
-  Params P{p.q, p.w, p.sx, p.sw, p.offsets, p.y, p.err, p.M, p.N, p.K, p.bf16, 0};
-  const int R = p.backward ? p.K : p.N;
-  const dim3 grid((R + kTile - 1) / kTile, (p.M + kTile - 1) / kTile, p.E);
-  if (grid.y > 65535) return QL_ERR_SHAPE;
-  if (p.backward)
-    product_kernel<true><<<grid, kTile * kTile, 0, p.stream>>>(P);
-  else
-    product_kernel<false><<<grid, kTile * kTile, 0, p.stream>>>(P);
-  return cudaGetLastError() == cudaSuccess ? QL_OK : QL_ERR_CUDA;
+  return p.backward ? launch<true>(p) : launch<false>(p);
 }
 
 }  // namespace qfp8

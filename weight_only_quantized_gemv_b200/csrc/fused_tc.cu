@@ -60,6 +60,7 @@
 #include "kernels.cuh"
 #include "layout.h"
 #include "tc.cuh"
+#include "tc_pipe.cuh"
 
 using namespace qlayout;
 using namespace qtc;
@@ -140,11 +141,6 @@ struct TcParams {
   uint32_t test_us;              // tests of the waits: delays (qfused::WaitTest)
 };
 
-__device__ __forceinline__ long long run_begin(int w, long long U, int W) { return w * U / W; }
-__device__ __forceinline__ int worker_of(long long u, long long U, int W) {
-  return (int)(((u + 1) * W - 1) / U);
-}
-
 // The work of a worker (CTA or pair): whole tiles w, w + W, ..., then its run of the stages of
 // tiles [whole, tiles), cut at tile boundaries.
 struct Segments {
@@ -184,94 +180,6 @@ struct Segments {
     return t >= P.whole && left <= 0;
   }
 };
-
-// ---------------------------------------------------------------------------
-// bounded waits
-
-struct WaitCtx {
-  uint32_t abort;  // shared-memory address of the CTA's abort flag
-  uint32_t* err;   // global memory
-  uint32_t limit_us;
-};
-
-// Suspends the thread until the phase completes, or for up to kSuspendNs; whether it completed.
-// (Polling instead took as many issue slots as the decoding.)
-constexpr uint32_t kSuspendNs = 20000;
-__device__ __forceinline__ bool try_wait(uint32_t bar, uint32_t parity, bool cluster) {
-  uint32_t done;
-  if (cluster)
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2, %3;\n\t"
-        "selp.u32 %0, 1, 0, p;\n\t}"
-        : "=r"(done)
-        : "r"(bar), "r"(parity), "r"(kSuspendNs)
-        : "memory");
-  else
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
-        "selp.u32 %0, 1, 0, p;\n\t}"
-        : "=r"(done)
-        : "r"(bar), "r"(parity), "r"(kSuspendNs)
-        : "memory");
-  return done != 0;
-}
-
-// The phase has not completed within one suspension: keep waiting up to the limit, or until
-// another role has given up; then set the flag.
-__device__ __noinline__ bool wait_slow(uint32_t bar, uint32_t parity, uint32_t abort, uint32_t* err,
-                                       uint32_t limit_us, uint32_t bit, bool honor_abort,
-                                       bool cluster) {
-  const uint64_t t0 = globaltimer_ns();
-  for (;;) {
-    if (try_wait(bar, parity, cluster)) return true;
-    if (honor_abort) {
-      uint32_t a;
-      asm volatile("ld.volatile.shared.u32 %0, [%1];" : "=r"(a) : "r"(abort) : "memory");
-      if (a) break;
-    }
-    if (globaltimer_ns() - t0 > 1000ull * limit_us) break;
-  }
-  atomicOr(err, bit);
-  asm volatile("st.volatile.shared.u32 [%0], %1;" ::"r"(abort), "r"(1u) : "memory");
-  return false;
-}
-
-// Waking up from a suspended wait takes hundreds of cycles; polling takes issue slots.  So the
-// waits between the pipeline's roles (SPIN > 0) poll SPIN times first where the MMAs set the pace
-// (256-token tiles: 190 against 290 us on 1024 x 4096 x 28672 backward) and suspend at once where
-// the decoding does (32 rows, 8192 x 18944: 35.1 against 37.6 us).
-// CLUSTER: some of the arrivals come from the pair's other CTA (acquire at cluster scope).
-
-// One thread.
-template <int SPIN>
-__device__ __forceinline__ bool wait(uint32_t bar, uint32_t parity, const WaitCtx& w, uint32_t bit,
-                                     bool honor_abort = true) {
-#pragma unroll 1
-  for (int i = 0; i < SPIN; ++i)
-    if (mbar_ready(bar, parity, false)) return true;
-  return try_wait(bar, parity, false) ||
-         wait_slow(bar, parity, w.abort, w.err, w.limit_us, bit, honor_abort, false);
-}
-
-// A whole warp: every lane sees the phase complete (the usual case), or one lane waits on.
-template <int SPIN, bool CLUSTER = false>
-__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, const WaitCtx& w,
-                                          uint32_t bit, int lane, bool honor_abort = true) {
-#pragma unroll 1
-  for (int i = 0; i < SPIN; ++i)
-    if (__all_sync(0xffffffffu, mbar_ready(bar, parity, CLUSTER))) return true;
-  if (__all_sync(0xffffffffu, try_wait(bar, parity, CLUSTER))) return true;
-  bool ok = true;
-  if (lane == 0)
-    ok = wait_slow(bar, parity, w.abort, w.err, w.limit_us, bit, honor_abort, CLUSTER);
-  return __shfl_sync(0xffffffffu, ok, 0);
-}
-
-// A role that gave up: what it has sent to the pair's other CTA, or has that CTA's barriers count,
-// arrives long before this ends (nothing is left to wait on).
-constexpr uint32_t kSettleUs = 20000;
 
 // ---------------------------------------------------------------------------
 // decoding: one warp, one 16-column tile of a unit, into rows 16 tile .. 16 tile + 15 of the
@@ -548,16 +456,6 @@ constexpr uint32_t kDescHi = 64u | (1u << 14) | (2u << 29);
 constexpr uint32_t kDescLoK = 1u << 16, kDescLoMn = (128u * 128u / 16u) << 16;
 constexpr uint32_t kTransposeA = 1u << 15;  // instruction descriptor: A is MN-major
 
-// Split-sum arrival with a weight; the count before it.
-__device__ __forceinline__ uint32_t arrive_weight(uint32_t* counter, uint32_t weight) {
-  uint32_t old;
-  asm volatile("atom.add.acq_rel.gpu.global.u32 %0, [%1], %2;"
-               : "=r"(old)
-               : "l"(counter), "r"(weight)
-               : "memory");
-  return old;
-}
-
 // A stage of the pair's other CTA is complete: arrive on the leader's barrier.  The default scope
 // (the CTA) orders nothing between the two CTAs in the memory model, so this is what it rests on:
 // no thread of the leader reads what the arrival stands for.  A pair's MMA takes each half of
@@ -570,27 +468,6 @@ __device__ __forceinline__ uint32_t arrive_weight(uint32_t* counter, uint32_t we
 // that way 61), 2048 x 28672 x 8192 1010 against 750, timed in turn.
 __device__ __forceinline__ void arrive_stage(uint32_t bar) {
   asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
-}
-
-// Every thread of the CTA (PAIR: of both CTAs).  The roles leave their warps divergent, so the
-// lanes meet first, and the cluster barrier is the form that does not ask for it.
-template <bool PAIR>
-__device__ __forceinline__ void sync_all() {
-  __syncwarp();
-  if constexpr (PAIR)
-    asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
-  else
-    __syncthreads();
-  __syncwarp();
-}
-
-// One lane of the warp, the same every time.
-__device__ __forceinline__ bool elect_one() {
-  uint32_t p;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}"
-      : "=r"(p));
-  return p != 0;
 }
 
 template <bool PAIR>
@@ -1038,20 +915,6 @@ __global__ void __launch_bounds__(TcCfg<BNX, FMT, PAIR, EP>::kThreads, 1)
 
 // ---------------------------------------------------------------------------
 // host side
-
-PFN_cuTensorMapEncodeTiled_v12000 encoder() {
-  static std::atomic<PFN_cuTensorMapEncodeTiled_v12000> fn{nullptr};
-  PFN_cuTensorMapEncodeTiled_v12000 f = fn.load(std::memory_order_acquire);
-  if (f) return f;
-  void* p = nullptr;
-  cudaDriverEntryPointQueryResult q;
-  if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault,
-                                       &q) == cudaSuccess &&
-      q == cudaDriverEntryPointSuccess)
-    f = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
-  fn.store(f, std::memory_order_release);
-  return f;
-}
 
 // fp16 [rows][cols], box 64 columns x box_rows rows, 128-byte swizzle; outside: zeros
 bool encode_rows(CUtensorMap* map, const void* base, int rows, int cols, int box_rows) {
