@@ -57,7 +57,7 @@ template <int BNX_, bool PAIR_>
 struct Cfg {
   static constexpr int BNX = BNX_;                 // most rows of q per tile
   static constexpr bool PAIR = PAIR_;
-  static constexpr int kCtas = PAIR ? 2 : 1;
+  static constexpr int kCtas = PAIR ? 2 : 1, kBlocks = kCtas;
   static constexpr int kGran = 16 * kCtas;         // a tile's rows of q: a multiple
   static constexpr int kBRows = BNX / kCtas;       // most that one CTA copies
   static constexpr int kABytes = 128 * 128;
@@ -70,7 +70,7 @@ struct Cfg {
   static constexpr int kEpiWarp0 = 4;
   static constexpr int kWarps = kEpiWarp0 + kEpiWarps;
   static constexpr int kThreads = 32 * kWarps;
-  static constexpr int kAcc = BNX > 128 ? 2 : 4;   // accumulators
+  static constexpr int kAcc = 4;   // accumulators
   static constexpr uint32_t kTmemCols = kAcc * BNX;
   // Narrow tiles: stages for two CTAs on an SM, so that the next call's weights are on their way
   // while this one ends.
@@ -85,12 +85,8 @@ struct Cfg {
   static constexpr int kMiscOff = kBarOff + 8 * kBars;       // tensor memory's base, abort flag
   static constexpr int kTableOff = kMiscOff + 16;            // start[E + 1], tiles before [E + 1]
   static constexpr int smem(int E) { return kTableOff + 8 * (E + 1); }
-  static constexpr int kMaxSmem = smem(kMaxExperts);
+  static constexpr int kMaxSmem = kTableOff + 8 * (kMaxExperts + 1);
   static_assert(kMaxSmem <= 232448, "shared memory");
-  // setmaxnreg: the epilogue warps of wide tiles hold 128 sums a thread
-  static constexpr bool kSplit = kCols == 128;
-  static constexpr int kRegsEpi = 216, kRegsOther = 72;
-  static_assert(!kSplit || (kThreads == 384 && 2 * kRegsEpi + kRegsOther <= 3 * 168), "registers");
 };
 
 struct Params {
@@ -121,19 +117,62 @@ struct Plan {
   int tiles, whole, runners;
 };
 
-template <class C>
-__device__ __forceinline__ Tile tile_of(const Params& P, const Plan& plan, int t) {
-  int e = 0;
-  if (P.E > 1) {  // the last expert with pre[e] <= t (one with tiles)
-    int hi = P.E;
-    while (hi - e > 1) {
-      const int mid = (e + hi) >> 1;
-      if (plan.pre[mid] <= t)
-        e = mid;
-      else
-        hi = mid;
+// The experts' first rows and tiles of BN rows of q, by one warp.
+template <int BN>
+__device__ __forceinline__ void make_table(const Params& P, int* start, int* pre, int lane) {
+  if (P.offsets) qlk::grid_dependency_wait();
+  int top = 0, before = 0;
+  bool bad = false;
+  for (int b = 0; b <= P.E; b += 32) {
+    const int j = b + lane;
+    const int raw = j > P.E ? 0 : P.offsets ? __ldcg(P.offsets + j) : j ? P.M : 0;
+    int v = min(max(raw, 0), P.M);
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int u = __shfl_up_sync(0xffffffffu, v, o);
+      if (lane >= o) v = max(v, u);
+    }
+    v = max(v, top);
+    top = __shfl_sync(0xffffffffu, v, 31);
+    if (j <= P.E) {
+      start[j] = v;
+      bad |= v != raw;
     }
   }
+  __syncwarp();
+  if (lane == 0) pre[0] = 0;
+  for (int b = 0; b < P.E; b += 32) {
+    const int j = b + lane;
+    int v = j < P.E ? (start[j + 1] - start[j] + BN - 1) / BN * P.rtiles : 0;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int u = __shfl_up_sync(0xffffffffu, v, o);
+      if (lane >= o) v += u;
+    }
+    v += before;
+    before = __shfl_sync(0xffffffffu, v, 31);
+    if (j < P.E) pre[j + 1] = v;
+  }
+  if (blockIdx.x == 0 && __any_sync(0xffffffffu, bad) && lane == 0) atomicOr(P.err, kErrOffsets);
+}
+
+// The last expert with pre[e] <= t (one with tiles).
+__device__ __forceinline__ int expert_of(const Params& P, const Plan& plan, int t) {
+  int e = 0, hi = P.E;
+  while (hi - e > 1) {
+    const int mid = (e + hi) >> 1;
+    if (plan.pre[mid] <= t)
+      e = mid;
+    else
+      hi = mid;
+  }
+  return e;
+}
+
+// Tiles of equal width, a multiple of the granularity; or (wide_tile_of) of 256 rows of q.
+template <class C>
+__device__ __forceinline__ Tile tile_of(const Params& P, const Plan& plan, int t) {
+  const int e = expert_of(P, plan, t);
   Tile r;
   r.e = e;
   const int lo = plan.start[e], cnt = plan.start[e + 1] - lo;
@@ -144,6 +183,12 @@ __device__ __forceinline__ Tile tile_of(const Params& P, const Plan& plan, int t
   r.m0 = lo + m;
   r.rows = min(r.bn, cnt - m);
   return r;
+}
+__device__ __forceinline__ Tile wide_tile_of(const Params& P, const Plan& plan, int t) {
+  const int e = expert_of(P, plan, t);
+  const int lo = plan.start[e], cnt = plan.start[e + 1] - lo;
+  const int mt = (cnt + 255) / 256, l = t - plan.pre[e], rt = l / mt, m = 256 * (l - rt * mt);
+  return Tile{e, rt, lo + m, min(256, cnt - m), 256};
 }
 
 // The work of a worker (CTA or pair): whole tiles w, w + W, ..., then its run of the steps of
@@ -202,7 +247,7 @@ __device__ __forceinline__ void schedule(Plan& p, int steps, int W) {
 
 constexpr uint32_t kDescHi = 64u | (1u << 14) | (2u << 29);  // 8-row groups 1024 bytes apart, 128-byte swizzle
 constexpr uint32_t kDescLo = 1u << 16;
-constexpr uint32_t kTransposeA = 1u << 15;  // instruction descriptor: A is MN-major
+constexpr uint32_t kTransposeA = 1u << 15, kTransposeB = 1u << 16;  // instruction descriptor: MN-major
 
 // e4m3 operands, fp32 accumulator
 template <bool PAIR>
@@ -273,6 +318,11 @@ __device__ __forceinline__ void add_scaled(pair_t& acc, uint32_t lo, uint32_t hi
       : "+l"(acc)
       : "r"(lo), "r"(hi), "l"(s));
 }
+__device__ __forceinline__ pair_t both(float f) {
+  pair_t v;
+  asm("mov.b64 %0, {%1, %1};" : "=l"(v) : "f"(f));
+  return v;
+}
 __device__ __forceinline__ float2 halves(pair_t v) {
   float2 f;
   asm("mov.b64 {%0, %1}, %2;" : "=f"(f.x), "=f"(f.y) : "l"(v));
@@ -282,6 +332,33 @@ __device__ __forceinline__ pair_t add_pairs(pair_t a, pair_t b) {
   pair_t r;
   asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
   return r;
+}
+
+// 32 lanes of tensor memory x 32 columns: register i holds column i of the lane's row.
+__device__ __forceinline__ void tmem_ld_32x32(uint32_t taddr, uint32_t (&r)[32]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, "
+      "%12, %13, %14, %15, %16, %17, %18, %19, %20, %21, %22, %23, "
+      "%24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]),
+        "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]),
+        "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]),
+        "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]),
+        "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]),
+        "=r"(r[30]), "=r"(r[31])
+      : "r"(taddr)
+      : "memory");
+}
+__device__ __forceinline__ void wait_loads(uint32_t (&r)[32]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]),
+                 "+r"(r[6]), "+r"(r[7]), "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]),
+                 "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]), "+r"(r[16]), "+r"(r[17]),
+                 "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]), "+r"(r[22]), "+r"(r[23]),
+                 "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]), "+r"(r[29]),
+                 "+r"(r[30]), "+r"(r[31])
+               :
+               : "memory");
 }
 
 // Four 8 x 8 matrices of 16-bit values, transposed: lane 8 j + i gives the address of row i of
@@ -343,43 +420,7 @@ __global__ void __launch_bounds__(Cfg<BNX, PAIR>::kThreads, PAIR ? 1 : 2)
     misc[1] = 0u;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
-  if (warp == 0) {
-    // the experts' rows and tiles
-    if (P.offsets) qlk::grid_dependency_wait();
-    int top = 0, before = 0;
-    bool bad = false;
-    for (int b = 0; b <= P.E; b += 32) {
-      const int j = b + lane;
-      const int raw = j > P.E ? 0 : P.offsets ? __ldcg(P.offsets + j) : j ? P.M : 0;
-      int v = min(max(raw, 0), P.M);
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int u = __shfl_up_sync(0xffffffffu, v, o);
-        if (lane >= o) v = max(v, u);
-      }
-      v = max(v, top);
-      top = __shfl_sync(0xffffffffu, v, 31);
-      if (j <= P.E) {
-        start[j] = v;
-        bad |= v != raw;
-      }
-    }
-    __syncwarp();
-    if (lane == 0) pre[0] = 0;
-    for (int b = 0; b < P.E; b += 32) {
-      const int j = b + lane;
-      int v = j < P.E ? (start[j + 1] - start[j] + BNX - 1) / BNX * P.rtiles : 0;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int u = __shfl_up_sync(0xffffffffu, v, o);
-        if (lane >= o) v += u;
-      }
-      v += before;
-      before = __shfl_sync(0xffffffffu, v, 31);
-      if (j < P.E) pre[j + 1] = v;
-    }
-    if (blockIdx.x == 0 && __any_sync(0xffffffffu, bad) && lane == 0) atomicOr(P.err, kErrOffsets);
-  }
+  if (warp == 0) make_table<BNX>(P, start, pre, lane);
   sync_all<PAIR>();  // barriers are set up (a pair's allocation also wants both CTAs running)
   if (warp == 1) tmem_alloc<PAIR>(ring + C::kMiscOff, C::kTmemCols);
   tc_fence_before();
@@ -395,7 +436,6 @@ __global__ void __launch_bounds__(Cfg<BNX, PAIR>::kThreads, PAIR ? 1 : 2)
   int t, k0, k1, slot = 0;
 
   if (warp < C::kEpiWarp0) {
-    if constexpr (C::kSplit) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::kRegsOther));
     if (warp == 0) {
       // ---- copies
       if (lane == 0) {
@@ -562,7 +602,6 @@ __global__ void __launch_bounds__(Cfg<BNX, PAIR>::kThreads, PAIR ? 1 : 2)
     }
   } else {
     // ---- epilogue: accumulator lanes 32 q .. 32 q + 31, columns of group g
-    if constexpr (C::kSplit) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::kRegsEpi));
     qlk::grid_dependency_wait();
     constexpr int kChunks = C::kCols / 16;
     const int ew = warp - C::kEpiWarp0, q = warp & 3, g = ew >> 2;
@@ -715,6 +754,306 @@ __global__ void __launch_bounds__(Cfg<BNX, PAIR>::kThreads, PAIR ? 1 : 2)
 }
 
 // ---------------------------------------------------------------------------
+// Many rows of q: they are the MMA's A operand, 256 per pair of CTAs, and 256 of D's rows its B
+// operand.  A thread's share of the accumulator is then a row of q and 128 of D's rows, one block
+// of the weights, so that a step has one product of scales per thread, which it makes itself.
+
+struct Wide {
+  static constexpr int BNX = 256, kCtas = 2, kBlocks = 2, kBRows = 128;
+  static constexpr int kBytes = 128 * 128;         // of an operand, per CTA and step
+  static constexpr int S = 6, kStageBytes = 2 * kBytes;
+  static constexpr int kEpiWarps = 8, kEpiWarp0 = 4;
+  static constexpr int kThreads = 32 * (kEpiWarp0 + kEpiWarps);
+  static constexpr int kAcc = 2;
+  static constexpr int kStagingOff = S * kStageBytes;
+  static constexpr int kStaging = 32 * kTokStride; // per epilogue warp: 32 rows of 32 columns
+  static constexpr int kBarOff = kStagingOff + kEpiWarps * kStaging;
+  static constexpr int kBars = 2 * S + 2 * kAcc + 1;  // full[S] empty[S] accf[2] acce[2] fin
+  static constexpr int kMiscOff = kBarOff + 8 * kBars + 8;
+  static constexpr int kTableOff = kMiscOff + 16;
+  static constexpr int smem(int E) { return kTableOff + 8 * (E + 1); }
+  static constexpr int kMaxSmem = kTableOff + 8 * (kMaxExperts + 1);
+  static_assert(kMaxSmem <= 232448, "shared memory");
+  // setmaxnreg: the epilogue's threads hold 128 sums each
+  static constexpr int kRegsEpi = 216, kRegsOther = 72;
+  static_assert(kThreads == 384 && 2 * kRegsEpi + kRegsOther <= 3 * 168, "registers");
+};
+
+template <bool BWD>
+__global__ void __launch_bounds__(Wide::kThreads, 1)
+    fp8_wide_kernel(const Params P, const __grid_constant__ Maps maps) {
+  using C = Wide;
+  extern __shared__ __align__(1024) uint8_t smem[];
+  const uint32_t ring = qlk::smem_addr(smem);
+  const uint32_t bars = ring + C::kBarOff;
+  auto full = [&](int s) { return bars + 8 * s; };
+  auto empty = [&](int s) { return bars + 8 * (C::S + s); };
+  auto accf = [&](int a) { return bars + 8 * (2 * C::S + a); };
+  auto acce = [&](int a) { return bars + 8 * (2 * C::S + C::kAcc + a); };
+  const uint32_t fin = bars + 8 * (2 * C::S + 2 * C::kAcc);
+  volatile uint32_t* misc = reinterpret_cast<volatile uint32_t*>(smem + C::kMiscOff);
+  int* const start = reinterpret_cast<int*>(smem + C::kTableOff);
+  int* const pre = start + P.E + 1;
+  const WaitCtx W{ring + C::kMiscOff + 4, P.err, P.wait_us};
+  const int warp = __shfl_sync(0xffffffffu, (int)(threadIdx.x >> 5), 0);  // uniform
+  const int lane = threadIdx.x & 31;
+  const uint32_t rank = blockIdx.x & 1u;
+  const bool leader = rank == 0;
+  const int wk = (int)(blockIdx.x >> 1), nwk = (int)(gridDim.x >> 1);
+  auto lead = [&](uint32_t b) { return leader ? b : cluster_addr(b, 0); };
+  auto commit_both = [&](uint32_t b) {
+    tc_commit<true>(b);
+    tc_commit<true>(cluster_addr(b, 1));
+  };
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < C::S; ++s) {
+      qlk::mbar_init(full(s), 1);
+      qlk::mbar_init(empty(s), 1);
+    }
+    for (int a = 0; a < C::kAcc; ++a) {
+      qlk::mbar_init(accf(a), 1);
+      qlk::mbar_init(acce(a), 2 * C::kEpiWarps);
+    }
+    qlk::mbar_init(fin, 1);
+    misc[1] = 0u;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  if (warp == 0) make_table<256>(P, start, pre, lane);
+  sync_all<true>();
+  if (warp == 1) tmem_alloc<true>(ring + C::kMiscOff, 512);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = misc[0];
+  qlk::grid_dependents_launch();  // (behind the allocation: the next grid's must not come first)
+
+  Plan plan{start, pre, pre[P.E], 0, 0};
+  schedule(plan, P.steps, nwk);
+  Segments sg;
+  sg.init(plan, P.steps, wk, nwk);
+  int t, k0, k1, slot = 0;
+
+  if (warp < C::kEpiWarp0) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::kRegsOther));
+    if (warp == 0) {
+      // ---- copies
+      if (lane == 0) {
+        int s = 0, ph = 1, n = 0;
+        bool ok = true;
+        qlk::grid_dependency_wait();
+        if ((P.test_us & 0xFFFFu) && wk == 0) qlk::test_delay(P.test_us & 0xFFFFu);
+        while (ok && sg.next(plan, P.steps, t, k0, k1, slot)) {
+          const Tile T = wide_tile_of(P, plan, t);
+          const int m = T.m0 + (int)rank * 128, row = (T.rt * 2 + (int)rank) * 128;
+#pragma unroll 1
+          for (int k = k0; k < k1; ++k) {
+            if (n >= C::S && !(ok = wait<64>(empty(s), ph, W, kErrStage))) break;
+            const uint32_t a = ring + s * C::kStageBytes;
+            if (leader) qlk::mbar_arrive_expect_tx(full(s), 2 * C::kStageBytes);
+            tma_2d_pair(a, &maps.q[0], k * 128, m, lead(full(s)));
+            copy_3d<true>(a + C::kBytes, &maps.w, BWD ? row : k * 128, BWD ? k * 128 : row, T.e,
+                          lead(full(s)));
+            ++n;
+            if (++s == C::S) {
+              s = 0;
+              ph ^= 1;
+            }
+          }
+        }
+        // (as in fp8_tc_kernel)
+        for (int i = n > C::S ? n - C::S : 0; ok && i < n; ++i)
+          ok = wait<0>(empty(i % C::S), (i / C::S) & 1, W, kErrStage);
+        if (leader)
+          for (int i = n > C::S ? n - C::S : 0; i < n; ++i)
+            wait<0>(full(i % C::S), (i / C::S) & 1, W, kErrStage, false);
+        if (!ok) qlk::test_delay(kSettleUs);
+      }
+    } else if (warp == 1 && leader) {
+      // ---- MMA issue
+      qlk::grid_dependency_wait();
+      if ((P.test_us >> 16) && wk == 0) qlk::test_delay(P.test_us >> 16);
+      constexpr uint32_t idesc = idesc_f16(256, 256) | (BWD ? kTransposeB : 0u);
+      int s = 0, ph = 0, a = 0, aph = 1, n = 0;
+      bool ok = true;
+      while (ok && sg.next(plan, P.steps, t, k0, k1, slot)) {
+#pragma unroll 1
+        for (int k = k0; k < k1; ++k, ++n) {
+          if (n >= C::kAcc && !(ok = warp_wait<64, true>(acce(a), aph, W, kErrAcc, lane))) break;
+          if (!(ok = warp_wait<64, true>(full(s), ph, W, kErrStage, lane))) break;
+          tc_fence_after();
+          const uint32_t pa = ((ring + s * C::kStageBytes) >> 4) | kDescLo;
+          const uint32_t pb = pa + (C::kBytes >> 4);
+          if (elect_one()) {
+#pragma unroll
+            for (int kk = 0; kk < 4; ++kk)
+              mma<true>(tmem + a * 256, pa + 2 * kk, pb + (BWD ? 256 : 2) * kk, idesc, kk != 0);
+            commit_both(empty(s));
+            commit_both(accf(a));
+          }
+          __syncwarp();
+          if (++s == C::S) {
+            s = 0;
+            ph ^= 1;
+          }
+          if (++a == C::kAcc) {
+            a = 0;
+            aph ^= 1;
+          }
+        }
+      }
+      if (n > 0) {
+        if (elect_one()) tc_commit<true>(fin);
+        __syncwarp();
+        warp_wait<0>(fin, 0, W, kErrAcc, lane, false);
+      }
+      if (!ok || misc[1]) qlk::test_delay(kSettleUs);
+    }
+  } else {
+    // ---- epilogue: rows 32 q + lane of this CTA's rows of q, columns of group g
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::kRegsEpi));
+    qlk::grid_dependency_wait();
+    const int ew = warp - C::kEpiWarp0, q = warp & 3, g = ew >> 2;
+    const long long U = (long long)(plan.tiles - plan.whole) * P.steps;
+    const uint32_t staging = ring + C::kStagingOff + ew * C::kStaging;
+    int a = 0, aph = 0;
+    bool ok = true;
+    while (ok && sg.next(plan, P.steps, t, k0, k1, slot)) {
+      const Tile T = wide_tile_of(P, plan, t);
+      const int lrow = (int)rank * 128 + 32 * q + lane;  // of the tile
+      const int rb = min(T.rt * 2 + g, (BWD ? P.kb : P.nb) - 1);
+      const float* sw = P.sw + (size_t)T.e * P.nb * P.kb + (BWD ? (size_t)rb : (size_t)rb * P.kb);
+      const int hop = BWD ? P.kb : 1;
+      const float* sx = P.sx + (size_t)(T.m0 + min(lrow, T.rows - 1)) * P.steps;
+      // the scales of the four steps ahead
+      float v[4], w[4];
+      auto load = [&](int k) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const int kk = min(k + j, k1 - 1);
+          v[j] = __ldcg(sx + kk);
+          w[j] = __ldg(sw + (size_t)kk * hop);
+        }
+      };
+      load(k0);
+      pair_t acc[64];
+#pragma unroll
+      for (int c = 0; c < 64; ++c) acc[c] = 0ull;
+#pragma unroll 1
+      for (int k = k0; ok && k < k1; k += 4) {
+        float scale[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) scale[j] = v[j] * w[j];
+        load(k + 4);
+#pragma unroll 1
+        for (int j = 0; j < 4 && k + j < k1; ++j) {
+          if (!(ok = warp_wait<256>(accf(a), aph, W, kErrAcc, lane))) break;
+          tc_fence_after();
+          const uint32_t ta = tmem + ((uint32_t)(32 * q) << 16) + (uint32_t)(a * 256 + g * 128);
+          const float f = j == 0 ? scale[0] : j == 1 ? scale[1] : j == 2 ? scale[2] : scale[3];
+          const pair_t ff = both(f);
+          uint32_t r[2][32];
+          tmem_ld_32x32(ta, r[0]);
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            wait_loads(r[c & 1]);
+            if (c < 3) {
+              tmem_ld_32x32(ta + 32 * (c + 1), r[(c + 1) & 1]);
+            } else {  // the accumulator is free
+              tc_fence_before();
+              __syncwarp();
+              if (lane == 0) {
+                if (leader)
+                  qlk::mbar_arrive(acce(a));
+                else  // (says only when: see arrive_stage in fused_tc.cu)
+                  asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(lead(acce(a)))
+                               : "memory");
+              }
+            }
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+              add_scaled(acc[16 * c + i], r[c & 1][2 * i], r[c & 1][2 * i + 1], ff);
+          }
+          if (++a == C::kAcc) {
+            a = 0;
+            aph ^= 1;
+          }
+        }
+      }
+      if (!ok) break;
+      if (k0 != 0 || k1 != P.steps) {
+        // part of a tile (as in fp8_tc_kernel)
+        constexpr size_t kWarpBytes = 32 * 128 * 4, kSlot = C::kEpiWarps * kWarpBytes;
+        uint8_t* base = reinterpret_cast<uint8_t*>(P.partials) + ew * kWarpBytes + 16 * lane;
+        uint8_t* mine = base + (size_t)(2 * blockIdx.x + slot) * kSlot;
+#pragma unroll
+        for (int c = 0; c < 32; ++c)
+          __stcg(reinterpret_cast<ulonglong2*>(mine + c * 512),
+                 make_ulonglong2(acc[2 * c], acc[2 * c + 1]));
+        __syncwarp();
+        const long long ub = (long long)(t - plan.whole) * P.steps;
+        const int wf = worker_of(ub, U, plan.runners);
+        const int wl = worker_of(ub + P.steps - 1, U, plan.runners);
+        uint32_t* counter =
+            P.counters + ((size_t)(t - plan.whole) * 2 + rank) * C::kEpiWarps + ew;
+        uint32_t prev = 0;
+        if (lane == 0) prev = arrive_weight(counter, 1u);
+        prev = __shfl_sync(0xffffffffu, prev, 0);
+        if (prev != (uint32_t)(wl - wf)) continue;
+        __syncwarp();
+        const int first = run_begin(wf, U, plan.runners) >= ub ? 0 : 1;
+#pragma unroll
+        for (int c = 0; c < 64; ++c) acc[c] = 0ull;
+#pragma unroll 1
+        for (int w2 = wf; w2 <= wl; ++w2) {
+          const uint8_t* src =
+              base + (size_t)(2 * (w2 * 2 + (int)rank) + (w2 == wf ? first : 0)) * kSlot;
+#pragma unroll
+          for (int c = 0; c < 32; ++c) {
+            const ulonglong2 x = __ldcg(reinterpret_cast<const ulonglong2*>(src + c * 512));
+            acc[2 * c] = add_pairs(acc[2 * c], x.x);
+            acc[2 * c + 1] = add_pairs(acc[2 * c + 1], x.y);
+          }
+        }
+        if (lane == 0) *counter = 0u;  // ready for the next call
+      }
+      // 32 columns at a time through shared memory: 64 contiguous bytes of a row of y per warp
+      const int m = T.m0 + (int)rank * 128 + 32 * q + (lane >> 2);
+      const int n = (T.rt * 2 + g) * 128 + 8 * (lane & 3);
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        __syncwarp();
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          uint32_t p[4];
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const float2 x = halves(acc[16 * c + 4 * i + j]);
+            p[j] = P.bf16 ? pack2<true>(x.x, x.y) : pack2<false>(x.x, x.y);
+          }
+          sts128(staging + lane * kTokStride + 16 * i, make_uint4(p[0], p[1], p[2], p[3]));
+        }
+        __syncwarp();
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const uint4 x = qlk::lds128(staging + (8 * i + (lane >> 2)) * kTokStride + 16 * (lane & 3));
+          if (m + 8 * i < T.m0 + T.rows && n + 32 * c < P.R)
+            *reinterpret_cast<uint4*>(static_cast<uint16_t*>(P.y) + (size_t)(m + 8 * i) * P.R + n +
+                                      32 * c) = x;
+        }
+      }
+    }
+  }
+
+  tc_fence_before();
+  sync_all<true>();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc<true>(tmem, 512);
+  }
+}
+
+// ---------------------------------------------------------------------------
 // host side
 
 constexpr int kMaxDevices = 64;
@@ -730,17 +1069,17 @@ bool encode(CUtensorMap* map, const void* base, int rank, const cuuint64_t* dims
              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int BNX, bool PAIR>
+// attr: two entries, the cluster first (the occupancy query takes that one alone)
+template <class C>
 void launch_config(cudaLaunchConfig_t* cfg, cudaLaunchAttribute* attr, unsigned ctas, int E,
                    cudaStream_t st) {
-  using C = Cfg<BNX, PAIR>;
   *cfg = cudaLaunchConfig_t{};
   cfg->gridDim = dim3(ctas);
   cfg->blockDim = dim3(C::kThreads);
   cfg->dynamicSmemBytes = C::smem(E);
   cfg->stream = st;
   int n = 0;
-  if constexpr (PAIR) {
+  if constexpr (C::kCtas == 2) {
     attr[n].id = cudaLaunchAttributeClusterDimension;
     attr[n].val.clusterDim.x = 2;
     attr[n].val.clusterDim.y = 1;
@@ -753,27 +1092,27 @@ void launch_config(cudaLaunchConfig_t* cfg, cudaLaunchAttribute* attr, unsigned 
   cfg->numAttrs = n + 1;
 }
 
-// Workers resident at once, once per instance and device.
-template <int BNX, bool PAIR, bool BWD>
+using Kernel = void (*)(const Params, const Maps);
+
+// Workers resident at once, once per kernel and device.
+template <class C, Kernel kernel>
 int resident_workers(int dev, int sms) {
-  using C = Cfg<BNX, PAIR>;
   static std::atomic<int> known[kMaxDevices];
   if (dev < 0 || dev >= kMaxDevices) return 0;
   int n = known[dev].load(std::memory_order_acquire);
   if (n > 0) return n;
-  auto fn = fp8_tc_kernel<BNX, PAIR, BWD>;
-  if (cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kMaxSmem) !=
+  if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kMaxSmem) !=
       cudaSuccess)
     return 0;
-  if constexpr (PAIR) {
+  if constexpr (C::kCtas == 2) {
     cudaLaunchConfig_t cfg;
     cudaLaunchAttribute attr[2];
-    launch_config<BNX, PAIR>(&cfg, attr, 2 * (sms / 2), kMaxExperts, nullptr);
+    launch_config<C>(&cfg, attr, 2 * (sms / 2), kMaxExperts, nullptr);
     cfg.numAttrs = 1;
-    if (cudaOccupancyMaxActiveClusters(&n, fn, &cfg) != cudaSuccess) n = 0;
+    if (cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) != cudaSuccess) n = 0;
   } else {
     int occ = 0;
-    n = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&occ, fn, C::kThreads, C::kMaxSmem) ==
+    n = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&occ, kernel, C::kThreads, C::kMaxSmem) ==
                     cudaSuccess && occ >= 1
             ? sms
             : 0;
@@ -782,14 +1121,14 @@ int resident_workers(int dev, int sms) {
   return n;
 }
 
-template <int BNX, bool PAIR, bool BWD>
+// C: rows of q (BNX) and blocks of 128 rows of D (kBlocks) per tile.
+template <class C, Kernel kernel, bool BWD>
 ql_status launch_as(const Product& p) {
-  using C = Cfg<BNX, PAIR>;
   int dev = 0, sms = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return QL_ERR_CUDA;
   if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
     return QL_ERR_CUDA;
-  const int maxw = resident_workers<BNX, PAIR, BWD>(dev, sms);
+  const int maxw = resident_workers<C, kernel>(dev, sms);
   if (maxw <= 0) return QL_ERR_CUDA;
   Params P;
   P.sx = p.sx;
@@ -805,16 +1144,16 @@ ql_status launch_as(const Product& p) {
   P.nb = blocks_of(p.N);
   P.kb = blocks_of(p.K);
   P.steps = BWD ? P.nb : P.kb;
-  P.rtiles = (blocks_of(P.R) + C::kCtas - 1) / C::kCtas;
+  P.rtiles = (blocks_of(P.R) + C::kBlocks - 1) / C::kBlocks;
   P.bf16 = p.bf16;
   // no more tiles than these, whatever the offsets
-  const long long tiles =
-      (long long)P.rtiles * (p.offsets ? p.M / BNX + (p.E < p.M ? p.E : p.M) : (p.M + BNX - 1) / BNX);
+  const long long tiles = (long long)P.rtiles * (p.offsets ? p.M / C::BNX + (p.E < p.M ? p.E : p.M)
+                                                           : (p.M + C::BNX - 1) / C::BNX);
   if (tiles >= (1LL << 31) || (long long)p.N * p.K >= (1LL << 40)) return QL_ERR_SHAPE;
-  // (a split tile has fewer companions than there are workers)
+  // (fewer tiles than workers are split)
   if ((size_t)maxw * C::kCtas * C::kEpiWarps * sizeof(uint32_t) > qfused::kTcCounterBytes)
     return QL_ERR_UNSUPPORTED;
-  if (p.partial_bytes < (size_t)2 * sms * 128 * BNX * sizeof(float)) return QL_ERR_WORKSPACE;
+  if (p.partial_bytes < (size_t)2 * sms * 128 * C::BNX * sizeof(float)) return QL_ERR_WORKSPACE;
   const qfused::WaitTest wt = qfused::wait_test();
   P.wait_us = (wt.limit_us < 1000000000u ? wt.limit_us : 1000000000u) + 4u * (uint32_t)P.steps;
   P.test_us = wt.delays;
@@ -829,20 +1168,23 @@ ql_status launch_as(const Product& p) {
   const int workers = units < maxw ? (int)units : maxw;
   cudaLaunchConfig_t cfg;
   cudaLaunchAttribute attr[2];
-  launch_config<BNX, PAIR>(&cfg, attr, (unsigned)(workers * C::kCtas), p.E, p.stream);
-  return cudaLaunchKernelEx(&cfg, fp8_tc_kernel<BNX, PAIR, BWD>, P, maps) == cudaSuccess
-             ? QL_OK
-             : QL_ERR_CUDA;
+  launch_config<C>(&cfg, attr, (unsigned)(workers * C::kCtas), p.E, p.stream);
+  return cudaLaunchKernelEx(&cfg, kernel, P, maps) == cudaSuccess ? QL_OK : QL_ERR_CUDA;
+}
+
+template <int BNX, bool PAIR, bool BWD>
+ql_status launch_narrow(const Product& p) {
+  return launch_as<Cfg<BNX, PAIR>, fp8_tc_kernel<BNX, PAIR, BWD>, BWD>(p);
 }
 
 template <bool BWD>
 ql_status launch(const Product& p) {
   const int rows = (p.M + p.E - 1) / p.E;  // of an average expert
-  if (rows <= 16) return launch_as<16, false, BWD>(p);
-  if (rows <= 32) return launch_as<32, false, BWD>(p);
-  if (rows <= 64) return launch_as<64, false, BWD>(p);
-  if (rows <= 128) return launch_as<128, true, BWD>(p);
-  return launch_as<256, true, BWD>(p);
+  if (rows <= 16) return launch_narrow<16, false, BWD>(p);
+  if (rows <= 32) return launch_narrow<32, false, BWD>(p);
+  if (rows <= 64) return launch_narrow<64, false, BWD>(p);
+  if (rows <= 128) return launch_narrow<128, true, BWD>(p);
+  return launch_as<Wide, fp8_wide_kernel<BWD>, BWD>(p);
 }
 
 }  // namespace
