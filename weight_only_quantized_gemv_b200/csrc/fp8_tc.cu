@@ -102,6 +102,7 @@ struct Params {
   int nb, kb;         // blocks of the weights' N and K
   int rtiles;         // tiles of D's rows
   int bf16;
+  int vec;            // scales of a row that one load may take
   uint32_t wait_us, test_us;
 };
 
@@ -269,6 +270,20 @@ __device__ __forceinline__ void mma(uint32_t d, uint32_t alo, uint32_t blo, uint
         : "memory");
 }
 
+// Arrive on the barrier `bar` of this CTA (PAIR: of both, at the same offset) once the MMAs issued so
+// far have completed.
+template <bool PAIR>
+__device__ __forceinline__ void commit_both(uint32_t bar) {
+  if constexpr (PAIR)
+    asm volatile(
+        "{\n\t.reg .b16 m;\n\tmov.b16 m, 3;\n\t"
+        "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 "
+        "[%0], m;\n\t}" ::"r"(bar)
+        : "memory");
+  else
+    tc_commit<false>(bar);
+}
+
 template <bool PAIR>
 __device__ __forceinline__ void copy_3d(uint32_t dst, const CUtensorMap* map, int c0, int c1,
                                         int c2, uint32_t bar) {
@@ -317,11 +332,6 @@ __device__ __forceinline__ void add_scaled(pair_t& acc, uint32_t lo, uint32_t hi
   asm("{\n\t.reg .b64 t;\n\tmov.b64 t, {%1, %2};\n\tfma.rn.f32x2 %0, t, %3, %0;\n\t}"
       : "+l"(acc)
       : "r"(lo), "r"(hi), "l"(s));
-}
-__device__ __forceinline__ pair_t both(float f) {
-  pair_t v;
-  asm("mov.b64 %0, {%1, %1};" : "=l"(v) : "f"(f));
-  return v;
 }
 __device__ __forceinline__ float2 halves(pair_t v) {
   float2 f;
@@ -401,10 +411,6 @@ __global__ void __launch_bounds__(Cfg<BNX, PAIR>::kThreads, PAIR ? 1 : 2)
   const int wk = PAIR ? (int)(blockIdx.x >> 1) : (int)blockIdx.x;
   const int nwk = PAIR ? (int)(gridDim.x >> 1) : (int)gridDim.x;
   auto lead = [&](uint32_t b) { return (PAIR && !leader) ? cluster_addr(b, 0) : b; };
-  auto commit_both = [&](uint32_t b) {
-    tc_commit<PAIR>(b);
-    if constexpr (PAIR) tc_commit<PAIR>(cluster_addr(b, 1));
-  };
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < C::S; ++s) {
@@ -524,8 +530,8 @@ __global__ void __launch_bounds__(Cfg<BNX, PAIR>::kThreads, PAIR ? 1 : 2)
 #pragma unroll
               for (int kk = 0; kk < 4; ++kk)
                 mma<PAIR>(tmem + a * BNX, pa + (BWD ? 256 : 2) * kk, pb + 2 * kk, idesc, kk != 0);
-              commit_both(empty(s));
-              commit_both(accf(a));
+              commit_both<PAIR>(empty(s));
+              commit_both<PAIR>(accf(a));
             }
             __syncwarp();
             if (++s == C::S) {
@@ -756,7 +762,7 @@ __global__ void __launch_bounds__(Cfg<BNX, PAIR>::kThreads, PAIR ? 1 : 2)
 // ---------------------------------------------------------------------------
 // Many rows of q: they are the MMA's A operand, 256 per pair of CTAs, and 256 of D's rows its B
 // operand.  A thread's share of the accumulator is then a row of q and 128 of D's rows, one block
-// of the weights, so that a step has one product of scales per thread, which it makes itself.
+// of the weights: a step has one product of scales per thread.
 
 struct Wide {
   static constexpr int BNX = 256, kCtas = 2, kBlocks = 2, kBRows = 128;
@@ -767,8 +773,11 @@ struct Wide {
   static constexpr int kAcc = 2;
   static constexpr int kStagingOff = S * kStageBytes;
   static constexpr int kStaging = 32 * kTokStride; // per epilogue warp: 32 rows of 32 columns
-  static constexpr int kBarOff = kStagingOff + kEpiWarps * kStaging;
-  static constexpr int kBars = 2 * S + 2 * kAcc + 1;  // full[S] empty[S] accf[2] acce[2] fin
+  static constexpr int kScaleWarps = 2;
+  static constexpr int kScaleOff = kStagingOff + kEpiWarps * kStaging;  // [kAcc][2 blocks][128 rows]
+  static constexpr int kBarOff = kScaleOff + kAcc * 256 * 4;
+  // full[S] empty[S] accf[2] acce[2] sempty[2] fin
+  static constexpr int kBars = 2 * S + 3 * kAcc + 1;
   static constexpr int kMiscOff = kBarOff + 8 * kBars + 8;
   static constexpr int kTableOff = kMiscOff + 16;
   static constexpr int smem(int E) { return kTableOff + 8 * (E + 1); }
@@ -790,7 +799,8 @@ __global__ void __launch_bounds__(Wide::kThreads, 1)
   auto empty = [&](int s) { return bars + 8 * (C::S + s); };
   auto accf = [&](int a) { return bars + 8 * (2 * C::S + a); };
   auto acce = [&](int a) { return bars + 8 * (2 * C::S + C::kAcc + a); };
-  const uint32_t fin = bars + 8 * (2 * C::S + 2 * C::kAcc);
+  auto sempty = [&](int a) { return bars + 8 * (2 * C::S + 2 * C::kAcc + a); };
+  const uint32_t fin = bars + 8 * (2 * C::S + 3 * C::kAcc);
   volatile uint32_t* misc = reinterpret_cast<volatile uint32_t*>(smem + C::kMiscOff);
   int* const start = reinterpret_cast<int*>(smem + C::kTableOff);
   int* const pre = start + P.E + 1;
@@ -801,10 +811,6 @@ __global__ void __launch_bounds__(Wide::kThreads, 1)
   const bool leader = rank == 0;
   const int wk = (int)(blockIdx.x >> 1), nwk = (int)(gridDim.x >> 1);
   auto lead = [&](uint32_t b) { return leader ? b : cluster_addr(b, 0); };
-  auto commit_both = [&](uint32_t b) {
-    tc_commit<true>(b);
-    tc_commit<true>(cluster_addr(b, 1));
-  };
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < C::S; ++s) {
@@ -812,8 +818,9 @@ __global__ void __launch_bounds__(Wide::kThreads, 1)
       qlk::mbar_init(empty(s), 1);
     }
     for (int a = 0; a < C::kAcc; ++a) {
-      qlk::mbar_init(accf(a), 1);
+      qlk::mbar_init(accf(a), 1 + C::kScaleWarps);
       qlk::mbar_init(acce(a), 2 * C::kEpiWarps);
+      qlk::mbar_init(sempty(a), C::kEpiWarps);
     }
     qlk::mbar_init(fin, 1);
     misc[1] = 0u;
@@ -879,8 +886,8 @@ __global__ void __launch_bounds__(Wide::kThreads, 1)
       while (ok && sg.next(plan, P.steps, t, k0, k1, slot)) {
 #pragma unroll 1
         for (int k = k0; k < k1; ++k, ++n) {
-          if (n >= C::kAcc && !(ok = warp_wait<64, true>(acce(a), aph, W, kErrAcc, lane))) break;
-          if (!(ok = warp_wait<64, true>(full(s), ph, W, kErrStage, lane))) break;
+          if (!(ok = warp_wait<256>(full(s), ph, W, kErrStage, lane))) break;
+          if (n >= C::kAcc && !(ok = warp_wait<256>(acce(a), aph, W, kErrAcc, lane))) break;
           tc_fence_after();
           const uint32_t pa = ((ring + s * C::kStageBytes) >> 4) | kDescLo;
           const uint32_t pb = pa + (C::kBytes >> 4);
@@ -888,8 +895,8 @@ __global__ void __launch_bounds__(Wide::kThreads, 1)
 #pragma unroll
             for (int kk = 0; kk < 4; ++kk)
               mma<true>(tmem + a * 256, pa + 2 * kk, pb + (BWD ? 256 : 2) * kk, idesc, kk != 0);
-            commit_both(empty(s));
-            commit_both(accf(a));
+            commit_both<true>(accf(a));
+            commit_both<true>(empty(s));
           }
           __syncwarp();
           if (++s == C::S) {
@@ -908,6 +915,78 @@ __global__ void __launch_bounds__(Wide::kThreads, 1)
         warp_wait<0>(fin, 0, W, kErrAcc, lane, false);
       }
       if (!ok || misc[1]) qlk::test_delay(kSettleUs);
+    } else if (warp >= 2) {
+      // ---- products of scales: rows 64 i + 32 (warp - 2) + lane of this CTA's, by both blocks of
+      // the weights.  Groups of four steps, the next one on its way while one is handed out.
+      qlk::grid_dependency_wait();
+      int a = 0, aph = 1, n = 0;
+      bool ok = true;
+      while (ok && sg.next(plan, P.steps, t, k0, k1, slot)) {
+        const Tile T = wide_tile_of(P, plan, t);
+        const int r0 = 32 * (warp - 2) + lane, last = T.rows - 1 - (int)rank * 128;
+        const float *sx[2], *sw[2];
+        const int hop = BWD ? P.kb : 1;
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const int row = max(min(r0 + 64 * i, last), -(int)rank * 128);  // one of the tile's
+          sx[i] = P.sx + (size_t)(T.m0 + (int)rank * 128 + row) * P.steps;
+          const int rb = min(T.rt * 2 + i, (BWD ? P.kb : P.nb) - 1);
+          sw[i] = P.sw + (size_t)T.e * P.nb * P.kb + (BWD ? (size_t)rb : (size_t)rb * P.kb);
+        }
+        float v[2][4], w[2][4];
+        auto load = [&](int k) {  // steps k .. k + 3, k a multiple of four
+          if (k >= k1) return;
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+              w[i][j] = __ldg(sw[i] + (size_t)min(k + j, P.steps - 1) * hop);
+            if (P.vec == 4) {
+              const float4 x = __ldcg(reinterpret_cast<const float4*>(sx[i] + k));
+              v[i][0] = x.x;
+              v[i][1] = x.y;
+              v[i][2] = x.z;
+              v[i][3] = x.w;
+            } else if (P.vec == 2) {
+#pragma unroll
+              for (int j = 0; j < 4; j += 2) {
+                const float2 x =
+                    __ldcg(reinterpret_cast<const float2*>(sx[i] + min(k + j, P.steps - 2)));
+                v[i][j] = x.x;
+                v[i][j + 1] = x.y;
+              }
+            } else {
+#pragma unroll
+              for (int j = 0; j < 4; ++j) v[i][j] = __ldcg(sx[i] + min(k + j, P.steps - 1));
+            }
+          }
+        };
+        load(k0 & ~3);
+#pragma unroll 1
+        for (int k = k0 & ~3; ok && k < k1; k += 4) {
+          float f[4][4];
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) f[j][i] = v[i >> 1][j] * w[i & 1][j];
+          load(k + 4);
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            if (k + j < k0 || k + j >= k1) continue;
+            if (n >= C::kAcc && !(ok = warp_wait<256>(sempty(a), aph, W, kErrAcc, lane))) break;
+            float* o = reinterpret_cast<float*>(smem + C::kScaleOff) + a * 256 + r0;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) o[128 * (i & 1) + 64 * (i >> 1)] = f[j][i];
+            __syncwarp();
+            if (lane == 0) qlk::mbar_arrive(accf(a));
+            ++n;
+            if (++a == C::kAcc) {
+              a = 0;
+              aph ^= 1;
+            }
+          }
+        }
+      }
     }
   } else {
     // ---- epilogue: rows 32 q + lane of this CTA's rows of q, columns of group g
@@ -916,68 +995,47 @@ __global__ void __launch_bounds__(Wide::kThreads, 1)
     const int ew = warp - C::kEpiWarp0, q = warp & 3, g = ew >> 2;
     const long long U = (long long)(plan.tiles - plan.whole) * P.steps;
     const uint32_t staging = ring + C::kStagingOff + ew * C::kStaging;
+    const uint32_t tq = tmem + ((uint32_t)(32 * q) << 16) + (uint32_t)(g * 128);
+    const uint32_t sq = ring + C::kScaleOff + 4 * (128 * g + 32 * q + lane);
     int a = 0, aph = 0;
     bool ok = true;
     while (ok && sg.next(plan, P.steps, t, k0, k1, slot)) {
       const Tile T = wide_tile_of(P, plan, t);
-      const int lrow = (int)rank * 128 + 32 * q + lane;  // of the tile
-      const int rb = min(T.rt * 2 + g, (BWD ? P.kb : P.nb) - 1);
-      const float* sw = P.sw + (size_t)T.e * P.nb * P.kb + (BWD ? (size_t)rb : (size_t)rb * P.kb);
-      const int hop = BWD ? P.kb : 1;
-      const float* sx = P.sx + (size_t)(T.m0 + min(lrow, T.rows - 1)) * P.steps;
-      // the scales of the four steps ahead
-      float v[4], w[4];
-      auto load = [&](int k) {
+      float acc[128];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const int kk = min(k + j, k1 - 1);
-          v[j] = __ldcg(sx + kk);
-          w[j] = __ldg(sw + (size_t)kk * hop);
-        }
-      };
-      load(k0);
-      pair_t acc[64];
-#pragma unroll
-      for (int c = 0; c < 64; ++c) acc[c] = 0ull;
+      for (int c = 0; c < 128; ++c) acc[c] = 0.f;
 #pragma unroll 1
-      for (int k = k0; ok && k < k1; k += 4) {
-        float scale[4];
+      for (int k = k0; k < k1; ++k) {
+        if (!(ok = warp_wait<256>(accf(a), aph, W, kErrAcc, lane))) break;
+        tc_fence_after();
+        const uint32_t ta = tq + (uint32_t)(a * 256);
+        uint32_t r[2][32];
+        tmem_ld_32x32(ta, r[0]);
+        const float f = __uint_as_float(qlk::lds32(sq + a * 1024));
 #pragma unroll
-        for (int j = 0; j < 4; ++j) scale[j] = v[j] * w[j];
-        load(k + 4);
-#pragma unroll 1
-        for (int j = 0; j < 4 && k + j < k1; ++j) {
-          if (!(ok = warp_wait<256>(accf(a), aph, W, kErrAcc, lane))) break;
-          tc_fence_after();
-          const uint32_t ta = tmem + ((uint32_t)(32 * q) << 16) + (uint32_t)(a * 256 + g * 128);
-          const float f = j == 0 ? scale[0] : j == 1 ? scale[1] : j == 2 ? scale[2] : scale[3];
-          const pair_t ff = both(f);
-          uint32_t r[2][32];
-          tmem_ld_32x32(ta, r[0]);
-#pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            wait_loads(r[c & 1]);
-            if (c < 3) {
-              tmem_ld_32x32(ta + 32 * (c + 1), r[(c + 1) & 1]);
-            } else {  // the accumulator is free
-              tc_fence_before();
-              __syncwarp();
-              if (lane == 0) {
-                if (leader)
-                  qlk::mbar_arrive(acce(a));
-                else  // (says only when: see arrive_stage in fused_tc.cu)
-                  asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(lead(acce(a)))
-                               : "memory");
-              }
+        for (int c = 0; c < 4; ++c) {
+          wait_loads(r[c & 1]);
+          if (c < 3) {
+            tmem_ld_32x32(ta + 32 * (c + 1), r[(c + 1) & 1]);
+          } else {  // the accumulator is free
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) {
+              if (leader)
+                qlk::mbar_arrive(acce(a));
+              else  // (says only when: see arrive_stage in fused_tc.cu)
+                asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(lead(acce(a)))
+                             : "memory");
+              qlk::mbar_arrive(sempty(a));
             }
+          }
 #pragma unroll
-            for (int i = 0; i < 16; ++i)
-              add_scaled(acc[16 * c + i], r[c & 1][2 * i], r[c & 1][2 * i + 1], ff);
-          }
-          if (++a == C::kAcc) {
-            a = 0;
-            aph ^= 1;
-          }
+          for (int i = 0; i < 32; ++i)
+            acc[32 * c + i] = fmaf(__uint_as_float(r[c & 1][i]), f, acc[32 * c + i]);
+        }
+        if (++a == C::kAcc) {
+          a = 0;
+          aph ^= 1;
         }
       }
       if (!ok) break;
@@ -988,8 +1046,8 @@ __global__ void __launch_bounds__(Wide::kThreads, 1)
         uint8_t* mine = base + (size_t)(2 * blockIdx.x + slot) * kSlot;
 #pragma unroll
         for (int c = 0; c < 32; ++c)
-          __stcg(reinterpret_cast<ulonglong2*>(mine + c * 512),
-                 make_ulonglong2(acc[2 * c], acc[2 * c + 1]));
+          __stcg(reinterpret_cast<float4*>(mine + c * 512),
+                 make_float4(acc[4 * c], acc[4 * c + 1], acc[4 * c + 2], acc[4 * c + 3]));
         __syncwarp();
         const long long ub = (long long)(t - plan.whole) * P.steps;
         const int wf = worker_of(ub, U, plan.runners);
@@ -1003,16 +1061,18 @@ __global__ void __launch_bounds__(Wide::kThreads, 1)
         __syncwarp();
         const int first = run_begin(wf, U, plan.runners) >= ub ? 0 : 1;
 #pragma unroll
-        for (int c = 0; c < 64; ++c) acc[c] = 0ull;
+        for (int c = 0; c < 128; ++c) acc[c] = 0.f;
 #pragma unroll 1
         for (int w2 = wf; w2 <= wl; ++w2) {
           const uint8_t* src =
               base + (size_t)(2 * (w2 * 2 + (int)rank) + (w2 == wf ? first : 0)) * kSlot;
 #pragma unroll
           for (int c = 0; c < 32; ++c) {
-            const ulonglong2 x = __ldcg(reinterpret_cast<const ulonglong2*>(src + c * 512));
-            acc[2 * c] = add_pairs(acc[2 * c], x.x);
-            acc[2 * c + 1] = add_pairs(acc[2 * c + 1], x.y);
+            const float4 x = __ldcg(reinterpret_cast<const float4*>(src + c * 512));
+            acc[4 * c] += x.x;
+            acc[4 * c + 1] += x.y;
+            acc[4 * c + 2] += x.z;
+            acc[4 * c + 3] += x.w;
           }
         }
         if (lane == 0) *counter = 0u;  // ready for the next call
@@ -1028,8 +1088,8 @@ __global__ void __launch_bounds__(Wide::kThreads, 1)
           uint32_t p[4];
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
-            const float2 x = halves(acc[16 * c + 4 * i + j]);
-            p[j] = P.bf16 ? pack2<true>(x.x, x.y) : pack2<false>(x.x, x.y);
+            const float x0 = acc[32 * c + 8 * i + 2 * j], x1 = acc[32 * c + 8 * i + 2 * j + 1];
+            p[j] = P.bf16 ? pack2<true>(x0, x1) : pack2<false>(x0, x1);
           }
           sts128(staging + lane * kTokStride + 16 * i, make_uint4(p[0], p[1], p[2], p[3]));
         }
@@ -1146,6 +1206,9 @@ ql_status launch_as(const Product& p) {
   P.steps = BWD ? P.nb : P.kb;
   P.rtiles = (blocks_of(P.R) + C::kBlocks - 1) / C::kBlocks;
   P.bf16 = p.bf16;
+  P.vec = P.steps % 4 == 0 && (uintptr_t)p.sx % 16 == 0 ? 4
+          : P.steps % 2 == 0 && (uintptr_t)p.sx % 8 == 0 ? 2
+                                                         : 1;
   // no more tiles than these, whatever the offsets
   const long long tiles = (long long)P.rtiles * (p.offsets ? p.M / C::BNX + (p.E < p.M ? p.E : p.M)
                                                            : (p.M + C::BNX - 1) / C::BNX);
