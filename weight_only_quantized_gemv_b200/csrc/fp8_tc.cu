@@ -72,9 +72,10 @@ struct Cfg {
   static constexpr int kThreads = 32 * kWarps;
   static constexpr int kAcc = 4;   // accumulators
   static constexpr uint32_t kTmemCols = kAcc * BNX;
-  // Narrow tiles: stages for two CTAs on an SM, so that the next call's weights are on their way
-  // while this one ends.
-  static constexpr int kBudget = PAIR ? 200 * 1024 : 110 * 1024;
+  // Up to 64 rows of q a call is bound by reading the weights: two CTAs on an SM keep more of them
+  // on their way, and where one is enough the next call's first weights come while this one ends.
+  static constexpr int kPerSm = PAIR ? 1 : 2;
+  static constexpr int kBudget = PAIR ? 200 * 1024 : 104 * 1024;
   static constexpr int S = kBudget / kStageBytes < 8 ? kBudget / kStageBytes : 8;
   static constexpr int kStagingOff = S * kStageBytes;
   static constexpr int kStaging = 16 * kTokStride;           // per epilogue warp
@@ -86,7 +87,7 @@ struct Cfg {
   static constexpr int kTableOff = kMiscOff + 16;            // start[E + 1], tiles before [E + 1]
   static constexpr int smem(int E) { return kTableOff + 8 * (E + 1); }
   static constexpr int kMaxSmem = kTableOff + 8 * (kMaxExperts + 1);
-  static_assert(kMaxSmem <= 232448, "shared memory");
+  static_assert(kPerSm * (kTableOff + 8 * 256 + 1024) <= 233472, "shared memory");
 };
 
 struct Params {
@@ -388,7 +389,7 @@ struct Maps {
 };
 
 template <int BNX, bool PAIR, bool BWD>
-__global__ void __launch_bounds__(Cfg<BNX, PAIR>::kThreads, PAIR ? 1 : 2)
+__global__ void __launch_bounds__(Cfg<BNX, PAIR>::kThreads, Cfg<BNX, PAIR>::kPerSm)
     fp8_tc_kernel(const Params P, const __grid_constant__ Maps maps) {
   using C = Cfg<BNX, PAIR>;
   extern __shared__ __align__(1024) uint8_t smem[];
@@ -765,7 +766,7 @@ __global__ void __launch_bounds__(Cfg<BNX, PAIR>::kThreads, PAIR ? 1 : 2)
 // of the weights: a step has one product of scales per thread.
 
 struct Wide {
-  static constexpr int BNX = 256, kCtas = 2, kBlocks = 2, kBRows = 128;
+  static constexpr int BNX = 256, kCtas = 2, kBlocks = 2, kBRows = 128, kPerSm = 1;
   static constexpr int kBytes = 128 * 128;         // of an operand, per CTA and step
   static constexpr int S = 6, kStageBytes = 2 * kBytes;
   static constexpr int kEpiWarps = 8, kEpiWarp0 = 4;
@@ -1153,6 +1154,7 @@ void launch_config(cudaLaunchConfig_t* cfg, cudaLaunchAttribute* attr, unsigned 
 }
 
 using Kernel = void (*)(const Params, const Maps);
+constexpr int kLongRun = 16;
 
 // Workers resident at once, once per kernel and device.
 template <class C, Kernel kernel>
@@ -1171,6 +1173,8 @@ int resident_workers(int dev, int sms) {
     cfg.numAttrs = 1;
     if (cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) != cudaSuccess) n = 0;
   } else {
+    // (the query answers 1 for every kernel that allocates tensor memory; two do run at once, as
+    // timestamps show, and nothing rests on it)
     int occ = 0;
     n = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&occ, kernel, C::kThreads, C::kMaxSmem) ==
                     cudaSuccess && occ >= 1
@@ -1214,9 +1218,11 @@ ql_status launch_as(const Product& p) {
                                                            : (p.M + C::BNX - 1) / C::BNX);
   if (tiles >= (1LL << 31) || (long long)p.N * p.K >= (1LL << 40)) return QL_ERR_SHAPE;
   // (fewer tiles than workers are split)
-  if ((size_t)maxw * C::kCtas * C::kEpiWarps * sizeof(uint32_t) > qfused::kTcCounterBytes)
+  if ((size_t)C::kPerSm * maxw * C::kCtas * C::kEpiWarps * sizeof(uint32_t) >
+      qfused::kTcCounterBytes)
     return QL_ERR_UNSUPPORTED;
-  if (p.partial_bytes < (size_t)2 * sms * 128 * C::BNX * sizeof(float)) return QL_ERR_WORKSPACE;
+  if (p.partial_bytes < (size_t)2 * C::kPerSm * sms * 128 * C::BNX * sizeof(float))
+    return QL_ERR_WORKSPACE;
   const qfused::WaitTest wt = qfused::wait_test();
   P.wait_us = (wt.limit_us < 1000000000u ? wt.limit_us : 1000000000u) + 4u * (uint32_t)P.steps;
   P.test_us = wt.delays;
@@ -1226,9 +1232,11 @@ ql_status launch_as(const Product& p) {
   if (!encode(&maps.w, p.w, 3, wdims, 128)) return QL_ERR_CUDA;
   for (int i = 0; i < 4; ++i)
     if ((128 >> i) <= C::kBRows && !encode(&maps.q[i], p.q, 2, qdims, 128 >> i)) return QL_ERR_CUDA;
-  // every worker that can run: how many have work is known on the device
+  // every worker that can run: how many have work is known on the device.  A second CTA on each SM
+  // where both have kLongRun steps and more
   const long long units = tiles * P.steps;
-  const int workers = units < maxw ? (int)units : maxw;
+  const int most = units >= (long long)2 * maxw * kLongRun && p.E < 256 ? C::kPerSm * maxw : maxw;
+  const int workers = units < most ? (int)units : most;
   cudaLaunchConfig_t cfg;
   cudaLaunchAttribute attr[2];
   launch_config<C>(&cfg, attr, (unsigned)(workers * C::kCtas), p.E, p.stream);
@@ -1254,8 +1262,8 @@ ql_status launch(const Product& p) {
 
 namespace qfp8 {
 
-// Two fp32 partial tiles of 128 rows per CTA, of the widest tile that a call with at most M rows
-// has.
+// Two fp32 partial tiles of 128 rows per CTA (two CTAs to an SM up to 64 rows), of the widest tile
+// that a call with at most M rows has.
 size_t product_partial_bytes(int M, int E) {
   int dev = 0, sms = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return 0;
@@ -1263,7 +1271,7 @@ size_t product_partial_bytes(int M, int E) {
   const int rows = (M + E - 1) / E;
   int bn = 16;
   while (bn < 256 && bn < rows) bn *= 2;
-  return (size_t)2 * sms * 128 * bn * sizeof(float);
+  return (size_t)2 * sms * 128 * (bn <= 128 ? 128 : bn) * sizeof(float);
 }
 
 ql_status launch_product(const Product& p) {

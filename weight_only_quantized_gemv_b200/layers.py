@@ -659,22 +659,31 @@ def _raw_stream(stream, index: int):
     return _current_stream(index) if stream is None else getattr(stream, "cuda_stream", stream)
 
 
-def _new(like: torch.Tensor, shape: tuple, dtype, index: int, stream) -> torch.Tensor:
+_empties: dict = {}  # (dtype, device index): an empty tensor, from which new ones are quickest made
+
+
+def _new(shape: tuple, dtype, index: int, stream) -> torch.Tensor:
     """A new tensor on the call's stream."""
+    like = _empties.get((dtype, index))
+    if like is None:
+        like = _empties[dtype, index] = torch.empty(0, dtype=dtype, device=f"cuda:{index}")
     if stream is None:
-        return like.new_empty(shape, dtype=dtype)
+        return like.new_empty(shape)
     with torch.cuda.stream(_as_stream(stream, index)):
-        return like.new_empty(shape, dtype=dtype)
+        return like.new_empty(shape)
 
 
-def _codes_out(like, q, scales, M: int, C: int, index: int, stream) -> tuple:
-    """Codes [M, C] and scales, made where they are not given."""
+def _codes_out(q, scales, M: int, C: int, index: int, stream) -> tuple:
+    """Codes [M, C] and scales, made where they are not given, and their data pointers."""
     if q is None:
-        q = _new(like, (M, C), _F8, index, stream)
+        q = _new((M, C), _F8, index, stream)
+        pq = q.data_ptr()
+    else:
+        pq = _fused_ptr(q, (M, C), index, "q", _F8)
     if scales is None:
-        scales = _new(like, (M, _blocks(C)), _F32, index, stream)
-    return (q, scales, _fused_ptr(q, (M, C), index, "q", _F8),
-            _fused_ptr(scales, (M, _blocks(C)), index, "scales", _F32))
+        scales = _new((M, (C + 127) // 128), _F32, index, stream)
+        return q, scales, pq, scales.data_ptr()
+    return q, scales, pq, _fused_ptr(scales, (M, (C + 127) // 128), index, "scales", _F32)
 
 
 def _on_device(index: int, method, *args):
@@ -691,7 +700,7 @@ def fp8_quantize(x: torch.Tensor, q: Optional[torch.Tensor] = None,
     if torch.cuda.current_device() != index:
         return _on_device(index, fp8_quantize, x, q, scales, stream)
     px, ldx = _row_ptr(x, index, "x")
-    q, scales, pq, ps = _codes_out(x, q, scales, M, K, index, stream)
+    q, scales, pq, ps = _codes_out(q, scales, M, K, index, stream)
     if M:
         _check(_lib.qlinear_fp8_quantize(kind, px, ldx, pq, ps, M, K, _raw_stream(stream, index)),
                "qlinear_fp8_quantize")
@@ -708,7 +717,7 @@ def fp8_gated(gu: torch.Tensor, act: str = "silu", q: Optional[torch.Tensor] = N
     if C % 2:
         raise ValueError("gu holds gate and up values, 2 F columns")
     pgu = _fused_ptr(gu, (M, C), index, "gu", gu.dtype)
-    q, scales, pq, ps = _codes_out(gu, q, scales, M, C // 2, index, stream)
+    q, scales, pq, ps = _codes_out(q, scales, M, C // 2, index, stream)
     if M:
         _check(_lib.qlinear_fp8_gated(kind, _act(act), pgu, pq, ps, M, C // 2,
                                       _raw_stream(stream, index)), "qlinear_fp8_gated")
@@ -727,7 +736,7 @@ def fp8_gated_backward(dh: torch.Tensor, gu: torch.Tensor, act: str = "silu",
         raise ValueError("gu holds gate and up values, 2 F columns")
     pgu = _fused_ptr(gu, (M, C), index, "gu", gu.dtype)
     pdh = _fused_ptr(dh, (M, C // 2), index, "dh", gu.dtype)
-    q, scales, pq, ps = _codes_out(gu, q, scales, M, C, index, stream)
+    q, scales, pq, ps = _codes_out(q, scales, M, C, index, stream)
     if M:
         _check(_lib.qlinear_fp8_gated_backward(kind, _act(act), pdh, pgu, pq, ps, M, C // 2,
                                                _raw_stream(stream, index)),
@@ -744,8 +753,8 @@ def fp8_quantize_weights(w: torch.Tensor, stream=None) -> tuple:
     *lead, N, K = w.shape
     with torch.cuda.device(index):
         _fused_ptr(w, w.shape, index, "w", w.dtype)
-        codes = _new(w, w.shape, _F8, index, stream)
-        scales = _new(w, (*lead, _blocks(N), _blocks(K)), _F32, index, stream)
+        codes = _new(w.shape, _F8, index, stream)
+        scales = _new((*lead, _blocks(N), _blocks(K)), _F32, index, stream)
         qlinear_fp8_quantize_weights(kind, w, codes, scales, lead[0] if lead else 1, N, K, stream)
     return codes, scales
 
@@ -787,7 +796,7 @@ class RMSNorm(_FusedWorkspace):
         if x.dtype is not dtype or x.dim() != 2 or x.shape[1] != K or x.get_device() != index:
             _fused_ptr(x, (M, K), index, "x", dtype)
         px, ldx = _row_ptr(x, index, "x")
-        q, scales, pq, ps = _codes_out(x, q, scales, M, K, index, stream)
+        q, scales, pq, ps = _codes_out(q, scales, M, K, index, stream)
         head = (_TYPE_OF[dtype], px, ldx, _fused_ptr(residual, (M, K), index, "residual", dtype),
                 weight.data_ptr(), self.eps, _fused_ptr(total, (M, K), index, "total", dtype),
                 _fused_ptr(y, (M, K), index, "y", dtype), pq, ps,
@@ -857,6 +866,10 @@ class _Fp8Weights(_FusedWorkspace):
         self._fused = (None, N, K, self.codes.get_device())
 
     @property
+    def _pointers(self) -> tuple:
+        return self.codes.data_ptr(), self.scales.data_ptr()
+
+    @property
     def weight_bytes(self) -> int:
         return self.codes.numel() + 4 * self.scales.numel()
 
@@ -873,15 +886,18 @@ class _Fp8Weights(_FusedWorkspace):
         index = self._fused[3]
         M = q.shape[0]
         pq = _fused_ptr(q, (M, C), index, "q", _F8)
-        if out is None:
-            out = _new(q, (M, R), dtype, index, stream)
-        kind = _TYPE_OF.get(out.dtype)
+        if out is not None:
+            dtype = out.dtype
+        kind = _TYPE_OF.get(dtype)
         if kind is None:
-            raise ValueError(f"{what} is a float16 or bfloat16 tensor, not {out.dtype}")
+            raise ValueError(f"{what} is a float16 or bfloat16 tensor, not {dtype}")
+        if out is None:
+            out = _new((M, R), dtype, index, stream)
+            pout = out.data_ptr()
+        else:
+            pout = _fused_ptr(out, (M, R), index, what, dtype)
         head = (kind, pq, _fused_ptr(scales, (M, (C + 127) // 128), index, "scales", _F32),
-                *offsets, self.codes.data_ptr(), self.scales.data_ptr(),
-                _fused_ptr(out, (M, R), index, what, out.dtype), M,
-                *((self.E,) if offsets else ()), self.N, self.K)
+                *offsets, *self._pointers, pout, M, *((self.E,) if offsets else ()), self.N, self.K)
         if M:
             self._fused_call(entry, name, head, M, backward, workspace, stream)
         return out
