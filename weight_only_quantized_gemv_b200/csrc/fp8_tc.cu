@@ -774,12 +774,12 @@ struct Wide {
   static constexpr int kAcc = 2;
   static constexpr int kStagingOff = S * kStageBytes;
   static constexpr int kStaging = 32 * kTokStride; // per epilogue warp: 32 rows of 32 columns
-  static constexpr int kScaleWarps = 2;
+  static constexpr int kScaleWarps = 1;
   static constexpr int kScaleOff = kStagingOff + kEpiWarps * kStaging;  // [kAcc][2 blocks][128 rows]
   static constexpr int kBarOff = kScaleOff + kAcc * 256 * 4;
-  // full[S] empty[S] accf[2] acce[2] sempty[2] fin
-  static constexpr int kBars = 2 * S + 3 * kAcc + 1;
-  static constexpr int kMiscOff = kBarOff + 8 * kBars + 8;
+  // full[S] empty[S] accf[2] acce[2] sempty[2] fin[2]
+  static constexpr int kBars = 2 * S + 4 * kAcc;
+  static constexpr int kMiscOff = kBarOff + 8 * kBars;
   static constexpr int kTableOff = kMiscOff + 16;
   static constexpr int smem(int E) { return kTableOff + 8 * (E + 1); }
   static constexpr int kMaxSmem = kTableOff + 8 * (kMaxExperts + 1);
@@ -801,7 +801,6 @@ __global__ void __launch_bounds__(Wide::kThreads, 1)
   auto accf = [&](int a) { return bars + 8 * (2 * C::S + a); };
   auto acce = [&](int a) { return bars + 8 * (2 * C::S + C::kAcc + a); };
   auto sempty = [&](int a) { return bars + 8 * (2 * C::S + 2 * C::kAcc + a); };
-  const uint32_t fin = bars + 8 * (2 * C::S + 3 * C::kAcc);
   volatile uint32_t* misc = reinterpret_cast<volatile uint32_t*>(smem + C::kMiscOff);
   int* const start = reinterpret_cast<int*>(smem + C::kTableOff);
   int* const pre = start + P.E + 1;
@@ -822,8 +821,8 @@ __global__ void __launch_bounds__(Wide::kThreads, 1)
       qlk::mbar_init(accf(a), 1 + C::kScaleWarps);
       qlk::mbar_init(acce(a), 2 * C::kEpiWarps);
       qlk::mbar_init(sempty(a), C::kEpiWarps);
+      qlk::mbar_init(bars + 8 * (2 * C::S + 3 * C::kAcc + a), 1);  // fin
     }
-    qlk::mbar_init(fin, 1);
     misc[1] = 0u;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
@@ -877,107 +876,104 @@ __global__ void __launch_bounds__(Wide::kThreads, 1)
             wait<0>(full(i % C::S), (i / C::S) & 1, W, kErrStage, false);
         if (!ok) qlk::test_delay(kSettleUs);
       }
-    } else if (warp == 1 && leader) {
-      // ---- MMA issue
-      qlk::grid_dependency_wait();
-      if ((P.test_us >> 16) && wk == 0) qlk::test_delay(P.test_us >> 16);
-      constexpr uint32_t idesc = idesc_f16(256, 256) | (BWD ? kTransposeB : 0u);
-      int s = 0, ph = 0, a = 0, aph = 1, n = 0;
-      bool ok = true;
-      while (ok && sg.next(plan, P.steps, t, k0, k1, slot)) {
+    } else if (warp & 1) {
+      // ---- MMA issue by the leader: warp 1 the even steps, warp 3 the odd ones, an accumulator each.
+      // What a warp takes to see its barriers complete and to issue is then hidden behind the other
+      // step's MMAs.
+      if (leader) {
+        qlk::grid_dependency_wait();
+        if ((P.test_us >> 16) && wk == 0) qlk::test_delay(P.test_us >> 16);
+        constexpr uint32_t idesc = idesc_f16(256, 256) | (BWD ? kTransposeB : 0u);
+        const int a = warp >> 1;
+        const uint32_t fin = bars + 8 * (2 * C::S + 3 * C::kAcc + a);
+        int s = a, ph = 0, aph = 1, n = 0;
+        bool ok = true, mine = a == 0;
+        while (ok && sg.next(plan, P.steps, t, k0, k1, slot)) {
 #pragma unroll 1
-        for (int k = k0; k < k1; ++k, ++n) {
-          if (!(ok = warp_wait<256>(full(s), ph, W, kErrStage, lane))) break;
-          if (n >= C::kAcc && !(ok = warp_wait<256>(acce(a), aph, W, kErrAcc, lane))) break;
-          tc_fence_after();
-          const uint32_t pa = ((ring + s * C::kStageBytes) >> 4) | kDescLo;
-          const uint32_t pb = pa + (C::kBytes >> 4);
-          if (elect_one()) {
+          for (int k = k0; k < k1; ++k, mine = !mine) {
+            if (!mine) continue;
+            if (!(ok = warp_wait<0>(full(s), ph, W, kErrStage, lane))) break;
+            if (n > 0 && !(ok = warp_wait<0>(acce(a), aph, W, kErrAcc, lane))) break;
+            tc_fence_after();
+            const uint32_t pa = ((ring + s * C::kStageBytes) >> 4) | kDescLo;
+            const uint32_t pb = pa + (C::kBytes >> 4);
+            if (elect_one()) {
 #pragma unroll
-            for (int kk = 0; kk < 4; ++kk)
-              mma<true>(tmem + a * 256, pa + 2 * kk, pb + (BWD ? 256 : 2) * kk, idesc, kk != 0);
-            commit_both<true>(accf(a));
-            commit_both<true>(empty(s));
-          }
-          __syncwarp();
-          if (++s == C::S) {
-            s = 0;
-            ph ^= 1;
-          }
-          if (++a == C::kAcc) {
-            a = 0;
+              for (int kk = 0; kk < 4; ++kk)
+                mma<true>(tmem + a * 256, pa + 2 * kk, pb + (BWD ? 256 : 2) * kk, idesc, kk != 0);
+              commit_both<true>(accf(a));
+              commit_both<true>(empty(s));
+            }
+            __syncwarp();
+            ++n;
             aph ^= 1;
+            if ((s += 2) >= C::S) {
+              s -= C::S;
+              ph ^= 1;
+            }
           }
         }
+        if (n > 0) {
+          if (elect_one()) tc_commit<true>(fin);
+          __syncwarp();
+          warp_wait<0>(fin, 0, W, kErrAcc, lane, false);
+        }
+        if (!ok || misc[1]) qlk::test_delay(kSettleUs);
       }
-      if (n > 0) {
-        if (elect_one()) tc_commit<true>(fin);
-        __syncwarp();
-        warp_wait<0>(fin, 0, W, kErrAcc, lane, false);
-      }
-      if (!ok || misc[1]) qlk::test_delay(kSettleUs);
-    } else if (warp >= 2) {
-      // ---- products of scales: rows 64 i + 32 (warp - 2) + lane of this CTA's, by both blocks of
-      // the weights.  Groups of four steps, the next one on its way while one is handed out.
+    } else {
+      // ---- products of scales: rows 32 i + lane of this CTA's, by both blocks of the weights.  Two
+      // steps at a time, the next two on their way while they are handed out.
       qlk::grid_dependency_wait();
       int a = 0, aph = 1, n = 0;
       bool ok = true;
       while (ok && sg.next(plan, P.steps, t, k0, k1, slot)) {
         const Tile T = wide_tile_of(P, plan, t);
-        const int r0 = 32 * (warp - 2) + lane, last = T.rows - 1 - (int)rank * 128;
-        const float *sx[2], *sw[2];
+        const int last = T.rows - 1 - (int)rank * 128, least = -(int)rank * 128;
+        const float* sx = P.sx + (size_t)(T.m0 - least) * P.steps;
+        int row[4];  // of the tile's rows, in scales
+#pragma unroll
+        for (int i = 0; i < 4; ++i) row[i] = max(min(lane + 32 * i, last), least) * P.steps;
+        // the blocks of the weights (the second may lie behind the last: any scale does)
+        const float* sw =
+            P.sw + (size_t)T.e * P.nb * P.kb + (size_t)(2 * T.rt) * (BWD ? 1 : P.kb);
+        const int other = 2 * T.rt + 1 < (BWD ? P.kb : P.nb) ? (BWD ? 1 : P.kb) : 0;
         const int hop = BWD ? P.kb : 1;
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const int row = max(min(r0 + 64 * i, last), -(int)rank * 128);  // one of the tile's
-          sx[i] = P.sx + (size_t)(T.m0 + (int)rank * 128 + row) * P.steps;
-          const int rb = min(T.rt * 2 + i, (BWD ? P.kb : P.nb) - 1);
-          sw[i] = P.sw + (size_t)T.e * P.nb * P.kb + (BWD ? (size_t)rb : (size_t)rb * P.kb);
-        }
-        float v[2][4], w[2][4];
-        auto load = [&](int k) {  // steps k .. k + 3, k a multiple of four
+        float v[4][2], w[2][2];
+        auto load = [&](int k) {  // steps k, k + 1, k even
           if (k >= k1) return;
+          const int k2 = min(k + 1, P.steps - 1);
+          w[0][0] = __ldg(sw + (size_t)k * hop);
+          w[0][1] = __ldg(sw + (size_t)k2 * hop);
+          w[1][0] = __ldg(sw + other + (size_t)k * hop);
+          w[1][1] = __ldg(sw + other + (size_t)k2 * hop);
 #pragma unroll
-          for (int i = 0; i < 2; ++i) {
-#pragma unroll
-            for (int j = 0; j < 4; ++j)
-              w[i][j] = __ldg(sw[i] + (size_t)min(k + j, P.steps - 1) * hop);
-            if (P.vec == 4) {
-              const float4 x = __ldcg(reinterpret_cast<const float4*>(sx[i] + k));
+          for (int i = 0; i < 4; ++i) {
+            if (P.vec == 2) {
+              const float2 x = __ldcg(reinterpret_cast<const float2*>(sx + row[i] + k));
               v[i][0] = x.x;
               v[i][1] = x.y;
-              v[i][2] = x.z;
-              v[i][3] = x.w;
-            } else if (P.vec == 2) {
-#pragma unroll
-              for (int j = 0; j < 4; j += 2) {
-                const float2 x =
-                    __ldcg(reinterpret_cast<const float2*>(sx[i] + min(k + j, P.steps - 2)));
-                v[i][j] = x.x;
-                v[i][j + 1] = x.y;
-              }
             } else {
-#pragma unroll
-              for (int j = 0; j < 4; ++j) v[i][j] = __ldcg(sx[i] + min(k + j, P.steps - 1));
+              v[i][0] = __ldcg(sx + row[i] + k);
+              v[i][1] = __ldcg(sx + row[i] + k2);
             }
           }
         };
-        load(k0 & ~3);
+        load(k0 & ~1);
 #pragma unroll 1
-        for (int k = k0 & ~3; ok && k < k1; k += 4) {
-          float f[4][4];
+        for (int k = k0 & ~1; ok && k < k1; k += 2) {
+          float f[2][8];  // [step][block of the weights, row]
 #pragma unroll
-          for (int j = 0; j < 4; ++j)
+          for (int j = 0; j < 2; ++j)
 #pragma unroll
-            for (int i = 0; i < 4; ++i) f[j][i] = v[i >> 1][j] * w[i & 1][j];
-          load(k + 4);
+            for (int i = 0; i < 8; ++i) f[j][i] = v[i & 3][j] * w[i >> 2][j];
+          load(k + 2);
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
+          for (int j = 0; j < 2; ++j) {
             if (k + j < k0 || k + j >= k1) continue;
-            if (n >= C::kAcc && !(ok = warp_wait<256>(sempty(a), aph, W, kErrAcc, lane))) break;
-            float* o = reinterpret_cast<float*>(smem + C::kScaleOff) + a * 256 + r0;
+            if (n >= C::kAcc && !(ok = warp_wait<0>(sempty(a), aph, W, kErrAcc, lane))) break;
+            float* o = reinterpret_cast<float*>(smem + C::kScaleOff) + a * 256 + lane;
 #pragma unroll
-            for (int i = 0; i < 4; ++i) o[128 * (i & 1) + 64 * (i >> 1)] = f[j][i];
+            for (int i = 0; i < 8; ++i) o[32 * i] = f[j][i];
             __syncwarp();
             if (lane == 0) qlk::mbar_arrive(accf(a));
             ++n;
@@ -1007,7 +1003,7 @@ __global__ void __launch_bounds__(Wide::kThreads, 1)
       for (int c = 0; c < 128; ++c) acc[c] = 0.f;
 #pragma unroll 1
       for (int k = k0; k < k1; ++k) {
-        if (!(ok = warp_wait<256>(accf(a), aph, W, kErrAcc, lane))) break;
+        if (!(ok = warp_wait<0>(accf(a), aph, W, kErrAcc, lane))) break;
         tc_fence_after();
         const uint32_t ta = tq + (uint32_t)(a * 256);
         uint32_t r[2][32];
@@ -1210,9 +1206,7 @@ ql_status launch_as(const Product& p) {
   P.steps = BWD ? P.nb : P.kb;
   P.rtiles = (blocks_of(P.R) + C::kBlocks - 1) / C::kBlocks;
   P.bf16 = p.bf16;
-  P.vec = P.steps % 4 == 0 && (uintptr_t)p.sx % 16 == 0 ? 4
-          : P.steps % 2 == 0 && (uintptr_t)p.sx % 8 == 0 ? 2
-                                                         : 1;
+  P.vec = P.steps % 2 == 0 && (uintptr_t)p.sx % 8 == 0 ? 2 : 1;
   // no more tiles than these, whatever the offsets
   const long long tiles = (long long)P.rtiles * (p.offsets ? p.M / C::BNX + (p.E < p.M ? p.E : p.M)
                                                            : (p.M + C::BNX - 1) / C::BNX);
