@@ -53,30 +53,23 @@ namespace {
 constexpr uint32_t kErrStage = 1u, kErrAcc = 2u, kErrOffsets = 4u;
 constexpr int kTokStride = 80;  // bytes of a staged row of q's outputs: 32 of them and 16 more
 
-template <int BNX_, bool PAIR_>
+template <int BNX_>
 struct Cfg {
   static constexpr int BNX = BNX_;                 // most rows of q per tile
-  static constexpr bool PAIR = PAIR_;
-  static constexpr int kCtas = PAIR ? 2 : 1, kBlocks = kCtas;
-  static constexpr int kGran = 16 * kCtas;         // a tile's rows of q: a multiple
-  static constexpr int kBRows = BNX / kCtas;       // most that one CTA copies
+  static constexpr int kCtas = 1, kBlocks = 1;
+  static constexpr int kGran = 16;                 // a tile's rows of q: a multiple
+  static constexpr int kBRows = BNX;
   static constexpr int kABytes = 128 * 128;
-  static constexpr int kBBytes = kBRows * 128;
+  static constexpr int kBBytes = BNX * 128;
   static constexpr int kStageBytes = kABytes + kBBytes;
-  static constexpr int kGroups = BNX > 64 ? 2 : 1; // column groups of the accumulator
-  static constexpr int kCols = BNX / kGroups;      // most columns of a group
-  static constexpr int kEpiWarps = 4 * kGroups;
-  static constexpr int kScaleWarps = BNX > 64 ? 2 : 1;
-  static constexpr int kEpiWarp0 = 4;
-  static constexpr int kWarps = kEpiWarp0 + kEpiWarps;
-  static constexpr int kThreads = 32 * kWarps;
-  static constexpr int kAcc = 4;   // accumulators
+  static constexpr int kEpiWarps = 4, kEpiWarp0 = 4;
+  static constexpr int kThreads = 32 * (kEpiWarp0 + kEpiWarps);
+  static constexpr int kAcc = 4;                   // accumulators
   static constexpr uint32_t kTmemCols = kAcc * BNX;
-  // Up to 64 rows of q a call is bound by reading the weights: two CTAs on an SM keep more of them
-  // on their way, and where one is enough the next call's first weights come while this one ends.
-  static constexpr int kPerSm = PAIR ? 1 : 2;
-  static constexpr int kBudget = PAIR ? 200 * 1024 : 104 * 1024;
-  static constexpr int S = kBudget / kStageBytes < 8 ? kBudget / kStageBytes : 8;
+  // A call is bound by reading the weights: two CTAs on an SM keep more of them on their way, and
+  // where one is enough the next call's first weights come while this one ends.
+  static constexpr int kPerSm = 2;
+  static constexpr int S = 104 * 1024 / kStageBytes;
   static constexpr int kStagingOff = S * kStageBytes;
   static constexpr int kStaging = 16 * kTokStride;           // per epilogue warp
   static constexpr int kScaleOff = kStagingOff + kEpiWarps * kStaging;
@@ -230,15 +223,17 @@ struct Segments {
 };
 
 // The R tiles behind the whole waves, over `runners` workers: each in f equal parts (f workers to a
-// tile), or where that would leave many workers idle in W equal runs.
+// tile), or (RUNS) where that would leave many workers idle in W equal runs.  A call that is bound by
+// reading the weights has no use for runs: fewer workers read as fast, and sums of parts cost.
 constexpr int kMaxParts = 8;
+template <bool RUNS>
 __device__ __forceinline__ void schedule(Plan& p, int steps, int W) {
   const int R = p.tiles % W;
   p.whole = p.tiles - R;
   p.runners = 0;
   if (R == 0) return;
   const int f = min(min(W / R, steps), kMaxParts);
-  if (f < kMaxParts && 100 * R * f < 85 * W && (long long)R * steps >= W)
+  if (RUNS && f < kMaxParts && 100 * R * f < 85 * W && (long long)R * steps >= W)
     p.runners = W;
   else
     p.runners = R * f;
@@ -388,10 +383,10 @@ struct Maps {
   CUtensorMap w, q[4];
 };
 
-template <int BNX, bool PAIR, bool BWD>
-__global__ void __launch_bounds__(Cfg<BNX, PAIR>::kThreads, Cfg<BNX, PAIR>::kPerSm)
+template <int BNX, bool BWD>
+__global__ void __launch_bounds__(Cfg<BNX>::kThreads, Cfg<BNX>::kPerSm)
     fp8_tc_kernel(const Params P, const __grid_constant__ Maps maps) {
-  using C = Cfg<BNX, PAIR>;
+  using C = Cfg<BNX>;
   extern __shared__ __align__(1024) uint8_t smem[];
   const uint32_t ring = qlk::smem_addr(smem);  // 1024-byte aligned, as the swizzle wants
   const uint32_t bars = ring + C::kBarOff;
@@ -407,11 +402,7 @@ __global__ void __launch_bounds__(Cfg<BNX, PAIR>::kThreads, Cfg<BNX, PAIR>::kPer
   const WaitCtx W{ring + C::kMiscOff + 4, P.err, P.wait_us};
   const int warp = __shfl_sync(0xffffffffu, (int)(threadIdx.x >> 5), 0);  // uniform
   const int lane = threadIdx.x & 31;
-  const uint32_t rank = PAIR ? blockIdx.x & 1u : 0u;  // of the cluster (2, 1, 1)
-  const bool leader = rank == 0;
-  const int wk = PAIR ? (int)(blockIdx.x >> 1) : (int)blockIdx.x;
-  const int nwk = PAIR ? (int)(gridDim.x >> 1) : (int)gridDim.x;
-  auto lead = [&](uint32_t b) { return (PAIR && !leader) ? cluster_addr(b, 0) : b; };
+  const int wk = (int)blockIdx.x, nwk = (int)gridDim.x;
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < C::S; ++s) {
@@ -419,8 +410,8 @@ __global__ void __launch_bounds__(Cfg<BNX, PAIR>::kThreads, Cfg<BNX, PAIR>::kPer
       qlk::mbar_init(empty(s), 1);
     }
     for (int a = 0; a < C::kAcc; ++a) {
-      qlk::mbar_init(accf(a), 1 + C::kScaleWarps);
-      qlk::mbar_init(acce(a), C::kCtas * C::kEpiWarps);
+      qlk::mbar_init(accf(a), 2);  // the MMAs, the scales
+      qlk::mbar_init(acce(a), C::kEpiWarps);
       qlk::mbar_init(sempty(a), C::kEpiWarps);
     }
     qlk::mbar_init(fin, 1);
@@ -428,8 +419,8 @@ __global__ void __launch_bounds__(Cfg<BNX, PAIR>::kThreads, Cfg<BNX, PAIR>::kPer
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   if (warp == 0) make_table<BNX>(P, start, pre, lane);
-  sync_all<PAIR>();  // barriers are set up (a pair's allocation also wants both CTAs running)
-  if (warp == 1) tmem_alloc<PAIR>(ring + C::kMiscOff, C::kTmemCols);
+  sync_all<false>();
+  if (warp == 1) tmem_alloc<false>(ring + C::kMiscOff, C::kTmemCols);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -437,7 +428,7 @@ __global__ void __launch_bounds__(Cfg<BNX, PAIR>::kThreads, Cfg<BNX, PAIR>::kPer
   qlk::grid_dependents_launch();  // (behind the allocation: the next grid's must not come first)
 
   Plan plan{start, pre, pre[P.E], 0, 0};
-  schedule(plan, P.steps, nwk);
+  schedule<false>(plan, P.steps, nwk);
   Segments sg;
   sg.init(plan, P.steps, wk, nwk);
   int t, k0, k1, slot = 0;
@@ -453,12 +444,11 @@ __global__ void __launch_bounds__(Cfg<BNX, PAIR>::kThreads, Cfg<BNX, PAIR>::kPer
           Segments ahead = sg;
           while (n < C::S && ahead.next(plan, P.steps, t, k0, k1, slot)) {
             const Tile T = tile_of<C>(P, plan, t);
-            const int row = (T.rt * C::kCtas + (int)rank) * 128;
+            const int row = T.rt * 128;
             for (int k = k0; k < k1 && n < C::S; ++k, ++n) {
-              if (leader)
-                qlk::mbar_arrive_expect_tx(full(n), C::kCtas * C::kABytes + T.bn * 128);
-              copy_3d<PAIR>(ring + n * C::kStageBytes, &maps.w, BWD ? row : k * 128,
-                            BWD ? k * 128 : row, T.e, lead(full(n)));
+              qlk::mbar_arrive_expect_tx(full(n), C::kABytes + T.bn * 128);
+              copy_3d<false>(ring + n * C::kStageBytes, &maps.w, BWD ? row : k * 128,
+                             BWD ? k * 128 : row, T.e, full(n));
             }
           }
         }
@@ -468,27 +458,21 @@ __global__ void __launch_bounds__(Cfg<BNX, PAIR>::kThreads, Cfg<BNX, PAIR>::kPer
         if ((P.test_us & 0xFFFFu) && wk == 0) qlk::test_delay(P.test_us & 0xFFFFu);
         while (ok && sg.next(plan, P.steps, t, k0, k1, slot)) {
           const Tile T = tile_of<C>(P, plan, t);
-          const int row = (T.rt * C::kCtas + (int)rank) * 128, half = T.bn / C::kCtas;
-          const int m = T.m0 + (int)rank * half;
+          const int row = T.rt * 128;
 #pragma unroll 1
           for (int k = k0; k < k1; ++k) {
             if (n >= C::S && !(ok = wait<64>(empty(s), ph, W, kErrStage))) break;
             const uint32_t a = ring + s * C::kStageBytes, b = a + C::kABytes;
             if (n >= early) {
-              if (leader)
-                qlk::mbar_arrive_expect_tx(full(s), C::kCtas * C::kABytes + T.bn * 128);
-              copy_3d<PAIR>(a, &maps.w, BWD ? row : k * 128, BWD ? k * 128 : row, T.e,
-                            lead(full(s)));
+              qlk::mbar_arrive_expect_tx(full(s), C::kABytes + T.bn * 128);
+              copy_3d<false>(a, &maps.w, BWD ? row : k * 128, BWD ? k * 128 : row, T.e, full(s));
             }
             int at = 0;
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const int rows = 128 >> i;
-              if (rows > C::kBRows || !(half & rows)) continue;
-              if constexpr (PAIR)
-                tma_2d_pair(b + at * 128, &maps.q[i], k * 128, m + at, lead(full(s)));
-              else
-                tma_2d(b + at * 128, &maps.q[i], k * 128, m + at, full(s));
+            for (int i = 0; i < 3; ++i) {  // 64, 32 and 16 rows
+              const int rows = 64 >> i;
+              if (rows > BNX || !(T.bn & rows)) continue;
+              tma_2d(b + at * 128, &maps.q[i + 1], k * 128, T.m0 + at, full(s));
               at += rows;
             }
             ++n;
@@ -498,20 +482,15 @@ __global__ void __launch_bounds__(Cfg<BNX, PAIR>::kThreads, Cfg<BNX, PAIR>::kPer
             }
           }
         }
-        // all stages are handed back (a pair's other CTA gets these arrivals from the leader: none
-        // may be on its way when it exits), and no copy is in flight (the leader's barriers count
-        // both CTAs')
-        const int last = n > early ? n : early;
-        for (int i = n > C::S ? n - C::S : 0; ok && i < n; ++i)
-          ok = wait<0>(empty(i % C::S), (i / C::S) & 1, W, kErrStage);
-        if (leader)
-          for (int i = last > C::S ? last - C::S : 0; i < last; ++i)
-            wait<0>(full(i % C::S), (i / C::S) & 1, W, kErrStage, false);
-        if (PAIR && !ok) qlk::test_delay(kSettleUs);
+        // no copy is in flight at the end.  (Of a stage whose weights came early and whose rows of
+        // q do not any more, since a wait ran out, the bytes on their way have long arrived.)
+        for (int i = n > C::S ? n - C::S : 0; i < n; ++i)
+          wait<0>(full(i % C::S), (i / C::S) & 1, W, kErrStage, false);
+        if (!ok || n < early) qlk::test_delay(kSettleUs);
       }
     } else if (warp == 1) {
-      // ---- MMA issue (the leader of a pair)
-      if (leader) {
+      // ---- MMA issue
+      {
         qlk::grid_dependency_wait();
         if ((P.test_us >> 16) && wk == 0) qlk::test_delay(P.test_us >> 16);
         int s = 0, ph = 0, a = 0, aph = 1, n = 0;
@@ -519,20 +498,20 @@ __global__ void __launch_bounds__(Cfg<BNX, PAIR>::kThreads, Cfg<BNX, PAIR>::kPer
         while (ok && sg.next(plan, P.steps, t, k0, k1, slot)) {
           const Tile T = tile_of<C>(P, plan, t);
           // (the type fields of e4m3 are zeros, as those of fp16 in kind::f16)
-          const uint32_t idesc = idesc_f16(128 * C::kCtas, T.bn) | (BWD ? kTransposeA : 0u);
+          const uint32_t idesc = idesc_f16(128, T.bn) | (BWD ? kTransposeA : 0u);
 #pragma unroll 1
           for (int k = k0; k < k1; ++k, ++n) {
-            if (n >= C::kAcc && !(ok = warp_wait<64, PAIR>(acce(a), aph, W, kErrAcc, lane))) break;
-            if (!(ok = warp_wait<64, PAIR>(full(s), ph, W, kErrStage, lane))) break;
+            if (n >= C::kAcc && !(ok = warp_wait<64>(acce(a), aph, W, kErrAcc, lane))) break;
+            if (!(ok = warp_wait<64>(full(s), ph, W, kErrStage, lane))) break;
             tc_fence_after();
             const uint32_t pa = ((ring + s * C::kStageBytes) >> 4) | kDescLo;
             const uint32_t pb = pa + (C::kABytes >> 4);
             if (elect_one()) {
 #pragma unroll
               for (int kk = 0; kk < 4; ++kk)
-                mma<PAIR>(tmem + a * BNX, pa + (BWD ? 256 : 2) * kk, pb + 2 * kk, idesc, kk != 0);
-              commit_both<PAIR>(empty(s));
-              commit_both<PAIR>(accf(a));
+                mma<false>(tmem + a * BNX, pa + (BWD ? 256 : 2) * kk, pb + 2 * kk, idesc, kk != 0);
+              tc_commit<false>(empty(s));
+              tc_commit<false>(accf(a));
             }
             __syncwarp();
             if (++s == C::S) {
@@ -546,27 +525,25 @@ __global__ void __launch_bounds__(Cfg<BNX, PAIR>::kThreads, Cfg<BNX, PAIR>::kPer
           }
         }
         if (n > 0) {
-          if (elect_one()) tc_commit<PAIR>(fin);
+          if (elect_one()) tc_commit<false>(fin);
           __syncwarp();
           warp_wait<0>(fin, 0, W, kErrAcc, lane, false);
         }
-        if (PAIR && (!ok || misc[1])) qlk::test_delay(kSettleUs);
       }
-    } else if (warp < 2 + C::kScaleWarps) {
-      // ---- products of scales: columns lane + 32 (warp - 2 + kScaleWarps i) of the tile, four steps
-      // in registers while the four before them are handed out
-      constexpr int kPer = (BNX + 32 * C::kScaleWarps - 1) / (32 * C::kScaleWarps), kAhead = 4;
+    } else if (warp == 2) {
+      // ---- products of scales: columns lane + 32 i of the tile, four steps in registers while the
+      // four before them are handed out
+      constexpr int kPer = (BNX + 31) / 32, kAhead = 4;
       qlk::grid_dependency_wait();
       int a = 0, aph = 1, n = 0;
       bool ok = true;
       while (ok && sg.next(plan, P.steps, t, k0, k1, slot)) {
         const Tile T = tile_of<C>(P, plan, t);
-        const int rb = min(T.rt * C::kCtas + (int)rank, (BWD ? P.kb : P.nb) - 1);
+        const int rb = T.rt;
         const float* sw = P.sw + (size_t)T.e * P.nb * P.kb + (BWD ? (size_t)rb : (size_t)rb * P.kb);
         const int hop = BWD ? P.kb : 1;
-        const int c0 = lane + 32 * (warp - 2);
-        const float* sx = P.sx + (size_t)(T.m0 + c0) * P.steps;
-        const size_t skip = (size_t)32 * C::kScaleWarps * P.steps;
+        const float* sx = P.sx + (size_t)(T.m0 + lane) * P.steps;
+        const size_t skip = (size_t)32 * P.steps;
         float v[kPer][kAhead], w[kAhead];
         auto load = [&](int k) {
 #pragma unroll
@@ -575,7 +552,7 @@ __global__ void __launch_bounds__(Cfg<BNX, PAIR>::kThreads, Cfg<BNX, PAIR>::kPer
             w[j] = in ? __ldg(sw + (size_t)(k + j) * hop) : 0.f;
 #pragma unroll
             for (int i = 0; i < kPer; ++i)
-              v[i][j] = in && c0 + 32 * C::kScaleWarps * i < T.rows ? __ldcg(sx + i * skip + k + j)
+              v[i][j] = in && lane + 32 * i < T.rows ? __ldcg(sx + i * skip + k + j)
                                                                     : 0.f;
           }
         };
@@ -592,10 +569,10 @@ __global__ void __launch_bounds__(Cfg<BNX, PAIR>::kThreads, Cfg<BNX, PAIR>::kPer
           for (int j = 0; j < kAhead; ++j) {
             if (k + j >= k1) break;
             if (n >= C::kAcc && !(ok = warp_wait<64>(sempty(a), aph, W, kErrAcc, lane))) break;
-            float* o = reinterpret_cast<float*>(smem + C::kScaleOff) + a * BNX + c0;
+            float* o = reinterpret_cast<float*>(smem + C::kScaleOff) + a * BNX + lane;
 #pragma unroll
             for (int i = 0; i < kPer; ++i)
-              if (c0 + 32 * C::kScaleWarps * i < BNX) o[32 * C::kScaleWarps * i] = s[i][j];
+              if (lane + 32 * i < BNX) o[32 * i] = s[i][j];
             __syncwarp();
             if (lane == 0) qlk::mbar_arrive(accf(a));
             ++n;
@@ -608,18 +585,17 @@ __global__ void __launch_bounds__(Cfg<BNX, PAIR>::kThreads, Cfg<BNX, PAIR>::kPer
       }
     }
   } else {
-    // ---- epilogue: accumulator lanes 32 q .. 32 q + 31, columns of group g
+    // ---- epilogue: accumulator lanes 32 q .. 32 q + 31
     qlk::grid_dependency_wait();
-    constexpr int kChunks = C::kCols / 16;
-    const int ew = warp - C::kEpiWarp0, q = warp & 3, g = ew >> 2;
+    constexpr int kChunks = BNX / 16;
+    const int q = warp & 3;
     const long long U = (long long)(plan.tiles - plan.whole) * P.steps;
-    const uint32_t staging = ring + C::kStagingOff + ew * C::kStaging;
+    const uint32_t staging = ring + C::kStagingOff + q * C::kStaging;
     int a = 0, aph = 0;
     bool ok = true;
     while (ok && sg.next(plan, P.steps, t, k0, k1, slot)) {
       const Tile T = tile_of<C>(P, plan, t);
-      const int cols = T.bn / C::kGroups;           // of this group
-      const int chunks = (cols + 15) / 16, col0 = g * cols;
+      const int chunks = T.bn / 16;
       pair_t acc[kChunks][2][2][2];                 // [chunk][16 lanes][8 columns][8 lanes]
 #pragma unroll
       for (int c = 0; c < kChunks; ++c)
@@ -629,8 +605,8 @@ __global__ void __launch_bounds__(Cfg<BNX, PAIR>::kThreads, Cfg<BNX, PAIR>::kPer
       for (int k = k0; k < k1; ++k) {
         if (!(ok = warp_wait<256>(accf(a), aph, W, kErrAcc, lane))) break;
         tc_fence_after();
-        const uint32_t ta = tmem + ((uint32_t)(32 * q) << 16) + (uint32_t)(a * BNX + col0);
-        const uint32_t sa = ring + C::kScaleOff + 4 * (a * BNX + col0 + 2 * (lane & 3));
+        const uint32_t ta = tmem + ((uint32_t)(32 * q) << 16) + (uint32_t)(a * BNX);
+        const uint32_t sa = ring + C::kScaleOff + 4 * (a * BNX + 2 * (lane & 3));
         uint32_t r[2][2][8];
         tmem_ld_16x16(ta, r[0][0]);
         tmem_ld_16x16(ta + (16u << 16), r[0][1]);
@@ -656,12 +632,7 @@ __global__ void __launch_bounds__(Cfg<BNX, PAIR>::kThreads, Cfg<BNX, PAIR>::kPer
         tc_fence_before();
         __syncwarp();
         if (lane == 0) {
-          // (for a pair's other CTA the arrival says only when: see arrive_stage in fused_tc.cu)
-          if (PAIR && !leader)
-            asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(lead(acce(a)))
-                         : "memory");
-          else
-            qlk::mbar_arrive(acce(a));
+          qlk::mbar_arrive(acce(a));
           qlk::mbar_arrive(sempty(a));
         }
         if (++a == C::kAcc) {
@@ -672,8 +643,8 @@ __global__ void __launch_bounds__(Cfg<BNX, PAIR>::kThreads, Cfg<BNX, PAIR>::kPer
       if (!ok) break;
       if (k0 != 0 || k1 != P.steps) {
         // part of a tile: the last contributor goes on, with the sums of all
-        constexpr size_t kWarpBytes = (size_t)32 * C::kCols * 4;
-        uint8_t* base = reinterpret_cast<uint8_t*>(P.partials) + ew * kWarpBytes + 16 * lane;
+        constexpr size_t kWarpBytes = (size_t)32 * BNX * 4;
+        uint8_t* base = reinterpret_cast<uint8_t*>(P.partials) + q * kWarpBytes + 16 * lane;
         constexpr size_t kSlot = C::kEpiWarps * kWarpBytes;
         uint8_t* mine = base + (size_t)(2 * blockIdx.x + slot) * kSlot;
 #pragma unroll
@@ -690,7 +661,7 @@ __global__ void __launch_bounds__(Cfg<BNX, PAIR>::kThreads, Cfg<BNX, PAIR>::kPer
         const int wf = worker_of(ub, U, plan.runners);
         const int wl = worker_of(ub + P.steps - 1, U, plan.runners);
         uint32_t* counter =
-            P.counters + ((size_t)(t - plan.whole) * C::kCtas + rank) * C::kEpiWarps + ew;
+            P.counters + (size_t)(t - plan.whole) * C::kEpiWarps + q;
         uint32_t prev = 0;
         if (lane == 0) prev = arrive_weight(counter, 1u);
         prev = __shfl_sync(0xffffffffu, prev, 0);
@@ -706,8 +677,7 @@ __global__ void __launch_bounds__(Cfg<BNX, PAIR>::kThreads, Cfg<BNX, PAIR>::kPer
             for (int i = 0; i < 8; ++i) acc[c][i >> 2][(i >> 1) & 1][i & 1] = 0ull;
 #pragma unroll 1
         for (int w = wf; w <= wl; ++w) {
-          const uint8_t* src =
-              base + (size_t)(2 * (w * C::kCtas + (int)rank) + (w == wf ? first : 0)) * kSlot;
+          const uint8_t* src = base + (size_t)(2 * w + (w == wf ? first : 0)) * kSlot;
 #pragma unroll
           for (int c = 0; c < kChunks; ++c)
             if (c < chunks)
@@ -724,7 +694,7 @@ __global__ void __launch_bounds__(Cfg<BNX, PAIR>::kThreads, Cfg<BNX, PAIR>::kPer
         if (lane == 0) *counter = 0u;  // ready for the next call
       }
       // 16 rows of q at a time through shared memory: 64 contiguous bytes of a row of y per warp
-      const int n = (T.rt * C::kCtas + (int)rank) * 128 + 32 * q + 8 * (lane & 3);
+      const int n = T.rt * 128 + 32 * q + 8 * (lane & 3);
 #pragma unroll
       for (int c = 0; c < kChunks; ++c)
         if (c < chunks) {
@@ -744,19 +714,19 @@ __global__ void __launch_bounds__(Cfg<BNX, PAIR>::kThreads, Cfg<BNX, PAIR>::kPer
           for (int i = 0; i < 2; ++i) {
             const int row = 16 * c + 8 * i + (lane >> 2);
             const uint4 v = qlk::lds128(staging + (8 * i + (lane >> 2)) * kTokStride + (lane & 3) * 16);
-            if (row < cols && col0 + row < T.rows && n < P.R)
-              *reinterpret_cast<uint4*>(static_cast<uint16_t*>(P.y) +
-                                        (size_t)(T.m0 + col0 + row) * P.R + n) = v;
+            if (row < T.rows && n < P.R)
+              *reinterpret_cast<uint4*>(static_cast<uint16_t*>(P.y) + (size_t)(T.m0 + row) * P.R +
+                                        n) = v;
           }
         }
     }
   }
 
   tc_fence_before();
-  sync_all<PAIR>();
+  sync_all<false>();
   if (warp == 1) {
     tc_fence_after();
-    tmem_dealloc<PAIR>(tmem, C::kTmemCols);
+    tmem_dealloc<false>(tmem, C::kTmemCols);
   }
 }
 
@@ -836,7 +806,7 @@ __global__ void __launch_bounds__(Wide::kThreads, 1)
   qlk::grid_dependents_launch();  // (behind the allocation: the next grid's must not come first)
 
   Plan plan{start, pre, pre[P.E], 0, 0};
-  schedule(plan, P.steps, nwk);
+  schedule<true>(plan, P.steps, nwk);
   Segments sg;
   sg.init(plan, P.steps, wk, nwk);
   int t, k0, k1, slot = 0;
@@ -1224,7 +1194,7 @@ ql_status launch_as(const Product& p) {
   const cuuint64_t wdims[3] = {(cuuint64_t)p.K, (cuuint64_t)p.N, (cuuint64_t)p.E};
   const cuuint64_t qdims[2] = {(cuuint64_t)(BWD ? p.N : p.K), (cuuint64_t)p.M};
   if (!encode(&maps.w, p.w, 3, wdims, 128)) return QL_ERR_CUDA;
-  for (int i = 0; i < 4; ++i)
+  for (int i = C::kCtas == 2 ? 0 : 1; i < (C::kCtas == 2 ? 1 : 4); ++i)
     if ((128 >> i) <= C::kBRows && !encode(&maps.q[i], p.q, 2, qdims, 128 >> i)) return QL_ERR_CUDA;
   // every worker that can run: how many have work is known on the device.  A second CTA on each SM
   // where both have kLongRun steps and more
@@ -1237,18 +1207,17 @@ ql_status launch_as(const Product& p) {
   return cudaLaunchKernelEx(&cfg, kernel, P, maps) == cudaSuccess ? QL_OK : QL_ERR_CUDA;
 }
 
-template <int BNX, bool PAIR, bool BWD>
+template <int BNX, bool BWD>
 ql_status launch_narrow(const Product& p) {
-  return launch_as<Cfg<BNX, PAIR>, fp8_tc_kernel<BNX, PAIR, BWD>, BWD>(p);
+  return launch_as<Cfg<BNX>, fp8_tc_kernel<BNX, BWD>, BWD>(p);
 }
 
 template <bool BWD>
 ql_status launch(const Product& p) {
   const int rows = (p.M + p.E - 1) / p.E;  // of an average expert
-  if (rows <= 16) return launch_narrow<16, false, BWD>(p);
-  if (rows <= 32) return launch_narrow<32, false, BWD>(p);
-  if (rows <= 64) return launch_narrow<64, false, BWD>(p);
-  if (rows <= 128) return launch_narrow<128, true, BWD>(p);
+  if (rows <= 16) return launch_narrow<16, BWD>(p);
+  if (rows <= 32) return launch_narrow<32, BWD>(p);
+  if (rows <= 64) return launch_narrow<64, BWD>(p);
   return launch_as<Wide, fp8_wide_kernel<BWD>, BWD>(p);
 }
 
@@ -1265,7 +1234,7 @@ size_t product_partial_bytes(int M, int E) {
   const int rows = (M + E - 1) / E;
   int bn = 16;
   while (bn < 256 && bn < rows) bn *= 2;
-  return (size_t)2 * sms * 128 * (bn <= 128 ? 128 : bn) * sizeof(float);
+  return (size_t)2 * sms * 128 * (bn <= 64 ? 2 * bn : 256) * sizeof(float);
 }
 
 ql_status launch_product(const Product& p) {
