@@ -1120,7 +1120,7 @@ void launch_config(cudaLaunchConfig_t* cfg, cudaLaunchAttribute* attr, unsigned 
 }
 
 using Kernel = void (*)(const Params, const Maps);
-constexpr int kLongRun = 16;
+constexpr int kLongRun = 8;
 
 // Workers resident at once, once per kernel and device.
 template <class C, Kernel kernel>

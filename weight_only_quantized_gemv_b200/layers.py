@@ -635,38 +635,39 @@ def _blocks(columns: int) -> int:
     return (columns + 127) // 128
 
 
-def _type_of(t: torch.Tensor, name: str) -> int:
+def _matrix(t: torch.Tensor, name: str) -> tuple:
+    """(ql_type, device index, rows, columns) of a 16-bit matrix."""
     kind = _TYPE_OF.get(t.dtype)
-    if kind is None or t.dim() != 2 or not t.is_cuda:
+    index = t.get_device()
+    if kind is None or t.dim() != 2 or index < 0:
         raise ValueError(f"{name} must be a float16 or bfloat16 matrix on a CUDA device, not "
                          f"{t.dtype} {tuple(t.shape)} on {t.device}")
-    return kind
+    return kind, index, *t.shape
 
 
 def _row_ptr(x: torch.Tensor, index: int, name: str) -> tuple:
     """(data pointer, elements between rows) of a matrix whose rows are contiguous, once checked
     like ``_fused_ptr``'s."""
-    if x.is_contiguous():
-        return _fused_ptr(x, x.shape, index, name, x.dtype), x.shape[1]
     M, K = x.shape
-    if x.requires_grad and torch.is_grad_enabled() or x.stride(1) != 1 and K > 1 or (
-            M > 1 and x.stride(0) < K):
+    ld = x.stride(0) if M > 1 else K
+    if x.requires_grad and torch.is_grad_enabled() or x.stride(1) != 1 and K > 1 or ld < K:
         _fused_ptr(x, (M, K), index, name, x.dtype)  # says why not
-    return x.data_ptr(), x.stride(0) if M > 1 else K
+    return x.data_ptr(), ld
 
 
 def _raw_stream(stream, index: int):
     return _current_stream(index) if stream is None else getattr(stream, "cuda_stream", stream)
 
 
-_empties: dict = {}  # (dtype, device index): an empty tensor, from which new ones are quickest made
+# an empty tensor for each type and device index, from which new ones are quickest made
+_empties: dict = {dtype: {} for dtype in (_F8, _F32, *_TYPE_OF)}
 
 
 def _new(shape: tuple, dtype, index: int, stream) -> torch.Tensor:
     """A new tensor on the call's stream."""
-    like = _empties.get((dtype, index))
+    like = _empties[dtype].get(index)
     if like is None:
-        like = _empties[dtype, index] = torch.empty(0, dtype=dtype, device=f"cuda:{index}")
+        like = _empties[dtype][index] = torch.empty(0, dtype=dtype, device=f"cuda:{index}")
     if stream is None:
         return like.new_empty(shape)
     with torch.cuda.stream(_as_stream(stream, index)):
@@ -696,7 +697,7 @@ def fp8_quantize(x: torch.Tensor, q: Optional[torch.Tensor] = None,
                  scales: Optional[torch.Tensor] = None, stream=None) -> tuple:
     """(q, scales): e4m3 codes [M, K] of x[M, K] (fp16 or bf16; its rows may lie apart) and an fp32
     scale for every 128 columns, [M, ceil(K / 128)]; x is about q * scale."""
-    kind, index, (M, K) = _type_of(x, "x"), x.get_device(), x.shape
+    kind, index, M, K = _matrix(x, "x")
     if torch.cuda.current_device() != index:
         return _on_device(index, fp8_quantize, x, q, scales, stream)
     px, ldx = _row_ptr(x, index, "x")
@@ -711,7 +712,7 @@ def fp8_gated(gu: torch.Tensor, act: str = "silu", q: Optional[torch.Tensor] = N
               scales: Optional[torch.Tensor] = None, stream=None) -> tuple:
     """(q, scales): codes [M, F] and scales of act(g) * u, where gu[M, 2 F] = (g, u) (fp16 or
     bf16) is the output of a product with the gate's and the up projection's rows."""
-    kind, index, (M, C) = _type_of(gu, "gu"), gu.get_device(), gu.shape
+    kind, index, M, C = _matrix(gu, "gu")
     if torch.cuda.current_device() != index:
         return _on_device(index, fp8_gated, gu, act, q, scales, stream)
     if C % 2:
@@ -729,7 +730,7 @@ def fp8_gated_backward(dh: torch.Tensor, gu: torch.Tensor, act: str = "silu",
                        stream=None) -> tuple:
     """(q, scales): codes [M, 2 F] and scales of the gradients of g and u, from dh[M, F] and the gu
     that ``fp8_gated`` read."""
-    kind, index, (M, C) = _type_of(gu, "gu"), gu.get_device(), gu.shape
+    kind, index, M, C = _matrix(gu, "gu")
     if torch.cuda.current_device() != index:
         return _on_device(index, fp8_gated_backward, dh, gu, act, q, scales, stream)
     if C % 2:
@@ -793,16 +794,25 @@ class RMSNorm(_FusedWorkspace):
             return self._fused_elsewhere(self.forward, x, residual, total, y, rstd, q, scales,
                                          stream)
         dtype, M = weight.dtype, x.shape[0]
-        if x.dtype is not dtype or x.dim() != 2 or x.shape[1] != K or x.get_device() != index:
-            _fused_ptr(x, (M, K), index, "x", dtype)
+        shape = (M, K)
+        if x.dtype is not dtype or x.shape != shape or x.get_device() != index:
+            _fused_ptr(x, shape, index, "x", dtype)  # says why not
         px, ldx = _row_ptr(x, index, "x")
+        if residual is not None:
+            residual = _fused_ptr(residual, shape, index, "residual", dtype)
+        if total is not None:
+            total = _fused_ptr(total, shape, index, "total", dtype)
+        if y is not None:
+            y = _fused_ptr(y, shape, index, "y", dtype)
+        if rstd is not None:
+            rstd = _fused_ptr(rstd, (M,), index, "rstd", _F32)
         q, scales, pq, ps = _codes_out(q, scales, M, K, index, stream)
-        head = (_TYPE_OF[dtype], px, ldx, _fused_ptr(residual, (M, K), index, "residual", dtype),
-                weight.data_ptr(), self.eps, _fused_ptr(total, (M, K), index, "total", dtype),
-                _fused_ptr(y, (M, K), index, "y", dtype), pq, ps,
-                _fused_ptr(rstd, (M,), index, "rstd", _F32), M, K)
         if M:
-            _check(_lib.qlinear_rmsnorm(*head, _raw_stream(stream, index)), "qlinear_rmsnorm")
+            status = _lib.qlinear_rmsnorm(
+                _TYPE_OF[dtype], px, ldx, residual, weight.data_ptr(), self.eps, total, y, pq, ps,
+                rstd, M, K, _current_stream(index) if stream is None else _raw_stream(stream, index))
+            if status:
+                _check(status, "qlinear_rmsnorm")
         return q, scales
 
     def backward(self, dy: torch.Tensor, total: torch.Tensor, rstd: torch.Tensor,
@@ -866,10 +876,6 @@ class _Fp8Weights(_FusedWorkspace):
         self._fused = (None, N, K, self.codes.get_device())
 
     @property
-    def _pointers(self) -> tuple:
-        return self.codes.data_ptr(), self.scales.data_ptr()
-
-    @property
     def weight_bytes(self) -> int:
         return self.codes.numel() + 4 * self.scales.numel()
 
@@ -896,8 +902,13 @@ class _Fp8Weights(_FusedWorkspace):
             pout = out.data_ptr()
         else:
             pout = _fused_ptr(out, (M, R), index, what, dtype)
-        head = (kind, pq, _fused_ptr(scales, (M, (C + 127) // 128), index, "scales", _F32),
-                *offsets, *self._pointers, pout, M, *((self.E,) if offsets else ()), self.N, self.K)
+        ps = _fused_ptr(scales, (M, (C + 127) // 128), index, "scales", _F32)
+        if offsets:
+            head = (kind, pq, ps, *offsets, self.codes.data_ptr(), self.scales.data_ptr(), pout, M,
+                    self.E, self.N, self.K)
+        else:
+            head = (kind, pq, ps, self.codes.data_ptr(), self.scales.data_ptr(), pout, M, self.N,
+                    self.K)
         if M:
             self._fused_call(entry, name, head, M, backward, workspace, stream)
         return out
