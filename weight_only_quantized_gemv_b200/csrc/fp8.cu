@@ -225,64 +225,109 @@ __global__ void __launch_bounds__(32 * kJoinWarps) norm_join_kernel(const float*
 }
 
 // ---------------------------------------------------------------------------
-// quantization of rows: of x, of act(g) u, or of the gated pair's gradients
+// quantization of rows: of x, of act(g) u, or of the gated pair's gradients.
+//
+// The gradients of a pair have their codes F columns apart.  Where F is a multiple of 128 both lie at
+// the same place of their blocks and a thread makes both (kPair); where it is not, a thread makes one
+// and the inputs are read twice (kGatedGrad).
 
-enum { kPlain, kGated, kGatedGrad };
+enum { kPlain, kGated, kGatedGrad, kPair };
 
 struct CodeParams {
   const uint16_t* x;   // kPlain: rows ldx apart; else gu [M][2 F]
-  const uint16_t* dh;  // kGatedGrad: [M][F]
+  const uint16_t* dh;  // gradients: [M][F]
   uint8_t* q;          // [M][C]
   float* scales;       // [M][blocks of C]
   long long ldx;
   int M, C, F, act;    // C columns of output: K, F, 2 F
-  int chunks;          // of kCodeCols columns in a row
+  int slots;           // vectors of eight columns in a row, whole blocks of sixteen (kPair: of F)
 };
 
-constexpr int kCodeThreads = 256, kCodeCols = 8 * kCodeThreads;
+constexpr int kCodeThreads = 256;
 
-template <int WHAT, bool BF16, int ACT>
-__device__ __forceinline__ void code_values(const CodeParams& P, int row, int c, float (&v)[8]) {
+template <int WHAT>
+struct Inputs {
+  uint4 a, b, c;  // x; or g, u; and dh
+};
+template <int WHAT>
+__device__ __forceinline__ void load_inputs(const CodeParams& P, int row, int c,
+                                            Inputs<WHAT>& in) {
   if constexpr (WHAT == kPlain) {
-    unpack8<BF16>(load16(P.x + (size_t)row * P.ldx + c), v);
+    in.a = load16(P.x + (size_t)row * P.ldx + c);
   } else {
-    const int f = c < P.F ? c : c - P.F;  // (kGated: always c)
+    const int f = WHAT == kGatedGrad && c >= P.F ? c - P.F : c;
     const uint16_t* gu = P.x + (size_t)row * 2 * P.F + f;
-    const uint4 gv = load16(gu), uv = load16(gu + P.F);
-    float g[8], u[8];
-    unpack8<BF16>(gv, g);
-    unpack8<BF16>(uv, u);
-    if constexpr (WHAT == kGated) {
+    in.a = load16(gu);
+    in.b = load16(gu + P.F);
+    if constexpr (WHAT != kGated) in.c = load16(P.dh + (size_t)row * P.F + f);
+  }
+}
+// v: the values to code (kPair: dg, and du in w)
+template <int WHAT, bool BF16, int ACT>
+__device__ __forceinline__ void code_values(const Inputs<WHAT>& in, bool second, float (&v)[8],
+                                            float (&w)[8]) {
+  unpack8<BF16>(in.a, v);
+  if constexpr (WHAT == kPlain) return;
+  float u[8];
+  unpack8<BF16>(in.b, u);
+  if constexpr (WHAT == kGated) {
 #pragma unroll
-      for (int e = 0; e < 8; ++e) v[e] = qact::act_forward(ACT, g[e]) * u[e];
-    } else {
-      float d[8];
-      unpack8<BF16>(load16(P.dh + (size_t)row * P.F + f), d);
+    for (int e = 0; e < 8; ++e) v[e] = qact::act_forward(ACT, v[e]) * u[e];
+  } else {
+    float d[8];
+    unpack8<BF16>(in.c, d);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        float y, dy;
-        qact::act_both<true>(ACT, g[e], y, dy);
-        v[e] = c < P.F ? d[e] * u[e] * dy : d[e] * y;
-      }
+    for (int e = 0; e < 8; ++e) {
+      float y, dy;
+      qact::act_both<true>(ACT, v[e], y, dy);
+      const float dg = d[e] * u[e] * dy, du = d[e] * y;
+      v[e] = WHAT == kGatedGrad && second ? du : dg;
+      w[e] = du;
     }
   }
 }
+// The whole warp: sixteen lanes to a block, `in`: the lane's vector lies within its row.
+__device__ __forceinline__ void store_codes(const CodeParams& P, bool in, int row, int c,
+                                            const float (&v)[8]) {
+  const float scale = scale_of(top_of_block(top8(v)));
+  if (in) {
+    *reinterpret_cast<uint2*>(P.q + (size_t)row * P.C + c) = encode8(v, scale);
+    if ((threadIdx.x & 15) == 0) P.scales[(size_t)row * blocks_of(P.C) + c / kBlock] = scale;
+  }
+}
 
-template <int WHAT, bool BF16, int ACT>
+// U vectors to a thread: all of their loads are under way before the first is used.  Measured, 1024
+// rows: see launch_codes_as.
+template <int WHAT, bool BF16, int ACT, int U>
 __global__ void __launch_bounds__(kCodeThreads) code_kernel(const CodeParams P) {
   qlk::grid_dependents_launch();
   qlk::grid_dependency_wait();
-  const long long n = (long long)P.M * P.chunks;
-  for (long long i = blockIdx.x; i < n; i += gridDim.x) {
-    const int row = (int)(i / P.chunks);
-    const int c = (int)(i - (long long)row * P.chunks) * kCodeCols + 8 * (int)threadIdx.x;
-    float v[8] = {};
-    if (c < P.C) code_values<WHAT, BF16, ACT>(P, row, c, v);
-    const float scale = scale_of(top_of_block(top8(v)));
-    if (c < P.C) {
-      *reinterpret_cast<uint2*>(P.q + (size_t)row * P.C + c) = encode8(v, scale);
-      if ((threadIdx.x & 15) == 0)
-        P.scales[(size_t)row * blocks_of(P.C) + c / kBlock] = scale;
+  constexpr int kStep = kCodeThreads * U;
+  const unsigned slots = (unsigned)P.slots;
+  const long long n = (long long)P.M * P.slots;
+  for (long long base = (long long)blockIdx.x * kStep; base < n;
+       base += (long long)gridDim.x * kStep) {
+    // (a 64-bit division costs as much as coding a vector)
+    const int row0 = n >> 32 ? (int)(base / P.slots) : (int)((unsigned)base / slots);
+    const unsigned at0 = (unsigned)(base - (long long)row0 * P.slots) + threadIdx.x;
+    int row[U], c[U];
+    bool in[U];
+    Inputs<WHAT> x[U];
+#pragma unroll
+    for (int i = 0; i < U; ++i) {
+      const unsigned at = at0 + i * kCodeThreads, r = at / slots;
+      row[i] = row0 + (int)r;
+      c[i] = 8 * (int)(at - r * slots);
+      in[i] = row[i] < P.M && c[i] < P.C;
+      x[i].a = x[i].b = x[i].c = make_uint4(0, 0, 0, 0);
+      if (in[i]) load_inputs<WHAT>(P, row[i], c[i], x[i]);
+    }
+#pragma unroll
+    for (int i = 0; i < U; ++i) {
+      float v[8], w[8];
+      code_values<WHAT, BF16, ACT>(x[i], c[i] >= P.F, v, w);
+      store_codes(P, in[i], row[i], c[i], v);
+      if constexpr (WHAT == kPair) store_codes(P, in[i], row[i], P.F + c[i], w);
     }
   }
 }
@@ -299,7 +344,7 @@ struct WeightParams {
 
 template <bool BF16>
 __global__ void __launch_bounds__(256) weight_kernel(const WeightParams P) {
-  __shared__ float red[8];
+  __shared__ uint32_t red[8];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int nb = blocks_of(P.N), kb = blocks_of(P.K);
   const long long b = blockIdx.x;
@@ -308,7 +353,7 @@ __global__ void __launch_bounds__(256) weight_kernel(const WeightParams P) {
   const int n0 = (int)(rest % nb) * kBlock + (int)(threadIdx.x >> 4);
   const size_t base = (size_t)(rest / nb) * P.N * P.K + k;
   uint4 v[8];
-  float top = 0.f;
+  uint32_t top = 0;
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
     v[i] = make_uint4(0, 0, 0, 0);
@@ -318,14 +363,14 @@ __global__ void __launch_bounds__(256) weight_kernel(const WeightParams P) {
   for (int i = 0; i < 8; ++i) {
     float f[8];
     unpack8<BF16>(v[i], f);
-    top = max_nan(top, top8(f));
+    top = max(top, top8(f));
   }
 #pragma unroll
-  for (int o = 16; o; o >>= 1) top = max_nan(top, __shfl_xor_sync(0xffffffffu, top, o));
+  for (int o = 16; o; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
   if (lane == 0) red[warp] = top;
   __syncthreads();
 #pragma unroll
-  for (int i = 0; i < 8; ++i) top = max_nan(top, red[i]);
+  for (int i = 0; i < 8; ++i) top = max(top, red[i]);
   const float scale = scale_of(top);
   if (threadIdx.x == 0) P.scales[b] = scale;
 #pragma unroll
@@ -391,7 +436,7 @@ ql_status launch_early(void (*kernel)(Params...), unsigned grid, int threads, ql
 
 // Threads of a norm's block, for V vectors each.
 int norm_threads(int K, int V) { return (K / 8 + 32 * V - 1) / (32 * V) * 32; }
-int norm_vectors(int K) { return K <= 8192 ? 1 : K <= 16384 ? 2 : 4; }
+int norm_vectors(int K) { return K <= 2048 ? 1 : K <= 8192 ? 2 : 4; }
 
 template <bool BF16>
 ql_status launch_norm(const NormParams& P, ql_stream_t st) {
@@ -415,10 +460,14 @@ ql_status launch_norm_grad(const NormGradParams& P, int blocks, ql_stream_t st) 
 
 template <int WHAT, bool BF16, int ACT>
 ql_status launch_codes_as(CodeParams P, ql_stream_t st) {
-  P.chunks = (P.C + kCodeCols - 1) / kCodeCols;
-  const long long n = (long long)P.M * P.chunks, most = 1 << 20;
-  return launch_early(code_kernel<WHAT, BF16, ACT>, (unsigned)(n < most ? n : most), kCodeThreads,
-                      st, P);
+  P.slots = blocks_of(WHAT == kPair ? P.F : P.C) * 16;
+  const long long n = (long long)P.M * P.slots, most = 1 << 20;
+  // two vectors to a thread once there are enough threads for every SM with one
+  const int U = n >= 2048LL * 148 ? 2 : 1;
+  const long long blocks = (n + kCodeThreads * U - 1) / (kCodeThreads * U);
+  const unsigned grid = (unsigned)(blocks < most ? blocks : most);
+  return U == 2 ? launch_early(code_kernel<WHAT, BF16, ACT, 2>, grid, kCodeThreads, st, P)
+                : launch_early(code_kernel<WHAT, BF16, ACT, 1>, grid, kCodeThreads, st, P);
 }
 template <int WHAT, bool BF16>
 ql_status launch_codes(const CodeParams& P, ql_stream_t st) {
@@ -552,7 +601,7 @@ extern "C" ql_status qlinear_fp8_gated_backward(int type, int act, const void* d
   P.C = 2 * F;
   P.F = F;
   P.act = act;
-  return codes<kGatedGrad>(type, P, stream);
+  return F % kBlock == 0 ? codes<kPair>(type, P, stream) : codes<kGatedGrad>(type, P, stream);
 }
 
 extern "C" ql_status qlinear_fp8_quantize_weights(int type, const void* w, uint8_t* q,

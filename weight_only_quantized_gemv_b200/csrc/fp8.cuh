@@ -20,13 +20,12 @@ constexpr float kFloor = 7.88860905e-31f;  // 2^-100, see above
 
 __host__ __device__ constexpr int blocks_of(int n) { return (n + kBlock - 1) / kBlock; }
 
-// The larger of two sizes; a NaN stays (fmaxf would drop it).
-__device__ __forceinline__ float max_nan(float a, float b) {
-  float r;
-  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
-  return r;
+// Sizes are compared as the bits of |v|, whose order is that of the numbers, infinity above them and
+// NaN above that (fmaxf would drop a NaN).
+__device__ __forceinline__ uint32_t size_of(float v) { return __float_as_uint(v) & 0x7FFFFFFFu; }
+__device__ __forceinline__ float scale_of(uint32_t top) {
+  return __uint_as_float(max(top, __float_as_uint(kFloor))) * (1.f / kTop);
 }
-__device__ __forceinline__ float scale_of(float top) { return max_nan(top, kFloor) / kTop; }
 
 // Two codes, the first in the low byte.
 __device__ __forceinline__ uint32_t encode2(float a, float b) {
@@ -34,10 +33,11 @@ __device__ __forceinline__ uint32_t encode2(float a, float b) {
   asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(b), "f"(a));
   return r;
 }
-// Eight codes of v / scale.  The reciprocal is rounded once and so is the product: together at most
-// 2^-23 of the value off the quotient, which changes a code only that close to a border of two.
+// Eight codes of v / scale.  The fast reciprocal is off by at most 2^-23 (scales are normal numbers
+// below 2^120) and the product rounded once: together less than 2^-22 of the value, which changes a
+// code only that close to a border of two.
 __device__ __forceinline__ uint2 encode8(const float (&v)[8], float scale) {
-  const float inv = 1.f / scale;
+  const float inv = __fdividef(1.f, scale);
   uint2 r;
   r.x = encode2(v[0] * inv, v[1] * inv) | encode2(v[2] * inv, v[3] * inv) << 16;
   r.y = encode2(v[4] * inv, v[5] * inv) | encode2(v[6] * inv, v[7] * inv) << 16;
@@ -78,16 +78,16 @@ __device__ __forceinline__ uint4 pack8(const float (&f)[8]) {
                     pack2<BF16>(f[6], f[7]));
 }
 
-__device__ __forceinline__ float top8(const float (&v)[8]) {
-  float t = fabsf(v[0]);
+__device__ __forceinline__ uint32_t top8(const float (&v)[8]) {
+  uint32_t t = size_of(v[0]);
 #pragma unroll
-  for (int i = 1; i < 8; ++i) t = max_nan(t, fabsf(v[i]));
+  for (int i = 1; i < 8; ++i) t = max(t, size_of(v[i]));
   return t;
 }
 // Over the sixteen lanes whose eight columns each make up a block.
-__device__ __forceinline__ float top_of_block(float t) {
+__device__ __forceinline__ uint32_t top_of_block(uint32_t t) {
 #pragma unroll
-  for (int o = 8; o; o >>= 1) t = max_nan(t, __shfl_xor_sync(0xffffffffu, t, o));
+  for (int o = 8; o; o >>= 1) t = max(t, __shfl_xor_sync(0xffffffffu, t, o));
   return t;
 }
 
