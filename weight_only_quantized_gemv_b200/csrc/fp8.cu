@@ -241,6 +241,7 @@ struct CodeParams {
   long long ldx;
   int M, C, F, act;    // C columns of output: K, F, 2 F
   int slots;           // vectors of eight columns in a row, whole blocks of sixteen (kPair: of F)
+  float inv_slots;     // 1 / slots
 };
 
 constexpr int kCodeThreads = 256;
@@ -262,6 +263,29 @@ __device__ __forceinline__ void load_inputs(const CodeParams& P, int row, int c,
     if constexpr (WHAT != kGated) in.c = load16(P.dh + (size_t)row * P.F + f);
   }
 }
+// The activation, and with it the derivative, from the sigmoid with the short exponential and
+// reciprocal: the values are coded in 8 bits.  (Where e^-x leaves the normal numbers the sigmoid is
+// 0 or 1; x times what is lost is below 2^-119.)
+template <int ACT>
+__device__ __forceinline__ float act_value(float z) {
+  if constexpr (ACT == QL_ACT_SILU) {
+    return z * rcp_fast(1.f + exp2_fast(z * -1.44269504f));
+  } else {
+    return qact::act_forward(ACT, z);
+  }
+}
+template <int ACT>
+__device__ __forceinline__ void act_pair(float z, float& f, float& df) {
+  if constexpr (ACT == QL_ACT_SILU) {
+    const float e = exp2_fast(fabsf(z) * -1.44269504f), r = rcp_fast(1.f + e), er = e * r;
+    const float s = z < 0.f ? er : r, c = z < 0.f ? r : er;  // sigma(z), 1 - sigma(z)
+    f = z * s;
+    df = fmaf(f, c, s);
+  } else {
+    qact::act_both<true>(ACT, z, f, df);
+  }
+}
+
 // v: the values to code (kPair: dg, and du in w)
 template <int WHAT, bool BF16, int ACT>
 __device__ __forceinline__ void code_values(const Inputs<WHAT>& in, bool second, float (&v)[8],
@@ -272,14 +296,14 @@ __device__ __forceinline__ void code_values(const Inputs<WHAT>& in, bool second,
   unpack8<BF16>(in.b, u);
   if constexpr (WHAT == kGated) {
 #pragma unroll
-    for (int e = 0; e < 8; ++e) v[e] = qact::act_forward(ACT, v[e]) * u[e];
+    for (int e = 0; e < 8; ++e) v[e] = act_value<ACT>(v[e]) * u[e];
   } else {
     float d[8];
     unpack8<BF16>(in.c, d);
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
       float y, dy;
-      qact::act_both<true>(ACT, v[e], y, dy);
+      act_pair<ACT>(v[e], y, dy);
       const float dg = d[e] * u[e] * dy, du = d[e] * y;
       v[e] = WHAT == kGatedGrad && second ? du : dg;
       w[e] = du;
@@ -288,8 +312,8 @@ __device__ __forceinline__ void code_values(const Inputs<WHAT>& in, bool second,
 }
 // The whole warp: sixteen lanes to a block, `in`: the lane's vector lies within its row.
 __device__ __forceinline__ void store_codes(const CodeParams& P, bool in, int row, int c,
-                                            const float (&v)[8]) {
-  const float scale = scale_of(top_of_block(top8(v)));
+                                            const float (&v)[8], uint32_t top) {
+  const float scale = scale_of(top_of_block(top));
   if (in) {
     *reinterpret_cast<uint2*>(P.q + (size_t)row * P.C + c) = encode8(v, scale);
     if ((threadIdx.x & 15) == 0) P.scales[(size_t)row * blocks_of(P.C) + c / kBlock] = scale;
@@ -303,21 +327,29 @@ __global__ void __launch_bounds__(kCodeThreads) code_kernel(const CodeParams P) 
   qlk::grid_dependents_launch();
   qlk::grid_dependency_wait();
   constexpr int kStep = kCodeThreads * U;
-  const unsigned slots = (unsigned)P.slots;
   const long long n = (long long)P.M * P.slots;
   for (long long base = (long long)blockIdx.x * kStep; base < n;
        base += (long long)gridDim.x * kStep) {
     // (a 64-bit division costs as much as coding a vector)
-    const int row0 = n >> 32 ? (int)(base / P.slots) : (int)((unsigned)base / slots);
-    const unsigned at0 = (unsigned)(base - (long long)row0 * P.slots) + threadIdx.x;
+    const int row0 = n >> 32 ? (int)(base / P.slots) : (int)((unsigned)base / (unsigned)P.slots);
+    const int at0 = (int)(base - (long long)row0 * P.slots) + (int)threadIdx.x;
     int row[U], c[U];
     bool in[U];
     Inputs<WHAT> x[U];
 #pragma unroll
     for (int i = 0; i < U; ++i) {
-      const unsigned at = at0 + i * kCodeThreads, r = at / slots;
-      row[i] = row0 + (int)r;
-      c[i] = 8 * (int)(at - r * slots);
+      // the quotient by the reciprocal is at most one off (at < 2 slots + 512)
+      const int at = at0 + i * kCodeThreads;
+      int r = __float2int_rz(__int2float_rn(at) * P.inv_slots), rest = at - r * P.slots;
+      if (rest < 0) {
+        --r;
+        rest += P.slots;
+      } else if (rest >= P.slots) {
+        ++r;
+        rest -= P.slots;
+      }
+      row[i] = row0 + r;
+      c[i] = 8 * rest;
       in[i] = row[i] < P.M && c[i] < P.C;
       x[i].a = x[i].b = x[i].c = make_uint4(0, 0, 0, 0);
       if (in[i]) load_inputs<WHAT>(P, row[i], c[i], x[i]);
@@ -326,8 +358,9 @@ __global__ void __launch_bounds__(kCodeThreads) code_kernel(const CodeParams P) 
     for (int i = 0; i < U; ++i) {
       float v[8], w[8];
       code_values<WHAT, BF16, ACT>(x[i], c[i] >= P.F, v, w);
-      store_codes(P, in[i], row[i], c[i], v);
-      if constexpr (WHAT == kPair) store_codes(P, in[i], row[i], P.F + c[i], w);
+      store_codes(P, in[i], row[i], c[i], v,
+                  WHAT == kPlain ? top_of_words<BF16>(x[i].a) : top8(v));
+      if constexpr (WHAT == kPair) store_codes(P, in[i], row[i], P.F + c[i], w, top8(w));
     }
   }
 }
@@ -461,6 +494,7 @@ ql_status launch_norm_grad(const NormGradParams& P, int blocks, ql_stream_t st) 
 template <int WHAT, bool BF16, int ACT>
 ql_status launch_codes_as(CodeParams P, ql_stream_t st) {
   P.slots = blocks_of(WHAT == kPair ? P.F : P.C) * 16;
+  P.inv_slots = 1.f / (float)P.slots;
   const long long n = (long long)P.M * P.slots, most = 1 << 20;
   // two vectors to a thread once there are enough threads for every SM with one
   const int U = n >= 2048LL * 148 ? 2 : 1;

@@ -27,17 +27,29 @@ __device__ __forceinline__ float scale_of(uint32_t top) {
   return __uint_as_float(max(top, __float_as_uint(kFloor))) * (1.f / kTop);
 }
 
+// Without the steps that would keep subnormal arguments and results: off by 2^-22 and 2^-23.
+__device__ __forceinline__ float exp2_fast(float x) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+__device__ __forceinline__ float rcp_fast(float x) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+
 // Two codes, the first in the low byte.
 __device__ __forceinline__ uint32_t encode2(float a, float b) {
   uint16_t r;
   asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(b), "f"(a));
   return r;
 }
-// Eight codes of v / scale.  The fast reciprocal is off by at most 2^-23 (scales are normal numbers
-// below 2^120) and the product rounded once: together less than 2^-22 of the value, which changes a
-// code only that close to a border of two.
+// Eight codes of v / scale.  Scales are normal numbers below 2^120; their reciprocal is off by at most
+// 2^-23 and the product rounded once: together less than 2^-22 of the value, which changes a code only
+// that close to a border of two.
 __device__ __forceinline__ uint2 encode8(const float (&v)[8], float scale) {
-  const float inv = __fdividef(1.f, scale);
+  const float inv = rcp_fast(scale);
   uint2 r;
   r.x = encode2(v[0] * inv, v[1] * inv) | encode2(v[2] * inv, v[3] * inv) << 16;
   r.y = encode2(v[4] * inv, v[5] * inv) | encode2(v[6] * inv, v[7] * inv) << 16;
@@ -83,6 +95,14 @@ __device__ __forceinline__ uint32_t top8(const float (&v)[8]) {
 #pragma unroll
   for (int i = 1; i < 8; ++i) t = max(t, size_of(v[i]));
   return t;
+}
+// The same of eight 16-bit values, whose bits are ordered alike.
+template <bool BF16>
+__device__ __forceinline__ uint32_t top_of_words(uint4 v) {
+  constexpr uint32_t kSign = 0x7FFF7FFFu;
+  const uint32_t t = __vmaxu2(__vmaxu2(v.x & kSign, v.y & kSign), __vmaxu2(v.z & kSign, v.w & kSign));
+  const float2 f = unpack2<BF16>(t);
+  return max(__float_as_uint(f.x), __float_as_uint(f.y));
 }
 // Over the sixteen lanes whose eight columns each make up a block.
 __device__ __forceinline__ uint32_t top_of_block(uint32_t t) {
