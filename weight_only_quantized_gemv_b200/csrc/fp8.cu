@@ -26,14 +26,22 @@ __device__ __forceinline__ uint4 load16(const void* p) {
   return __ldcg(reinterpret_cast<const uint4*>(p));
 }
 
-// The block's sum, in every thread; `red` has a word per warp and is used in turn (`half`).
-__device__ __forceinline__ float block_sum(float v, float (&red)[2][32], int half) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
+// 16 bytes into shared memory, past L1.
+__device__ __forceinline__ void copy16(uint4* dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(qlk::smem_addr(dst)), "l"(src)
+               : "memory");
+}
+
+// The sum over a group of whole warps, in every one of its threads; `red` has a word per warp and
+// two of them are used in turn, `barrier` is the group's own (0: the block is the group).
+__device__ __forceinline__ float group_sum(float v, float (&red)[32], int tid, int threads,
+                                           int barrier) {
+  const int lane = tid & 31;
 #pragma unroll
   for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-  if (lane == 0) red[half][warp] = v;
-  __syncthreads();
-  v = lane < warps ? red[half][lane] : 0.f;
+  if (lane == 0) red[tid >> 5] = v;
+  asm volatile("bar.sync %0, %1;" ::"r"(barrier), "r"(threads) : "memory");
+  v = lane < threads >> 5 ? red[lane] : 0.f;
 #pragma unroll
   for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
   return v;
@@ -60,7 +68,7 @@ struct NormParams {
 // output, so that the row is read once.
 template <bool BF16, int V>
 __global__ void __launch_bounds__(1024) norm_kernel(const NormParams P) {
-  __shared__ float red[2][32];
+  __shared__ float red[32];
   const int row = blockIdx.x, step = 8 * (int)blockDim.x, c0 = 8 * (int)threadIdx.x;
   const size_t base = (size_t)row * P.K;
   uint4 w[V];
@@ -96,7 +104,7 @@ __global__ void __launch_bounds__(1024) norm_kernel(const NormParams P) {
 #pragma unroll
     for (int e = 0; e < 8; ++e) sum = fmaf(t[e], t[e], sum);
   }
-  const float rstd = rsqrtf(block_sum(sum, red, 0) / (float)P.K + P.eps);
+  const float rstd = rsqrtf(group_sum(sum, red, threadIdx.x, blockDim.x, 0) / (float)P.K + P.eps);
   if (P.rstd && threadIdx.x == 0) P.rstd[row] = rstd;
 #pragma unroll
   for (int i = 0; i < V; ++i) {
@@ -128,41 +136,62 @@ struct NormGradParams {
   const uint16_t* dtotal;  // [M][K] or null
   uint16_t* dx;            // [M][K]
   float* partials;         // [blocks][K] or null: sums of dy t rstd over a block's rows
-  int M, K;
+  int M, K, threads;       // threads of a group
 };
 
-// A block takes every gridDim-th row and keeps the sums of its columns in registers.
-template <bool BF16, int V>
+// A block is up to eight groups of P.threads threads.  A group takes a row at a time and keeps the
+// sums of the columns in registers; the groups' meet at the end, so that a block leaves one set of
+// sums.  A thread copies its own vectors of the S - 1 rows ahead into shared memory (no other thread
+// reads them), since the wait for a row's sum leaves no other way to keep enough loads under way.
+template <bool BF16, int V, int S>
 __global__ void __launch_bounds__(1024) norm_grad_kernel(const NormGradParams P) {
-  __shared__ float red[2][32];
-  const int step = 8 * (int)blockDim.x, c0 = 8 * (int)threadIdx.x;
+  extern __shared__ __align__(16) uint4 stages[];  // [group][S][array][V][thread]; then the sums
+  __shared__ float red[8][2][32];
+  const int threads = P.threads, groups = (int)blockDim.x / threads;
+  const int group = (int)threadIdx.x / threads, tid = (int)threadIdx.x - group * threads;
+  const int step = 8 * threads, c0 = 8 * tid;
+  const int arrays = P.dtotal ? 3 : 2;
+  const int hop = V * threads, stage = arrays * hop;
+  uint4* const mine = stages + group * S * stage + tid;
   uint4 w[V];
   float dw[V][8] = {};
 #pragma unroll
-  for (int i = 0; i < V; ++i)
+  for (int i = 0; i < V; ++i) {
+    w[i] = make_uint4(0, 0, 0, 0);
     if (c0 + i * step < P.K) w[i] = *reinterpret_cast<const uint4*>(P.weight + c0 + i * step);
+  }
   qlk::grid_dependents_launch();
   qlk::grid_dependency_wait();
-  int half = 0;
-  for (int row = blockIdx.x; row < P.M; row += gridDim.x, half ^= 1) {
+  auto copy = [&](int row, int s) {
     const size_t base = (size_t)row * P.K;
-    uint4 a[V], d[V], r[V];
 #pragma unroll
     for (int i = 0; i < V; ++i) {
       const int c = c0 + i * step;
-      if (c >= P.K) continue;
-      a[i] = load16(P.total + base + c);
-      d[i] = load16(P.dy + base + c);
-      if (P.dtotal) r[i] = load16(P.dtotal + base + c);
+      if (row < P.M && c < P.K) {
+        uint4* o = mine + s * stage + i * threads;
+        copy16(o, P.total + base + c);
+        copy16(o + hop, P.dy + base + c);
+        if (P.dtotal) copy16(o + 2 * hop, P.dtotal + base + c);
+      }
     }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  };
+  const int rows = (int)gridDim.x * groups;
+  int row = (int)blockIdx.x * groups + group;
+#pragma unroll
+  for (int s = 0; s < S - 1; ++s) copy(row + s * rows, s);
+  for (int s = 0, half = 0; row < P.M; row += rows, half ^= 1) {
+    copy(row + (S - 1) * rows, s + S - 1 < S ? s + S - 1 : s - 1);
     const float rstd = __ldcg(P.rstd + row);
+    asm volatile("cp.async.wait_group %0;" ::"n"(S - 1) : "memory");
+    const uint4* x = mine + s * stage;
     float sum = 0.f;
 #pragma unroll
     for (int i = 0; i < V; ++i) {
       if (c0 + i * step >= P.K) continue;
       float t[8], g[8], v[8];
-      unpack8<BF16>(a[i], t);
-      unpack8<BF16>(d[i], g);
+      unpack8<BF16>(x[i * threads], t);
+      unpack8<BF16>(x[i * threads + hop], g);
       unpack8<BF16>(w[i], v);
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
@@ -171,39 +200,60 @@ __global__ void __launch_bounds__(1024) norm_grad_kernel(const NormGradParams P)
         dw[i][e] = fmaf(g[e], n, dw[i][e]);
       }
     }
-    const float mean = block_sum(sum, red, half) / (float)P.K;
+    const float mean = group_sum(sum, red[group][half], tid, threads, 1 + group) / (float)P.K;
 #pragma unroll
     for (int i = 0; i < V; ++i) {
       const int c = c0 + i * step;
       if (c >= P.K) continue;
       float t[8], g[8], v[8];
-      unpack8<BF16>(a[i], t);
-      unpack8<BF16>(d[i], g);
+      unpack8<BF16>(x[i * threads], t);
+      unpack8<BF16>(x[i * threads + hop], g);
       unpack8<BF16>(w[i], v);
 #pragma unroll
       for (int e = 0; e < 8; ++e) t[e] = rstd * (g[e] * v[e] - t[e] * rstd * mean);
       if (P.dtotal) {
-        unpack8<BF16>(r[i], g);
+        unpack8<BF16>(x[i * threads + 2 * hop], g);
 #pragma unroll
         for (int e = 0; e < 8; ++e) t[e] += g[e];
       }
-      *reinterpret_cast<uint4*>(P.dx + base + c) = pack8<BF16>(t);
+      *reinterpret_cast<uint4*>(P.dx + (size_t)row * P.K + c) = pack8<BF16>(t);
     }
+    s = s + 1 < S ? s + 1 : 0;
   }
-  if (P.partials)
+  asm volatile("cp.async.wait_group 0;" ::: "memory");
+  if (!P.partials) return;
+  // the groups' sums, added in their order: [group - 1][V][2][thread]
+  float4* const sums = reinterpret_cast<float4*>(stages) + tid;
+  if (groups > 1) {
+    __syncthreads();
+    if (group > 0)
 #pragma unroll
-    for (int i = 0; i < V; ++i) {
-      const int c = c0 + i * step;
-      if (c >= P.K) continue;
-      float4* o = reinterpret_cast<float4*>(P.partials + (size_t)blockIdx.x * P.K + c);
-      o[0] = make_float4(dw[i][0], dw[i][1], dw[i][2], dw[i][3]);
-      o[1] = make_float4(dw[i][4], dw[i][5], dw[i][6], dw[i][7]);
+      for (int i = 0; i < 2 * V; ++i) {
+        const float* d = &dw[i >> 1][4 * (i & 1)];
+        sums[(group - 1) * 2 * hop + i * threads] = make_float4(d[0], d[1], d[2], d[3]);
+      }
+    __syncthreads();
+    if (group > 0) return;
+  }
+#pragma unroll
+  for (int i = 0; i < 2 * V; ++i) {
+    const float* d = &dw[i >> 1][4 * (i & 1)];
+    float4 t = make_float4(d[0], d[1], d[2], d[3]);
+    for (int g = 1; g < groups; ++g) {
+      const float4 o = sums[(g - 1) * 2 * hop + i * threads];
+      t.x += o.x;
+      t.y += o.y;
+      t.z += o.z;
+      t.w += o.w;
     }
+    const int c = c0 + (i >> 1) * step + 4 * (i & 1);
+    if (c < P.K) *reinterpret_cast<float4*>(P.partials + (size_t)blockIdx.x * P.K + c) = t;
+  }
 }
 
-// dweight[c] = the blocks' sums, added in a fixed order: warp w of a block takes every eighth, its
-// lanes the columns, and the eight meet in shared memory.
-constexpr int kJoinWarps = 8;
+// dweight[c] = the blocks' sums, added in a fixed order: warp w of a block takes every 32nd, its
+// lanes the columns, and they meet in shared memory.
+constexpr int kJoinWarps = 32;
 __global__ void __launch_bounds__(32 * kJoinWarps) norm_join_kernel(const float* partials,
                                                                     float* dweight, int blocks,
                                                                     int K) {
@@ -453,11 +503,12 @@ int sm_count() {
 
 // The kernel may start while the one before it ends (it waits for that one's results itself).
 template <class... Params, class... Args>
-ql_status launch_early(void (*kernel)(Params...), unsigned grid, int threads, ql_stream_t stream,
-                       const Args&... args) {
+ql_status launch_early_smem(void (*kernel)(Params...), unsigned grid, int threads, size_t smem,
+                            ql_stream_t stream, const Args&... args) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(grid);
   cfg.blockDim = dim3((unsigned)threads);
+  cfg.dynamicSmemBytes = smem;
   cfg.stream = reinterpret_cast<cudaStream_t>(stream);
   cudaLaunchAttribute attr;
   attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -465,6 +516,11 @@ ql_status launch_early(void (*kernel)(Params...), unsigned grid, int threads, ql
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
   return cudaLaunchKernelEx(&cfg, kernel, args...) == cudaSuccess ? QL_OK : QL_ERR_CUDA;
+}
+template <class... Params, class... Args>
+ql_status launch_early(void (*kernel)(Params...), unsigned grid, int threads, ql_stream_t stream,
+                       const Args&... args) {
+  return launch_early_smem(kernel, grid, threads, 0, stream, args...);
 }
 
 // Threads of a norm's block, for V vectors each.
@@ -479,16 +535,38 @@ ql_status launch_norm(const NormParams& P, ql_stream_t st) {
   return launch_early(norm_kernel<BF16, 4>, P.M, t, st, P);
 }
 
-int norm_grad_blocks(int M, int K, int sms) {
-  const int t = norm_threads(K, norm_vectors(K)), per = t <= 512 ? 2 : 1;
-  return M < sms * per ? M : sms * per;
+// The norm's gradient: one block per SM, its groups filling it.
+constexpr int kGradSmem = 200 * 1024;
+int norm_grad_vectors(int K) { return K <= 2048 ? 1 : K <= 16384 ? 2 : 4; }
+int norm_grad_blocks(int M, int sms) { return M < sms ? M : sms; }
+template <bool BF16, int V, int S>
+ql_status launch_norm_grad_as(const NormGradParams& P, int blocks, int groups, size_t bytes,
+                              ql_stream_t st) {
+  auto kernel = norm_grad_kernel<BF16, V, S>;
+  // (set with each launch: it is the current device's)
+  if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kGradSmem) !=
+      cudaSuccess)
+    return QL_ERR_CUDA;
+  // (the groups' sums, two thirds of a stage's two arrays and more, use the same memory)
+  return launch_early_smem(kernel, blocks, groups * P.threads, groups * S * bytes, st, P);
+}
+template <bool BF16, int V>
+ql_status launch_norm_grad_v(NormGradParams P, int blocks, ql_stream_t st) {
+  P.threads = norm_threads(P.K, V);
+  const size_t bytes = (size_t)(P.dtotal ? 3 : 2) * V * P.threads * 16;  // of a row
+  int groups = P.M < 2 * blocks ? 1 : 1024 / P.threads < 8 ? 1024 / P.threads : 8;
+  while (groups > 1 && 2 * bytes * groups > kGradSmem) --groups;  // the next row on its way at least
+  const size_t room = kGradSmem / groups;
+  if (4 * bytes <= room) return launch_norm_grad_as<BF16, V, 4>(P, blocks, groups, bytes, st);
+  if (2 * bytes <= room) return launch_norm_grad_as<BF16, V, 2>(P, blocks, groups, bytes, st);
+  return launch_norm_grad_as<BF16, V, 1>(P, blocks, groups, bytes, st);
 }
 template <bool BF16>
 ql_status launch_norm_grad(const NormGradParams& P, int blocks, ql_stream_t st) {
-  const int V = norm_vectors(P.K), t = norm_threads(P.K, V);
-  if (V == 1) return launch_early(norm_grad_kernel<BF16, 1>, blocks, t, st, P);
-  if (V == 2) return launch_early(norm_grad_kernel<BF16, 2>, blocks, t, st, P);
-  return launch_early(norm_grad_kernel<BF16, 4>, blocks, t, st, P);
+  const int V = norm_grad_vectors(P.K);
+  if (V == 1) return launch_norm_grad_v<BF16, 1>(P, blocks, st);
+  if (V == 2) return launch_norm_grad_v<BF16, 2>(P, blocks, st);
+  return launch_norm_grad_v<BF16, 4>(P, blocks, st);
 }
 
 template <int WHAT, bool BF16, int ACT>
@@ -703,7 +781,7 @@ extern "C" ql_status qlinear_rmsnorm(int type, const void* x, long long ldx, con
 extern "C" size_t qlinear_rmsnorm_workspace_bytes(int M, int K) {
   if (M < 1 || M > kMaxRows || !cols_ok(K) || K > kMaxNorm) return 0;
   const int sms = sm_count();
-  return sms > 0 ? kPartials + qfused::align_up((size_t)norm_grad_blocks(M, K, sms) * K * 4, 256)
+  return sms > 0 ? kPartials + qfused::align_up((size_t)norm_grad_blocks(M, sms) * K * 4, 256)
                  : 0;
 }
 
@@ -720,7 +798,7 @@ extern "C" ql_status qlinear_rmsnorm_backward(int type, const void* dy, const vo
     return QL_ERR_ALIGN;
   const int sms = sm_count();
   if (sms <= 0) return QL_ERR_CUDA;
-  const int blocks = norm_grad_blocks(M, K, sms);
+  const int blocks = norm_grad_blocks(M, sms);
   if (dweight) {
     if (!workspace || workspace_bytes < kPartials + (size_t)blocks * K * 4)
       return QL_ERR_WORKSPACE;
