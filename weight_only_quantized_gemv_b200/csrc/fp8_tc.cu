@@ -233,10 +233,8 @@ __device__ __forceinline__ void schedule(Plan& p, int steps, int W) {
   p.runners = 0;
   if (R == 0) return;
   const int f = min(min(W / R, steps), kMaxParts);
-  if (RUNS && f < kMaxParts && 100 * R * f < 85 * W && (long long)R * steps >= W)
-    p.runners = W;
-  else
-    p.runners = R * f;
+  const bool runs = RUNS && f < kMaxParts && (long long)R * steps >= W && 100 * R * f < 60 * W;
+  p.runners = runs ? W : R * f;
 }
 
 // ---------------------------------------------------------------------------
@@ -822,13 +820,23 @@ __global__ void __launch_bounds__(Wide::kThreads, 1)
         if ((P.test_us & 0xFFFFu) && wk == 0) qlk::test_delay(P.test_us & 0xFFFFu);
         while (ok && sg.next(plan, P.steps, t, k0, k1, slot)) {
           const Tile T = wide_tile_of(P, plan, t);
-          const int m = T.m0 + (int)rank * 128, row = (T.rt * 2 + (int)rank) * 128;
+          const int row = (T.rt * 2 + (int)rank) * 128;
+          // rows of q that the CTAs copy, in units of 32 (the others' products are not stored)
+          const int need = (T.rows + 31) & ~31, mine = min(max(need - (int)rank * 128, 0), 128);
+          const uint32_t bytes = 2 * C::kBytes + need * 128;
 #pragma unroll 1
           for (int k = k0; k < k1; ++k) {
             if (n >= C::S && !(ok = wait<64>(empty(s), ph, W, kErrStage))) break;
             const uint32_t a = ring + s * C::kStageBytes;
-            if (leader) qlk::mbar_arrive_expect_tx(full(s), 2 * C::kStageBytes);
-            tma_2d_pair(a, &maps.q[0], k * 128, m, lead(full(s)));
+            if (leader) qlk::mbar_arrive_expect_tx(full(s), bytes);
+            int at = 0;
+#pragma unroll
+            for (int i = 0; i < 3; ++i) {  // 128, 64 and 32 rows
+              if (!(mine & (128 >> i))) continue;
+              tma_2d_pair(a + at * 128, &maps.q[i], k * 128, T.m0 + (int)rank * 128 + at,
+                          lead(full(s)));
+              at += 128 >> i;
+            }
             copy_3d<true>(a + C::kBytes, &maps.w, BWD ? row : k * 128, BWD ? k * 128 : row, T.e,
                           lead(full(s)));
             ++n;
@@ -1194,7 +1202,7 @@ ql_status launch_as(const Product& p) {
   const cuuint64_t wdims[3] = {(cuuint64_t)p.K, (cuuint64_t)p.N, (cuuint64_t)p.E};
   const cuuint64_t qdims[2] = {(cuuint64_t)(BWD ? p.N : p.K), (cuuint64_t)p.M};
   if (!encode(&maps.w, p.w, 3, wdims, 128)) return QL_ERR_CUDA;
-  for (int i = C::kCtas == 2 ? 0 : 1; i < (C::kCtas == 2 ? 1 : 4); ++i)
+  for (int i = C::kCtas == 2 ? 0 : 1; i < (C::kCtas == 2 ? 3 : 4); ++i)
     if ((128 >> i) <= C::kBRows && !encode(&maps.q[i], p.q, 2, qdims, 128 >> i)) return QL_ERR_CUDA;
   // every worker that can run: how many have work is known on the device.  A second CTA on each SM
   // where both have kLongRun steps and more
