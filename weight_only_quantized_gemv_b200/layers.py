@@ -766,9 +766,11 @@ class RMSNorm(_FusedWorkspace):
 
     def __init__(self, weight: torch.Tensor, eps: float = 1e-6):
         weight = weight.detach()
-        if weight.dtype not in _TYPE_OF or weight.dim() != 1 or not weight.is_cuda:
-            raise ValueError("the weight is a float16 or bfloat16 vector on a CUDA device")
-        self.weight, self.eps, self.K = weight.contiguous(), eps, weight.shape[0]
+        if (weight.dtype not in _TYPE_OF or weight.dim() != 1 or not weight.is_cuda
+                or not weight.is_contiguous()):
+            raise ValueError("the weight is a contiguous float16 or bfloat16 vector on a CUDA "
+                             "device")
+        self.weight, self.eps, self.K = weight, eps, weight.shape[0]
         self._fused_lock = threading.RLock()
         self._fused = (None, self.K, self.K, weight.get_device())
 
@@ -851,7 +853,7 @@ class RMSNorm(_FusedWorkspace):
 class _Fp8Weights(_FusedWorkspace):
     """e4m3 codes [..., N, K] and scales [..., ceil(N / 128), ceil(K / 128)] on a CUDA device; a
     workspace as in the fused layers, which any of these layers' calls that follow one another may
-    share."""
+    share.  The constructor waits for the current stream: a layer's weights are complete."""
 
     def _fp8_setup(self, codes, scales, dims: int, device) -> None:
         codes = torch.as_tensor(codes).detach()
@@ -872,6 +874,9 @@ class _Fp8Weights(_FusedWorkspace):
         self.scales = scales.to(device).contiguous()
         self.device, self.N, self.K = self.codes.device, N, K
         self.E = lead[0] if lead else 1
+        if self.device.type == "cuda":
+            # the products read weights before the kernels ahead of them have ended
+            torch.cuda.current_stream(self.device).synchronize()
         self._fused_lock = threading.RLock()
         self._fused = (None, N, K, self.codes.get_device())
 
@@ -1001,8 +1006,9 @@ class Fp8GatedMLP:
                 layer.reserve(rows, backward)
 
     def new_workspace(self, rows: int, backward: bool = True) -> torch.Tensor:
-        """A zero-filled workspace for the products of calls of up to `rows` rows."""
-        return max((lay.new_workspace(rows, backward) for lay in (self.gate_up, self.down)),
+        """A zero-filled workspace for calls of up to `rows` rows."""
+        layers = [self.gate_up, self.down] + ([self.norm] if self.norm is not None else [])
+        return max((lay.new_workspace(rows, backward) for lay in layers),
                    key=lambda ws: ws.numel())
 
     def _rows(self, offsets) -> tuple:
@@ -1051,4 +1057,4 @@ class Fp8GatedMLP:
         dv = self.gate_up.backward(q, scales, *rows, dtype=dy.dtype, workspace=workspace,
                                    stream=stream)
         return self.norm.backward(dv, total, rstd, dtotal=dtotal, dx=dx, dweight=dweight,
-                                  stream=stream)
+                                  workspace=workspace, stream=stream)
