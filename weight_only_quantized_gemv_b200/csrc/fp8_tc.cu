@@ -69,6 +69,7 @@ struct Cfg {
   // A call is bound by reading the weights: two CTAs on an SM keep more of them on their way, and
   // where one is enough the next call's first weights come while this one ends.
   static constexpr int kPerSm = 2;
+  static constexpr size_t kTileBytes = 128 * BNX * 4;  // of a CTA's sums
   static constexpr int S = 104 * 1024 / kStageBytes;
   static constexpr int kStagingOff = S * kStageBytes;
   static constexpr int kStaging = 16 * kTokStride;           // per epilogue warp
@@ -164,7 +165,7 @@ __device__ __forceinline__ int expert_of(const Params& P, const Plan& plan, int 
   return e;
 }
 
-// Tiles of equal width, a multiple of the granularity; or (wide_tile_of) of 256 rows of q.
+// Tiles of equal width, a multiple of the granularity; or (wide_tile_of) of BNX rows of q.
 template <class C>
 __device__ __forceinline__ Tile tile_of(const Params& P, const Plan& plan, int t) {
   const int e = expert_of(P, plan, t);
@@ -179,11 +180,13 @@ __device__ __forceinline__ Tile tile_of(const Params& P, const Plan& plan, int t
   r.rows = min(r.bn, cnt - m);
   return r;
 }
+template <class C>
 __device__ __forceinline__ Tile wide_tile_of(const Params& P, const Plan& plan, int t) {
   const int e = expert_of(P, plan, t);
   const int lo = plan.start[e], cnt = plan.start[e + 1] - lo;
-  const int mt = (cnt + 255) / 256, l = t - plan.pre[e], rt = l / mt, m = 256 * (l - rt * mt);
-  return Tile{e, rt, lo + m, min(256, cnt - m), 256};
+  const int mt = (cnt + C::BNX - 1) / C::BNX, l = t - plan.pre[e], rt = l / mt;
+  const int m = C::BNX * (l - rt * mt);
+  return Tile{e, rt, lo + m, min(C::BNX, cnt - m), C::BNX};
 }
 
 // The work of a worker (CTA or pair): whole tiles w, w + W, ..., then its run of the steps of
@@ -733,13 +736,21 @@ __global__ void __launch_bounds__(Cfg<BNX>::kThreads, Cfg<BNX>::kPerSm)
 // operand.  A thread's share of the accumulator is then a row of q and 128 of D's rows, one block
 // of the weights: a step has one product of scales per thread.
 
+//
+// Up to 128 rows of q (an expert's, on average) single CTAs take 128 x 256 tiles, !PAIR: they read
+// weights at twice the rate.
+template <bool PAIR_>
 struct Wide {
-  static constexpr int BNX = 256, kCtas = 2, kBlocks = 2, kBRows = 128, kPerSm = 1;
-  static constexpr int kBytes = 128 * 128;         // of an operand, per CTA and step
-  static constexpr int S = 6, kStageBytes = 2 * kBytes;
+  static constexpr bool PAIR = PAIR_;
+  static constexpr int kCtas = PAIR ? 2 : 1, kBlocks = 2, kBRows = 128, kPerSm = 1;
+  static constexpr int BNX = 128 * kCtas;          // rows of q per tile
+  static constexpr int kBytes = 128 * 128;         // of 128 rows of an operand, per step
+  static constexpr int kOwn = 2 / kCtas;           // of the tile's two blocks of weights, a CTA's
+  static constexpr int kStageBytes = (1 + kOwn) * kBytes, S = 200 * 1024 / kStageBytes;
   static constexpr int kEpiWarps = 8, kEpiWarp0 = 4;
   static constexpr int kThreads = 32 * (kEpiWarp0 + kEpiWarps);
   static constexpr int kAcc = 2;
+  static constexpr size_t kTileBytes = 128 * 256 * 4;  // of a CTA's sums
   static constexpr int kStagingOff = S * kStageBytes;
   static constexpr int kStaging = 32 * kTokStride; // per epilogue warp: 32 rows of 32 columns
   static constexpr int kScaleWarps = 1;
@@ -757,10 +768,10 @@ struct Wide {
   static_assert(kThreads == 384 && 2 * kRegsEpi + kRegsOther <= 3 * 168, "registers");
 };
 
-template <bool BWD>
-__global__ void __launch_bounds__(Wide::kThreads, 1)
+template <bool PAIR, bool BWD>
+__global__ void __launch_bounds__(Wide<PAIR>::kThreads, 1)
     fp8_wide_kernel(const Params P, const __grid_constant__ Maps maps) {
-  using C = Wide;
+  using C = Wide<PAIR>;
   extern __shared__ __align__(1024) uint8_t smem[];
   const uint32_t ring = qlk::smem_addr(smem);
   const uint32_t bars = ring + C::kBarOff;
@@ -775,10 +786,10 @@ __global__ void __launch_bounds__(Wide::kThreads, 1)
   const WaitCtx W{ring + C::kMiscOff + 4, P.err, P.wait_us};
   const int warp = __shfl_sync(0xffffffffu, (int)(threadIdx.x >> 5), 0);  // uniform
   const int lane = threadIdx.x & 31;
-  const uint32_t rank = blockIdx.x & 1u;
+  const uint32_t rank = PAIR ? blockIdx.x & 1u : 0u;  // of the cluster (2, 1, 1)
   const bool leader = rank == 0;
-  const int wk = (int)(blockIdx.x >> 1), nwk = (int)(gridDim.x >> 1);
-  auto lead = [&](uint32_t b) { return leader ? b : cluster_addr(b, 0); };
+  const int wk = (int)blockIdx.x / C::kCtas, nwk = (int)gridDim.x / C::kCtas;
+  auto lead = [&](uint32_t b) { return PAIR && !leader ? cluster_addr(b, 0) : b; };
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < C::S; ++s) {
@@ -787,16 +798,16 @@ __global__ void __launch_bounds__(Wide::kThreads, 1)
     }
     for (int a = 0; a < C::kAcc; ++a) {
       qlk::mbar_init(accf(a), 1 + C::kScaleWarps);
-      qlk::mbar_init(acce(a), 2 * C::kEpiWarps);
+      qlk::mbar_init(acce(a), C::kCtas * C::kEpiWarps);
       qlk::mbar_init(sempty(a), C::kEpiWarps);
       qlk::mbar_init(bars + 8 * (2 * C::S + 3 * C::kAcc + a), 1);  // fin
     }
     misc[1] = 0u;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
-  if (warp == 0) make_table<256>(P, start, pre, lane);
-  sync_all<true>();
-  if (warp == 1) tmem_alloc<true>(ring + C::kMiscOff, 512);
+  if (warp == 0) make_table<C::BNX>(P, start, pre, lane);
+  sync_all<PAIR>();
+  if (warp == 1) tmem_alloc<PAIR>(ring + C::kMiscOff, 512);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -804,7 +815,7 @@ __global__ void __launch_bounds__(Wide::kThreads, 1)
   qlk::grid_dependents_launch();  // (behind the allocation: the next grid's must not come first)
 
   Plan plan{start, pre, pre[P.E], 0, 0};
-  schedule<true>(plan, P.steps, nwk);
+  schedule<PAIR>(plan, P.steps, nwk);
   Segments sg;
   sg.init(plan, P.steps, wk, nwk);
   int t, k0, k1, slot = 0;
@@ -819,11 +830,11 @@ __global__ void __launch_bounds__(Wide::kThreads, 1)
         qlk::grid_dependency_wait();
         if ((P.test_us & 0xFFFFu) && wk == 0) qlk::test_delay(P.test_us & 0xFFFFu);
         while (ok && sg.next(plan, P.steps, t, k0, k1, slot)) {
-          const Tile T = wide_tile_of(P, plan, t);
-          const int row = (T.rt * 2 + (int)rank) * 128;
+          const Tile T = wide_tile_of<C>(P, plan, t);
+          const int row = (T.rt * 2 + (int)rank * C::kOwn) * 128;  // of D
           // rows of q that the CTAs copy, in units of 32 (the others' products are not stored)
           const int need = (T.rows + 31) & ~31, mine = min(max(need - (int)rank * 128, 0), 128);
-          const uint32_t bytes = 2 * C::kBytes + need * 128;
+          const uint32_t bytes = 2 * C::kBytes + need * 128;  // of both CTAs of a pair
 #pragma unroll 1
           for (int k = k0; k < k1; ++k) {
             if (n >= C::S && !(ok = wait<64>(empty(s), ph, W, kErrStage))) break;
@@ -833,12 +844,19 @@ __global__ void __launch_bounds__(Wide::kThreads, 1)
 #pragma unroll
             for (int i = 0; i < 3; ++i) {  // 128, 64 and 32 rows
               if (!(mine & (128 >> i))) continue;
-              tma_2d_pair(a + at * 128, &maps.q[i], k * 128, T.m0 + (int)rank * 128 + at,
-                          lead(full(s)));
+              const int m = T.m0 + (int)rank * 128 + at;
+              if constexpr (PAIR)
+                tma_2d_pair(a + at * 128, &maps.q[i], k * 128, m, lead(full(s)));
+              else
+                tma_2d(a + at * 128, &maps.q[i], k * 128, m, full(s));
               at += 128 >> i;
             }
-            copy_3d<true>(a + C::kBytes, &maps.w, BWD ? row : k * 128, BWD ? k * 128 : row, T.e,
-                          lead(full(s)));
+#pragma unroll
+            for (int b = 0; b < C::kOwn; ++b) {
+              const int r = row + b * 128;
+              copy_3d<PAIR>(a + (1 + b) * C::kBytes, &maps.w, BWD ? r : k * 128,
+                            BWD ? k * 128 : r, T.e, lead(full(s)));
+            }
             ++n;
             if (++s == C::S) {
               s = 0;
@@ -852,7 +870,7 @@ __global__ void __launch_bounds__(Wide::kThreads, 1)
         if (leader)
           for (int i = n > C::S ? n - C::S : 0; i < n; ++i)
             wait<0>(full(i % C::S), (i / C::S) & 1, W, kErrStage, false);
-        if (!ok) qlk::test_delay(kSettleUs);
+        if (PAIR && !ok) qlk::test_delay(kSettleUs);
       }
     } else if (warp & 1) {
       // ---- MMA issue by the leader: warp 1 the even steps, warp 3 the odd ones, an accumulator each.
@@ -861,7 +879,9 @@ __global__ void __launch_bounds__(Wide::kThreads, 1)
       if (leader) {
         qlk::grid_dependency_wait();
         if ((P.test_us >> 16) && wk == 0) qlk::test_delay(P.test_us >> 16);
-        constexpr uint32_t idesc = idesc_f16(256, 256) | (BWD ? kTransposeB : 0u);
+        constexpr uint32_t idesc = idesc_f16(128 * C::kCtas, 256) | (BWD ? kTransposeB : 0u);
+        // (read MN-major a single CTA's two blocks of the weights are panels 16384 bytes apart)
+        constexpr uint32_t kDescLoB = BWD ? (uint32_t)(C::kBytes / 16) << 16 : kDescLo;
         const int a = warp >> 1;
         const uint32_t fin = bars + 8 * (2 * C::S + 3 * C::kAcc + a);
         int s = a, ph = 0, aph = 1, n = 0;
@@ -873,14 +893,14 @@ __global__ void __launch_bounds__(Wide::kThreads, 1)
             if (!(ok = warp_wait<0>(full(s), ph, W, kErrStage, lane))) break;
             if (n > 0 && !(ok = warp_wait<0>(acce(a), aph, W, kErrAcc, lane))) break;
             tc_fence_after();
-            const uint32_t pa = ((ring + s * C::kStageBytes) >> 4) | kDescLo;
-            const uint32_t pb = pa + (C::kBytes >> 4);
+            const uint32_t st = (ring + s * C::kStageBytes) >> 4;
+            const uint32_t pa = st | kDescLo, pb = (st + (C::kBytes >> 4)) | kDescLoB;
             if (elect_one()) {
 #pragma unroll
               for (int kk = 0; kk < 4; ++kk)
-                mma<true>(tmem + a * 256, pa + 2 * kk, pb + (BWD ? 256 : 2) * kk, idesc, kk != 0);
-              commit_both<true>(accf(a));
-              commit_both<true>(empty(s));
+                mma<PAIR>(tmem + a * 256, pa + 2 * kk, pb + (BWD ? 256 : 2) * kk, idesc, kk != 0);
+              commit_both<PAIR>(accf(a));
+              commit_both<PAIR>(empty(s));
             }
             __syncwarp();
             ++n;
@@ -892,11 +912,11 @@ __global__ void __launch_bounds__(Wide::kThreads, 1)
           }
         }
         if (n > 0) {
-          if (elect_one()) tc_commit<true>(fin);
+          if (elect_one()) tc_commit<PAIR>(fin);
           __syncwarp();
           warp_wait<0>(fin, 0, W, kErrAcc, lane, false);
         }
-        if (!ok || misc[1]) qlk::test_delay(kSettleUs);
+        if (PAIR && (!ok || misc[1])) qlk::test_delay(kSettleUs);
       }
     } else {
       // ---- products of scales: rows 32 i + lane of this CTA's, by both blocks of the weights.  Two
@@ -905,7 +925,7 @@ __global__ void __launch_bounds__(Wide::kThreads, 1)
       int a = 0, aph = 1, n = 0;
       bool ok = true;
       while (ok && sg.next(plan, P.steps, t, k0, k1, slot)) {
-        const Tile T = wide_tile_of(P, plan, t);
+        const Tile T = wide_tile_of<C>(P, plan, t);
         const int last = T.rows - 1 - (int)rank * 128, least = -(int)rank * 128;
         const float* sx = P.sx + (size_t)(T.m0 - least) * P.steps;
         int row[4];  // of the tile's rows, in scales
@@ -975,7 +995,7 @@ __global__ void __launch_bounds__(Wide::kThreads, 1)
     int a = 0, aph = 0;
     bool ok = true;
     while (ok && sg.next(plan, P.steps, t, k0, k1, slot)) {
-      const Tile T = wide_tile_of(P, plan, t);
+      const Tile T = wide_tile_of<C>(P, plan, t);
       float acc[128];
 #pragma unroll
       for (int c = 0; c < 128; ++c) acc[c] = 0.f;
@@ -996,7 +1016,7 @@ __global__ void __launch_bounds__(Wide::kThreads, 1)
             tc_fence_before();
             __syncwarp();
             if (lane == 0) {
-              if (leader)
+              if (!PAIR || leader)
                 qlk::mbar_arrive(acce(a));
               else  // (says only when: see arrive_stage in fused_tc.cu)
                 asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(lead(acce(a)))
@@ -1028,7 +1048,7 @@ __global__ void __launch_bounds__(Wide::kThreads, 1)
         const int wf = worker_of(ub, U, plan.runners);
         const int wl = worker_of(ub + P.steps - 1, U, plan.runners);
         uint32_t* counter =
-            P.counters + ((size_t)(t - plan.whole) * 2 + rank) * C::kEpiWarps + ew;
+            P.counters + ((size_t)(t - plan.whole) * C::kCtas + rank) * C::kEpiWarps + ew;
         uint32_t prev = 0;
         if (lane == 0) prev = arrive_weight(counter, 1u);
         prev = __shfl_sync(0xffffffffu, prev, 0);
@@ -1040,7 +1060,7 @@ __global__ void __launch_bounds__(Wide::kThreads, 1)
 #pragma unroll 1
         for (int w2 = wf; w2 <= wl; ++w2) {
           const uint8_t* src =
-              base + (size_t)(2 * (w2 * 2 + (int)rank) + (w2 == wf ? first : 0)) * kSlot;
+              base + (size_t)(2 * (w2 * C::kCtas + (int)rank) + (w2 == wf ? first : 0)) * kSlot;
 #pragma unroll
           for (int c = 0; c < 32; ++c) {
             const float4 x = __ldcg(reinterpret_cast<const float4*>(src + c * 512));
@@ -1081,10 +1101,10 @@ __global__ void __launch_bounds__(Wide::kThreads, 1)
   }
 
   tc_fence_before();
-  sync_all<true>();
+  sync_all<PAIR>();
   if (warp == 1) {
     tc_fence_after();
-    tmem_dealloc<true>(tmem, 512);
+    tmem_dealloc<PAIR>(tmem, 512);
   }
 }
 
@@ -1193,8 +1213,7 @@ ql_status launch_as(const Product& p) {
   if ((size_t)C::kPerSm * maxw * C::kCtas * C::kEpiWarps * sizeof(uint32_t) >
       qfused::kTcCounterBytes)
     return QL_ERR_UNSUPPORTED;
-  if (p.partial_bytes < (size_t)2 * C::kPerSm * sms * 128 * C::BNX * sizeof(float))
-    return QL_ERR_WORKSPACE;
+  if (p.partial_bytes < (size_t)2 * C::kPerSm * sms * C::kTileBytes) return QL_ERR_WORKSPACE;
   const qfused::WaitTest wt = qfused::wait_test();
   P.wait_us = (wt.limit_us < 1000000000u ? wt.limit_us : 1000000000u) + 4u * (uint32_t)P.steps;
   P.test_us = wt.delays;
@@ -1202,8 +1221,8 @@ ql_status launch_as(const Product& p) {
   const cuuint64_t wdims[3] = {(cuuint64_t)p.K, (cuuint64_t)p.N, (cuuint64_t)p.E};
   const cuuint64_t qdims[2] = {(cuuint64_t)(BWD ? p.N : p.K), (cuuint64_t)p.M};
   if (!encode(&maps.w, p.w, 3, wdims, 128)) return QL_ERR_CUDA;
-  for (int i = C::kCtas == 2 ? 0 : 1; i < (C::kCtas == 2 ? 3 : 4); ++i)
-    if ((128 >> i) <= C::kBRows && !encode(&maps.q[i], p.q, 2, qdims, 128 >> i)) return QL_ERR_CUDA;
+  for (int i = 0; i < 4; ++i)  // (narrow tiles: 64, 32 and 16 rows; wide ones: 128, 64 and 32)
+    if ((128 >> i) <= C::kBRows && (i < 3 || C::kBRows < 128) && !encode(&maps.q[i], p.q, 2, qdims, 128 >> i)) return QL_ERR_CUDA;
   // every worker that can run: how many have work is known on the device.  A second CTA on each SM
   // where both have kLongRun steps and more
   const long long units = tiles * P.steps;
@@ -1226,7 +1245,9 @@ ql_status launch(const Product& p) {
   if (rows <= 16) return launch_narrow<16, BWD>(p);
   if (rows <= 32) return launch_narrow<32, BWD>(p);
   if (rows <= 64) return launch_narrow<64, BWD>(p);
-  return launch_as<Wide, fp8_wide_kernel<BWD>, BWD>(p);
+  if (rows <= (p.offsets ? 256 : 128))
+    return launch_as<Wide<false>, fp8_wide_kernel<false, BWD>, BWD>(p);
+  return launch_as<Wide<true>, fp8_wide_kernel<true, BWD>, BWD>(p);
 }
 
 }  // namespace
