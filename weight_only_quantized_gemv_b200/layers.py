@@ -649,6 +649,8 @@ def _row_ptr(x: torch.Tensor, index: int, name: str) -> tuple:
     """(data pointer, elements between rows) of a matrix whose rows are contiguous, once checked
     like ``_fused_ptr``'s."""
     M, K = x.shape
+    if x.is_contiguous() and not x.requires_grad:
+        return x.data_ptr(), K
     ld = x.stride(0) if M > 1 else K
     if x.requires_grad and torch.is_grad_enabled() or x.stride(1) != 1 and K > 1 or ld < K:
         _fused_ptr(x, (M, K), index, name, x.dtype)  # says why not
@@ -663,26 +665,26 @@ def _raw_stream(stream, index: int):
 _empties: dict = {dtype: {} for dtype in (_F8, _F32, *_TYPE_OF)}
 
 
-def _new(shape: tuple, dtype, index: int, stream) -> torch.Tensor:
+def _new(dtype, index: int, stream, *shape) -> torch.Tensor:
     """A new tensor on the call's stream."""
     like = _empties[dtype].get(index)
     if like is None:
         like = _empties[dtype][index] = torch.empty(0, dtype=dtype, device=f"cuda:{index}")
     if stream is None:
-        return like.new_empty(shape)
+        return like.new_empty(*shape)  # (quicker than with a tuple)
     with torch.cuda.stream(_as_stream(stream, index)):
-        return like.new_empty(shape)
+        return like.new_empty(*shape)
 
 
 def _codes_out(q, scales, M: int, C: int, index: int, stream) -> tuple:
     """Codes [M, C] and scales, made where they are not given, and their data pointers."""
     if q is None:
-        q = _new((M, C), _F8, index, stream)
+        q = _new(_F8, index, stream, M, C)
         pq = q.data_ptr()
     else:
         pq = _fused_ptr(q, (M, C), index, "q", _F8)
     if scales is None:
-        scales = _new((M, (C + 127) // 128), _F32, index, stream)
+        scales = _new(_F32, index, stream, M, (C + 127) // 128)
         return q, scales, pq, scales.data_ptr()
     return q, scales, pq, _fused_ptr(scales, (M, (C + 127) // 128), index, "scales", _F32)
 
@@ -754,8 +756,8 @@ def fp8_quantize_weights(w: torch.Tensor, stream=None) -> tuple:
     *lead, N, K = w.shape
     with torch.cuda.device(index):
         _fused_ptr(w, w.shape, index, "w", w.dtype)
-        codes = _new(w.shape, _F8, index, stream)
-        scales = _new((*lead, _blocks(N), _blocks(K)), _F32, index, stream)
+        codes = _new(_F8, index, stream, *w.shape)
+        scales = _new(_F32, index, stream, *lead, _blocks(N), _blocks(K))
         qlinear_fp8_quantize_weights(kind, w, codes, scales, lead[0] if lead else 1, N, K, stream)
     return codes, scales
 
@@ -903,7 +905,7 @@ class _Fp8Weights(_FusedWorkspace):
         if kind is None:
             raise ValueError(f"{what} is a float16 or bfloat16 tensor, not {dtype}")
         if out is None:
-            out = _new((M, R), dtype, index, stream)
+            out = _new(dtype, index, stream, M, R)
             pout = out.data_ptr()
         else:
             pout = _fused_ptr(out, (M, R), index, what, dtype)
