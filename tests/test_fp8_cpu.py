@@ -182,3 +182,13 @@ def test_weights_are_checked():
             f(torch.ones(2, 32))
     with pytest.raises(ValueError):
         layers.fp8_quantize_weights(torch.ones(16, 16))
+
+
+def test_run_fp8_helpers():
+    pytest.importorskip("torch")
+    from weight_only_quantized_gemv_b200 import run_fp8
+    at = run_fp8.ragged_offsets(100, 8)
+    assert at[0] == 0 and at[-1] == 100 and sorted(at) == at and at[3] == at[4]
+    assert run_fp8.ragged_offsets(7, 1) == [0, 7]
+    assert run_fp8.moved_bytes("quantize", 2, 0, 256) == 2 * 2 * 256 + 2 * 256 + 4 * 2 * 2
+    assert run_fp8.moved_bytes("linear", 3, 144, 256) == 144 * 256 + 16 + 3 * 256 + 24 + 2 * 3 * 144

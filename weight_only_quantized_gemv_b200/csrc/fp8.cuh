@@ -3,10 +3,11 @@
 //
 // scale = max|v| / 448 over a block, codes e4m3(v / scale), rounded to nearest even.  The codes use
 // the block's largest value for the top of their range, so a value down to 1 / 28672 of it (448
-// over 2^-6, the smallest normal code) keeps its four significant bits.  A block of zeros, or of values
-// below 2^-100, is coded as if its largest value were 2^-100: the scale stays a normal number, and
-// so does its product with a weight's scale above 2^-17.  A block with a NaN or an infinity has a
-// scale that is not finite and a NaN code where the value was, so that no product hides it.
+// over 2^-6, the smallest normal code) keeps its four significant bits.  A block of zeros, or of
+// values below 2^-100, is coded as if its largest value were 2^-100: the scale stays a normal
+// number, and so does its product with a weight's scale above 2^-17.  A block with a NaN or an
+// infinity has a scale that is not finite and a NaN code where the value was, so that no product
+// hides it.
 #pragma once
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -20,8 +21,8 @@ constexpr float kFloor = 7.88860905e-31f;  // 2^-100, see above
 
 __host__ __device__ constexpr int blocks_of(int n) { return (n + kBlock - 1) / kBlock; }
 
-// Sizes are compared as the bits of |v|, whose order is that of the numbers, infinity above them and
-// NaN above that (fmaxf would drop a NaN).
+// Sizes are compared as the bits of |v|, whose order is that of the numbers, infinity above them
+// and NaN above that (fmaxf would drop a NaN).
 __device__ __forceinline__ uint32_t size_of(float v) { return __float_as_uint(v) & 0x7FFFFFFFu; }
 __device__ __forceinline__ float scale_of(uint32_t top) {
   return __uint_as_float(max(top, __float_as_uint(kFloor))) * (1.f / kTop);
@@ -45,9 +46,9 @@ __device__ __forceinline__ uint32_t encode2(float a, float b) {
   asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(b), "f"(a));
   return r;
 }
-// Eight codes of v / scale.  Scales are normal numbers below 2^120; their reciprocal is off by at most
-// 2^-23 and the product rounded once: together less than 2^-22 of the value, which changes a code only
-// that close to a border of two.
+// Eight codes of v / scale.  Scales are normal numbers below 2^120; their reciprocal is off by at
+// most 2^-23 and the product rounded once: together less than 2^-22 of the value, which changes a
+// code only that close to a border of two.
 __device__ __forceinline__ uint2 encode8(const float (&v)[8], float scale) {
   const float inv = rcp_fast(scale);
   uint2 r;
@@ -100,7 +101,8 @@ __device__ __forceinline__ uint32_t top8(const float (&v)[8]) {
 template <bool BF16>
 __device__ __forceinline__ uint32_t top_of_words(uint4 v) {
   constexpr uint32_t kSign = 0x7FFF7FFFu;
-  const uint32_t t = __vmaxu2(__vmaxu2(v.x & kSign, v.y & kSign), __vmaxu2(v.z & kSign, v.w & kSign));
+  const uint32_t t =
+      __vmaxu2(__vmaxu2(v.x & kSign, v.y & kSign), __vmaxu2(v.z & kSign, v.w & kSign));
   const float2 f = unpack2<BF16>(t);
   return max(__float_as_uint(f.x), __float_as_uint(f.y));
 }

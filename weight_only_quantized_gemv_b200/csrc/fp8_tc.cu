@@ -3,9 +3,7 @@
 //   forward   D[n][m] = sum_b sx[m][b] sw[n / 128][b] sum_{k in block b} W[n][k] q[m][k]
 //   backward  D[k][m] = sum_b sd[m][b] sw[b][k / 128] sum_{n in block b} W[n][k] q[m][n]
 //
-// for one matrix or for one per expert, whose rows of q follow one another.  The weights are the
-// MMA's A operand (128 rows per CTA), the rows of q its B operand, so that any multiple of 16 rows
-// makes a tile: what an expert's few rows leave empty is small.
+// for one matrix or for one per expert, whose rows of q follow one another.
 //
 // A pipeline step is one block of the summed index: 128 bytes of every row, the width of the
 // 128-byte swizzle.  Both operands come by tensor copies.  The backward product reads the same
@@ -14,22 +12,23 @@
 //
 // The scales differ from block to block, so the tensor cores' sum covers one block: a step's four
 // MMAs write a fresh accumulator in tensor memory, and the epilogue warps add it, times sx sw, to
-// fp32 sums in registers.  In their share of the accumulator (tcgen05.ld 16x256b) a thread holds
-// two neighbouring columns of each eight, so a step's scales are one 8-byte shared load per four
-// of its packed multiply-adds.
+// fp32 sums in registers.  A warp makes the products of scales, steps ahead, in shared memory.
 //
-// Roles: warp 0 copies, 1 MMA issue and tensor memory, 2 (and 3 for wide tiles) the step's
-// products of scales, then four epilogue warps per column group.
+// Two kernels, by the rows of q that an average expert has:
+//   up to 64     fp8_tc_kernel: the weights are the MMA's A operand (128 rows), q's rows its B
+//                operand, any multiple of 16 of them.  Bound by reading the weights.
+//   above        fp8_wide_kernel: q's rows are the A operand, 256 of D's rows the B operand.
 //
-// PAIR: a cluster of two CTAs on two SMs computes 256 rows with tcgen05 cta_group::2; each CTA
-// copies its own 128 rows of weights and half of the rows of q.
-//
-// Work: tiles of 128 (PAIR 256) rows x up to BNX rows of q.  Whole waves of tiles go round the
-// workers; the rest are cut into runs of steps, whose sums meet in the workspace: the last
-// contributor to arrive adds them in worker order, nobody waits.  For experts all of this is
-// computed on the device, from the offsets.
+// Work: whole waves of tiles go round the workers; the rest are cut by steps (schedule), and the
+// parts' sums meet in the workspace: the last contributor to arrive adds them in worker order,
+// nobody waits.  For experts all of this is computed on the device, from the offsets.
 //
 // Every barrier wait is bounded in time as in the fused products (fused_tc.cu).
+//
+// Measured, us (in brackets the bytes' or the operations' time at the card's rates: a copy's 6.55
+// TB/s, twice cuBLAS' bf16 1.63 PFLOP/s): 1 x 28672 x 8192 39.8 (35.9), 33 rows 44.8 (36.2), 128 x
+// 8192 x 28672 56 (36), 777 x 4096 x 12304 backward 53 (24), 2048 x 8192 x 4096 75 (42), 4096 x
+// 28672 x 8192 879 (589; call after call at the power limit of 1000 W, 1.5 GHz: 1015).
 #include <cuda.h>
 #include <cudaTypedefs.h>
 #include <cuda_runtime.h>
@@ -53,6 +52,9 @@ namespace {
 constexpr uint32_t kErrStage = 1u, kErrAcc = 2u, kErrOffsets = 4u;
 constexpr int kTokStride = 80;  // bytes of a staged row of q's outputs: 32 of them and 16 more
 
+// Few rows of q.  A thread of the epilogue holds two neighbouring columns (rows of q) of each eight
+// (tcgen05.ld 16x256b), so a step's scales are one 8-byte shared load per four of its packed
+// multiply-adds.  Warps: 0 copies, 1 MMA issue and tensor memory, 2 scales, 4 .. 7 epilogue.
 template <int BNX_>
 struct Cfg {
   static constexpr int BNX = BNX_;                 // most rows of q per tile
@@ -226,8 +228,8 @@ struct Segments {
 };
 
 // The R tiles behind the whole waves, over `runners` workers: each in f equal parts (f workers to a
-// tile), or (RUNS) where that would leave many workers idle in W equal runs.  A call that is bound by
-// reading the weights has no use for runs: fewer workers read as fast, and sums of parts cost.
+// tile), or (RUNS) where that would leave many workers idle in W equal runs.  A call that is bound
+// by reading the weights has no use for runs: fewer workers read as fast, and sums of parts cost.
 constexpr int kMaxParts = 8;
 template <bool RUNS>
 __device__ __forceinline__ void schedule(Plan& p, int steps, int W) {
@@ -243,9 +245,11 @@ __device__ __forceinline__ void schedule(Plan& p, int steps, int W) {
 // ---------------------------------------------------------------------------
 // instructions
 
-constexpr uint32_t kDescHi = 64u | (1u << 14) | (2u << 29);  // 8-row groups 1024 bytes apart, 128-byte swizzle
+// Operand descriptors in two words, as in fused_tc.cu: 8-row groups 1024 bytes apart, 128-byte
+// swizzle.  Instruction descriptor: A, B MN-major.
+constexpr uint32_t kDescHi = 64u | (1u << 14) | (2u << 29);
 constexpr uint32_t kDescLo = 1u << 16;
-constexpr uint32_t kTransposeA = 1u << 15, kTransposeB = 1u << 16;  // instruction descriptor: MN-major
+constexpr uint32_t kTransposeA = 1u << 15, kTransposeB = 1u << 16;
 
 // e4m3 operands, fp32 accumulator
 template <bool PAIR>
@@ -267,8 +271,8 @@ __device__ __forceinline__ void mma(uint32_t d, uint32_t alo, uint32_t blo, uint
         : "memory");
 }
 
-// Arrive on the barrier `bar` of this CTA (PAIR: of both, at the same offset) once the MMAs issued so
-// far have completed.
+// Arrive on the barrier `bar` of this CTA (PAIR: of both, at the same offset) once the MMAs issued
+// so far have completed.
 template <bool PAIR>
 __device__ __forceinline__ void commit_both(uint32_t bar) {
   if constexpr (PAIR)
@@ -491,45 +495,43 @@ __global__ void __launch_bounds__(Cfg<BNX>::kThreads, Cfg<BNX>::kPerSm)
       }
     } else if (warp == 1) {
       // ---- MMA issue
-      {
-        qlk::grid_dependency_wait();
-        if ((P.test_us >> 16) && wk == 0) qlk::test_delay(P.test_us >> 16);
-        int s = 0, ph = 0, a = 0, aph = 1, n = 0;
-        bool ok = true;
-        while (ok && sg.next(plan, P.steps, t, k0, k1, slot)) {
-          const Tile T = tile_of<C>(P, plan, t);
-          // (the type fields of e4m3 are zeros, as those of fp16 in kind::f16)
-          const uint32_t idesc = idesc_f16(128, T.bn) | (BWD ? kTransposeA : 0u);
+      qlk::grid_dependency_wait();
+      if ((P.test_us >> 16) && wk == 0) qlk::test_delay(P.test_us >> 16);
+      int s = 0, ph = 0, a = 0, aph = 1, n = 0;
+      bool ok = true;
+      while (ok && sg.next(plan, P.steps, t, k0, k1, slot)) {
+        const Tile T = tile_of<C>(P, plan, t);
+        // (the type fields of e4m3 are zeros, as those of fp16 in kind::f16)
+        const uint32_t idesc = idesc_f16(128, T.bn) | (BWD ? kTransposeA : 0u);
 #pragma unroll 1
-          for (int k = k0; k < k1; ++k, ++n) {
-            if (n >= C::kAcc && !(ok = warp_wait<64>(acce(a), aph, W, kErrAcc, lane))) break;
-            if (!(ok = warp_wait<64>(full(s), ph, W, kErrStage, lane))) break;
-            tc_fence_after();
-            const uint32_t pa = ((ring + s * C::kStageBytes) >> 4) | kDescLo;
-            const uint32_t pb = pa + (C::kABytes >> 4);
-            if (elect_one()) {
+        for (int k = k0; k < k1; ++k, ++n) {
+          if (n >= C::kAcc && !(ok = warp_wait<64>(acce(a), aph, W, kErrAcc, lane))) break;
+          if (!(ok = warp_wait<64>(full(s), ph, W, kErrStage, lane))) break;
+          tc_fence_after();
+          const uint32_t pa = ((ring + s * C::kStageBytes) >> 4) | kDescLo;
+          const uint32_t pb = pa + (C::kABytes >> 4);
+          if (elect_one()) {
 #pragma unroll
-              for (int kk = 0; kk < 4; ++kk)
-                mma<false>(tmem + a * BNX, pa + (BWD ? 256 : 2) * kk, pb + 2 * kk, idesc, kk != 0);
-              tc_commit<false>(empty(s));
-              tc_commit<false>(accf(a));
-            }
-            __syncwarp();
-            if (++s == C::S) {
-              s = 0;
-              ph ^= 1;
-            }
-            if (++a == C::kAcc) {
-              a = 0;
-              aph ^= 1;
-            }
+            for (int kk = 0; kk < 4; ++kk)
+              mma<false>(tmem + a * BNX, pa + (BWD ? 256 : 2) * kk, pb + 2 * kk, idesc, kk != 0);
+            tc_commit<false>(empty(s));
+            tc_commit<false>(accf(a));
+          }
+          __syncwarp();
+          if (++s == C::S) {
+            s = 0;
+            ph ^= 1;
+          }
+          if (++a == C::kAcc) {
+            a = 0;
+            aph ^= 1;
           }
         }
-        if (n > 0) {
-          if (elect_one()) tc_commit<false>(fin);
-          __syncwarp();
-          warp_wait<0>(fin, 0, W, kErrAcc, lane, false);
-        }
+      }
+      if (n > 0) {
+        if (elect_one()) tc_commit<false>(fin);
+        __syncwarp();
+        warp_wait<0>(fin, 0, W, kErrAcc, lane, false);
       }
     } else if (warp == 2) {
       // ---- products of scales: columns lane + 32 i of the tile, four steps in registers while the
@@ -540,8 +542,8 @@ __global__ void __launch_bounds__(Cfg<BNX>::kThreads, Cfg<BNX>::kPerSm)
       bool ok = true;
       while (ok && sg.next(plan, P.steps, t, k0, k1, slot)) {
         const Tile T = tile_of<C>(P, plan, t);
-        const int rb = T.rt;
-        const float* sw = P.sw + (size_t)T.e * P.nb * P.kb + (BWD ? (size_t)rb : (size_t)rb * P.kb);
+        const float* sw =
+            P.sw + (size_t)T.e * P.nb * P.kb + (size_t)T.rt * (BWD ? 1 : P.kb);
         const int hop = BWD ? P.kb : 1;
         const float* sx = P.sx + (size_t)(T.m0 + lane) * P.steps;
         const size_t skip = (size_t)32 * P.steps;
@@ -553,8 +555,7 @@ __global__ void __launch_bounds__(Cfg<BNX>::kThreads, Cfg<BNX>::kPerSm)
             w[j] = in ? __ldg(sw + (size_t)(k + j) * hop) : 0.f;
 #pragma unroll
             for (int i = 0; i < kPer; ++i)
-              v[i][j] = in && lane + 32 * i < T.rows ? __ldcg(sx + i * skip + k + j)
-                                                                    : 0.f;
+              v[i][j] = in && lane + 32 * i < T.rows ? __ldcg(sx + i * skip + k + j) : 0.f;
           }
         };
         load(k0);
@@ -661,8 +662,7 @@ __global__ void __launch_bounds__(Cfg<BNX>::kThreads, Cfg<BNX>::kPerSm)
         const long long ub = (long long)(t - plan.whole) * P.steps;
         const int wf = worker_of(ub, U, plan.runners);
         const int wl = worker_of(ub + P.steps - 1, U, plan.runners);
-        uint32_t* counter =
-            P.counters + (size_t)(t - plan.whole) * C::kEpiWarps + q;
+        uint32_t* counter = P.counters + (size_t)(t - plan.whole) * C::kEpiWarps + q;
         uint32_t prev = 0;
         if (lane == 0) prev = arrive_weight(counter, 1u);
         prev = __shfl_sync(0xffffffffu, prev, 0);
@@ -714,7 +714,8 @@ __global__ void __launch_bounds__(Cfg<BNX>::kThreads, Cfg<BNX>::kPerSm)
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
             const int row = 16 * c + 8 * i + (lane >> 2);
-            const uint4 v = qlk::lds128(staging + (8 * i + (lane >> 2)) * kTokStride + (lane & 3) * 16);
+            const uint4 v =
+                qlk::lds128(staging + (8 * i + (lane >> 2)) * kTokStride + (lane & 3) * 16);
             if (row < T.rows && n < P.R)
               *reinterpret_cast<uint4*>(static_cast<uint16_t*>(P.y) + (size_t)(T.m0 + row) * P.R +
                                         n) = v;
@@ -731,14 +732,30 @@ __global__ void __launch_bounds__(Cfg<BNX>::kThreads, Cfg<BNX>::kPerSm)
   }
 }
 
-// ---------------------------------------------------------------------------
-// Many rows of q: they are the MMA's A operand, 256 per pair of CTAs, and 256 of D's rows its B
-// operand.  A thread's share of the accumulator is then a row of q and 128 of D's rows, one block
-// of the weights: a step has one product of scales per thread.
-
+// --------------------------------------------------------------------------- Many rows of q: they
+// are the MMA's A operand, 128 per CTA, and 256 of D's rows its B operand.  A thread of the
+// epilogue holds a row of q and 128 of D's rows, one block of the weights: a step has one product
+// of scales per thread.  (The other way round a step's scales are as many shared loads as a quarter
+// of its multiply-adds: 585 against 346 cycles.)
 //
-// Up to 128 rows of q (an expert's, on average) single CTAs take 128 x 256 tiles, !PAIR: they read
-// weights at twice the rate.
+// PAIR: a cluster of two CTAs on two SMs computes a tile of 256 rows of q with tcgen05
+// cta_group::2; each copies its 128 rows and one of the two blocks of weights, 64 KB a step for
+// both, which the L2 gives in about 0.40 us.  Single CTAs copy both blocks, 48 KB: weights come at
+// twice the rate, rows of q in tiles of 128.  They take calls of up to 128 rows, which the weights
+// bound (128 x 8192 x 28672 56 against 68 us), and of up to 256 per expert, whose last tiles are
+// half as empty (64 experts of 2048 x 4096 with 16384 rows 218 against 228 us; without experts 200
+// x 8192 x 8192 31.6 against 28.9).
+//
+// A step of a pair takes 0.54 us and more: 512 cycles of MMAs, the copies' 0.40 us, and in the
+// epilogue 128 multiply-adds of two warps to a scheduler, 346 cycles, which overlap but for what
+// the way of an accumulator from the MMAs to the epilogue and back costs, with two of them in
+// tensor memory. Without the multiply-adds 4096 x 28672 x 8192 takes 737 us, without the MMAs 692,
+// with the copies alone 624.  Measured and left: packed multiply-adds (988 us: the pairs' registers
+// spill), two accumulators of 128 columns a step (909), sixteen epilogue warps (887), polls instead
+// of suspended waits (892), one warp to issue the MMAs (885).  Two warps issue them, a step each in
+// turn.
+//
+// Warps: 0 copies, 1 and 3 MMA issue (1 the tensor memory), 2 scales, 4 .. 11 epilogue.
 template <bool PAIR_>
 struct Wide {
   static constexpr bool PAIR = PAIR_;
@@ -754,7 +771,8 @@ struct Wide {
   static constexpr int kStagingOff = S * kStageBytes;
   static constexpr int kStaging = 32 * kTokStride; // per epilogue warp: 32 rows of 32 columns
   static constexpr int kScaleWarps = 1;
-  static constexpr int kScaleOff = kStagingOff + kEpiWarps * kStaging;  // [kAcc][2 blocks][128 rows]
+  // products of scales [kAcc][2 blocks][128 rows]
+  static constexpr int kScaleOff = kStagingOff + kEpiWarps * kStaging;
   static constexpr int kBarOff = kScaleOff + kAcc * 256 * 4;
   // full[S] empty[S] accf[2] acce[2] sempty[2] fin[2]
   static constexpr int kBars = 2 * S + 4 * kAcc;
@@ -873,9 +891,9 @@ __global__ void __launch_bounds__(Wide<PAIR>::kThreads, 1)
         if (PAIR && !ok) qlk::test_delay(kSettleUs);
       }
     } else if (warp & 1) {
-      // ---- MMA issue by the leader: warp 1 the even steps, warp 3 the odd ones, an accumulator each.
-      // What a warp takes to see its barriers complete and to issue is then hidden behind the other
-      // step's MMAs.
+      // ---- MMA issue by the leader: warp 1 the even steps, warp 3 the odd ones, an accumulator
+      // each. What a warp takes to see its barriers complete and to issue is then hidden behind the
+      // other step's MMAs.
       if (leader) {
         qlk::grid_dependency_wait();
         if ((P.test_us >> 16) && wk == 0) qlk::test_delay(P.test_us >> 16);
@@ -919,8 +937,8 @@ __global__ void __launch_bounds__(Wide<PAIR>::kThreads, 1)
         if (PAIR && (!ok || misc[1])) qlk::test_delay(kSettleUs);
       }
     } else {
-      // ---- products of scales: rows 32 i + lane of this CTA's, by both blocks of the weights.  Two
-      // steps at a time, the next two on their way while they are handed out.
+      // ---- products of scales: rows 32 i + lane of this CTA's, by both blocks of the weights.
+      // Two steps at a time, the next two on their way while they are handed out.
       qlk::grid_dependency_wait();
       int a = 0, aph = 1, n = 0;
       bool ok = true;
@@ -1091,7 +1109,8 @@ __global__ void __launch_bounds__(Wide<PAIR>::kThreads, 1)
         __syncwarp();
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          const uint4 x = qlk::lds128(staging + (8 * i + (lane >> 2)) * kTokStride + 16 * (lane & 3));
+          const uint4 x =
+              qlk::lds128(staging + (8 * i + (lane >> 2)) * kTokStride + 16 * (lane & 3));
           if (m + 8 * i < T.m0 + T.rows && n + 32 * c < P.R)
             *reinterpret_cast<uint4*>(static_cast<uint16_t*>(P.y) + (size_t)(m + 8 * i) * P.R + n +
                                       32 * c) = x;
@@ -1222,7 +1241,9 @@ ql_status launch_as(const Product& p) {
   const cuuint64_t qdims[2] = {(cuuint64_t)(BWD ? p.N : p.K), (cuuint64_t)p.M};
   if (!encode(&maps.w, p.w, 3, wdims, 128)) return QL_ERR_CUDA;
   for (int i = 0; i < 4; ++i)  // (narrow tiles: 64, 32 and 16 rows; wide ones: 128, 64 and 32)
-    if ((128 >> i) <= C::kBRows && (i < 3 || C::kBRows < 128) && !encode(&maps.q[i], p.q, 2, qdims, 128 >> i)) return QL_ERR_CUDA;
+    if ((128 >> i) <= C::kBRows && (i < 3 || C::kBRows < 128) &&
+        !encode(&maps.q[i], p.q, 2, qdims, 128 >> i))
+      return QL_ERR_CUDA;
   // every worker that can run: how many have work is known on the device.  A second CTA on each SM
   // where both have kLongRun steps and more
   const long long units = tiles * P.steps;

@@ -814,7 +814,7 @@ class RMSNorm(_FusedWorkspace):
         if M:
             status = _lib.qlinear_rmsnorm(
                 _TYPE_OF[dtype], px, ldx, residual, weight.data_ptr(), self.eps, total, y, pq, ps,
-                rstd, M, K, _current_stream(index) if stream is None else _raw_stream(stream, index))
+                rstd, M, K, _raw_stream(stream, index))
             if status:
                 _check(status, "qlinear_rmsnorm")
         return q, scales
@@ -823,10 +823,10 @@ class RMSNorm(_FusedWorkspace):
                  dtotal: Optional[torch.Tensor] = None, dx: Optional[torch.Tensor] = None,
                  dweight: Optional[torch.Tensor] = None,
                  workspace: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
-        """dx[M, K], the gradient of x and of the residual, from the gradient dy of the norm's values
-        (the quantization has the identity's), the kept total and rstd, and dtotal, the gradient
-        that comes to total from elsewhere (dx may be dtotal itself).  dweight (fp32 [K]), when
-        given, receives the weight's."""
+        """dx[M, K], the gradient of x and of the residual, from the gradient dy of the norm's
+        values (the quantization has the identity's), the kept total and rstd, and dtotal, the
+        gradient that comes to total from elsewhere (dx may be dtotal itself).  dweight (fp32
+        [K]), when given, receives the weight's."""
         weight, (_, _, K, index) = self.weight, self._fused
         if torch.cuda.current_device() != index:
             return self._fused_elsewhere(self.backward, dy, total, rstd, dtotal, dx, dweight,
