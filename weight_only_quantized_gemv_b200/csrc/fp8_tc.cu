@@ -764,6 +764,7 @@ struct Wide {
   static constexpr int kBytes = 128 * 128;         // of 128 rows of an operand, per step
   static constexpr int kOwn = 2 / kCtas;           // of the tile's two blocks of weights, a CTA's
   static constexpr int kStageBytes = (1 + kOwn) * kBytes, S = 200 * 1024 / kStageBytes;
+  static_assert(S % 2 == 0, "a stage's barrier is always the same MMA warp's (a parity wait)");
   static constexpr int kEpiWarps = 8, kEpiWarp0 = 4;
   static constexpr int kThreads = 32 * (kEpiWarp0 + kEpiWarps);
   static constexpr int kAcc = 2;
@@ -1034,9 +1035,12 @@ __global__ void __launch_bounds__(Wide<PAIR>::kThreads, 1)
             tc_fence_before();
             __syncwarp();
             if (lane == 0) {
+              // (the loads have completed, nothing in memory is to be ordered: the other CTA's
+              // arrival says only when, and the default scope is enough, see arrive_stage in
+              // fused_tc.cu)
               if (!PAIR || leader)
                 qlk::mbar_arrive(acce(a));
-              else  // (says only when: see arrive_stage in fused_tc.cu)
+              else
                 asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(lead(acce(a)))
                              : "memory");
               qlk::mbar_arrive(sempty(a));
