@@ -606,8 +606,9 @@ ql_status qlinear_rmsnorm_backward(int type, const void* dy, const void* total, 
 /* For calls with these M and K on the current device; 0 for invalid arguments or no device. */
 size_t qlinear_rmsnorm_workspace_bytes(int M, int K);
 
-/* Bytes of a product's workspace for calls with at most M rows and E experts (1 for the linear
- * entries), in both directions, on the current device; 0 for invalid arguments or no device. */
+/* Bytes of a product's workspace for calls with at most M rows over E experts (exactly E; 1 for the
+ * linear entries), in both directions, on the current device; 0 for invalid arguments or no
+ * device. */
 size_t qlinear_fp8_workspace_bytes(int M, int E, int N, int K);
 
 /* y [M][N] from the codes q [M][K] and scales of x, and w [N][K]. */

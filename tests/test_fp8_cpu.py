@@ -169,6 +169,14 @@ def test_weights_are_checked():
                  (codes[None], scales[None])):
         with pytest.raises(ValueError):
             layers.Fp8Linear(c, s, device="cpu")
+    for shape in ((40, 128), (48, 120), (0, 128), (1025, 16, 16)):  # not multiples of 16, too many
+        with pytest.raises(ValueError):
+            (layers.Fp8Linear if len(shape) == 2 else layers.Fp8Experts)(
+                torch.zeros(shape, dtype=torch.uint8),
+                torch.ones(*shape[:-2], -(-shape[-2] // 128), 1), device="cpu")
+    for rows, columns in ((2 ** 24 + 1, 16), (1, 2 ** 30 + 16), (2 ** 32 + 1, 16)):
+        with pytest.raises(ValueError):
+            layers._check_size(rows, columns)
     with pytest.raises(ValueError):
         layers.Fp8Experts(codes, scales, device="cpu")
     experts = layers.Fp8Experts(codes[None], scales[None], device="cpu")

@@ -631,8 +631,17 @@ _F8, _I32 = torch.float8_e4m3fn, torch.int32
 _TYPE_OF = {torch.float16: 0, torch.bfloat16: 1}  # ql_type
 
 
+_MAX_COLUMNS = 1 << 30
+
+
 def _blocks(columns: int) -> int:
     return (columns + 127) // 128
+
+
+def _check_size(rows: int, columns: int) -> None:
+    """(The library counts in 32 bits and checks what it is given, which larger numbers are not.)"""
+    if rows > _MAX_ROWS or columns > _MAX_COLUMNS:
+        raise ValueError(f"{rows} rows of {columns} columns: up to 2^24 and 2^30 are supported")
 
 
 def _matrix(t: torch.Tensor, name: str) -> tuple:
@@ -642,7 +651,9 @@ def _matrix(t: torch.Tensor, name: str) -> tuple:
     if kind is None or t.dim() != 2 or index < 0:
         raise ValueError(f"{name} must be a float16 or bfloat16 matrix on a CUDA device, not "
                          f"{t.dtype} {tuple(t.shape)} on {t.device}")
-    return kind, index, *t.shape
+    M, C = t.shape
+    _check_size(M, C)
+    return kind, index, M, C
 
 
 def _row_ptr(x: torch.Tensor, index: int, name: str) -> tuple:
@@ -697,8 +708,9 @@ def _on_device(index: int, method, *args):
 
 def fp8_quantize(x: torch.Tensor, q: Optional[torch.Tensor] = None,
                  scales: Optional[torch.Tensor] = None, stream=None) -> tuple:
-    """(q, scales): e4m3 codes [M, K] of x[M, K] (fp16 or bf16; its rows may lie apart) and an fp32
-    scale for every 128 columns, [M, ceil(K / 128)]; x is about q * scale."""
+    """(q, scales): e4m3 codes [M, K] of x[M, K] (fp16 or bf16, K a multiple of 16; its rows may lie
+    apart, by a multiple of 8) and an fp32 scale for every 128 columns, [M, ceil(K / 128)]; x is
+    about q * scale."""
     kind, index, M, K = _matrix(x, "x")
     if torch.cuda.current_device() != index:
         return _on_device(index, fp8_quantize, x, q, scales, stream)
@@ -748,8 +760,9 @@ def fp8_gated_backward(dh: torch.Tensor, gu: torch.Tensor, act: str = "silu",
 
 
 def fp8_quantize_weights(w: torch.Tensor, stream=None) -> tuple:
-    """(codes, scales) of w[N, K] or w[E, N, K] (fp16 or bf16, contiguous): e4m3 codes of the same
-    shape and an fp32 scale per 128 x 128 block, for ``Fp8Linear`` and ``Fp8Experts``."""
+    """(codes, scales) of w[N, K] or w[E, N, K] (fp16 or bf16, contiguous, N and K multiples of
+    16): e4m3 codes of the same shape and an fp32 scale per 128 x 128 block, for ``Fp8Linear`` and
+    ``Fp8Experts``."""
     kind, index = _TYPE_OF.get(w.dtype), w.get_device()
     if kind is None or w.dim() not in (2, 3) or index < 0:
         raise ValueError("w must be a float16 or bfloat16 [N, K] or [E, N, K] on a CUDA device")
@@ -773,6 +786,8 @@ class RMSNorm(_FusedWorkspace):
             raise ValueError("the weight is a contiguous float16 or bfloat16 vector on a CUDA "
                              "device")
         self.weight, self.eps, self.K = weight, eps, weight.shape[0]
+        if self.K % 16 or not 16 <= self.K <= 32768:
+            raise ValueError(f"a norm has a multiple of 16 columns up to 32768, not {self.K}")
         self._fused_lock = threading.RLock()
         self._fused = (None, self.K, self.K, weight.get_device())
 
@@ -799,6 +814,7 @@ class RMSNorm(_FusedWorkspace):
                                          stream)
         dtype, M = weight.dtype, x.shape[0]
         shape = (M, K)
+        _check_size(M, K)
         if x.dtype is not dtype or x.shape != shape or x.get_device() != index:
             _fused_ptr(x, shape, index, "x", dtype)  # says why not
         px, ldx = _row_ptr(x, index, "x")
@@ -832,6 +848,7 @@ class RMSNorm(_FusedWorkspace):
             return self._fused_elsewhere(self.backward, dy, total, rstd, dtotal, dx, dweight,
                                          workspace, stream)
         dtype, M = weight.dtype, dy.shape[0]
+        _check_size(M, K)
         pdy = _fused_ptr(dy, (M, K), index, "dy", dtype)
         if dx is None:
             dx = self._fused_new(dy, (M, K), index, stream)
@@ -869,6 +886,10 @@ class _Fp8Weights(_FusedWorkspace):
                              f"their bytes) and fp32 scales, not {codes.dtype} "
                              f"{tuple(codes.shape)} and {scales.dtype}")
         *lead, N, K = codes.shape
+        if N % 16 or K % 16 or not (16 <= N <= _MAX_COLUMNS and 16 <= K <= _MAX_COLUMNS) or (
+                lead and not 1 <= lead[0] <= 1024):
+            raise ValueError(f"codes {tuple(codes.shape)}: N and K are multiples of 16 up to 2^30, "
+                             "with 1 to 1024 experts")
         if tuple(scales.shape) != (*lead, _blocks(N), _blocks(K)):
             raise ValueError(f"codes {tuple(codes.shape)} have a scale per 128 x 128 block: "
                              f"{(*lead, _blocks(N), _blocks(K))}, not {tuple(scales.shape)}")
@@ -898,6 +919,7 @@ class _Fp8Weights(_FusedWorkspace):
                  workspace, stream):
         index = self._fused[3]
         M = q.shape[0]
+        _check_size(M, C)
         pq = _fused_ptr(q, (M, C), index, "q", _F8)
         if out is not None:
             dtype = out.dtype

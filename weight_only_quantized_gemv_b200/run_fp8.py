@@ -7,9 +7,10 @@ with e4m3 output, and the products, dense or grouped by expert, with their backw
 K: columns of the norm and of the product's input; N: columns of the product's output and 2 F of the
 gated activation.  With --E the product's rows are spread over that many matrices, some with twice
 the average and some with none.  Enough copies of the weights are cycled that no launch finds them
-in L2 (the row kernels' inputs may be there).  Without `--time` the chosen entries run `--launches` times (for profiler captures); with it
-each is timed with CUDA events on the launching stream after warm-up, and one JSON line gives
-microseconds, GB/s (every input read once, every output written once) and for products TFLOP/s.
+in L2 (the row kernels' inputs may be there).  Without `--time` the chosen entries run `--launches`
+times (for profiler captures); with it each is timed with CUDA events on the launching stream after
+warm-up, and one JSON line gives microseconds, GB/s (every input read once, every output written
+once) and for products TFLOP/s.
 """
 from __future__ import annotations
 
