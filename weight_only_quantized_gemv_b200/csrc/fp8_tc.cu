@@ -323,6 +323,16 @@ __device__ __forceinline__ void wait_loads(uint32_t (&a)[8], uint32_t (&b)[8]) {
                : "memory");
 }
 
+// Lane 0 arrives on two barriers, without a branch: a shared::cluster address, one of this CTA's.
+__device__ __forceinline__ void arrive_both(uint32_t cluster_bar, uint32_t bar, int lane) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.eq.s32 p, %2, 0;\n\t"
+      "@p mbarrier.arrive.shared::cluster.b64 _, [%0];\n\t"
+      "@p mbarrier.arrive.shared::cta.b64 _, [%1];\n\t}" ::"r"(cluster_bar),
+      "r"(bar), "r"(lane)
+      : "memory");
+}
+
 using pair_t = unsigned long long;  // two fp32
 __device__ __forceinline__ pair_t lds_pair(uint32_t a) {
   pair_t v;
@@ -1011,6 +1021,7 @@ __global__ void __launch_bounds__(Wide<PAIR>::kThreads, 1)
     const uint32_t staging = ring + C::kStagingOff + ew * C::kStaging;
     const uint32_t tq = tmem + ((uint32_t)(32 * q) << 16) + (uint32_t)(g * 128);
     const uint32_t sq = ring + C::kScaleOff + 4 * (128 * g + 32 * q + lane);
+    const uint32_t free = lead(acce(0));  // the leader's
     int a = 0, aph = 0;
     bool ok = true;
     while (ok && sg.next(plan, P.steps, t, k0, k1, slot)) {
@@ -1034,17 +1045,9 @@ __global__ void __launch_bounds__(Wide<PAIR>::kThreads, 1)
           } else {  // the accumulator is free
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) {
-              // (the loads have completed, nothing in memory is to be ordered: the other CTA's
-              // arrival says only when, and the default scope is enough, see arrive_stage in
-              // fused_tc.cu)
-              if (!PAIR || leader)
-                qlk::mbar_arrive(acce(a));
-              else
-                asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(lead(acce(a)))
-                             : "memory");
-              qlk::mbar_arrive(sempty(a));
-            }
+            // (the loads have completed, nothing in memory is to be ordered: the other CTA's arrival
+            // says only when, and the default scope is enough, see arrive_stage in fused_tc.cu)
+            arrive_both(free + 8 * a, sempty(0) + 8 * a, lane);
           }
 #pragma unroll
           for (int i = 0; i < 32; ++i)
