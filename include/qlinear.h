@@ -566,9 +566,10 @@ ql_status qlinear_pack_params_gated(int fmt, const void* gate, const void* up, v
  *                    flag, zero-fill it again.
  * Asynchronous on `stream`; nothing is allocated.  An output may not overlap an input or another
  * output (QL_ERR_ALIAS), but for the cases named.  Shapes: 1 <= M <= 2^24; N, K and F multiples of
- * 16 up to 2^30 (F 2^29, the norm's K 32768); 1 <= E <= 1024 (QL_ERR_SHAPE).  Weights (codes,
- * scales and the norm's) must not be written by work still running on the stream, unless that is
- * qlinear_fp8_quantize_weights: they are read before earlier kernels end.
+ * 16 up to 2^30 (F 2^29, the norm's K 32768); 1 <= E <= 1024 (QL_ERR_SHAPE).  A product's weights
+ * (codes and scales) must not be written by work still running on the stream,
+ * qlinear_fp8_quantize_weights included: they are read before earlier kernels end.  The norm's
+ * weight is read in the stream's order, like x.
  * ------------------------------------------------------------------------- */
 typedef enum { QL_TYPE_F16 = 0, QL_TYPE_BF16 = 1 } ql_type;
 

@@ -326,3 +326,45 @@ def test_random_shapes(seed):
                 ref.check(out[a:b], want, err, f"E={E} N={N} K={K} M={M} {backward}")
             assert not out[int(at[-1]):].any()
         assert lay.fused_read_error() == 0
+
+
+# ---------------------------------------------------------------------------
+# a norm's weight that the stream's work just before the call writes
+
+
+@pytest.mark.parametrize("writer", ["product", "step"])
+@pytest.mark.parametrize("M,K", [(1, 256), (3, 4096), (700, 1040)])
+def test_norm_weight_in_stream_order(M, K, writer):
+    gen = _gen(M + K)
+    lin = layers.Fp8Linear(*ref.weights(gen, K, 16384))
+    x = torch.randn(M, K, generator=gen, device="cuda").bfloat16()
+    dy = torch.randn(M, K, generator=gen, device="cuda").bfloat16()
+    rstd = torch.rand(M, generator=gen, device="cuda") + 0.5
+    norm = layers.RMSNorm(torch.zeros(K, dtype=torch.bfloat16, device="cuda"))
+    inputs = [_codes(gen, 1, 16384) for _ in range(6)]
+
+    def write(i, w):
+        if writer == "product":  # lets the next grid start before it has written
+            lin.forward(*inputs[i], y=w.view(1, K))
+        else:
+            for _ in range(4):
+                w.add_(i + 1.0)
+
+    def run(wait):
+        norm.weight.zero_()
+        got = []
+        for i in range(len(inputs)):
+            for backward in (False, True):
+                write(i, norm.weight)
+                if wait:
+                    torch.cuda.synchronize()
+                dw = torch.empty(K, device="cuda")
+                got += ([norm.backward(dy, x, rstd, dweight=dw), dw] if backward
+                        else norm.forward(x))
+        torch.cuda.synchronize()
+        return got
+
+    want = run(True)
+    assert not _same(want[1], want[5])  # the weight matters (the codes' scales)
+    for a, b in zip(run(False), want, strict=True):
+        assert _same(a, b)

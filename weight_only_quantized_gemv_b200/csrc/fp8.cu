@@ -71,19 +71,17 @@ __global__ void __launch_bounds__(1024) norm_kernel(const NormParams P) {
   __shared__ float red[32];
   const int row = blockIdx.x, step = 8 * (int)blockDim.x, c0 = 8 * (int)threadIdx.x;
   const size_t base = (size_t)row * P.K;
-  uint4 w[V];
-#pragma unroll
-  for (int i = 0; i < V; ++i)
-    if (c0 + i * step < P.K) w[i] = *reinterpret_cast<const uint4*>(P.weight + c0 + i * step);
   qlk::grid_dependents_launch();
   qlk::grid_dependency_wait();
-  uint4 a[V], r[V];
+  // (the weight too: it is trained, by work that may be the stream's last before this)
+  uint4 a[V], r[V], w[V];
 #pragma unroll
   for (int i = 0; i < V; ++i) {
     const int c = c0 + i * step;
     if (c >= P.K) continue;
     a[i] = load16(P.x + (size_t)row * P.ldx + c);
     if (P.residual) r[i] = load16(P.residual + base + c);
+    w[i] = load16(P.weight + c);
   }
   float sum = 0.f;
 #pragma unroll
@@ -156,11 +154,6 @@ __global__ void __launch_bounds__(1024) norm_grad_kernel(const NormGradParams P)
   uint4* const mine = stages + group * S * stage + tid;
   uint4 w[V];
   float dw[V][8] = {};
-#pragma unroll
-  for (int i = 0; i < V; ++i) {
-    w[i] = make_uint4(0, 0, 0, 0);
-    if (c0 + i * step < P.K) w[i] = *reinterpret_cast<const uint4*>(P.weight + c0 + i * step);
-  }
   qlk::grid_dependents_launch();
   qlk::grid_dependency_wait();
   auto copy = [&](int row, int s) {
@@ -181,6 +174,11 @@ __global__ void __launch_bounds__(1024) norm_grad_kernel(const NormGradParams P)
   int row = (int)blockIdx.x * groups + group;
 #pragma unroll
   for (int s = 0; s < S - 1; ++s) copy(row + s * rows, s);
+#pragma unroll
+  for (int i = 0; i < V; ++i) {
+    w[i] = make_uint4(0, 0, 0, 0);
+    if (c0 + i * step < P.K) w[i] = load16(P.weight + c0 + i * step);
+  }
   for (int s = 0, half = 0; row < P.M; row += rows, half ^= 1) {
     copy(row + (S - 1) * rows, s + S - 1 < S ? s + S - 1 : s - 1);
     const float rstd = __ldcg(P.rstd + row);
@@ -734,7 +732,6 @@ extern "C" ql_status qlinear_fp8_quantize_weights(int type, const void* w, uint8
   const Span ins[1] = {{w, count * 2}};
   if (!disjoint(outs, ins)) return QL_ERR_ALIAS;
   const WeightParams P{static_cast<const uint16_t*>(w), q, scales, N, K};
-  // an ordinary launch: what reads the weights may start early and does not wait for them
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   if (type == QL_TYPE_BF16)
     weight_kernel<true><<<(unsigned)blocks, 256, 0, st>>>(P);

@@ -777,7 +777,8 @@ def fp8_quantize_weights(w: torch.Tensor, stream=None) -> tuple:
 
 class RMSNorm(_FusedWorkspace):
     """RMS norm with the residual's addition and e4m3 output: weight [K] (fp16 or bf16, the type of
-    the stream) on a CUDA device."""
+    the stream) on a CUDA device.  The weight stays the caller's tensor, and a call uses the values
+    that the stream's earlier work leaves in it."""
 
     def __init__(self, weight: torch.Tensor, eps: float = 1e-6):
         weight = weight.detach()
@@ -872,7 +873,9 @@ class RMSNorm(_FusedWorkspace):
 class _Fp8Weights(_FusedWorkspace):
     """e4m3 codes [..., N, K] and scales [..., ceil(N / 128), ceil(K / 128)] on a CUDA device; a
     workspace as in the fused layers, which any of these layers' calls that follow one another may
-    share.  The constructor waits for the current stream: a layer's weights are complete."""
+    share.  The constructor waits for the current stream (so that it cannot be part of a graph): the
+    products read codes and scales before the work ahead of them on the stream has ended.  Whoever
+    writes them later waits for that before the next call."""
 
     def _fp8_setup(self, codes, scales, dims: int, device) -> None:
         codes = torch.as_tensor(codes).detach()
