@@ -27,9 +27,8 @@ __device__ __forceinline__ uint4 load16(const void* p) {
 }
 
 // 16 bytes into shared memory, past L1.
-__device__ __forceinline__ void copy16(uint4* dst, const void* src) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(qlk::smem_addr(dst)), "l"(src)
-               : "memory");
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
 }
 
 // The sum over a group of whole warps, in every one of its threads; `red` has a word per warp and
@@ -65,7 +64,8 @@ struct NormParams {
 };
 
 // A block takes a row; a thread keeps its V vectors in registers between the sum of squares and the
-// output, so that the row is read once.
+// output, so that the row is read once.  Measured, cold, bf16, with residual, total, y and codes:
+// 4096 x 8192 47.4 us for 302 MB (6.4 TB/s, 97 % of a copy's rate).
 template <bool BF16, int V>
 __global__ void __launch_bounds__(1024) norm_kernel(const NormParams P) {
   __shared__ float red[32];
@@ -141,7 +141,10 @@ struct NormGradParams {
 // sums of the columns in registers; the groups' meet at the end, so that a block leaves one set of
 // sums.  A thread copies its own vectors of the S - 1 rows ahead into shared memory (no other
 // thread reads them), since the wait for a row's sum leaves no other way to keep enough loads under
-// way.
+// way.  Measured, cold, bf16, with dtotal and dweight: 4096 x 8192 54.7 us (4.9 TB/s), 2047 x 8192
+// 32.7 us (4.1), 700 x 14336 27.7 us (2.9), the join among them: the passes between a row's
+// arrival and its barrier, which issue in 60 % of the slots.  (Addresses in 64 bits took 57.6 us,
+// 34.2 and 28.8.)
 template <bool BF16, int V, int S>
 __global__ void __launch_bounds__(1024) norm_grad_kernel(const NormGradParams P) {
   extern __shared__ __align__(16) uint4 stages[];  // [group][S][array][V][thread]; then the sums
@@ -150,23 +153,23 @@ __global__ void __launch_bounds__(1024) norm_grad_kernel(const NormGradParams P)
   const int group = (int)threadIdx.x / threads, tid = (int)threadIdx.x - group * threads;
   const int step = 8 * threads, c0 = 8 * tid;
   const int arrays = P.dtotal ? 3 : 2;
-  const int hop = V * threads, stage = arrays * hop;
-  uint4* const mine = stages + group * S * stage + tid;
+  const int hop = V * threads, stage = arrays * hop;  // vectors
+  const uint32_t mine = qlk::smem_addr(stages + group * S * stage + tid);
   uint4 w[V];
   float dw[V][8] = {};
   qlk::grid_dependents_launch();
   qlk::grid_dependency_wait();
   auto copy = [&](int row, int s) {
-    const size_t base = (size_t)row * P.K;
+    if (row < P.M) {
+      const size_t at = (size_t)row * P.K + c0;
+      const uint32_t o = mine + 16 * s * stage;
 #pragma unroll
-    for (int i = 0; i < V; ++i) {
-      const int c = c0 + i * step;
-      if (row < P.M && c < P.K) {
-        uint4* o = mine + s * stage + i * threads;
-        copy16(o, P.total + base + c);
-        copy16(o + hop, P.dy + base + c);
-        if (P.dtotal) copy16(o + 2 * hop, P.dtotal + base + c);
-      }
+      for (int i = 0; i < V; ++i)
+        if (c0 + i * step < P.K) {
+          copy16(o + 16 * i * threads, P.total + at + i * step);
+          copy16(o + 16 * (i * threads + hop), P.dy + at + i * step);
+          if (P.dtotal) copy16(o + 16 * (i * threads + 2 * hop), P.dtotal + at + i * step);
+        }
     }
     asm volatile("cp.async.commit_group;" ::: "memory");
   };
@@ -183,14 +186,14 @@ __global__ void __launch_bounds__(1024) norm_grad_kernel(const NormGradParams P)
     copy(row + (S - 1) * rows, s + S - 1 < S ? s + S - 1 : s - 1);
     const float rstd = __ldcg(P.rstd + row);
     asm volatile("cp.async.wait_group %0;" ::"n"(S - 1) : "memory");
-    const uint4* x = mine + s * stage;
+    const uint32_t x = mine + 16 * s * stage;
     float sum = 0.f;
 #pragma unroll
     for (int i = 0; i < V; ++i) {
       if (c0 + i * step >= P.K) continue;
       float t[8], g[8], v[8];
-      unpack8<BF16>(x[i * threads], t);
-      unpack8<BF16>(x[i * threads + hop], g);
+      unpack8<BF16>(qlk::lds128(x + 16 * i * threads), t);
+      unpack8<BF16>(qlk::lds128(x + 16 * (i * threads + hop)), g);
       unpack8<BF16>(w[i], v);
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
@@ -200,18 +203,19 @@ __global__ void __launch_bounds__(1024) norm_grad_kernel(const NormGradParams P)
       }
     }
     const float mean = group_sum(sum, red[group][half], tid, threads, 1 + group) / (float)P.K;
+    const float back = -rstd * mean;
 #pragma unroll
     for (int i = 0; i < V; ++i) {
       const int c = c0 + i * step;
       if (c >= P.K) continue;
       float t[8], g[8], v[8];
-      unpack8<BF16>(x[i * threads], t);
-      unpack8<BF16>(x[i * threads + hop], g);
+      unpack8<BF16>(qlk::lds128(x + 16 * i * threads), t);
+      unpack8<BF16>(qlk::lds128(x + 16 * (i * threads + hop)), g);
       unpack8<BF16>(w[i], v);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) t[e] = rstd * (g[e] * v[e] - t[e] * rstd * mean);
+      for (int e = 0; e < 8; ++e) t[e] = rstd * fmaf(g[e], v[e], back * t[e]);
       if (P.dtotal) {
-        unpack8<BF16>(x[i * threads + 2 * hop], g);
+        unpack8<BF16>(qlk::lds128(x + 16 * (i * threads + 2 * hop)), g);
 #pragma unroll
         for (int e = 0; e < 8; ++e) t[e] += g[e];
       }
@@ -369,10 +373,11 @@ __device__ __forceinline__ void store_codes(const CodeParams& P, bool in, int ro
   }
 }
 
-// U vectors to a thread: all of their loads are under way before the first is used.  Measured, cold,
-// bf16, 1024 x 14336: plain 10.1 us for 44 MB (4.3 TB/s), gated SiLU 14.6 us for 73 MB (5.0), its
-// gradients 24.9 us for 117 MB (4.7): bound by issue (80 % of the slots), GELU more so (22.9 and
-// 30.8 us).  A thread to one gradient took 38 us, a 64-bit division for a vector's row 5 us more.
+// U vectors to a thread: all of their loads are under way before the first is used.  Measured,
+// cold, bf16, 1024 x 14336: plain 10.1 us for 44 MB (4.3 TB/s), gated SiLU 14.6 us for 73 MB (5.0),
+// its gradients 24.9 us for 117 MB (4.7): bound by issue (80 % of the slots), GELU more so (22.9
+// and 30.8 us).  A thread to one gradient took 38 us, a 64-bit division for a vector's row 5 us
+// more.
 template <int WHAT, bool BF16, int ACT, int U>
 __global__ void __launch_bounds__(kCodeThreads) code_kernel(const CodeParams P) {
   qlk::grid_dependents_launch();
