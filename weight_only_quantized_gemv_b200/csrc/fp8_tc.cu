@@ -27,8 +27,8 @@
 //
 // Measured, us (in brackets the bytes' or the operations' time at the card's rates: a copy's 6.55
 // TB/s, twice cuBLAS' bf16 1.63 PFLOP/s): 1 x 28672 x 8192 39.8 (35.9), 33 rows 44.8 (36.2), 128 x
-// 8192 x 28672 56 (36), 777 x 4096 x 12304 backward 53 (24), 2048 x 8192 x 4096 75 (42), 4096 x
-// 28672 x 8192 879 (589; call after call at the power limit of 1000 W, 1.5 GHz: 1015).
+// 8192 x 28672 56 (36), 777 x 4096 x 12304 backward 53 (24), 2048 x 8192 x 4096 73 (42), 4096 x
+// 28672 x 8192 871 to 892 (589; call after call at the power limit of 1000 W, 1.5 GHz: 1000).
 #include <cuda.h>
 #include <cudaTypedefs.h>
 #include <cuda_runtime.h>
@@ -752,9 +752,11 @@ __global__ void __launch_bounds__(Cfg<BNX>::kThreads, Cfg<BNX>::kPerSm)
 // cta_group::2; each copies its 128 rows and one of the two blocks of weights, 64 KB a step for
 // both, which the L2 gives in about 0.40 us.  Single CTAs copy both blocks, 48 KB: weights come at
 // twice the rate, rows of q in tiles of 128.  They take calls of up to 128 rows, which the weights
-// bound (128 x 8192 x 28672 56 against 68 us), and of up to 256 per expert, whose last tiles are
-// half as empty (64 experts of 2048 x 4096 with 16384 rows 218 against 228 us; without experts 200
-// x 8192 x 8192 31.6 against 28.9).
+// bound (128 x 8192 x 28672 56 against 68 us; 200 x 8192 x 8192 31.6 against 28.9), and of up to
+// 288 per expert, whose last tiles are half as empty.  (Random splits: 64 experts of 2048 x 4096,
+// 256 rows each 221 against 230 us, 312 rows 252 against 249, backward 272 against 266, 512 rows
+// 378 against 371; 8 of 14336 x 4096, backward, 256 rows 194 against 202, 312 rows 222 against
+// 233, 437 rows 280 against 270.)
 //
 // A step of a pair takes 0.54 us and more: 512 cycles of MMAs, the copies' 0.40 us, and in the
 // epilogue 128 multiply-adds of two warps to a scheduler, 346 cycles, which overlap but for what
@@ -1273,7 +1275,7 @@ ql_status launch(const Product& p) {
   if (rows <= 16) return launch_narrow<16, BWD>(p);
   if (rows <= 32) return launch_narrow<32, BWD>(p);
   if (rows <= 64) return launch_narrow<64, BWD>(p);
-  if (rows <= (p.offsets ? 256 : 128))
+  if (rows <= (p.offsets ? 288 : 128))
     return launch_as<Wide<false>, fp8_wide_kernel<false, BWD>, BWD>(p);
   return launch_as<Wide<true>, fp8_wide_kernel<true, BWD>, BWD>(p);
 }
