@@ -142,7 +142,7 @@ struct NormGradParams {
 // sums.  A thread copies its own vectors of the S - 1 rows ahead into shared memory (no other
 // thread reads them), since the wait for a row's sum leaves no other way to keep enough loads under
 // way.  Measured, cold, bf16, with dtotal and dweight: 4096 x 8192 54.7 us (4.9 TB/s), 2047 x 8192
-// 32.7 us (4.1), 700 x 14336 27.7 us (2.9), the join among them: the passes between a row's
+// 32.6 us (4.1), 700 x 14336 25.7 us (3.1), the join among them: the passes between a row's
 // arrival and its barrier, which issue in 60 % of the slots.  (Addresses in 64 bits took 57.6 us,
 // 34.2 and 28.8.)
 template <bool BF16, int V, int S>
@@ -254,25 +254,26 @@ __global__ void __launch_bounds__(1024) norm_grad_kernel(const NormGradParams P)
   }
 }
 
-// dweight[c] = the blocks' sums, added in a fixed order: warp w of a block takes every 32nd, its
-// lanes the columns, and they meet in shared memory.
-constexpr int kJoinWarps = 32;
-__global__ void __launch_bounds__(32 * kJoinWarps) norm_join_kernel(const float* partials,
-                                                                    float* dweight, int blocks,
-                                                                    int K) {
-  __shared__ float red[kJoinWarps][33];
+// dweight[c] = the blocks' sums, added in a fixed order: warp w of a block takes every W-th, its
+// lanes the columns, and they meet in shared memory.  W is 32 while the blocks are one wave of two
+// to an SM, above that 16.  Measured, with the gradients before it, us of 32 and of 16: 2047 x 8192
+// 32.6 and 33.3, 700 x 14336 27.0 and 25.7; without the weight's sums 28.3 and 20.2.
+template <int W>
+__global__ void __launch_bounds__(32 * W) norm_join_kernel(const float* partials, float* dweight,
+                                                           int blocks, int K) {
+  __shared__ float red[W][33];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, c = 32 * blockIdx.x + lane;
   qlk::grid_dependents_launch();
   qlk::grid_dependency_wait();
   float s = 0.f;
   if (c < K)
-#pragma unroll 8
-    for (int b = warp; b < blocks; b += kJoinWarps) s += __ldcg(partials + (size_t)b * K + c);
+#pragma unroll 5
+    for (int b = warp; b < blocks; b += W) s += __ldcg(partials + (size_t)b * K + c);
   red[warp][lane] = s;
   __syncthreads();
   if (warp == 0 && c < K) {
 #pragma unroll
-    for (int w = 1; w < kJoinWarps; ++w) s += red[w][lane];
+    for (int w = 1; w < W; ++w) s += red[w][lane];
     dweight[c] = s;
   }
 }
@@ -830,8 +831,11 @@ extern "C" ql_status qlinear_rmsnorm_backward(int type, const void* dy, const vo
   const ql_status s = type == QL_TYPE_BF16 ? launch_norm_grad<true>(P, blocks, stream)
                                            : launch_norm_grad<false>(P, blocks, stream);
   if (s != QL_OK || !dweight) return s;
-  return launch_early(norm_join_kernel, (unsigned)((K + 31) / 32), 32 * kJoinWarps, stream,
-                      (const float*)P.partials, dweight, blocks, K);
+  const unsigned joins = (unsigned)((K + 31) / 32);
+  const float* sums = P.partials;
+  return joins <= 2u * (unsigned)sms
+             ? launch_early(norm_join_kernel<32>, joins, 32 * 32, stream, sums, dweight, blocks, K)
+             : launch_early(norm_join_kernel<16>, joins, 32 * 16, stream, sums, dweight, blocks, K);
 }
 
 extern "C" size_t qlinear_fp8_workspace_bytes(int M, int E, int N, int K) {
