@@ -368,3 +368,25 @@ def test_norm_weight_in_stream_order(M, K, writer):
     assert not _same(want[1], want[5])  # the weight matters (the codes' scales)
     for a, b in zip(run(False), want, strict=True):
         assert _same(a, b)
+
+
+# ---------------------------------------------------------------------------
+# a norm's weight gradient from a set of sums per multiprocessor, joined by blocks of either size
+
+
+@pytest.mark.parametrize("K", [9472, 9488, 14336])
+@pytest.mark.parametrize("M", [147, 148, 149, 300])
+def test_norm_weight_sums_of_wide_rows(M, K):
+    gen = _gen(M + K)
+    t = ref.activations(gen, M, K, torch.bfloat16)
+    weight = (1 + 0.2 * torch.randn(K, generator=gen, device="cuda")).bfloat16()
+    dy = (0.1 * torch.randn(M, K, generator=gen, device="cuda")).bfloat16()
+    norm = layers.RMSNorm(weight, eps=1e-6)
+    rstd = torch.empty(M, device="cuda")
+    norm.forward(t, rstd=rstd)
+    dweight = torch.full((K,), float("nan"), device="cuda")
+    dx = norm.backward(dy, t, rstd, dweight=dweight)
+    want, err, want_w, err_w = ref.norm_backward(dy, t, rstd, weight, None)
+    ref.check(dx, want, err, "dx")
+    off = (dweight.double() - want_w).abs()
+    assert bool((off <= err_w).all()), (off / err_w).max().item()
