@@ -604,6 +604,14 @@ ql_status qlinear_rmsnorm_backward(int type, const void* dy, const void* total, 
                                    const void* weight, const void* dtotal, void* dx,
                                    float* dweight, int M, int K, void* workspace,
                                    size_t workspace_bytes, ql_stream_t stream);
+/* The same where dy is the output of a grouped product with these offsets (int32 [E + 1], device
+ * memory): rows before offsets[0] and behind offsets[E], each taken into 0 .. M, have no dy.  What
+ * dy, total and rstd hold there is not used; such a row's dx is dtotal, or 0 without one. */
+ql_status qlinear_rmsnorm_backward_grouped(int type, const void* dy, const void* total,
+                                           const float* rstd, const void* weight,
+                                           const void* dtotal, const int* offsets, void* dx,
+                                           float* dweight, int M, int E, int K, void* workspace,
+                                           size_t workspace_bytes, ql_stream_t stream);
 /* For calls with these M and K on the current device; 0 for invalid arguments or no device. */
 size_t qlinear_rmsnorm_workspace_bytes(int M, int K);
 

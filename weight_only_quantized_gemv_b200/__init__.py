@@ -113,6 +113,8 @@ _SIGS = {
     "qlinear_rmsnorm": (_I, [_I, _P, _LL, _P, _P, ctypes.c_float, _P, _P, _P, _P, _P, _I, _I,
                              _P]),
     "qlinear_rmsnorm_backward": (_I, [_I, _P, _P, _P, _P, _P, _P, _P, _I, _I, _P, _SZ, _P]),
+    "qlinear_rmsnorm_backward_grouped": (_I, [_I, _P, _P, _P, _P, _P, _P, _P, _P, _I, _I, _I, _P,
+                                              _SZ, _P]),
     "qlinear_rmsnorm_workspace_bytes": (_SZ, [_I, _I]),
     "qlinear_fp8_workspace_bytes": (_SZ, [_I, _I, _I, _I]),
     "qlinear_fp8_linear": (_I, [_I, _P, _P, _P, _P, _P, _I, _I, _I, _P, _SZ, _P]),
@@ -621,6 +623,18 @@ def qlinear_rmsnorm_backward(type_, dy, total, rstd, weight, dx, M, K, dtotal=No
                                          _ptr(weight), _ptr(dtotal), _ptr(dx), _ptr(dweight), M,
                                          K, *_ws(workspace), _stream(stream)),
            "qlinear_rmsnorm_backward")
+    return dx
+
+
+def qlinear_rmsnorm_backward_grouped(type_, dy, total, rstd, weight, offsets, dx, M, E, K,
+                                     dtotal=None, dweight=None, workspace=None, stream=None):
+    """qlinear_rmsnorm_backward where only the rows offsets[0] .. offsets[E] - 1 have a dy; offsets
+    int32 [E + 1] on the device."""
+    _check(_lib.qlinear_rmsnorm_backward_grouped(_type(type_), _ptr(dy), _ptr(total), _ptr(rstd),
+                                                 _ptr(weight), _ptr(dtotal), _ptr(offsets),
+                                                 _ptr(dx), _ptr(dweight), M, E, K,
+                                                 *_ws(workspace), _stream(stream)),
+           "qlinear_rmsnorm_backward_grouped")
     return dx
 
 

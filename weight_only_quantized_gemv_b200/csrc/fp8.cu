@@ -132,9 +132,10 @@ struct NormGradParams {
   const float* rstd;       // [M]
   const uint16_t* weight;  // [K]
   const uint16_t* dtotal;  // [M][K] or null
+  const int* offsets;      // PART, [E + 1]: rows outside of offsets[0] .. offsets[E] have no dy
   uint16_t* dx;            // [M][K]
   float* partials;         // [blocks][K] or null: sums of dy t rstd over a block's rows
-  int M, K, threads;       // threads of a group
+  int M, E, K, threads;    // threads of a group
 };
 
 // A block is up to eight groups of P.threads threads.  A group takes a row at a time and keeps the
@@ -145,7 +146,10 @@ struct NormGradParams {
 // 32.6 us (4.1), 700 x 14336 25.7 us (3.1), the join among them: the passes between a row's
 // arrival and its barrier, which issue in 60 % of the slots.  (Addresses in 64 bits took 57.6 us,
 // 34.2 and 28.8.)
-template <bool BF16, int V, int S>
+//
+// PART: rows may be without a dy (of no expert: nobody wrote it).  Such a row adds to no sum, and its
+// dx is dtotal, or 0.  (An instance of its own: the tests of rows cost the others 1 to 2 %.)
+template <bool BF16, bool PART, int V, int S>
 __global__ void __launch_bounds__(1024) norm_grad_kernel(const NormGradParams P) {
   extern __shared__ __align__(16) uint4 stages[];  // [group][S][array][V][thread]; then the sums
   __shared__ float red[8][2][32];
@@ -159,15 +163,24 @@ __global__ void __launch_bounds__(1024) norm_grad_kernel(const NormGradParams P)
   float dw[V][8] = {};
   qlk::grid_dependents_launch();
   qlk::grid_dependency_wait();
+  int lo = 0, hi = P.M;
+  if constexpr (PART) {
+    lo = max(__ldcg(P.offsets), 0);
+    hi = min(__ldcg(P.offsets + P.E), P.M);
+  }
+  auto has_dy = [&](int row) { return !PART || (row >= lo && row < hi); };
   auto copy = [&](int row, int s) {
     if (row < P.M) {
+      const bool own = has_dy(row);
       const size_t at = (size_t)row * P.K + c0;
       const uint32_t o = mine + 16 * s * stage;
 #pragma unroll
       for (int i = 0; i < V; ++i)
         if (c0 + i * step < P.K) {
-          copy16(o + 16 * i * threads, P.total + at + i * step);
-          copy16(o + 16 * (i * threads + hop), P.dy + at + i * step);
+          if (own) {
+            copy16(o + 16 * i * threads, P.total + at + i * step);
+            copy16(o + 16 * (i * threads + hop), P.dy + at + i * step);
+          }
           if (P.dtotal) copy16(o + 16 * (i * threads + 2 * hop), P.dtotal + at + i * step);
         }
     }
@@ -187,6 +200,18 @@ __global__ void __launch_bounds__(1024) norm_grad_kernel(const NormGradParams P)
     const float rstd = __ldcg(P.rstd + row);
     asm volatile("cp.async.wait_group %0;" ::"n"(S - 1) : "memory");
     const uint32_t x = mine + 16 * s * stage;
+    if (!has_dy(row)) {  // for the whole group, which uses neither its barrier nor this half
+#pragma unroll
+      for (int i = 0; i < V; ++i)
+        if (c0 + i * step < P.K) {
+          uint4 t = make_uint4(0, 0, 0, 0);
+          if (P.dtotal) t = qlk::lds128(x + 16 * (i * threads + 2 * hop));
+          *reinterpret_cast<uint4*>(P.dx + (size_t)row * P.K + c0 + i * step) = t;
+        }
+      s = s + 1 < S ? s + 1 : 0;
+      half ^= 1;
+      continue;
+    }
     float sum = 0.f;
 #pragma unroll
     for (int i = 0; i < V; ++i) {
@@ -546,10 +571,10 @@ ql_status launch_norm(const NormParams& P, ql_stream_t st) {
 constexpr int kGradSmem = 200 * 1024;
 int norm_grad_vectors(int K) { return K <= 2048 ? 1 : K <= 16384 ? 2 : 4; }
 int norm_grad_blocks(int M, int sms) { return M < sms ? M : sms; }
-template <bool BF16, int V, int S>
+template <bool BF16, bool PART, int V, int S>
 ql_status launch_norm_grad_as(const NormGradParams& P, int blocks, int groups, size_t bytes,
                               ql_stream_t st) {
-  auto kernel = norm_grad_kernel<BF16, V, S>;
+  auto kernel = norm_grad_kernel<BF16, PART, V, S>;
   // (set with each launch: it is the current device's)
   if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kGradSmem) !=
       cudaSuccess)
@@ -557,7 +582,7 @@ ql_status launch_norm_grad_as(const NormGradParams& P, int blocks, int groups, s
   // (the groups' sums, two thirds of a stage's two arrays and more, use the same memory)
   return launch_early_smem(kernel, blocks, groups * P.threads, groups * S * bytes, st, P);
 }
-template <bool BF16, int V>
+template <bool BF16, bool PART, int V>
 ql_status launch_norm_grad_v(NormGradParams P, int blocks, ql_stream_t st) {
   P.threads = norm_threads(P.K, V);
   const size_t bytes = (size_t)(P.dtotal ? 3 : 2) * V * P.threads * 16;  // of a row
@@ -565,16 +590,21 @@ ql_status launch_norm_grad_v(NormGradParams P, int blocks, ql_stream_t st) {
   // the next row, at least, is on its way
   while (groups > 1 && 2 * bytes * groups > kGradSmem) --groups;
   const size_t room = kGradSmem / groups;
-  if (4 * bytes <= room) return launch_norm_grad_as<BF16, V, 4>(P, blocks, groups, bytes, st);
-  if (2 * bytes <= room) return launch_norm_grad_as<BF16, V, 2>(P, blocks, groups, bytes, st);
-  return launch_norm_grad_as<BF16, V, 1>(P, blocks, groups, bytes, st);
+  if (4 * bytes <= room) return launch_norm_grad_as<BF16, PART, V, 4>(P, blocks, groups, bytes, st);
+  if (2 * bytes <= room) return launch_norm_grad_as<BF16, PART, V, 2>(P, blocks, groups, bytes, st);
+  return launch_norm_grad_as<BF16, PART, V, 1>(P, blocks, groups, bytes, st);
+}
+template <bool BF16, bool PART>
+ql_status launch_norm_grad_rows(const NormGradParams& P, int blocks, ql_stream_t st) {
+  const int V = norm_grad_vectors(P.K);
+  if (V == 1) return launch_norm_grad_v<BF16, PART, 1>(P, blocks, st);
+  if (V == 2) return launch_norm_grad_v<BF16, PART, 2>(P, blocks, st);
+  return launch_norm_grad_v<BF16, PART, 4>(P, blocks, st);
 }
 template <bool BF16>
 ql_status launch_norm_grad(const NormGradParams& P, int blocks, ql_stream_t st) {
-  const int V = norm_grad_vectors(P.K);
-  if (V == 1) return launch_norm_grad_v<BF16, 1>(P, blocks, st);
-  if (V == 2) return launch_norm_grad_v<BF16, 2>(P, blocks, st);
-  return launch_norm_grad_v<BF16, 4>(P, blocks, st);
+  return P.offsets ? launch_norm_grad_rows<BF16, true>(P, blocks, st)
+                   : launch_norm_grad_rows<BF16, false>(P, blocks, st);
 }
 
 template <int WHAT, bool BF16, int ACT>
@@ -656,6 +686,54 @@ ql_status product(int type, const uint8_t* q, const float* scales, const int* of
   p.partial_bytes = workspace_bytes - kPartials;
   p.stream = reinterpret_cast<cudaStream_t>(stream);
   return launch_product(p);
+}
+
+// The checks and the launches of the norm's backward pass; offsets: null, or [E + 1].
+ql_status norm_backward(int type, const void* dy, const void* total, const float* rstd,
+                        const void* weight, const void* dtotal, const int* offsets, void* dx,
+                        float* dweight, int M, int E, int K, void* workspace,
+                        size_t workspace_bytes, ql_stream_t stream) {
+  if (!type_ok(type)) return QL_ERR_UNSUPPORTED;
+  if (!dy || !total || !rstd || !weight || !dx) return QL_ERR_NULL;
+  if (M < 1 || M > kMaxRows || !cols_ok(K) || K > kMaxNorm) return QL_ERR_SHAPE;
+  if (!aligned(dy, 16) || !aligned(total, 16) || !aligned(rstd, 4) || !aligned(weight, 16) ||
+      !aligned(dtotal, 16) || !aligned(offsets, 4) || !aligned(dx, 16) || !aligned(dweight, 4))
+    return QL_ERR_ALIGN;
+  const int sms = sm_count();
+  if (sms <= 0) return QL_ERR_CUDA;
+  const int blocks = norm_grad_blocks(M, sms);
+  if (dweight) {
+    if (!workspace || workspace_bytes < kPartials + (size_t)blocks * K * 4)
+      return QL_ERR_WORKSPACE;
+    if (!aligned(workspace, 256)) return QL_ERR_ALIGN;
+  }
+  const size_t mk = (size_t)M * K * 2;
+  const Span outs[3] = {{dx, mk}, {dweight, (size_t)K * 4},
+                        {dweight ? workspace : nullptr, workspace_bytes}};
+  const Span ins[6] = {{dy, mk}, {total, mk}, {rstd, (size_t)M * 4}, {weight, (size_t)K * 2},
+                       {dtotal == dx ? nullptr : dtotal, mk}, {offsets, (size_t)(E + 1) * 4}};
+  if (!disjoint(outs, ins)) return QL_ERR_ALIAS;
+  NormGradParams P{};
+  P.dy = static_cast<const uint16_t*>(dy);
+  P.total = static_cast<const uint16_t*>(total);
+  P.rstd = rstd;
+  P.weight = static_cast<const uint16_t*>(weight);
+  P.dtotal = static_cast<const uint16_t*>(dtotal);
+  P.offsets = offsets;
+  P.dx = static_cast<uint16_t*>(dx);
+  P.partials = dweight ? reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + kPartials)
+                       : nullptr;
+  P.M = M;
+  P.E = E;
+  P.K = K;
+  const ql_status s = type == QL_TYPE_BF16 ? launch_norm_grad<true>(P, blocks, stream)
+                                           : launch_norm_grad<false>(P, blocks, stream);
+  if (s != QL_OK || !dweight) return s;
+  const unsigned joins = (unsigned)((K + 31) / 32);
+  const float* sums = P.partials;
+  return joins <= 2u * (unsigned)sms
+             ? launch_early(norm_join_kernel<32>, joins, 32 * 32, stream, sums, dweight, blocks, K)
+             : launch_early(norm_join_kernel<16>, joins, 32 * 16, stream, sums, dweight, blocks, K);
 }
 
 }  // namespace
@@ -797,45 +875,18 @@ extern "C" ql_status qlinear_rmsnorm_backward(int type, const void* dy, const vo
                                               const void* dtotal, void* dx, float* dweight, int M,
                                               int K, void* workspace, size_t workspace_bytes,
                                               ql_stream_t stream) {
+  return norm_backward(type, dy, total, rstd, weight, dtotal, nullptr, dx, dweight, M, 0, K,
+                       workspace, workspace_bytes, stream);
+}
+extern "C" ql_status qlinear_rmsnorm_backward_grouped(
+    int type, const void* dy, const void* total, const float* rstd, const void* weight,
+    const void* dtotal, const int* offsets, void* dx, float* dweight, int M, int E, int K,
+    void* workspace, size_t workspace_bytes, ql_stream_t stream) {
   if (!type_ok(type)) return QL_ERR_UNSUPPORTED;
-  if (!dy || !total || !rstd || !weight || !dx) return QL_ERR_NULL;
-  if (M < 1 || M > kMaxRows || !cols_ok(K) || K > kMaxNorm) return QL_ERR_SHAPE;
-  if (!aligned(dy, 16) || !aligned(total, 16) || !aligned(rstd, 4) || !aligned(weight, 16) ||
-      !aligned(dtotal, 16) || !aligned(dx, 16) || !aligned(dweight, 4))
-    return QL_ERR_ALIGN;
-  const int sms = sm_count();
-  if (sms <= 0) return QL_ERR_CUDA;
-  const int blocks = norm_grad_blocks(M, sms);
-  if (dweight) {
-    if (!workspace || workspace_bytes < kPartials + (size_t)blocks * K * 4)
-      return QL_ERR_WORKSPACE;
-    if (!aligned(workspace, 256)) return QL_ERR_ALIGN;
-  }
-  const size_t mk = (size_t)M * K * 2;
-  const Span outs[3] = {{dx, mk}, {dweight, (size_t)K * 4},
-                        {dweight ? workspace : nullptr, workspace_bytes}};
-  const Span ins[5] = {{dy, mk}, {total, mk}, {rstd, (size_t)M * 4}, {weight, (size_t)K * 2},
-                       {dtotal == dx ? nullptr : dtotal, mk}};
-  if (!disjoint(outs, ins)) return QL_ERR_ALIAS;
-  NormGradParams P{};
-  P.dy = static_cast<const uint16_t*>(dy);
-  P.total = static_cast<const uint16_t*>(total);
-  P.rstd = rstd;
-  P.weight = static_cast<const uint16_t*>(weight);
-  P.dtotal = static_cast<const uint16_t*>(dtotal);
-  P.dx = static_cast<uint16_t*>(dx);
-  P.partials = dweight ? reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + kPartials)
-                       : nullptr;
-  P.M = M;
-  P.K = K;
-  const ql_status s = type == QL_TYPE_BF16 ? launch_norm_grad<true>(P, blocks, stream)
-                                           : launch_norm_grad<false>(P, blocks, stream);
-  if (s != QL_OK || !dweight) return s;
-  const unsigned joins = (unsigned)((K + 31) / 32);
-  const float* sums = P.partials;
-  return joins <= 2u * (unsigned)sms
-             ? launch_early(norm_join_kernel<32>, joins, 32 * 32, stream, sums, dweight, blocks, K)
-             : launch_early(norm_join_kernel<16>, joins, 32 * 16, stream, sums, dweight, blocks, K);
+  if (!offsets) return QL_ERR_NULL;
+  if (E < 1 || E > kMaxExperts) return QL_ERR_SHAPE;
+  return norm_backward(type, dy, total, rstd, weight, dtotal, offsets, dx, dweight, M, E, K,
+                       workspace, workspace_bytes, stream);
 }
 
 extern "C" size_t qlinear_fp8_workspace_bytes(int M, int E, int N, int K) {

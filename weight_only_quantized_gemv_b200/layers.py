@@ -632,6 +632,7 @@ _TYPE_OF = {torch.float16: 0, torch.bfloat16: 1}  # ql_type
 
 
 _MAX_COLUMNS = 1 << 30
+_MAX_EXPERTS = 1024
 
 
 def _blocks(columns: int) -> int:
@@ -839,15 +840,18 @@ class RMSNorm(_FusedWorkspace):
     def backward(self, dy: torch.Tensor, total: torch.Tensor, rstd: torch.Tensor,
                  dtotal: Optional[torch.Tensor] = None, dx: Optional[torch.Tensor] = None,
                  dweight: Optional[torch.Tensor] = None,
-                 workspace: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+                 workspace: Optional[torch.Tensor] = None, stream=None,
+                 offsets: Optional[torch.Tensor] = None) -> torch.Tensor:
         """dx[M, K], the gradient of x and of the residual, from the gradient dy of the norm's
         values (the quantization has the identity's), the kept total and rstd, and dtotal, the
         gradient that comes to total from elsewhere (dx may be dtotal itself).  dweight (fp32
-        [K]), when given, receives the weight's."""
+        [K]), when given, receives the weight's.  offsets: those of the ``Fp8Experts`` call that dy
+        comes from, where they leave rows out.  These have no dy: they add nothing to dweight, and
+        their dx is dtotal, or 0 without one."""
         weight, (_, _, K, index) = self.weight, self._fused
         if torch.cuda.current_device() != index:
             return self._fused_elsewhere(self.backward, dy, total, rstd, dtotal, dx, dweight,
-                                         workspace, stream)
+                                         workspace, stream, offsets)
         dtype, M = weight.dtype, dy.shape[0]
         _check_size(M, K)
         pdy = _fused_ptr(dy, (M, K), index, "dy", dtype)
@@ -856,14 +860,22 @@ class RMSNorm(_FusedWorkspace):
         pdw = _fused_ptr(dweight, (K,), index, "dweight", _F32)
         head = (_TYPE_OF[dtype], pdy, _fused_ptr(total, (M, K), index, "total", dtype),
                 _fused_ptr(rstd, (M,), index, "rstd", _F32), weight.data_ptr(),
-                _fused_ptr(dtotal, (M, K), index, "dtotal", dtype),
-                _fused_ptr(dx, (M, K), index, "dx", dtype), pdw, M, K)
+                _fused_ptr(dtotal, (M, K), index, "dtotal", dtype))
+        pdx = _fused_ptr(dx, (M, K), index, "dx", dtype)
+        if offsets is None:
+            entry, name = _lib.qlinear_rmsnorm_backward, "qlinear_rmsnorm_backward"
+            head = (*head, pdx, pdw, M, K)
+        else:
+            E = offsets.numel() - 1
+            if not 1 <= E <= _MAX_EXPERTS:
+                raise ValueError(f"offsets are those of 1 to {_MAX_EXPERTS} experts, not {E}")
+            entry = _lib.qlinear_rmsnorm_backward_grouped
+            name = "qlinear_rmsnorm_backward_grouped"
+            head = (*head, _fused_ptr(offsets, (E + 1,), index, "offsets", _I32), pdx, pdw, M, E, K)
         if M and dweight is None:
-            _check(_lib.qlinear_rmsnorm_backward(*head, None, 0, _raw_stream(stream, index)),
-                   "qlinear_rmsnorm_backward")
+            _check(entry(*head, None, 0, _raw_stream(stream, index)), name)
         elif M:
-            self._fused_call(_lib.qlinear_rmsnorm_backward, "qlinear_rmsnorm_backward", head, M,
-                             True, workspace, stream)
+            self._fused_call(entry, name, head, M, True, workspace, stream)
         elif dweight is not None:
             with torch.cuda.stream(_as_stream(stream, index)):
                 dweight.zero_()
@@ -890,7 +902,7 @@ class _Fp8Weights(_FusedWorkspace):
                              f"{tuple(codes.shape)} and {scales.dtype}")
         *lead, N, K = codes.shape
         if N % 16 or K % 16 or not (16 <= N <= _MAX_COLUMNS and 16 <= K <= _MAX_COLUMNS) or (
-                lead and not 1 <= lead[0] <= 1024):
+                lead and not 1 <= lead[0] <= _MAX_EXPERTS):
             raise ValueError(f"codes {tuple(codes.shape)}: N and K are multiples of 16 up to 2^30, "
                              "with 1 to 1024 experts")
         if tuple(scales.shape) != (*lead, _blocks(N), _blocks(K)):
@@ -1017,7 +1029,12 @@ class Fp8GatedMLP:
     (g, u) = v Wgu^T, where v is the RMS norm of x + residual (with a norm) or x itself.  gate_up
     holds the gate's rows before the up projection's.  Both may be ``Fp8Linear``, or both
     ``Fp8Experts``, whose calls take offsets and rows in the order of the experts.  backward goes
-    through the frozen weights from what forward was given to keep."""
+    through the frozen weights from what forward was given to keep.
+
+    Rows of no expert (before the first and behind the last offset): forward writes total and rstd
+    for them, but neither gu nor y.  What those and dy hold there goes into nothing.  In backward
+    they add nothing to dweight; their dx is dtotal, or 0 without one, and without a norm it is not
+    written."""
 
     def __init__(self, gate_up, down, norm: Optional[RMSNorm] = None, act: str = "silu"):
         if type(gate_up) is not type(down) or gate_up.E != down.E:
@@ -1084,4 +1101,4 @@ class Fp8GatedMLP:
         dv = self.gate_up.backward(q, scales, *rows, dtype=dy.dtype, workspace=workspace,
                                    stream=stream)
         return self.norm.backward(dv, total, rstd, dtotal=dtotal, dx=dx, dweight=dweight,
-                                  workspace=workspace, stream=stream)
+                                  workspace=workspace, stream=stream, offsets=offsets)
