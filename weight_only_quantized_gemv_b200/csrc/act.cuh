@@ -88,11 +88,14 @@ __device__ __forceinline__ void act_both(int act, float z, float& f, float& df) 
       df = fmaf(z * kInvSqrt2Pi, e, cdf);
       return;
     }
-    case QL_ACT_GELU_TANH:
+    case QL_ACT_GELU_TANH: {
       sigmoid_both<FAST>(2.f * kSqrt2OverPi * (z + kGeluCubic * z * z * z), s, c);
       f = z * s;
-      df = fmaf(f * c, 2.f * kSqrt2OverPi * (1.f + 3.f * kGeluCubic * z * z), s);
+      // (f c is 0 long before 10^4; the square of a bf16 z would overflow and make that a NaN)
+      const float a = fminf(fabsf(z), 1e4f);
+      df = fmaf(f * c, 2.f * kSqrt2OverPi * (1.f + 3.f * kGeluCubic * a * a), s);
       return;
+    }
     case QL_ACT_SILU:
       sigmoid_both<FAST>(z, s, c);
       f = z * s;
