@@ -466,9 +466,10 @@ ql_status qlinear_matmul(int fmt, const uint16_t* x, const void* packed, const v
  *   act            : a ql_act
  *   workspace      : qlinear_fused_workspace_bytes(), 256-byte aligned, zero-filled once
  *                    before its first use; calls that share it must not overlap in time, but
- *                    may be of different entries, formats and shapes (up to N = 524288
- *                    columns; gated: N = 2 F).  qlinear_read_error reads its error word; after
- *                    a flag, zero-fill it again (a call that gave up leaves its counters).
+ *                    may be of different entries, formats and shapes (beyond N = 524288,
+ *                    gated 2 F, a call clears the counters that others do not keep: a memset).
+ *                    qlinear_read_error reads its error word; after a flag, zero-fill it again
+ *                    (a call that gave up leaves its counters).
  *   fp16 tensors   : 16-byte aligned; fp32 dbias 16-byte aligned
  * Asynchronous on `stream`; nothing is allocated.  An output may not overlap an input or
  * another output (QL_ERR_ALIAS), except that y may be exactly the residual.

@@ -429,6 +429,16 @@ size_t backward_partial_bytes(int M, int N) {
   return qfused::align_up(a > b ? a : b, 256);
 }
 
+// The counters of more columns than the fixed region covers lie where calls with fewer columns, which
+// may share the workspace, have their partial sums: such a call clears them first.
+ql_status clear_further_counters(uint8_t* ws, int N, cudaStream_t st) {
+  const size_t fixed = qfused::kVecCounterOffset + qfused::kVecCounterBytes;
+  const size_t off = qfused::partial_offset(N);
+  if (off > fixed && cudaMemsetAsync(ws + fixed, 0, off - fixed, st) != cudaSuccess)
+    return QL_ERR_CUDA;
+  return QL_OK;
+}
+
 // Runs a forward product: the GEMV up to 16 rows if it has a plan, else the tensor-core product.
 ql_status forward(qfused::Product& p, void* workspace, size_t workspace_bytes) {
   const size_t off = qfused::partial_offset(p.N);
@@ -440,6 +450,7 @@ ql_status forward(qfused::Product& p, void* workspace, size_t workspace_bytes) {
   p.partials = reinterpret_cast<float*>(ws + off);
   if (p.M <= kGemvRows) {
     p.counters = reinterpret_cast<uint32_t*>(ws + qfused::kVecCounterOffset);
+    if (const ql_status s = clear_further_counters(ws, p.N, p.stream)) return s;
     const ql_status s = qfused::launch_gemv(p);
     if (s != QL_ERR_SHAPE) return s;
   }
@@ -497,6 +508,8 @@ ql_status backward(qfused::Product& p, const __half* dy, const __half* z, int W,
   p.partial_bytes = part;
   p.x = dz_is_dy ? dy : dz;
   p.epi.unscale = dz_is_dy ? nullptr : unscale;
+  if (dbias)
+    if (const ql_status s = clear_further_counters(ws, p.N, p.stream)) return s;
   if (!dz_is_dy || dbias) {
     GradParams g;
     g.d = DzParams{dy, dz_is_dy ? nullptr : z, dz_is_dy ? nullptr : dz, unscale, W, p.epi.act};

@@ -44,7 +44,7 @@ struct Product {
 
 // Workspace: one layout for every entry and shape, so that calls of different layers may share
 // one (the counters of any call sit where every other call's counters sit, never under its
-// partial sums).
+// partial sums; those behind the fixed region, beyond N = 524288, are cleared by their call).
 constexpr size_t kErrBytes = 256;
 constexpr size_t kTcCounterBytes = 16384 - kErrBytes;     // tensor-core products
 constexpr size_t kVecCounterOffset = 16384;               // GEMV, column sums
