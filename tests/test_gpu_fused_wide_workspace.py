@@ -48,6 +48,15 @@ def test_gemv_of_a_wide_layer_in_turn_with_others():
                 norm.backward(t, t, rstd, dweight=dw, workspace=ws)
             y = torch.full_like(want, float("nan"))
             assert torch.equal(wide.linear(x, y=y, workspace=ws), want), (M, other)
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            f8.forward(q, s, workspace=ws)
+            wide.linear(x, y=y, workspace=ws)
+        for _ in range(2):
+            y.fill_(float("nan"))
+            graph.replay()
+            assert torch.equal(y, want), M
+        del graph
     assert ql.qlinear_read_error(ws) == 0
 
 
