@@ -1,5 +1,5 @@
 """More of the 8-bit floating-point layers without a GPU: refusals of the norm's backward pass where
-rows have no expert."""
+rows have no expert, and of tensors that forward-mode differentiation follows."""
 import pytest
 
 import weight_only_quantized_gemv_b200 as ql
@@ -39,3 +39,39 @@ def test_offsets_of_the_norm_are_counted():
     with pytest.raises(ValueError):
         layers.Fp8Experts(torch.zeros(1025, 16, 16, dtype=torch.uint8), torch.ones(1025, 1, 1),
                           device="cpu")
+
+
+def test_tangents_are_refused():
+    torch = pytest.importorskip("torch")
+    from torch.autograd import forward_ad
+    from weight_only_quantized_gemv_b200 import layers
+    plain, seen = torch.randn(4, 32).half(), []
+
+    def checks(t):
+        return (lambda: layers._fused_ptr(t, (4, 32), -1, "x", torch.float16),
+                lambda: layers._row_ptr(t, -1, "x"))
+
+    class Inside(torch.autograd.Function):
+        @staticmethod
+        def forward(ctx, a):
+            seen.extend(f() for f in checks(a))
+            return a.clone()
+
+        @staticmethod
+        def jvp(ctx, g):
+            return g
+
+    with forward_ad.dual_level():
+        dual = forward_ad.make_dual(plain, torch.ones_like(plain))
+        for t in (dual, dual.clone(), dual.view(4, 32)):
+            for f in checks(t):
+                with pytest.raises(ValueError, match="tangent"):
+                    f()
+        with pytest.raises(ValueError, match="tangent"):
+            layers._row_ptr(dual[:, :16], -1, "x")
+        for f in checks(plain):
+            f()
+        Inside.apply(dual)
+    assert seen == [plain.data_ptr(), (plain.data_ptr(), 32)]
+    for f in checks(plain):
+        f()

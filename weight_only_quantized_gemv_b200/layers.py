@@ -8,10 +8,12 @@ class only moves and marshals data; every operation runs in ``libqlinear.so``.
 from __future__ import annotations
 
 import threading
+from types import SimpleNamespace
 from typing import Optional
 
 import numpy as np
 import torch
+from torch.autograd import forward_ad
 
 from . import (QL_ERR_WORKSPACE, QL_FMT_CB, QL_FMT_LUT4, QL_FMT_W2, QL_FMT_W3, QL_FMT_W4, QL_FMT_W8,
                qlinear_codebook, qlinear_codebook_tc, qlinear_codebook_workspace_bytes,
@@ -50,6 +52,8 @@ _MAX_ROWS = 1 << 24  # of a fused call
 # (the handle alone, without a Stream object around it, where torch offers that)
 _current_stream = getattr(torch._C, "_cuda_getCurrentRawStream",
                           lambda index: torch.cuda.current_stream(index).cuda_stream)
+# (outside of a dual level no tensor has a tangent, and asking takes as long as its other checks)
+_levels = forward_ad if hasattr(forward_ad, "_current_level") else SimpleNamespace(_current_level=0)
 
 
 def _as_stream(stream, index: int) -> torch.cuda.Stream:
@@ -63,6 +67,11 @@ def _as_stream(stream, index: int) -> torch.cuda.Stream:
             else torch.cuda.default_stream(device))
 
 
+def _dual(t: torch.Tensor) -> bool:
+    """Whether forward-mode differentiation follows `t` (not inside an autograd.Function)."""
+    return forward_ad.unpack_dual(t).tangent is not None
+
+
 def _fused_ptr(t, shape: tuple, index: int, name: str, dtype=_F16) -> Optional[int]:
     """The data pointer of `t` once checked (None for None): `shape`, `dtype`, contiguous, on
     CUDA device `index`, and nothing that autograd would have to follow."""
@@ -72,6 +81,9 @@ def _fused_ptr(t, shape: tuple, index: int, name: str, dtype=_F16) -> Optional[i
         raise ValueError(f"{name} requires a gradient, which autograd does not carry through the "
                          "fused layers: call them under torch.no_grad() (as inside an "
                          "autograd.Function) and their backward methods for the gradient")
+    if _levels._current_level >= 0 and _dual(t):
+        raise ValueError(f"{name} has a tangent, which forward-mode differentiation does not carry "
+                         "through the fused layers: call them inside an autograd.Function")
     if (t.dtype is not dtype or t.shape != shape or not t.is_contiguous()
             or t.get_device() != index):
         raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {shape} on "
@@ -661,10 +673,12 @@ def _row_ptr(x: torch.Tensor, index: int, name: str) -> tuple:
     """(data pointer, elements between rows) of a matrix whose rows are contiguous, once checked
     like ``_fused_ptr``'s."""
     M, K = x.shape
-    if x.is_contiguous() and not x.requires_grad:
+    dual = _levels._current_level >= 0 and _dual(x)
+    if x.is_contiguous() and not x.requires_grad and not dual:
         return x.data_ptr(), K
     ld = x.stride(0) if M > 1 else K
-    if x.requires_grad and torch.is_grad_enabled() or x.stride(1) != 1 and K > 1 or ld < K:
+    if (dual or x.requires_grad and torch.is_grad_enabled() or x.stride(1) != 1 and K > 1
+            or ld < K):
         _fused_ptr(x, (M, K), index, name, x.dtype)  # says why not
     return x.data_ptr(), ld
 
