@@ -1,5 +1,6 @@
 """More of the 8-bit floating-point layers without a GPU: refusals of the norm's backward pass where
-rows have no expert, and of tensors that forward-mode differentiation follows."""
+rows have no expert, of tensors that forward-mode differentiation follows, and of sizes whose products
+pass 64 bits."""
 import pytest
 
 import weight_only_quantized_gemv_b200 as ql
@@ -30,6 +31,18 @@ def test_norm_backward_by_expert_refusals():
         assert _norm_bwd(**{a: 20 * P + 8}) == ALIGN
     for a in ("rstd", "off", "dw"):
         assert _norm_bwd(**{a: 20 * P + 2}) == ALIGN
+
+
+@pytest.mark.parametrize("E", [0, 1, 1024])
+@pytest.mark.parametrize("backward", [False, True], ids=["forward", "backward"])
+@pytest.mark.parametrize("M,N,K", [(16 * ((1 << 20) - 1), 1 << 30, 1 << 30), (4, 1 << 20, 1 << 20),
+                                   (1 << 24, 1 << 30, 1 << 10), (1, 1 << 30, 1 << 30)])
+def test_products_of_sizes(M, N, K, backward, E):
+    """Blocks of the output, experts, rows and blocks of the sum: 2^66 and 2^76 in the first case."""
+    name = ("qlinear_fp8_grouped" if E else "qlinear_fp8_linear") + ("_backward" if backward else "")
+    head = (0, P, 2 * P, 7 * P) if E else (0, P, 2 * P)
+    rows = (M, E) if E else (M,)
+    assert getattr(L, name)(*head, 3 * P, 4 * P, 5 * P, *rows, N, K, 6 * P, 1 << 20, None) == SHAPE
 
 
 def test_offsets_of_the_norm_are_counted():

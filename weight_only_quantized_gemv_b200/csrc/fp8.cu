@@ -652,10 +652,8 @@ ql_status product(int type, const uint8_t* q, const float* scales, const int* of
   if (M < 1 || M > kMaxRows || !cols_ok(N) || !cols_ok(K) || E < 1 || E > kMaxExperts)
     return QL_ERR_SHAPE;
   const int C = backward ? N : K, R = backward ? K : N;
-  // (a tensor copy's coordinates and the units of work are 32-bit)
-  if ((long long)blocks_of(R) * E * (M < 16 ? 1 : (M + 15) / 16 + 1) * blocks_of(C) >=
-      (1LL << 46))
-    return QL_ERR_SHAPE;
+  // a tensor map's strides, an expert's codes among them, are below 2^40 bytes
+  if ((long long)N * K >= (1LL << 40)) return QL_ERR_SHAPE;
   if (!aligned(q, 16) || !aligned(scales, 4) || !aligned(w, 16) || !aligned(wscales, 4) ||
       !aligned(y, 16) || !aligned(offsets, 4))
     return QL_ERR_ALIGN;

@@ -1236,7 +1236,8 @@ ql_status launch_as(const Product& p) {
   // no more tiles than these, whatever the offsets
   const long long tiles = (long long)P.rtiles * (p.offsets ? p.M / C::BNX + (p.E < p.M ? p.E : p.M)
                                                            : (p.M + C::BNX - 1) / C::BNX);
-  if (tiles >= (1LL << 31) || (long long)p.N * p.K >= (1LL << 40)) return QL_ERR_SHAPE;
+  // (a worker's tile number passes the last one by less than the workers)
+  if (tiles >= (1LL << 31) - (1 << 16)) return QL_ERR_SHAPE;
   // (fewer tiles than workers are split)
   if ((size_t)C::kPerSm * maxw * C::kCtas * C::kEpiWarps * sizeof(uint32_t) >
       qfused::kTcCounterBytes)
