@@ -589,10 +589,12 @@ ql_status launch_norm_grad_v(NormGradParams P, int blocks, ql_stream_t st) {
   int groups = P.M < 2 * blocks ? 1 : 1024 / P.threads < 8 ? 1024 / P.threads : 8;
   // the next row, at least, is on its way
   while (groups > 1 && 2 * bytes * groups > kGradSmem) --groups;
-  const size_t room = kGradSmem / groups;
-  if (4 * bytes <= room) return launch_norm_grad_as<BF16, PART, V, 4>(P, blocks, groups, bytes, st);
-  if (2 * bytes <= room) return launch_norm_grad_as<BF16, PART, V, 2>(P, blocks, groups, bytes, st);
-  return launch_norm_grad_as<BF16, PART, V, 1>(P, blocks, groups, bytes, st);
+  // as many stages as there is room for: four with one vector to a thread (192 KB at most), four or
+  // two with two, two or one with four
+  constexpr int kMost = V == 4 ? 2 : 4, kLeast = V == 1 ? 4 : kMost / 2;
+  if (groups * kMost * bytes <= kGradSmem)
+    return launch_norm_grad_as<BF16, PART, V, kMost>(P, blocks, groups, bytes, st);
+  return launch_norm_grad_as<BF16, PART, V, kLeast>(P, blocks, groups, bytes, st);
 }
 template <bool BF16, bool PART>
 ql_status launch_norm_grad_rows(const NormGradParams& P, int blocks, ql_stream_t st) {
