@@ -535,6 +535,7 @@ ql_status qlinear_pack_params_gated(int fmt, const void* gate, const void* up, v
  *
  *   codes of rows    for every 128 columns (the last block may be shorter): scale = max|v| / 448,
  *                    q = e4m3(v / scale) to nearest even.  scales fp32 [rows][ceil(columns / 128)]
+ *                    (both divisions by reciprocals in fp32: within 2^-23 and 2^-22 of themselves)
  *   codes of weights one scale per 128 x 128 block: fp32 [ceil(N / 128)][ceil(K / 128)]
  *   linear           y[m][n] = sum_b sx[m][b] sw[n / 128][b] sum_{k in block b} q[m][k] w[n][k]
  *   linear_backward  dx[m][k] = sum_b sd[m][b] sw[b][k / 128] sum_{n in block b} qd[m][n] w[n][k]

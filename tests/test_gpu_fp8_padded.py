@@ -57,10 +57,13 @@ def test_block_backward(E, H, F, front, rows, behind, dtype, monkeypatch):
     monkeypatch.setattr(layers.RMSNorm, "_fused_new",
                         staticmethod(_nan_filled(layers.RMSNorm._fused_new)))
     x, r = (ref.activations(gen, M, H, dtype) for _ in range(2))
+    x[:front], x[front + rows:] = float("inf"), float("nan")
     total, rstd = torch.empty_like(x), torch.empty(M, device="cuda")
     gu = torch.full((M, 2 * F), float("nan"), dtype=dtype, device="cuda")
-    block.forward(x, r, at, total=total, rstd=rstd, gu=gu)
+    y = block.forward(x, r, at, total=total, rstd=rstd, gu=gu)
+    assert bool(torch.isfinite(y[own]).all()) and bool(torch.isfinite(gu[own]).all())
     dy, dt = _randn(gen, M, H, dtype=dtype), _randn(gen, M, H, dtype=dtype)
+    dy[:front], dy[front + rows:] = float("nan"), float("inf")
 
     q, s = layers.fp8_quantize(dy)
     dh = block.down.backward(q, s, at, dtype=dtype)
@@ -75,7 +78,7 @@ def test_block_backward(E, H, F, front, rows, behind, dtype, monkeypatch):
             None if through is None else through[own])
         ref.check(dx[own], want, err, "dx")
         assert bool(((dweight.double() - want_w).abs() <= err_w).all())
-        none = torch.zeros_like(dy) if through is None else through
+        none = torch.zeros_like(dx) if through is None else through
         for rest in (slice(0, front), slice(front + rows, M)):
             assert torch.equal(dx[rest], none[rest])
         if through is not None:  # in place

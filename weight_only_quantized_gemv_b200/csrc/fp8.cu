@@ -65,7 +65,8 @@ struct NormParams {
 
 // A block takes a row; a thread keeps its V vectors in registers between the sum of squares and the
 // output, so that the row is read once.  Measured, cold, bf16, with residual, total, y and codes:
-// 4096 x 8192 47.4 us for 302 MB (6.4 TB/s, 97 % of a copy's rate).
+// 4096 x 8192 47.4 us for 302 MB (6.4 TB/s, 97 % of a copy's rate); with V = 4, where 48 bytes
+// spill, 4096 x 12288 74.3 us, 16384 93.2 us and 32768 200 us (6.1, 6.5 and 6.1 TB/s).
 template <bool BF16, int V>
 __global__ void __launch_bounds__(1024) norm_kernel(const NormParams P) {
   __shared__ float red[32];
@@ -145,10 +146,10 @@ struct NormGradParams {
 // way.  Measured, cold, bf16, with dtotal and dweight: 4096 x 8192 54.7 us (4.9 TB/s), 2047 x 8192
 // 32.6 us (4.1), 700 x 14336 25.7 us (3.1), the join among them: the passes between a row's
 // arrival and its barrier, which issue in 60 % of the slots.  (Addresses in 64 bits took 57.6 us,
-// 34.2 and 28.8.)
+// 34.2 and 28.8.)  V = 4 spills 104 to 120 bytes: 1024 x 20480 66.2 us, 1024 x 32768 86.5 us.
 //
-// PART: rows may be without a dy (of no expert: nobody wrote it).  Such a row adds to no sum, and its
-// dx is dtotal, or 0.  (An instance of its own: the tests of rows cost the others 1 to 2 %.)
+// PART: rows may be without a dy (of no expert: nobody wrote it).  Such a row adds to no sum, and
+// its dx is dtotal, or 0.  (An instance of its own: the tests of rows cost the others 1 to 2 %.)
 template <bool BF16, bool PART, int V, int S>
 __global__ void __launch_bounds__(1024) norm_grad_kernel(const NormGradParams P) {
   extern __shared__ __align__(16) uint4 stages[];  // [group][S][array][V][thread]; then the sums
@@ -448,7 +449,8 @@ __global__ void __launch_bounds__(kCodeThreads) code_kernel(const CodeParams P) 
 }
 
 // ---------------------------------------------------------------------------
-// weights: a block of threads to a 128 x 128 block
+// weights: a block of threads to a 128 x 128 block.  Measured, cold, bf16: 28672 x 8192 118 us (6.0
+// TB/s), 4096 x 4096 15.3 us (3.3).
 
 struct WeightParams {
   const uint16_t* w;  // [E][N][K]
@@ -614,7 +616,7 @@ ql_status launch_codes_as(CodeParams P, ql_stream_t st) {
   P.slots = blocks_of(WHAT == kPair ? P.F : P.C) * 16;
   P.inv_slots = 1.f / (float)P.slots;
   const long long n = (long long)P.M * P.slots, most = 1 << 20;
-  // two vectors to a thread once there are enough threads for every SM with one
+  // two vectors to a thread once there are enough threads with one for every SM of a B200 (148)
   const int U = n >= 2048LL * 148 ? 2 : 1;
   const long long blocks = (n + kCodeThreads * U - 1) / (kCodeThreads * U);
   const unsigned grid = (unsigned)(blocks < most ? blocks : most);

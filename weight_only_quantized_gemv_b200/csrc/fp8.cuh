@@ -1,7 +1,8 @@
 // 8-bit floating-point codes (e4m3: four exponent bits, three of fraction, largest value 448, no
 // infinity, NaN 0x7F / 0xFF) with a scale per block of 128, and the 16-bit types around them.
 //
-// scale = max|v| / 448 over a block, codes e4m3(v / scale), rounded to nearest even.  The codes use
+// scale = max|v| / 448 over a block, codes e4m3(v / scale), rounded to nearest even (by the
+// reciprocals of both divisors: scale_of, encode8).  The codes use
 // the block's largest value for the top of their range, so a value down to 1 / 28672 of it (448
 // over 2^-6, the smallest normal code) keeps its four significant bits.  A block of zeros, or of
 // values below 2^-100, is coded as if its largest value were 2^-100: the scale stays a normal

@@ -14,7 +14,9 @@
 // MMAs write a fresh accumulator in tensor memory, and the epilogue warps add it, times sx sw, to
 // fp32 sums in registers.  A warp makes the products of scales, steps ahead, in shared memory.
 //
-// Two kernels, by the rows of q that an average expert has:
+// Two kernels, by the rows of q that an average expert has (of all E: the host does not read the
+// offsets, so rows on few experts get narrow tiles, each of which reads the weights again.  64
+// experts of 2048 x 4096, 1024 rows: on all of them 113 us, on 8 or fewer 66; by one matrix 29):
 //   up to 64     fp8_tc_kernel: the weights are the MMA's A operand (128 rows), q's rows its B
 //                operand, any multiple of 16 of them.  Bound by reading the weights.
 //   above        fp8_wide_kernel: q's rows are the A operand, 256 of D's rows the B operand.
@@ -27,8 +29,9 @@
 //
 // Measured, us (in brackets the bytes' or the operations' time at the card's rates: a copy's 6.55
 // TB/s, twice cuBLAS' bf16 1.63 PFLOP/s): 1 x 28672 x 8192 39.8 (35.9), 33 rows 44.8 (36.2), 128 x
-// 8192 x 28672 56 (36), 777 x 4096 x 12304 backward 53 (24), 2048 x 8192 x 4096 73 (42), 4096 x
-// 28672 x 8192 871 to 892 (589; call after call at the power limit of 1000 W, 1.5 GHz: 1000).
+// 8192 x 28672 56 (36), 777 x 4096 x 12304 backward 64 (24; weights in L2: 53), 2048 x 8192 x 4096
+// 73 (42), 4096 x 28672 x 8192 871 to 896 (589; call after call at the power limit of 1000 W, 1.5
+// GHz, 985 to 1030).
 #include <cuda.h>
 #include <cudaTypedefs.h>
 #include <cuda_runtime.h>
@@ -756,7 +759,8 @@ __global__ void __launch_bounds__(Cfg<BNX>::kThreads, Cfg<BNX>::kPerSm)
 // 288 per expert, whose last tiles are half as empty.  (Random splits: 64 experts of 2048 x 4096,
 // 256 rows each 221 against 230 us, 312 rows 252 against 249, backward 272 against 266, 512 rows
 // 378 against 371; 8 of 14336 x 4096, backward, 256 rows 194 against 202, 312 rows 222 against
-// 233, 437 rows 280 against 270.)
+// 233, 437 rows 280 against 270.  Where the two are equal goes by how the tiles fill the last wave:
+// between 300 and 400 rows here.)
 //
 // A step of a pair takes 0.54 us and more: 512 cycles of MMAs, the copies' 0.40 us, and in the
 // epilogue 128 multiply-adds of two warps to a scheduler, 346 cycles, which overlap but for what

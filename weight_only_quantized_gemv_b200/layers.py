@@ -1007,7 +1007,8 @@ class Fp8Experts(_Fp8Weights):
     ceil(K / 128)] as in ``Fp8Linear``, up to 1024 experts.  The rows of a call are in the order of
     the experts: rows offsets[e] .. offsets[e + 1] - 1 are expert e's, any number of them, none
     included.  offsets (int32 [E + 1], on the device) is read by the kernel alone.  Rows before the
-    first and behind the last offset are neither read nor written."""
+    first and behind the last offset are neither read nor written.  The tiles' width goes by the
+    call's rows over all E experts: many rows on few of many experts cost more than they need to."""
 
     def __init__(self, codes, scales, device=None):
         self._fp8_setup(codes, scales, 3, device)
